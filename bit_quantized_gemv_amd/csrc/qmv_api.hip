@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "qmv.h"
+#include "qmv_ops.h"
 #include "qmv_dispatch.hpp"
 
 namespace {
@@ -668,6 +669,11 @@ const char* qmv_status_string(int status)
     case QMV_E_ROWS: return "QMV_E_ROWS";
     case QMV_E_ALIAS: return "QMV_E_ALIAS";
     case QMV_E_LAUNCH: return "QMV_E_LAUNCH";
+    case QMV_E_RANK: return "QMV_E_RANK";
+    case QMV_E_EXPERTS: return "QMV_E_EXPERTS";
+    case QMV_E_WORKSPACE: return "QMV_E_WORKSPACE";
+    case QMV_E_VOCAB: return "QMV_E_VOCAB";
+    case QMV_E_STRIDE: return "QMV_E_STRIDE";
     default: return "QMV_E_UNKNOWN";
     }
 }
