@@ -1,0 +1,363 @@
+// ops_moe.hip -- qmv_route, qmv_experts and qmv_moe: checks, the router's
+// kernels, the weighted sum of the experts' outputs, and the launches.
+#include "ops_moe.hpp"
+
+#include <algorithm>
+
+#include "ops_check.hpp"
+#include "ops_tile.hpp"
+
+namespace ops {
+namespace {
+
+typedef __attribute__((ext_vector_type(4))) double f64x4;
+
+constexpr int kRouteWaves = 4;
+constexpr int kRouteK = 512;                    // columns of D per workgroup
+constexpr int kRouteSteps = kRouteK / kRouteWaves / 32;
+
+int route_pieces(int D) { return (D + kRouteK - 1) / kRouteK; }
+
+struct RouteParams {
+    const char* x;
+    const char* r;
+    double* part;       // [pieces][T][E]
+    float* weights;
+    int32_t* ids;
+    int T, D, E, k, pieces;
+    bool renorm;
+};
+
+// Eight values of a row at d.. as doubles; zero past the row's end.
+template <bool F32>
+__device__ __forceinline__ void load8d(double (&o)[8], const char* row, int d, int D)
+{
+    if (d >= D) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) o[i] = 0.0;
+        return;
+    }
+    if constexpr (F32) {
+        const f32x4* p = reinterpret_cast<const f32x4*>(row + (size_t)d * 4);
+        const f32x4 a = p[0], b = p[1];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[i] = a[i];
+            o[4 + i] = b[i];
+        }
+    } else {
+        const u32x4 v = *reinterpret_cast<const u32x4*>(row + (size_t)d * 2);
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            o[2 * i] = bits_f32(v[i] << 16);
+            o[2 * i + 1] = bits_f32(v[i] & 0xffff0000u);
+        }
+    }
+}
+
+// Router products of 16 tokens and 16 experts over a piece of D, in fp64 on
+// matrix instructions (v_mfma_f64_16x16x4_f64: rows and columns l & 15, k =
+// l >> 4, results at row 4 i + (l >> 4)).  fp64, because the choice of experts
+// hangs on the order of nearly equal logits: bf16 and fp32 products are exact
+// there, and the sums off by 2^-53 of their terms.
+template <bool XF32, bool RF32>
+__global__ __launch_bounds__(kRouteWaves* kWave) void logits_kernel(RouteParams p)
+{
+    __shared__ double join[kRouteWaves][4][64];
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
+    const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, z = blockIdx.z;
+    const char* xr = p.x + (size_t)min(t0 + c, p.T - 1) * p.D * (XF32 ? 4 : 2);
+    const char* rr = p.r + (size_t)min(e0 + c, p.E - 1) * p.D * (RF32 ? 4 : 2);
+    const int d0 = z * kRouteK + wave * (kRouteK / kRouteWaves) + 8 * q;
+    f64x4 acc = {0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+    for (int s = 0; s < kRouteSteps; ++s) {
+        double a[8], b[8];
+        load8d<XF32>(a, xr, d0 + 32 * s, p.D);
+        load8d<RF32>(b, rr, d0 + 32 * s, p.D);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) acc = __builtin_amdgcn_mfma_f64_16x16x4f64(a[i], b[i], acc, 0, 0, 0);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i) join[wave][i][lane] = acc[i];
+    __syncthreads();
+    const int i = threadIdx.x >> 6, t = t0 + 4 * i + q, e = e0 + c;    // one result per thread
+    double v = join[0][i][lane];
+#pragma unroll
+    for (int w = 1; w < kRouteWaves; ++w) v += join[w][i][lane];
+    if (t < p.T && e < p.E) p.part[((size_t)z * p.T + t) * p.E + e] = v;
+}
+
+struct Best {
+    double v;
+    int i;
+};
+
+__device__ __forceinline__ Best better(Best a, Best b) { return b.v > a.v || (b.v == a.v && b.i < a.i) ? b : a; }
+
+// Top-k and softmax of one token's logits by a wave: lane l holds the experts
+// l + 64 j; k rounds of the largest left.
+__global__ __launch_bounds__(4 * kWave) void topk_kernel(RouteParams p)
+{
+    constexpr int PER = QMV_MAX_EXPERTS / kWave;
+    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + uniform(threadIdx.x >> 6);
+    if (t >= p.T) return;
+    double v[PER];
+    int id[PER];
+    const double low = -__builtin_huge_val();
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = lane + kWave * j;
+        v[j] = low;
+        id[j] = 0x7fffffff;
+        if (e < p.E) {
+            double s = 0.0;
+            for (int z = 0; z < p.pieces; ++z) s += p.part[((size_t)z * p.T + t) * p.E + e];
+            v[j] = s != s ? low : s;
+            id[j] = e;
+        }
+    }
+    double mine = 0.0, all = 0.0, top = 0.0;
+    int my_id = 0;
+    for (int r = 0; r < p.k; ++r) {
+        Best b{low, 0x7fffffff};
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (kWave * j < p.E) b = better(b, Best{v[j], id[j]});
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) b = better(b, Best{__shfl_xor(b.v, o), __shfl_xor(b.i, o)});
+        if (r == 0) {
+            top = b.v;
+            if (!p.renorm) {
+#pragma unroll
+                for (int j = 0; j < PER; ++j)
+                    if (id[j] < p.E) all += exp(v[j] - top);
+#pragma unroll
+                for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
+            }
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (id[j] == b.i) {
+                v[j] = low;
+                id[j] = 0x7fffffff;
+            }
+        const double w = exp(b.v - top);
+        if (p.renorm) all += w;
+        if (lane == r) {
+            mine = w;
+            my_id = b.i;
+        }
+    }
+    if (lane < p.k) {
+        p.weights[(size_t)t * p.k + lane] = (float)(mine / all);
+        p.ids[(size_t)t * p.k + lane] = my_id;
+    }
+}
+
+// y[t] = sum of weight * expert output over the token's slots, in their order
+__global__ __launch_bounds__(256) void combine_kernel(const float* z, const float* weights, const int32_t* ids, void* y,
+                                                      int D, int E, int k, bool yf32)
+{
+    const int d = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
+    if (d >= D) return;
+    float v = 0.0f;
+    for (int j = 0; j < k; ++j) {
+        const size_t pair = (size_t)t * k + j;
+        const int e = ids[pair];
+        if (e >= 0 && e < E) v = __builtin_fmaf(weights[pair], z[pair * D + d], v);
+    }
+    store_y(y, (size_t)t * D + d, v, yf32);
+}
+
+bool launch(const void* fn, dim3 grid, int threads, void** args, hipStream_t st)
+{
+    return hipLaunchKernel(fn, grid, dim3(threads), args, 0, st) == hipSuccess;
+}
+
+int check_route(int T, int D, int E, int k, int x_dt, int r_dt)
+{
+    if (T < 1 || T > QMV_MAX_M) return QMV_E_M_RANGE;
+    if (D < 8 || D > QMV_MAX_K || D % 8 != 0) return QMV_E_SHAPE;
+    if (E < 1 || E > QMV_MAX_EXPERTS || k < 1 || k > E || k > QMV_MAX_TOP_K) return QMV_E_EXPERTS;
+    if (!wide(x_dt) || !wide(r_dt)) return QMV_E_DTYPE;
+    return QMV_OK;
+}
+
+int check_experts(int T, int D, int F, int E, int k, int bits, int gs, int x_dt, int sb_dt, int y_dt)
+{
+    if (const int e = check_matrix(2LL * F, D, bits, gs)) return e;
+    if (const int e = check_matrix(D, F, bits, gs)) return e;
+    if (T < 1 || T > QMV_MAX_M) return QMV_E_M_RANGE;
+    if (E < 1 || E > QMV_MAX_EXPERTS || k < 1 || k > QMV_MAX_TOP_K) return QMV_E_EXPERTS;
+    if (!wide(x_dt) || !half(sb_dt) || !wide(y_dt)) return QMV_E_DTYPE;
+    return QMV_OK;
+}
+
+int run_route(const char* x, const void* router, float* weights, int32_t* ids, void* ws, int T, int D, int E, int k,
+              bool renorm, int x_dt, int r_dt, hipStream_t st)
+{
+    const bool xf = x_dt == QMV_DT_F32, rf = r_dt == QMV_DT_F32;
+    const void* fn = xf ? (rf ? (const void*)&logits_kernel<true, true> : (const void*)&logits_kernel<true, false>)
+                        : (rf ? (const void*)&logits_kernel<false, true> : (const void*)&logits_kernel<false, false>);
+    for (int t = 0; t < T; t += kMoeTile) {
+        RouteParams p;
+        p.x = x + (size_t)t * D * size_of(x_dt);
+        p.r = static_cast<const char*>(router);
+        p.part = static_cast<double*>(ws);
+        p.weights = weights + (size_t)t * k;
+        p.ids = ids + (size_t)t * k;
+        p.T = std::min(kMoeTile, T - t);
+        p.D = D;
+        p.E = E;
+        p.k = k;
+        p.pieces = route_pieces(D);
+        p.renorm = renorm;
+        void* args[] = {&p};
+        if (!launch(fn, dim3((E + 15) / 16, (p.T + 15) / 16, p.pieces), kRouteWaves * kWave, args, st) ||
+            !launch((const void*)&topk_kernel, dim3((p.T + 3) / 4), 4 * kWave, args, st))
+            return QMV_E_LAUNCH;
+    }
+    return QMV_OK;
+}
+
+int run_experts(const char* x, const float* weights, const int32_t* ids, const uint32_t* w13, const void* s13,
+                const void* b13, const uint32_t* w2, const void* s2, const void* b2, char* y, void* ws, int T, int D,
+                int F, int E, int k, int bits, int gs, int x_dt, int sb_dt, int y_dt, hipStream_t st)
+{
+    const auto go = bits == 4 ? (gs == 64 ? expert_launch_b4_g64 : expert_launch_b4_g128)
+                              : (gs == 64 ? expert_launch_b2_g64 : expert_launch_b2_g128);
+    const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16;
+    bool yf32 = y_dt == QMV_DT_F32;
+    for (int t = 0; t < T; t += kMoeTile) {
+        const int n = std::min(kMoeTile, T - t);
+        ExpertParams p;
+        p.x = x + (size_t)t * D * size_of(x_dt);
+        p.ids = ids + (size_t)t * k;
+        p.w13 = w13;
+        p.s13 = static_cast<const uint16_t*>(s13);
+        p.b13 = static_cast<const uint16_t*>(b13);
+        p.w2 = w2;
+        p.s2 = static_cast<const uint16_t*>(s2);
+        p.b2 = static_cast<const uint16_t*>(b2);
+        p.P = n * k;
+        p.k = k;
+        p.D = D;
+        p.F = F;
+        p.E = E;
+        p.slots = std::min(p.P, E);
+        p.h = static_cast<float*>(ws);
+        p.z = reinterpret_cast<float*>(static_cast<char*>(ws) + piece(4LL * p.P * F));
+        const int ct = p.P <= 12 * E ? 1 : 2;
+        if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;
+        const float* z = p.z;
+        const float* wt = weights + (size_t)t * k;
+        void* yt = y + (size_t)t * D * size_of(y_dt);
+        void* args[] = {&z, &wt, &p.ids, &yt, &D, &E, &k, &yf32};
+        if (!launch((const void*)&combine_kernel, dim3((D + 255) / 256, n), 256, args, st)) return QMV_E_LAUNCH;
+    }
+    return QMV_OK;
+}
+
+}  // namespace
+}  // namespace ops
+
+extern "C" {
+
+long long qmv_route_workspace(int T, int D, int n_experts)
+{
+    if (T < 1 || T > QMV_MAX_M || D < 1 || D > QMV_MAX_K || n_experts < 1 || n_experts > QMV_MAX_EXPERTS) return -1;
+    return ops::piece(8LL * ops::route_pieces(D) * std::min(T, ops::kMoeTile) * n_experts);
+}
+
+int qmv_route(const void* x, const void* router, float* weights, int32_t* ids, void* workspace,
+              long long workspace_bytes, int T, int D, int n_experts, int top_k, int renormalize,
+              int x_dt, int r_dt, void* stream)
+{
+    using namespace ops;
+    if (!x || !router || !weights || !ids || !workspace) return QMV_E_NULL;
+    if (const int e = check_route(T, D, n_experts, top_k, x_dt, r_dt)) return e;
+    if (!aligned(x, 16) || !aligned(router, 16) || !aligned(weights, 4) || !aligned(ids, 4) || !aligned(workspace, 16))
+        return QMV_E_ALIGN;
+    const long long need = qmv_route_workspace(T, D, n_experts);
+    if (workspace_bytes < need) return QMV_E_WORKSPACE;
+    const Span in[] = {{x, (size_t)T * D * size_of(x_dt)}, {router, (size_t)n_experts * D * size_of(r_dt)}};
+    const Span out[] = {{weights, (size_t)T * top_k * 4}, {ids, (size_t)T * top_k * 4}, {workspace, (size_t)need}};
+    if (!disjoint(in, out)) return QMV_E_ALIAS;
+    return run_route(static_cast<const char*>(x), router, weights, ids, workspace, T, D, n_experts, top_k,
+                     renormalize != 0, x_dt, r_dt, static_cast<hipStream_t>(stream));
+}
+
+long long qmv_experts_workspace(int T, int D, int F, int top_k)
+{
+    if (T < 1 || T > QMV_MAX_M || D < 1 || D > QMV_MAX_K || F < 1 || F > QMV_MAX_K || top_k < 1 || top_k > QMV_MAX_TOP_K)
+        return -1;
+    const long long pairs = (long long)std::min(T, ops::kMoeTile) * top_k;
+    return ops::piece(4 * pairs * F) + ops::piece(4 * pairs * D);
+}
+
+int qmv_experts(const void* x, const float* weights, const int32_t* ids, const uint32_t* w13,
+                const void* s13, const void* b13, const uint32_t* w2, const void* s2,
+                const void* b2, void* y, void* workspace, long long workspace_bytes, int T, int D,
+                int F, int n_experts, int top_k, int bits, int group_size, int x_dt, int sb_dt,
+                int y_dt, void* stream)
+{
+    using namespace ops;
+    if (!x || !weights || !ids || !w13 || !s13 || !b13 || !w2 || !s2 || !b2 || !y || !workspace) return QMV_E_NULL;
+    if (const int e = check_experts(T, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt)) return e;
+    if (!aligned(x, 16) || !aligned(w13, 16) || !aligned(s13, 16) || !aligned(b13, 16) || !aligned(w2, 16) ||
+        !aligned(s2, 16) || !aligned(b2, 16) || !aligned(weights, 4) || !aligned(ids, 4) || !aligned(workspace, 16) ||
+        !aligned(y, size_of(y_dt)))
+        return QMV_E_ALIGN;
+    const long long need = qmv_experts_workspace(T, D, F, top_k);
+    if (workspace_bytes < need) return QMV_E_WORKSPACE;
+    const size_t E = (size_t)n_experts, nw = E * D * F * bits / 8, ns = E * D * (F / group_size) * 2;
+    const size_t ns13 = E * 2 * F * (D / group_size) * 2;
+    const Span in[] = {{x, (size_t)T * D * size_of(x_dt)}, {weights, (size_t)T * top_k * 4}, {ids, (size_t)T * top_k * 4},
+                       {w13, 2 * nw}, {s13, ns13}, {b13, ns13}, {w2, nw}, {s2, ns}, {b2, ns}};
+    const Span out[] = {{y, (size_t)T * D * size_of(y_dt)}, {workspace, (size_t)need}};
+    if (!disjoint(in, out)) return QMV_E_ALIAS;
+    return run_experts(static_cast<const char*>(x), weights, ids, w13, s13, b13, w2, s2, b2, static_cast<char*>(y),
+                       workspace, T, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt,
+                       static_cast<hipStream_t>(stream));
+}
+
+long long qmv_moe_workspace(int T, int D, int F, int n_experts, int top_k)
+{
+    const long long r = qmv_route_workspace(T, D, n_experts), e = qmv_experts_workspace(T, D, F, top_k);
+    return r < 0 || e < 0 ? -1 : std::max(r, e);
+}
+
+int qmv_moe(const void* x, const void* router, const uint32_t* w13, const void* s13,
+            const void* b13, const uint32_t* w2, const void* s2, const void* b2, void* y,
+            float* weights, int32_t* ids, void* workspace, long long workspace_bytes, int T, int D,
+            int F, int n_experts, int top_k, int renormalize, int bits, int group_size, int x_dt,
+            int r_dt, int sb_dt, int y_dt, void* stream)
+{
+    using namespace ops;
+    if (!x || !router || !weights || !ids || !w13 || !s13 || !b13 || !w2 || !s2 || !b2 || !y || !workspace)
+        return QMV_E_NULL;
+    if (const int e = check_experts(T, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt)) return e;
+    if (const int e = check_route(T, D, n_experts, top_k, x_dt, r_dt)) return e;
+    if (!aligned(x, 16) || !aligned(router, 16) || !aligned(w13, 16) || !aligned(s13, 16) || !aligned(b13, 16) ||
+        !aligned(w2, 16) || !aligned(s2, 16) || !aligned(b2, 16) || !aligned(weights, 4) || !aligned(ids, 4) ||
+        !aligned(workspace, 16) || !aligned(y, size_of(y_dt)))
+        return QMV_E_ALIGN;
+    const long long need = qmv_moe_workspace(T, D, F, n_experts, top_k);
+    if (workspace_bytes < need) return QMV_E_WORKSPACE;
+    const size_t E = (size_t)n_experts, nw = E * D * F * bits / 8, ns = E * D * (F / group_size) * 2;
+    const size_t ns13 = E * 2 * F * (D / group_size) * 2;
+    const Span in[] = {{x, (size_t)T * D * size_of(x_dt)}, {router, E * D * size_of(r_dt)},
+                       {w13, 2 * nw}, {s13, ns13}, {b13, ns13}, {w2, nw}, {s2, ns}, {b2, ns}};
+    const Span out[] = {{y, (size_t)T * D * size_of(y_dt)}, {weights, (size_t)T * top_k * 4},
+                        {ids, (size_t)T * top_k * 4}, {workspace, (size_t)need}};
+    if (!disjoint(in, out)) return QMV_E_ALIAS;
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    if (const int e = run_route(static_cast<const char*>(x), router, weights, ids, workspace, T, D, n_experts, top_k,
+                                renormalize != 0, x_dt, r_dt, st))
+        return e;
+    return run_experts(static_cast<const char*>(x), weights, ids, w13, s13, b13, w2, s2, b2, static_cast<char*>(y),
+                       workspace, T, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt, st);
+}
+
+}  // extern "C"

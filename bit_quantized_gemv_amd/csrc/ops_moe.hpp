@@ -1,0 +1,32 @@
+// ops_moe.hpp -- parameters and launches of the expert products (qmv_experts).
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+namespace ops {
+
+constexpr int kMoeTile = 256;      // tokens per set of launches
+
+struct ExpertParams {
+    const char* x;                 // [T][D]
+    const int32_t* ids;            // [P], P = T * k (token, slot) pairs
+    const uint32_t* w13;
+    const uint16_t* s13;
+    const uint16_t* b13;
+    const uint32_t* w2;
+    const uint16_t* s2;
+    const uint16_t* b2;
+    float* h;                      // [P][F]
+    float* z;                      // [P][D]
+    int P, k, D, F, E;
+    int slots;                     // P: a workgroup per pair, its expert's first; E: one per expert
+};
+
+// which = 0: gate and up products and the activation (x -> h); 1: down product (h -> z)
+int expert_launch_b4_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b4_g128(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b2_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b2_g128(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
+
+}  // namespace ops

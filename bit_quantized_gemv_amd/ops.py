@@ -23,10 +23,14 @@ def _load():
         import torch
         L = qmv.lib()
         P, I, Q = ctypes.c_void_p, ctypes.c_int, ctypes.c_longlong
-        for name, args in (("qmv_affine_lora", [P] * 10 + [Q] + [I] * 11 + [P]),):
+        for name, args in (("qmv_affine_lora", [P] * 10 + [Q] + [I] * 11 + [P]),
+                           ("qmv_route", [P] * 5 + [Q] + [I] * 7 + [P]),
+                           ("qmv_experts", [P] * 11 + [Q] + [I] * 10 + [P]),
+                           ("qmv_moe", [P] * 12 + [Q] + [I] * 12 + [P])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, I
-        for name, n in (("qmv_affine_lora_workspace", 3),):
+        for name, n in (("qmv_affine_lora_workspace", 3), ("qmv_route_workspace", 3), ("qmv_experts_workspace", 4),
+                        ("qmv_moe_workspace", 5)):
             f = getattr(L, name)
             f.argtypes, f.restype = [I] * n, Q
         _DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
@@ -157,3 +161,134 @@ def affine_lora(w, scales, biases, x, lora_a, lora_b, ids, *, bits: int, group_s
     if status != 0:
         raise QmvError(status, "qmv_affine_lora")
     return out[0] if squeeze else out
+
+
+def _tokens(x):
+    import torch
+    if x.dim() != 2:
+        raise ValueError("x must be [T][D]")
+    _dtype(x, "x", torch.bfloat16, torch.float32)
+    return x.shape
+
+
+def _router(x, router, top_k):
+    import torch
+    _dtype(router, "router", torch.bfloat16, torch.float32)
+    if router.dim() != 2 or router.shape[1] != x.shape[1]:
+        raise ValueError(f"router must be [E][{x.shape[1]}], got {tuple(router.shape)}")
+    E = router.shape[0]
+    if not 1 <= top_k <= E:
+        raise ValueError(f"top_k must be in [1, {E}], got {top_k}")
+    return E
+
+
+def _expert_weights(gate_up, down, E, D, bits, gs):
+    w13, s13, b13 = gate_up
+    w2, s2, b2 = down
+    if w13.dim() != 3 or w13.shape[1] % 2 != 0:
+        raise ValueError("the gate and up codes must be [E][2F][D*bits/32]")
+    E = w13.shape[0] if E is None else E
+    F = w13.shape[1] // 2
+    _matrix(w13, s13, b13, (E, 2 * F), D, bits, gs, "gate_up")
+    _matrix(w2, s2, b2, (E, D), F, bits, gs, "down")
+    if s2.dtype != s13.dtype:
+        raise TypeError("the two products' scales must share a dtype")
+    return E, F, [(w13, "gate_up"), (s13, "gate_up scales"), (b13, "gate_up biases"), (w2, "down"), (s2, "down scales"),
+                  (b2, "down biases")]
+
+
+def route(x, router, *, top_k: int, renormalize: bool = True, stream=None):
+    """(weights, ids) of a mixture-of-experts router: the top_k largest products
+    x[t] . router[e] of every token in descending order (ties to the lowest expert;
+    computed in fp64) and their softmax, over the chosen experts if `renormalize`, else
+    over all.
+
+    x: bf16 or fp32 [T][D]; router: bf16 or fp32 [E][D], D a multiple of 8;
+    weights: fp32 [T][top_k]; ids: int32 [T][top_k].
+    """
+    import torch
+    L_ = _lib or _load()
+    T, D = _tokens(x)
+    E = _router(x, router, top_k)
+    qmv._check_tensors(((x, "x"), (router, "router")))
+    dev = x.device
+    with _On(dev, stream, (x, router)) as st:
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        if T == 0:
+            return weights, ids
+        nbytes = L_.qmv_route_workspace(T, D, E)
+        ws = _space(max(nbytes, 0), dev, torch)
+        status = L_.qmv_route(x.data_ptr(), router.data_ptr(), weights.data_ptr(), ids.data_ptr(), ws.data_ptr(), nbytes,
+                              T, D, E, top_k, renormalize, _DT[x.dtype], _DT[router.dtype], st)
+    if status != 0:
+        raise QmvError(status, "qmv_route")
+    return weights, ids
+
+
+def experts(x, weights, ids, gate_up, down, *, bits: int, group_size: int, out=None, out_dtype=None, stream=None):
+    """y[t] = sum over j of weights[t][j] * Down_e(silu(Gate_e x[t]) * Up_e x[t]),
+    e = ids[t][j]: the chosen affine-quantized experts of every token.
+
+    x: bf16 or fp32 [T][D]; weights: fp32 [T][k]; ids: int32 [T][k], a value
+    outside [0, E) is an empty slot; gate_up: (codes [E][2F][D*bits/32], scales, biases
+    [E][2F][D/group_size]), F gate rows before F up rows; down: (codes
+    [E][D][F*bits/32], scales, biases [E][D][F/group_size]); out, out_dtype: as
+    `affine`.  Everything between is fp32; each token is bit-identical to a call with
+    that token alone.
+    """
+    import torch
+    L_ = _lib or _load()
+    T, D = _tokens(x)
+    E, F, mats = _expert_weights(gate_up, down, None, D, bits, group_size)
+    _dtype(weights, "weights", torch.float32)
+    _dtype(ids, "ids", torch.int32)
+    if ids.dim() != 2:
+        raise ValueError("ids must be [T][k]")
+    k = ids.shape[1]
+    _shape(ids, "ids", T, k)
+    _shape(weights, "weights", T, k)
+    named = [(x, "x"), (weights, "weights"), (ids, "ids")] + mats
+    qmv._check_tensors(named)
+    dev = x.device
+    with _On(dev, stream, [t for t, _ in named] + [out]) as st:
+        out = _out(out, out_dtype, (T, D), dev, torch)
+        if T == 0:
+            return out
+        nbytes = L_.qmv_experts_workspace(T, D, F, k)
+        ws = _space(max(nbytes, 0), dev, torch)
+        status = L_.qmv_experts(x.data_ptr(), weights.data_ptr(), ids.data_ptr(), *[t.data_ptr() for t, _ in mats],
+                                out.data_ptr(), ws.data_ptr(), nbytes, T, D, F, E, k, bits, group_size,
+                                _DT[x.dtype], _DT[mats[1][0].dtype], _DT[out.dtype], st)
+    if status != 0:
+        raise QmvError(status, "qmv_experts")
+    return out
+
+
+def moe(x, router, gate_up, down, *, top_k: int, bits: int, group_size: int, renormalize: bool = True,
+        out=None, out_dtype=None, return_routing: bool = False, stream=None):
+    """A whole mixture-of-experts layer: `route`, then `experts` on what it
+    chose.  Returns y [T][D], or (y, weights, ids) with return_routing."""
+    import torch
+    L_ = _lib or _load()
+    T, D = _tokens(x)
+    E = _router(x, router, top_k)
+    E, F, mats = _expert_weights(gate_up, down, E, D, bits, group_size)
+    named = [(x, "x"), (router, "router")] + mats
+    qmv._check_tensors(named)
+    dev = x.device
+    with _On(dev, stream, [t for t, _ in named] + [out]) as st:
+        out = _out(out, out_dtype, (T, D), dev, torch)
+        weights = torch.empty((T, top_k), dtype=torch.float32, device=dev)
+        ids = torch.empty((T, top_k), dtype=torch.int32, device=dev)
+        status = 0
+        if T != 0:
+            nbytes = L_.qmv_moe_workspace(T, D, F, E, top_k)
+            ws = _space(max(nbytes, 0), dev, torch)
+            status = L_.qmv_moe(x.data_ptr(), router.data_ptr(), *[t.data_ptr() for t, _ in mats], out.data_ptr(),
+                                weights.data_ptr(), ids.data_ptr(), ws.data_ptr(), nbytes, T, D, F, E, top_k,
+                                renormalize, bits, group_size, _DT[x.dtype], _DT[router.dtype],
+                                _DT[mats[1][0].dtype], _DT[out.dtype], st)
+    if status != 0:
+        raise QmvError(status, "qmv_moe")
+    return (out, weights, ids) if return_routing else out
