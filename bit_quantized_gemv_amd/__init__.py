@@ -8,9 +8,9 @@ marshal torch tensors into it.
 from .qmv import (QmvError, affine, affine_ptr, kernel_info, status_string, library_path, lib,
                   stream_read_ptr, stream_read_ex_ptr, mxfp4, mxfp4_ptr, timeline, timeline_ptr,
                   shape_ptr, KernelInfo, TimelineInfo, STAMPS, DT_F32, DT_F16, DT_BF16, MAX_M)
-from .ops import affine_lora, experts, moe, route
+from .ops import affine_lora, experts, moe, route, verify
 
 __all__ = ["QmvError", "affine", "affine_ptr", "kernel_info", "status_string", "library_path", "lib",
            "stream_read_ptr", "stream_read_ex_ptr", "mxfp4", "mxfp4_ptr", "timeline", "timeline_ptr",
            "shape_ptr", "KernelInfo", "TimelineInfo", "STAMPS", "DT_F32", "DT_F16", "DT_BF16", "MAX_M",
-           "affine_lora", "experts", "moe", "route"]
+           "affine_lora", "experts", "moe", "route", "verify"]

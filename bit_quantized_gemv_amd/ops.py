@@ -26,11 +26,12 @@ def _load():
         for name, args in (("qmv_affine_lora", [P] * 10 + [Q] + [I] * 11 + [P]),
                            ("qmv_route", [P] * 5 + [Q] + [I] * 7 + [P]),
                            ("qmv_experts", [P] * 11 + [Q] + [I] * 10 + [P]),
-                           ("qmv_moe", [P] * 12 + [Q] + [I] * 12 + [P])):
+                           ("qmv_moe", [P] * 12 + [Q] + [I] * 12 + [P]),
+                           ("qmv_verify", [P] * 9 + [Q] + [I] * 3 + [Q] * 4 + [I] * 2 + [P])):
             f = getattr(L, name)
             f.argtypes, f.restype = args, I
         for name, n in (("qmv_affine_lora_workspace", 3), ("qmv_route_workspace", 3), ("qmv_experts_workspace", 4),
-                        ("qmv_moe_workspace", 5)):
+                        ("qmv_moe_workspace", 5), ("qmv_verify_workspace", 3)):
             f = getattr(L, name)
             f.argtypes, f.restype = [I] * n, Q
         _DT = {torch.float32: DT_F32, torch.float16: DT_F16, torch.bfloat16: DT_BF16}
@@ -292,3 +293,77 @@ def moe(x, router, gate_up, down, *, top_k: int, bits: int, group_size: int, ren
     if status != 0:
         raise QmvError(status, "qmv_moe")
     return (out, weights, ids) if return_routing else out
+
+
+def verify(logits, draft, uniforms, *, draft_probs=None, temperature=None, lengths=None, stream=None):
+    """(tokens, accepted): drafted tokens accepted or replaced so that what is
+    emitted follows the target's distribution p = softmax(logits / temperature).
+
+    logits: bf16 or fp32 [B][S+1][V], rows of contiguous values at any stride; draft: int32
+    [B][S]; uniforms: fp32 [B][S+1] in [0, 1); draft_probs: the drafter's probabilities q,
+    bf16 or fp32 [B][S][V], or None for a drafter that gives tokens only (q is 1 at the
+    drafted token); temperature: fp32 [B], not above 0 for greedy, default 1;
+    lengths: int32 [B], how many of a request's S tokens are drafted, default all.
+
+    Position j < lengths[b] is accepted while uniforms[b][j] * q(x_j) < p(x_j).  The first
+    that is not gets a token sampled from max(p - q, 0) (from p if nothing is left of it); if
+    all are accepted, the position after them gets one sampled from p.  Samples
+    are the lowest index whose prefix sum passes uniforms[b][lengths[b]] times the total, in
+    fp64.  NaN and -inf logits have probability 0; a row with nothing else rejects its
+    position and gives the token -1.
+
+    tokens: int32 [B][S+1], the accepted tokens, the sampled one, then -1; accepted: int32 [B].
+    """
+    import torch
+    L_ = _lib or _load()
+    if logits.dim() != 3 or logits.shape[1] < 1:
+        raise ValueError("logits must be [B][S+1][V]")
+    B, S1, V = logits.shape
+    S = S1 - 1
+    _dtype(logits, "logits", torch.bfloat16, torch.float32)
+    _dtype(draft, "draft", torch.int32)
+    _shape(draft, "draft", B, S)
+    _dtype(uniforms, "uniforms", torch.float32)
+    _shape(uniforms, "uniforms", B, S1)
+    named = [(draft, "draft"), (uniforms, "uniforms")]
+    rows = [(logits, "logits")]
+    if draft_probs is not None:
+        _dtype(draft_probs, "draft_probs", torch.bfloat16, torch.float32)
+        _shape(draft_probs, "draft_probs", B, S, V)
+        rows.append((draft_probs, "draft_probs"))
+    if temperature is not None:
+        _dtype(temperature, "temperature", torch.float32)
+        _shape(temperature, "temperature", B)
+        named.append((temperature, "temperature"))
+    if lengths is not None:
+        _dtype(lengths, "lengths", torch.int32)
+        _shape(lengths, "lengths", B)
+        named.append((lengths, "lengths"))
+    dev = logits.device
+    for t, n in rows:
+        if not t.is_cuda:
+            raise ValueError(f"{n} must be a CUDA (HIP) tensor")
+        if t.device != dev:
+            raise ValueError(f"{n} is on {t.device}, the other inputs on {dev}")
+        if V > 1 and t.stride(2) != 1:
+            raise ValueError(f"{n}: the values of a row must be contiguous")
+    qmv._check_tensors(named)
+    if draft.device != dev:
+        raise ValueError(f"draft is on {draft.device}, the other inputs on {dev}")
+    with _On(dev, stream, [t for t, _ in named + rows]) as st:
+        tokens = torch.empty((B, S1), dtype=torch.int32, device=dev)
+        accepted = torch.empty(B, dtype=torch.int32, device=dev)
+        if B == 0:
+            return tokens, accepted
+        nbytes = L_.qmv_verify_workspace(B, S, V)
+        ws = _space(max(nbytes, 0), dev, torch)
+        q = draft_probs if S > 0 else None
+        status = L_.qmv_verify(
+            logits.data_ptr(), draft.data_ptr(), uniforms.data_ptr(), None if q is None else q.data_ptr(),
+            None if temperature is None else temperature.data_ptr(), None if lengths is None else lengths.data_ptr(),
+            tokens.data_ptr(), accepted.data_ptr(), ws.data_ptr(), nbytes, B, S, V, logits.stride(0), logits.stride(1),
+            0 if q is None else q.stride(0), 0 if q is None else q.stride(1), _DT[logits.dtype],
+            DT_F32 if q is None else _DT[q.dtype], st)
+    if status != 0:
+        raise QmvError(status, "qmv_verify")
+    return tokens, accepted

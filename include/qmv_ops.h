@@ -51,7 +51,7 @@ enum {
                              [1, min(experts, QMV_MAX_TOP_K)] */
     QMV_E_WORKSPACE = 13, /* the workspace is smaller than the call needs */
     QMV_E_VOCAB = 14,     /* vocabulary, draft length or batch outside the limits */
-    QMV_E_STRIDE = 15     /* a row stride smaller than the row */
+    QMV_E_STRIDE = 15     /* a stride is negative or above 2^40 */
 };
 
 #define QMV_MAX_RANK 512
