@@ -1,17 +1,26 @@
 // ops_verify.hip -- qmv_verify: drafted tokens accepted or replaced by the
 // target's probabilities and given random numbers.
 //
-// Two launches.  The first passes over all logits once, in chunks of a row: the
-// largest value, its first index, and the sum of exp((l - largest) / T).  In the
+// Two launches.  The first passes over all logits once; every wave takes a span
+// of a row: the largest value and the sum of exp((l - largest) / T).  In the
 // second, every workgroup of a request joins those of its rows, makes the same
 // accept decisions, and adds up the weights of its chunk of the one row that is
 // sampled; the last to finish turns the chunks' sums into the token.  Bound by
-// the read of the logits.
+// the read of the logits where there are many, by the chain of dependent loads
+// of the second launch where there are few.
 //
-// fp64 throughout.  A token is chosen where a prefix sum of up to 2^17 and more
-// terms first passes a random number; with fp32 exponentials every one of those
-// borders moves by 2^-24 of its term, and over a vocabulary about one request
-// in a thousand would get a neighbour of the token that the definition gives.
+// Precision.  An accept decision compares one number with one border, so the
+// rows' sums may be off by 2^-20: the first pass takes fp32 exponentials, which
+// is what lets it keep up with the read.  A sampled token is where a prefix sum
+// of up to 2^17 and more terms first passes a number: with fp32 exponentials
+// every one of those borders moves, and over a vocabulary about one request in a
+// thousand would get a neighbour of the token that the definition gives.  So the
+// sampled row is summed again, in fp64.  Its total Z is known only when all of its
+// chunks are summed, but the weights max(e_i - q_i Z, 0) are needed with it: each
+// chunk adds up e_i and q_i where e_i > q_i Z0 for the first pass's Z0, and their
+// sums give those of the weights for the true Z, up to the values so near the
+// border that Z and Z0 disagree about them; where those could matter the sums are
+// taken once more.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -26,13 +35,24 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef u32x4 __attribute__((aligned(2))) u32x4_any;      // rows may start anywhere
 
 constexpr int kThreads = 256;
-constexpr int kPer = 16;                      // values per thread and chunk
-constexpr int kChunk = kThreads * kPer;
+constexpr int kWaves = kThreads / 64;
+constexpr int kSpanPer = 32;                  // first launch: values per lane
+constexpr int kSpan = 64 * kSpanPer;          // and per wave
+constexpr int kPer = 8;                       // second launch: values per thread
+constexpr int kChunk = kThreads * kPer;       // and per workgroup
+constexpr float kNone = -__builtin_huge_valf();
+constexpr int kNoIndex = 0x7fffffff;
 
-struct Stat {          // of a chunk of a row
+struct Stat {          // of a wave's stretch of a row
     double sum;        // of exp((l - top) / T)
     float top;         // the largest value, -inf if none counts
-    int at;            // its first index
+    int at;            // greedy: its first index
+};
+
+struct Part {          // of a chunk of the sampled row
+    double p;          // sum of e
+    double e, q;       // sums of e and q over the values with e > q Z0
+    double near;       // sum of e over those too near to say
 };
 
 struct VerifyParams {
@@ -44,48 +64,15 @@ struct VerifyParams {
     const int32_t* lengths;
     int32_t* tokens;
     int32_t* accepted;
-    Stat* stats;       // [B][S + 1][chunks]
-    double* part;      // [B][chunks]
+    Stat* stats;       // [B][S + 1][stretches]
+    Part* part;        // [B][chunks]
     uint32_t* tickets; // [B]
     int B, S, V, chunks;
+    int walk, stretches; // first launch: spans per wave, waves per row
     long long l_batch, l_row, q_batch, q_row;
 };
 
 __device__ __forceinline__ float bits_f32(uint32_t u) { return __builtin_bit_cast(float, u); }
-
-// sixteen values of a row from i on; -inf (or zero) past its end
-template <bool F32>
-__device__ __forceinline__ void load16(float (&o)[kPer], const char* row, long long i, int V, float none)
-{
-    constexpr int SZ = F32 ? 4 : 2;
-    if (i + kPer <= V) {
-        const u32x4_any* p = reinterpret_cast<const u32x4_any*>(row + i * SZ);
-#pragma unroll
-        for (int v = 0; v < SZ; ++v) {
-            const u32x4 w = p[v];
-#pragma unroll
-            for (int d = 0; d < 4; ++d) {
-                if constexpr (F32) {
-                    o[4 * v + d] = bits_f32(w[d]);
-                } else {
-                    o[8 * v + 2 * d] = bits_f32(w[d] << 16);
-                    o[8 * v + 2 * d + 1] = bits_f32(w[d] & 0xffff0000u);
-                }
-            }
-        }
-        return;
-    }
-#pragma unroll
-    for (int j = 0; j < kPer; ++j) {
-        o[j] = none;
-        if (i + j < V) {
-            if constexpr (F32)
-                o[j] = reinterpret_cast<const float*>(row)[i + j];
-            else
-                o[j] = bits_f32((uint32_t)reinterpret_cast<const uint16_t*>(row)[i + j] << 16);
-        }
-    }
-}
 
 template <bool F32>
 __device__ __forceinline__ float load1(const char* row, long long i)
@@ -94,7 +81,118 @@ __device__ __forceinline__ float load1(const char* row, long long i)
     return bits_f32((uint32_t)reinterpret_cast<const uint16_t*>(row)[i] << 16);
 }
 
-__device__ __forceinline__ float no_nan(float v) { return v != v ? -__builtin_huge_valf() : v; }
+// the values of one 16-byte piece
+template <bool F32>
+__device__ __forceinline__ void unpack(float* o, const u32x4& w)
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) {
+        if constexpr (F32) {
+            o[d] = bits_f32(w[d]);
+        } else {
+            o[2 * d] = bits_f32(w[d] << 16);
+            o[2 * d + 1] = bits_f32(w[d] & 0xffff0000u);
+        }
+    }
+}
+
+// NV 16-byte pieces of a row, piece v from i + v * step on; `none` past its end
+template <bool F32, int NV>
+__device__ __forceinline__ void load_raw(u32x4 (&w)[NV], const char* row, long long i, int step, int V, float none)
+{
+    constexpr int SZ = F32 ? 4 : 2, PER = 16 / SZ;
+    if (i + (NV - 1) * step + PER <= V) {
+#pragma unroll
+        for (int v = 0; v < NV; ++v) w[v] = *reinterpret_cast<const u32x4_any*>(row + (i + v * step) * SZ);
+        return;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int d = 0; d < 4; ++d) {
+            const long long at = i + v * step + d * (PER / 4);
+            const uint32_t a = __builtin_bit_cast(uint32_t, at < V ? load1<F32>(row, at) : none);
+            if constexpr (F32) {
+                w[v][d] = a;
+            } else {
+                const uint32_t b = __builtin_bit_cast(uint32_t, at + 1 < V ? load1<F32>(row, at + 1) : none);
+                w[v][d] = (a >> 16) | (b & 0xffff0000u);
+            }
+        }
+}
+
+template <bool F32, int N>
+__device__ __forceinline__ void load_row(float (&o)[N], const char* row, long long i, int step, int V, float none)
+{
+    constexpr int PER = F32 ? 4 : 8;
+    u32x4 w[N / PER];
+    load_raw<F32>(w, row, i, step, V, none);
+#pragma unroll
+    for (int v = 0; v < N / PER; ++v) unpack<F32>(o + v * PER, w[v]);
+}
+
+__device__ __forceinline__ float no_nan(float v) { return v != v ? kNone : v; }
+
+// Reductions over a wave in one fixed order, the result in every lane: pairs and
+// quads by dpp, halves of a row by its mirrors, rows by swaps.
+template <int CTRL>
+__device__ __forceinline__ uint32_t dpp(uint32_t v)
+{
+    return (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, false);
+}
+
+template <class Op>
+__device__ __forceinline__ uint32_t wave_fold(uint32_t v, Op op)
+{
+    v = op(v, dpp<0xB1>(v));
+    v = op(v, dpp<0x4E>(v));
+    v = op(v, dpp<0x141>(v));
+    v = op(v, dpp<0x140>(v));
+    const auto a = __builtin_amdgcn_permlane16_swap(v, v, false, false);
+    v = op(a[0], a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(v, v, false, false);
+    return op(b[0], b[1]);
+}
+
+__device__ __forceinline__ float wave_max(float v)
+{
+    return bits_f32(wave_fold(__builtin_bit_cast(uint32_t, v), [](uint32_t a, uint32_t b) {
+        return __builtin_bit_cast(uint32_t, __builtin_fmaxf(bits_f32(a), bits_f32(b)));
+    }));
+}
+
+__device__ __forceinline__ int wave_min(int v)
+{
+    return (int)wave_fold((uint32_t)v, [](uint32_t a, uint32_t b) { return (uint32_t)min((int)a, (int)b); });
+}
+
+__device__ __forceinline__ double two(uint32_t lo, uint32_t hi)
+{
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
+}
+
+template <int CTRL>
+__device__ __forceinline__ double dpp(double v)
+{
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return two(dpp<CTRL>((uint32_t)u), dpp<CTRL>((uint32_t)(u >> 32)));
+}
+
+__device__ __forceinline__ double wave_sum(double v)
+{
+    v += dpp<0xB1>(v);
+    v += dpp<0x4E>(v);
+    v += dpp<0x141>(v);
+    v += dpp<0x140>(v);
+    uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const auto al = __builtin_amdgcn_permlane16_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto ah = __builtin_amdgcn_permlane16_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    v = two(al[0], ah[0]) + two(al[1], ah[1]);
+    u = __builtin_bit_cast(uint64_t, v);
+    const auto bl = __builtin_amdgcn_permlane32_swap((uint32_t)u, (uint32_t)u, false, false);
+    const auto bh = __builtin_amdgcn_permlane32_swap((uint32_t)(u >> 32), (uint32_t)(u >> 32), false, false);
+    return two(bl[0], bh[0]) + two(bl[1], bh[1]);
+}
 
 // 2^t for t <= 0: 2^n by the exponent, 2^f for |f| <= 1/2 by the series of
 // exp(f ln 2) up to the tenth power (2e-13 of the value); 0 below 2^-1000.
@@ -116,262 +214,435 @@ __device__ __forceinline__ double exp2_down(double t)
     return __builtin_ldexp(p, (int)n);
 }
 
-// exp((l - top) / T), rate = log2(e) / T: 1 at the top (an infinite one too), 0 at -inf
+// exp((l - top) / T), rate = log2(e) / T: 1 at the top (an infinite one too), 0 at -inf and NaN
 __device__ __forceinline__ double weight(float l, float top, double rate)
 {
+    if (!(l > kNone)) return 0.0;
     return l == top ? 1.0 : exp2_down(((double)l - (double)top) * rate);
 }
 
 __device__ __forceinline__ double rate_of(float t) { return 1.4426950408889634074 / (double)t; }
-
-__device__ __forceinline__ void join(float& top, int& at, float top2, int at2)
-{
-    if (top2 > top || (top2 == top && at2 < at)) {
-        top = top2;
-        at = at2;
-    }
-}
 
 __device__ __forceinline__ int length_of(const VerifyParams& p, int b)
 {
     return p.lengths ? min(max(p.lengths[b], 0), p.S) : p.S;
 }
 
+// A wave walks p.walk spans of one row, the next one's loads in flight.
+//
+// A lane takes e = 2^t, t = l * hi + ref, in fp32: hi is log2(e) / T rounded and
+// ref about -(its largest value) * hi, so that ref and hi are exact as they stand
+// and only t is rounded, either way.  The rest lo of the rate would shift all
+// terms one way; to first order it adds ln 2 * lo * sum(e (l - largest)), from
+// sum(e t).
 template <bool LF32>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
 {
-    __shared__ float tops[kThreads / 64];
-    __shared__ int ats[kThreads / 64];
-    __shared__ double sums[kThreads / 64];
-    const int chunk = blockIdx.x, row = blockIdx.y, b = row / (p.S + 1), j = row % (p.S + 1);
-    if (chunk == 0 && j == 0 && threadIdx.x == 0) p.tickets[b] = 0;
-    if (j > length_of(p, b)) return;
+    constexpr int PER = LF32 ? 4 : 8, NV = kSpanPer / PER, SZ = LF32 ? 4 : 2;
+    const int lane = threadIdx.x & 63, at_row = blockIdx.x * kWaves + (threadIdx.x >> 6);
+    const int b = blockIdx.z, j = blockIdx.y, row = b * (p.S + 1) + j;
+    if (j == 0 && at_row == 0 && lane == 0) p.tickets[b] = 0;
+    if (at_row >= p.stretches || j > length_of(p, b)) return;
     const float T = p.temperature ? p.temperature[b] : 1.0f;
-    const char* l = p.logits + (b * p.l_batch + j * p.l_row) * (LF32 ? 4 : 2);
-    const long long i0 = (long long)chunk * kChunk + threadIdx.x * kPer;
-    float v[kPer];
-    load16<LF32>(v, l, i0, p.V, -__builtin_huge_valf());
-    float top = -__builtin_huge_valf();
-    int at = 0x7fffffff;
+    const char* l = p.logits + (b * p.l_batch + j * p.l_row) * SZ;
+    const int spans = min(p.walk, (p.V + kSpan - 1) / kSpan - at_row * p.walk);
+    const long long i0 = (long long)at_row * p.walk * kSpan + lane * PER;
+    float top = kNone;
+    int at = kNoIndex;
+    double sum = 0.0;
+    u32x4 w[NV], next[NV];
+    float v[kSpanPer];
+    constexpr double kLn2 = 0.69314718055994530942;
+    bool strange = !(T < 1e18f) || T <= 1e-18f;
+    if (T > 0.0f && !strange) {
+        const double rate = rate_of(T);
+        const float hi = (float)rate;
+        load_raw<LF32>(next, l, i0, 64 * PER, p.V, kNone);
+        float mine = -1e18f, ref = 0.0f, s[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < spans; ++i) {
 #pragma unroll
-    for (int i = 0; i < kPer; ++i) {
-        v[i] = no_nan(v[i]);
-        if (v[i] > top) {
-            top = v[i];
-            at = (int)i0 + i;
+            for (int d = 0; d < NV; ++d) w[d] = next[d];
+            if (i + 1 < spans) load_raw<LF32>(next, l, i0 + (long long)(i + 1) * kSpan, 64 * PER, p.V, kNone);
+#pragma unroll
+            for (int d = 0; d < NV; ++d) unpack<LF32>(v + d * PER, w[d]);
+            // the median of a value, the largest so far and +inf is the larger of the first two, and passes NaN over
+            float t4[4] = {mine, mine, mine, mine};
+#pragma unroll
+            for (int d = 0; d < kSpanPer; ++d) t4[d & 3] = __builtin_amdgcn_fmed3f(v[d], t4[d & 3], __builtin_huge_valf());
+            mine = __builtin_fmaxf(__builtin_fmaxf(t4[0], t4[1]), __builtin_fmaxf(t4[2], t4[3]));
+            const float old = ref;
+            ref = -(mine * hi);
+            if (i > 0) {
+                const float up = ref - old, f = __builtin_amdgcn_exp2f(up);
+#pragma unroll
+                for (int d = 0; d < 4; ++d) {
+                    c[d] = f * __builtin_fmaf(up, s[d], c[d]);
+                    s[d] *= f;
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < kSpanPer; ++d) {
+                const float t = __builtin_fmaxf(__builtin_fmaf(v[d], hi, ref), -200.0f);   // masked and NaN: 2^-200, 0 in fp32
+                const float e = __builtin_amdgcn_exp2f(t);
+                s[d & 3] += e;
+                c[d & 3] = __builtin_fmaf(e, t, c[d & 3]);
+            }
+        }
+        top = wave_max(mine);
+        strange = !(__builtin_fabsf(top) < 1e18f);
+        if (!strange) {
+            const double sa = (double)((s[0] + s[1]) + (s[2] + s[3])), ca = (double)((c[0] + c[1]) + (c[2] + c[3]));
+            const double off = (double)mine * (double)hi + (double)ref;            // t at the lane's largest
+            const double all = sa + kLn2 * (rate / (double)hi - 1.0) * (ca - off * sa);
+            const double t = ((double)mine - (double)top) * rate - off;            // from there to the wave's largest
+            const float near = __builtin_fmaxf((float)t, -200.0f), e = __builtin_amdgcn_exp2f(near);
+            sum = wave_sum(all * ((double)e + kLn2 * (double)e * __builtin_fmax(t - (double)near, -1.0)));
         }
     }
+    if (strange || !(T > 0.0f)) {
+        // greedy requests, and what the arithmetic above has no range for
+        float mine = kNone;
+        for (int i = 0; i < spans; ++i) {
+            load_row<LF32>(v, l, i0 + (long long)i * kSpan, 64 * PER, p.V, kNone);
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) join(top, at, __shfl_xor(top, o), __shfl_xor(at, o));
-    const int wave = threadIdx.x >> 6;
-    if ((threadIdx.x & 63) == 0) {
-        tops[wave] = top;
-        ats[wave] = at;
+            for (int d = 0; d < kSpanPer; ++d)
+                if (v[d] > mine) {
+                    mine = v[d];
+                    at = (int)i0 + i * kSpan + (d / PER) * 64 * PER + d % PER;
+                }
+        }
+        top = wave_max(mine);
+        at = wave_min(mine == top ? at : kNoIndex);
+        if (T > 0.0f && top > kNone) {
+            const double rate = rate_of(T);
+            sum = 0.0;
+            for (int i = 0; i < spans; ++i) {
+                load_row<LF32>(v, l, i0 + (long long)i * kSpan, 64 * PER, p.V, kNone);
+#pragma unroll
+                for (int d = 0; d < kSpanPer; ++d) sum += weight(v[d], top, rate);
+            }
+            sum = wave_sum(sum);
+        }
     }
-    __syncthreads();
-#pragma unroll
-    for (int w = 0; w < kThreads / 64; ++w) join(top, at, tops[w], ats[w]);
-    double s = 0.0;
-    if (T > 0.0f && at != 0x7fffffff) {
-        const double rate = rate_of(T);
-#pragma unroll
-        for (int i = 0; i < kPer; ++i)
-            if (v[i] > -__builtin_huge_valf()) s += weight(v[i], top, rate);
-    }
-#pragma unroll
-    for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-    if ((threadIdx.x & 63) == 0) sums[wave] = s;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        for (int w = 1; w < kThreads / 64; ++w) s += sums[w];
-        p.stats[(size_t)row * p.chunks + chunk] = Stat{s, top, at};
-    }
+    if (lane == 0) p.stats[(size_t)row * p.stretches + at_row] = Stat{sum, top, at};
 }
 
-// Which of the values get(0..n) a prefix sum first passes target(total) in, by
-// all threads: its index, or the last positive value's if none does, or -1 if no
-// value is positive.  before: the sum of the values before it.
+// Sum over the workgroup, in every thread; `shared` of kWaves values is free again after the next barrier.
+__device__ __forceinline__ double block_sum(double v, double* shared)
+{
+    v = wave_sum(v);
+    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
+    __syncthreads();
+    v = shared[0];
+#pragma unroll
+    for (int w = 1; w < kWaves; ++w) v += shared[w];
+    return v;
+}
+
+// The sums of the threads before this one, and of all.
+__device__ __forceinline__ double block_scan(double v, double* shared, double& total)
+{
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double s = v;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const double add = __shfl_up(s, o);
+        if (lane >= o) s += add;
+    }
+    if (lane == 63) shared[wave] = s;
+    __syncthreads();
+    double before = 0.0;
+    total = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) before = total;
+        total += shared[w];
+    }
+    const double prev = __shfl_up(s, 1);
+    return lane > 0 ? before + prev : before;
+}
+
+// The lowest index given by any thread that found one, else the highest last
+// index of a positive value, else -1; and the number that goes with it.
 struct Pick {
     int index;
     double before;
 };
 
-template <class Get, class Target>
-__device__ __forceinline__ Pick pick(int n, Get get, Target target)
+struct PickSpace {
+    int found, last;
+    double found_before, last_before;
+};
+
+__device__ __forceinline__ Pick block_pick(Pick found, Pick last, PickSpace* sp)
 {
-    __shared__ double sums[kThreads];
-    __shared__ int found, last;
-    __shared__ double found_before, last_before;
-    const int per = (n + kThreads - 1) / kThreads, i0 = min((int)threadIdx.x * per, n), i1 = min(i0 + per, n);
     __syncthreads();
-    double s = 0.0;
-    for (int i = i0; i < i1; ++i) s += get(i);
-    sums[threadIdx.x] = s;
     if (threadIdx.x == 0) {
-        found = 0x7fffffff;
-        last = -1;
+        sp->found = kNoIndex;
+        sp->last = -1;
     }
     __syncthreads();
-    for (int o = 1; o < kThreads; o <<= 1) {
-        const double add = (int)threadIdx.x >= o ? sums[threadIdx.x - o] : 0.0;
-        __syncthreads();
-        sums[threadIdx.x] += add;
-        __syncthreads();
-    }
-    const double t = target(sums[kThreads - 1]);
-    double c = threadIdx.x > 0 ? sums[threadIdx.x - 1] : 0.0;
-    int mine = -1, mine_last = -1;
-    double mine_before = 0.0, mine_last_before = 0.0;
-    for (int i = i0; i < i1; ++i) {
-        const double v = get(i);
-        if (v > 0.0) {
-            mine_last = i;
-            mine_last_before = c;
-            if (mine < 0 && c + v > t) {
-                mine = i;
-                mine_before = c;
-            }
-        }
-        c += v;
-    }
-    if (mine >= 0) atomicMin(&found, mine);
-    if (mine_last >= 0) atomicMax(&last, mine_last);
+    if (found.index >= 0) atomicMin(&sp->found, found.index);
+    if (last.index >= 0) atomicMax(&sp->last, last.index);
     __syncthreads();
-    if (mine >= 0 && found == mine) found_before = mine_before;
-    if (mine_last >= 0 && last == mine_last) last_before = mine_last_before;
+    if (found.index >= 0 && sp->found == found.index) sp->found_before = found.before;
+    if (last.index >= 0 && sp->last == last.index) sp->last_before = last.before;
     __syncthreads();
-    if (found != 0x7fffffff) return Pick{found, found_before};
-    return Pick{last, last_before};
+    if (sp->found != kNoIndex) return Pick{sp->found, sp->found_before};
+    return Pick{sp->last, sp->last_before};
+}
+
+// one more value v at index i with the sum c before it
+__device__ __forceinline__ void consider(Pick& found, Pick& last, int i, double v, double& c, double target)
+{
+    if (v > 0.0) {
+        last = Pick{i, c};
+        if (found.index < 0 && c + v > target) found = Pick{i, c};
+    }
+    c += v;
+}
+
+__device__ __forceinline__ void put(double* p, double v)
+{
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+
+__device__ __forceinline__ double get(const double* p)
+{
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
 }
 
 template <bool LF32, bool QF32>
 __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
 {
-    constexpr int kMaxRows = QMV_MAX_DRAFT + 1;
+    constexpr int kMaxRows = QMV_MAX_DRAFT + 1, LSZ = LF32 ? 4 : 2, QSZ = QF32 ? 4 : 2;
+    static_assert(QMV_MAX_DRAFT < kThreads, "a thread per position");
     __shared__ float tops[kMaxRows];
     __shared__ int ats[kMaxRows];
     __shared__ double sums[kMaxRows];
+    __shared__ double space[5][kWaves];
+    __shared__ PickSpace pick_space;
     __shared__ int first_bad;
-    __shared__ double partial[kThreads / 64];
     __shared__ bool am_last;
-    const int chunk = blockIdx.x, b = blockIdx.y, len = length_of(p, b);
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int chunk = blockIdx.x, b = blockIdx.y, len = length_of(p, b), tid = threadIdx.x;
+    const int lane = tid & 63, wave = tid >> 6;
     const float T = p.temperature ? p.temperature[b] : 1.0f;
     const bool greedy = !(T > 0.0f);
     const double rate = greedy ? 0.0 : rate_of(T);
-    const float none = -__builtin_huge_valf();
-    const char* lb = p.logits + b * p.l_batch * (LF32 ? 4 : 2);
-    const char* qb = p.probs ? p.probs + b * p.q_batch * (QF32 ? 4 : 2) : nullptr;
+    const char* lb = p.logits + b * p.l_batch * LSZ;
+    const char* qb = p.probs ? p.probs + b * p.q_batch * QSZ : nullptr;
+    const float* ub = p.u + (size_t)b * (p.S + 1);
 
-    // the rows' largest values and sums
-    if (threadIdx.x == 0) first_bad = len;
-    for (int j = wave; j <= len; j += kThreads / 64) {
-        const Stat* st = p.stats + ((size_t)b * (p.S + 1) + j) * p.chunks;
-        float top = none;
-        int at = 0x7fffffff;
-        for (int c = lane; c < p.chunks; c += 64) join(top, at, st[c].top, st[c].at);
-        for (int o = 32; o > 0; o >>= 1) join(top, at, __shfl_xor(top, o), __shfl_xor(at, o));
-        double s = 0.0;
-        if (!greedy)
-            for (int c = lane; c < p.chunks; c += 64)
-                if (st[c].top > none) s += st[c].sum * weight(st[c].top, top, rate);
-        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-        if (lane == 0) {
-            tops[j] = top;
-            ats[j] = at;
-            sums[j] = s;
+    // what the decisions need, on its way while the rows' statistics are joined
+    const float u_last = ub[len];
+    int x = -1;
+    float u_at = 0.0f, l_at = kNone, q_at = 1.0f;
+    if (tid < p.S) {           // positions past the length are read, not used
+        x = p.draft[(size_t)b * p.S + tid];
+        u_at = ub[tid];
+        if (x >= 0 && x < p.V) {
+            l_at = no_nan(load1<LF32>(lb + (size_t)tid * p.l_row * LSZ, x));
+            if (qb) q_at = load1<QF32>(qb + (size_t)tid * p.q_row * QSZ, x);
+        }
+    }
+    if (tid == 0) first_bad = len;
+    const Stat* sb = p.stats + (size_t)b * (p.S + 1) * p.stretches;
+    for (int j0 = wave; j0 <= len; j0 += 4 * kWaves) {
+        Stat st[4];                                  // four rows' first spans at once
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + i * kWaves;
+            st[i] = Stat{0.0, kNone, kNoIndex};
+            if (j <= p.S && lane < p.stretches) st[i] = sb[(size_t)j * p.stretches + lane];
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int j = j0 + i * kWaves;
+            if (j > len) break;
+            const Stat* row = sb + (size_t)j * p.stretches;
+            float top = st[i].top;
+            for (int c = lane + 64; c < p.stretches; c += 64) top = __builtin_fmaxf(top, row[c].top);
+            top = wave_max(top);
+            if (greedy) {
+                int at = st[i].top == top ? st[i].at : kNoIndex;
+                for (int c = lane + 64; c < p.stretches; c += 64)
+                    if (row[c].top == top) at = min(at, row[c].at);
+                at = wave_min(at);
+                if (lane == 0) ats[j] = at;
+            } else {
+                double s = st[i].sum * weight(st[i].top, top, rate);
+                for (int c = lane + 64; c < p.stretches; c += 64) s += row[c].sum * weight(row[c].top, top, rate);
+                s = wave_sum(s);
+                if (lane == 0) sums[j] = s;
+            }
+            if (lane == 0) tops[j] = top;
         }
     }
     __syncthreads();
     // the first position that is not accepted
-    for (int j = threadIdx.x; j < len; j += kThreads) {
-        const int x = p.draft[(size_t)b * p.S + j];
+    if (tid < len) {
         bool yes = false;
         if (x >= 0 && x < p.V) {
-            const float l = no_nan(load1<LF32>(lb + (size_t)j * p.l_row * (LF32 ? 4 : 2), x));
-            const double q = qb ? (double)load1<QF32>(qb + (size_t)j * p.q_row * (QF32 ? 4 : 2), x) : 1.0;
-            const double u = p.u[(size_t)b * (p.S + 1) + j];
+            const double uq = (double)u_at * (double)q_at;
             if (greedy)
-                yes = x == ats[j] && u * q < 1.0;
+                yes = x == ats[tid] && uq < 1.0;
             else
-                yes = l > none && u * q * sums[j] < weight(l, tops[j], rate);
+                yes = l_at > kNone && uq * sums[tid] < weight(l_at, tops[tid], rate);
         }
-        if (!yes) atomicMin(&first_bad, j);
+        if (!yes) atomicMin(&first_bad, tid);
     }
     __syncthreads();
     const int n = first_bad;
     const float top = tops[n];
-    const double Z = sums[n];
-    const char* ln = lb + (size_t)n * p.l_row * (LF32 ? 4 : 2);
-    const char* qn = qb ? qb + (size_t)n * p.q_row * (QF32 ? 4 : 2) : nullptr;
-    const int xn = n < len ? p.draft[(size_t)b * p.S + n] : -1;
-    // Only a rejected position's rest needs another pass over its row: greedy
-    // requests take the largest, and a position after the last draft has the sums.
-    const bool rest = n < len && !greedy;
-    if (!rest && chunk != 0) return;
-
-    // probability left for value i of the row, by chunk-wise loads
-    auto rest_of = [&](float l, float q, int i) {
-        const double e = l > none ? weight(l, top, rate) / Z : 0.0;
-        const double d = e - (qn ? (double)q : i == xn ? 1.0 : 0.0);
-        return d > 0.0 ? d : 0.0;
-    };
-    if (rest) {
-        const long long i0 = (long long)chunk * kChunk + threadIdx.x * kPer;
-        float l[kPer], q[kPer];
-        load16<LF32>(l, ln, i0, p.V, none);
-        if (qn) load16<QF32>(q, qn, i0, p.V, 0.0f);
-        double s = 0.0;
-#pragma unroll
-        for (int i = 0; i < kPer; ++i) s += rest_of(no_nan(l[i]), qn ? q[i] : 0.0f, (int)i0 + i);
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) s += __shfl_xor(s, o);
-        if (lane == 0) partial[wave] = s;
-        __syncthreads();
-        if (threadIdx.x == 0) {
-            for (int w = 1; w < kThreads / 64; ++w) s += partial[w];
-            __hip_atomic_store(&p.part[(size_t)b * p.chunks + chunk], s, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            am_last = __hip_atomic_fetch_add(&p.tickets[b], 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) ==
-                      (uint32_t)p.chunks - 1;
-        }
-        __syncthreads();
-        if (!am_last) return;
-    }
+    const bool sampled = !greedy && top > kNone, rest = sampled && n < len;
+    if (!sampled && chunk != 0) return;
 
     int token = -1;
     if (greedy) {
-        token = ats[n] == 0x7fffffff ? -1 : ats[n];
-    } else if (top > none) {
-        const double u = p.u[(size_t)b * (p.S + 1) + len];
-        const Stat* st = p.stats + ((size_t)b * (p.S + 1) + n) * p.chunks;
-        double target = 0.0;
-        auto aim = [&](double total) { return target = u * total; };
-        bool use = rest;
-        Pick k{-1, 0.0};
-        if (use) {
-            k = pick(p.chunks, [&](int c) {
-                return __hip_atomic_load(&p.part[(size_t)b * p.chunks + c], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-            }, aim);
-            use = k.index >= 0;     // nothing left: sampled from the target itself
+        token = ats[n] == kNoIndex ? -1 : ats[n];
+    } else if (sampled) {
+        const double Z0 = sums[n];
+        const char* ln = lb + (size_t)n * p.l_row * LSZ;
+        const char* qn = rest && qb ? qb + (size_t)n * p.q_row * QSZ : nullptr;
+        const int xn = rest ? p.draft[(size_t)b * p.S + n] : -1;
+        double e[kPer], q[kPer];
+        auto load_chunk = [&](int c) {
+            const long long i0 = (long long)c * kChunk + tid * kPer;
+            float lf[kPer], qf[kPer];
+            load_row<LF32>(lf, ln, i0, 16 / LSZ, p.V, kNone);
+            if (qn) load_row<QF32>(qf, qn, i0, 16 / QSZ, p.V, 0.0f);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                e[i] = weight(lf[i], top, rate);
+                q[i] = qn ? (double)qf[i] : i0 + i == xn ? 1.0 : 0.0;
+            }
+        };
+        Part* parts = p.part + (size_t)b * p.chunks;
+        for (int c = chunk; c < p.chunks; c += gridDim.x) {
+            load_chunk(c);
+            Part mine{0.0, 0.0, 0.0, 0.0};
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                mine.p += e[i];
+                const double d = __builtin_fma(-q[i], Z0, e[i]);
+                if (d > 0.0) {
+                    mine.e += e[i];
+                    mine.q += q[i];
+                }
+                if (__builtin_fabs(d) <= 0x1p-20 * e[i]) mine.near += e[i];
+            }
+            mine.p = wave_sum(mine.p);
+            if (rest) {
+                mine.e = wave_sum(mine.e);
+                mine.q = wave_sum(mine.q);
+                mine.near = wave_sum(mine.near);
+            }
+            __syncthreads();
+            if (lane == 0) {
+                space[0][wave] = mine.p;
+                space[1][wave] = mine.e;
+                space[2][wave] = mine.q;
+                space[3][wave] = mine.near;
+            }
+            __syncthreads();
+            if (tid < 4) {
+                double s = space[tid][0];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) s += space[tid][w];
+                put(reinterpret_cast<double*>(parts + c) + tid, s);
+            }
         }
-        if (!use)
-            k = pick(p.chunks, [&](int c) { return st[c].top > none ? st[c].sum * weight(st[c].top, top, rate) : 0.0; }, aim);
+        // The parts are written through by the first wave and read past the
+        // caches, so its count after they have arrived orders them; a release of
+        // the whole cache (about 40 us with 2048 workgroups) is not needed.
+        if (tid == 0) {
+            asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
+            am_last = __hip_atomic_fetch_add(&p.tickets[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+        }
+        __syncthreads();
+        if (!am_last) return;
+
+        // The totals, then the chunk in which the prefix sum passes the number:
+        // every thread holds some neighbouring chunks, the first of them in registers.
+        const int per = (p.chunks + kThreads - 1) / kThreads, c0 = min(tid * per, p.chunks), c1 = min(c0 + per, p.chunks);
+        auto part = [&](int c) { return Part{get(&parts[c].p), get(&parts[c].e), get(&parts[c].q), get(&parts[c].near)}; };
+        Part first{0.0, 0.0, 0.0, 0.0};
+        if (c0 < c1) first = part(c0);
+        Part t = first;
+        for (int c = c0 + 1; c < c1; ++c) {
+            const Part x = part(c);
+            t.p += x.p;
+            t.e += x.e;
+            t.q += x.q;
+            t.near += x.near;
+        }
+        const double Z = block_sum(t.p, space[4]);
+        bool use = false, again = false;
+        if (rest) {
+            const double near = block_sum(t.near, space[0]);
+            const double left = block_sum(t.e, space[1]) - Z * block_sum(t.q, space[2]);
+            again = near * 0x1p13 > left;     // the border's values could move the sums by 2^-33 of them
+            use = left > 0.0;
+        }
+        if (again) {
+            double all = 0.0;
+            for (int c = 0; c < p.chunks; ++c) {
+                load_chunk(c);
+                double s = 0.0;
+#pragma unroll
+                for (int i = 0; i < kPer; ++i) s += __builtin_fmax(__builtin_fma(-q[i], Z, e[i]), 0.0);
+                __syncthreads();
+                s = block_sum(s, space[3]);
+                all += s;
+                if (tid == 0) {
+                    put(&parts[c].e, s);
+                    put(&parts[c].q, 0.0);
+                }
+            }
+            use = all > 0.0;
+            __threadfence();
+            __syncthreads();
+            if (c0 < c1) first = part(c0);
+        }
+        // nothing left: sampled from the target itself
+        auto weight_of = [&](int c) {
+            const Part x = c == c0 ? first : part(c);
+            return use ? __builtin_fmax(x.e - Z * x.q, 0.0) : x.p;
+        };
+        double s = 0.0, total;
+        for (int c = c0; c < c1; ++c) s += weight_of(c);
+        __syncthreads();
+        double before = block_scan(s, space[0], total);
+        const double target = (double)u_last * total;
+        Pick found{-1, 0.0}, last{-1, 0.0};
+        for (int c = c0; c < c1; ++c) consider(found, last, c, weight_of(c), before, target);
+        const Pick k = block_pick(found, last, &pick_space);
         if (k.index >= 0) {
-            const int c0 = k.index * kChunk, m = min(kChunk, p.V - c0);
-            const double left = target - k.before;
-            const Pick i = pick(m, [&](int i) {
-                const float l = no_nan(load1<LF32>(ln, c0 + i));
-                if (!use) return l > none ? weight(l, top, rate) : 0.0;
-                return rest_of(l, qn ? load1<QF32>(qn, c0 + i) : 0.0f, c0 + i);
-            }, [&](double) { return left; });
-            token = c0 + i.index;
+            load_chunk(k.index);
+            double w[kPer], sum = 0.0;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) {
+                w[i] = use ? __builtin_fmax(__builtin_fma(-q[i], Z, e[i]), 0.0) : e[i];
+                sum += w[i];
+            }
+            double at = k.before + block_scan(sum, space[1], total);
+            found = last = Pick{-1, 0.0};
+            const int i0 = k.index * kChunk + tid * kPer;
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) consider(found, last, i0 + i, w[i], at, target);
+            token = block_pick(found, last, &pick_space).index;
         }
     }
-    for (int j = threadIdx.x; j <= p.S; j += kThreads)
+    for (int j = tid; j <= p.S; j += kThreads)
         p.tokens[(size_t)b * (p.S + 1) + j] = j < n ? p.draft[(size_t)b * p.S + j] : j == n ? token : -1;
-    if (threadIdx.x == 0) p.accepted[b] = n;
+    if (tid == 0) p.accepted[b] = n;
 }
 
+int spans_of(int V) { return (V + kSpan - 1) / kSpan; }
+
+// Spans per wave of the first launch: one while that leaves up to 16 waves for
+// every compute unit, then more, which spreads a wave's joins over more values.
+int walk_of(int B, int S, int V) { return std::min(8, std::max(1, (int)((long long)B * (S + 1) * spans_of(V) / 4096))); }
 int chunks_of(int V) { return (V + kChunk - 1) / kChunk; }
 
 bool verify_sizes(int B, int S, int V)
@@ -388,8 +659,8 @@ long long qmv_verify_workspace(int B, int S, int V)
 {
     using namespace ops;
     if (!verify_sizes(B, S, V)) return -1;
-    const long long c = chunks_of(V);
-    return piece((long long)sizeof(Stat) * B * (S + 1) * c) + piece(8LL * B * c) + piece(4LL * B);
+    return piece((long long)sizeof(Stat) * B * (S + 1) * spans_of(V)) + piece((long long)sizeof(Part) * B * chunks_of(V)) +
+           piece(4LL * B);
 }
 
 int qmv_verify(const void* logits, const int32_t* draft, const float* uniforms, const void* probs,
@@ -432,12 +703,14 @@ int qmv_verify(const void* logits, const int32_t* draft, const float* uniforms, 
     p.B = B;
     p.S = S;
     p.V = V;
+    p.walk = walk_of(B, S, V);
+    p.stretches = (spans_of(V) + p.walk - 1) / p.walk;
     p.chunks = chunks_of(V);
     char* ws = static_cast<char*>(workspace);
     p.stats = reinterpret_cast<Stat*>(ws);
-    ws += piece((long long)sizeof(Stat) * B * (S + 1) * p.chunks);
-    p.part = reinterpret_cast<double*>(ws);
-    ws += piece(8LL * B * p.chunks);
+    ws += piece((long long)sizeof(Stat) * B * (S + 1) * spans_of(V));
+    p.part = reinterpret_cast<Part*>(ws);
+    ws += piece((long long)sizeof(Part) * B * p.chunks);
     p.tickets = reinterpret_cast<uint32_t*>(ws);
     p.l_batch = l_batch;
     p.l_row = l_row;
@@ -449,28 +722,12 @@ int qmv_verify(const void* logits, const int32_t* draft, const float* uniforms, 
                         : (qf ? (const void*)&sample_kernel<false, true> : (const void*)&sample_kernel<false, false>);
     void* args[] = {&p};
     hipStream_t st = static_cast<hipStream_t>(stream);
-    // the grid's second dimension ends at 65535: batches in slices of whole requests
-    const int step = std::max(1, 65535 / (S + 1));
-    for (int b = 0; b < B; b += step) {
-        VerifyParams s = p;
-        const int n = std::min(step, B - b);
-        s.B = n;
-        s.logits += (size_t)(b * l_batch) * size_of(l_dt);
-        if (S > 0) s.draft += (size_t)b * S;
-        s.u += (size_t)b * (S + 1);
-        if (probs) s.probs += (size_t)(b * q_batch) * size_of(q_dt);
-        if (temperature) s.temperature += b;
-        if (lengths) s.lengths += b;
-        s.tokens += (size_t)b * (S + 1);
-        s.accepted += b;
-        s.stats += (size_t)b * (S + 1) * p.chunks;
-        s.part += (size_t)b * p.chunks;
-        s.tickets += b;
-        args[0] = &s;
-        if (hipLaunchKernel(f1, dim3(p.chunks, n * (S + 1)), dim3(kThreads), args, 0, st) != hipSuccess ||
-            hipLaunchKernel(f2, dim3(p.chunks, n), dim3(kThreads), args, 0, st) != hipSuccess)
-            return QMV_E_LAUNCH;
-    }
+    // Workgroups per request of the second launch: each repeats the decisions, so
+    // no more than are resident at once.
+    const int groups = std::min(p.chunks, std::max(1, 1024 / B));
+    if (hipLaunchKernel(f1, dim3((p.stretches + kWaves - 1) / kWaves, S + 1, B), dim3(kThreads), args, 0, st) != hipSuccess ||
+        hipLaunchKernel(f2, dim3(groups, B), dim3(kThreads), args, 0, st) != hipSuccess)
+        return QMV_E_LAUNCH;
     return QMV_OK;
 }
 

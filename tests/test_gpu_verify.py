@@ -214,6 +214,34 @@ def test_many_requests():
     check(l, draft, u, pr)
 
 
+@pytest.mark.parametrize("logits", ["bf16", "f32"])
+def test_many_rows(logits):
+    """Rows enough that a wave walks several spans and a workgroup several chunks; masks over whole spans; temperatures."""
+    B, S, V = 48, 7, 40001
+    l, draft, u, pr = problem(B, S, V, logits, "bf16", seed=6)
+    l[0, :, 2000:12000] = -math.inf
+    l[1, :, 100:] = -math.inf
+    l[2, :, :39990] = torch.finfo(l.dtype).min
+    l[3, 1, 77] = float("nan")
+    l[4, :, 30000] = math.inf
+    temp = torch.full((B,), 0.8)
+    temp[5], temp[6], temp[7], temp[8], temp[9] = 0.0, 1e-6, 1e-25, 1e25, 3.0
+    lens = (torch.arange(B) * 3 % (S + 1)).int()
+    check(l, draft, u, pr, temp=temp)
+    check(l, draft, u, None, temp=temp, lens=lens)
+
+
+@pytest.mark.parametrize("V", [500, 5000])
+def test_drafter_that_agrees(V):
+    """Where the drafter's probabilities are the target's, rounded to fp32, what is left of them is their rounding."""
+    l, _, u, _ = problem(3, 2, V, seed=8)
+    pr = torch.softmax(l[:, :2].double(), -1).float()
+    check(l, torch.full((3, 2), V, dtype=torch.int32), u, pr)           # no such token: rejected
+    one = pr.clone()
+    one[..., 3] += 0.25                                                   # but for one value, which is below the target's elsewhere
+    check(l, torch.full((3, 2), V, dtype=torch.int32), u, one)
+
+
 def test_long_draft():
     check(*problem(2, 255, 40, seed=5, noise=0.01))
 
