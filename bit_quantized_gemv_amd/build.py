@@ -1,5 +1,6 @@
 """Build the gfx950 HIP library libqmv.so in-tree (hipcc, one object per
-kernel-instance unit, compiled in parallel, then linked)."""
+kernel-instance unit, compiled in parallel, then linked), and the torch binding
+qmv_ops_py.so beside it (g++)."""
 from __future__ import annotations
 
 import concurrent.futures as cf
@@ -13,7 +14,9 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIBDIR = os.path.join(PKG, "lib")
 LIB = os.path.join(LIBDIR, "libqmv.so")
-HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
+PY = os.path.join(LIBDIR, "qmv_ops_py.so")
+ROCM = "/opt/rocm"
+HIPCC = os.environ.get("HIPCC", os.path.join(ROCM, "bin", "hipcc"))
 
 # -ffp-contract=off: every fused multiply-add in the kernels is written out
 # explicitly, so no instance can fuse differently from another.  Packed fp32
@@ -30,11 +33,36 @@ def sources():
 def _compile(src: str) -> str:
     obj = os.path.join(BUILD, os.path.basename(src)[:-4] + ".o")
     cmd = [HIPCC, *FLAGS, "-c", src, "-o", obj]
+    _run(cmd, f"hipcc failed on {src}")
+    return obj
+
+
+def _run(cmd, what: str) -> None:
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:
         sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError(f"hipcc failed on {src}")
+        raise RuntimeError(what)
+
+
+def _compile_binding() -> str:
+    import sysconfig
+    import torch
+    obj = os.path.join(BUILD, "ops_py.o")
+    inc = os.path.join(os.path.dirname(torch.__file__), "include")
+    _run(["g++", "-O2", "-std=c++17", "-fPIC", "-DUSE_ROCM", "-D__HIP_PLATFORM_AMD__=1",
+          f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}", "-I", os.path.join(ROOT, "include"),
+          "-isystem", inc, "-isystem", os.path.join(inc, "torch", "csrc", "api", "include"), "-isystem", f"{ROCM}/include",
+          "-isystem", sysconfig.get_paths()["include"], "-c", os.path.join(CSRC, "ops_py.cpp"), "-o", obj],
+         "g++ failed on ops_py.cpp")
     return obj
+
+
+def _link_binding(obj: str) -> None:
+    import torch
+    _run(["g++", "-shared", "-o", PY + ".tmp", obj, "-L", LIBDIR, "-lqmv", "-L", os.path.join(os.path.dirname(torch.__file__), "lib"),
+          "-lc10", "-ltorch_cpu", "-ltorch_python", "-lc10_hip", "-ltorch_hip", "-Wl,-rpath,$ORIGIN"],
+         "link of qmv_ops_py.so failed")
+    os.replace(PY + ".tmp", PY)
 
 
 def build(jobs: int | None = None) -> str:
@@ -42,14 +70,14 @@ def build(jobs: int | None = None) -> str:
     os.makedirs(LIBDIR, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
+        binding = ex.submit(_compile_binding)
         objs = list(ex.map(_compile, sources()))
+        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
-    r = subprocess.run(cmd, capture_output=True, text=True)
-    if r.returncode != 0:
-        sys.stderr.write(r.stdout + r.stderr)
-        raise RuntimeError("link of libqmv.so failed")
+    _run(cmd, "link of libqmv.so failed")
     os.replace(tmp, LIB)
+    _link_binding(binding)
     return LIB
 
 
