@@ -10,83 +10,129 @@
 namespace ops {
 namespace {
 
+constexpr int kPackWords = kMaxWaves * kWave;   // words of codes whose activations a workgroup of the first kernel packs
+
 // h[piece][m][r] = sum over a piece of K of A_a[r][k] x[m][k].
 //
-// One workgroup per 16 ranks, piece of K and token; it does the work of all
-// tokens of its block of 16 that share the token's adapter, and leaves at once if an
-// earlier one does.  Bound by the latency of one round of loads: every wave
-// has its whole share (8 steps of 16 x 32 values) in flight at once.
+// A workgroup takes 16 ranks, a piece of K and a token: it does the work of all
+// tokens of its block of 64 that share the token's adapter, 16 at a time, and
+// leaves at once if an earlier one does.  Bound by the latency of one round of
+// loads: every wave has its whole share (8 steps of 16 x 32 values) in flight at
+// once.  Workgroups past those list a block's adapters, or pack activations, for
+// the second kernel.
 template <bool XF32, bool ADF16>
-__global__ __launch_bounds__(kMaxWaves* kWave) void shrink_kernel(LoraParams p)
+__global__ __launch_bounds__(kMaxWaves* kWave) void shrink_kernel(LoraParams p, int bits, int gs)
 {
     constexpr int NP = XF32 ? 3 : 1, XV = XF32 ? 2 : 1, STEPS = kShrinkK / kMaxWaves / 32;
     __shared__ float join[kMaxWaves * Join<1>::kWords];
+    __shared__ uint8_t order[kMaxWaves][kBlock];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int r0 = blockIdx.x * 16, z = blockIdx.y, m = blockIdx.z, m0 = m & ~15;
-    const int tok = min(m0 + c, p.M - 1);
+    const int rtiles = p.Rp / 16, blocks = (p.M + kBlock - 1) / kBlock;
+    int at = blockIdx.x;
+    if (at < blocks) {
+        if (wave > 0) return;
+        const int m = at * kBlock + lane, id = p.ids[min(m, p.M - 1)];
+        const bool has = m < p.M && id >= 0 && id < p.L;
+        const float scaling = has && p.scaling ? p.scaling[id] : 1.0f;
+        unsigned long long left = __ballot(has);
+        AdapterList& list = p.lists[at];
+        int n = 0;
+        if (lane == 0) list.any = left;
+        for (; left != 0; ++n) {
+            const int lead = __builtin_ctzll(left), a = __builtin_amdgcn_readlane(id, lead);
+            const unsigned long long same = __ballot(has && id == a);
+            if (lane == lead) {
+                list.scaling[n] = scaling;
+                list.adapter[n] = a;
+                list.tokens[n] = same;
+            }
+            left &= ~same;
+        }
+        if (lane == 0) list.count = n;
+        return;
+    }
+    at -= blocks;
+    if (at >= rtiles * p.pieces * p.M) {
+        const Packed pk(p.K, bits, gs, true);
+        pack(p.x, p.xp, p.M, p.K, pk, XF32, (size_t)(at - rtiles * p.pieces * p.M) * kPackWords + threadIdx.x);
+        return;
+    }
+    const int r0 = at % rtiles * 16, z = at / rtiles % p.pieces, m = at / (rtiles * p.pieces), m0 = m & ~(kBlock - 1);
+    const int tok = min(m0 + lane, p.M - 1);
     const int mine = p.ids[tok], a = p.ids[m];
     if (a < 0 || a >= p.L) return;
-    const uint32_t same = (uint32_t)__ballot(m0 + c < p.M && mine == a) & 0xffffu;
-    if (__builtin_ctz(same) != m - m0) return;
+    const unsigned long long same = __ballot(m0 + lane < p.M && mine == a);
+    if (__builtin_ctzll(same) != m - m0) return;
+    const int n = __popcll(same);
+    if ((same >> lane) & 1) order[wave][__popcll(same & ((1ull << lane) - 1))] = (uint8_t)lane;
+    __builtin_amdgcn_wave_barrier();
 
     const int k0 = z * kShrinkK + wave * (kShrinkK / kMaxWaves);
     const uint16_t* ar = p.la + ((size_t)a * p.R + min(r0 + c, p.R - 1)) * p.K + 8 * q;
-    const char* xr = p.x + ((size_t)tok * p.K + 8 * q) * (XF32 ? 4 : 2);
-    u32x4 av[STEPS], xv[STEPS][XV];
+    u32x4 av[STEPS];
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        const int k = min(k0 + 32 * i, p.K - 32);       // past the end: read, not used
-        av[i] = *reinterpret_cast<const u32x4*>(ar + k);
+    for (int i = 0; i < STEPS; ++i)
+        av[i] = *reinterpret_cast<const u32x4*>(ar + min(k0 + 32 * i, p.K - 32));       // past the end: read, not used
+    for (int t0 = 0; t0 < n; t0 += 16) {
+        const char* xr = p.x + ((size_t)(m0 + order[wave][min(t0 + c, n - 1)]) * p.K + 8 * q) * (XF32 ? 4 : 2);
+        u32x4 xv[STEPS][XV];
 #pragma unroll
-        for (int v = 0; v < XV; ++v)
-            xv[i][v] = reinterpret_cast<const u32x4*>(xr + (size_t)k * (XF32 ? 4 : 2))[v];
-    }
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+        for (int i = 0; i < STEPS; ++i)
 #pragma unroll
-    for (int i = 0; i < STEPS; ++i) {
-        if (k0 + 32 * i >= p.K) break;
-        u32x4 xo[3];
-        if constexpr (XF32)
-            split_f32(__builtin_bit_cast(f32x4, xv[i][0]), __builtin_bit_cast(f32x4, xv[i][XV - 1]), xo);
-        else
-            xo[0] = xv[i][0];
-        if constexpr (ADF16) {
-            u32x4 h, l;
-            split_f16(av[i], h, l);
+            for (int v = 0; v < XV; ++v)
+                xv[i][v] = reinterpret_cast<const u32x4*>(xr + (size_t)min(k0 + 32 * i, p.K - 32) * (XF32 ? 4 : 2))[v];
+        f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int e = 0; e < NP; ++e) acc = mfma(xo[e], l, mfma(xo[e], h, acc));
-        } else {
+        for (int i = 0; i < STEPS; ++i) {
+            if (k0 + 32 * i >= p.K) break;
+            u32x4 xo[3];
+            if constexpr (XF32)
+                split_f32(__builtin_bit_cast(f32x4, xv[i][0]), __builtin_bit_cast(f32x4, xv[i][XV - 1]), xo);
+            else
+                xo[0] = xv[i][0];
+            if constexpr (ADF16) {
+                u32x4 h, l;
+                split_f16(av[i], h, l);
 #pragma unroll
-            for (int e = 0; e < NP; ++e) acc = mfma(xo[e], av[i], acc);
+                for (int e = 0; e < NP; ++e) acc = mfma(xo[e], l, mfma(xo[e], h, acc));
+            } else {
+#pragma unroll
+                for (int e = 0; e < NP; ++e) acc = mfma(xo[e], av[i], acc);
+            }
         }
-    }
-    Join<1>::write(join, wave, lane, 0, acc);
-    __syncthreads();
-    if (threadIdx.x < 256) {
-        const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
-        if ((same >> t) & 1)      // ranks past the last are zero: the second kernel's steps are of 32
-            p.h[((size_t)z * p.M + m0 + t) * p.Rp + r0 + r] =
-                r0 + r < p.R ? Join<1>::sum(join, kMaxWaves, Join<1>::at(r, t)) : 0.0f;
+        if (t0 > 0) __syncthreads();
+        Join<1>::write(join, wave, lane, 0, acc);
+        __syncthreads();
+        if (threadIdx.x < 256) {
+            const int r = threadIdx.x & 15, t = threadIdx.x >> 4;
+            if (t0 + t < n)      // ranks past the last are zero: the second kernel's steps are of 32
+                p.h[((size_t)z * p.M + m0 + order[wave][t0 + t]) * p.Rp + r0 + r] =
+                    r0 + r < p.R ? Join<1>::sum(join, 0, kMaxWaves, Join<1>::at(r, t)) : 0.0f;
+        }
     }
 }
 
-int shrink_launch(const LoraParams& p, bool xf32, hipStream_t st)
+int shrink_launch(const LoraParams& p, int bits, int gs, bool xf32, hipStream_t st)
 {
     const void* fn = xf32 ? (p.adf16 ? (const void*)&shrink_kernel<true, true> : (const void*)&shrink_kernel<true, false>)
                           : (p.adf16 ? (const void*)&shrink_kernel<false, true> : (const void*)&shrink_kernel<false, false>);
     LoraParams q = p;
-    void* args[] = {&q};
-    return hipLaunchKernel(fn, dim3(p.Rp / 16, p.pieces, p.M), dim3(kMaxWaves * kWave), args, 0, st) == hipSuccess ? 0 : 1;
+    void* args[] = {&q, &bits, &gs};
+    const long long blocks = (p.M + kBlock - 1) / kBlock, packs = ((long long)p.M * (p.K * bits / 32) + kPackWords - 1) / kPackWords;
+    const long long grid = blocks + (long long)p.Rp / 16 * p.pieces * p.M + packs;
+    return hipLaunchKernel(fn, dim3((uint32_t)grid), dim3(kMaxWaves * kWave), args, 0, st) == hipSuccess ? 0 : 1;
 }
 
-// Row tiles per workgroup: as many as leave a workgroup for about every
-// compute unit, since a workgroup reads all activations once.
-int row_tiles(int N)
-{
-    const int tiles = (N + 15) / 16;
-    return tiles >= 4 * 200 ? 4 : tiles >= 2 * 200 ? 2 : 1;
-}
+struct LoraPieces {
+    long long h, lists, all;
+    LoraPieces(int M, int K, int R)       // M: tokens of one pair of launches
+    {
+        h = piece(4LL * shrink_pieces(K) * M * pad_rank(R));
+        lists = h + piece((long long)sizeof(AdapterList) * ((M + kBlock - 1) / kBlock));
+        all = lists + piece(6LL * ((M + 15) / 16 * 16) * ((K + 255) / 256 * 256));     // three planes of two bytes, for fp32, in whole slabs
+    }
+};
 
 }  // namespace
 }  // namespace ops
@@ -96,7 +142,7 @@ extern "C" {
 long long qmv_affine_lora_workspace(int M, int K, int rank)
 {
     if (M < 1 || M > QMV_MAX_M || K < 1 || K > QMV_MAX_K || rank < 1 || rank > QMV_MAX_RANK) return -1;
-    return ops::piece(4LL * ops::shrink_pieces(K) * std::min(M, ops::kLoraTile) * ops::pad_rank(rank));
+    return ops::LoraPieces(std::min(M, ops::kLoraTile), K, rank).all;
 }
 
 int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, const void* x,
@@ -126,6 +172,7 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
 
     hipStream_t st = static_cast<hipStream_t>(stream);
     const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16;
+    const LoraPieces at(std::min(M, kLoraTile), K, rank);
     for (int m = 0; m < M; m += kLoraTile) {
         LoraParams p;
         p.w = w;
@@ -138,6 +185,9 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         p.ids = ids + m;
         p.scaling = scaling;
         p.h = static_cast<float*>(workspace);
+        p.lists = reinterpret_cast<AdapterList*>(static_cast<char*>(workspace) + at.h);
+        p.xp = static_cast<char*>(workspace) + at.lists;
+        p.plane = Packed(K, bits, group_size, true).plane(std::min(kLoraTile, M - m));
         p.M = std::min(kLoraTile, M - m);
         p.N = N;
         p.K = K;
@@ -145,10 +195,14 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         p.R = rank;
         p.Rp = pad_rank(rank);
         p.pieces = shrink_pieces(K);
+        p.parts = parts_of(K * bits / 128);
         p.yf32 = y_dt == QMV_DT_F32;
         p.adf16 = ad_dt == QMV_DT_F16;
-        if (shrink_launch(p, xf32, st)) return QMV_E_LAUNCH;
-        const int rt = row_tiles(N), ct = p.M <= 16 ? 1 : p.M <= 32 ? 2 : 4;
+        if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;
+        // Four token tiles read the codes once for 64 tokens; hidden values of more
+        // than 256 ranks of so many do not fit the shared memory.  Two row tiles
+        // halve the reads of activations, one leaves more workgroups.
+        const int ct = p.M <= 16 ? 1 : p.M <= 32 || p.Rp > 256 ? 2 : 4, rt = N >= 8192 ? 2 : 1;
         const int bad = bits == 4 ? (group_size == 64 ? lora_launch_b4_g64(p, rt, ct, xf32, sbf, st)
                                                       : lora_launch_b4_g128(p, rt, ct, xf32, sbf, st))
                                   : (group_size == 64 ? lora_launch_b2_g64(p, rt, ct, xf32, sbf, st)

@@ -6,19 +6,30 @@
 
 namespace ops {
 
-// Eight values of a row of B_a at r.. as bf16 operands: one piece, or two for
-// fp16 (8 + 3 bits).  Ranks that are no multiple of 8 have unaligned rows and are read
-// value by value.
-__device__ __forceinline__ u32x4 load8(const uint16_t* row, int r, int R)
+// Eight values of a row of B_a at r.., zero past the rank.  Ranks that are a
+// multiple of 8 have aligned rows: raw8 is a load, and trim8 clears what is past
+// the rank when it is used; others are read value by value.
+__device__ __forceinline__ u32x4 raw8(const uint16_t* row, int r, int R)
 {
-    if (r >= R) return u32x4{0, 0, 0, 0};
-    if ((R & 7) == 0) return *reinterpret_cast<const u32x4*>(row + r);
+    return *reinterpret_cast<const u32x4*>(row + min(r, R - 8));
+}
+
+__device__ __forceinline__ u32x4 trim8(u32x4 v, int r, int R)
+{
+#pragma unroll
+    for (int d = 0; d < 4; ++d) v[d] = r < R ? v[d] : 0;
+    return v;
+}
+
+__device__ __forceinline__ u32x4 slow8(const uint16_t* row, int r, int R)
+{
+    uint32_t x[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) x[i] = row[min(r + i, R - 1)];
     u32x4 v;
 #pragma unroll
-    for (int d = 0; d < 4; ++d) {
-        const uint32_t a = r + 2 * d < R ? row[r + 2 * d] : 0, b = r + 2 * d + 1 < R ? row[r + 2 * d + 1] : 0;
-        v[d] = a | (b << 16);
-    }
+    for (int d = 0; d < 4; ++d)
+        v[d] = (r + 2 * d < R ? x[2 * d] : 0) | (r + 2 * d + 1 < R ? x[2 * d + 1] << 16 : 0);
     return v;
 }
 
@@ -49,155 +60,248 @@ __device__ __forceinline__ void split_f32(const f32x4& lo, const f32x4& hi, u32x
     }
 }
 
-template <class T>
-__global__ __launch_bounds__(kMaxWaves* kWave) void lora_kernel(LoraParams p)
-{
-    constexpr int RT = T::RT, CT = T::CT;
-    using J = Join<RT>;
-    __shared__ float join[kMaxWaves * J::kWords];
-    __shared__ float delta[J::kWords];
+// LDS of the kernel, in bytes: the scales and biases, the slabs being turned over
+// and, in their place when the product is done, the waves' partial results; the
+// adapters' terms of the workgroup's row tiles, and the hidden values; a byte per
+// token for every wave.
+struct LoraSpace {
+    int biases, turn, delta, hidden, order, bytes;
+    __host__ __device__ LoraSpace(const Meta& meta, int waves, int rt, int ct, int parts, int Rp)
+    {
+        const int tiles = waves / parts * rt, tokens = 16 * ct;
+        biases = meta.bytes(16 * tiles) / 2;
+        turn = 2 * biases;
+        delta = turn + waves * rt * Join<1>::kWords * 4;
+        hidden = delta + tiles * tokens * 64;
+        order = hidden + tokens * (Rp + 4) * 4;
+        bytes = order + waves * kBlock;
+    }
+};
 
+// One workgroup per groups of 16 * RT rows and 16 * CT tokens; the waves of a
+// group each sum a part of K.  What does not depend on another load is asked for
+// first: the first slabs of codes and activations, and by way of the list of
+// adapters the first of their factors and the hidden values, which go to LDS.  The
+// adapters' terms follow the product, their factors streaming through a ring of
+// registers that the product has left.
+template <class T>
+__global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraParams p)
+{
+    constexpr int RT = T::RT, CT = T::CT, DEPTH = 4;
+    using J = Join<RT>;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6;
     const int c = lane & 15, q = lane >> 4;
-    const int n0 = blockIdx.x * 16 * RT, m0 = blockIdx.y * 16 * CT;
+    const int parts = p.parts, groups = waves / parts, tiles = groups * RT;
+    const int first = blockIdx.x * tiles * 16, m0 = blockIdx.y * 16 * CT, tokens = min(16 * CT, p.M - m0);
+    const int n0 = first + wave / parts * RT * 16, part = wave % parts, rows = min(16 * tiles, p.N - first);
+    const Meta meta(16 * tiles, p.K, T::BITS, T::GS, parts);
+    const LoraSpace sp(meta, waves, RT, CT, parts, p.Rp);
+    uint16_t* const scales = reinterpret_cast<uint16_t*>(lds);
+    uint16_t* const biases = reinterpret_cast<uint16_t*>(lds + sp.biases);
+    float* const join = reinterpret_cast<float*>(lds + sp.turn);
+    float* const delta = reinterpret_cast<float*>(lds + sp.delta);
+    float* const hidden = reinterpret_cast<float*>(lds + sp.hidden);
+    uint8_t* const order = reinterpret_cast<uint8_t*>(lds + sp.order) + wave * kBlock;
 
     typename T::Rows r;
-    r.K = p.K;
     r.G = p.K / T::GS;
     r.chunks = p.K / (4 * T::VPW);
-    r.meta_al = r.G % T::NG == 0;
-    const uint16_t* lb_row[RT];
+    r.plane = p.plane;
+    r.turn = lds + sp.turn + wave * T::TURN;
+    r.even = meta.groups % T::NG == 0;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const size_t n = min(n0 + 16 * i + c, p.N - 1);     // rows past the last repeat it and are not stored
-        r.w[i] = reinterpret_cast<const u32x4*>(p.w) + n * r.chunks;
-        r.s[i] = p.s + n * r.G;
-        r.b[i] = p.b + n * r.G;
-        lb_row[i] = p.lb + n * p.R;
+        const int row = min(n0 + 16 * i, p.N - 1);          // rows past the last repeat it and are not stored
+        T::set_codes(r, i, p.w, row, p.N - row);
+        const int at = min(n0 - first + 16 * i + c, rows - 1) * meta.groups;
+        r.s[i] = scales + at;
+        r.b[i] = biases + at;
     }
 #pragma unroll
-    for (int j = 0; j < CT; ++j)
-        r.x[j] = p.x + (size_t)min(m0 + 16 * j + c, p.M - 1) * p.K * (T::XF32 ? 4 : 2);
+    for (int j = 0; j < CT; ++j) T::set_token(r, j, p.xp, min(m0 + 16 * j + c, p.M - 1));
+    const int slabs = slabs_of(r.chunks), s0 = part * slabs / parts, s1 = (part + 1) * slabs / parts;
+    typename T::Ring ring;
+    int a0 = s0, a1 = min(s0 + meta.window, s1);
+    const bool active = n0 < p.N;
+    if (meta.windows == 1) {
+        stage_meta(scales, p.s + (size_t)first * r.G, rows * r.G);
+        stage_meta(biases, p.b + (size_t)first * r.G, rows * r.G);
+    } else {
+        stage_window(scales, p.s + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, 0);
+        stage_window(biases, p.b + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, 0);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            r.s[i] += (part * meta.window - a0) * T::NG;
+            r.b[i] += (part * meta.window - a0) * T::NG;
+        }
+    }
+    T::begin(ring, r, a0, a1);
+
+    // The adapters' terms: a unit is an adapter and a row tile, the waves taking
+    // them in turn.  The adapter's tokens are gathered into the 16 rows of a
+    // matrix instruction, so every token's term has one writer and one order.
+    const AdapterList& list = p.lists[m0 / kBlock];
+    const int units = list.count * tiles;
+    const unsigned long long here = ~0ull >> (64 - 16 * CT), adapted = list.any >> (m0 % kBlock);
+    const bool r8 = p.R % 8 == 0;
+    u32x4 v[DEPTH][2];
+    auto b_row = [&](int u) {
+        return p.lb + ((size_t)list.adapter[u / tiles] * p.N + min(first + u % tiles * 16 + c, p.N - 1)) * p.R;
+    };
+    auto load_unit = [&](u32x4 (&to)[2], int u) {
+        const uint16_t* row = b_row(u);
+        to[0] = raw8(row, 8 * q, p.R);
+        to[1] = raw8(row, 8 * q + 32, p.R);
+    };
+    if (r8 && wave < units) load_unit(v[0], wave);
+    if (units > 0) {
+        const int quads = p.Rp / 4;
+        for (int e = threadIdx.x; e < tokens * quads; e += blockDim.x) {
+            const int t = e / quads, k = e % quads * 4;
+            const char* hp = reinterpret_cast<const char*>(p.h + (size_t)(m0 + t) * p.Rp + k);
+            const size_t piece = (size_t)p.M * p.Rp * 4;
+            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+            for (int z0 = 0; z0 < p.pieces; z0 += 8) {
+                f32x4 x[8];
+#pragma unroll
+                for (int z = 0; z < 8; ++z) x[z] = *reinterpret_cast<const f32x4*>(hp + min(z0 + z, p.pieces - 1) * piece);
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    if (z0 + z < p.pieces)
+#pragma unroll
+                        for (int d = 0; d < 4; ++d) sum[d] += x[z][d];
+            }
+            *reinterpret_cast<f32x4*>(hidden + t * (p.Rp + 4) + k) = sum;
+        }
+    }
+    lds_barrier();
 
     f32x4 acc[RT][CT];
     T::clear(acc);
-    const int n = slabs_of(r.chunks);
-    T::run(acc, r, wave * n / waves, (wave + 1) * n / waves, q);
+    for (int k = 1;; ++k) {
+        if (active) T::run(acc, ring, r, a0, a1);
+        if (k >= meta.windows) break;
+        lds_barrier();
+        stage_window(scales, p.s + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, k);
+        stage_window(biases, p.b + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, k);
+        lds_barrier();
+        a0 = a1;             // a part may end a window early: nothing is left of it then
+        a1 = min(a0 + meta.window, s1);
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            r.s[i] -= meta.window * T::NG;
+            r.b[i] -= meta.window * T::NG;
+        }
+        if (a0 < a1) T::begin(ring, r, a0, a1);
+    }
 
-    const size_t lb_adapter = (size_t)p.N * p.R;
-#pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int mj = m0 + 16 * j;
-        if (mj >= p.M) break;
-#pragma unroll
-        for (int i = 0; i < RT; ++i) J::write(join, wave, lane, i, acc[i][j]);
-
-        // The adapters of these 16 tokens, the waves taking them in turn.  An
-        // adapter's product is computed on all 16 tokens with the others'
-        // hidden values zero, and written for its own alone, so every token's
-        // term has one writer and one order.
-        const int mine = p.ids[min(mj + c, p.M - 1)];
-        const bool has = mj + c < p.M && mine >= 0 && mine < p.L;
-        uint32_t left = (uint32_t)__ballot(has) & 0xffffu;
-        for (int d = 0; left != 0; ++d) {
-            const int a = __builtin_amdgcn_readlane(mine, __builtin_ctz(left));
-            const bool in = has && mine == a;
-            const uint32_t same = (uint32_t)__ballot(in) & 0xffffu;
-            left &= ~same;
-            if (d % waves != wave) continue;
-            f32x4 acc2[RT];
-#pragma unroll
-            for (int i = 0; i < RT; ++i) acc2[i] = f32x4{0.f, 0.f, 0.f, 0.f};
-            const float* hrow = p.h + (size_t)min(mj + c, p.M - 1) * p.Rp;
-            for (int k = 8 * q; k < p.Rp; k += 32) {
-                f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-                if (in)
-                    for (int z = 0; z < p.pieces; ++z) {
-                        const f32x4* hp = reinterpret_cast<const f32x4*>(hrow + (size_t)z * p.M * p.Rp + k);
-                        const f32x4 l4 = hp[0], h4 = hp[1];
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            lo[e] += l4[e];
-                            hi[e] += h4[e];
-                        }
-                    }
+    auto unit = [&](const u32x4 (&b)[2], int u) {
+        const int tile = u % tiles;
+        const unsigned long long mine = (list.tokens[u / tiles] >> (m0 % kBlock)) & here;
+        const int n = __popcll(mine);
+        const float scale = list.scaling[u / tiles];
+        if ((mine >> lane) & 1) order[__popcll(mine & ((1ull << lane) - 1))] = (uint8_t)lane;
+        __builtin_amdgcn_wave_barrier();
+        for (int t0 = 0; t0 < n; t0 += 16) {
+            const float* hrow = hidden + order[min(t0 + c, n - 1)] * (p.Rp + 4) + 8 * q;
+            f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+            for (int k = 0; k < p.Rp; k += 32) {
+                u32x4 x;
+                if (!r8)
+                    x = slow8(b_row(u), 8 * q + k, p.R);
+                else
+                    x = trim8(k == 0 ? b[0] : k == 32 ? b[1] : raw8(b_row(u), 8 * q + k, p.R), 8 * q + k, p.R);
                 u32x4 ho[3];
-                split_f32(lo, hi, ho);
+                split_f32(*reinterpret_cast<const f32x4*>(hrow + k), *reinterpret_cast<const f32x4*>(hrow + k + 4), ho);
+                if (p.adf16) {
+                    u32x4 xh, xl;
+                    split_f16(x, xh, xl);
 #pragma unroll
-                for (int i = 0; i < RT; ++i) {
-                    const u32x4 v = load8(lb_row[i] + (size_t)a * lb_adapter, k, p.R);
-                    if (p.adf16) {
-                        u32x4 vh, vl;
-                        split_f16(v, vh, vl);
+                    for (int e = 0; e < 3; ++e) acc = mfma(ho[e], xl, mfma(ho[e], xh, acc));
+                } else {
 #pragma unroll
-                        for (int e = 0; e < 3; ++e) acc2[i] = mfma(ho[e], vl, mfma(ho[e], vh, acc2[i]));
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 3; ++e) acc2[i] = mfma(ho[e], v, acc2[i]);
-                    }
+                    for (int e = 0; e < 3; ++e) acc = mfma(ho[e], x, acc);
                 }
             }
 #pragma unroll
-            for (int i = 0; i < RT; ++i)
-#pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    if ((same >> (4 * q + e)) & 1) delta[i * J::kTile + e * 64 + lane] = acc2[i][e];
+            for (int e = 0; e < 4; ++e)
+                if (t0 + 4 * q + e < n) delta[(tile * 16 * CT + order[t0 + 4 * q + e]) * 16 + c] = scale * acc[e];
         }
-        __syncthreads();
-        for (int e = threadIdx.x; e < 256 * RT; e += blockDim.x) {
-            const int en = e % (16 * RT), et = e / (16 * RT);
-            if (n0 + en < p.N && mj + et < p.M) {
-                float v = J::sum(join, waves, J::at(en, et));
-                const int a = p.ids[mj + et];
-                if (a >= 0 && a < p.L)
-                    v = __builtin_fmaf(p.scaling ? p.scaling[a] : 1.0f, delta[J::at(en, et)], v);
-                store_y(p.y, (size_t)(mj + et) * p.N + n0 + en, v, p.yf32);
+        __builtin_amdgcn_wave_barrier();
+    };
+    if (r8) {
+#pragma unroll
+        for (int i = 1; i < DEPTH; ++i)
+            if (wave + i * waves < units) load_unit(v[i], wave + i * waves);
+    }
+    for (int u = wave; u < units; u += DEPTH * waves) {
+#pragma unroll
+        for (int i = 0; i < DEPTH; ++i) {
+            const int at = u + i * waves, next = at + DEPTH * waves;
+            if (at < units) {
+                const u32x4 b[2] = {v[i][0], v[i][1]};
+                if (r8 && next < units) load_unit(v[i], next);
+                unit(b, at);
             }
         }
-        if (j + 1 < CT) __syncthreads();
+    }
+
+    lds_barrier();        // the turning space is the join's from here
+#pragma unroll
+    for (int j = 0; j < CT; ++j) {
+        const int mj = 16 * j;
+        if (mj >= tokens) break;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) J::write(join, wave, lane, i, acc[i][j]);
+        lds_barrier();
+        for (int e = threadIdx.x; e < 256 * tiles; e += blockDim.x) {
+            const int en = e % (16 * tiles), t = mj + e / (16 * tiles), n = first + en;
+            if (n < p.N && t < tokens) {
+                const int group = en / (16 * RT);
+                float y = J::sum(join, group * parts, parts, J::at(en % (16 * RT), t & 15));
+                if ((adapted >> t) & 1) y += delta[((en >> 4) * 16 * CT + t) * 16 + (en & 15)];
+                store_y(p.y, (size_t)(m0 + t) * p.N + n, y, p.yf32);
+            }
+        }
+        if (j + 1 < CT) lds_barrier();
     }
 }
 
 template <class T>
 int lora_start(const LoraParams& p, hipStream_t st)
 {
-    const dim3 grid((p.N + 16 * T::RT - 1) / (16 * T::RT), (p.M + 16 * T::CT - 1) / (16 * T::CT));
+    const int waves = waves_of(p.parts), rows = waves / p.parts * 16 * T::RT;
+    const dim3 grid((p.N + rows - 1) / rows, (p.M + 16 * T::CT - 1) / (16 * T::CT));
+    const LoraSpace sp(Meta(rows, p.K, T::BITS, T::GS, p.parts), waves, T::RT, T::CT, p.parts, p.Rp);
+    const void* fn = reinterpret_cast<const void*>(&lora_kernel<T>);
+    if (sp.bytes > 64 * 1024 &&
+        hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, sp.bytes) != hipSuccess)
+        return 1;
     LoraParams q = p;
     void* args[] = {&q};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&lora_kernel<T>), grid,
-                           dim3(kWave * waves_of(p.K / (4 * T::VPW))), args, 0, st) == hipSuccess
-               ? 0
-               : 1;
+    return hipLaunchKernel(fn, grid, dim3(kWave * waves), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }
 
-template <int BITS, int GS, int RT, int CT>
-int lora_types(const LoraParams& p, bool xf32, bool sbf, hipStream_t st)
+template <int BITS, int GS, int RT, int CT, int NP>
+int lora_scales(const LoraParams& p, bool sbf, hipStream_t st)
 {
-    if (xf32) {
-        constexpr int C = CT > 2 ? 2 : CT;     // three pieces of four token tiles do not fit the registers
-        return sbf ? lora_start<Tile<BITS, GS, RT, C, true, true>>(p, st)
-                   : lora_start<Tile<BITS, GS, RT, C, true, false>>(p, st);
-    }
-    return sbf ? lora_start<Tile<BITS, GS, RT, CT, false, true>>(p, st)
-               : lora_start<Tile<BITS, GS, RT, CT, false, false>>(p, st);
+    return sbf ? lora_start<Tile<BITS, GS, RT, CT, NP, true, true>>(p, st) : lora_start<Tile<BITS, GS, RT, CT, NP, false, true>>(p, st);
 }
 
+// Token tiles per wave: as many as the tokens fill and the registers hold.
 template <int BITS, int GS>
 int lora_pick(const LoraParams& p, int rt, int ct, bool xf32, bool sbf, hipStream_t st)
 {
-    if (ct == 1) {
-        if (rt == 1) return lora_types<BITS, GS, 1, 1>(p, xf32, sbf, st);
-        if (rt == 2) return lora_types<BITS, GS, 2, 1>(p, xf32, sbf, st);
-        return lora_types<BITS, GS, 4, 1>(p, xf32, sbf, st);
+    if (xf32) {
+        if constexpr (BITS == 4)
+            if (ct > 1) return lora_scales<BITS, GS, 2, 2, 3>(p, sbf, st);
+        return rt == 1 ? lora_scales<BITS, GS, 1, 1, 3>(p, sbf, st) : lora_scales<BITS, GS, 2, 1, 3>(p, sbf, st);
     }
-    if (ct == 2) {
-        if (rt == 1) return lora_types<BITS, GS, 1, 2>(p, xf32, sbf, st);
-        if (rt == 2) return lora_types<BITS, GS, 2, 2>(p, xf32, sbf, st);
-        return lora_types<BITS, GS, 4, 2>(p, xf32, sbf, st);
-    }
-    if (rt == 1) return lora_types<BITS, GS, 1, 4>(p, xf32, sbf, st);
-    if (rt == 2) return lora_types<BITS, GS, 2, 4>(p, xf32, sbf, st);
-    return lora_types<BITS, GS, 4, 4>(p, xf32, sbf, st);
+    if constexpr (BITS == 4)
+        if (ct == 4) return lora_scales<BITS, GS, 2, 4, 1>(p, sbf, st);
+    if (ct > 1) return lora_scales<BITS, GS, 2, 2, 1>(p, sbf, st);
+    return rt == 1 ? lora_scales<BITS, GS, 1, 1, 1>(p, sbf, st) : lora_scales<BITS, GS, 2, 1, 1>(p, sbf, st);
 }
 
 }  // namespace ops

@@ -15,11 +15,35 @@
 // The layout.  v_mfma_f32_16x16x32_bf16 with the tokens as the first operand's
 // rows and the weight rows as the second's columns: lane l holds token (l & 15)
 // and weight row (l & 15) at k = 8 * (l >> 4) + j, and the result of weight row
-// (l & 15), tokens 4 * (l >> 4) + i.  So the lane that loads a row's codes also
-// needs that row's scale and bias, and no exchange is needed for the fold.
-// Each lane loads 16 bytes of its row (a slab of 4 x 16 bytes per row and wave
-// step); where those hold more than one group, permlane swaps turn the four
-// lanes' words so that every matrix instruction's k lies in one group.
+// (l & 15), tokens 4 * (l >> 4) + i.  So the lane that multiplies a row's codes also
+// needs that row's scale and bias, and no exchange is needed for the fold.  A row's
+// slab is four 16-byte pieces, one per lane that multiplies it; where those hold
+// more than one group, permlane swaps turn the four lanes' words so that every
+// matrix instruction's k lies in one group.
+//
+// Codes.  The vector memory unit takes a wave's addresses four lanes at a time,
+// and lanes that multiply neighbouring rows would have it look up a cache line for
+// every lane.  So four neighbouring lanes load the 64 bytes of one row, and the
+// wave turns the pieces over through LDS (a write and a read of 16 bytes a lane,
+// one slab ahead; which piece a lane loads is swizzled so that the reads meet
+// distinct banks).  Without this, and with scales loaded by each lane for itself, a
+// 17408 x 5120 product of 16 tokens took 51 us instead of TURNED us.
+//
+// Scales and biases go to LDS before the product, whole rows at a time: a row's
+// few bytes per slab would cost as many lookups as its codes.
+//
+// Activations come packed (packed_word): one bf16 plane, or three that add up to
+// an fp32 value exactly, with the two values that a dword of codes meets next to
+// each other and the pieces in the order of the lanes, so they are operands as
+// loaded; 16 tokens together (FRAG), or each by itself where they are gathered.
+//
+// The pipeline.  A wave keeps PF slabs of codes and activations in flight in
+// registers.  Loads come back in order, so the activations, though near,
+// are asked for as early as the codes: an activation load waited for would
+// otherwise wait for every code load before it.  The loop body has no branch
+// around a load, which would make each wait assume the shorter path, and the loads
+// keep their order (slab by slab, before the loop as in it): a wait counts the
+// loads after the one it needs, and takes the smaller count of the two ways in.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -33,7 +57,7 @@ typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
 typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
 
 constexpr int kWave = 64;
-constexpr int kMaxWaves = 8;
+constexpr int kMaxWaves = 8;        // of a workgroup
 
 __device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c)
 {
@@ -79,142 +103,251 @@ __device__ __forceinline__ void store_y(void* y, size_t at, float v, bool f32)
         static_cast<uint16_t*>(y)[at] = to_bf16(v);
 }
 
+// nothing but loads and stores from memory stays on its side
+__device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x78F); }
+
 __device__ __forceinline__ int uniform(int v) { return __builtin_amdgcn_readfirstlane(v); }
 
 // Slabs of K a row of `chunks` 16-byte pieces is walked in, four pieces each.
 __host__ __device__ inline int slabs_of(int chunks) { return (chunks + 3) / 4; }
 
-// Wavefronts that share a row's K: two slabs each at least, so that a wave has
-// a load in flight behind the one it computes on; depends on the row length
-// alone, as the order of the join does.
-inline int waves_of(int chunks)
+// Parts that a row's K is cut into, a wave each: enough waves to keep loads in
+// flight where rows are few, and enough slabs per wave to pay for its start
+// and the join.  Depends on the row length alone, as the order of the join does.
+__host__ __device__ inline int parts_of(int chunks)
 {
     const int n = slabs_of(chunks);
-    return n >= 16 ? 8 : n >= 6 ? 4 : n >= 2 ? 2 : 1;
+    return n >= 64 ? 8 : n >= 24 ? 4 : n >= 4 ? 2 : 1;
 }
 
-template <int BITS_, int GS_, int RT_, int CT_, bool XF32_, bool SBF_>
+// Waves of a workgroup, and row tile groups: the parts of several groups of rows.
+__host__ __device__ inline int waves_of(int parts) { return parts > 4 ? parts : 4; }
+
+// Where a row's packed word lies among a slab's operands, 16 words to a slab: the
+// group and word of the lane and the lane's quarter.
+struct WordAt {
+    int op, q;       // first operand of the word; (l >> 4) of the lane
+};
+
+__host__ __device__ inline WordAt word_at(int w, int bits, int gs)
+{
+    const int fpw = bits == 4 ? 1 : 2, ng = 16 * (32 / bits) / gs;
+    if (ng == 1) return {(w & 3) * fpw, w >> 2};
+    if (ng == 2) return {((w >> 3) * 2 + (w & 1)) * fpw, ((w >> 2) & 1) | (w & 2)};
+    return {(w >> 2) * fpw, w & 3};
+}
+
+// Packed activations: planes of [tiles of 16 tokens][slabs][operands][64 lanes][16 bytes]
+// (FRAG), or of [tokens][slabs][operands][4 quarters][16 bytes].
+struct Packed {
+    int bits, gs, slabs, ops;
+    bool frag;
+    __host__ __device__ Packed(int K, int bits_, int gs_, bool frag_)
+        : bits(bits_), gs(gs_), slabs(slabs_of(K * bits_ / 128)), ops(bits_ == 4 ? 4 : 8), frag(frag_)
+    {
+    }
+    __host__ __device__ size_t plane(int tokens) const { return (size_t)(frag ? (tokens + 15) / 16 * 16 : tokens) * slabs * ops * 64; }
+    // byte offset of the first operand of word w (of a whole row) of a token; further ones are op_step() on
+    __device__ __forceinline__ size_t word(int token, int w) const
+    {
+        const WordAt a = word_at(w & 15, bits, gs);
+        if (frag) return (((size_t)(token >> 4) * slabs + (w >> 4)) * ops + a.op) * 1024 + a.q * 256 + (token & 15) * 16;
+        return (((size_t)token * slabs + (w >> 4)) * ops + a.op) * 64 + a.q * 16;
+    }
+    __device__ __forceinline__ int op_step() const { return frag ? 1024 : 64; }
+};
+
+// One word's activations, VPW values at `from` (fp32 or bf16), to the planes at `to`.
+template <int BITS, bool F32>
+__device__ __forceinline__ void pack_word(const char* from, char* to, size_t plane, int step)
+{
+    constexpr int VPW = 32 / BITS, H = VPW / 2, NV = VPW * (F32 ? 4 : 2) / 16;
+    u32x4 v[NV];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) v[i] = reinterpret_cast<const u32x4*>(from)[i];
+    u32x4 o[F32 ? 3 : 1][H / 4];
+#pragma unroll
+    for (int i = 0; i < H; ++i) {       // dword i pairs values i and i + H
+        if constexpr (F32) {
+            uint32_t ah, am, al, bh, bm, bl;
+            split3(bits_f32(v[i / 4][i % 4]), ah, am, al);
+            split3(bits_f32(v[(i + H) / 4][(i + H) % 4]), bh, bm, bl);
+            o[0][i / 4][i % 4] = hi16(ah, bh);
+            o[1][i / 4][i % 4] = hi16(am, bm);
+            o[2][i / 4][i % 4] = hi16(al, bl);
+        } else {
+            const uint32_t a = v[(i / 2) / 4][(i / 2) % 4], b = v[((i + H) / 2) / 4][((i + H) / 2) % 4];
+            o[0][i / 4][i % 4] = (i & 1) ? hi16(a, b) : lo16(a, b);
+        }
+    }
+#pragma unroll
+    for (int p = 0; p < (F32 ? 3 : 1); ++p)
+#pragma unroll
+        for (int i = 0; i < H / 4; ++i) *reinterpret_cast<u32x4*>(to + p * plane + i * step) = o[p][i];
+}
+
+// Packs word number `at` of the tokens' rows of K values.
+__device__ __forceinline__ void pack(const char* x, char* to, int tokens, int K, const Packed& pk, bool f32, size_t at)
+{
+    const int words = K * pk.bits / 32;
+    if (at >= (size_t)tokens * words) return;
+    const int t = (int)(at / words), w = (int)(at % words);
+    const size_t k = (size_t)t * K + (size_t)w * (32 / pk.bits);
+    char* o = to + pk.word(t, w);
+    const size_t plane = pk.plane(tokens);
+    if (pk.bits == 4) {
+        if (f32)
+            pack_word<4, true>(x + k * 4, o, plane, pk.op_step());
+        else
+            pack_word<4, false>(x + k * 2, o, plane, pk.op_step());
+    } else {
+        if (f32)
+            pack_word<2, true>(x + k * 4, o, plane, pk.op_step());
+        else
+            pack_word<2, false>(x + k * 2, o, plane, pk.op_step());
+    }
+}
+
+// Scales and biases of a workgroup's rows in LDS.  All groups of a row at once
+// where they fit; else a window of each part's groups at a time.
+struct Meta {
+    int groups;        // values per row in LDS
+    int window;        // slabs of a part per window
+    int windows;
+    __host__ __device__ Meta(int rows, int K, int bits, int gs, int parts)
+    {
+        constexpr int kMost = 48 * 1024;
+        const int G = K / gs, slabs = slabs_of(K * bits / 128), ng = 16 * (32 / bits) / gs;
+        const int per = (slabs + parts - 1) / parts;
+        if (rows * G * 4 <= kMost) {
+            groups = G;
+            window = per;
+            windows = 1;
+        } else {
+            window = kMost / (rows * 4 * parts * ng);
+            groups = parts * window * ng;
+            windows = (per + window - 1) / window;
+        }
+    }
+    __host__ __device__ int bytes(int rows) const { return rows * ((groups + 7) / 8 * 8) * 4; }     // both arrays, 16-byte pieces
+};
+
+template <int BITS_, int GS_, int RT_, int CT_, int NP_, bool SBF_, bool FRAG_>
 struct Tile {
     static constexpr int BITS = BITS_, GS = GS_, RT = RT_, CT = CT_;
-    static constexpr bool XF32 = XF32_, SBF = SBF_;
+    static constexpr int NP = NP_;                    // planes of the activations
+    static constexpr bool SBF = SBF_, FRAG = FRAG_;
     static constexpr int VPW = 32 / BITS;             // codes per word
     static constexpr int SLAB = 16 * VPW;             // codes of a row per slab
     static constexpr int NG = SLAB / GS;              // groups per slab
     static constexpr int WPG = 4 / NG;                // words of a lane per group
     static constexpr int FPW = VPW / 8;               // matrix instructions per word
     static constexpr int NF = WPG * FPW;              // and per group
-    static constexpr int NP = XF32 ? 3 : 1;           // bf16 pieces of an activation
-    static constexpr int XV = VPW / (XF32 ? 4 : 8);   // 16-byte loads per word's activations
+    static constexpr int NM = (NG + 1) / 2;           // dwords of scales per slab
+    static constexpr int XOP = FRAG ? 1024 : 64, XQ = FRAG ? 256 : 16;       // bytes from operand to operand, quarter to quarter
     static constexpr uint32_t MASK = BITS == 4 ? 0x00780078u : 0x00600060u;
     static constexpr uint32_t BASE = BITS == 4 ? 0x41804180u : 0x40804080u;  // 16, 4
     static constexpr uint32_t NEG = BITS == 4 ? 0xC180C180u : 0xC080C080u;   // -16, -4
     static constexpr float INV = BITS == 4 ? -1.0f / 16 : -1.0f / 4;
-    // Slabs of codes in flight per wave, about 4 KB; the activations fly with
-    // them where one token tile's fit the registers beside, and are loaded for
-    // the slab at hand otherwise.
-    static constexpr bool XAHEAD = !XF32 && CT == 1;
-    static constexpr int PF = RT == 1 ? 4 : (RT == 2 || (CT == 1 && !XF32)) ? 2 : 1;
+    // slabs in flight: about 90 registers of them, four at most; for one row tile,
+    // taken where there is hardly a workgroup per compute unit, a third more
+    static constexpr int SLAB_REGS = 4 * NG * NF * NP * CT + RT * 4;
+    static constexpr int BUDGET = RT == 1 ? 120 : 90, MOST = RT == 1 ? 8 : 4;
+    static constexpr int PF = SLAB_REGS * 2 > BUDGET ? 1 : BUDGET / SLAB_REGS < MOST ? BUDGET / SLAB_REGS : MOST;
+    // waves per SIMD that its kernels leave registers for
+    static constexpr int WAVES = RT > 1 && SLAB_REGS * PF + 8 * RT * CT <= 90 ? 3 : 2;
+    static constexpr int TURN = RT * 1024;            // bytes of LDS per wave to turn a slab over
 
-    struct Rows {                  // a lane's operands
-        const u32x4* w[RT];        // codes of its weight row
-        const uint16_t* s[RT];     // scales and biases of its weight row
+    struct Rows {                  // what a wave multiplies
+        const char* w[RT];         // the row tiles' codes (the same for all lanes)
+        uint32_t wo[RT];           // the row whose piece the lane loads
+        const uint16_t* s[RT];     // scales and biases of the lane's row in LDS, less the groups before the window
         const uint16_t* b[RT];
-        const char* x[CT];         // its token's activations
-        int chunks, G, K;
-        bool meta_al;              // rows of scales start at a multiple of NG of them
+        const char* x[CT];         // the lane's token
+        size_t plane;              // bytes between the activations' planes
+        char* turn;
+        int chunks, G;
+        bool even;                 // LDS rows start at a multiple of a slab's groups
     };
 
-    struct Slab {
-        u32x4 w[RT];
-        uint32_t s[RT][(NG + 1) / 2], b[RT][(NG + 1) / 2];
-    };
-    struct Acts {
-        u32x4 x[CT][NG][WPG][XV];
+    struct Ring {
+        u32x4 w[PF][RT];
+        u32x4 x[PF][CT][NG][NF][NP];
     };
 
-    static __device__ __forceinline__ void load_meta(uint32_t (&v)[(NG + 1) / 2], const uint16_t* p, int g0,
-                                                     int G, bool al)
+    static __device__ __forceinline__ int lane() { return threadIdx.x & 63; }
+
+    // the piece that lane 4 r + i of a load has: of row r, and which of the four
+    static __device__ __forceinline__ int piece() { return (lane() & 3) ^ ((lane() >> 3) & 3); }
+
+    // codes of the tile i whose first row is `row`, of which `left` exist: lanes past them repeat the last
+    static __device__ __forceinline__ void set_codes(Rows& r, int i, const void* w, size_t row, int left)
+    {
+        r.w[i] = static_cast<const char*>(w) + row * r.chunks * 16;
+        r.wo[i] = (uint32_t)min(lane() >> 2, left - 1) * r.chunks * 16;
+    }
+
+    static __device__ __forceinline__ void set_token(Rows& r, int j, const char* x, int token)
+    {
+        const int q = lane() >> 4;
+        r.x[j] = x + (FRAG ? (size_t)(token >> 4) * 16 : (size_t)token) * slabs_of(r.chunks) * (NG * NF * 64) + q * XQ + (FRAG ? (token & 15) * 16 : 0);
+    }
+
+    static __device__ __forceinline__ void load_w(Ring& t, int u, const Rows& r, int slab)
+    {
+        const uint32_t at = 16 * (uint32_t)min(4 * slab + piece(), r.chunks - 1);   // a part slab's pieces past the row repeat its last
+#pragma unroll
+        for (int i = 0; i < RT; ++i)
+            t.w[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(r.w[i] + (r.wo[i] + at)));
+    }
+
+    static __device__ __forceinline__ void load_x(Ring& t, int u, int j, int g, const Rows& r, int slab)
+    {
+        const char* p = r.x[j] + (size_t)slab * (NG * NF * XOP);
+#pragma unroll
+        for (int f = 0; f < NF; ++f)
+#pragma unroll
+            for (int e = 0; e < NP; ++e)
+                t.x[u][j][g][f][e] = *reinterpret_cast<const u32x4*>(p + (g * NF + f) * XOP + e * r.plane);
+    }
+
+    // a slab's pieces from the lanes that loaded them to those that multiply them
+    static __device__ __forceinline__ void turn(u32x4 (&w)[RT], const Ring& t, int u, const Rows& r)
+    {
+        const int c = lane() & 15, q = lane() >> 4;
+        char* to = r.turn + lane() * 16;
+        const char* from = r.turn + (4 * c + (q ^ ((c >> 1) & 3))) * 16;
+#pragma unroll
+        for (int i = 0; i < RT; ++i) *reinterpret_cast<u32x4*>(to + i * 1024) = t.w[u][i];
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < RT; ++i) w[i] = *reinterpret_cast<const u32x4*>(from + i * 1024);
+        __builtin_amdgcn_wave_barrier();
+    }
+
+    static __device__ __forceinline__ void meta(uint32_t (&v)[NM], const uint16_t* p, bool even)
     {
         if constexpr (NG == 1) {
-            v[0] = p[g0];
-        } else if (al) {
+            v[0] = p[0];
+        } else if (even) {
             if constexpr (NG == 2) {
-                v[0] = *reinterpret_cast<const uint32_t*>(p + g0);
+                v[0] = *reinterpret_cast<const uint32_t*>(p);
             } else {
-                const u32x2 t = *reinterpret_cast<const u32x2*>(p + g0);
+                const u32x2 t = *reinterpret_cast<const u32x2*>(p);
                 v[0] = t[0];
-                v[1] = t[1];
+                v[NM - 1] = t[1];
             }
         } else {
 #pragma unroll
-            for (int i = 0; i < NG; i += 2) {
-                const uint32_t lo = p[min(g0 + i, G - 1)], hi = p[min(g0 + i + 1, G - 1)];
-                v[i / 2] = lo | (hi << 16);
-            }
+            for (int m = 0; m < NM; ++m) v[m] = p[2 * m] | ((uint32_t)p[2 * m + 1] << 16);
         }
     }
 
-    // where a lane's activations for word c of group g of a slab start
-    static __device__ __forceinline__ int x_at(int g, int c, int q)
-    {
-        if constexpr (NG == 1) return (GS / 4) * q + VPW * c;
-        if constexpr (NG == 2) return GS * g + (GS / 2) * (q & 1) + VPW * (2 * (q >> 1) + c);
-        return GS * g + VPW * q;
-    }
-
-    static __device__ __forceinline__ void load(Slab& t, const Rows& r, int slab, int q)
-    {
-        const int chunk = min(4 * slab + q, r.chunks - 1);   // a part slab's lanes past the row read its last piece
-#pragma unroll
-        for (int i = 0; i < RT; ++i) {
-            t.w[i] = __builtin_nontemporal_load(r.w[i] + chunk);
-            load_meta(t.s[i], r.s[i], slab * NG, r.G, r.meta_al);
-            load_meta(t.b[i], r.b[i], slab * NG, r.G, r.meta_al);
-        }
-    }
-
-    static __device__ __forceinline__ void load_x(Acts& t, const Rows& r, int slab, int q)
-    {
-#pragma unroll
-        for (int j = 0; j < CT; ++j)
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-                for (int c = 0; c < WPG; ++c) {
-                    const int k = min(slab * SLAB + x_at(g, c, q), r.K - VPW);
-                    const u32x4* p = reinterpret_cast<const u32x4*>(r.x[j] + (size_t)k * (XF32 ? 4 : 2));
-#pragma unroll
-                    for (int v = 0; v < XV; ++v) t.x[j][g][c][v] = p[v];
-                }
-    }
-
-    static __device__ __forceinline__ float param(const uint32_t (&v)[(NG + 1) / 2], int g)
+    static __device__ __forceinline__ float param(const uint32_t (&v)[NM], int g)
     {
         const uint32_t u = v[g / 2];
         if constexpr (SBF) return bits_f32((g & 1) ? (u & 0xffff0000u) : (u << 16));
         return half_bits((g & 1) ? (u >> 16) : (u & 0xffffu));
-    }
-
-    // The operand of matrix instruction f of a word's activations, whose dword d
-    // pairs fields p = 4 f + d and p + VPW / 2, as the codes' does.
-    static __device__ __forceinline__ void x_operand(const u32x4 (&x)[XV], int f, u32x4 (&o)[NP])
-    {
-        constexpr int H = VPW / 2;
-#pragma unroll
-        for (int d = 0; d < 4; ++d) {
-            const int p = 4 * f + d;
-            if constexpr (!XF32) {
-                const uint32_t a = x[(p / 2) / 4][(p / 2) % 4], b = x[((p + H) / 2) / 4][((p + H) / 2) % 4];
-                o[0][d] = (p & 1) ? hi16(a, b) : lo16(a, b);
-            } else {
-                uint32_t ah, am, al, bh, bm, bl;
-                split3(bits_f32(x[p / 4][p % 4]), ah, am, al);
-                split3(bits_f32(x[(p + H) / 4][(p + H) % 4]), bh, bm, bl);
-                o[0][d] = hi16(ah, bh);
-                o[1][d] = hi16(am, bm);
-                o[2][d] = hi16(al, bl);
-            }
-        }
     }
 
     // the codes of matrix instruction f of a word, as 16 + q (4 + q)
@@ -229,89 +362,120 @@ struct Tile {
         return o;
     }
 
-    static __device__ __forceinline__ void compute(f32x4 (&acc)[RT][CT], Slab& t, const Acts& a, const Rows& r, int slab)
+    // acc += the slab whose codes are w and whose activations are slot u's; where
+    // MORE, those of slab `next` go in flight in their place, piece by piece
+    template <bool MORE>
+    static __device__ __forceinline__ void step(f32x4 (&acc)[RT][CT], u32x4 (&w)[RT], Ring& t, int u, const Rows& r, int slab, int next)
     {
+        uint32_t s[RT][NM], b[RT][NM];
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            meta(s[i], r.s[i] + slab * NG, r.even);
+            meta(b[i], r.b[i] + slab * NG, r.even);
+        }
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             if constexpr (NG >= 2) {
-                const auto u = __builtin_amdgcn_permlane32_swap(t.w[i][0], t.w[i][2], false, false);
-                const auto v = __builtin_amdgcn_permlane32_swap(t.w[i][1], t.w[i][3], false, false);
-                t.w[i] = u32x4{u[0], v[0], u[1], v[1]};
+                const auto p = __builtin_amdgcn_permlane32_swap(w[i][0], w[i][2], false, false);
+                const auto v = __builtin_amdgcn_permlane32_swap(w[i][1], w[i][3], false, false);
+                w[i] = u32x4{p[0], v[0], p[1], v[1]};
             }
             if constexpr (NG == 4) {
-                const auto u = __builtin_amdgcn_permlane16_swap(t.w[i][0], t.w[i][1], false, false);
-                const auto v = __builtin_amdgcn_permlane16_swap(t.w[i][2], t.w[i][3], false, false);
-                t.w[i] = u32x4{u[0], u[1], v[0], v[1]};
+                const auto p = __builtin_amdgcn_permlane16_swap(w[i][0], w[i][1], false, false);
+                const auto v = __builtin_amdgcn_permlane16_swap(w[i][2], w[i][3], false, false);
+                w[i] = u32x4{p[0], p[1], v[0], v[1]};
             }
         }
         const u32x4 neg = {NEG, NEG, NEG, NEG};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            if (g > 0 && slab * NG + g >= r.G) break;
-            u32x4 xo[CT][NF][NP];
-            f32x4 c0[CT];
+            if (!MORE && g > 0 && slab * NG + g >= r.G) break;
+            u32x4 wo[RT][NF];
+#pragma unroll
+            for (int i = 0; i < RT; ++i)
+#pragma unroll
+                for (int c = 0; c < WPG; ++c)
+#pragma unroll
+                    for (int f = 0; f < FPW; ++f) wo[i][c * FPW + f] = w_operand(w[i][g * WPG + c], f);
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
-                c0[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+                f32x4 c0 = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-                for (int c = 0; c < WPG; ++c)
+                for (int f = 0; f < NF; ++f)
 #pragma unroll
-                    for (int f = 0; f < FPW; ++f) {
-                        x_operand(a.x[j][g][c], f, xo[j][c * FPW + f]);
+                    for (int p = 0; p < NP; ++p) c0 = mfma(t.x[u][j][g][f][p], neg, c0);
+                f32x4 d[RT];
 #pragma unroll
-                        for (int p = 0; p < NP; ++p) c0[j] = mfma(xo[j][c * FPW + f][p], neg, c0[j]);
-                    }
-            }
+                for (int i = 0; i < RT; ++i) d[i] = c0;
 #pragma unroll
-            for (int i = 0; i < RT; ++i) {
-                const float s = param(t.s[i], g), nb = param(t.b[i], g) * INV;
-                u32x4 wo[NF];
+                for (int f = 0; f < NF; ++f)
 #pragma unroll
-                for (int c = 0; c < WPG; ++c)
+                    for (int p = 0; p < NP; ++p)
 #pragma unroll
-                    for (int f = 0; f < FPW; ++f) wo[c * FPW + f] = w_operand(t.w[i][g * WPG + c], f);
+                        for (int i = 0; i < RT; ++i) d[i] = mfma(t.x[u][j][g][f][p], wo[i][f], d[i]);
+                if constexpr (MORE) {
+                    keep_order();
+                    load_x(t, u, j, g, r, next);
+                    keep_order();
+                }
 #pragma unroll
-                for (int j = 0; j < CT; ++j) {
-                    f32x4 d = c0[j];
-#pragma unroll
-                    for (int f = 0; f < NF; ++f)
-#pragma unroll
-                        for (int p = 0; p < NP; ++p) d = mfma(xo[j][f][p], wo[f], d);
+                for (int i = 0; i < RT; ++i) {
+                    const float sc = param(s[i], g), nb = param(b[i], g) * INV;
 #pragma unroll
                     for (int e = 0; e < 4; ++e)
-                        acc[i][j][e] = __builtin_fmaf(nb, c0[j][e], __builtin_fmaf(s, d[e], acc[i][j][e]));
+                        acc[i][j][e] = __builtin_fmaf(nb, c0[e], __builtin_fmaf(sc, d[i][e], acc[i][j][e]));
                 }
             }
         }
     }
 
-    // acc += the products over slabs [s0, s1), PF of them in flight
-    static __device__ __forceinline__ void run(f32x4 (&acc)[RT][CT], const Rows& r, int s0, int s1, int q)
+    // slabs s0.. of [s0, s1) (s0 < s1) go in flight
+    static __device__ __forceinline__ void begin(Ring& t, const Rows& r, int s0, int s1)
     {
-        Slab t[PF];
-        Acts x[XAHEAD ? PF : 1];
 #pragma unroll
-        for (int u = 0; u < PF; ++u)
-            if (s0 + u < s1) {
-                if constexpr (XAHEAD) load_x(x[u], r, s0 + u, q);
-                load(t[u], r, s0 + u, q);
-            }
-        for (int s = s0; s < s1; s += PF) {
+        for (int u = 0; u < PF; ++u) {
+            load_w(t, u, r, min(s0 + u, s1 - 1));
+            keep_order();
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+                for (int j = 0; j < CT; ++j) load_x(t, u, j, g, r, min(s0 + u, s1 - 1));
+            keep_order();
+        }
+    }
+
+    // acc += the products over slabs [s0, s1) (none if s0 >= s1), begun by begin.  A
+    // slab's codes are turned over while the one before it is multiplied.
+    static __device__ __forceinline__ void run(f32x4 (&acc)[RT][CT], Ring& t, const Rows& r, int s0, int s1)
+    {
+        if (s0 >= s1) return;
+        u32x4 w[RT];
+        turn(w, t, 0, r);
+        int s = s0;
+        for (; s + PF < s1; s += PF) {
 #pragma unroll
             for (int u = 0; u < PF; ++u) {
-                if (s + u < s1) {
-                    Acts& a = x[XAHEAD ? u : 0];
-                    if constexpr (!XAHEAD) load_x(a, r, s + u, q);
-                    Slab now = t[u];
-                    const Acts an = a;
-                    if (s + u + PF < s1) {
-                        if constexpr (XAHEAD) load_x(a, r, s + u + PF, q);
-                        load(t[u], r, s + u + PF, q);
-                    }
-                    compute(acc, now, an, r, s + u);
-                }
+                __builtin_amdgcn_sched_barrier(0);
+                load_w(t, u, r, min(s + u + PF, s1 - 1));      // slot u's codes are in w
+                keep_order();
+                u32x4 n[RT];
+                turn(n, t, (u + 1) % PF, r);
+                step<true>(acc, w, t, u, r, s + u, min(s + u + PF, s1 - 1));
+#pragma unroll
+                for (int i = 0; i < RT; ++i) w[i] = n[i];
             }
         }
+#pragma unroll
+        for (int u = 0; u < PF; ++u)
+            if (s + u < s1) {
+                __builtin_amdgcn_sched_barrier(0);
+                u32x4 n[RT];
+                if (u + 1 < PF) turn(n, t, (u + 1) % PF, r);
+                step<false>(acc, w, t, u, r, s + u, 0);
+                if (u + 1 < PF)
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) w[i] = n[i];
+            }
     }
 
     static __device__ __forceinline__ void clear(f32x4 (&acc)[RT][CT])
@@ -322,6 +486,35 @@ struct Tile {
             for (int j = 0; j < CT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     }
 };
+
+// `count` scales from memory (16-byte aligned) to LDS, by all threads.
+__device__ __forceinline__ void stage_meta(uint16_t* to, const uint16_t* from, int count)
+{
+    const int whole = count / 8;
+    for (int i = threadIdx.x; i < whole; i += blockDim.x)
+        reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(from)[i];
+    const int at = whole * 8 + threadIdx.x;
+    if (at < count) to[at] = from[at];
+}
+
+// A window of every part's groups, of `rows` rows: row-major, part by part.
+__device__ __forceinline__ void stage_window(uint16_t* to, const uint16_t* from, int rows, int G, int ng, int slabs, int parts,
+                                             int window, int number)
+{
+    const int wg = window * ng, row = parts * wg;
+    for (int i = threadIdx.x; i < rows * row; i += blockDim.x) {
+        const int part = i % row / wg, g = (part * slabs / parts + number * window) * ng + i % wg;
+        if (g < G) to[i] = from[(size_t)(i / row) * G + g];
+    }
+}
+
+// A barrier for LDS alone: loads from memory stay in flight over it.
+__device__ __forceinline__ void lds_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
 
 // The waves' partial results of one 16-token column of tiles, joined in the
 // order of the waves.  Write: wave, row tile and result register; read:
@@ -341,10 +534,11 @@ struct Join {
     {
         return (n >> 4) * kTile + (t & 3) * 64 + (t >> 2) * 16 + (n & 15);
     }
-    static __device__ __forceinline__ float sum(const float* lds, int waves, int at)
+    // of waves first.. in their order
+    static __device__ __forceinline__ float sum(const float* lds, int first, int waves, int at)
     {
-        float v = lds[at];
-        for (int w = 1; w < waves; ++w) v += lds[w * kWords + at];
+        float v = lds[first * kWords + at];
+        for (int w = 1; w < waves; ++w) v += lds[(first + w) * kWords + at];
         return v;
     }
 };

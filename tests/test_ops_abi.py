@@ -112,8 +112,8 @@ def test_verify_refuses(L, kw, code):
 
 
 def test_workspaces(L):
-    assert L.qmv_affine_lora_workspace(1, 512, 5) == 128 * 2           # 32 padded ranks of 4 bytes, in 256-byte pieces
-    assert L.qmv_affine_lora_workspace(65536, 512, 32) == 1024 * 32 * 4
+    assert L.qmv_affine_lora_workspace(1, 512, 5) >= 512 * 2 + 32 * 4          # packed activations, padded ranks
+    assert L.qmv_affine_lora_workspace(65536, 512, 32) == L.qmv_affine_lora_workspace(4096, 512, 32)   # taken in pieces
     for bad in ((0, 512, 5), (1, 0, 5), (1, 512, 0), (1, 512, 513)):
         assert L.qmv_affine_lora_workspace(*bad) == -1
     assert L.qmv_moe_workspace(4, 512, 256, 8, 2) == max(L.qmv_route_workspace(4, 512, 8), L.qmv_experts_workspace(4, 512, 256, 2))
