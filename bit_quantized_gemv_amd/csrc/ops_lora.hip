@@ -26,9 +26,12 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void shrink_kernel(LoraParams p, 
     constexpr int NP = XF32 ? 3 : 1, XV = XF32 ? 2 : 1, STEPS = kShrinkK / kMaxWaves / 32;
     __shared__ float join[kMaxWaves * Join<1>::kWords];
     __shared__ uint8_t order[kMaxWaves][kBlock];
+    __shared__ __attribute__((aligned(16))) char turns[kMaxWaves][1024 * (1 + XV)];
+    together(p.x, p.la, p.ids, p.scaling, p.h, p.lists, p.xp, p.M, p.K, p.L, p.R, p.Rp, p.pieces, bits, gs);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
     const int rtiles = p.Rp / 16, blocks = (p.M + kBlock - 1) / kBlock;
+    char* const turn = turns[wave];
     int at = blockIdx.x;
     if (at < blocks) {
         if (wave > 0) return;
@@ -68,37 +71,52 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void shrink_kernel(LoraParams p, 
     if ((same >> lane) & 1) order[wave][__popcll(same & ((1ull << lane) - 1))] = (uint8_t)lane;
     __builtin_amdgcn_wave_barrier();
 
+    // Four (eight for fp32) neighbouring lanes load a row's pieces, and the wave
+    // turns them over through LDS into the order of the matrix instruction.
     const int k0 = z * kShrinkK + wave * (kShrinkK / kMaxWaves);
-    const uint16_t* ar = p.la + ((size_t)a * p.R + min(r0 + c, p.R - 1)) * p.K + 8 * q;
+    const int row = lane >> 2, pc = (lane & 3) ^ ((row >> 1) & 3);
+    const uint16_t* ar = p.la + ((size_t)a * p.R + min(r0 + row, p.R - 1)) * p.K + 8 * pc;
     u32x4 av[STEPS];
 #pragma unroll
     for (int i = 0; i < STEPS; ++i)
         av[i] = *reinterpret_cast<const u32x4*>(ar + min(k0 + 32 * i, p.K - 32));       // past the end: read, not used
     for (int t0 = 0; t0 < n; t0 += 16) {
-        const char* xr = p.x + ((size_t)(m0 + order[wave][min(t0 + c, n - 1)]) * p.K + 8 * q) * (XF32 ? 4 : 2);
         u32x4 xv[STEPS][XV];
 #pragma unroll
-        for (int i = 0; i < STEPS; ++i)
+        for (int v = 0; v < XV; ++v) {
+            const int t = XF32 ? (lane >> 3) + 8 * v : row, piece = XF32 ? (lane & 7) ^ (t & 7) : 2 * pc;     // of four values
+            const char* xr = p.x + ((size_t)(m0 + order[wave][min(t0 + t, n - 1)]) * p.K + 4 * piece) * (XF32 ? 4 : 2);
 #pragma unroll
-            for (int v = 0; v < XV; ++v)
-                xv[i][v] = reinterpret_cast<const u32x4*>(xr + (size_t)min(k0 + 32 * i, p.K - 32) * (XF32 ? 4 : 2))[v];
+            for (int i = 0; i < STEPS; ++i)
+                xv[i][v] = *reinterpret_cast<const u32x4*>(xr + (size_t)min(k0 + 32 * i, p.K - 32) * (XF32 ? 4 : 2));
+        }
         f32x4 acc = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
         for (int i = 0; i < STEPS; ++i) {
             if (k0 + 32 * i >= p.K) break;
+            *reinterpret_cast<u32x4*>(turn + lane * 16) = av[i];
+#pragma unroll
+            for (int v = 0; v < XV; ++v) *reinterpret_cast<u32x4*>(turn + 1024 + v * 1024 + lane * 16) = xv[i][v];
+            __builtin_amdgcn_wave_barrier();
+            const char* at4 = turn + (4 * c + (q ^ ((c >> 1) & 3))) * 16;
+            const u32x4 ao = *reinterpret_cast<const u32x4*>(at4);
             u32x4 xo[3];
-            if constexpr (XF32)
-                split_f32(__builtin_bit_cast(f32x4, xv[i][0]), __builtin_bit_cast(f32x4, xv[i][XV - 1]), xo);
-            else
-                xo[0] = xv[i][0];
+            if constexpr (XF32) {
+                const char* at8 = turn + 1024 + c * 128;
+                split_f32(*reinterpret_cast<const f32x4*>(at8 + ((2 * q) ^ (c & 7)) * 16),
+                          *reinterpret_cast<const f32x4*>(at8 + ((2 * q + 1) ^ (c & 7)) * 16), xo);
+            } else {
+                xo[0] = *reinterpret_cast<const u32x4*>(at4 + 1024);
+            }
+            __builtin_amdgcn_wave_barrier();
             if constexpr (ADF16) {
                 u32x4 h, l;
-                split_f16(av[i], h, l);
+                split_f16(ao, h, l);
 #pragma unroll
                 for (int e = 0; e < NP; ++e) acc = mfma(xo[e], l, mfma(xo[e], h, acc));
             } else {
 #pragma unroll
-                for (int e = 0; e < NP; ++e) acc = mfma(xo[e], av[i], acc);
+                for (int e = 0; e < NP; ++e) acc = mfma(xo[e], ao, acc);
             }
         }
         if (t0 > 0) __syncthreads();

@@ -60,21 +60,23 @@ __device__ __forceinline__ void split_f32(const f32x4& lo, const f32x4& hi, u32x
     }
 }
 
-// LDS of the kernel, in bytes: the scales and biases, the slabs being turned over
+constexpr int kFactorTurn = 16 * 9 * 16;       // bytes of LDS per wave to turn a unit's factors over
+
+// LDS of the kernel, in bytes: the scales and biases; the slabs being turned over
 // and, in their place when the product is done, the waves' partial results; the
-// adapters' terms of the workgroup's row tiles, and the hidden values; a byte per
-// token for every wave.
+// factors being turned over; the adapters' terms of the workgroup's row tiles; and
+// the hidden values in three bf16 planes.
 struct LoraSpace {
-    int biases, turn, delta, hidden, order, bytes;
+    int biases, turn, factors, delta, hidden, bytes;
     __host__ __device__ LoraSpace(const Meta& meta, int waves, int rt, int ct, int parts, int Rp)
     {
         const int tiles = waves / parts * rt, tokens = 16 * ct;
         biases = meta.bytes(16 * tiles) / 2;
         turn = 2 * biases;
-        delta = turn + waves * rt * Join<1>::kWords * 4;
+        factors = turn + waves * rt * Join<1>::kWords * 4;
+        delta = factors + waves * kFactorTurn;
         hidden = delta + tiles * tokens * 64;
-        order = hidden + tokens * (Rp + 4) * 4;
-        bytes = order + waves * kBlock;
+        bytes = hidden + 3 * tokens * (Rp + 8) * 2;
     }
 };
 
@@ -90,9 +92,10 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     constexpr int RT = T::RT, CT = T::CT, DEPTH = 4;
     using J = Join<RT>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6;
+    together(p.w, p.s, p.b, p.y, p.lb, p.h, p.lists, p.xp, p.plane, p.M, p.N, p.K, p.R, p.Rp, p.pieces, p.parts);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int parts = p.parts, groups = waves / parts, tiles = groups * RT;
+    const int parts = p.parts, waves = waves_of(parts), groups = waves / parts, tiles = groups * RT;       // powers of two
     const int first = blockIdx.x * tiles * 16, m0 = blockIdx.y * 16 * CT, tokens = min(16 * CT, p.M - m0);
     const int n0 = first + wave / parts * RT * 16, part = wave % parts, rows = min(16 * tiles, p.N - first);
     const Meta meta(16 * tiles, p.K, T::BITS, T::GS, parts);
@@ -101,8 +104,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     uint16_t* const biases = reinterpret_cast<uint16_t*>(lds + sp.biases);
     float* const join = reinterpret_cast<float*>(lds + sp.turn);
     float* const delta = reinterpret_cast<float*>(lds + sp.delta);
-    float* const hidden = reinterpret_cast<float*>(lds + sp.hidden);
-    uint8_t* const order = reinterpret_cast<uint8_t*>(lds + sp.order) + wave * kBlock;
+    char* const hidden = lds + sp.hidden;
+    const int hrow = (p.Rp + 8) * 2, hplane = 16 * CT * hrow;
 
     typename T::Rows r;
     r.G = p.K / T::GS;
@@ -124,55 +127,83 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     typename T::Ring ring;
     int a0 = s0, a1 = min(s0 + meta.window, s1);
     const bool active = n0 < p.N;
+    MetaCopy<4> copy(p.s + (size_t)first * r.G, p.b + (size_t)first * r.G, rows * r.G, kWave * waves);
     if (meta.windows == 1) {
-        stage_meta(scales, p.s + (size_t)first * r.G, rows * r.G);
-        stage_meta(biases, p.b + (size_t)first * r.G, rows * r.G);
+        copy.ask();
     } else {
-        stage_window(scales, p.s + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, 0);
-        stage_window(biases, p.b + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, 0);
+        stage_window(scales, copy.s, rows, r.G, T::NG, slabs, parts, meta.window, 0, kWave * waves);
+        stage_window(biases, copy.b, rows, r.G, T::NG, slabs, parts, meta.window, 0, kWave * waves);
 #pragma unroll
         for (int i = 0; i < RT; ++i) {
             r.s[i] += (part * meta.window - a0) * T::NG;
             r.b[i] += (part * meta.window - a0) * T::NG;
         }
     }
+    keep_order();
     T::begin(ring, r, a0, a1);
 
     // The adapters' terms: a unit is an adapter and a row tile, the waves taking
-    // them in turn.  The adapter's tokens are gathered into the 16 rows of a
-    // matrix instruction, so every token's term has one writer and one order.
+    // them in turn.  An adapter's product is computed on whole tiles of 16 tokens and
+    // kept for its own tokens alone, so every token's term has one writer and one
+    // order.  Lane l holds entry l of the list.
     const AdapterList& list = p.lists[m0 / kBlock];
-    const int units = list.count * tiles;
-    const unsigned long long here = ~0ull >> (64 - 16 * CT), adapted = list.any >> (m0 % kBlock);
+    const int list_adapter = list.adapter[lane], list_count = list.count;
+    const float list_scaling = list.scaling[lane];
+    const unsigned long long list_tokens = list.tokens[lane] >> (m0 % kBlock), adapted = list.any >> (m0 % kBlock);
+    const int units = uniform(list_count) * tiles, shift = __builtin_ctz(tiles);
     const bool r8 = p.R % 8 == 0;
     u32x4 v[DEPTH][2];
-    auto b_row = [&](int u) {
-        return p.lb + ((size_t)list.adapter[u / tiles] * p.N + min(first + u % tiles * 16 + c, p.N - 1)) * p.R;
+    // A unit's factors up to rank 64 lie together: the lanes load them in order
+    // and turn them over through LDS, a row's pieces at an odd stride of 16 bytes.
+    const int pieces = min(p.R / 8, 8), stride = pieces | 1;
+    int at_row[2], at_piece[2];
+#pragma unroll
+    for (int s = 0; s < 2; ++s) {
+        at_row[s] = (lane + 64 * s) / max(pieces, 1);
+        at_piece[s] = (lane + 64 * s) % max(pieces, 1);
+    }
+    auto unit_rows = [&](int u) {
+        const int a = __builtin_amdgcn_readlane(list_adapter, u >> shift);
+        return p.lb + ((size_t)a * p.N + first + (u & (tiles - 1)) * 16) * p.R;
     };
+    auto unit_left = [&](int u) { return min(16, p.N - (first + (u & (tiles - 1)) * 16)); };       // none past the last row
     auto load_unit = [&](u32x4 (&to)[2], int u) {
-        const uint16_t* row = b_row(u);
-        to[0] = raw8(row, 8 * q, p.R);
-        to[1] = raw8(row, 8 * q + 32, p.R);
+        const uint16_t* rows = unit_rows(u);
+        const int last = unit_left(u) - 1;
+#pragma unroll
+        for (int s = 0; s < 2; ++s)
+            to[s] = *reinterpret_cast<const u32x4*>(rows + (size_t)min(at_row[s], last) * p.R + at_piece[s] * 8);
     };
-    if (r8 && wave < units) load_unit(v[0], wave);
+    char* const turn = lds + sp.factors + wave * kFactorTurn;
+    if (r8 && wave < units && unit_left(wave) > 0) load_unit(v[0], wave);
+    if (meta.windows == 1) copy.put(scales, biases);
     if (units > 0) {
-        const int quads = p.Rp / 4;
-        for (int e = threadIdx.x; e < tokens * quads; e += blockDim.x) {
-            const int t = e / quads, k = e % quads * 4;
+        const int octs = p.Rp / 8;
+        for (int e = threadIdx.x; e < tokens * octs; e += kWave * waves) {
+            const int t = e / octs, k = e % octs * 8;
             const char* hp = reinterpret_cast<const char*>(p.h + (size_t)(m0 + t) * p.Rp + k);
             const size_t piece = (size_t)p.M * p.Rp * 4;
-            f32x4 sum = {0.f, 0.f, 0.f, 0.f};
+            f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
             for (int z0 = 0; z0 < p.pieces; z0 += 8) {
-                f32x4 x[8];
+                f32x4 x[8][2];
 #pragma unroll
-                for (int z = 0; z < 8; ++z) x[z] = *reinterpret_cast<const f32x4*>(hp + min(z0 + z, p.pieces - 1) * piece);
+                for (int z = 0; z < 8; ++z)
+#pragma unroll
+                    for (int i = 0; i < 2; ++i)
+                        x[z][i] = reinterpret_cast<const f32x4*>(hp + min(z0 + z, p.pieces - 1) * piece)[i];
 #pragma unroll
                 for (int z = 0; z < 8; ++z)
                     if (z0 + z < p.pieces)
 #pragma unroll
-                        for (int d = 0; d < 4; ++d) sum[d] += x[z][d];
+                        for (int d = 0; d < 4; ++d) {
+                            lo[d] += x[z][0][d];
+                            hi[d] += x[z][1][d];
+                        }
             }
-            *reinterpret_cast<f32x4*>(hidden + t * (p.Rp + 4) + k) = sum;
+            u32x4 o[3];
+            split_f32(lo, hi, o);
+#pragma unroll
+            for (int i = 0; i < 3; ++i) *reinterpret_cast<u32x4*>(hidden + i * hplane + t * hrow + k * 2) = o[i];
         }
     }
     lds_barrier();
@@ -183,8 +214,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         if (active) T::run(acc, ring, r, a0, a1);
         if (k >= meta.windows) break;
         lds_barrier();
-        stage_window(scales, p.s + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, k);
-        stage_window(biases, p.b + (size_t)first * r.G, rows, r.G, T::NG, slabs, parts, meta.window, k);
+        stage_window(scales, copy.s, rows, r.G, T::NG, slabs, parts, meta.window, k, kWave * waves);
+        stage_window(biases, copy.b, rows, r.G, T::NG, slabs, parts, meta.window, k, kWave * waves);
         lds_barrier();
         a0 = a1;             // a part may end a window early: nothing is left of it then
         a1 = min(a0 + meta.window, s1);
@@ -196,53 +227,66 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         if (a0 < a1) T::begin(ring, r, a0, a1);
     }
 
-    auto unit = [&](const u32x4 (&b)[2], int u) {
-        const int tile = u % tiles;
-        const unsigned long long mine = (list.tokens[u / tiles] >> (m0 % kBlock)) & here;
-        const int n = __popcll(mine);
-        const float scale = list.scaling[u / tiles];
-        if ((mine >> lane) & 1) order[__popcll(mine & ((1ull << lane) - 1))] = (uint8_t)lane;
-        __builtin_amdgcn_wave_barrier();
-        for (int t0 = 0; t0 < n; t0 += 16) {
-            const float* hrow = hidden + order[min(t0 + c, n - 1)] * (p.Rp + 4) + 8 * q;
+    auto unit = [&](const u32x4 (&raw)[2], int u) {
+        const int tile = u & (tiles - 1), left = unit_left(u), entry = u >> shift;
+        if (left <= 0) return;
+        const unsigned long long mine =
+            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)list_tokens, entry) |
+            (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(list_tokens >> 32), entry) << 32;
+        const float scale = bits_f32(__builtin_amdgcn_readlane(f32_bits(list_scaling), entry));
+        const uint16_t* const row = unit_rows(u) + (size_t)min(c, left - 1) * p.R;
+        u32x4 b[2];
+        if (r8) {
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                if (at_row[s] < 16) *reinterpret_cast<u32x4*>(turn + (at_row[s] * stride + at_piece[s]) * 16) = raw[s];
+            __builtin_amdgcn_wave_barrier();
+#pragma unroll
+            for (int s = 0; s < 2; ++s)
+                b[s] = trim8(*reinterpret_cast<const u32x4*>(turn + (c * stride + min(q + 4 * s, pieces - 1)) * 16), 8 * q + 32 * s, p.R);
+            __builtin_amdgcn_wave_barrier();
+        } else {
+#pragma unroll
+            for (int s = 0; s < 2; ++s) b[s] = slow8(row, 8 * q + 32 * s, p.R);
+        }
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const uint32_t of_tile = (uint32_t)(mine >> (16 * j)) & 0xffffu;
+            if (of_tile == 0) continue;
+            const char* hr = hidden + (16 * j + c) * hrow + 16 * q;
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-            for (int k = 0; k < p.Rp; k += 32) {
-                u32x4 x;
-                if (!r8)
-                    x = slow8(b_row(u), 8 * q + k, p.R);
-                else
-                    x = trim8(k == 0 ? b[0] : k == 32 ? b[1] : raw8(b_row(u), 8 * q + k, p.R), 8 * q + k, p.R);
-                u32x4 ho[3];
-                split_f32(*reinterpret_cast<const f32x4*>(hrow + k), *reinterpret_cast<const f32x4*>(hrow + k + 4), ho);
-                if (p.adf16) {
-                    u32x4 xh, xl;
-                    split_f16(x, xh, xl);
+            auto step = [&](const u32x4& x, int k) {
+                u32x4 xh = x, xl = x;
+                if (p.adf16) split_f16(x, xh, xl);
 #pragma unroll
-                    for (int e = 0; e < 3; ++e) acc = mfma(ho[e], xl, mfma(ho[e], xh, acc));
-                } else {
-#pragma unroll
-                    for (int e = 0; e < 3; ++e) acc = mfma(ho[e], x, acc);
+                for (int e = 0; e < 3; ++e) {
+                    const u32x4 ho = *reinterpret_cast<const u32x4*>(hr + e * hplane + 2 * k);
+                    acc = mfma(ho, xh, acc);
+                    if (p.adf16) acc = mfma(ho, xl, acc);
                 }
-            }
+            };
+            step(b[0], 0);
+            if (p.Rp > 32) step(b[1], 32);
+            for (int k = 64; k < p.Rp; k += 32)
+                step(r8 ? trim8(raw8(row, 8 * q + k, p.R), 8 * q + k, p.R) : slow8(row, 8 * q + k, p.R), k);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
-                if (t0 + 4 * q + e < n) delta[(tile * 16 * CT + order[t0 + 4 * q + e]) * 16 + c] = scale * acc[e];
+                if ((of_tile >> (4 * q + e)) & 1) delta[(tile * 16 * CT + 16 * j + 4 * q + e) * 16 + c] = scale * acc[e];
         }
-        __builtin_amdgcn_wave_barrier();
     };
     if (r8) {
 #pragma unroll
         for (int i = 1; i < DEPTH; ++i)
-            if (wave + i * waves < units) load_unit(v[i], wave + i * waves);
+            if (wave + i * waves < units && unit_left(wave + i * waves) > 0) load_unit(v[i], wave + i * waves);
     }
     for (int u = wave; u < units; u += DEPTH * waves) {
 #pragma unroll
         for (int i = 0; i < DEPTH; ++i) {
             const int at = u + i * waves, next = at + DEPTH * waves;
             if (at < units) {
-                const u32x4 b[2] = {v[i][0], v[i][1]};
-                if (r8 && next < units) load_unit(v[i], next);
-                unit(b, at);
+                const u32x4 raw[2] = {v[i][0], v[i][1]};
+                if (r8 && next < units && unit_left(next) > 0) load_unit(v[i], next);
+                unit(raw, at);
             }
         }
     }
@@ -255,8 +299,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
 #pragma unroll
         for (int i = 0; i < RT; ++i) J::write(join, wave, lane, i, acc[i][j]);
         lds_barrier();
-        for (int e = threadIdx.x; e < 256 * tiles; e += blockDim.x) {
-            const int en = e % (16 * tiles), t = mj + e / (16 * tiles), n = first + en;
+        for (int e = threadIdx.x; e < 256 * tiles; e += kWave * waves) {
+            const int en = e & (16 * tiles - 1), t = mj + (e >> (4 + shift)), n = first + en;
             if (n < p.N && t < tokens) {
                 const int group = en / (16 * RT);
                 float y = J::sum(join, group * parts, parts, J::at(en % (16 * RT), t & 15));

@@ -26,6 +26,8 @@ struct RouteParams {
     int32_t* ids;
     int T, D, E, k, pieces;
     bool renorm;
+    char* xp;           // where not null: the activations packed for codes of `bits` in groups of `gs`
+    int bits, gs;
 };
 
 // Eight values of a row at d.. as doubles; zero past the row's end.
@@ -64,8 +66,16 @@ template <bool XF32, bool RF32>
 __global__ __launch_bounds__(kRouteWaves* kWave) void logits_kernel(RouteParams p)
 {
     __shared__ double join[kRouteWaves][4][64];
+    together(p.x, p.r, p.part, p.xp, p.T, p.D, p.E, p.pieces, p.bits, p.gs);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15, q = lane >> 4;
-    const int e0 = blockIdx.x * 16, t0 = blockIdx.y * 16, z = blockIdx.z;
+    const int etiles = (p.E + 15) / 16, ttiles = (p.T + 15) / 16;
+    int at = blockIdx.x;
+    if (at >= etiles * ttiles * p.pieces) {
+        const Packed pk(p.D, p.bits, p.gs, false);
+        pack(p.x, p.xp, p.T, p.D, pk, XF32, (size_t)(at - etiles * ttiles * p.pieces) * (kRouteWaves * kWave) + threadIdx.x);
+        return;
+    }
+    const int e0 = at % etiles * 16, t0 = at / etiles % ttiles * 16, z = at / (etiles * ttiles);
     const char* xr = p.x + (size_t)min(t0 + c, p.T - 1) * p.D * (XF32 ? 4 : 2);
     const char* rr = p.r + (size_t)min(e0 + c, p.E - 1) * p.D * (RF32 ? 4 : 2);
     const int d0 = z * kRouteK + wave * (kRouteK / kRouteWaves) + 8 * q;
@@ -88,70 +98,91 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void logits_kernel(RouteParams 
     if (t < p.T && e < p.E) p.part[((size_t)z * p.T + t) * p.E + e] = v;
 }
 
-struct Best {
-    double v;
-    int i;
-};
-
-__device__ __forceinline__ Best better(Best a, Best b) { return b.v > a.v || (b.v == a.v && b.i < a.i) ? b : a; }
-
-// Top-k and softmax of one token's logits by a wave: lane l holds the experts
-// l + 64 j; k rounds of the largest left.
-__global__ __launch_bounds__(4 * kWave) void topk_kernel(RouteParams p)
+__global__ __launch_bounds__(kRouteWaves* kWave) void pack_kernel(const char* x, char* xp, int T, int D, int bits, int gs, bool f32)
 {
-    constexpr int PER = QMV_MAX_EXPERTS / kWave;
-    const int lane = threadIdx.x & 63, t = blockIdx.x * 4 + uniform(threadIdx.x >> 6);
-    if (t >= p.T) return;
-    double v[PER];
-    int id[PER];
+    const Packed pk(D, bits, gs, false);
+    pack(x, xp, T, D, pk, f32, (size_t)blockIdx.x * (kRouteWaves * kWave) + threadIdx.x);
+}
+
+// Top-k and softmax of one token's logits by a workgroup.  An expert's place is the
+// number of experts before it (a larger logit, or an equal one of a lower index),
+// counted against all of them from LDS; with few experts the threads share the
+// counting of each.
+__global__ __launch_bounds__(kRouteWaves* kWave) void topk_kernel(RouteParams p)
+{
+    constexpr int THREADS = kRouteWaves * kWave, PER = QMV_MAX_EXPERTS / THREADS;
+    __shared__ double value[QMV_MAX_EXPERTS];
+    __shared__ int place[QMV_MAX_EXPERTS];
+    __shared__ double top_value[QMV_MAX_TOP_K];
+    __shared__ int top_id[QMV_MAX_TOP_K];
+    __shared__ double sums[kRouteWaves];
+    together(p.part, p.weights, p.ids, p.T, p.E, p.k, p.pieces);
+    const int tid = threadIdx.x, t = blockIdx.x;
     const double low = -__builtin_huge_val();
+    double v[PER];
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
-        const int e = lane + kWave * j;
+        const int e = tid + THREADS * j;
         v[j] = low;
-        id[j] = 0x7fffffff;
-        if (e < p.E) {
+        if (THREADS * j < p.E && e < p.E) {
             double s = 0.0;
-            for (int z = 0; z < p.pieces; ++z) s += p.part[((size_t)z * p.T + t) * p.E + e];
+            for (int z0 = 0; z0 < p.pieces; z0 += 8) {
+                double x[8];
+#pragma unroll
+                for (int z = 0; z < 8; ++z) x[z] = p.part[((size_t)min(z0 + z, p.pieces - 1) * p.T + t) * p.E + e];
+#pragma unroll
+                for (int z = 0; z < 8; ++z)
+                    if (z0 + z < p.pieces) s += x[z];
+            }
             v[j] = s != s ? low : s;
-            id[j] = e;
+            value[e] = v[j];
+            place[e] = 0;
         }
     }
-    double mine = 0.0, all = 0.0, top = 0.0;
-    int my_id = 0;
-    for (int r = 0; r < p.k; ++r) {
-        Best b{low, 0x7fffffff};
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (kWave * j < p.E) b = better(b, Best{v[j], id[j]});
-#pragma unroll
-        for (int o = 32; o > 0; o >>= 1) b = better(b, Best{__shfl_xor(b.v, o), __shfl_xor(b.i, o)});
-        if (r == 0) {
-            top = b.v;
-            if (!p.renorm) {
-#pragma unroll
-                for (int j = 0; j < PER; ++j)
-                    if (id[j] < p.E) all += exp(v[j] - top);
-#pragma unroll
-                for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
-            }
+    __syncthreads();
+    const int share = p.E <= 64 ? 4 : p.E <= 128 ? 2 : 1, wide = THREADS / share;      // threads per expert; experts at a time
+    for (int e = tid % wide; e < p.E; e += wide) {
+        const int part = tid / wide, j0 = part * p.E / share, j1 = (part + 1) * p.E / share;
+        const double mine = value[e];
+        int n = 0;
+#pragma unroll 8
+        for (int j = j0; j < j1; ++j) {
+            const double x = value[j];
+            n += x > mine || (x == mine && j < e) ? 1 : 0;
         }
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-            if (id[j] == b.i) {
-                v[j] = low;
-                id[j] = 0x7fffffff;
-            }
-        const double w = exp(b.v - top);
-        if (p.renorm) all += w;
-        if (lane == r) {
-            mine = w;
-            my_id = b.i;
+        if (share == 1)
+            place[e] = n;
+        else
+            atomicAdd(&place[e], n);
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += THREADS) {
+        const int at = place[e];
+        if (at < p.k) {
+            top_value[at] = value[e];
+            top_id[at] = e;
         }
     }
-    if (lane < p.k) {
-        p.weights[(size_t)t * p.k + lane] = (float)(mine / all);
-        p.ids[(size_t)t * p.k + lane] = my_id;
+    __syncthreads();
+    const double top = top_value[0];
+    double all = 0.0;
+    if (p.renorm) {
+        for (int j = 0; j < p.k; ++j) all += exp(top_value[j] - top);
+    } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+            if (tid + THREADS * j < p.E) all += exp(v[j] - top);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) all += __shfl_xor(all, o);
+        if ((tid & 63) == 0) sums[tid >> 6] = all;
+        __syncthreads();
+        all = sums[0];
+#pragma unroll
+        for (int w = 1; w < kRouteWaves; ++w) all += sums[w];
+    }
+    if (tid < p.k) {
+        p.weights[(size_t)t * p.k + tid] = (float)(exp(top_value[tid] - top) / all);
+        p.ids[(size_t)t * p.k + tid] = top_id[tid];
     }
 }
 
@@ -194,69 +225,92 @@ int check_experts(int T, int D, int F, int E, int k, int bits, int gs, int x_dt,
     return QMV_OK;
 }
 
-int run_route(const char* x, const void* router, float* weights, int32_t* ids, void* ws, int T, int D, int E, int k,
-              bool renorm, int x_dt, int r_dt, hipStream_t st)
+// the router of n tokens; where xp is not null their activations are packed too
+int run_route(const char* x, const void* router, float* weights, int32_t* ids, void* part, char* xp, int n, int D, int E, int k,
+              bool renorm, int x_dt, int r_dt, int bits, int gs, hipStream_t st)
 {
     const bool xf = x_dt == QMV_DT_F32, rf = r_dt == QMV_DT_F32;
     const void* fn = xf ? (rf ? (const void*)&logits_kernel<true, true> : (const void*)&logits_kernel<true, false>)
                         : (rf ? (const void*)&logits_kernel<false, true> : (const void*)&logits_kernel<false, false>);
-    for (int t = 0; t < T; t += kMoeTile) {
-        RouteParams p;
-        p.x = x + (size_t)t * D * size_of(x_dt);
-        p.r = static_cast<const char*>(router);
-        p.part = static_cast<double*>(ws);
-        p.weights = weights + (size_t)t * k;
-        p.ids = ids + (size_t)t * k;
-        p.T = std::min(kMoeTile, T - t);
-        p.D = D;
-        p.E = E;
-        p.k = k;
-        p.pieces = route_pieces(D);
-        p.renorm = renorm;
-        void* args[] = {&p};
-        if (!launch(fn, dim3((E + 15) / 16, (p.T + 15) / 16, p.pieces), kRouteWaves * kWave, args, st) ||
-            !launch((const void*)&topk_kernel, dim3((p.T + 3) / 4), 4 * kWave, args, st))
-            return QMV_E_LAUNCH;
-    }
-    return QMV_OK;
+    RouteParams p;
+    p.x = x;
+    p.r = static_cast<const char*>(router);
+    p.part = static_cast<double*>(part);
+    p.weights = weights;
+    p.ids = ids;
+    p.T = n;
+    p.D = D;
+    p.E = E;
+    p.k = k;
+    p.pieces = route_pieces(D);
+    p.renorm = renorm;
+    p.xp = xp;
+    p.bits = bits;
+    p.gs = gs;
+    constexpr int threads = kRouteWaves * kWave;
+    const int packs = xp ? (int)(((long long)n * (D * bits / 32) + threads - 1) / threads) : 0;
+    void* args[] = {&p};
+    return launch(fn, dim3((E + 15) / 16 * ((n + 15) / 16) * p.pieces + packs), threads, args, st) &&
+                   launch((const void*)&topk_kernel, dim3(n), threads, args, st)
+               ? QMV_OK
+               : QMV_E_LAUNCH;
 }
 
-int run_experts(const char* x, const float* weights, const int32_t* ids, const uint32_t* w13, const void* s13,
-                const void* b13, const uint32_t* w2, const void* s2, const void* b2, char* y, void* ws, int T, int D,
-                int F, int E, int k, int bits, int gs, int x_dt, int sb_dt, int y_dt, hipStream_t st)
+// Scratch memory of the experts' products for n tokens.
+struct ExpertPieces {
+    long long h, z, all;       // where the hidden values and the outputs start; the packed activations come first
+    size_t x_plane, h_plane;
+    ExpertPieces(int n, int D, int F, int k, int bits, int gs)
+    {
+        x_plane = Packed(D, bits, gs, false).plane(n);
+        h_plane = Packed(F, bits, gs, false).plane(n * k);
+        h = piece(3 * (long long)x_plane);
+        z = h + piece(3 * (long long)h_plane);
+        all = z + piece(4LL * n * k * D);
+    }
+};
+
+// The same for any codes: rows are rounded up to whole slabs of 256 or 128 codes, so the larger bounds both.
+long long expert_bytes(int T, int D, int F, int k)
+{
+    return ExpertPieces(std::min(T, kMoeTile), (D + 255) / 256 * 256, (F + 255) / 256 * 256, k, 4, 64).all;
+}
+
+// the experts of n tokens, whose activations lie packed at the start of ws
+int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, const void* s13, const void* b13,
+                const uint32_t* w2, const void* s2, const void* b2, char* y, char* ws, int n, int D, int F, int E, int k, int bits,
+                int gs, int x_dt, int sb_dt, int y_dt, hipStream_t st)
 {
     const auto go = bits == 4 ? (gs == 64 ? expert_launch_b4_g64 : expert_launch_b4_g128)
                               : (gs == 64 ? expert_launch_b2_g64 : expert_launch_b2_g128);
     const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16;
     bool yf32 = y_dt == QMV_DT_F32;
-    for (int t = 0; t < T; t += kMoeTile) {
-        const int n = std::min(kMoeTile, T - t);
-        ExpertParams p;
-        p.x = x + (size_t)t * D * size_of(x_dt);
-        p.ids = ids + (size_t)t * k;
-        p.w13 = w13;
-        p.s13 = static_cast<const uint16_t*>(s13);
-        p.b13 = static_cast<const uint16_t*>(b13);
-        p.w2 = w2;
-        p.s2 = static_cast<const uint16_t*>(s2);
-        p.b2 = static_cast<const uint16_t*>(b2);
-        p.P = n * k;
-        p.k = k;
-        p.D = D;
-        p.F = F;
-        p.E = E;
-        p.slots = std::min(p.P, E);
-        p.h = static_cast<float*>(ws);
-        p.z = reinterpret_cast<float*>(static_cast<char*>(ws) + piece(4LL * p.P * F));
-        const int ct = p.P <= 12 * E ? 1 : 2;
-        if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;
-        const float* z = p.z;
-        const float* wt = weights + (size_t)t * k;
-        void* yt = y + (size_t)t * D * size_of(y_dt);
-        void* args[] = {&z, &wt, &p.ids, &yt, &D, &E, &k, &yf32};
-        if (!launch((const void*)&combine_kernel, dim3((D + 255) / 256, n), 256, args, st)) return QMV_E_LAUNCH;
-    }
-    return QMV_OK;
+    const ExpertPieces at(n, D, F, k, bits, gs);
+    ExpertParams p;
+    p.xp = ws;
+    p.ids = ids;
+    p.w13 = w13;
+    p.s13 = static_cast<const uint16_t*>(s13);
+    p.b13 = static_cast<const uint16_t*>(b13);
+    p.w2 = w2;
+    p.s2 = static_cast<const uint16_t*>(s2);
+    p.b2 = static_cast<const uint16_t*>(b2);
+    p.h = ws + at.h;
+    p.z = reinterpret_cast<float*>(ws + at.z);
+    p.x_plane = at.x_plane;
+    p.h_plane = at.h_plane;
+    p.P = n * k;
+    p.k = k;
+    p.D = D;
+    p.F = F;
+    p.E = E;
+    p.slots = std::min(p.P, E);
+    p.parts = 0;
+    const int ct = p.P <= 12 * E ? 1 : 2;
+    if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;
+    const float* z = p.z;
+    void* args[] = {&z, &weights, &ids, &y, &D, &E, &k, &yf32};
+    return launch((const void*)&combine_kernel, dim3((D + 255) / 256, n), 256, args, st) ? QMV_OK : QMV_E_LAUNCH;
 }
 
 }  // namespace
@@ -284,16 +338,19 @@ int qmv_route(const void* x, const void* router, float* weights, int32_t* ids, v
     const Span in[] = {{x, (size_t)T * D * size_of(x_dt)}, {router, (size_t)n_experts * D * size_of(r_dt)}};
     const Span out[] = {{weights, (size_t)T * top_k * 4}, {ids, (size_t)T * top_k * 4}, {workspace, (size_t)need}};
     if (!disjoint(in, out)) return QMV_E_ALIAS;
-    return run_route(static_cast<const char*>(x), router, weights, ids, workspace, T, D, n_experts, top_k,
-                     renormalize != 0, x_dt, r_dt, static_cast<hipStream_t>(stream));
+    for (int t = 0; t < T; t += kMoeTile)
+        if (const int e = run_route(static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt), router, weights + (size_t)t * top_k,
+                                    ids + (size_t)t * top_k, workspace, nullptr, std::min(kMoeTile, T - t), D, n_experts, top_k,
+                                    renormalize != 0, x_dt, r_dt, 4, 64, static_cast<hipStream_t>(stream)))
+            return e;
+    return QMV_OK;
 }
 
 long long qmv_experts_workspace(int T, int D, int F, int top_k)
 {
     if (T < 1 || T > QMV_MAX_M || D < 1 || D > QMV_MAX_K || F < 1 || F > QMV_MAX_K || top_k < 1 || top_k > QMV_MAX_TOP_K)
         return -1;
-    const long long pairs = (long long)std::min(T, ops::kMoeTile) * top_k;
-    return ops::piece(4 * pairs * F) + ops::piece(4 * pairs * D);
+    return ops::expert_bytes(T, D, F, top_k);
 }
 
 int qmv_experts(const void* x, const float* weights, const int32_t* ids, const uint32_t* w13,
@@ -317,15 +374,28 @@ int qmv_experts(const void* x, const float* weights, const int32_t* ids, const u
                        {w13, 2 * nw}, {s13, ns13}, {b13, ns13}, {w2, nw}, {s2, ns}, {b2, ns}};
     const Span out[] = {{y, (size_t)T * D * size_of(y_dt)}, {workspace, (size_t)need}};
     if (!disjoint(in, out)) return QMV_E_ALIAS;
-    return run_experts(static_cast<const char*>(x), weights, ids, w13, s13, b13, w2, s2, b2, static_cast<char*>(y),
-                       workspace, T, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt,
-                       static_cast<hipStream_t>(stream));
+    hipStream_t st = static_cast<hipStream_t>(stream);
+    char* ws = static_cast<char*>(workspace);
+    constexpr int threads = kRouteWaves * kWave;
+    for (int t = 0; t < T; t += kMoeTile) {
+        int n = std::min(kMoeTile, T - t);
+        const char* xt = static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt);
+        bool f32 = x_dt == QMV_DT_F32;
+        void* args[] = {&xt, &ws, &n, &D, &bits, &group_size, &f32};
+        const int packs = (int)(((long long)n * (D * bits / 32) + threads - 1) / threads);
+        if (!launch((const void*)&pack_kernel, dim3(packs), threads, args, st)) return QMV_E_LAUNCH;
+        if (const int e = run_experts(weights + (size_t)t * top_k, ids + (size_t)t * top_k, w13, s13, b13, w2, s2, b2,
+                                      static_cast<char*>(y) + (size_t)t * D * size_of(y_dt), ws, n, D, F, n_experts, top_k, bits,
+                                      group_size, x_dt, sb_dt, y_dt, st))
+            return e;
+    }
+    return QMV_OK;
 }
 
 long long qmv_moe_workspace(int T, int D, int F, int n_experts, int top_k)
 {
     const long long r = qmv_route_workspace(T, D, n_experts), e = qmv_experts_workspace(T, D, F, top_k);
-    return r < 0 || e < 0 ? -1 : std::max(r, e);
+    return r < 0 || e < 0 ? -1 : r + e;
 }
 
 int qmv_moe(const void* x, const void* router, const uint32_t* w13, const void* s13,
@@ -353,11 +423,21 @@ int qmv_moe(const void* x, const void* router, const uint32_t* w13, const void* 
                         {ids, (size_t)T * top_k * 4}, {workspace, (size_t)need}};
     if (!disjoint(in, out)) return QMV_E_ALIAS;
     hipStream_t st = static_cast<hipStream_t>(stream);
-    if (const int e = run_route(static_cast<const char*>(x), router, weights, ids, workspace, T, D, n_experts, top_k,
-                                renormalize != 0, x_dt, r_dt, st))
-        return e;
-    return run_experts(static_cast<const char*>(x), weights, ids, w13, s13, b13, w2, s2, b2, static_cast<char*>(y),
-                       workspace, T, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt, st);
+    char* const part = static_cast<char*>(workspace) + qmv_experts_workspace(T, D, F, top_k);
+    for (int t = 0; t < T; t += kMoeTile) {
+        const int n = std::min(kMoeTile, T - t);
+        float* const wt = weights + (size_t)t * top_k;
+        int32_t* const it = ids + (size_t)t * top_k;
+        if (const int e = run_route(static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt), router, wt, it, part,
+                                    static_cast<char*>(workspace), n, D, n_experts, top_k, renormalize != 0, x_dt, r_dt, bits,
+                                    group_size, st))
+            return e;
+        if (const int e = run_experts(wt, it, w13, s13, b13, w2, s2, b2, static_cast<char*>(y) + (size_t)t * D * size_of(y_dt),
+                                      static_cast<char*>(workspace), n, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt,
+                                      st))
+            return e;
+    }
+    return QMV_OK;
 }
 
 }  // extern "C"

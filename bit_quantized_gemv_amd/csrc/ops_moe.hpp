@@ -9,7 +9,7 @@ namespace ops {
 constexpr int kMoeTile = 256;      // tokens per set of launches
 
 struct ExpertParams {
-    const char* x;                 // [T][D]
+    const char* xp;                // packed activations of the tokens
     const int32_t* ids;            // [P], P = T * k (token, slot) pairs
     const uint32_t* w13;
     const uint16_t* s13;
@@ -17,13 +17,15 @@ struct ExpertParams {
     const uint32_t* w2;
     const uint16_t* s2;
     const uint16_t* b2;
-    float* h;                      // [P][F]
+    char* h;                       // packed hidden values of the pairs, three planes
     float* z;                      // [P][D]
+    size_t x_plane, h_plane;       // bytes of a plane
     int P, k, D, F, E;
     int slots;                     // P: a workgroup per pair, its expert's first; E: one per expert
+    int parts;                     // of a row's K
 };
 
-// which = 0: gate and up products and the activation (x -> h); 1: down product (h -> z)
+// which = 0: gate and up products and the activation (xp -> h); 1: down product (h -> z)
 int expert_launch_b4_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
 int expert_launch_b4_g128(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
 int expert_launch_b2_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);

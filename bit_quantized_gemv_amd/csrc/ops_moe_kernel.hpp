@@ -1,9 +1,9 @@
 // ops_moe_kernel.hpp -- the two products of the experts.
 //
-// A workgroup takes one expert and 16 gate rows with their 16 up rows (or 16
-// rows of the down product), collects the (token, slot) pairs that chose the
-// expert, and multiplies their activations 16 * CT at a time.  With few tokens
-// every chosen expert's weights are read once and bound the time.
+// A workgroup takes one expert and, for each group of its waves, 16 gate rows with
+// their 16 up rows (or 32 rows of the down product), finds the (token, slot) pairs
+// that chose the expert, and multiplies their activations 16 * CT at a time.  With
+// few tokens every chosen expert's weights are read once and bound the time.
 #pragma once
 #include "ops_moe.hpp"
 #include "ops_tile.hpp"
@@ -12,99 +12,188 @@ namespace ops {
 
 constexpr int kMaxPairs = kMoeTile * 32;
 
-// The expert of this workgroup and its pairs in ascending order, in `list`;
-// their count, or 0 if another workgroup takes them.  All threads.
-__device__ __forceinline__ int collect(const ExpertParams& p, int slot, int& e, uint16_t* list, int* count)
+// The pairs that chose expert e, in ascending order: their count, and whether the
+// first of them is `slot`.  Every wave by itself; the first wave writes the list.
+struct Found {
+    int n;
+    bool first;
+};
+
+__device__ __forceinline__ Found find_pairs(const int32_t* ids, int P, int e, int slot, uint16_t* list)
 {
-    e = p.slots == p.P ? p.ids[slot] : slot;
-    if (e < 0 || e >= p.E) return 0;
-    if (threadIdx.x < kWave) {
-        const int lane = threadIdx.x;
-        int n = 0;
-        for (int base = 0; base < p.P; base += 4 * kWave) {
-            int id[4];
+    const int lane = threadIdx.x & 63;
+    const bool writes = threadIdx.x < kWave;
+    int n = 0, lowest = -1;
+    for (int base = 0; base < P; base += 4 * kWave) {
+        int id[4];
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const int at = base + i * kWave + lane;
-                id[i] = at < p.P ? p.ids[at] : -1;
-            }
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const unsigned long long hit = __ballot(id[i] == e);
-                const int before = __popcll(hit & ((1ull << lane) - 1));
-                if (id[i] == e) list[n + before] = (uint16_t)(base + i * kWave + lane);
-                n += __popcll(hit);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const int at = base + i * kWave + lane;
+            const int v = ids[min(at, P - 1)];
+            id[i] = at < P ? v : -1;
         }
-        if (lane == 0) *count = n;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const unsigned long long hit = __ballot(id[i] == e);
+            if (lowest < 0 && hit != 0) lowest = base + i * kWave + __builtin_ctzll(hit);
+            if (writes && id[i] == e) list[n + __popcll(hit & ((1ull << lane) - 1))] = (uint16_t)(base + i * kWave + lane);
+            n += __popcll(hit);
+        }
     }
-    __syncthreads();
-    const int n = *count;
-    return n > 0 && p.slots == p.P && list[0] != slot ? 0 : n;
+    return {uniform(n), uniform(lowest) == slot};
 }
 
 __device__ __forceinline__ float silu(float g) { return g / (1.0f + expf(-g)); }
 
+struct ExpertSpace {
+    int biases, turn, list, bytes;
+    __host__ __device__ ExpertSpace(const Meta& meta, int waves, int rows, int P)
+    {
+        biases = meta.bytes(rows) / 2;
+        turn = 2 * biases;
+        list = turn + waves * 2 * Join<1>::kWords * 4;
+        bytes = list + (P * 2 + 15) / 16 * 16;
+    }
+};
+
 // GATE: T::RT = 2 row tiles, the gate rows and the up rows
 template <class T, bool GATE>
-__global__ __launch_bounds__(kMaxWaves* kWave) void expert_kernel(ExpertParams p)
+__global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(ExpertParams p)
 {
-    constexpr int RT = T::RT, CT = T::CT;
+    constexpr int RT = 2, CT = T::CT;
+    static_assert(T::RT == RT, "");
     using J = Join<RT>;
-    __shared__ float join[kMaxWaves * J::kWords];
-    __shared__ uint16_t list[kMaxPairs];
-    __shared__ int count;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    together(p.ids, GATE ? p.w13 : p.w2, GATE ? p.s13 : p.s2, GATE ? p.b13 : p.b2, GATE ? p.xp : p.h, GATE ? p.x_plane : p.h_plane,
+             p.P, p.k, p.D, p.F, p.E, p.slots, p.parts);
+    const int slot = blockIdx.y;
+    const bool by_pair = p.slots == p.P;
+    const int e = by_pair ? p.ids[slot] : slot;
+    if (e < 0 || e >= p.E) return;
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
+    const int c = lane & 15, parts = p.parts, waves = waves_of(parts), groups = waves / parts, threads = kWave * waves;
+    const int group = wave / parts, part = wave % parts;
+    const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;            // N is a multiple of 64
+    constexpr int ROWS = GATE ? 16 : 32;                             // outputs of a group
+    const int first = blockIdx.x * ROWS * groups, left = min(ROWS * groups, N - first), n0 = first + group * ROWS;
+    const Meta meta(32 * groups, K, T::BITS, T::GS, parts);
+    const ExpertSpace sp(meta, waves, 32 * groups, p.P);
+    uint16_t* const scales = reinterpret_cast<uint16_t*>(lds);
+    uint16_t* const biases = reinterpret_cast<uint16_t*>(lds + sp.biases);
+    float* const join = reinterpret_cast<float*>(lds + sp.turn);
+    uint16_t* const list = reinterpret_cast<uint16_t*>(lds + sp.list);
 
-    int e;
-    const int n = uniform(collect(p, blockIdx.y, e, list, &count));
-    if (n == 0) return;
+    const Found found = find_pairs(p.ids, p.P, e, slot, list);
+    if (found.n == 0 || (by_pair && !found.first)) return;
+    const int n = found.n;
 
-    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), waves = blockDim.x >> 6;
-    const int c = lane & 15, q = lane >> 4;
-    const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;   // N is a multiple of 64
-    const int n0 = blockIdx.x * 16 * (GATE ? 1 : RT);
+    // LDS rows: GATE: the groups' gate rows, then their up rows
     typename T::Rows r;
-    r.K = K;
     r.G = K / T::GS;
     r.chunks = K / (4 * T::VPW);
-    r.meta_al = r.G % T::NG == 0;
+    r.plane = GATE ? p.x_plane : p.h_plane;
+    r.turn = lds + sp.turn + wave * T::TURN;
+    r.even = meta.groups % T::NG == 0;
+    const size_t row0 = (size_t)e * (GATE ? 2 * N : N);
+    const bool active = n0 < N;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const size_t row = GATE ? (size_t)e * 2 * N + (size_t)i * N + n0 + c : (size_t)e * N + n0 + 16 * i + c;
-        r.w[i] = reinterpret_cast<const u32x4*>(GATE ? p.w13 : p.w2) + row * r.chunks;
-        r.s[i] = (GATE ? p.s13 : p.s2) + row * r.G;
-        r.b[i] = (GATE ? p.b13 : p.b2) + row * r.G;
+        const int local = GATE ? i * 16 * groups + group * 16 : group * 32 + 16 * i;
+        T::set_codes(r, i, GATE ? p.w13 : p.w2, row0 + (GATE ? (size_t)i * N + min(n0, N - 16) : min(n0 + 16 * i, N - 16)), 16);
+        r.s[i] = scales + (local + c) * meta.groups;
+        r.b[i] = biases + (local + c) * meta.groups;
     }
-    const int slabs = slabs_of(r.chunks);
+    const uint16_t* const ms = (GATE ? p.s13 : p.s2) + (row0 + first) * r.G;
+    const uint16_t* const mb = (GATE ? p.b13 : p.b2) + (row0 + first) * r.G;
+    const size_t up = (size_t)N * r.G;
+    const int slabs = slabs_of(r.chunks), s0 = part * slabs / parts, s1 = (part + 1) * slabs / parts;
+    MetaCopy<GATE ? 2 : 4> copy(ms, mb, left * r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left * r.G, threads);
+    const int half = 16 * groups * meta.groups;       // the up rows' place
+    auto stage = [&](int k) {
+        stage_window(scales, ms, left, r.G, T::NG, slabs, parts, meta.window, k, threads);
+        stage_window(biases, mb, left, r.G, T::NG, slabs, parts, meta.window, k, threads);
+        if (GATE) {
+            stage_window(scales + half, ms + up, left, r.G, T::NG, slabs, parts, meta.window, k, threads);
+            stage_window(biases + half, mb + up, left, r.G, T::NG, slabs, parts, meta.window, k, threads);
+        }
+    };
+    int shifted = 0;
+    auto shift = [&](int to) {
+#pragma unroll
+        for (int i = 0; i < RT; ++i) {
+            r.s[i] += (to - shifted) * T::NG;
+            r.b[i] += (to - shifted) * T::NG;
+        }
+        shifted = to;
+    };
+    if (meta.windows == 1) {
+        copy.ask();
+        if (GATE) copy_up.ask();
+        keep_order();
+    }
+    const Packed pk(p.F, T::BITS, T::GS, false);
+    typename T::Ring ring;
     for (int t0 = 0; t0 < n; t0 += 16 * CT) {
+        lds_barrier();              // the list is there; the partial results before are read
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const int pair = list[min(t0 + 16 * j + c, n - 1)];
-            r.x[j] = GATE ? p.x + (size_t)(pair / p.k) * K * (T::XF32 ? 4 : 2)
-                          : reinterpret_cast<const char*>(p.h + (size_t)pair * K);
+            T::set_token(r, j, GATE ? p.xp : p.h, GATE ? pair / p.k : pair);
         }
         f32x4 acc[RT][CT];
         T::clear(acc);
-        T::run(acc, r, wave * slabs / waves, (wave + 1) * slabs / waves, q);
+        for (int k = 0; k < meta.windows; ++k) {
+            if (meta.windows > 1) {
+                if (k > 0) lds_barrier();
+                stage(k);
+                lds_barrier();
+                shift((part - k) * meta.window - s0);
+            }
+            const int a0 = min(s0 + k * meta.window, s1), a1 = min(a0 + meta.window, s1);
+            T::begin(ring, r, min(a0, s1 - 1), max(a1, s0 + 1));
+            if (meta.windows == 1 && t0 == 0) {
+                copy.put(scales, biases);
+                if (GATE) copy_up.put(scales + half, biases + half);
+                lds_barrier();
+            }
+            if (active) T::run(acc, ring, r, a0, a1);
+        }
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             if (t0 + 16 * j >= n) break;
+            lds_barrier();          // the turning space is the join's from here
 #pragma unroll
             for (int i = 0; i < RT; ++i) J::write(join, wave, lane, i, acc[i][j]);
-            __syncthreads();
-            constexpr int ROWS = GATE ? 16 : 16 * RT;
-            for (int i = threadIdx.x; i < 16 * ROWS; i += blockDim.x) {
-                const int en = i % ROWS, et = i / ROWS;
-                if (t0 + 16 * j + et < n) {
-                    const size_t pair = list[t0 + 16 * j + et];
-                    const float v = J::sum(join, waves, J::at(en, et));
-                    if constexpr (GATE)
-                        p.h[pair * N + n0 + en] = silu(v) * J::sum(join, waves, J::at(16 + en, et));
-                    else
-                        p.z[pair * N + n0 + en] = v;
+            lds_barrier();
+            if constexpr (GATE) {
+                // two hidden values at a time, those that a dword of codes meets
+                constexpr int H = T::VPW / 2;
+                for (int i = threadIdx.x; i < 128 * groups; i += threads) {
+                    const int et = i & 15, d = (i >> 4) & 7, g = i >> 7;
+                    if (t0 + 16 * j + et < n && g * 16 < left) {
+                        const size_t pair = list[t0 + 16 * j + et];
+                        const int word = d / H, ii = d % H, en = word * T::VPW + ii;
+                        float v[2];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b)
+                            v[b] = silu(J::sum(join, g * parts, parts, J::at(en + b * H, et))) *
+                                   J::sum(join, g * parts, parts, J::at(16 + en + b * H, et));
+                        uint32_t ah, am, al, bh, bm, bl;
+                        split3(v[0], ah, am, al);
+                        split3(v[1], bh, bm, bl);
+                        char* to = p.h + pk.word((int)pair, (first + g * 16) / T::VPW + word) + (ii / 4) * 64 + (ii % 4) * 4;
+                        *reinterpret_cast<uint32_t*>(to) = hi16(ah, bh);
+                        *reinterpret_cast<uint32_t*>(to + p.h_plane) = hi16(am, bm);
+                        *reinterpret_cast<uint32_t*>(to + 2 * p.h_plane) = hi16(al, bl);
+                    }
+                }
+            } else {
+                for (int i = threadIdx.x; i < 16 * 32 * groups; i += threads) {
+                    const int en = i & 31, g = (i >> 5) % groups, et = (i >> 5) / groups;
+                    if (t0 + 16 * j + et < n && g * 32 + en < left)
+                        p.z[(size_t)list[t0 + 16 * j + et] * N + first + g * 32 + en] = J::sum(join, g * parts, parts, J::at(en, et));
                 }
             }
-            __syncthreads();
         }
     }
 }
@@ -112,27 +201,26 @@ __global__ __launch_bounds__(kMaxWaves* kWave) void expert_kernel(ExpertParams p
 template <class T, bool GATE>
 int expert_start(const ExpertParams& p, hipStream_t st)
 {
-    const int K = GATE ? p.D : p.F, rows = GATE ? p.F : p.D;
+    const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;
     ExpertParams q = p;
+    q.parts = parts_of(K / (4 * T::VPW));
+    const int waves = waves_of(q.parts), groups = waves / q.parts, rows = (GATE ? 16 : 32) * groups;
+    const ExpertSpace sp(Meta(32 * groups, K, T::BITS, T::GS, q.parts), waves, 32 * groups, p.P);
+    const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
+    if (sp.bytes > 64 * 1024 &&
+        hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, sp.bytes) != hipSuccess)
+        return 1;
     void* args[] = {&q};
-    return hipLaunchKernel(reinterpret_cast<const void*>(&expert_kernel<T, GATE>),
-                           dim3(rows / (16 * (GATE ? 1 : T::RT)), p.slots), dim3(kWave * waves_of(K / (4 * T::VPW))),
-                           args, 0, st) == hipSuccess
-               ? 0
-               : 1;
+    return hipLaunchKernel(fn, dim3((N + rows - 1) / rows, p.slots), dim3(kWave * waves), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }
 
 template <int BITS, int GS, bool SBF>
 int expert_pick(int which, const ExpertParams& p, int ct, bool xf32, hipStream_t st)
 {
-    if (which == 1)
-        return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, true, SBF>, false>(p, st)
-                       : expert_start<Tile<BITS, GS, 2, 2, true, SBF>, false>(p, st);
-    if (xf32)
-        return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, true, SBF>, true>(p, st)
-                       : expert_start<Tile<BITS, GS, 2, 2, true, SBF>, true>(p, st);
-    return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, false, SBF>, true>(p, st)
-                   : expert_start<Tile<BITS, GS, 2, 2, false, SBF>, true>(p, st);
+    if (which == 1) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, false>(p, st);
+    if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, true>(p, st);
+    return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, 1, SBF, false>, true>(p, st)
+                   : expert_start<Tile<BITS, GS, 2, 2, 1, SBF, false>, true>(p, st);
 }
 
 }  // namespace ops

@@ -103,6 +103,14 @@ __device__ __forceinline__ void store_y(void* y, size_t at, float v, bool f32)
         static_cast<uint16_t*>(y)[at] = to_bf16(v);
 }
 
+// Kernel arguments are asked for all at once: read where they are first needed, each
+// would be a round trip of its own to memory that no cache near the wave holds.
+template <class... A>
+__device__ __forceinline__ void together(const A&... a)
+{
+    (([](const A& v) { asm volatile("" ::"s"(v)); })(a), ...);
+}
+
 // nothing but loads and stores from memory stays on its side
 __device__ __forceinline__ void keep_order() { __builtin_amdgcn_sched_barrier(0x78F); }
 
@@ -487,22 +495,56 @@ struct Tile {
     }
 };
 
-// `count` scales from memory (16-byte aligned) to LDS, by all threads.
-__device__ __forceinline__ void stage_meta(uint16_t* to, const uint16_t* from, int count)
-{
-    const int whole = count / 8;
-    for (int i = threadIdx.x; i < whole; i += blockDim.x)
-        reinterpret_cast<u32x4*>(to)[i] = reinterpret_cast<const u32x4*>(from)[i];
-    const int at = whole * 8 + threadIdx.x;
-    if (at < count) to[at] = from[at];
-}
+// Scales and biases of `rows` rows from memory to LDS, by all threads, in 16-byte
+// pieces: the first ones wait in registers while other loads are asked for.
+template <int HELD>
+struct MetaCopy {
+    u32x4 v[HELD];
+    const uint16_t *s, *b;
+    int count, whole;      // values, and whole pieces, of each
+    int threads;           // of the workgroup (blockDim is an argument of its own, and a round trip)
+    __device__ __forceinline__ MetaCopy(const uint16_t* s_, const uint16_t* b_, int count_, int threads_)
+        : s(s_), b(b_), count(count_), whole(count_ / 8), threads(threads_)
+    {
+    }
+    __device__ __forceinline__ u32x4 load(int i) const
+    {
+        return i < whole ? reinterpret_cast<const u32x4*>(s)[i] : reinterpret_cast<const u32x4*>(b)[min(i - whole, whole - 1)];
+    }
+    __device__ __forceinline__ void ask()
+    {
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) {
+            const int i = min((int)(threadIdx.x + k * threads), 2 * whole - 1);
+            if (whole > 0) v[k] = load(i);
+        }
+    }
+    __device__ __forceinline__ void put(uint16_t* ts, uint16_t* tb) const
+    {
+        auto store = [&](int i, const u32x4& x) {
+            if (i < whole)
+                reinterpret_cast<u32x4*>(ts)[i] = x;
+            else if (i < 2 * whole)
+                reinterpret_cast<u32x4*>(tb)[i - whole] = x;
+        };
+#pragma unroll
+        for (int k = 0; k < HELD; ++k) store(threadIdx.x + k * threads, v[k]);
+        for (int i = threadIdx.x + HELD * threads; i < 2 * whole; i += threads) store(i, load(i));
+        int at = whole * 8 + threadIdx.x;
+        asm volatile("" : "+v"(at));        // these loads stay here, behind those in flight
+        if (at < count) {
+            ts[at] = s[at];
+            tb[at] = b[at];
+        }
+    }
+};
 
 // A window of every part's groups, of `rows` rows: row-major, part by part.
 __device__ __forceinline__ void stage_window(uint16_t* to, const uint16_t* from, int rows, int G, int ng, int slabs, int parts,
-                                             int window, int number)
+                                             int window, int number, int threads)
 {
     const int wg = window * ng, row = parts * wg;
-    for (int i = threadIdx.x; i < rows * row; i += blockDim.x) {
+    for (int i = threadIdx.x; i < rows * row; i += threads) {
         const int part = i % row / wg, g = (part * slabs / parts + number * window) * ng + i % wg;
         if (g < G) to[i] = from[(size_t)(i / row) * G + g];
     }

@@ -116,7 +116,7 @@ def test_workspaces(L):
     assert L.qmv_affine_lora_workspace(65536, 512, 32) == L.qmv_affine_lora_workspace(4096, 512, 32)   # taken in pieces
     for bad in ((0, 512, 5), (1, 0, 5), (1, 512, 0), (1, 512, 513)):
         assert L.qmv_affine_lora_workspace(*bad) == -1
-    assert L.qmv_moe_workspace(4, 512, 256, 8, 2) == max(L.qmv_route_workspace(4, 512, 8), L.qmv_experts_workspace(4, 512, 256, 2))
+    assert L.qmv_moe_workspace(4, 512, 256, 8, 2) >= max(L.qmv_route_workspace(4, 512, 8), L.qmv_experts_workspace(4, 512, 256, 2))
     assert L.qmv_moe_workspace(4, 512, 256, 0, 2) == -1 and L.qmv_experts_workspace(4, 512, 256, 33) == -1
     assert L.qmv_verify_workspace(1, 256, 10) == -1 and L.qmv_verify_workspace(2, 3, 1000) > 0
 
