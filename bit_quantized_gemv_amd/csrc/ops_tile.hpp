@@ -49,6 +49,8 @@
 
 #include <cstdint>
 
+#include "ops_args.hpp"
+
 namespace ops {
 
 typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
@@ -101,14 +103,6 @@ __device__ __forceinline__ void store_y(void* y, size_t at, float v, bool f32)
         static_cast<float*>(y)[at] = v;
     else
         static_cast<uint16_t*>(y)[at] = to_bf16(v);
-}
-
-// Kernel arguments are asked for all at once: read where they are first needed, each
-// would be a round trip of its own to memory that no cache near the wave holds.
-template <class... A>
-__device__ __forceinline__ void together(const A&... a)
-{
-    (([](const A& v) { asm volatile("" ::"s"(v)); })(a), ...);
 }
 
 // nothing but loads and stores from memory stays on its side

@@ -26,6 +26,7 @@
 #include <algorithm>
 #include <cstdint>
 
+#include "ops_args.hpp"
 #include "ops_check.hpp"
 
 namespace ops {
@@ -69,6 +70,7 @@ struct VerifyParams {
     uint32_t* tickets; // [B]
     int B, S, V, chunks;
     int walk, stretches; // first launch: spans per wave, waves per row
+    int groups;          // second launch: workgroups per request
     long long l_batch, l_row, q_batch, q_row;
 };
 
@@ -239,6 +241,7 @@ template <bool LF32>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
 {
     constexpr int PER = LF32 ? 4 : 8, NV = kSpanPer / PER, SZ = LF32 ? 4 : 2;
+    together(p.logits, p.temperature, p.lengths, p.stats, p.tickets, p.S, p.V, p.walk, p.stretches, p.l_batch, p.l_row);
     const int lane = threadIdx.x & 63, at_row = blockIdx.x * kWaves + (threadIdx.x >> 6);
     const int b = blockIdx.z, j = blockIdx.y, row = b * (p.S + 1) + j;
     if (j == 0 && at_row == 0 && lane == 0) p.tickets[b] = 0;
@@ -424,6 +427,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
     __shared__ PickSpace pick_space;
     __shared__ int first_bad;
     __shared__ bool am_last;
+    together(p.logits, p.draft, p.u, p.probs, p.temperature, p.lengths, p.stats, p.part, p.tickets, p.S, p.V, p.chunks, p.stretches,
+             p.groups, p.l_batch, p.l_row, p.q_batch, p.q_row);
     const int chunk = blockIdx.x, b = blockIdx.y, len = length_of(p, b), tid = threadIdx.x;
     const int lane = tid & 63, wave = tid >> 6;
     const float T = p.temperature ? p.temperature[b] : 1.0f;
@@ -518,7 +523,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
             }
         };
         Part* parts = p.part + (size_t)b * p.chunks;
-        for (int c = chunk; c < p.chunks; c += gridDim.x) {
+        for (int c = chunk; c < p.chunks; c += p.groups) {
             load_chunk(c);
             Part mine{0.0, 0.0, 0.0, 0.0};
 #pragma unroll
@@ -557,7 +562,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
         // the whole cache (about 40 us with 2048 workgroups) is not needed.
         if (tid == 0) {
             asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
-            am_last = __hip_atomic_fetch_add(&p.tickets[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+            am_last = __hip_atomic_fetch_add(&p.tickets[b], 1u, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == (uint32_t)p.groups - 1;
         }
         __syncthreads();
         if (!am_last) return;
@@ -724,9 +729,9 @@ int qmv_verify(const void* logits, const int32_t* draft, const float* uniforms, 
     hipStream_t st = static_cast<hipStream_t>(stream);
     // Workgroups per request of the second launch: each repeats the decisions, so
     // no more than are resident at once.
-    const int groups = std::min(p.chunks, std::max(1, 1024 / B));
+    p.groups = std::min(p.chunks, std::max(1, 1024 / B));
     if (hipLaunchKernel(f1, dim3((p.stretches + kWaves - 1) / kWaves, S + 1, B), dim3(kThreads), args, 0, st) != hipSuccess ||
-        hipLaunchKernel(f2, dim3(groups, B), dim3(kThreads), args, 0, st) != hipSuccess)
+        hipLaunchKernel(f2, dim3(p.groups, B), dim3(kThreads), args, 0, st) != hipSuccess)
         return QMV_E_LAUNCH;
     return QMV_OK;
 }
