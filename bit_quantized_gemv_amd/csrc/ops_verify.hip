@@ -330,79 +330,90 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
     if (lane == 0) p.stats[(size_t)row * p.stretches + at_row] = Stat{sum, top, at};
 }
 
-// Sum over the workgroup, in every thread; `shared` of kWaves values is free again after the next barrier.
-__device__ __forceinline__ double block_sum(double v, double* shared)
+// Sums of the lanes up to each, by dpp: within rows of 16, then from row to row.
+template <int CTRL, int ROWS>
+__device__ __forceinline__ double add_dpp(double v)
 {
-    v = wave_sum(v);
-    if ((threadIdx.x & 63) == 0) shared[threadIdx.x >> 6] = v;
-    __syncthreads();
-    v = shared[0];
-#pragma unroll
-    for (int w = 1; w < kWaves; ++w) v += shared[w];
-    return v;
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(uint32_t)u, CTRL, ROWS, 0xf, false);
+    const uint32_t hi = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)(u >> 32), CTRL, ROWS, 0xf, false);
+    return v + two(lo, hi);
 }
 
-// The sums of the threads before this one, and of all.
-__device__ __forceinline__ double block_scan(double v, double* shared, double& total)
+__device__ __forceinline__ double wave_scan(double v)
 {
-    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-    double s = v;
-#pragma unroll
-    for (int o = 1; o < 64; o <<= 1) {
-        const double add = __shfl_up(s, o);
-        if (lane >= o) s += add;
-    }
-    if (lane == 63) shared[wave] = s;
-    __syncthreads();
-    double before = 0.0;
-    total = 0.0;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) {
-        if (w == wave) before = total;
-        total += shared[w];
-    }
-    const double prev = __shfl_up(s, 1);
-    return lane > 0 ? before + prev : before;
+    v = add_dpp<0x111, 0xf>(v);      // from 1, 2, 4 and 8 lanes below, zero from outside the row
+    v = add_dpp<0x112, 0xf>(v);
+    v = add_dpp<0x114, 0xf>(v);
+    v = add_dpp<0x118, 0xf>(v);
+    v = add_dpp<0x142, 0xa>(v);      // lane 15 of the row below to rows 1 and 3
+    return add_dpp<0x143, 0xc>(v);   // lane 31 to rows 2 and 3
 }
 
-// The lowest index given by any thread that found one, else the highest last
-// index of a positive value, else -1; and the number that goes with it.
+// The LDS of one choice among what all threads hold.
+struct PickSpace {
+    double sums[kWaves];
+    double before[kWaves][2];
+    int index[kWaves][2];
+};
+
+// Every thread holds the values get(i), i0 <= i < i1, in the threads' order, and
+// their sum: the lowest index whose prefix sum passes target(total), or the highest of a
+// positive value if none does (-1 if there is no such value), and the sum before it.
 struct Pick {
     int index;
     double before;
 };
 
-struct PickSpace {
-    int found, last;
-    double found_before, last_before;
-};
-
-__device__ __forceinline__ Pick block_pick(Pick found, Pick last, PickSpace* sp)
+template <class Get, class Target>
+__device__ __forceinline__ Pick block_pick(PickSpace& sp, int i0, int i1, double sum, Get get, Target target)
 {
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    double to = wave_scan(sum);
+    if (lane == 63) sp.sums[wave] = to;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        sp->found = kNoIndex;
-        sp->last = -1;
+    double total = 0.0, below = 0.0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) {
+        if (w == wave) below = total;
+        total += sp.sums[w];
+    }
+    const double t = target(total);
+    to += below;
+    const unsigned long long over = __ballot(to > t), some = __ballot(sum > 0.0);
+    if (lane < 2) sp.index[wave][lane] = -1;
+    // the first thread past the number, and the last with anything, look through their values
+    const bool first = over != 0 && lane == __builtin_ctzll(over), last = some != 0 && lane == 63 - __builtin_clzll(some);
+    if (first || last) {
+        double c = to - sum;
+        Pick found{-1, 0.0}, end{-1, 0.0};
+        for (int i = i0; i < i1; ++i) {
+            const double v = get(i);
+            if (v > 0.0) {
+                end = Pick{i, c};
+                if (found.index < 0 && c + v > t) found = end;
+            }
+            c += v;
+        }
+        if (found.index < 0) found = end;        // the sums were rounded otherwise
+        if (first) {
+            sp.index[wave][0] = found.index;
+            sp.before[wave][0] = found.before;
+        }
+        if (last) {
+            sp.index[wave][1] = end.index;
+            sp.before[wave][1] = end.before;
+        }
     }
     __syncthreads();
-    if (found.index >= 0) atomicMin(&sp->found, found.index);
-    if (last.index >= 0) atomicMax(&sp->last, last.index);
-    __syncthreads();
-    if (found.index >= 0 && sp->found == found.index) sp->found_before = found.before;
-    if (last.index >= 0 && sp->last == last.index) sp->last_before = last.before;
-    __syncthreads();
-    if (sp->found != kNoIndex) return Pick{sp->found, sp->found_before};
-    return Pick{sp->last, sp->last_before};
-}
-
-// one more value v at index i with the sum c before it
-__device__ __forceinline__ void consider(Pick& found, Pick& last, int i, double v, double& c, double target)
-{
-    if (v > 0.0) {
-        last = Pick{i, c};
-        if (found.index < 0 && c + v > target) found = Pick{i, c};
-    }
-    c += v;
+    Pick r{-1, 0.0};
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w)
+        if (sp.index[w][1] >= 0) r = Pick{sp.index[w][1], sp.before[w][1]};
+#pragma unroll
+    for (int w = kWaves - 1; w >= 0; --w)
+        if (sp.index[w][0] >= 0) r = Pick{sp.index[w][0], sp.before[w][0]};
+    return r;
 }
 
 __device__ __forceinline__ void put(double* p, double v)
@@ -423,8 +434,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
     __shared__ float tops[kMaxRows];
     __shared__ int ats[kMaxRows];
     __shared__ double sums[kMaxRows];
-    __shared__ double space[5][kWaves];
-    __shared__ PickSpace pick_space;
+    __shared__ double space[2][4][kWaves];
+    __shared__ PickSpace picks[2];
     __shared__ int first_bad;
     __shared__ bool am_last;
     together(p.logits, p.draft, p.u, p.probs, p.temperature, p.lengths, p.stats, p.part, p.tickets, p.S, p.V, p.chunks, p.stretches,
@@ -544,16 +555,16 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
             }
             __syncthreads();
             if (lane == 0) {
-                space[0][wave] = mine.p;
-                space[1][wave] = mine.e;
-                space[2][wave] = mine.q;
-                space[3][wave] = mine.near;
+                space[0][0][wave] = mine.p;
+                space[0][1][wave] = mine.e;
+                space[0][2][wave] = mine.q;
+                space[0][3][wave] = mine.near;
             }
             __syncthreads();
             if (tid < 4) {
-                double s = space[tid][0];
+                double s = space[0][tid][0];
 #pragma unroll
-                for (int w = 1; w < kWaves; ++w) s += space[tid][w];
+                for (int w = 1; w < kWaves; ++w) s += space[0][tid][w];
                 put(reinterpret_cast<double*>(parts + c) + tid, s);
             }
         }
@@ -581,15 +592,29 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
             t.q += x.q;
             t.near += x.near;
         }
-        const double Z = block_sum(t.p, space[4]);
-        bool use = false, again = false;
-        if (rest) {
-            const double near = block_sum(t.near, space[0]);
-            const double left = block_sum(t.e, space[1]) - Z * block_sum(t.q, space[2]);
-            again = near * 0x1p13 > left;     // the border's values could move the sums by 2^-33 of them
-            use = left > 0.0;
-        }
-        if (again) {
+        // sums over the workgroup of four numbers at once
+        auto all_of = [&](Part v) {
+            v = Part{wave_sum(v.p), wave_sum(v.e), wave_sum(v.q), wave_sum(v.near)};
+            if (lane == 0) {
+                space[1][0][wave] = v.p;
+                space[1][1][wave] = v.e;
+                space[1][2][wave] = v.q;
+                space[1][3][wave] = v.near;
+            }
+            __syncthreads();
+            double r[4];
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                r[k] = space[1][k][0];
+#pragma unroll
+                for (int w = 1; w < kWaves; ++w) r[k] += space[1][k][w];
+            }
+            return Part{r[0], r[1], r[2], r[3]};
+        };
+        t = all_of(t);
+        const double Z = t.p, left = t.e - Z * t.q;
+        bool use = rest && left > 0.0;
+        if (rest && t.near * 0x1p13 > left) {     // the border's values could move the sums by 2^-33 of them
             double all = 0.0;
             for (int c = 0; c < p.chunks; ++c) {
                 load_chunk(c);
@@ -597,7 +622,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
 #pragma unroll
                 for (int i = 0; i < kPer; ++i) s += __builtin_fmax(__builtin_fma(-q[i], Z, e[i]), 0.0);
                 __syncthreads();
-                s = block_sum(s, space[3]);
+                s = all_of(Part{s, 0.0, 0.0, 0.0}).p;
                 all += s;
                 if (tid == 0) {
                     put(&parts[c].e, s);
@@ -614,14 +639,9 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
             const Part x = c == c0 ? first : part(c);
             return use ? __builtin_fmax(x.e - Z * x.q, 0.0) : x.p;
         };
-        double s = 0.0, total;
+        double s = 0.0, aim = 0.0;
         for (int c = c0; c < c1; ++c) s += weight_of(c);
-        __syncthreads();
-        double before = block_scan(s, space[0], total);
-        const double target = (double)u_last * total;
-        Pick found{-1, 0.0}, last{-1, 0.0};
-        for (int c = c0; c < c1; ++c) consider(found, last, c, weight_of(c), before, target);
-        const Pick k = block_pick(found, last, &pick_space);
+        const Pick k = block_pick(picks[0], c0, c1, s, weight_of, [&](double total) { return aim = (double)u_last * total; });
         if (k.index >= 0) {
             load_chunk(k.index);
             double w[kPer], sum = 0.0;
@@ -630,12 +650,14 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
                 w[i] = use ? __builtin_fmax(__builtin_fma(-q[i], Z, e[i]), 0.0) : e[i];
                 sum += w[i];
             }
-            double at = k.before + block_scan(sum, space[1], total);
-            found = last = Pick{-1, 0.0};
-            const int i0 = k.index * kChunk + tid * kPer;
+            const double rest_of_aim = aim - k.before;
+            const Pick i = block_pick(picks[1], tid * kPer, tid * kPer + kPer, sum, [&](int i) {
+                double v = w[0];
 #pragma unroll
-            for (int i = 0; i < kPer; ++i) consider(found, last, i0 + i, w[i], at, target);
-            token = block_pick(found, last, &pick_space).index;
+                for (int j = 1; j < kPer; ++j) v = i - tid * kPer == j ? w[j] : v;
+                return v;
+            }, [&](double) { return rest_of_aim; });
+            token = i.index < 0 ? -1 : k.index * kChunk + i.index;
         }
     }
     for (int j = tid; j <= p.S; j += kThreads)
