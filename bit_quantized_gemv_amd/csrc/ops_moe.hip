@@ -104,6 +104,105 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void pack_kernel(const char* x,
     pack(x, xp, T, D, pk, f32, (size_t)blockIdx.x * (kRouteWaves * kWave) + threadIdx.x);
 }
 
+// The pairs sorted by expert: each expert's take whole tiles of 16 rows, in their
+// order.  A workgroup per pair counts for itself where its row lies, and packs the
+// token's activations there; the first one notes every expert's place and count.
+struct SortParams {
+    const char* x;
+    char* xp;
+    const int32_t* ids;
+    int* base;
+    int* count;
+    int* place;
+    size_t plane;
+    int P, k, D, E, bits, gs;
+    bool f32;
+};
+
+__global__ __launch_bounds__(kRouteWaves* kWave) void sort_kernel(SortParams p)
+{
+    constexpr int THREADS = kRouteWaves * kWave, PER = QMV_MAX_EXPERTS / THREADS;
+    __shared__ int counts[QMV_MAX_EXPERTS];
+    __shared__ int sums[2][kRouteWaves];
+    together(p.x, p.xp, p.ids, p.base, p.count, p.place, p.plane, p.P, p.k, p.D, p.E, p.bits, p.gs);
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, pair = blockIdx.x;
+    const int id = p.ids[pair];
+    const bool valid = id >= 0 && id < p.E;
+    if (!valid && pair != 0) {
+        if (tid == 0) p.place[pair] = -1;
+        return;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) counts[tid + THREADS * j] = 0;
+    __syncthreads();
+    int before = 0;                     // pairs before this one of its expert
+    for (int i = tid; i < p.P; i += THREADS) {
+        const int v = p.ids[i];
+        if (v >= 0 && v < p.E) {
+            atomicAdd(&counts[v], 1);
+            if (i < pair && v == id) ++before;
+        }
+    }
+    __syncthreads();
+    // a thread's PER neighbouring experts; their tiles, and those of the threads before it
+    int tiles[PER], own = 0;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        tiles[j] = (counts[tid * PER + j] + 15) / 16;
+        own += tiles[j];
+    }
+    int to = own;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int add = __shfl_up(to, o);
+        if (lane >= o) to += add;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) before += __shfl_xor(before, o);
+    if (lane == 63) sums[0][wave] = to;
+    if (lane == 0) sums[1][wave] = before;
+    __syncthreads();
+    int at = to - own;
+    before = 0;
+#pragma unroll
+    for (int w = 0; w < kRouteWaves; ++w) {
+        if (w < wave) at += sums[0][w];
+        before += sums[1][w];
+    }
+    __shared__ int bases[QMV_MAX_EXPERTS];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+        const int e = tid * PER + j;
+        bases[e] = at;
+        if (pair == 0 && e < p.E) {
+            p.base[e] = at;
+            p.count[e] = counts[e];
+        }
+        at += tiles[j];
+    }
+    __syncthreads();
+    const int row = valid ? bases[id] * 16 + before : -1;
+    if (tid == 0) p.place[pair] = row;
+    if (!valid) return;
+    const Packed pk(p.D, p.bits, p.gs, true);
+    const int words = p.D * p.bits / 32, vpw = 32 / p.bits;
+    for (int w = tid; w < words; w += THREADS) {
+        const size_t k = (size_t)(pair / p.k) * p.D + (size_t)w * vpw;
+        char* o = p.xp + pk.word(row, w);
+        if (p.bits == 4) {
+            if (p.f32)
+                pack_word<4, true>(p.x + k * 4, o, p.plane, pk.op_step());
+            else
+                pack_word<4, false>(p.x + k * 2, o, p.plane, pk.op_step());
+        } else {
+            if (p.f32)
+                pack_word<2, true>(p.x + k * 4, o, p.plane, pk.op_step());
+            else
+                pack_word<2, false>(p.x + k * 2, o, p.plane, pk.op_step());
+        }
+    }
+}
+
 // Top-k and softmax of one token's logits by a workgroup.  An expert's place is the
 // number of experts before it (a larger logit, or an equal one of a lower index),
 // counted against all of them from LDS; with few experts the threads share the
@@ -187,8 +286,8 @@ __global__ __launch_bounds__(kRouteWaves* kWave) void topk_kernel(RouteParams p)
 }
 
 // y[t] = sum of weight * expert output over the token's slots, in their order
-__global__ __launch_bounds__(256) void combine_kernel(const float* z, const float* weights, const int32_t* ids, void* y,
-                                                      int D, int E, int k, bool yf32)
+__global__ __launch_bounds__(256) void combine_kernel(const float* z, const float* weights, const int32_t* ids, const int* place,
+                                                      void* y, int D, int E, int k, bool yf32)
 {
     const int d = blockIdx.x * 256 + threadIdx.x, t = blockIdx.y;
     if (d >= D) return;
@@ -196,7 +295,7 @@ __global__ __launch_bounds__(256) void combine_kernel(const float* z, const floa
     for (int j = 0; j < k; ++j) {
         const size_t pair = (size_t)t * k + j;
         const int e = ids[pair];
-        if (e >= 0 && e < E) v = __builtin_fmaf(weights[pair], z[pair * D + d], v);
+        if (e >= 0 && e < E) v = __builtin_fmaf(weights[pair], z[(place ? (size_t)place[pair] : pair) * D + d], v);
     }
     store_y(y, (size_t)t * D + d, v, yf32);
 }
@@ -256,24 +355,66 @@ int run_route(const char* x, const void* router, float* weights, int32_t* ids, v
                : QMV_E_LAUNCH;
 }
 
+// Pairs are sorted by expert where an expert meets eight or more on average: below
+// that a wave's 16 rows are mostly repeats of a few, which cost it little, and
+// sorting is a launch (13 tokens over 128 experts 116 us unsorted; 128 over 32 SORTED
+// us sorted and 236 not).
+bool sorted(int n, int k, int E) { return (long long)n * k >= 8LL * E; }
+
 // Scratch memory of the experts' products for n tokens.
 struct ExpertPieces {
-    long long h, z, all;       // where the hidden values and the outputs start; the packed activations come first
+    long long h, z, plan, all;       // where the hidden values, the outputs and the plan start; the packed activations come first
     size_t x_plane, h_plane;
-    ExpertPieces(int n, int D, int F, int k, int bits, int gs)
+    ExpertPieces(int n, int D, int F, int k, int E, int bits, int gs)
     {
-        x_plane = Packed(D, bits, gs, false).plane(n);
-        h_plane = Packed(F, bits, gs, false).plane(n * k);
+        const bool s = sorted(n, k, E);
+        const int rows = s ? (n * k / 16 + std::min(E, n * k)) * 16 : n * k;
+        x_plane = Packed(D, bits, gs, s).plane(s ? rows : n);
+        h_plane = Packed(F, bits, gs, s).plane(rows);
         h = piece(3 * (long long)x_plane);
         z = h + piece(3 * (long long)h_plane);
-        all = z + piece(4LL * n * k * D);
+        plan = z + piece(4LL * rows * D);
+        all = plan + piece(4LL * (2 * E + n * k));
     }
 };
 
-// The same for any codes: rows are rounded up to whole slabs of 256 or 128 codes, so the larger bounds both.
+// The same for any codes and experts: rows are rounded up to whole slabs of 256 or
+// 128 codes, and sorted pairs, eight to an expert or more, take three rows each at most.
 long long expert_bytes(int T, int D, int F, int k)
 {
-    return ExpertPieces(std::min(T, kMoeTile), (D + 255) / 256 * 256, (F + 255) / 256 * 256, k, 4, 64).all;
+    const int n = std::min(T, kMoeTile), d = (D + 255) / 256 * 256, f = (F + 255) / 256 * 256;
+    const ExpertPieces a(n, d, f, k, QMV_MAX_EXPERTS, 4, 64), b(n, d, f, k, std::max(1, n * k / 8), 4, 64);
+    return std::max(a.all, b.all);
+}
+
+// Packs the activations of n tokens for experts whose ids are known: sorted, or as they come.
+int run_pack(const char* x, const int32_t* ids, char* ws, int n, int D, int F, int E, int k, int bits, int gs, int x_dt, hipStream_t st)
+{
+    constexpr int threads = kRouteWaves * kWave;
+    bool f32 = x_dt == QMV_DT_F32;
+    if (!sorted(n, k, E)) {
+        void* args[] = {&x, &ws, &n, &D, &bits, &gs, &f32};
+        const int packs = (int)(((long long)n * (D * bits / 32) + threads - 1) / threads);
+        return launch((const void*)&pack_kernel, dim3(packs), threads, args, st) ? QMV_OK : QMV_E_LAUNCH;
+    }
+    const ExpertPieces at(n, D, F, k, E, bits, gs);
+    SortParams p;
+    p.x = x;
+    p.xp = ws;
+    p.ids = ids;
+    p.base = reinterpret_cast<int*>(ws + at.plan);
+    p.count = p.base + E;
+    p.place = p.count + E;
+    p.plane = at.x_plane;
+    p.P = n * k;
+    p.k = k;
+    p.D = D;
+    p.E = E;
+    p.bits = bits;
+    p.gs = gs;
+    p.f32 = f32;
+    void* args[] = {&p};
+    return launch((const void*)&sort_kernel, dim3(p.P), threads, args, st) ? QMV_OK : QMV_E_LAUNCH;
 }
 
 // the experts of n tokens, whose activations lie packed at the start of ws
@@ -283,9 +424,9 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
 {
     const auto go = bits == 4 ? (gs == 64 ? expert_launch_b4_g64 : expert_launch_b4_g128)
                               : (gs == 64 ? expert_launch_b2_g64 : expert_launch_b2_g128);
-    const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16;
+    const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16, by_expert = sorted(n, k, E);
     bool yf32 = y_dt == QMV_DT_F32;
-    const ExpertPieces at(n, D, F, k, bits, gs);
+    const ExpertPieces at(n, D, F, k, E, bits, gs);
     ExpertParams p;
     p.xp = ws;
     p.ids = ids;
@@ -304,12 +445,15 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
     p.D = D;
     p.F = F;
     p.E = E;
-    p.slots = std::min(p.P, E);
+    p.slots = by_expert ? E : std::min(p.P, E);
+    p.base = by_expert ? reinterpret_cast<const int*>(ws + at.plan) : nullptr;
+    p.count = by_expert ? p.base + E : nullptr;
     p.parts = 0;
     const int ct = p.P <= 12 * E ? 1 : 2;
     if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;
     const float* z = p.z;
-    void* args[] = {&z, &weights, &ids, &y, &D, &E, &k, &yf32};
+    const int* place = by_expert ? p.count + E : nullptr;
+    void* args[] = {&z, &weights, &ids, &place, &y, &D, &E, &k, &yf32};
     return launch((const void*)&combine_kernel, dim3((D + 255) / 256, n), 256, args, st) ? QMV_OK : QMV_E_LAUNCH;
 }
 
@@ -376,14 +520,11 @@ int qmv_experts(const void* x, const float* weights, const int32_t* ids, const u
     if (!disjoint(in, out)) return QMV_E_ALIAS;
     hipStream_t st = static_cast<hipStream_t>(stream);
     char* ws = static_cast<char*>(workspace);
-    constexpr int threads = kRouteWaves * kWave;
     for (int t = 0; t < T; t += kMoeTile) {
-        int n = std::min(kMoeTile, T - t);
-        const char* xt = static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt);
-        bool f32 = x_dt == QMV_DT_F32;
-        void* args[] = {&xt, &ws, &n, &D, &bits, &group_size, &f32};
-        const int packs = (int)(((long long)n * (D * bits / 32) + threads - 1) / threads);
-        if (!launch((const void*)&pack_kernel, dim3(packs), threads, args, st)) return QMV_E_LAUNCH;
+        const int n = std::min(kMoeTile, T - t);
+        if (const int e = run_pack(static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt), ids + (size_t)t * top_k, ws, n, D, F,
+                                   n_experts, top_k, bits, group_size, x_dt, st))
+            return e;
         if (const int e = run_experts(weights + (size_t)t * top_k, ids + (size_t)t * top_k, w13, s13, b13, w2, s2, b2,
                                       static_cast<char*>(y) + (size_t)t * D * size_of(y_dt), ws, n, D, F, n_experts, top_k, bits,
                                       group_size, x_dt, sb_dt, y_dt, st))
@@ -428,13 +569,16 @@ int qmv_moe(const void* x, const void* router, const uint32_t* w13, const void* 
         const int n = std::min(kMoeTile, T - t);
         float* const wt = weights + (size_t)t * top_k;
         int32_t* const it = ids + (size_t)t * top_k;
-        if (const int e = run_route(static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt), router, wt, it, part,
-                                    static_cast<char*>(workspace), n, D, n_experts, top_k, renormalize != 0, x_dt, r_dt, bits,
-                                    group_size, st))
+        const char* const xt = static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt);
+        char* const ws = static_cast<char*>(workspace);
+        const bool later = sorted(n, top_k, n_experts);         // packed when the ids are known
+        if (const int e = run_route(xt, router, wt, it, part, later ? nullptr : ws, n, D, n_experts, top_k, renormalize != 0, x_dt,
+                                    r_dt, bits, group_size, st))
             return e;
+        if (later)
+            if (const int e = run_pack(xt, it, ws, n, D, F, n_experts, top_k, bits, group_size, x_dt, st)) return e;
         if (const int e = run_experts(wt, it, w13, s13, b13, w2, s2, b2, static_cast<char*>(y) + (size_t)t * D * size_of(y_dt),
-                                      static_cast<char*>(workspace), n, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt,
-                                      st))
+                                      ws, n, D, F, n_experts, top_k, bits, group_size, x_dt, sb_dt, y_dt, st))
             return e;
     }
     return QMV_OK;

@@ -18,10 +18,12 @@ struct ExpertParams {
     const uint16_t* s2;
     const uint16_t* b2;
     char* h;                       // packed hidden values of the pairs, three planes
-    float* z;                      // [P][D]
+    float* z;                      // [rows][D]
     size_t x_plane, h_plane;       // bytes of a plane
     int P, k, D, F, E;
     int slots;                     // P: a workgroup per pair, its expert's first; E: one per expert
+    const int* base;               // sorted pairs: an expert's first tile of 16, its pairs, and each
+    const int* count;              // pair's place (a row of xp, h and z); null where pairs keep their order
     int parts;                     // of a row's K
 };
 

@@ -3,7 +3,10 @@
 // A workgroup takes one expert and, for each group of its waves, 16 gate rows with
 // their 16 up rows (or 32 rows of the down product), finds the (token, slot) pairs
 // that chose the expert, and multiplies their activations 16 * CT at a time.  With
-// few tokens every chosen expert's weights are read once and bound the time.
+// few tokens every chosen expert's weights are read once and bound the time.  Where
+// an expert meets many pairs, they have been sorted by expert, in tiles of 16 whose
+// activations lie in the order of the lanes (FRAG): gathered row by row, each of a
+// wave's activation loads would look up a cache line per lane.
 #pragma once
 #include "ops_moe.hpp"
 #include "ops_tile.hpp"
@@ -83,9 +86,17 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     float* const join = reinterpret_cast<float*>(lds + sp.turn);
     uint16_t* const list = reinterpret_cast<uint16_t*>(lds + sp.list);
 
-    const Found found = find_pairs(p.ids, p.P, e, slot, list);
-    if (found.n == 0 || (by_pair && !found.first)) return;
-    const int n = found.n;
+    int n, base = 0;
+    if constexpr (T::FRAG) {
+        n = p.count[e];
+        base = p.base[e] * 16;
+    } else {
+        const Found found = find_pairs(p.ids, p.P, e, slot, list);
+        n = by_pair && !found.first ? 0 : found.n;
+    }
+    if (n == 0) return;
+    // the row of the expert's pair number t
+    auto row_of = [&](int t) { return T::FRAG ? base + t : (int)list[t]; };
 
     // LDS rows: GATE: the groups' gate rows, then their up rows
     typename T::Rows r;
@@ -131,14 +142,14 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
         if (GATE) copy_up.ask();
         keep_order();
     }
-    const Packed pk(p.F, T::BITS, T::GS, false);
+    const Packed pk(p.F, T::BITS, T::GS, T::FRAG);
     typename T::Ring ring;
     for (int t0 = 0; t0 < n; t0 += 16 * CT) {
         lds_barrier();              // the list is there; the partial results before are read
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            const int pair = list[min(t0 + 16 * j + c, n - 1)];
-            T::set_token(r, j, GATE ? p.xp : p.h, GATE ? pair / p.k : pair);
+            const int row = row_of(min(t0 + 16 * j + c, n - 1));
+            T::set_token(r, j, GATE ? p.xp : p.h, GATE && !T::FRAG ? row / p.k : row);
         }
         f32x4 acc[RT][CT];
         T::clear(acc);
@@ -171,7 +182,6 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                 for (int i = threadIdx.x; i < 128 * groups; i += threads) {
                     const int et = i & 15, d = (i >> 4) & 7, g = i >> 7;
                     if (t0 + 16 * j + et < n && g * 16 < left) {
-                        const size_t pair = list[t0 + 16 * j + et];
                         const int word = d / H, ii = d % H, en = word * T::VPW + ii;
                         float v[2];
 #pragma unroll
@@ -181,7 +191,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                         uint32_t ah, am, al, bh, bm, bl;
                         split3(v[0], ah, am, al);
                         split3(v[1], bh, bm, bl);
-                        char* to = p.h + pk.word((int)pair, (first + g * 16) / T::VPW + word) + (ii / 4) * 64 + (ii % 4) * 4;
+                        char* to = p.h + pk.word(row_of(t0 + 16 * j + et), (first + g * 16) / T::VPW + word) + (ii / 4) * pk.op_step() + (ii % 4) * 4;
                         *reinterpret_cast<uint32_t*>(to) = hi16(ah, bh);
                         *reinterpret_cast<uint32_t*>(to + p.h_plane) = hi16(am, bm);
                         *reinterpret_cast<uint32_t*>(to + 2 * p.h_plane) = hi16(al, bl);
@@ -191,7 +201,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                 for (int i = threadIdx.x; i < 16 * 32 * groups; i += threads) {
                     const int en = i & 31, g = (i >> 5) % groups, et = (i >> 5) / groups;
                     if (t0 + 16 * j + et < n && g * 32 + en < left)
-                        p.z[(size_t)list[t0 + 16 * j + et] * N + first + g * 32 + en] = J::sum(join, g * parts, parts, J::at(en, et));
+                        p.z[(size_t)row_of(t0 + 16 * j + et) * N + first + g * 32 + en] = J::sum(join, g * parts, parts, J::at(en, et));
                 }
             }
         }
@@ -217,10 +227,15 @@ int expert_start(const ExpertParams& p, hipStream_t st)
 template <int BITS, int GS, bool SBF>
 int expert_pick(int which, const ExpertParams& p, int ct, bool xf32, hipStream_t st)
 {
+    if (p.base) {
+        if (which == 1) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, false>(p, st);
+        if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, true>(p, st);
+        return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, 1, SBF, true>, true>(p, st)
+                       : expert_start<Tile<BITS, GS, 2, 2, 1, SBF, true>, true>(p, st);
+    }
     if (which == 1) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, false>(p, st);
     if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, true>(p, st);
-    return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, 1, SBF, false>, true>(p, st)
-                   : expert_start<Tile<BITS, GS, 2, 2, 1, SBF, false>, true>(p, st);
+    return expert_start<Tile<BITS, GS, 2, 1, 1, SBF, false>, true>(p, st);
 }
 
 }  // namespace ops
