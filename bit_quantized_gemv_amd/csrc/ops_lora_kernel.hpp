@@ -123,7 +123,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     }
 #pragma unroll
     for (int j = 0; j < CT; ++j) T::set_token(r, j, p.xp, min(m0 + 16 * j + c, p.M - 1));
-    const int slabs = slabs_of(r.chunks), s0 = part * slabs / parts, s1 = (part + 1) * slabs / parts;
+    const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, parts, part), s1 = part_start(slabs, parts, part + 1);
     typename T::Ring ring;
     int a0 = s0, a1 = min(s0 + meta.window, s1);
     const bool active = n0 < p.N;

@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     const uint16_t* const ms = (GATE ? p.s13 : p.s2) + (row0 + first) * r.G;
     const uint16_t* const mb = (GATE ? p.b13 : p.b2) + (row0 + first) * r.G;
     const size_t up = (size_t)N * r.G;
-    const int slabs = slabs_of(r.chunks), s0 = part * slabs / parts, s1 = (part + 1) * slabs / parts;
+    const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, parts, part), s1 = part_start(slabs, parts, part + 1);
     MetaCopy<GATE ? 2 : 4> copy(ms, mb, left * r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left * r.G, threads);
     const int half = 16 * groups * meta.groups;       // the up rows' place
     auto stage = [&](int k) {

@@ -27,7 +27,9 @@
 // wave turns the pieces over through LDS (a write and a read of 16 bytes a lane,
 // one slab ahead; which piece a lane loads is swizzled so that the reads meet
 // distinct banks).  Without this, and with scales loaded by each lane for itself, a
-// 17408 x 5120 product of 16 tokens took 51 us instead of TURNED us.
+// 17408 x 5120 product of 16 tokens took 51 us instead of TURNED us.  Codes are asked
+// for by two slabs, the two halves of a cache line: one at a time, half of the lines
+// were read from memory twice (128 experts, 13 tokens: 249 MB for 168).
 //
 // Scales and biases go to LDS before the product, whole rows at a time: a row's
 // few bytes per slab would cost as many lookups as its codes.
@@ -120,6 +122,13 @@ __host__ __device__ inline int parts_of(int chunks)
 {
     const int n = slabs_of(chunks);
     return n >= 64 ? 8 : n >= 24 ? 4 : n >= 4 ? 2 : 1;
+}
+
+// The slabs of a part: whole pairs, since two slabs of a row share a cache line.
+__host__ __device__ inline int part_start(int slabs, int parts, int part)
+{
+    const int at = 2 * (part * ((slabs + 1) / 2) / parts);
+    return at < slabs ? at : slabs;
 }
 
 // Waves of a workgroup, and row tile groups: the parts of several groups of rows.
@@ -220,13 +229,13 @@ struct Meta {
     {
         constexpr int kMost = 48 * 1024;
         const int G = K / gs, slabs = slabs_of(K * bits / 128), ng = 16 * (32 / bits) / gs;
-        const int per = (slabs + parts - 1) / parts;
+        const int per = ((slabs + 1) / 2 + parts - 1) / parts * 2;
         if (rows * G * 4 <= kMost) {
             groups = G;
             window = per;
             windows = 1;
         } else {
-            window = kMost / (rows * 4 * parts * ng);
+            window = kMost / (rows * 4 * parts * ng) & ~1;
             groups = parts * window * ng;
             windows = (per + window - 1) / window;
         }
@@ -251,13 +260,13 @@ struct Tile {
     static constexpr uint32_t BASE = BITS == 4 ? 0x41804180u : 0x40804080u;  // 16, 4
     static constexpr uint32_t NEG = BITS == 4 ? 0xC180C180u : 0xC080C080u;   // -16, -4
     static constexpr float INV = BITS == 4 ? -1.0f / 16 : -1.0f / 4;
-    // slabs in flight: about 90 registers of them, four at most; for one row tile,
-    // taken where there is hardly a workgroup per compute unit, a third more
+    // Slabs in flight: about 100 registers of them, four at most, or two; codes by two
+    // slabs at once, the halves of a cache line, even where activations go one by one.
     static constexpr int SLAB_REGS = 4 * NG * NF * NP * CT + RT * 4;
-    static constexpr int BUDGET = RT == 1 ? 120 : 90, MOST = RT == 1 ? 8 : 4;
-    static constexpr int PF = SLAB_REGS * 2 > BUDGET ? 1 : BUDGET / SLAB_REGS < MOST ? BUDGET / SLAB_REGS : MOST;
+    static constexpr int PF = SLAB_REGS * 4 <= 100 ? 4 : SLAB_REGS * 2 <= 100 ? 2 : 1;
+    static constexpr int WPF = PF < 2 ? 2 : PF;
     // waves per SIMD that its kernels leave registers for
-    static constexpr int WAVES = RT > 1 && SLAB_REGS * PF + 8 * RT * CT <= 90 ? 3 : 2;
+    static constexpr int WAVES = SLAB_REGS * PF + 8 * RT * CT <= 64 ? 3 : 2;
     static constexpr int TURN = RT * 1024;            // bytes of LDS per wave to turn a slab over
 
     struct Rows {                  // what a wave multiplies
@@ -273,7 +282,7 @@ struct Tile {
     };
 
     struct Ring {
-        u32x4 w[PF][RT];
+        u32x4 w[WPF][RT];
         u32x4 x[PF][CT][NG][NF][NP];
     };
 
@@ -365,8 +374,8 @@ struct Tile {
     }
 
     // acc += the slab whose codes are w and whose activations are slot u's; where
-    // MORE, those of slab `next` go in flight in their place, piece by piece
-    template <bool MORE>
+    // MORE, the activations of slab `next` go in flight in their place, piece by piece
+    template <bool MORE, bool TAIL>
     static __device__ __forceinline__ void step(f32x4 (&acc)[RT][CT], u32x4 (&w)[RT], Ring& t, int u, const Rows& r, int slab, int next)
     {
         uint32_t s[RT][NM], b[RT][NM];
@@ -391,7 +400,7 @@ struct Tile {
         const u32x4 neg = {NEG, NEG, NEG, NEG};
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            if (!MORE && g > 0 && slab * NG + g >= r.G) break;
+            if (TAIL && g > 0 && slab * NG + g >= r.G) break;      // past the row's end, in its last slab
             u32x4 wo[RT][NF];
 #pragma unroll
             for (int i = 0; i < RT; ++i)
@@ -431,18 +440,23 @@ struct Tile {
         }
     }
 
-    // slabs s0.. of [s0, s1) (s0 < s1) go in flight
+    // slabs s0.. of [s0, s1) (s0 < s1, s0 even) go in flight
     static __device__ __forceinline__ void begin(Ring& t, const Rows& r, int s0, int s1)
     {
 #pragma unroll
-        for (int u = 0; u < PF; ++u) {
-            load_w(t, u, r, min(s0 + u, s1 - 1));
-            keep_order();
+        for (int u = 0; u < WPF; ++u) {
+            if (u % 2 == 0) {
+                load_w(t, u, r, min(s0 + u, s1 - 1));
+                load_w(t, u + 1, r, min(s0 + u + 1, s1 - 1));
+                keep_order();
+            }
+            if (u < PF) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g)
+                for (int g = 0; g < NG; ++g)
 #pragma unroll
-                for (int j = 0; j < CT; ++j) load_x(t, u, j, g, r, min(s0 + u, s1 - 1));
-            keep_order();
+                    for (int j = 0; j < CT; ++j) load_x(t, u, j, g, r, min(s0 + u, s1 - 1));
+                keep_order();
+            }
         }
     }
 
@@ -454,27 +468,34 @@ struct Tile {
         u32x4 w[RT];
         turn(w, t, 0, r);
         int s = s0;
-        for (; s + PF < s1; s += PF) {
+        for (; s + WPF < s1; s += WPF) {
 #pragma unroll
-            for (int u = 0; u < PF; ++u) {
+            for (int u = 0; u < WPF; ++u) {
                 __builtin_amdgcn_sched_barrier(0);
-                load_w(t, u, r, min(s + u + PF, s1 - 1));      // slot u's codes are in w
-                keep_order();
                 u32x4 n[RT];
-                turn(n, t, (u + 1) % PF, r);
-                step<true>(acc, w, t, u, r, s + u, min(s + u + PF, s1 - 1));
+                turn(n, t, (u + 1) % WPF, r);
+                if (u % 2 == 0) {                              // both slots' codes are in w and n
+                    keep_order();
+                    load_w(t, u, r, min(s + u + WPF, s1 - 1));
+                    load_w(t, u + 1, r, min(s + u + 1 + WPF, s1 - 1));
+                    keep_order();
+                }
+                step<true, false>(acc, w, t, u % PF, r, s + u, min(s + u + PF, s1 - 1));
 #pragma unroll
                 for (int i = 0; i < RT; ++i) w[i] = n[i];
             }
         }
 #pragma unroll
-        for (int u = 0; u < PF; ++u)
+        for (int u = 0; u < WPF; ++u)
             if (s + u < s1) {
                 __builtin_amdgcn_sched_barrier(0);
                 u32x4 n[RT];
-                if (u + 1 < PF) turn(n, t, (u + 1) % PF, r);
-                step<false>(acc, w, t, u, r, s + u, 0);
-                if (u + 1 < PF)
+                if (u + 1 < WPF) turn(n, t, (u + 1) % WPF, r);
+                if (u + PF < WPF)
+                    step<true, true>(acc, w, t, u % PF, r, s + u, min(s + u + PF, s1 - 1));
+                else
+                    step<false, true>(acc, w, t, u % PF, r, s + u, 0);
+                if (u + 1 < WPF)
 #pragma unroll
                     for (int i = 0; i < RT; ++i) w[i] = n[i];
             }
@@ -539,7 +560,7 @@ __device__ __forceinline__ void stage_window(uint16_t* to, const uint16_t* from,
 {
     const int wg = window * ng, row = parts * wg;
     for (int i = threadIdx.x; i < rows * row; i += threads) {
-        const int part = i % row / wg, g = (part * slabs / parts + number * window) * ng + i % wg;
+        const int part = i % row / wg, g = (part_start(slabs, parts, part) + number * window) * ng + i % wg;
         if (g < G) to[i] = from[(size_t)(i / row) * G + g];
     }
 }
