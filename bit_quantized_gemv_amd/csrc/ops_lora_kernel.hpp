@@ -127,7 +127,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     typename T::Ring ring;
     int a0 = s0, a1 = min(s0 + meta.window, s1);
     const bool active = n0 < p.N;
-    MetaCopy<4> copy(p.s + (size_t)first * r.G, p.b + (size_t)first * r.G, rows * r.G, kWave * waves);
+    MetaCopy<4> copy(p.s + (size_t)first * r.G, p.b + (size_t)first * r.G, rows, r.G, kWave * waves);
     if (meta.windows == 1) {
         copy.ask();
     } else {

@@ -17,7 +17,7 @@ struct ExpertParams {
     const uint32_t* w2;
     const uint16_t* s2;
     const uint16_t* b2;
-    char* h;                       // packed hidden values of the pairs, three planes
+    char* h;                       // packed hidden values of the pairs, in planes
     float* z;                      // [rows][D]
     size_t x_plane, h_plane;       // bytes of a plane
     int P, k, D, F, E;
@@ -25,6 +25,8 @@ struct ExpertParams {
     const int* base;               // sorted pairs: an expert's first tile of 16, its pairs, and each
     const int* count;              // pair's place (a row of xp, h and z); null where pairs keep their order
     int parts;                     // of a row's K
+    int h_planes;                  // three: exact; two, for bf16 outputs: off by 2^-17, a two hundred and fiftieth of
+                                   // their rounding, for a third less of the down product's work
 };
 
 // which = 0: gate and up products and the activation (xp -> h); 1: down product (h -> z)

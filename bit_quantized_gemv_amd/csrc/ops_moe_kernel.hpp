@@ -118,7 +118,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     const uint16_t* const mb = (GATE ? p.b13 : p.b2) + (row0 + first) * r.G;
     const size_t up = (size_t)N * r.G;
     const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, parts, part), s1 = part_start(slabs, parts, part + 1);
-    MetaCopy<GATE ? 2 : 4> copy(ms, mb, left * r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left * r.G, threads);
+    MetaCopy<GATE ? 2 : 4> copy(ms, mb, left, r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left, r.G, threads);
     const int half = 16 * groups * meta.groups;       // the up rows' place
     auto stage = [&](int k) {
         stage_window(scales, ms, left, r.G, T::NG, slabs, parts, meta.window, k, threads);
@@ -188,13 +188,18 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                         for (int b = 0; b < 2; ++b)
                             v[b] = silu(J::sum(join, g * parts, parts, J::at(en + b * H, et))) *
                                    J::sum(join, g * parts, parts, J::at(16 + en + b * H, et));
-                        uint32_t ah, am, al, bh, bm, bl;
-                        split3(v[0], ah, am, al);
-                        split3(v[1], bh, bm, bl);
+                        uint32_t ah, am, al = 0, bh, bm, bl = 0;
+                        if (p.h_planes == 3) {
+                            split3(v[0], ah, am, al);
+                            split3(v[1], bh, bm, bl);
+                        } else {
+                            split2(v[0], ah, am);
+                            split2(v[1], bh, bm);
+                        }
                         char* to = p.h + pk.word(row_of(t0 + 16 * j + et), (first + g * 16) / T::VPW + word) + (ii / 4) * pk.op_step() + (ii % 4) * 4;
                         *reinterpret_cast<uint32_t*>(to) = hi16(ah, bh);
                         *reinterpret_cast<uint32_t*>(to + p.h_plane) = hi16(am, bm);
-                        *reinterpret_cast<uint32_t*>(to + 2 * p.h_plane) = hi16(al, bl);
+                        if (p.h_planes == 3) *reinterpret_cast<uint32_t*>(to + 2 * p.h_plane) = hi16(al, bl);
                     }
                 }
             } else {
@@ -224,16 +229,23 @@ int expert_start(const ExpertParams& p, hipStream_t st)
     return hipLaunchKernel(fn, dim3((N + rows - 1) / rows, p.slots), dim3(kWave * waves), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }
 
+template <int BITS, int GS, bool SBF, bool SORTED>
+int expert_down(const ExpertParams& p, hipStream_t st)
+{
+    return p.h_planes == 3 ? expert_start<Tile<BITS, GS, 2, 1, 3, SBF, SORTED>, false>(p, st)
+                           : expert_start<Tile<BITS, GS, 2, 1, 2, SBF, SORTED>, false>(p, st);
+}
+
 template <int BITS, int GS, bool SBF>
 int expert_pick(int which, const ExpertParams& p, int ct, bool xf32, hipStream_t st)
 {
     if (p.base) {
-        if (which == 1) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, false>(p, st);
+        if (which == 1) return expert_down<BITS, GS, SBF, true>(p, st);
         if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, true>(p, st);
         return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, 1, SBF, true>, true>(p, st)
                        : expert_start<Tile<BITS, GS, 2, 2, 1, SBF, true>, true>(p, st);
     }
-    if (which == 1) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, false>(p, st);
+    if (which == 1) return expert_down<BITS, GS, SBF, false>(p, st);
     if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, true>(p, st);
     return expert_start<Tile<BITS, GS, 2, 1, 1, SBF, false>, true>(p, st);
 }

@@ -91,6 +91,15 @@ __device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& m, uint32
     l = f32_bits(r - bits_f32(m));
 }
 
+__device__ __forceinline__ uint16_t to_bf16(float f);
+
+// An fp32 value as two bf16 values, rounded to nearest: off by 2^-17 of it at most.
+__device__ __forceinline__ void split2(float v, uint32_t& h, uint32_t& m)
+{
+    h = (uint32_t)to_bf16(v) << 16;
+    m = (uint32_t)to_bf16(v - bits_f32(h)) << 16;
+}
+
 // round to nearest even; NaN stays NaN
 __device__ __forceinline__ uint16_t to_bf16(float f)
 {
@@ -222,7 +231,8 @@ __device__ __forceinline__ void pack(const char* x, char* to, int tokens, int K,
 // Scales and biases of a workgroup's rows in LDS.  All groups of a row at once
 // where they fit; else a window of each part's groups at a time.
 struct Meta {
-    int groups;        // values per row in LDS
+    int groups;        // values per row in LDS: a row's and, where rows are whole 16-byte pieces, one piece
+                       // more, which puts 16 rows on different banks
     int window;        // slabs of a part per window
     int windows;
     __host__ __device__ Meta(int rows, int K, int bits, int gs, int parts)
@@ -231,7 +241,7 @@ struct Meta {
         const int G = K / gs, slabs = slabs_of(K * bits / 128), ng = 16 * (32 / bits) / gs;
         const int per = ((slabs + 1) / 2 + parts - 1) / parts * 2;
         if (rows * G * 4 <= kMost) {
-            groups = G;
+            groups = G % 8 == 0 ? G + 8 : G;
             window = per;
             windows = 1;
         } else {
@@ -260,13 +270,15 @@ struct Tile {
     static constexpr uint32_t BASE = BITS == 4 ? 0x41804180u : 0x40804080u;  // 16, 4
     static constexpr uint32_t NEG = BITS == 4 ? 0xC180C180u : 0xC080C080u;   // -16, -4
     static constexpr float INV = BITS == 4 ? -1.0f / 16 : -1.0f / 4;
-    // Slabs in flight: about 100 registers of them, four at most, or two; codes by two
+    // Slabs in flight: about 100 registers of them, four at most, or two.  The lightest
+    // instances take two and a third wave per SIMD (one token, 15360 x 3840: 17.8 us against 18.8).  Codes go by two
     // slabs at once, the halves of a cache line, even where activations go one by one.
+    static constexpr bool LIGHT = BITS_ == 4 && RT_ == 2 && CT_ == 1 && NP_ == 1;
     static constexpr int SLAB_REGS = 4 * NG * NF * NP * CT + RT * 4;
-    static constexpr int PF = SLAB_REGS * 4 <= 100 ? 4 : SLAB_REGS * 2 <= 100 ? 2 : 1;
+    static constexpr int PF = !LIGHT && SLAB_REGS * 4 <= 100 ? 4 : SLAB_REGS * 2 <= 100 ? 2 : 1;
     static constexpr int WPF = PF < 2 ? 2 : PF;
     // waves per SIMD that its kernels leave registers for
-    static constexpr int WAVES = SLAB_REGS * PF + 8 * RT * CT <= 64 ? 3 : 2;
+    static constexpr int WAVES = LIGHT ? 3 : 2;
     static constexpr int TURN = RT * 1024;            // bytes of LDS per wave to turn a slab over
 
     struct Rows {                  // what a wave multiplies
@@ -517,9 +529,10 @@ struct MetaCopy {
     u32x4 v[HELD];
     const uint16_t *s, *b;
     int count, whole;      // values, and whole pieces, of each
+    int row;               // pieces per row where LDS rows are padded, else 0
     int threads;           // of the workgroup (blockDim is an argument of its own, and a round trip)
-    __device__ __forceinline__ MetaCopy(const uint16_t* s_, const uint16_t* b_, int count_, int threads_)
-        : s(s_), b(b_), count(count_), whole(count_ / 8), threads(threads_)
+    __device__ __forceinline__ MetaCopy(const uint16_t* s_, const uint16_t* b_, int rows, int G, int threads_)
+        : s(s_), b(b_), count(rows * G), whole(rows * G / 8), row(G % 8 == 0 ? G / 8 : 0), threads(threads_)
     {
     }
     __device__ __forceinline__ u32x4 load(int i) const
@@ -537,10 +550,8 @@ struct MetaCopy {
     __device__ __forceinline__ void put(uint16_t* ts, uint16_t* tb) const
     {
         auto store = [&](int i, const u32x4& x) {
-            if (i < whole)
-                reinterpret_cast<u32x4*>(ts)[i] = x;
-            else if (i < 2 * whole)
-                reinterpret_cast<u32x4*>(tb)[i - whole] = x;
+            const int at = i < whole ? i : i - whole;
+            if (i < 2 * whole) reinterpret_cast<u32x4*>(i < whole ? ts : tb)[row > 0 ? at + at / row : at] = x;
         };
 #pragma unroll
         for (int k = 0; k < HELD; ++k) store(threadIdx.x + k * threads, v[k]);
