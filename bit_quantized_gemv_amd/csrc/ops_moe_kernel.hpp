@@ -213,12 +213,21 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     }
 }
 
+// Parts of a row's K: with many experts there are waves enough, and a wave of few slabs
+// is mostly its start and end (13 tokens over 128 experts 108 us with two parts of 8
+// and of 4 slabs, 98 with one).
+inline int expert_parts(int chunks)
+{
+    const int n = slabs_of(chunks);
+    return n >= 64 ? 8 : n >= 24 ? 4 : 1;
+}
+
 template <class T, bool GATE>
 int expert_start(const ExpertParams& p, hipStream_t st)
 {
     const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;
     ExpertParams q = p;
-    q.parts = parts_of(K / (4 * T::VPW));
+    q.parts = expert_parts(K / (4 * T::VPW));
     const int waves = waves_of(q.parts), groups = waves / q.parts, rows = (GATE ? 16 : 32) * groups;
     const ExpertSpace sp(Meta(32 * groups, K, T::BITS, T::GS, q.parts), waves, 32 * groups, p.P);
     const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
