@@ -213,7 +213,7 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         p.R = rank;
         p.Rp = pad_rank(rank);
         p.pieces = shrink_pieces(K);
-        p.parts = parts_of(K * bits / 128);
+        p.log_parts = __builtin_ctz(parts_of(K * bits / 128));
         p.yf32 = y_dt == QMV_DT_F32;
         p.adf16 = ad_dt == QMV_DT_F16;
         if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;

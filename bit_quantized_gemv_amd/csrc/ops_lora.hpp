@@ -5,6 +5,8 @@
 
 #include <cstdint>
 
+#include "ops_tile.hpp"
+
 namespace ops {
 
 // Columns of K that one workgroup of the first kernel sums: 8 waves of 8 steps
@@ -39,7 +41,8 @@ struct LoraParams {
     AdapterList* lists;   // [blocks of tokens]
     char* xp;             // packed activations
     size_t plane;         // bytes of one of their planes
-    int M, N, K, L, R, Rp, pieces, parts;
+    int M, N, K, L, R, Rp, pieces, log_parts;
+    Meta meta;
     bool yf32, adf16;
 };
 

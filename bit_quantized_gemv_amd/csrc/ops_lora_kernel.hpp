@@ -68,9 +68,9 @@ constexpr int kFactorTurn = 16 * 9 * 16;       // bytes of LDS per wave to turn 
 // the hidden values in three bf16 planes.
 struct LoraSpace {
     int biases, turn, factors, delta, hidden, bytes;
-    __host__ __device__ LoraSpace(const Meta& meta, int waves, int rt, int ct, int parts, int Rp)
+    __host__ __device__ LoraSpace(const Meta& meta, int waves, int groups, int rt, int ct, int Rp)
     {
-        const int tiles = waves / parts * rt, tokens = 16 * ct;
+        const int tiles = groups * rt, tokens = 16 * ct;
         biases = meta.bytes(16 * tiles) / 2;
         turn = 2 * biases;
         factors = turn + waves * rt * Join<1>::kWords * 4;
@@ -92,14 +92,15 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     constexpr int RT = T::RT, CT = T::CT, DEPTH = 4;
     using J = Join<RT>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    together(p.w, p.s, p.b, p.y, p.lb, p.h, p.lists, p.xp, p.plane, p.M, p.N, p.K, p.R, p.Rp, p.pieces, p.parts);
+    together(p.w, p.s, p.b, p.y, p.lb, p.h, p.lists, p.xp, p.plane, p.M, p.N, p.K, p.R, p.Rp, p.pieces, p.log_parts, p.meta.groups,
+             p.meta.window, p.meta.windows);
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
     const int c = lane & 15, q = lane >> 4;
-    const int parts = p.parts, waves = waves_of(parts), groups = waves / parts, tiles = groups * RT;       // powers of two
+    const int lp = p.log_parts, parts = 1 << lp, waves = waves_of(parts), groups = waves >> lp, tiles = groups * RT;      // powers of two
     const int first = blockIdx.x * tiles * 16, m0 = blockIdx.y * 16 * CT, tokens = min(16 * CT, p.M - m0);
-    const int n0 = first + wave / parts * RT * 16, part = wave % parts, rows = min(16 * tiles, p.N - first);
-    const Meta meta(16 * tiles, p.K, T::BITS, T::GS, parts);
-    const LoraSpace sp(meta, waves, RT, CT, parts, p.Rp);
+    const int n0 = first + (wave >> lp) * RT * 16, part = wave & (parts - 1), rows = min(16 * tiles, p.N - first);
+    const Meta& meta = p.meta;
+    const LoraSpace sp(meta, waves, groups, RT, CT, p.Rp);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(lds);
     uint16_t* const biases = reinterpret_cast<uint16_t*>(lds + sp.biases);
     float* const join = reinterpret_cast<float*>(lds + sp.turn);
@@ -123,7 +124,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     }
 #pragma unroll
     for (int j = 0; j < CT; ++j) T::set_token(r, j, p.xp, min(m0 + 16 * j + c, p.M - 1));
-    const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, parts, part), s1 = part_start(slabs, parts, part + 1);
+    const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, lp, part), s1 = part_start(slabs, lp, part + 1);
     typename T::Ring ring;
     int a0 = s0, a1 = min(s0 + meta.window, s1);
     const bool active = n0 < p.N;
@@ -159,8 +160,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     int at_row[2], at_piece[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
-        at_row[s] = (lane + 64 * s) / max(pieces, 1);
-        at_piece[s] = (lane + 64 * s) % max(pieces, 1);
+        at_row[s] = small_div(lane + 64 * s, 1.0f / (float)max(pieces, 1));
+        at_piece[s] = lane + 64 * s - at_row[s] * pieces;
     }
     auto unit_rows = [&](int u) {
         const int a = __builtin_amdgcn_readlane(list_adapter, u >> shift);
@@ -179,8 +180,9 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     if (meta.windows == 1) copy.put(scales, biases);
     if (units > 0) {
         const int octs = p.Rp / 8;
+        const float per_oct = 1.0f / (float)octs;
         for (int e = threadIdx.x; e < tokens * octs; e += kWave * waves) {
-            const int t = e / octs, k = e % octs * 8;
+            const int t = small_div(e, per_oct), k = (e - t * octs) * 8;
             const char* hp = reinterpret_cast<const char*>(p.h + (size_t)(m0 + t) * p.Rp + k);
             const size_t piece = (size_t)p.M * p.Rp * 4;
             f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
@@ -315,14 +317,15 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
 template <class T>
 int lora_start(const LoraParams& p, hipStream_t st)
 {
-    const int waves = waves_of(p.parts), rows = waves / p.parts * 16 * T::RT;
+    const int parts = 1 << p.log_parts, waves = waves_of(parts), groups = waves / parts, rows = groups * 16 * T::RT;
     const dim3 grid((p.N + rows - 1) / rows, (p.M + 16 * T::CT - 1) / (16 * T::CT));
-    const LoraSpace sp(Meta(rows, p.K, T::BITS, T::GS, p.parts), waves, T::RT, T::CT, p.parts, p.Rp);
+    LoraParams q = p;
+    q.meta = Meta(rows, p.K, T::BITS, T::GS, parts);
+    const LoraSpace sp(q.meta, waves, groups, T::RT, T::CT, p.Rp);
     const void* fn = reinterpret_cast<const void*>(&lora_kernel<T>);
     if (sp.bytes > 64 * 1024 &&
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, sp.bytes) != hipSuccess)
         return 1;
-    LoraParams q = p;
     void* args[] = {&q};
     return hipLaunchKernel(fn, grid, dim3(kWave * waves), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }

@@ -448,7 +448,8 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
     p.slots = by_expert ? E : std::min(p.P, E);
     p.base = by_expert ? reinterpret_cast<const int*>(ws + at.plan) : nullptr;
     p.count = by_expert ? p.base + E : nullptr;
-    p.parts = 0;
+    p.log_parts = 0;
+    p.per_k = 1.0f / (float)k;
     p.h_planes = yf32 ? 3 : 2;
     const int ct = p.P <= 12 * E ? 1 : 2;
     if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;

@@ -4,6 +4,8 @@
 
 #include <cstdint>
 
+#include "ops_tile.hpp"
+
 namespace ops {
 
 constexpr int kMoeTile = 256;      // tokens per set of launches
@@ -24,7 +26,9 @@ struct ExpertParams {
     int slots;                     // P: a workgroup per pair, its expert's first; E: one per expert
     const int* base;               // sorted pairs: an expert's first tile of 16, its pairs, and each
     const int* count;              // pair's place (a row of xp, h and z); null where pairs keep their order
-    int parts;                     // of a row's K
+    int log_parts;                 // of a row's K
+    Meta meta;
+    float per_k;                   // 1 / k
     int h_planes;                  // three: exact; two, for bf16 outputs: off by 2^-17, a two hundred and fiftieth of
                                    // their rounding, for a third less of the down product's work
 };

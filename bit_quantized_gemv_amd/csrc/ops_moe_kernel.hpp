@@ -68,18 +68,18 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     using J = Join<RT>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     together(p.ids, GATE ? p.w13 : p.w2, GATE ? p.s13 : p.s2, GATE ? p.b13 : p.b2, GATE ? p.xp : p.h, GATE ? p.x_plane : p.h_plane,
-             p.P, p.k, p.D, p.F, p.E, p.slots, p.parts);
+             p.P, p.D, p.F, p.E, p.slots, p.log_parts, p.meta.groups, p.meta.window, p.meta.windows, p.per_k);
     const int slot = blockIdx.y;
     const bool by_pair = p.slots == p.P;
     const int e = by_pair ? p.ids[slot] : slot;
     if (e < 0 || e >= p.E) return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int c = lane & 15, parts = p.parts, waves = waves_of(parts), groups = waves / parts, threads = kWave * waves;
-    const int group = wave / parts, part = wave % parts;
+    const int c = lane & 15, lp = p.log_parts, parts = 1 << lp, waves = waves_of(parts), groups = waves >> lp, threads = kWave * waves;
+    const int group = wave >> lp, part = wave & (parts - 1);
     const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;            // N is a multiple of 64
     constexpr int ROWS = GATE ? 16 : 32;                             // outputs of a group
     const int first = blockIdx.x * ROWS * groups, left = min(ROWS * groups, N - first), n0 = first + group * ROWS;
-    const Meta meta(32 * groups, K, T::BITS, T::GS, parts);
+    const Meta& meta = p.meta;
     const ExpertSpace sp(meta, waves, 32 * groups, p.P);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(lds);
     uint16_t* const biases = reinterpret_cast<uint16_t*>(lds + sp.biases);
@@ -117,7 +117,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     const uint16_t* const ms = (GATE ? p.s13 : p.s2) + (row0 + first) * r.G;
     const uint16_t* const mb = (GATE ? p.b13 : p.b2) + (row0 + first) * r.G;
     const size_t up = (size_t)N * r.G;
-    const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, parts, part), s1 = part_start(slabs, parts, part + 1);
+    const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, lp, part), s1 = part_start(slabs, lp, part + 1);
     MetaCopy<GATE ? 2 : 4> copy(ms, mb, left, r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left, r.G, threads);
     const int half = 16 * groups * meta.groups;       // the up rows' place
     auto stage = [&](int k) {
@@ -149,7 +149,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const int row = row_of(min(t0 + 16 * j + c, n - 1));
-            T::set_token(r, j, GATE ? p.xp : p.h, GATE && !T::FRAG ? row / p.k : row);
+            T::set_token(r, j, GATE ? p.xp : p.h, GATE && !T::FRAG ? small_div(row, p.per_k) : row);
         }
         f32x4 acc[RT][CT];
         T::clear(acc);
@@ -204,7 +204,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                 }
             } else {
                 for (int i = threadIdx.x; i < 16 * 32 * groups; i += threads) {
-                    const int en = i & 31, g = (i >> 5) % groups, et = (i >> 5) / groups;
+                    const int en = i & 31, g = (i >> 5) & (groups - 1), et = small_div(i >> 5, 1.0f / (float)groups);
                     if (t0 + 16 * j + et < n && g * 32 + en < left)
                         p.z[(size_t)row_of(t0 + 16 * j + et) * N + first + g * 32 + en] = J::sum(join, g * parts, parts, J::at(en, et));
                 }
@@ -227,9 +227,10 @@ int expert_start(const ExpertParams& p, hipStream_t st)
 {
     const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;
     ExpertParams q = p;
-    q.parts = expert_parts(K / (4 * T::VPW));
-    const int waves = waves_of(q.parts), groups = waves / q.parts, rows = (GATE ? 16 : 32) * groups;
-    const ExpertSpace sp(Meta(32 * groups, K, T::BITS, T::GS, q.parts), waves, 32 * groups, p.P);
+    const int parts = expert_parts(K / (4 * T::VPW)), waves = waves_of(parts), groups = waves / parts, rows = (GATE ? 16 : 32) * groups;
+    q.log_parts = __builtin_ctz(parts);
+    q.meta = Meta(32 * groups, K, T::BITS, T::GS, parts);
+    const ExpertSpace sp(q.meta, waves, 32 * groups, p.P);
     const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
     if (sp.bytes > 64 * 1024 &&
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, sp.bytes) != hipSuccess)

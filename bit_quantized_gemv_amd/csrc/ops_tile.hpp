@@ -134,11 +134,16 @@ __host__ __device__ inline int parts_of(int chunks)
 }
 
 // The slabs of a part: whole pairs, since two slabs of a row share a cache line.
-__host__ __device__ inline int part_start(int slabs, int parts, int part)
+__host__ __device__ inline int part_start(int slabs, int log_parts, int part)
 {
-    const int at = 2 * (part * ((slabs + 1) / 2) / parts);
+    const int at = (part * ((slabs + 1) / 2) >> log_parts) * 2;
     return at < slabs ? at : slabs;
 }
+
+// Small quotients: a / b with inv = 1 / b, for a below 2^20.  (A division by a number
+// that is not known when compiling is some forty instructions, and a kernel's start
+// is a good part of its time.)
+__device__ __forceinline__ int small_div(int a, float inv) { return (int)(((float)a + 0.5f) * inv); }
 
 // Waves of a workgroup, and row tile groups: the parts of several groups of rows.
 __host__ __device__ inline int waves_of(int parts) { return parts > 4 ? parts : 4; }
@@ -231,11 +236,12 @@ __device__ __forceinline__ void pack(const char* x, char* to, int tokens, int K,
 // Scales and biases of a workgroup's rows in LDS.  All groups of a row at once
 // where they fit; else a window of each part's groups at a time.
 struct Meta {
+    Meta() = default;
     int groups;        // values per row in LDS: a row's and, where rows are whole 16-byte pieces, one piece
                        // more, which puts 16 rows on different banks
     int window;        // slabs of a part per window
     int windows;
-    __host__ __device__ Meta(int rows, int K, int bits, int gs, int parts)
+    Meta(int rows, int K, int bits, int gs, int parts)       // on the host: a kernel argument
     {
         constexpr int kMost = 48 * 1024;
         const int G = K / gs, slabs = slabs_of(K * bits / 128), ng = 16 * (32 / bits) / gs;
@@ -529,10 +535,10 @@ struct MetaCopy {
     u32x4 v[HELD];
     const uint16_t *s, *b;
     int count, whole;      // values, and whole pieces, of each
-    int row;               // pieces per row where LDS rows are padded, else 0
+    float per_row;         // where LDS rows are padded: 1 / pieces per row, else 0
     int threads;           // of the workgroup (blockDim is an argument of its own, and a round trip)
     __device__ __forceinline__ MetaCopy(const uint16_t* s_, const uint16_t* b_, int rows, int G, int threads_)
-        : s(s_), b(b_), count(rows * G), whole(rows * G / 8), row(G % 8 == 0 ? G / 8 : 0), threads(threads_)
+        : s(s_), b(b_), count(rows * G), whole(rows * G / 8), per_row(G % 8 == 0 ? 8.0f / (float)G : 0.0f), threads(threads_)
     {
     }
     __device__ __forceinline__ u32x4 load(int i) const
@@ -551,7 +557,7 @@ struct MetaCopy {
     {
         auto store = [&](int i, const u32x4& x) {
             const int at = i < whole ? i : i - whole;
-            if (i < 2 * whole) reinterpret_cast<u32x4*>(i < whole ? ts : tb)[row > 0 ? at + at / row : at] = x;
+            if (i < 2 * whole) reinterpret_cast<u32x4*>(i < whole ? ts : tb)[at + small_div(at, per_row)] = x;      // (0.5 * 0 is no row)
         };
 #pragma unroll
         for (int k = 0; k < HELD; ++k) store(threadIdx.x + k * threads, v[k]);
@@ -569,9 +575,10 @@ struct MetaCopy {
 __device__ __forceinline__ void stage_window(uint16_t* to, const uint16_t* from, int rows, int G, int ng, int slabs, int parts,
                                              int window, int number, int threads)
 {
+    const int log_parts = __builtin_ctz(parts);
     const int wg = window * ng, row = parts * wg;
     for (int i = threadIdx.x; i < rows * row; i += threads) {
-        const int part = i % row / wg, g = (part_start(slabs, parts, part) + number * window) * ng + i % wg;
+        const int part = i % row / wg, g = (part_start(slabs, log_parts, part) + number * window) * ng + i % wg;
         if (g < G) to[i] = from[(size_t)(i / row) * G + g];
     }
 }
