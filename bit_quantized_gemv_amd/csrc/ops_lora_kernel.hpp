@@ -1,6 +1,8 @@
 // ops_lora_kernel.hpp -- the second kernel of the adapted projection: the
 // quantized product and, in its epilogue, the adapters' second product.
 #pragma once
+#include <type_traits>
+
 #include "ops_lora.hpp"
 #include "ops_tile.hpp"
 
@@ -163,20 +165,21 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         at_row[s] = small_div(lane + 64 * s, 1.0f / (float)max(pieces, 1));
         at_piece[s] = lane + 64 * s - at_row[s] * pieces;
     }
+    // a tile past the last row has no outputs: its loads repeat that row
     auto unit_rows = [&](int u) {
         const int a = __builtin_amdgcn_readlane(list_adapter, u >> shift);
-        return p.lb + ((size_t)a * p.N + first + (u & (tiles - 1)) * 16) * p.R;
+        return p.lb + ((size_t)a * p.N + min(first + (u & (tiles - 1)) * 16, p.N - 1)) * p.R;
     };
-    auto unit_left = [&](int u) { return min(16, p.N - (first + (u & (tiles - 1)) * 16)); };       // none past the last row
+    auto unit_left = [&](int u) { return min(16, p.N - (first + (u & (tiles - 1)) * 16)); };
     auto load_unit = [&](u32x4 (&to)[2], int u) {
         const uint16_t* rows = unit_rows(u);
-        const int last = unit_left(u) - 1;
+        const int last = max(unit_left(u), 1) - 1;
 #pragma unroll
         for (int s = 0; s < 2; ++s)
             to[s] = *reinterpret_cast<const u32x4*>(rows + (size_t)min(at_row[s], last) * p.R + at_piece[s] * 8);
     };
     char* const turn = lds + sp.factors + wave * kFactorTurn;
-    if (r8 && wave < units && unit_left(wave) > 0) load_unit(v[0], wave);
+    if (r8 && wave < units) load_unit(v[0], wave);
     if (meta.windows == 1) copy.put(scales, biases);
     if (units > 0) {
         const int octs = p.Rp / 8;
@@ -229,7 +232,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         if (a0 < a1) T::begin(ring, r, a0, a1);
     }
 
-    auto unit = [&](const u32x4 (&raw)[2], int u) {
+    auto unit = [&](auto aligned, const u32x4 (&raw)[2], int u) {
+        constexpr bool R8 = decltype(aligned)::value;
         const int tile = u & (tiles - 1), left = unit_left(u), entry = u >> shift;
         if (left <= 0) return;
         const unsigned long long mine =
@@ -238,7 +242,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         const float scale = bits_f32(__builtin_amdgcn_readlane(f32_bits(list_scaling), entry));
         const uint16_t* const row = unit_rows(u) + (size_t)min(c, left - 1) * p.R;
         u32x4 b[2];
-        if (r8) {
+        if constexpr (R8) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
                 if (at_row[s] < 16) *reinterpret_cast<u32x4*>(turn + (at_row[s] * stride + at_piece[s]) * 16) = raw[s];
@@ -270,27 +274,42 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
             step(b[0], 0);
             if (p.Rp > 32) step(b[1], 32);
             for (int k = 64; k < p.Rp; k += 32)
-                step(r8 ? trim8(raw8(row, 8 * q + k, p.R), 8 * q + k, p.R) : slow8(row, 8 * q + k, p.R), k);
+                step(R8 ? trim8(raw8(row, 8 * q + k, p.R), 8 * q + k, p.R) : slow8(row, 8 * q + k, p.R), k);
 #pragma unroll
             for (int e = 0; e < 4; ++e)
                 if ((of_tile >> (4 * q + e)) & 1) delta[(tile * 16 * CT + 16 * j + 4 * q + e) * 16 + c] = scale * acc[e];
         }
     };
+    // Of the loop's loads none is behind a branch (a wait would then assume it was not
+    // taken); the last rounds, which have fewer left to ask for, come after it.
     if (r8) {
+        constexpr std::true_type aligned{};
 #pragma unroll
         for (int i = 1; i < DEPTH; ++i)
-            if (wave + i * waves < units && unit_left(wave + i * waves) > 0) load_unit(v[i], wave + i * waves);
-    }
-    for (int u = wave; u < units; u += DEPTH * waves) {
+            if (wave + i * waves < units) load_unit(v[i], wave + i * waves);
+        int u = wave;
+        for (; u + (2 * DEPTH - 1) * waves < units; u += DEPTH * waves) {
 #pragma unroll
-        for (int i = 0; i < DEPTH; ++i) {
-            const int at = u + i * waves, next = at + DEPTH * waves;
-            if (at < units) {
+            for (int i = 0; i < DEPTH; ++i) {
                 const u32x4 raw[2] = {v[i][0], v[i][1]};
-                if (r8 && next < units && unit_left(next) > 0) load_unit(v[i], next);
-                unit(raw, at);
+                load_unit(v[i], u + (i + DEPTH) * waves);
+                keep_order();
+                unit(aligned, raw, u + i * waves);
             }
         }
+        for (; u < units; u += DEPTH * waves) {
+#pragma unroll
+            for (int i = 0; i < DEPTH; ++i) {
+                const int at = u + i * waves, next = at + DEPTH * waves;
+                if (at < units) {
+                    const u32x4 raw[2] = {v[i][0], v[i][1]};
+                    if (next < units) load_unit(v[i], next);
+                    unit(aligned, raw, at);
+                }
+            }
+        }
+    } else {
+        for (int u = wave; u < units; u += waves) unit(std::false_type{}, v[0], u);
     }
 
     lds_barrier();        // the turning space is the join's from here
