@@ -219,8 +219,10 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;
         // Four token tiles read the codes once for 64 tokens; hidden values of more
         // than 256 ranks of so many do not fit the shared memory.  Two row tiles
-        // halve the reads of activations, one leaves more workgroups.
-        const int ct = p.M <= 16 ? 1 : p.M <= 32 || p.Rp > 256 ? 2 : 4, rt = N >= 8192 ? 2 : 1;
+        // halve the reads of activations, one leaves more workgroups; rows that are not
+        // cut into parts, short ones, have a wave per row tile.
+        const bool whole = p.log_parts == 0;
+        const int ct = whole || p.M <= 16 ? 1 : p.M <= 32 || p.Rp > 256 ? 2 : 4, rt = N >= 8192 && !whole ? 2 : 1;
         const int bad = bits == 4 ? (group_size == 64 ? lora_launch_b4_g64(p, rt, ct, xf32, sbf, st)
                                                       : lora_launch_b4_g128(p, rt, ct, xf32, sbf, st))
                                   : (group_size == 64 ? lora_launch_b2_g64(p, rt, ct, xf32, sbf, st)

@@ -145,43 +145,44 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
     keep_order();
     T::begin(ring, r, a0, a1);
 
-    // The adapters' terms: a unit is an adapter and a row tile, the waves taking
-    // them in turn.  An adapter's product is computed on whole tiles of 16 tokens and
-    // kept for its own tokens alone, so every token's term has one writer and one
-    // order.  Lane l holds entry l of the list.
+    // The adapters' terms.  A wave has one row tile, and takes every so many of the
+    // block's adapters in turn.  An adapter's product is computed on whole tiles of 16
+    // tokens and kept for its own tokens alone (other rows may hold anything), in
+    // registers until the last, so every token's term has one writer and one order.
+    // Lane l holds entry l of the list.
     const AdapterList& list = p.lists[m0 / kBlock];
-    const int list_adapter = list.adapter[lane], list_count = list.count;
+    const int list_adapter = list.adapter[lane];
     const float list_scaling = list.scaling[lane];
     const unsigned long long list_tokens = list.tokens[lane] >> (m0 % kBlock), adapted = list.any >> (m0 % kBlock);
-    const int units = uniform(list_count) * tiles, shift = __builtin_ctz(tiles);
+    const int entries = uniform(list.count), shift = __builtin_ctz(tiles), tile = wave & (tiles - 1), every = waves >> shift;
     const bool r8 = p.R % 8 == 0;
     u32x4 v[DEPTH][2];
     // A unit's factors up to rank 64 lie together: the lanes load them in order
     // and turn them over through LDS, a row's pieces at an odd stride of 16 bytes.
     const int pieces = min(p.R / 8, 8), stride = pieces | 1;
-    int at_row[2], at_piece[2];
+    const int tile_row = min(first + tile * 16, p.N - 1), tile_last = min(16, p.N - tile_row) - 1;   // past the last row: not stored
+    const uint16_t* const tile_rows = p.lb + (size_t)tile_row * p.R;
+    const size_t per_adapter = (size_t)p.N * p.R;
+    int at_row[2];
+    uint32_t from[2];
 #pragma unroll
     for (int s = 0; s < 2; ++s) {
         at_row[s] = small_div(lane + 64 * s, 1.0f / (float)max(pieces, 1));
-        at_piece[s] = lane + 64 * s - at_row[s] * pieces;
+        const int piece = lane + 64 * s - at_row[s] * pieces;
+        from[s] = (uint32_t)(min(at_row[s], tile_last) * p.R + piece * 8);
+        at_row[s] = at_row[s] < 16 ? (at_row[s] * stride + piece) * 16 : -1;
     }
-    // a tile past the last row has no outputs: its loads repeat that row
-    auto unit_rows = [&](int u) {
-        const int a = __builtin_amdgcn_readlane(list_adapter, u >> shift);
-        return p.lb + ((size_t)a * p.N + min(first + (u & (tiles - 1)) * 16, p.N - 1)) * p.R;
-    };
-    auto unit_left = [&](int u) { return min(16, p.N - (first + (u & (tiles - 1)) * 16)); };
-    auto load_unit = [&](u32x4 (&to)[2], int u) {
-        const uint16_t* rows = unit_rows(u);
-        const int last = max(unit_left(u), 1) - 1;
+    auto entry_rows = [&](int d) { return tile_rows + __builtin_amdgcn_readlane(list_adapter, d) * per_adapter; };
+    auto load_unit = [&](u32x4 (&to)[2], int d) {
+        const uint16_t* rows = entry_rows(d);
 #pragma unroll
-        for (int s = 0; s < 2; ++s)
-            to[s] = *reinterpret_cast<const u32x4*>(rows + (size_t)min(at_row[s], last) * p.R + at_piece[s] * 8);
+        for (int s = 0; s < 2; ++s) to[s] = *reinterpret_cast<const u32x4*>(rows + from[s]);
     };
     char* const turn = lds + sp.factors + wave * kFactorTurn;
-    if (r8 && wave < units) load_unit(v[0], wave);
+    const int d0 = wave >> shift;
+    if (r8 && d0 < entries) load_unit(v[0], d0);
     if (meta.windows == 1) copy.put(scales, biases);
-    if (units > 0) {
+    if (entries > 0) {
         const int octs = p.Rp / 8;
         const float per_oct = 1.0f / (float)octs;
         for (int e = threadIdx.x; e < tokens * octs; e += kWave * waves) {
@@ -232,32 +233,34 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         if (a0 < a1) T::begin(ring, r, a0, a1);
     }
 
-    auto unit = [&](auto aligned, const u32x4 (&raw)[2], int u) {
+    f32x4 term[CT];
+#pragma unroll
+    for (int j = 0; j < CT; ++j) term[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto unit = [&](auto aligned, const u32x4 (&raw)[2], int d) {
         constexpr bool R8 = decltype(aligned)::value;
-        const int tile = u & (tiles - 1), left = unit_left(u), entry = u >> shift;
-        if (left <= 0) return;
-        const unsigned long long mine =
-            (uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)list_tokens, entry) |
-            (unsigned long long)(uint32_t)__builtin_amdgcn_readlane((int)(list_tokens >> 32), entry) << 32;
-        const float scale = bits_f32(__builtin_amdgcn_readlane(f32_bits(list_scaling), entry));
-        const uint16_t* const row = unit_rows(u) + (size_t)min(c, left - 1) * p.R;
+        const uint32_t mine[2] = {(uint32_t)__builtin_amdgcn_readlane((int)(uint32_t)list_tokens, d),
+                                  (uint32_t)__builtin_amdgcn_readlane((int)(list_tokens >> 32), d)};
+        const float scale = bits_f32(__builtin_amdgcn_readlane(f32_bits(list_scaling), d));
+        const uint16_t* const row = entry_rows(d) + (size_t)min(c, tile_last) * p.R;
         u32x4 b[2];
         if constexpr (R8) {
 #pragma unroll
             for (int s = 0; s < 2; ++s)
-                if (at_row[s] < 16) *reinterpret_cast<u32x4*>(turn + (at_row[s] * stride + at_piece[s]) * 16) = raw[s];
+                if (at_row[s] >= 0) *reinterpret_cast<u32x4*>(turn + at_row[s]) = raw[s];
             __builtin_amdgcn_wave_barrier();
 #pragma unroll
-            for (int s = 0; s < 2; ++s)
-                b[s] = trim8(*reinterpret_cast<const u32x4*>(turn + (c * stride + min(q + 4 * s, pieces - 1)) * 16), 8 * q + 32 * s, p.R);
+            for (int s = 0; s < 2; ++s) b[s] = *reinterpret_cast<const u32x4*>(turn + (c * stride + min(q + 4 * s, pieces - 1)) * 16);
             __builtin_amdgcn_wave_barrier();
+            if (p.R < 64)
+#pragma unroll
+                for (int s = 0; s < 2; ++s) b[s] = trim8(b[s], 8 * q + 32 * s, p.R);
         } else {
 #pragma unroll
             for (int s = 0; s < 2; ++s) b[s] = slow8(row, 8 * q + 32 * s, p.R);
         }
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
-            const uint32_t of_tile = (uint32_t)(mine >> (16 * j)) & 0xffffu;
+            const uint32_t of_tile = (mine[j / 2] >> (16 * (j % 2))) & 0xffffu;
             if (of_tile == 0) continue;
             const char* hr = hidden + (16 * j + c) * hrow + 16 * q;
             f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -275,9 +278,9 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
             if (p.Rp > 32) step(b[1], 32);
             for (int k = 64; k < p.Rp; k += 32)
                 step(R8 ? trim8(raw8(row, 8 * q + k, p.R), 8 * q + k, p.R) : slow8(row, 8 * q + k, p.R), k);
+            const uint32_t of_lane = of_tile >> (4 * q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if ((of_tile >> (4 * q + e)) & 1) delta[(tile * 16 * CT + 16 * j + 4 * q + e) * 16 + c] = scale * acc[e];
+            for (int e = 0; e < 4; ++e) term[j][e] = (of_lane >> e) & 1 ? scale * acc[e] : term[j][e];
         }
     };
     // Of the loop's loads none is behind a branch (a wait would then assume it was not
@@ -286,30 +289,47 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         constexpr std::true_type aligned{};
 #pragma unroll
         for (int i = 1; i < DEPTH; ++i)
-            if (wave + i * waves < units) load_unit(v[i], wave + i * waves);
-        int u = wave;
-        for (; u + (2 * DEPTH - 1) * waves < units; u += DEPTH * waves) {
+            if (d0 + i * every < entries) load_unit(v[i], d0 + i * every);
+        int d = d0;
+        for (; d + (2 * DEPTH - 1) * every < entries; d += DEPTH * every) {
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
                 const u32x4 raw[2] = {v[i][0], v[i][1]};
-                load_unit(v[i], u + (i + DEPTH) * waves);
+                load_unit(v[i], d + (i + DEPTH) * every);
                 keep_order();
-                unit(aligned, raw, u + i * waves);
+                unit(aligned, raw, d + i * every);
             }
         }
-        for (; u < units; u += DEPTH * waves) {
+        for (; d < entries; d += DEPTH * every) {
 #pragma unroll
             for (int i = 0; i < DEPTH; ++i) {
-                const int at = u + i * waves, next = at + DEPTH * waves;
-                if (at < units) {
+                const int at = d + i * every, next = at + DEPTH * every;
+                if (at < entries) {
                     const u32x4 raw[2] = {v[i][0], v[i][1]};
-                    if (next < units) load_unit(v[i], next);
+                    if (next < entries) load_unit(v[i], next);
                     unit(aligned, raw, at);
                 }
             }
         }
     } else {
-        for (int u = wave; u < units; u += waves) unit(std::false_type{}, v[0], u);
+        for (int d = d0; d < entries; d += every) unit(std::false_type{}, v[0], d);
+    }
+    // tokens of this wave's adapters
+    if (d0 < entries) {
+        const unsigned long long of_wave = lane < entries && (lane & (every - 1)) == d0 ? list_tokens : 0;
+        uint32_t lo = (uint32_t)of_wave, hi = (uint32_t)(of_wave >> 32);
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1) {
+            lo |= __shfl_xor((int)lo, o);
+            hi |= __shfl_xor((int)hi, o);
+        }
+#pragma unroll
+        for (int j = 0; j < CT; ++j) {
+            const uint32_t of_lane = ((j < 2 ? lo : hi) >> (16 * (j % 2))) >> (4 * q);
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                if ((of_lane >> e) & 1) delta[(tile * 16 * CT + 16 * j + 4 * q + e) * 16 + c] = term[j][e];
+        }
     }
 
     lds_barrier();        // the turning space is the join's from here
