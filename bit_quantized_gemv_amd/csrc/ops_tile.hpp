@@ -428,24 +428,40 @@ struct Tile {
                     for (int f = 0; f < FPW; ++f) wo[i][c * FPW + f] = w_operand(w[i][g * WPG + c], f);
 #pragma unroll
             for (int j = 0; j < CT; ++j) {
-                f32x4 c0 = {0.f, 0.f, 0.f, 0.f};
+                // The first plane and those below it add up apart: a sum passes through
+                // 16 times its terms, and would be rounded there once more per plane.
+                f32x4 c0 = {0.f, 0.f, 0.f, 0.f}, c1 = c0;
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
 #pragma unroll
-                    for (int p = 0; p < NP; ++p) c0 = mfma(t.x[u][j][g][f][p], neg, c0);
-                f32x4 d[RT];
+                    for (int p = 0; p < NP; ++p) {
+                        f32x4& to = p == 0 ? c0 : c1;
+                        to = mfma(t.x[u][j][g][f][p], neg, to);
+                    }
+                f32x4 d[RT], d1[RT];
 #pragma unroll
-                for (int i = 0; i < RT; ++i) d[i] = c0;
+                for (int i = 0; i < RT; ++i) {
+                    d[i] = c0;
+                    d1[i] = c1;
+                }
 #pragma unroll
                 for (int f = 0; f < NF; ++f)
 #pragma unroll
                     for (int p = 0; p < NP; ++p)
 #pragma unroll
-                        for (int i = 0; i < RT; ++i) d[i] = mfma(t.x[u][j][g][f][p], wo[i][f], d[i]);
+                        for (int i = 0; i < RT; ++i) {
+                            f32x4& to = p == 0 ? d[i] : d1[i];
+                            to = mfma(t.x[u][j][g][f][p], wo[i][f], to);
+                        }
                 if constexpr (MORE) {
                     keep_order();
                     load_x(t, u, j, g, r, next);
                     keep_order();
+                }
+                if constexpr (NP > 1) {
+                    c0 += c1;
+#pragma unroll
+                    for (int i = 0; i < RT; ++i) d[i] += d1[i];
                 }
 #pragma unroll
                 for (int i = 0; i < RT; ++i) {
