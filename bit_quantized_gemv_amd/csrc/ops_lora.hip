@@ -217,12 +217,12 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         p.yf32 = y_dt == QMV_DT_F32;
         p.adf16 = ad_dt == QMV_DT_F16;
         if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;
-        // Four token tiles read the codes once for 64 tokens; hidden values of more
-        // than 256 ranks of so many do not fit the shared memory.  Two row tiles
-        // halve the reads of activations, one leaves more workgroups; rows that are not
-        // cut into parts, short ones, have a wave per row tile.
+        // Four token tiles read the codes once for 64 tokens; the hidden values of so
+        // many have to fit the shared memory (52 KB of them beside 100 of the rest at
+        // most).  Two row tiles halve the reads of activations, one leaves more
+        // workgroups; rows that are not cut into parts, short ones, have a wave per row tile.
         const bool whole = p.log_parts == 0;
-        const int ct = whole || p.M <= 16 ? 1 : p.M <= 32 || p.Rp > 256 ? 2 : 4, rt = N >= 8192 && !whole ? 2 : 1;
+        const int ct = whole || p.M <= 16 || p.Rp > 256 ? 1 : p.M <= 32 || p.Rp > 128 ? 2 : 4, rt = N >= 8192 && !whole ? 2 : 1;
         const int bad = bits == 4 ? (group_size == 64 ? lora_launch_b4_g64(p, rt, ct, xf32, sbf, st)
                                                       : lora_launch_b4_g128(p, rt, ct, xf32, sbf, st))
                                   : (group_size == 64 ? lora_launch_b2_g64(p, rt, ct, xf32, sbf, st)

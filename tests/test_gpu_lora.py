@@ -62,6 +62,32 @@ def test_ranks(R, ad):
     check_rows(call(p), want(p), f"rank {R}", "f32")
 
 
+@pytest.mark.parametrize("M,N,K,R", [(70, 100, 5120, 512), (64, 8200, 1024, 200), (64, 70, 16384, 96), (20, 9000, 640, 300)])
+def test_many_ranks_of_many_tokens(M, N, K, R):
+    """Hidden values that fill the shared memory."""
+    p = problem(M, N, K, 4, 64, R=R, L=5)
+    check_rows(call(p), want(p), f"rank {R}", "f32")
+
+
+@pytest.mark.parametrize("bits,gs,M,N,K", [(4, 64, 3, 40, 65536), (2, 64, 20, 33, 65536 + 64), (4, 128, 2, 20, 131072),
+                                           (2, 128, 1, 8200, 98304), (4, 64, 40, 8192, 32768)])
+def test_long_rows(bits, gs, M, N, K):
+    """Rows whose scales go to the shared memory in windows."""
+    if N > 1000:
+        p = problem(M, 64, K, bits, gs, R=8)
+        reps = N // 64 + 1            # the same rows over and over: only the first 64 are compared in 64 bits
+        for n in ("w", "s", "b"):
+            p[n] = p[n].repeat(reps, 1)[:N].contiguous()
+        p["lb"] = p["lb"].repeat(1, reps, 1)[:, :N].contiguous()
+        y = call(p)
+        first = {**p, "w": p["w"][:64], "s": p["s"][:64], "b": p["b"][:64], "lb": p["lb"][:, :64]}
+        check_rows(y[:, :64], want(first), "first rows", "f32")
+        assert torch.equal(y, y[:, :64].repeat(1, reps)[:, :N])
+    else:
+        p = problem(M, N, K, bits, gs, R=8)
+        check_rows(call(p), want(p), "windows", "f32")
+
+
 @pytest.mark.parametrize("ids", [[-1] * 20, [0] * 20, list(range(20)), [7, -1, 99, 3, -5] * 4])
 def test_ids(ids):
     """No adapter, one for all, one each, and ids outside the range."""

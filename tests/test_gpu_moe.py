@@ -140,6 +140,32 @@ def test_odd_groups(D, F):
         check_rows(call_experts(p, weights, ids), want_experts(p, weights, ids), f"{bits}-bit", "f32")
 
 
+@pytest.mark.parametrize("bits,gs,T,D,F", [(4, 64, 2, 65536, 64), (2, 128, 20, 64 * 1024, 128), (4, 64, 3, 64, 40000 // 64 * 64), (2, 64, 40, 128, 81920)])
+def test_long_rows(bits, gs, T, D, F):
+    """Rows whose scales go to the shared memory in windows, by pairs and sorted."""
+    p = problem(T, 2, 2, D, F, bits, gs)
+    ids, weights = some_ids(T, 2, 2)
+    check_rows(call_experts(p, weights, ids), want_experts(p, weights, ids), "windows", "f32")
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 16, 2), (65, 16, 2), (16, 16, 8), (128, 3, 1), (256, 8, 2), (300, 2, 1)])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_sorted_pairs(T, E, k, x):
+    """Both sides of the rule by which pairs are sorted; experts that nothing chooses; empty slots among them."""
+    p = problem(T, E, k, 192, 128, x=x, seed=T)
+    ids, weights = some_ids(T, E, k)
+    ids[ids == E - 1] = 0                       # the last expert meets nothing
+    ids[::5, 0] = -1
+    for dtype in (torch.float32, torch.bfloat16):
+        want = want_experts(p, weights, ids)
+        y = call_experts(p, weights, ids, out_dtype=dtype)
+        keep = (want != 0).any(-1)
+        assert (y[~keep] == 0).all()
+        check_rows(y[keep], want[keep], str(dtype), "f32" if dtype == torch.float32 else "bf16")
+    rows = [0, 1, T // 2, T - 1]
+    assert torch.equal(call_experts(p, weights, ids, rows=rows), call_experts(p, weights, ids)[rows])
+
+
 def test_empty_slots_and_repeats():
     p = problem(5, 4, 3, 128, 128)
     ids = torch.tensor([[-1, -1, -1], [2, -1, 4], [1, 1, 1], [3, 0, -7], [2 ** 31 - 1, 3, 3]], dtype=torch.int32)
