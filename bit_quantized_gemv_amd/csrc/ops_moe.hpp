@@ -27,6 +27,7 @@ struct ExpertParams {
     const int* base;               // sorted pairs: an expert's first tile of 16, its pairs, and each
     const int* count;              // pair's place (a row of xp, h and z); null where pairs keep their order
     int log_parts;                 // of a row's K
+    int groups;                    // of waves in a workgroup
     Meta meta;
     float per_k;                   // 1 / k
     int h_planes;                  // three: exact; two, for bf16 outputs: off by 2^-17, a two hundred and fiftieth of

@@ -8,6 +8,8 @@
 // activations lie in the order of the lanes (FRAG): gathered row by row, each of a
 // wave's activation loads would look up a cache line per lane.
 #pragma once
+#include <algorithm>
+
 #include "ops_moe.hpp"
 #include "ops_tile.hpp"
 
@@ -68,17 +70,17 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     using J = Join<RT>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     together(p.ids, GATE ? p.w13 : p.w2, GATE ? p.s13 : p.s2, GATE ? p.b13 : p.b2, GATE ? p.xp : p.h, GATE ? p.x_plane : p.h_plane,
-             p.P, p.D, p.F, p.E, p.slots, p.log_parts, p.meta.groups, p.meta.window, p.meta.windows, p.per_k);
+             p.P, p.D, p.F, p.E, p.slots, p.log_parts, p.groups, p.meta.groups, p.meta.window, p.meta.windows, p.per_k);
     const int slot = blockIdx.y;
     const bool by_pair = p.slots == p.P;
     const int e = by_pair ? p.ids[slot] : slot;
     if (e < 0 || e >= p.E) return;
     const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6);
-    const int c = lane & 15, lp = p.log_parts, parts = 1 << lp, waves = waves_of(parts), groups = waves >> lp, threads = kWave * waves;
+    const int c = lane & 15, lp = p.log_parts, parts = 1 << lp, groups = p.groups, waves = groups << lp, threads = kWave * waves;
     const int group = wave >> lp, part = wave & (parts - 1);
-    const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;            // N is a multiple of 64
+    const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;
     constexpr int ROWS = GATE ? 16 : 32;                             // outputs of a group
-    const int first = blockIdx.x * ROWS * groups, left = min(ROWS * groups, N - first), n0 = first + group * ROWS;
+    const int left = ROWS * groups, first = blockIdx.x * left;       // N is a multiple of the workgroup's rows
     const Meta& meta = p.meta;
     const ExpertSpace sp(meta, waves, 32 * groups, p.P);
     uint16_t* const scales = reinterpret_cast<uint16_t*>(lds);
@@ -106,19 +108,18 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     r.turn = lds + sp.turn + wave * T::TURN;
     r.even = meta.groups % T::NG == 0;
     const size_t row0 = (size_t)e * (GATE ? 2 * N : N);
-    const bool active = n0 < N;
 #pragma unroll
     for (int i = 0; i < RT; ++i) {
-        const int local = GATE ? i * 16 * groups + group * 16 : group * 32 + 16 * i;
-        T::set_codes(r, i, GATE ? p.w13 : p.w2, row0 + (GATE ? (size_t)i * N + min(n0, N - 16) : min(n0 + 16 * i, N - 16)), 16);
-        r.s[i] = scales + (local + c) * meta.groups;
-        r.b[i] = biases + (local + c) * meta.groups;
+        T::set_codes(r, i, GATE ? p.w13 : p.w2, row0 + first + group * ROWS + (GATE ? (size_t)i * N : 16 * i), 16);
+        const int at = (GATE ? i * left + group * 16 : group * 32 + 16 * i) + c;
+        r.s[i] = scales + at * meta.groups;
+        r.b[i] = biases + at * meta.groups;
     }
     const uint16_t* const ms = (GATE ? p.s13 : p.s2) + (row0 + first) * r.G;
     const uint16_t* const mb = (GATE ? p.b13 : p.b2) + (row0 + first) * r.G;
     const size_t up = (size_t)N * r.G;
     const int slabs = slabs_of(r.chunks), s0 = part_start(slabs, lp, part), s1 = part_start(slabs, lp, part + 1);
-    MetaCopy<GATE ? 2 : 4> copy(ms, mb, left, r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left, r.G, threads);
+    MetaCopy<GATE ? 1 : 4> copy(ms, mb, left, r.G, threads), copy_up(ms + (GATE ? up : 0), mb + (GATE ? up : 0), left, r.G, threads);
     const int half = 16 * groups * meta.groups;       // the up rows' place
     auto stage = [&](int k) {
         stage_window(scales, ms, left, r.G, T::NG, slabs, parts, meta.window, k, threads);
@@ -167,7 +168,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                 if (GATE) copy_up.put(scales + half, biases + half);
                 lds_barrier();
             }
-            if (active) T::run(acc, ring, r, a0, a1);
+            T::run(acc, ring, r, a0, a1);
         }
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
@@ -181,7 +182,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                 constexpr int H = T::VPW / 2;
                 for (int i = threadIdx.x; i < 128 * groups; i += threads) {
                     const int et = i & 15, d = (i >> 4) & 7, g = i >> 7;
-                    if (t0 + 16 * j + et < n && g * 16 < left) {
+                    if (t0 + 16 * j + et < n) {
                         const int word = d / H, ii = d % H, en = word * T::VPW + ii;
                         float v[2];
 #pragma unroll
@@ -205,7 +206,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
             } else {
                 for (int i = threadIdx.x; i < 16 * 32 * groups; i += threads) {
                     const int en = i & 31, g = (i >> 5) & (groups - 1), et = small_div(i >> 5, 1.0f / (float)groups);
-                    if (t0 + 16 * j + et < n && g * 32 + en < left)
+                    if (t0 + 16 * j + et < n)
                         p.z[(size_t)row_of(t0 + 16 * j + et) * N + first + g * 32 + en] = J::sum(join, g * parts, parts, J::at(en, et));
                 }
             }
@@ -227,21 +228,27 @@ int expert_start(const ExpertParams& p, hipStream_t st)
 {
     const int K = GATE ? p.D : p.F, N = GATE ? p.F : p.D;
     ExpertParams q = p;
-    const int parts = expert_parts(K / (4 * T::VPW)), waves = waves_of(parts), groups = waves / parts, rows = (GATE ? 16 : 32) * groups;
+    constexpr int ROWS = GATE ? 16 : 32;
+    const int parts = expert_parts(K / (4 * T::VPW));
     q.log_parts = __builtin_ctz(parts);
-    q.meta = Meta(32 * groups, K, T::BITS, T::GS, parts);
-    const ExpertSpace sp(q.meta, waves, 32 * groups, p.P);
+    q.groups = std::max(1, 4 / parts);
+    while (N / ROWS % q.groups != 0) q.groups /= 2;
+    q.meta = Meta(32 * q.groups, K, T::BITS, T::GS, parts);
+    const ExpertSpace sp(q.meta, q.groups * parts, 32 * q.groups, p.P);
     const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
     if (sp.bytes > 64 * 1024 &&
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, sp.bytes) != hipSuccess)
         return 1;
     void* args[] = {&q};
-    return hipLaunchKernel(fn, dim3((N + rows - 1) / rows, p.slots), dim3(kWave * waves), args, sp.bytes, st) == hipSuccess ? 0 : 1;
+    const dim3 grid(N / (ROWS * q.groups), p.slots);
+    return hipLaunchKernel(fn, grid, dim3(kWave * q.groups * parts), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }
 
 template <int BITS, int GS, bool SBF, bool SORTED>
-int expert_down(const ExpertParams& p, hipStream_t st)
+int expert_down(const ExpertParams& p, int ct, hipStream_t st)
 {
+    if constexpr (SORTED && BITS == 4)          // (2-bit codes: 250 spills, 182 us against 68)
+        if (ct == 2 && p.h_planes == 2) return expert_start<Tile<BITS, GS, 2, 2, 2, SBF, true>, false>(p, st);
     return p.h_planes == 3 ? expert_start<Tile<BITS, GS, 2, 1, 3, SBF, SORTED>, false>(p, st)
                            : expert_start<Tile<BITS, GS, 2, 1, 2, SBF, SORTED>, false>(p, st);
 }
@@ -250,12 +257,12 @@ template <int BITS, int GS, bool SBF>
 int expert_pick(int which, const ExpertParams& p, int ct, bool xf32, hipStream_t st)
 {
     if (p.base) {
-        if (which == 1) return expert_down<BITS, GS, SBF, true>(p, st);
+        if (which == 1) return expert_down<BITS, GS, SBF, true>(p, ct, st);
         if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, true>(p, st);
         return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, 1, SBF, true>, true>(p, st)
                        : expert_start<Tile<BITS, GS, 2, 2, 1, SBF, true>, true>(p, st);
     }
-    if (which == 1) return expert_down<BITS, GS, SBF, false>(p, st);
+    if (which == 1) return expert_down<BITS, GS, SBF, false>(p, ct, st);
     if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, true>(p, st);
     return expert_start<Tile<BITS, GS, 2, 1, 1, SBF, false>, true>(p, st);
 }

@@ -419,6 +419,7 @@ struct Tile {
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
             if (TAIL && g > 0 && slab * NG + g >= r.G) break;      // past the row's end, in its last slab
+            if constexpr (BITS == 2) __builtin_amdgcn_sched_barrier(0);      // groups drawn together spill
             u32x4 wo[RT][NF];
 #pragma unroll
             for (int i = 0; i < RT; ++i)
