@@ -27,9 +27,9 @@
 // wave turns the pieces over through LDS (a write and a read of 16 bytes a lane,
 // one slab ahead; which piece a lane loads is swizzled so that the reads meet
 // distinct banks).  Without this, and with scales loaded by each lane for itself, a
-// 17408 x 5120 product of 16 tokens took 51 us instead of TURNED us.  Codes are asked
-// for by two slabs, the two halves of a cache line: one at a time, half of the lines
-// were read from memory twice (128 experts, 13 tokens: 249 MB for 168).
+// 17408 x 5120 product of 16 tokens took 51 us; with both, 29.  Codes are asked for by
+// two slabs, the two halves of a cache line: one at a time, half of the lines were
+// read from memory twice (128 experts, 13 tokens: 249 MB for 168; by two, 157).
 //
 // Scales and biases go to LDS before the product, whole rows at a time: a row's
 // few bytes per slab would cost as many lookups as its codes.
@@ -40,12 +40,17 @@
 // loaded; 16 tokens together (FRAG), or each by itself where they are gathered.
 //
 // The pipeline.  A wave keeps PF slabs of codes and activations in flight in
-// registers.  Loads come back in order, so the activations, though near,
-// are asked for as early as the codes: an activation load waited for would
-// otherwise wait for every code load before it.  The loop body has no branch
-// around a load, which would make each wait assume the shorter path, and the loads
-// keep their order (slab by slab, before the loop as in it): a wait counts the
-// loads after the one it needs, and takes the smaller count of the two ways in.
+// registers.  Loads come back in order, so the activations, though near, are asked
+// for as early as the codes: an activation load waited for would otherwise wait for
+// every code load before it.  The loop body has no branch around a load, which would
+// make each wait assume the shorter path, and the loads keep their order (slab by slab,
+// before the loop as in it): a wait counts the loads after the one it needs, and takes
+// the smaller count of the two ways in.
+//
+// What bounds it: with one token, the read of the codes and the start and end of a
+// workgroup (15360 x 3840 in 14.5 us, of which the codes and scales are 6.8 at the
+// rate of a large copy); from about 32 tokens the vector instructions of decoding and
+// folding beside the matrix instructions.
 #pragma once
 #include <hip/hip_runtime.h>
 

@@ -231,6 +231,15 @@ def test_many_rows(logits):
     check(l, draft, u, None, temp=temp, lens=lens)
 
 
+@pytest.mark.parametrize("V", [524289, 1200001])
+@pytest.mark.parametrize("logits,probs", [("bf16", "f32"), ("f32", "bf16"), ("f32", None)])
+def test_large_vocabularies(logits, probs, V):
+    """More chunks than a workgroup has threads."""
+    for seed in range(3):
+        l, draft, u, pr = problem(2, 1, V, logits, probs, seed=seed)
+        check(l, draft, u, pr, temp=torch.tensor([1.0, 0.6]))
+
+
 @pytest.mark.parametrize("V", [500, 5000])
 def test_drafter_that_agrees(V):
     """Where the drafter's probabilities are the target's, rounded to fp32, what is left of them is their rounding."""
