@@ -218,7 +218,7 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         p.adf16 = ad_dt == QMV_DT_F16;
         if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;
         // Four token tiles read the codes once for 64 tokens; the hidden values of so
-        // many have to fit the shared memory (52 KB of them beside 100 of the rest at
+        // many have to fit the shared memory (52 KB of them beside 90 of the rest at
         // most).  Two row tiles halve the reads of activations, one leaves more
         // workgroups; rows that are not cut into parts, short ones, have a wave per row tile.
         const bool whole = p.log_parts == 0;

@@ -64,21 +64,22 @@ __device__ __forceinline__ void split_f32(const f32x4& lo, const f32x4& hi, u32x
 
 constexpr int kFactorTurn = 16 * 9 * 16;       // bytes of LDS per wave to turn a unit's factors over
 
-// LDS of the kernel, in bytes: the scales and biases; the slabs being turned over
-// and, in their place when the product is done, the waves' partial results; the
-// factors being turned over; the adapters' terms of the workgroup's row tiles; and
-// the hidden values in three bf16 planes.
+// LDS of the kernel, in bytes: the scales and biases; the slabs being turned over,
+// the factors being turned over and the hidden values in three bf16 planes, and in
+// the place of all three, when they are done with, the waves' partial results; the
+// adapters' terms of the workgroup's row tiles.
 struct LoraSpace {
-    int biases, turn, factors, delta, hidden, bytes;
+    int biases, turn, factors, hidden, delta, bytes;
     __host__ __device__ LoraSpace(const Meta& meta, int waves, int groups, int rt, int ct, int Rp)
     {
         const int tiles = groups * rt, tokens = 16 * ct;
         biases = meta.bytes(16 * tiles) / 2;
         turn = 2 * biases;
-        factors = turn + waves * rt * Join<1>::kWords * 4;
-        delta = factors + waves * kFactorTurn;
-        hidden = delta + tiles * tokens * 64;
-        bytes = hidden + 3 * tokens * (Rp + 8) * 2;
+        factors = turn + waves * rt * 1024;
+        hidden = factors + waves * kFactorTurn;
+        const int join = turn + ct * waves * rt * Join<1>::kWords * 4, end = hidden + 3 * tokens * (Rp + 8) * 2;
+        delta = join > end ? join : end;
+        bytes = delta + tiles * tokens * 64;
     }
 };
 
@@ -190,15 +191,15 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
             const char* hp = reinterpret_cast<const char*>(p.h + (size_t)(m0 + t) * p.Rp + k);
             const size_t piece = (size_t)p.M * p.Rp * 4;
             f32x4 lo = {0.f, 0.f, 0.f, 0.f}, hi = lo;
-            for (int z0 = 0; z0 < p.pieces; z0 += 8) {
-                f32x4 x[8][2];
+            for (int z0 = 0; z0 < p.pieces; z0 += 4) {
+                f32x4 x[4][2];
 #pragma unroll
-                for (int z = 0; z < 8; ++z)
+                for (int z = 0; z < 4; ++z)
 #pragma unroll
                     for (int i = 0; i < 2; ++i)
                         x[z][i] = reinterpret_cast<const f32x4*>(hp + min(z0 + z, p.pieces - 1) * piece)[i];
 #pragma unroll
-                for (int z = 0; z < 8; ++z)
+                for (int z = 0; z < 4; ++z)
                     if (z0 + z < p.pieces)
 #pragma unroll
                         for (int d = 0; d < 4; ++d) {
@@ -332,24 +333,21 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void lora_kernel(LoraPa
         }
     }
 
-    lds_barrier();        // the turning space is the join's from here
+    lds_barrier();        // from here the join has the place of what came before
 #pragma unroll
-    for (int j = 0; j < CT; ++j) {
-        const int mj = 16 * j;
-        if (mj >= tokens) break;
+    for (int j = 0; j < CT; ++j)
 #pragma unroll
-        for (int i = 0; i < RT; ++i) J::write(join, wave, lane, i, acc[i][j]);
-        lds_barrier();
-        for (int e = threadIdx.x; e < 256 * tiles; e += kWave * waves) {
-            const int en = e & (16 * tiles - 1), t = mj + (e >> (4 + shift)), n = first + en;
-            if (n < p.N && t < tokens) {
-                const int group = en / (16 * RT);
-                float y = J::sum(join, group * parts, parts, J::at(en % (16 * RT), t & 15));
-                if ((adapted >> t) & 1) y += delta[((en >> 4) * 16 * CT + t) * 16 + (en & 15)];
-                store_y(p.y, (size_t)(m0 + t) * p.N + n, y, p.yf32);
-            }
+        for (int i = 0; i < RT; ++i) J::write(join + j * waves * J::kWords, wave, lane, i, acc[i][j]);
+    lds_barrier();
+    const int log_rows = 4 + shift;
+    for (int e = threadIdx.x; e < tokens << log_rows; e += kWave * waves) {
+        const int en = e & (16 * tiles - 1), t = e >> log_rows, n = first + en;
+        if (n < p.N) {
+            const int group = en / (16 * RT);
+            float y = J::sum(join + (t >> 4) * waves * J::kWords, group * parts, parts, J::at(en % (16 * RT), t & 15));
+            if ((adapted >> t) & 1) y += delta[((en >> 4) * 16 * CT + t) * 16 + (en & 15)];
+            store_y(p.y, (size_t)(m0 + t) * p.N + n, y, p.yf32);
         }
-        if (j + 1 < CT) lds_barrier();
     }
 }
 
