@@ -1,6 +1,7 @@
 // ops_moe.hip -- qmv_route, qmv_experts and qmv_moe: checks, the router's
 // kernels, the weighted sum of the experts' outputs, and the launches.
 #include "ops_moe.hpp"
+#include "ops_moe_kernel.hpp"
 
 #include <algorithm>
 
@@ -451,7 +452,11 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
     p.log_parts = 0;
     p.per_k = 1.0f / (float)k;
     p.h_planes = yf32 ? 3 : 2;
+    p.weights = weights;
+    p.y = y;
+    p.yf32 = yf32;
     const int ct = p.P <= 12 * E ? 1 : 2;
+    if (!by_expert && by_token(n, k, D, F, bits)) return go(0, p, ct, xf32, sbf, st) || go(2, p, ct, xf32, sbf, st) ? QMV_E_LAUNCH : QMV_OK;
     if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;
     const float* z = p.z;
     const int* place = by_expert ? p.count + E : nullptr;

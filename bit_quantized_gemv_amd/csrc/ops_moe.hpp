@@ -30,11 +30,15 @@ struct ExpertParams {
     int groups;                    // of waves in a workgroup
     Meta meta;
     float per_k;                   // 1 / k
+    const float* weights;          // [P]
+    void* y;                       // [P / k][D]
+    bool yf32;
     int h_planes;                  // three: exact; two, for bf16 outputs: off by 2^-17, a two hundred and fiftieth of
                                    // their rounding, for a third less of the down product's work
 };
 
-// which = 0: gate and up products and the activation (xp -> h); 1: down product (h -> z)
+// which = 0: gate and up products and the activation (xp -> h); 1: down product (h -> z);
+// 2: down products and weighted sums of whole tokens (h -> y)
 int expert_launch_b4_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
 int expert_launch_b4_g128(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
 int expert_launch_b2_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);

@@ -244,6 +244,90 @@ int expert_start(const ExpertParams& p, hipStream_t st)
     return hipLaunchKernel(fn, grid, dim3(kWave * q.groups * parts), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }
 
+// The down products of one token's experts and their weighted sum, a wave per slot
+// and 32 rows per workgroup: neither the experts' outputs are written nor another
+// launch adds them up, but an expert that two tokens chose is read for each.  The sums
+// are those of the two launches, bit for bit.  One token, 6 experts of 3840 x 1024:
+// 11.1 us for 13.3 MB, of which 3 are the launch and its arguments.
+constexpr int kTokenSlots = kMaxWaves;
+
+inline int token_bytes(const Meta& meta, int k) { return k * (2048 + 2 * Join<1>::kWords * 4 + meta.bytes(32)); }
+
+template <class T>
+__global__ __launch_bounds__(kTokenSlots* kWave, T::WAVES) void token_kernel(ExpertParams p)
+{
+    using J = Join<2>;
+    extern __shared__ __attribute__((aligned(16))) char lds[];
+    together(p.ids, p.weights, p.w2, p.s2, p.b2, p.h, p.h_plane, p.y, p.k, p.D, p.F, p.E, p.meta.groups);
+    const int lane = threadIdx.x & 63, wave = uniform(threadIdx.x >> 6), c = lane & 15;
+    const int n0 = blockIdx.x * 32, t = blockIdx.y, pair = t * p.k + wave, K = p.F, N = p.D;
+    float* const join = reinterpret_cast<float*>(lds + p.k * 2048);
+    char* const own = lds + p.k * (2048 + 2 * Join<1>::kWords * 4) + wave * p.meta.bytes(32);
+    uint16_t* const scales = reinterpret_cast<uint16_t*>(own);
+    uint16_t* const biases = reinterpret_cast<uint16_t*>(own + p.meta.bytes(32) / 2);
+    const int e = p.ids[pair];
+    if (e >= 0 && e < p.E) {
+        typename T::Rows r;
+        r.G = K / T::GS;
+        r.chunks = K / (4 * T::VPW);
+        r.plane = p.h_plane;
+        r.turn = lds + wave * 2048;
+        r.even = p.meta.groups % T::NG == 0;
+        const size_t row = (size_t)e * N + n0;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            T::set_codes(r, i, p.w2, row + 16 * i, 16);
+            r.s[i] = scales + (16 * i + c) * p.meta.groups;
+            r.b[i] = biases + (16 * i + c) * p.meta.groups;
+        }
+        MetaCopy<2> copy(p.s2 + row * r.G, p.b2 + row * r.G, 32, r.G, kWave, lane);
+        copy.ask();
+        keep_order();
+        T::set_token(r, 0, p.h, pair);
+        const int slabs = slabs_of(r.chunks);
+        typename T::Ring ring;
+        T::begin(ring, r, 0, slabs);
+        copy.put(scales, biases);
+        __builtin_amdgcn_wave_barrier();
+        f32x4 acc[2][1];
+        T::clear(acc);
+        T::run(acc, ring, r, 0, slabs);
+#pragma unroll
+        for (int i = 0; i < 2; ++i) J::write(join, wave, lane, i, acc[i][0]);
+    }
+    lds_barrier();
+    if (threadIdx.x >= 32) return;
+    float v = 0.0f;
+    for (int j = 0; j < p.k; ++j) {
+        const int id = p.ids[t * p.k + j];
+        if (id >= 0 && id < p.E) v = __builtin_fmaf(p.weights[t * p.k + j], join[j * J::kWords + J::at(lane, 0)], v);
+    }
+    store_y(p.y, (size_t)t * N + n0 + lane, v, p.yf32);
+}
+
+// Whole tokens where their slots fit the waves, a row of w2 is one wave's, and what is
+// read again for experts that tokens share costs less than a launch.  Whole layers, us,
+// by expert and by token: 1 token over 64 experts of 3840 x 1024, 6 each: 35.2, 32.3;
+// 2 tokens: 43.4, 37.0; 8: 89.6, 92.2.  4 experts of 4096 x 2048, 2 each: 4 tokens
+// 38.9, 37.5; 7: 39.8, 41.5.  16 experts of 512 x 512, 4 each, 16 tokens: 23.8, 19.6.
+// 2-bit, 16 experts of 5120 x 768, 8 each: 2 tokens 55.8, 54.3; 6: 61.6, 73.5.
+inline bool by_token(int n, int k, int D, int F, int bits)
+{
+    return k <= kTokenSlots && expert_parts(F * bits / 128) == 1 && (n == 1 || (long long)n * k * D * F <= 1 << 26);
+}
+
+template <class T>
+int token_start(const ExpertParams& p, hipStream_t st)
+{
+    ExpertParams q = p;
+    q.meta = Meta(32, p.F, T::BITS, T::GS, 1);
+    const int bytes = token_bytes(q.meta, p.k);
+    const void* fn = reinterpret_cast<const void*>(&token_kernel<T>);
+    if (bytes > 64 * 1024 && hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, bytes) != hipSuccess) return 1;
+    void* args[] = {&q};
+    return hipLaunchKernel(fn, dim3(p.D / 32, p.P / p.k), dim3(kWave * p.k), args, bytes, st) == hipSuccess ? 0 : 1;
+}
+
 template <int BITS, int GS, bool SBF, bool SORTED>
 int expert_down(const ExpertParams& p, int ct, hipStream_t st)
 {
@@ -256,6 +340,9 @@ int expert_down(const ExpertParams& p, int ct, hipStream_t st)
 template <int BITS, int GS, bool SBF>
 int expert_pick(int which, const ExpertParams& p, int ct, bool xf32, hipStream_t st)
 {
+    if (which == 2)
+        return p.h_planes == 3 ? token_start<Tile<BITS, GS, 2, 1, 3, SBF, false>>(p, st)
+                               : token_start<Tile<BITS, GS, 2, 1, 2, SBF, false>>(p, st);
     if (p.base) {
         if (which == 1) return expert_down<BITS, GS, SBF, true>(p, ct, st);
         if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, true>(p, st);

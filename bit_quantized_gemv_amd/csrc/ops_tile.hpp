@@ -558,9 +558,9 @@ struct MetaCopy {
     const uint16_t *s, *b;
     int count, whole;      // values, and whole pieces, of each
     float per_row;         // where LDS rows are padded: 1 / pieces per row, else 0
-    int threads;           // of the workgroup (blockDim is an argument of its own, and a round trip)
-    __device__ __forceinline__ MetaCopy(const uint16_t* s_, const uint16_t* b_, int rows, int G, int threads_)
-        : s(s_), b(b_), count(rows * G), whole(rows * G / 8), per_row(G % 8 == 0 ? 8.0f / (float)G : 0.0f), threads(threads_)
+    int thread, threads;   // of the workgroup (blockDim is an argument of its own, and a round trip), or of a wave
+    __device__ __forceinline__ MetaCopy(const uint16_t* s_, const uint16_t* b_, int rows, int G, int threads_, int thread_ = threadIdx.x)
+        : s(s_), b(b_), count(rows * G), whole(rows * G / 8), per_row(G % 8 == 0 ? 8.0f / (float)G : 0.0f), thread(thread_), threads(threads_)
     {
     }
     __device__ __forceinline__ u32x4 load(int i) const
@@ -571,7 +571,7 @@ struct MetaCopy {
     {
 #pragma unroll
         for (int k = 0; k < HELD; ++k) {
-            const int i = min((int)(threadIdx.x + k * threads), 2 * whole - 1);
+            const int i = min(thread + k * threads, 2 * whole - 1);
             if (whole > 0) v[k] = load(i);
         }
     }
@@ -582,9 +582,9 @@ struct MetaCopy {
             if (i < 2 * whole) reinterpret_cast<u32x4*>(i < whole ? ts : tb)[at + small_div(at, per_row)] = x;      // (0.5 * 0 is no row)
         };
 #pragma unroll
-        for (int k = 0; k < HELD; ++k) store(threadIdx.x + k * threads, v[k]);
-        for (int i = threadIdx.x + HELD * threads; i < 2 * whole; i += threads) store(i, load(i));
-        int at = whole * 8 + threadIdx.x;
+        for (int k = 0; k < HELD; ++k) store(thread + k * threads, v[k]);
+        for (int i = thread + HELD * threads; i < 2 * whole; i += threads) store(i, load(i));
+        int at = whole * 8 + thread;
         asm volatile("" : "+v"(at));        // these loads stay here, behind those in flight
         if (at < count) {
             ts[at] = s[at];

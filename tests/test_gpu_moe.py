@@ -195,6 +195,24 @@ def test_tokens_do_not_depend_on_the_call(x):
     assert torch.equal(call_experts(p, weights, ids, rows=list(range(59, -1, -1))), whole.flip(0))
 
 
+@pytest.mark.parametrize("bits,E,k,D,F", [(4, 16, 8, 1088, 960), (2, 40, 9, 256, 320), (4, 12, 1, 64, 2944), (2, 9, 8, 128, 5888)])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_whole_tokens_and_pairs_agree(bits, E, k, D, F, dtype):
+    """Few tokens, whose experts' outputs are added up at once; more slots than waves; more tokens, by expert."""
+    T = 9
+    p = problem(T, E, k, D, F, bits, 64, seed=k)
+    ids, weights = some_ids(T, E, k)
+    ids[1] = -1
+    ids[2, 0] = E
+    want = want_experts(p, weights, ids)
+    whole = call_experts(p, weights, ids, out_dtype=dtype)
+    keep = [t for t in range(T) if t != 1 and bool((want[t] != 0).any())]
+    check_rows(whole[keep], want[keep], "tokens", "f32" if dtype == torch.float32 else "bf16")
+    assert (whole[1] == 0).all()
+    for t in (0, 1, 2, 8):
+        assert torch.equal(call_experts(p, weights, ids, out_dtype=dtype, rows=[t])[0], whole[t]), t
+
+
 @pytest.mark.parametrize("T", [1, 2, 13, 40, 257, 520])
 @pytest.mark.parametrize("renorm", [True, False])
 def test_moe(T, renorm):
