@@ -145,28 +145,32 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     }
     const Packed pk(p.F, T::BITS, T::GS, T::FRAG);
     typename T::Ring ring;
-    for (int t0 = 0; t0 < n; t0 += 16 * CT) {
-        lds_barrier();              // the list is there; the partial results before are read
+    auto begin = [&](int t0) {
 #pragma unroll
         for (int j = 0; j < CT; ++j) {
             const int row = row_of(min(t0 + 16 * j + c, n - 1));
             T::set_token(r, j, GATE ? p.xp : p.h, GATE && !T::FRAG ? small_div(row, p.per_k) : row);
         }
+        if (meta.windows == 1) T::begin(ring, r, min(s0, s1 - 1), max(s1, s0 + 1));
+    };
+    if constexpr (!T::FRAG) lds_barrier();      // the list is there
+    begin(0);
+    if (meta.windows == 1) {
+        copy.put(scales, biases);
+        if (GATE) copy_up.put(scales + half, biases + half);
+    }
+    lds_barrier();
+    for (int t0 = 0; t0 < n; t0 += 16 * CT) {
         f32x4 acc[RT][CT];
         T::clear(acc);
         for (int k = 0; k < meta.windows; ++k) {
+            const int a0 = min(s0 + k * meta.window, s1), a1 = min(a0 + meta.window, s1);
             if (meta.windows > 1) {
-                if (k > 0) lds_barrier();
+                lds_barrier();
                 stage(k);
                 lds_barrier();
                 shift((part - k) * meta.window - s0);
-            }
-            const int a0 = min(s0 + k * meta.window, s1), a1 = min(a0 + meta.window, s1);
-            T::begin(ring, r, min(a0, s1 - 1), max(a1, s0 + 1));
-            if (meta.windows == 1 && t0 == 0) {
-                copy.put(scales, biases);
-                if (GATE) copy_up.put(scales + half, biases + half);
-                lds_barrier();
+                T::begin(ring, r, min(a0, s1 - 1), max(a1, s0 + 1));
             }
             T::run(acc, ring, r, a0, a1);
         }
@@ -210,6 +214,10 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                         p.z[(size_t)row_of(t0 + 16 * j + et) * N + first + g * 32 + en] = J::sum(join, g * parts, parts, J::at(en, et));
                 }
             }
+        }
+        if (t0 + 16 * CT < n) {
+            begin(t0 + 16 * CT);
+            lds_barrier();          // the partial results are read
         }
     }
 }
