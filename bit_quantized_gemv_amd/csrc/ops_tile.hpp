@@ -29,7 +29,10 @@
 // distinct banks).  Without this, and with scales loaded by each lane for itself, a
 // 17408 x 5120 product of 16 tokens took 51 us; with both, 29.  Codes are asked for by
 // two slabs, the two halves of a cache line: one at a time, half of the lines were
-// read from memory twice (128 experts, 13 tokens: 249 MB for 168; by two, 157).
+// read from memory twice (128 experts, 13 tokens: 249 MB for 157; by two, 168).  Rows
+// that start inside a line still meet lines twice, so the loads leave them in the
+// caches: as nontemporal ones, 32 experts of 3840 x 1920 in 2 bits read 394 MB for 199
+// and took 154 us, against 143.
 //
 // Scales and biases go to LDS before the product, whole rows at a time: a row's
 // few bytes per slab would cost as many lookups as its codes.
@@ -332,7 +335,7 @@ struct Tile {
         const uint32_t at = 16 * (uint32_t)min(4 * slab + piece(), r.chunks - 1);   // a part slab's pieces past the row repeat its last
 #pragma unroll
         for (int i = 0; i < RT; ++i)
-            t.w[u][i] = __builtin_nontemporal_load(reinterpret_cast<const u32x4*>(r.w[i] + (r.wo[i] + at)));
+            t.w[u][i] = *reinterpret_cast<const u32x4*>(r.w[i] + (r.wo[i] + at));
     }
 
     static __device__ __forceinline__ void load_x(Ring& t, int u, int j, int g, const Rows& r, int slab)
