@@ -88,9 +88,9 @@ struct LoraSpace {
 // first: the first slabs of codes and activations, and by way of the list of
 // adapters the first of their factors and the hidden values, which go to LDS.  The
 // adapters' terms follow the product, their factors streaming through a ring of
-// registers that the product has left.  15360 x 3840, one token, rank 16: 14.6 us,
-// 34 MB at 2.4 TB/s, most of it the start and end of a wave.  17408 x 5120, 64 tokens
-// of 32 adapters, rank 64: 82 us, 140 TFLOP/s, 134 MB, bound by the decoding of codes
+// registers that the product has left.  15360 x 3840, one token, rank 16: 13.8 us,
+// 34 MB at 2.5 TB/s, most of it the start and end of a wave.  17408 x 5120, 64 tokens
+// of 32 adapters, rank 64: 81 us, 140 TFLOP/s, 134 MB, bound by the decoding of codes
 // beside the matrix instructions, the 71 MB of factors, and a second round of 32
 // workgroups behind the 512 that fit.
 template <class T>

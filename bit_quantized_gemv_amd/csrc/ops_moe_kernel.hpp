@@ -10,8 +10,8 @@
 //
 // 13 tokens over 128 experts of 2048 x 1024, 8 each: gate and up 46 us, 168 MB at 3.6
 // TB/s; down 35 us, 84 MB at 2.4, whose rows are eight slabs: a wave is mostly its
-// start and end.  128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit: 71 us, 213
-// TFLOP/s, and 66 us, 115 (two planes of hidden values: twice the matrix
+// start and end.  128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit: 69 us, 219
+// TFLOP/s, and 61 us, 124 (two planes of hidden values: twice the matrix
 // instructions), bound by the decoding of codes beside the matrix instructions.
 #pragma once
 #include <algorithm>
@@ -262,7 +262,7 @@ int expert_start(const ExpertParams& p, hipStream_t st)
 // and 32 rows per workgroup: neither the experts' outputs are written nor another
 // launch adds them up, but an expert that two tokens chose is read for each.  The sums
 // are those of the two launches, bit for bit.  One token, 6 experts of 3840 x 1024:
-// 11.1 us for 13.3 MB, of which 3 are the launch and its arguments.
+// 10.5 us for 13.3 MB, of which 3 are the launch and its arguments.
 constexpr int kTokenSlots = kMaxWaves;
 
 inline int token_bytes(const Meta& meta, int k) { return k * (2048 + 2 * Join<1>::kWords * 4 + meta.bytes(32)); }
