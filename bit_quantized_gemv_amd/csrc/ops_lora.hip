@@ -220,10 +220,13 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;
         // Four token tiles read the codes once for 64 tokens; the hidden values of so
         // many have to fit the shared memory (52 KB of them beside 90 of the rest at
-        // most).  Two row tiles halve the reads of activations, one leaves more
-        // workgroups; rows that are not cut into parts, short ones, have a wave per row tile.
+        // most).  Two row tiles per wave where one each would take more waves than fit at
+        // once, two per SIMD: 4096 x 12288, 13 tokens, 2048 waves: 19.3 us with one, 21.7
+        // with two; 4608 x 12288: 29.6, 22.0; 12288 x 3840, 3072 waves of four to a
+        // workgroup, 18.7, 18.9; 15360 x 3840: 22.5, 19.2.  Rows that are not cut into
+        // parts, short ones, have a wave per row tile.
         const bool whole = p.log_parts == 0;
-        const int ct = whole || p.M <= 16 || p.Rp > 256 ? 1 : p.M <= 32 || p.Rp > 128 ? 2 : 4, rt = N >= 8192 && !whole ? 2 : 1;
+        const int ct = whole || p.M <= 16 || p.Rp > 256 ? 1 : p.M <= 32 || p.Rp > 128 ? 2 : 4, rt = ((N + 15) / 16 << p.log_parts) > 2048 && !whole ? 2 : 1;
         const int bad = bits == 4 ? (group_size == 64 ? lora_launch_b4_g64(p, rt, ct, xf32, sbf, st)
                                                       : lora_launch_b4_g128(p, rt, ct, xf32, sbf, st))
                                   : (group_size == 64 ? lora_launch_b2_g64(p, rt, ct, xf32, sbf, st)

@@ -103,6 +103,17 @@ def test_row_tiles(N):
         check_rows(call(p), want(p), f"M {M}", "f32")
 
 
+@pytest.mark.parametrize("bits,gs,N,K", [(4, 64, 16385, 512), (4, 128, 8215, 3200), (2, 64, 16417, 1024), (4, 64, 4129, 8256),
+                                         (2, 128, 8200, 6272)])
+@pytest.mark.parametrize("x,sb", [("bf16", "bf16"), ("f32", "f16")])
+def test_two_row_tiles(bits, gs, N, K, x, sb):
+    """More waves of one row tile than fit at once: two tiles each, the last one part empty."""
+    p = problem(3, N, K, bits, gs, x=x, sb=sb, R=8, seed=N)
+    y = call(p)
+    check_rows(y, want(p), "two tiles", "f32")
+    assert torch.equal(call(p, rows=[1])[0], y[1])
+
+
 @pytest.mark.parametrize("x", ["bf16", "f32"])
 def test_rows_do_not_depend_on_the_call(x):
     p = problem(70, 90, 1024, 4, 64, x=x, L=4)
