@@ -218,15 +218,22 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         p.yf32 = y_dt == QMV_DT_F32;
         p.adf16 = ad_dt == QMV_DT_F16;
         if (shrink_launch(p, bits, group_size, xf32, st)) return QMV_E_LAUNCH;
-        // Four token tiles read the codes once for 64 tokens; the hidden values of so
-        // many have to fit the shared memory (52 KB of them beside 90 of the rest at
-        // most).  Two row tiles per wave where one each would take more waves than fit at
-        // once, two per SIMD: 4096 x 12288, 13 tokens, 2048 waves: 19.3 us with one, 21.7
-        // with two; 4608 x 12288: 29.6, 22.0; 12288 x 3840, 3072 waves of four to a
-        // workgroup, 18.7, 18.9; 15360 x 3840: 22.5, 19.2.  Rows that are not cut into
-        // parts, short ones, have a wave per row tile.
+        // Row and token tiles of a wave: the fewest whose waves all fit at once, two per
+        // SIMD.  More tiles read codes and activations less often, but a second round of
+        // waves costs more, and idle SIMDs most.  Cold, us, one, two and four token tiles
+        // of two row tiles each (waves of one): 32 tokens, 3840 x 15360 (1920) 27.8, 35.5;
+        // 15360 x 3840 (3840), two and four: 26.5, 30.1; 64 tokens, 2048 x 2048 (512)
+        // 13.8, 22.1, 31.8; 3840 x 15360 (3840) 43.4, 35.1, 47.4; 15360 x 3840 (7680), two
+        // and four: 42.3, 35.4.  One and two row tiles, 13 tokens: 4096 x 12288 (2048
+        // waves of one) 19.3, 21.7; 4608 x 12288 (2304) 29.6, 22.0; 12288 x 3840 (3072, of
+        // fewer parts) 18.7, 18.9; 15360 x 3840 (3840) 22.5, 19.2.  The hidden values of
+        // the tokens have to fit the shared memory (52 KB of them beside 90 of the rest
+        // at most).  Rows that are not cut into parts, short ones, have a wave per row tile.
+        constexpr int kFit = 2048;
         const bool whole = p.log_parts == 0;
-        const int ct = whole || p.M <= 16 || p.Rp > 256 ? 1 : p.M <= 32 || p.Rp > 128 ? 2 : 4, rt = ((N + 15) / 16 << p.log_parts) > 2048 && !whole ? 2 : 1;
+        const int tiles = (p.M + 15) / 16, waves = (N + 31) / 32 << p.log_parts, most = p.Rp > 256 ? 1 : p.Rp > 128 ? 2 : 4;
+        const int fewest = whole || tiles == 1 || waves * tiles <= kFit ? 1 : tiles == 2 || waves * ((tiles + 1) / 2) <= kFit ? 2 : 4;
+        const int ct = std::min(fewest, most), rt = !whole && ((N + 15) / 16 << p.log_parts) * tiles > kFit ? 2 : 1;
         const int bad = bits == 4 ? (group_size == 64 ? lora_launch_b4_g64(p, rt, ct, xf32, sbf, st)
                                                       : lora_launch_b4_g128(p, rt, ct, xf32, sbf, st))
                                   : (group_size == 64 ? lora_launch_b2_g64(p, rt, ct, xf32, sbf, st)

@@ -377,7 +377,7 @@ int lora_scales(const LoraParams& p, bool sbf, hipStream_t st)
     return sbf ? lora_start<Tile<BITS, GS, RT, CT, NP, true, true>>(p, st) : lora_start<Tile<BITS, GS, RT, CT, NP, false, true>>(p, st);
 }
 
-// Token tiles per wave: as many as the tokens fill and the registers hold.
+// Token tiles per wave: as many as asked for and the registers hold.
 template <int BITS, int GS>
 int lora_pick(const LoraParams& p, int rt, int ct, bool xf32, bool sbf, hipStream_t st)
 {

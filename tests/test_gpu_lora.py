@@ -114,6 +114,18 @@ def test_two_row_tiles(bits, gs, N, K, x, sb):
     assert torch.equal(call(p, rows=[1])[0], y[1])
 
 
+@pytest.mark.parametrize("bits,gs,M,N,K", [(4, 64, 61, 17003, 512), (4, 128, 70, 8209, 1280), (4, 64, 23, 16390, 576),
+                                           (2, 64, 64, 17000, 1088), (4, 64, 47, 4500, 8192)])
+@pytest.mark.parametrize("x,sb,ad", [("bf16", "bf16", "f16"), ("f32", "f16", "bf16")])
+def test_token_tiles(bits, gs, M, N, K, x, sb, ad):
+    """More waves of one token tile than fit at once: two and four tiles each, the last one part empty."""
+    p = problem(M, N, K, bits, gs, x=x, sb=sb, ad=ad, R=24, L=5, seed=N)
+    y = call(p)
+    check_rows(y, want(p), "tiles", "f32")
+    rows = [0, 17, M - 1]
+    assert torch.equal(call(p, rows=rows), y[rows])
+
+
 @pytest.mark.parametrize("x", ["bf16", "f32"])
 def test_rows_do_not_depend_on_the_call(x):
     p = problem(70, 90, 1024, 4, 64, x=x, L=4)
