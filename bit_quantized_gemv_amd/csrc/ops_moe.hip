@@ -459,9 +459,8 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
     p.weights = weights;
     p.y = y;
     p.yf32 = yf32;
-    const int ct = p.P <= 12 * E ? 1 : 2;
-    if (!by_expert && by_token(n, k, D, F, bits)) return go(0, p, ct, xf32, sbf, st) || go(2, p, ct, xf32, sbf, st) ? QMV_E_LAUNCH : QMV_OK;
-    if (go(0, p, ct, xf32, sbf, st) || go(1, p, ct, xf32, sbf, st)) return QMV_E_LAUNCH;
+    if (!by_expert && by_token(n, k, D, F, bits)) return go(0, p, xf32, sbf, st) || go(2, p, xf32, sbf, st) ? QMV_E_LAUNCH : QMV_OK;
+    if (go(0, p, xf32, sbf, st) || go(1, p, xf32, sbf, st)) return QMV_E_LAUNCH;
     const float* z = p.z;
     const int* place = by_expert ? p.count + E : nullptr;
     void* args[] = {&z, &weights, &ids, &place, &y, &D, &E, &k, &yf32};

@@ -26,6 +26,7 @@ struct ExpertParams {
     int slots;                     // P: a workgroup per pair, its expert's first; E: one per expert
     const int* base;               // sorted pairs: an expert's first tile of 16, its pairs, and each
     const int* count;              // pair's place (a row of xp, h and z); null where pairs keep their order
+    int takers;                    // workgroups that share an expert's pairs
     int log_parts;                 // of a row's K
     int groups;                    // of waves in a workgroup
     Meta meta;
@@ -39,9 +40,9 @@ struct ExpertParams {
 
 // which = 0: gate and up products and the activation (xp -> h); 1: down product (h -> z);
 // 2: down products and weighted sums of whole tokens (h -> y)
-int expert_launch_b4_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
-int expert_launch_b4_g128(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
-int expert_launch_b2_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
-int expert_launch_b2_g128(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b4_g64(int which, const ExpertParams& p, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b4_g128(int which, const ExpertParams& p, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b2_g64(int which, const ExpertParams& p, bool xf32, bool sbf, hipStream_t st);
+int expert_launch_b2_g128(int which, const ExpertParams& p, bool xf32, bool sbf, hipStream_t st);
 
 }  // namespace ops

@@ -2,8 +2,8 @@
 #include "ops_moe_kernel.hpp"
 
 namespace ops {
-int expert_launch_b4_g64(int which, const ExpertParams& p, int ct, bool xf32, bool sbf, hipStream_t st)
+int expert_launch_b4_g64(int which, const ExpertParams& p, bool xf32, bool sbf, hipStream_t st)
 {
-    return sbf ? expert_pick<4, 64, true>(which, p, ct, xf32, st) : expert_pick<4, 64, false>(which, p, ct, xf32, st);
+    return sbf ? expert_pick<4, 64, true>(which, p, xf32, st) : expert_pick<4, 64, false>(which, p, xf32, st);
 }
 }  // namespace ops

@@ -76,7 +76,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
     using J = Join<RT>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     together(p.ids, GATE ? p.w13 : p.w2, GATE ? p.s13 : p.s2, GATE ? p.b13 : p.b2, GATE ? p.xp : p.h, GATE ? p.x_plane : p.h_plane,
-             p.P, p.D, p.F, p.E, p.slots, p.log_parts, p.groups, p.meta.groups, p.meta.window, p.meta.windows, p.per_k);
+             p.P, p.D, p.F, p.E, p.slots, p.takers, p.log_parts, p.groups, p.meta.groups, p.meta.window, p.meta.windows, p.per_k);
     const int slot = blockIdx.y;
     const bool by_pair = p.slots == p.P;
     const int e = by_pair ? p.ids[slot] : slot;
@@ -102,7 +102,9 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
         const Found found = find_pairs(p.ids, p.P, e, slot, list);
         n = by_pair && !found.first ? 0 : found.n;
     }
-    if (n == 0) return;
+    // the pairs 16 * CT at a time, in turn with the workgroups of the same rows
+    const int mine = T::FRAG ? 16 * CT * blockIdx.z : 0, next = 16 * CT * p.takers;
+    if (mine >= n) return;
     // the row of the expert's pair number t
     auto row_of = [&](int t) { return T::FRAG ? base + t : (int)list[t]; };
 
@@ -160,13 +162,13 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
         if (meta.windows == 1) T::begin(ring, r, min(s0, s1 - 1), max(s1, s0 + 1));
     };
     if constexpr (!T::FRAG) lds_barrier();      // the list is there
-    begin(0);
+    begin(mine);
     if (meta.windows == 1) {
         copy.put(scales, biases);
         if (GATE) copy_up.put(scales + half, biases + half);
     }
     lds_barrier();
-    for (int t0 = 0; t0 < n; t0 += 16 * CT) {
+    for (int t0 = mine; t0 < n; t0 += next) {
         f32x4 acc[RT][CT];
         T::clear(acc);
         for (int k = 0; k < meta.windows; ++k) {
@@ -221,8 +223,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                 }
             }
         }
-        if (t0 + 16 * CT < n) {
-            begin(t0 + 16 * CT);
+        if (t0 + next < n) {
+            begin(t0 + next);
             lds_barrier();          // the partial results are read
         }
     }
@@ -237,6 +239,11 @@ inline int expert_parts(int chunks)
     return n >= 64 ? 8 : n >= 24 ? 4 : 1;
 }
 
+constexpr int kFit = 2048;      // waves that run at once, two per SIMD
+
+// Waves of a product if every workgroup goes through all its expert's pairs.
+inline int expert_waves(const ExpertParams& p, int chunks, int tiles) { return p.slots * tiles * expert_parts(chunks); }
+
 template <class T, bool GATE>
 int expert_start(const ExpertParams& p, hipStream_t st)
 {
@@ -248,13 +255,19 @@ int expert_start(const ExpertParams& p, hipStream_t st)
     q.groups = std::max(1, 4 / parts);
     while (N / ROWS % q.groups != 0) q.groups /= 2;
     q.meta = Meta(32 * q.groups, K, T::BITS, T::GS, parts);
+    // Where the rows alone are fewer waves than fit at once, workgroups share an expert's
+    // pairs (as many as twice the average asks for, since experts differ): 128 tokens
+    // over 4 experts of 512 x 512, 2 each: 53.5 us without, 28.5 with; of 2048 x 1024,
+    // 89.0, 48.4; over 16 of 1024 x 768, 4 each: 54.1, 43.3.
+    q.takers = 1;
+    if (T::FRAG) q.takers = std::max(1, std::min(kFit / expert_waves(p, K / (4 * T::VPW), N / ROWS), (2 * p.P / p.E + 16 * T::CT - 1) / (16 * T::CT)));
     const ExpertSpace sp(q.meta, q.groups * parts, 32 * q.groups, p.P);
     const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
     if (sp.bytes > 64 * 1024 &&
         hipFuncSetAttribute(fn, hipFuncAttributeMaxDynamicSharedMemorySize, sp.bytes) != hipSuccess)
         return 1;
     void* args[] = {&q};
-    const dim3 grid(N / (ROWS * q.groups), p.slots);
+    const dim3 grid(N / (ROWS * q.groups), p.slots, q.takers);
     return hipLaunchKernel(fn, grid, dim3(kWave * q.groups * parts), args, sp.bytes, st) == hipSuccess ? 0 : 1;
 }
 
@@ -352,11 +365,16 @@ int expert_down(const ExpertParams& p, int ct, hipStream_t st)
 }
 
 template <int BITS, int GS, bool SBF>
-int expert_pick(int which, const ExpertParams& p, int ct, bool xf32, hipStream_t st)
+int expert_pick(int which, const ExpertParams& p, bool xf32, hipStream_t st)
 {
     if (which == 2)
         return p.h_planes == 3 ? token_start<Tile<BITS, GS, 2, 1, 3, SBF, false>>(p, st)
                                : token_start<Tile<BITS, GS, 2, 1, 2, SBF, false>>(p, st);
+    // Two token tiles per wave for sorted pairs of more than 12 per expert, where waves of
+    // one each do not fit at once: 128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit,
+    // whole layers: 152 us with two in the gate and up products, 177 with one.
+    const int waves = which == 0 ? expert_waves(p, p.D * BITS / 128, p.F / 16) : expert_waves(p, p.F * BITS / 128, p.D / 32);
+    const int ct = p.P > 12 * p.E && waves * ((p.P / p.E + 15) / 16) > kFit ? 2 : 1;
     if (p.base) {
         if (which == 1) return expert_down<BITS, GS, SBF, true>(p, ct, st);
         if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, true>(p, st);

@@ -166,6 +166,21 @@ def test_sorted_pairs(T, E, k, x):
     assert torch.equal(call_experts(p, weights, ids, rows=rows), call_experts(p, weights, ids)[rows])
 
 
+@pytest.mark.parametrize("bits,gs,T,E,k,D,F", [(4, 64, 150, 3, 1, 512, 5760), (2, 64, 90, 2, 2, 512, 5824), (4, 128, 254, 6, 1, 5888, 128),
+                                              (4, 64, 200, 2, 1, 576, 320)])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_many_tokens_per_expert(bits, gs, T, E, k, D, F, x):
+    """One and two token tiles per wave, an expert's pairs shared by workgroups or gone through by each; uneven counts."""
+    p = problem(T, E, k, D, F, bits, gs, x=x, seed=T)
+    ids, weights = some_ids(T, E, k)
+    ids[T // 4:T // 2, 0] = 0
+    for dtype in (torch.float32, torch.bfloat16):
+        want = want_experts(p, weights, ids)
+        check_rows(call_experts(p, weights, ids, out_dtype=dtype), want, str(dtype), "f32" if dtype == torch.float32 else "bf16")
+    rows = [0, T // 3, T - 1]
+    assert torch.equal(call_experts(p, weights, ids, rows=rows), call_experts(p, weights, ids)[rows])
+
+
 def test_empty_slots_and_repeats():
     p = problem(5, 4, 3, 128, 128)
     ids = torch.tensor([[-1, -1, -1], [2, -1, 4], [1, 1, 1], [3, 0, -7], [2 ** 31 - 1, 3, 3]], dtype=torch.int32)
