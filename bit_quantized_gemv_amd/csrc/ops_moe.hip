@@ -360,11 +360,15 @@ int run_route(const char* x, const void* router, float* weights, int32_t* ids, v
                : QMV_E_LAUNCH;
 }
 
-// Pairs are sorted by expert where an expert meets eight or more on average: below
-// that a wave's 16 rows are mostly repeats of a few, which cost it little, and
-// sorting is a launch of about 5 us (128 tokens over 32 experts, 16 pairs each: 181 us
-// sorted against 236).
-bool sorted(int n, int k, int E) { return (long long)n * k >= 8LL * E; }
+// Pairs are sorted by expert where an expert meets eight or more on average and the
+// products are not small.  Below that a wave's 16 rows are mostly repeats of a few,
+// which cost it little, and sorting is a launch of about 5 us (128 tokens over 32
+// experts of 3840 x 1920, 16 pairs each: 181 us sorted against 236; 64 tokens over 4 of
+// 512 x 512, 32 pairs each: 27.6 against 22.8; over 4 of 1024 x 512, 30.0, 29.7).
+bool sorted(int n, int k, int E, int D, int F)
+{
+    return (long long)n * k >= 8LL * E && (k > kTokenSlots || (long long)n * k * D * F > 1 << 25);
+}
 
 // Scratch memory of the experts' products for n tokens.
 struct ExpertPieces {
@@ -372,7 +376,7 @@ struct ExpertPieces {
     size_t x_plane, h_plane;
     ExpertPieces(int n, int D, int F, int k, int E, int bits, int gs)
     {
-        const bool s = sorted(n, k, E);
+        const bool s = sorted(n, k, E, D, F);
         const int rows = s ? (n * k / 16 + std::min(E, n * k)) * 16 : n * k;
         x_plane = Packed(D, bits, gs, s).plane(s ? rows : n);
         h_plane = Packed(F, bits, gs, s).plane(rows);
@@ -397,7 +401,7 @@ int run_pack(const char* x, const int32_t* ids, char* ws, int n, int D, int F, i
 {
     constexpr int threads = kRouteWaves * kWave;
     bool f32 = x_dt == QMV_DT_F32;
-    if (!sorted(n, k, E)) {
+    if (!sorted(n, k, E, D, F)) {
         void* args[] = {&x, &ws, &n, &D, &bits, &gs, &f32};
         const int packs = (int)(((long long)n * (D * bits / 32) + threads - 1) / threads);
         return launch((const void*)&pack_kernel, dim3(packs), threads, args, st) ? QMV_OK : QMV_E_LAUNCH;
@@ -429,7 +433,7 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
 {
     const auto go = bits == 4 ? (gs == 64 ? expert_launch_b4_g64 : expert_launch_b4_g128)
                               : (gs == 64 ? expert_launch_b2_g64 : expert_launch_b2_g128);
-    const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16, by_expert = sorted(n, k, E);
+    const bool xf32 = x_dt == QMV_DT_F32, sbf = sb_dt == QMV_DT_BF16, by_expert = sorted(n, k, E, D, F);
     bool yf32 = y_dt == QMV_DT_F32;
     const ExpertPieces at(n, D, F, k, E, bits, gs);
     ExpertParams p;
@@ -581,7 +585,7 @@ int qmv_moe(const void* x, const void* router, const uint32_t* w13, const void* 
         int32_t* const it = ids + (size_t)t * top_k;
         const char* const xt = static_cast<const char*>(x) + (size_t)t * D * size_of(x_dt);
         char* const ws = static_cast<char*>(workspace);
-        const bool later = sorted(n, top_k, n_experts);         // packed when the ids are known
+        const bool later = sorted(n, top_k, n_experts, D, F);         // packed when the ids are known
         if (const int e = run_route(xt, router, wt, it, part, later ? nullptr : ws, n, D, n_experts, top_k, renormalize != 0, x_dt,
                                     r_dt, bits, group_size, st))
             return e;

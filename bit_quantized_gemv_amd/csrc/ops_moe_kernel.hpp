@@ -103,7 +103,7 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
         n = by_pair && !found.first ? 0 : found.n;
     }
     // the pairs 16 * CT at a time, in turn with the workgroups of the same rows
-    const int mine = T::FRAG ? 16 * CT * blockIdx.z : 0, next = 16 * CT * p.takers;
+    const int mine = 16 * CT * blockIdx.z, next = 16 * CT * p.takers;
     if (mine >= n) return;
     // the row of the expert's pair number t
     auto row_of = [&](int t) { return T::FRAG ? base + t : (int)list[t]; };
@@ -259,8 +259,7 @@ int expert_start(const ExpertParams& p, hipStream_t st)
     // pairs (as many as twice the average asks for, since experts differ): 128 tokens
     // over 4 experts of 512 x 512, 2 each: 53.5 us without, 28.5 with; of 2048 x 1024,
     // 89.0, 48.4; over 16 of 1024 x 768, 4 each: 54.1, 43.3.
-    q.takers = 1;
-    if (T::FRAG) q.takers = std::max(1, std::min(kFit / expert_waves(p, K / (4 * T::VPW), N / ROWS), (2 * p.P / p.E + 16 * T::CT - 1) / (16 * T::CT)));
+    q.takers = std::max(1, std::min(kFit / expert_waves(p, K / (4 * T::VPW), N / ROWS), (2 * p.P / p.E + 16 * T::CT - 1) / (16 * T::CT)));
     const ExpertSpace sp(q.meta, q.groups * parts, 32 * q.groups, p.P);
     const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
     if (sp.bytes > 64 * 1024 &&

@@ -166,6 +166,24 @@ def test_sorted_pairs(T, E, k, x):
     assert torch.equal(call_experts(p, weights, ids, rows=rows), call_experts(p, weights, ids)[rows])
 
 
+@pytest.mark.parametrize("T,E,k,D,F", [(63, 16, 2, 1024, 512), (64, 16, 2, 1024, 512), (40, 5, 3, 576, 448), (44, 5, 3, 576, 448),
+                                       (20, 17, 9, 192, 128)])
+@pytest.mark.parametrize("x", ["bf16", "f32"])
+def test_sorted_pairs_of_larger_experts(T, E, k, D, F, x):
+    """Both sides of the rule, by the pairs of an expert, by the products' size and by the slots of a token."""
+    p = problem(T, E, k, D, F, x=x, seed=T)
+    ids, weights = some_ids(T, E, k)
+    ids[ids == E - 1] = 0
+    ids[::5, 0] = -1
+    want = want_experts(p, weights, ids)
+    y = call_experts(p, weights, ids)
+    keep = (want != 0).any(-1)
+    assert (y[~keep] == 0).all()
+    check_rows(y[keep], want[keep], "sorted", "f32")
+    rows = [0, 1, T // 2, T - 1]
+    assert torch.equal(call_experts(p, weights, ids, rows=rows), y[rows])
+
+
 @pytest.mark.parametrize("bits,gs,T,E,k,D,F", [(4, 64, 150, 3, 1, 512, 5760), (2, 64, 90, 2, 2, 512, 5824), (4, 128, 254, 6, 1, 5888, 128),
                                               (4, 64, 200, 2, 1, 576, 320)])
 @pytest.mark.parametrize("x", ["bf16", "f32"])
