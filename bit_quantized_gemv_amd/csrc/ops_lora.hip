@@ -225,8 +225,8 @@ int qmv_affine_lora(const uint32_t* w, const void* scales, const void* biases, c
         // 15360 x 3840 (3840), two and four: 26.5, 30.1; 64 tokens, 2048 x 2048 (512)
         // 13.8, 22.1, 31.8; 3840 x 15360 (3840) 43.4, 35.1, 47.4; 15360 x 3840 (7680), two
         // and four: 42.3, 35.4.  One and two row tiles, 13 tokens: 4096 x 12288 (2048
-        // waves of one) 19.3, 21.7; 4608 x 12288 (2304) 29.6, 22.0; 12288 x 3840 (3072, of
-        // fewer parts) 18.7, 18.9; 15360 x 3840 (3840) 22.5, 19.2.  The hidden values of
+        // waves of one) 19.3, 21.7; 4608 x 12288 (2304) 29.6, 22.0; 15360 x 3840
+        // (3840) 22.5, 19.2.  The hidden values of
         // the tokens have to fit the shared memory (52 KB of them beside 90 of the rest
         // at most).  Rows that are not cut into parts, short ones, have a wave per row tile.
         constexpr int kFit = 2048;
