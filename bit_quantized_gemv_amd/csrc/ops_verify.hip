@@ -234,11 +234,14 @@ __device__ __forceinline__ int length_of(const VerifyParams& p, int b)
 
 // A wave walks p.walk spans of one row, the next one's loads in flight.
 //
-// A lane takes e = 2^t, t = l * hi + ref, in fp32: hi is log2(e) / T rounded and
-// ref about -(its largest value) * hi, so that ref and hi are exact as they stand
-// and only t is rounded, either way.  The rest lo of the rate would shift all
-// terms one way; to first order it adds ln 2 * lo * sum(e (l - largest)), from
-// sum(e t).
+// A lane takes e = 2^t, t = (l - largest) * hi, in fp32: hi is log2(e) / T rounded
+// and `largest` the lane's own so far.  The two roundings of t are relative to t, so
+// they matter as little for values of 1e10 (a mask, a temperature near zero) as for
+// ones of 10, and t is 0 at the largest and never above.  (As l * hi - largest * hi
+// it would be off by an ulp of largest * hi, and e infinite where that passes 128.)
+// The rest of the rate would shift all terms one way; to first order it adds ln 2 *
+// (rate / hi - 1) * sum(e t).  Whatever is below 2^-200 of the largest, masks among
+// it, is 0 there, and finite: no term of a sum is infinite or NaN.
 template <bool LF32>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
 {
@@ -258,12 +261,13 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
     u32x4 w[NV], next[NV];
     float v[kSpanPer];
     constexpr double kLn2 = 0.69314718055994530942;
+    constexpr float kLeast = -200.0f;             // of a term's exponent: 0 in fp32
     bool strange = !(T < 1e18f) || T <= 1e-18f;
     if (T > 0.0f && !strange) {
         const double rate = rate_of(T);
         const float hi = (float)rate;
         load_raw<LF32>(next, l, i0, 64 * PER, p.V, kNone);
-        float mine = -1e18f, ref = 0.0f, s[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
+        float mine = -1e18f, s[4] = {0.f, 0.f, 0.f, 0.f}, c[4] = {0.f, 0.f, 0.f, 0.f};
         for (int i = 0; i < spans; ++i) {
 #pragma unroll
             for (int d = 0; d < NV; ++d) w[d] = next[d];
@@ -271,14 +275,13 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
 #pragma unroll
             for (int d = 0; d < NV; ++d) unpack<LF32>(v + d * PER, w[d]);
             // the median of a value, the largest so far and +inf is the larger of the first two, and passes NaN over
+            const float old = mine;
             float t4[4] = {mine, mine, mine, mine};
 #pragma unroll
             for (int d = 0; d < kSpanPer; ++d) t4[d & 3] = __builtin_amdgcn_fmed3f(v[d], t4[d & 3], __builtin_huge_valf());
             mine = __builtin_fmaxf(__builtin_fmaxf(t4[0], t4[1]), __builtin_fmaxf(t4[2], t4[3]));
-            const float old = ref;
-            ref = -(mine * hi);
             if (i > 0) {
-                const float up = ref - old, f = __builtin_amdgcn_exp2f(up);
+                const float up = __builtin_fmaxf((old - mine) * hi, kLeast), f = __builtin_amdgcn_exp2f(up);
 #pragma unroll
                 for (int d = 0; d < 4; ++d) {
                     c[d] = f * __builtin_fmaf(up, s[d], c[d]);
@@ -287,7 +290,7 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
             }
 #pragma unroll
             for (int d = 0; d < kSpanPer; ++d) {
-                const float t = __builtin_fmaxf(__builtin_fmaf(v[d], hi, ref), -200.0f);   // masked and NaN: 2^-200, 0 in fp32
+                const float t = __builtin_fmaxf((v[d] - mine) * hi, kLeast);      // masked and NaN too
                 const float e = __builtin_amdgcn_exp2f(t);
                 s[d & 3] += e;
                 c[d & 3] = __builtin_fmaf(e, t, c[d & 3]);
@@ -297,10 +300,9 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
         strange = !(__builtin_fabsf(top) < 1e18f);
         if (!strange) {
             const double sa = (double)((s[0] + s[1]) + (s[2] + s[3])), ca = (double)((c[0] + c[1]) + (c[2] + c[3]));
-            const double off = (double)mine * (double)hi + (double)ref;            // t at the lane's largest
-            const double all = sa + kLn2 * (rate / (double)hi - 1.0) * (ca - off * sa);
-            const double t = ((double)mine - (double)top) * rate - off;            // from there to the wave's largest
-            const float near = __builtin_fmaxf((float)t, -200.0f), e = __builtin_amdgcn_exp2f(near);
+            const double all = sa + kLn2 * (rate / (double)hi - 1.0) * ca;
+            const double t = ((double)mine - (double)top) * rate;                  // from the lane's largest to the wave's
+            const float near = __builtin_fmaxf((float)t, kLeast), e = __builtin_amdgcn_exp2f(near);
             sum = wave_sum(all * ((double)e + kLn2 * (double)e * __builtin_fmax(t - (double)near, -1.0)));
         }
     }

@@ -1,0 +1,90 @@
+"""verify where its sums come near a border: finite masks, very small temperatures,
+large logits."""
+import numpy as np
+import pytest
+import torch
+
+from ops_util import TORCH, gen
+from test_gpu_verify import check
+
+pytestmark = pytest.mark.gpu
+
+MASKS = [-1e4, -1e9, -1e10, -1e12, -1e15]
+
+
+def masked(B, S, V, dt, value, added, seed):
+    """Logits with finite masks over 95 of 100 values, whole lanes' values, whole spans and the end of the row, and a
+    drafter that keeps to what is left."""
+    g = gen(seed)
+    l = 2 * torch.randn(B, S + 1, V, generator=g)
+    l = torch.where(torch.rand(B, S + 1, V, generator=g) < min(0.5, 20 / V), l + 6, l)
+    i = torch.arange(V)
+    gone = torch.rand(B, S + 1, V, generator=g) < 0.95
+    gone[0::4] = (i // 8 % 64 < 60) & (i % 97 != 5)
+    gone[1::4, :, V // 8:3 * V // 4] = True
+    gone[2::4, :, V - V // 3:] = True
+    gone[3::4, :, 5] = False
+    near = l[:, :S] + 0.5 * torch.randn(B, S, V, generator=g)
+    l = torch.where(gone, l + value if added else torch.tensor(value), l)
+    probs = torch.softmax(torch.where(gone[:, :S], torch.tensor(-torch.inf), near), -1)
+    draft = torch.multinomial(probs.reshape(B * S, V), 1, generator=g).reshape(B, S).int()
+    return l.to(TORCH[dt]), draft, torch.rand(B, S + 1, generator=g), probs
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("value", MASKS)
+@pytest.mark.parametrize("added", [False, True])
+def test_finite_masks(dt, value, added):
+    """A mask of finite values is a probability of zero as -inf is: nothing of it may reach the rest of the row."""
+    B, S = 24, 3
+    temp = torch.linspace(0.1, 1.5, B)
+    temp[3], temp[7] = 1.0, 0.0
+    l, draft, u, probs = masked(B, S, 7001, dt, value, added, seed=int(-np.log10(-value)) + added + 100)
+    _, n = check(l, draft, u, probs, temp=temp)
+    assert n.sum() > B // 4             # drafts are accepted at all
+    check(l, draft, u, None, temp=temp)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("value", [-1e4, -1e10])
+def test_finite_masks_of_many_rows(dt, value):
+    """The same where a wave walks several spans of a row."""
+    B = 128
+    temp = torch.linspace(0.2, 1.5, B)
+    temp[2] = 1.0
+    l, draft, u, probs = masked(B, 1, 140001, dt, value, False, seed=9)
+    check(l, draft, u, probs, temp=temp)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1e-4, 1e-6, 1e-7, 1e-8, 1e-9, 1e-10, 1e-12, 1e-15, 2e-18, 1e-18, 1e-30])
+def test_small_temperatures(dt, T):
+    """All that is left is the largest value, or several equal ones, each with its share."""
+    B, S, V = 24, 3, 5000
+    g = gen(3)
+    l = 10 + 2 * torch.randn(B, S + 1, V, generator=g)
+    top = 20 + 30 * torch.rand(B, S + 1, 1, generator=g)
+    at = torch.randint(0, V, (B, S + 1, 3), generator=g)
+    l.scatter_(2, at[..., :1], top)
+    l[1::3] = l[1::3].scatter(2, at[1::3, :, :2], top[1::3].expand(-1, -1, 2))
+    l[2::3] = l[2::3].scatter(2, at[2::3], top[2::3].expand(-1, -1, 3))
+    draft, u = at[:, :S, 0].int().contiguous(), torch.rand(B, S + 1, generator=g)
+    probs = torch.full((B, S, V), 0.25 / V)
+    probs.scatter_(2, at[:, :S, :1], 0.75)
+    l = l.to(TORCH[dt])
+    temp = torch.full((B,), T)
+    _, n = check(l, draft, u, None, temp=temp)
+    assert (n[::3] == S).all()          # a token of probability 1 is accepted
+    check(l, draft, u, probs, temp=temp)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("scale", [1e6, 1e10, 1e14, 1e17])
+def test_large_logits(dt, scale):
+    B, S, V = 12, 2, 5000
+    g = gen(4)
+    l = scale * (1 + torch.rand(B, S + 1, V, generator=g)) * torch.where(torch.arange(B) % 2 == 0, 1.0, -1.0).reshape(B, 1, 1)
+    l = l.to(TORCH[dt])
+    draft = l[:, :S].float().argmax(-1).int()
+    check(l, draft, torch.rand(B, S + 1, generator=g), None, temp=torch.linspace(0.3, 3.0, B))
+    check(l, draft, torch.rand(B, S + 1, generator=g), None, temp=torch.linspace(0.3, 3.0, B) * scale)
