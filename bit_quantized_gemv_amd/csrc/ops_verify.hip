@@ -384,7 +384,9 @@ __device__ __forceinline__ Pick block_pick(PickSpace& sp, int i0, int i1, double
     }
     const double t = target(total);
     to += below;
-    const unsigned long long over = __ballot(to > t), some = __ballot(sum > 0.0);
+    // Of a thread's positive values only: the target may be below zero, by the rounding of a border
+    // that it lies on, and then every thread's sum is past it.
+    const unsigned long long some = __ballot(sum > 0.0), over = __ballot(to > t) & some;
     if (lane < 2) sp.index[wave][lane] = -1;
     // the first thread past the number, and the last with anything, look through their values
     const bool first = over != 0 && lane == __builtin_ctzll(over), last = some != 0 && lane == 63 - __builtin_clzll(some);

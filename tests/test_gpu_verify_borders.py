@@ -1,11 +1,13 @@
-"""verify where its sums come near a border: finite masks, very small temperatures,
-large logits."""
+"""verify where its sums and choices come near a border: finite masks, very small
+temperatures, large logits, numbers that fall on a prefix sum."""
 import numpy as np
 import pytest
 import torch
 
-from ops_util import TORCH, gen
+from ops_util import DEV, TORCH, gen
 from test_gpu_verify import check
+
+import bit_quantized_gemv_amd as q
 
 pytestmark = pytest.mark.gpu
 
@@ -88,3 +90,20 @@ def test_large_logits(dt, scale):
     draft = l[:, :S].float().argmax(-1).int()
     check(l, draft, torch.rand(B, S + 1, generator=g), None, temp=torch.linspace(0.3, 3.0, B))
     check(l, draft, torch.rand(B, S + 1, generator=g), None, temp=torch.linspace(0.3, 3.0, B) * scale)
+
+
+def test_a_number_on_the_border_of_two_halves():
+    """Two equal halves and u = 1/2: the last value of the first or, as in exact arithmetic, the first of the second."""
+    B = 300
+    h = 2 * torch.randn(B, 1, 4096, generator=gen(6))
+    h[..., :8] = -torch.inf
+    t, _ = q.verify(torch.cat([h, h], -1).to(DEV), torch.zeros(B, 0, dtype=torch.int32, device=DEV), torch.full((B, 1), 0.5, device=DEV))
+    assert set(t[:, 0].tolist()) <= {4095, 4104}
+
+
+@pytest.mark.parametrize("first", [1, 8, 600, 5000])
+def test_numbers_below_zero_take_the_first_value(first):
+    l = torch.randn(4, 1, 9000, generator=gen(7))
+    l[..., :first] = -torch.inf
+    t, _ = q.verify(l.to(DEV), torch.zeros(4, 0, dtype=torch.int32, device=DEV), torch.full((4, 1), -0.5, device=DEV))
+    assert t[:, 0].tolist() == [first] * 4
