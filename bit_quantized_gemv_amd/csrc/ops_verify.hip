@@ -21,8 +21,9 @@
 // chunks are summed, but the weights max(e_i - q_i Z, 0) are needed with it: each
 // chunk adds up e_i and q_i where e_i > q_i Z0 for the first pass's Z0, and their
 // sums give those of the weights for the true Z, up to the values so near the
-// border that Z and Z0 disagree about them; where those could matter the sums are
-// taken once more.
+// border that Z and Z0 disagree about them; where those could matter (a drafter whose
+// probabilities are the target's, u = 0) the sums are taken once more, by the last
+// workgroup alone: 1.6 us for every 2048 values, 115 us for a row of 131072 in place of 13.5.
 #include <hip/hip_runtime.h>
 
 #include <algorithm>
@@ -620,7 +621,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
         t = all_of(t);
         const double Z = t.p, left = t.e - Z * t.q;
         bool use = rest && left > 0.0;
-        if (rest && t.near * 0x1p13 > left) {     // the border's values could move the sums by 2^-33 of them
+        // the border's values could move the sums by 2^-33 of them, or are all that is left before a number this small
+        if (rest && (t.near * 0x1p13 > left || t.near > (double)u_last * left)) {
             double all = 0.0;
             for (int c = 0; c < p.chunks; ++c) {
                 load_chunk(c);

@@ -1,5 +1,5 @@
 """verify where its sums and choices come near a border: finite masks, very small
-temperatures, large logits, numbers that fall on a prefix sum."""
+temperatures, large logits, equal probabilities, numbers that fall on a prefix sum."""
 import numpy as np
 import pytest
 import torch
@@ -90,6 +90,25 @@ def test_large_logits(dt, scale):
     draft = l[:, :S].float().argmax(-1).int()
     check(l, draft, torch.rand(B, S + 1, generator=g), None, temp=torch.linspace(0.3, 3.0, B))
     check(l, draft, torch.rand(B, S + 1, generator=g), None, temp=torch.linspace(0.3, 3.0, B) * scale)
+
+
+@pytest.mark.parametrize("side", [1, -1])
+def test_zero_takes_the_first_value_left(side):
+    """u = 0 gives the lowest index of a positive weight, however small.  The first 2048 values have one that is not
+    masked, and the drafter's probability of it, in fp32, is the target's but for 2^-30 of it, above or below."""
+    B, V, n = 256, 4096, 20
+    live = 2 * torch.randn(1 << 17, n, generator=gen(5))
+    e = torch.exp(torch.cat([torch.full((1 << 17, 1), -12.0), live], 1).double())
+    p = e / e.sum(1, keepdim=True)
+    off = (p[:, 0].float().double() / p[:, 0] - 1) * side
+    rows = torch.nonzero((off > 2.0 ** -40) & (off < 2.0 ** -30)).squeeze(1)[:B]
+    assert len(rows) == B
+    l = torch.full((B, 2, V), -torch.inf)
+    l[..., 7], l[..., 2048:2048 + n] = -12.0, live[rows].unsqueeze(1)
+    probs = torch.zeros(B, 1, V)
+    probs[:, 0, 7], probs[:, 0, 2048:2048 + n] = p[rows, 0].float(), 0.5 * p[rows, 1:].float()
+    t, _ = check(l, torch.full((B, 1), V, dtype=torch.int32), torch.zeros(B, 2), probs)        # no such token: rejected
+    assert (t[:, 0] == (2048 if side > 0 else 7)).all()
 
 
 def test_a_number_on_the_border_of_two_halves():
