@@ -462,7 +462,6 @@ int run_experts(const float* weights, const int32_t* ids, const uint32_t* w13, c
     p.count = by_expert ? p.base + E : nullptr;
     p.log_parts = 0;
     p.per_k = 1.0f / (float)k;
-    p.h_planes = yf32 ? 3 : 2;
     p.weights = weights;
     p.y = y;
     p.yf32 = yf32;

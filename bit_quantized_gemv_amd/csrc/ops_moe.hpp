@@ -34,8 +34,6 @@ struct ExpertParams {
     const float* weights;          // [P]
     void* y;                       // [P / k][D]
     bool yf32;
-    int h_planes;                  // three: exact; two, for bf16 outputs: off by 2^-17, a two hundred and fiftieth of
-                                   // their rounding, for a third less of the down product's work
 };
 
 // which = 0: gate and up products and the activation (xp -> h); 1: down product (h -> z);

@@ -201,18 +201,13 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
                         for (int b = 0; b < 2; ++b)
                             v[b] = silu(J::sum(join, g * parts, parts, J::at(en + b * H, et))) *
                                    J::sum(join, g * parts, parts, J::at(16 + en + b * H, et));
-                        uint32_t ah, am, al = 0, bh, bm, bl = 0;
-                        if (p.h_planes == 3) {
-                            split3(v[0], ah, am, al);
-                            split3(v[1], bh, bm, bl);
-                        } else {
-                            split2(v[0], ah, am);
-                            split2(v[1], bh, bm);
-                        }
+                        uint32_t ah, am, al, bh, bm, bl;
+                        split3(v[0], ah, am, al);
+                        split3(v[1], bh, bm, bl);
                         char* to = p.h + pk.word(row_of(t0 + 16 * j + et), (first + g * 16) / T::VPW + word) + (ii / 4) * pk.op_step() + (ii % 4) * 4;
                         *reinterpret_cast<uint32_t*>(to) = hi16(ah, bh);
                         *reinterpret_cast<uint32_t*>(to + p.h_plane) = hi16(am, bm);
-                        if (p.h_planes == 3) *reinterpret_cast<uint32_t*>(to + 2 * p.h_plane) = hi16(al, bl);
+                        *reinterpret_cast<uint32_t*>(to + 2 * p.h_plane) = hi16(al, bl);
                     }
                 }
             } else {
@@ -354,33 +349,27 @@ int token_start(const ExpertParams& p, hipStream_t st)
     return hipLaunchKernel(fn, dim3(p.D / 32, p.P / p.k), dim3(kWave * p.k), args, bytes, st) == hipSuccess ? 0 : 1;
 }
 
-template <int BITS, int GS, bool SBF, bool SORTED>
-int expert_down(const ExpertParams& p, int ct, hipStream_t st)
-{
-    if constexpr (SORTED && BITS == 4)          // (2-bit codes: 250 spills, 182 us against 68)
-        if (ct == 2 && p.h_planes == 2) return expert_start<Tile<BITS, GS, 2, 2, 2, SBF, true>, false>(p, st);
-    return p.h_planes == 3 ? expert_start<Tile<BITS, GS, 2, 1, 3, SBF, SORTED>, false>(p, st)
-                           : expert_start<Tile<BITS, GS, 2, 1, 2, SBF, SORTED>, false>(p, st);
-}
-
 template <int BITS, int GS, bool SBF>
 int expert_pick(int which, const ExpertParams& p, bool xf32, hipStream_t st)
 {
-    if (which == 2)
-        return p.h_planes == 3 ? token_start<Tile<BITS, GS, 2, 1, 3, SBF, false>>(p, st)
-                               : token_start<Tile<BITS, GS, 2, 1, 2, SBF, false>>(p, st);
+    // The down products take the hidden values in three planes, exactly as fp32 held them.  (In two, off by 2^-17, 2.5
+    // of 1000 bf16 outputs were the neighbour of the right one; now 0.3, and 1 where products and sums are plain fp32.
+    // Layers were faster by up to a tenth, and with 2-bit codes in groups of 64, whose instances of three planes spill,
+    // by a fifth: 13 tokens over 128 experts of 2048 x 1024 93 us, now 99; 2-bit, 91, now 117.)
+    if (which == 2) return token_start<Tile<BITS, GS, 2, 1, 3, SBF, false>>(p, st);
+    if (which == 1)
+        return p.base ? expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, false>(p, st)
+                      : expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, false>(p, st);
     // Two token tiles per wave for sorted pairs of more than 12 per expert, where waves of
     // one each do not fit at once: 128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit,
     // whole layers: 152 us with two in the gate and up products, 177 with one.
-    const int waves = which == 0 ? expert_waves(p, p.D * BITS / 128, p.F / 16) : expert_waves(p, p.F * BITS / 128, p.D / 32);
+    const int waves = expert_waves(p, p.D * BITS / 128, p.F / 16);
     const int ct = p.P > 12 * p.E && waves * ((p.P / p.E + 15) / 16) > kFit ? 2 : 1;
     if (p.base) {
-        if (which == 1) return expert_down<BITS, GS, SBF, true>(p, ct, st);
         if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, true>, true>(p, st);
         return ct == 1 ? expert_start<Tile<BITS, GS, 2, 1, 1, SBF, true>, true>(p, st)
                        : expert_start<Tile<BITS, GS, 2, 2, 1, SBF, true>, true>(p, st);
     }
-    if (which == 1) return expert_down<BITS, GS, SBF, false>(p, ct, st);
     if (xf32) return expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, true>(p, st);
     return expert_start<Tile<BITS, GS, 2, 1, 1, SBF, false>, true>(p, st);
 }

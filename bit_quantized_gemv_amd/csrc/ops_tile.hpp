@@ -99,15 +99,6 @@ __device__ __forceinline__ void split3(float v, uint32_t& h, uint32_t& m, uint32
     l = f32_bits(r - bits_f32(m));
 }
 
-__device__ __forceinline__ uint16_t to_bf16(float f);
-
-// An fp32 value as two bf16 values, rounded to nearest: off by 2^-17 of it at most.
-__device__ __forceinline__ void split2(float v, uint32_t& h, uint32_t& m)
-{
-    h = (uint32_t)to_bf16(v) << 16;
-    m = (uint32_t)to_bf16(v - bits_f32(h)) << 16;
-}
-
 // round to nearest even; NaN stays NaN
 __device__ __forceinline__ uint16_t to_bf16(float f)
 {

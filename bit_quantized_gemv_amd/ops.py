@@ -110,8 +110,8 @@ def experts(x, weights, ids, gate_up, down, *, bits: int, group_size: int, out=N
     outside [0, E) is an empty slot; gate_up: (codes [E][2F][D*bits/32], scales, biases
     [E][2F][D/group_size]), F gate rows before F up rows; down: (codes
     [E][D][F*bits/32], scales, biases [E][D][F/group_size]); out, out_dtype: as
-    `affine`.  Everything between is fp32 (hidden values are held to 2^-17 for bf16
-    outputs); each token is bit-identical to a call with that token alone.
+    `affine`.  Everything between is fp32 and y is rounded once; each token is
+    bit-identical to a call with that token alone.
     """
     f = (_py or _binding()).experts
     args = (x, weights, ids, *gate_up, *down, bits, group_size, out, out_dtype)

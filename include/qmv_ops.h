@@ -97,9 +97,8 @@ int qmv_route(const void* x, const void* router, float* weights, int32_t* ids, v
  * Experts: y[t] = sum_j weights[t][j] * Down_e ( silu(Gate_e x[t]) * Up_e x[t] ),
  * e = ids[t][j], summed in the order of j; a slot whose id is outside
  * [0, n_experts) adds nothing (its weight is not read), and a token with no
- * other slots gets zeros.  Gate_e x, Up_e x and the experts' outputs are held in
- * fp32; so are the hidden values, in two bf16 pieces (off by 2^-17 at most) where
- * y is bf16.
+ * other slots gets zeros.  Gate_e x, Up_e x, the hidden values and the experts'
+ * outputs are held in fp32, and y is rounded once.
  *   w13 [n_experts][2F][D*bits/32]: F gate rows, then F up rows; s13, b13
  *   [n_experts][2F][D/gs]; w2 [n_experts][D][F*bits/32]; s2, b2
  *   [n_experts][D][F/gs]; x [T][D]; y [T][D]
