@@ -11,9 +11,10 @@
 // 11.3 us.  32 requests of 8 rows of 131072 in bf16: 14.5-15.3 us, 67 MB at 4.5 TB/s, which
 // is a large copy's rate, and 21.6.
 //
-// Precision.  An accept decision compares one number with one border, so the
-// rows' sums may be off by 2^-20: the first pass takes fp32 exponentials, which
-// is what lets it keep up with the read.  A sampled token is where a prefix sum
+// Precision.  An accept decision compares one number with one border.  The first
+// pass takes fp32 exponentials, which is what lets it keep up with the read, and
+// its sums are off by 2^-20 at most: that decides all but about one number in 2^17, and
+// for those the row is summed in fp64.  A sampled token is where a prefix sum
 // of up to 2^17 and more terms first passes a number: with fp32 exponentials
 // every one of those borders moves, and over a vocabulary about one request in a
 // thousand would get a neighbour of the token that the definition gives.  So the
@@ -443,7 +444,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
     __shared__ double sums[kMaxRows];
     __shared__ double space[2][4][kWaves];
     __shared__ PickSpace picks[2];
-    __shared__ int first_bad;
+    __shared__ int first_bad, first_close;
     __shared__ bool am_last;
     together(p.logits, p.draft, p.u, p.probs, p.temperature, p.lengths, p.stats, p.part, p.tickets, p.S, p.V, p.chunks, p.stretches,
              p.groups, p.l_batch, p.l_row, p.q_batch, p.q_row);
@@ -468,7 +469,10 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
             if (qb) q_at = load1<QF32>(qb + (size_t)tid * p.q_row * QSZ, x);
         }
     }
-    if (tid == 0) first_bad = len;
+    if (tid == 0) {
+        first_bad = len;
+        first_close = kNoIndex;
+    }
     const Stat* sb = p.stats + (size_t)b * (p.S + 1) * p.stretches;
     for (int j0 = wave; j0 <= len; j0 += 4 * kWaves) {
         Stat st[4];                                  // four rows' first spans at once
@@ -502,20 +506,51 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
         }
     }
     __syncthreads();
-    // the first position that is not accepted
-    if (tid < len) {
-        bool yes = false;
-        if (x >= 0 && x < p.V) {
-            const double uq = (double)u_at * (double)q_at;
-            if (greedy)
-                yes = x == ats[tid] && uq < 1.0;
-            else
-                yes = l_at > kNone && uq * sums[tid] < weight(l_at, tops[tid], rate);
+    // The first position that is not accepted.  One that is too close to call by the first pass's
+    // sum has its row summed in fp64 before it is called (about one in 2^17; 64 chunks of 2048
+    // values take 60 us).
+    bool called = false;
+    int n;
+    for (;;) {
+        if (tid < len) {
+            bool yes = false, close = false;
+            if (x >= 0 && x < p.V) {
+                const double uq = (double)u_at * (double)q_at;
+                if (greedy) {
+                    yes = x == ats[tid] && uq < 1.0;
+                } else if (l_at > kNone) {
+                    const double e = weight(l_at, tops[tid], rate), off = uq * sums[tid] - e;
+                    yes = off < 0.0;
+                    close = !called && __builtin_fabs(off) < 0x1p-19 * e;
+                }
+            }
+            if (!yes) atomicMin(&first_bad, tid);
+            if (close) atomicMin(&first_close, tid);
         }
-        if (!yes) atomicMin(&first_bad, tid);
+        __syncthreads();
+        const int j = first_close;
+        n = first_bad;
+        if (j > n) break;
+        double s = 0.0;
+        for (int c = 0; c < p.chunks; ++c) {
+            float v[kPer];
+            load_row<LF32>(v, lb + (size_t)j * p.l_row * LSZ, (long long)c * kChunk + tid * kPer, 16 / LSZ, p.V, kNone);
+#pragma unroll
+            for (int i = 0; i < kPer; ++i) s += weight(v[i], tops[j], rate);
+        }
+        s = wave_sum(s);
+        if (lane == 0) space[0][0][wave] = s;
+        __syncthreads();
+        if (tid == j) {
+            sums[j] = ((space[0][0][0] + space[0][0][1]) + space[0][0][2]) + space[0][0][3];
+            called = true;
+        }
+        if (tid == 0) {
+            first_bad = len;
+            first_close = kNoIndex;
+        }
+        __syncthreads();
     }
-    __syncthreads();
-    const int n = first_bad;
     const float top = tops[n];
     const bool sampled = !greedy && top > kNone, rest = sampled && n < len;
     if (!sampled && chunk != 0) return;

@@ -141,9 +141,9 @@ def verify(logits, draft, uniforms, *, draft_probs=None, temperature=None, lengt
     Position j < lengths[b] is accepted while uniforms[b][j] * q(x_j) < p(x_j).  The first
     that is not gets a token sampled from max(p - q, 0) (from p if nothing is left of it); if
     all are accepted, the position after them gets one sampled from p.  Samples
-    are the lowest index whose prefix sum passes uniforms[b][lengths[b]] times the total, in
-    fp64; the sums behind an accept decision are within 2^-20 of their value.  NaN and -inf logits have probability 0; a row with nothing else rejects its
-    position and gives the token -1.
+    are the lowest index whose prefix sum passes uniforms[b][lengths[b]] times the total.  All
+    decisions are those of fp64 sums.  NaN and -inf logits have probability 0; a row with nothing
+    else rejects its position and gives the token -1.
 
     tokens: int32 [B][S+1], the accepted tokens, the sampled one, then -1; accepted: int32 [B].
     """

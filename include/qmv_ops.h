@@ -131,8 +131,8 @@ int qmv_moe(const void* x, const void* router, const uint32_t* w13, const void* 
  *   accepted, position n is given one sampled from p_n.
  * A sample is the lowest index whose inclusive prefix sum passes
  * uniforms[b][n] times the total (the last index of positive weight if none
- * does).  Samples are taken in fp64; the sums behind an accept decision are
- * within 2^-20 of their value.  temperature[b] not above 0 is greedy: p_j is 1
+ * does).  Probabilities, accept decisions and samples are those of fp64 sums of
+ * the logits as they are given.  temperature[b] not above 0 is greedy: p_j is 1
  * at the largest logit (ties to the lowest index).  NaN and -inf logits have
  * probability 0; where the largest is +inf, the ones equal to it share 1.  A
  * row with no other logits rejects its position, and a token sampled from it

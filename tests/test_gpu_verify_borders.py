@@ -93,6 +93,30 @@ def test_large_logits(dt, scale):
 
 
 @pytest.mark.parametrize("side", [1, -1])
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_numbers_next_to_a_probability(side, dt):
+    """A token is accepted while u < p: u is p in fp32, off by 2^-30 of it at most, above or below, at every position."""
+    B, S, V, n, N = 64, 5, 4096, 20, 1 << 18
+    live = (2 * torch.randn(N, n, generator=gen(8))).to(TORCH[dt])
+    e = torch.exp(live.double())
+    p = e / e.sum(1, keepdim=True)
+    at = p.argmax(1, keepdim=True)
+    off = ((p.gather(1, at).float().double() / p.gather(1, at) - 1) * side).squeeze(1)
+    rows = torch.nonzero((off > 2.0 ** -40) & (off < 2.0 ** -30)).squeeze(1)[:B * S]
+    assert len(rows) == B * S
+    l = torch.full((B, S + 1, V), -torch.inf, dtype=TORCH[dt])
+    l[:, :S, :200 * n:200] = live[rows].reshape(B, S, n)
+    l[:, S, 0] = 0.0
+    draft = (200 * at[rows]).reshape(B, S).int()
+    u = torch.cat([p[rows].gather(1, at[rows]).float().reshape(B, S), torch.full((B, 1), 0.5)], 1)
+    _, k = check(l, draft, u, None)
+    assert (k == (0 if side > 0 else S)).all()
+    u[:, 0] = 0.0                                     # the first of them later
+    u[::2, 1] = 0.0
+    check(l, draft, u, None)
+
+
+@pytest.mark.parametrize("side", [1, -1])
 def test_zero_takes_the_first_value_left(side):
     """u = 0 gives the lowest index of a positive weight, however small.  The first 2048 values have one that is not
     masked, and the drafter's probability of it, in fp32, is the target's but for 2^-30 of it, above or below."""
