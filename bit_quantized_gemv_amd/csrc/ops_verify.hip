@@ -13,8 +13,8 @@
 //
 // Precision.  An accept decision compares one number with one border.  The first
 // pass takes fp32 exponentials, which is what lets it keep up with the read, and
-// its sums are off by 2^-20 at most: that decides all but about one number in 2^17, and
-// for those the row is summed in fp64.  A sampled token is where a prefix sum
+// its sums are off by less than 2^-19: that decides all but one number in 2^18, and
+// for that the row is summed in fp64.  A sampled token is where a prefix sum
 // of up to 2^17 and more terms first passes a number: with fp32 exponentials
 // every one of those borders moves, and over a vocabulary about one request in a
 // thousand would get a neighbour of the token that the definition gives.  So the
@@ -244,6 +244,11 @@ __device__ __forceinline__ int length_of(const VerifyParams& p, int b)
 // The rest of the rate would shift all terms one way; to first order it adds ln 2 *
 // (rate / hi - 1) * sum(e t).  Whatever is below 2^-200 of the largest, masks among
 // it, is 0 there, and finite: no term of a sum is infinite or NaN.
+//
+// How far a lane's sum of at most 256 values can be off, in units of 2^-20 of it: 0.42 for
+// t's roundings (2^-23 |t| ln 2 of a term, and the terms' mean |t| is 4.8 at most), 0.67 for
+// chains of 64 additions, 0.3 for the factors between spans, 0.13 for the exponentials.
+// (Observed: 0.2.)
 template <bool LF32>
 __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
 {
@@ -507,8 +512,8 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
     }
     __syncthreads();
     // The first position that is not accepted.  One that is too close to call by the first pass's
-    // sum has its row summed in fp64 before it is called (about one in 2^17; 64 chunks of 2048
-    // values take 60 us).
+    // sum has its row summed in fp64 before it is called (one in 2^18; 64 chunks of 2048 values
+    // take 60 us).
     bool called = false;
     int n;
     for (;;) {
@@ -587,7 +592,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
                     mine.e += e[i];
                     mine.q += q[i];
                 }
-                if (__builtin_fabs(d) <= 0x1p-20 * e[i]) mine.near += e[i];
+                if (__builtin_fabs(d) <= 0x1p-19 * e[i]) mine.near += e[i];
             }
             mine.p = wave_sum(mine.p);
             if (rest) {
@@ -656,7 +661,7 @@ __global__ __launch_bounds__(kThreads) void sample_kernel(VerifyParams p)
         t = all_of(t);
         const double Z = t.p, left = t.e - Z * t.q;
         bool use = rest && left > 0.0;
-        // the border's values could move the sums by 2^-33 of them, or are all that is left before a number this small
+        // the border's values could move the sums by 2^-32 of them, or are all that is left before a number this small
         if (rest && (t.near * 0x1p13 > left || t.near > (double)u_last * left)) {
             double all = 0.0;
             for (int c = 0; c < p.chunks; ++c) {
