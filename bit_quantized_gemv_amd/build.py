@@ -1,12 +1,16 @@
 """Build the gfx950 HIP library libqmv.so in-tree (hipcc, one object per
 kernel-instance unit, compiled in parallel, then linked), and the torch binding
-qmv_ops_py.so beside it (g++)."""
+qmv_ops_py.so beside it (g++).  The library needs hipcc alone: without torch, g++ or
+Python's headers it is built without the binding, and so are the C ABI's users served."""
 from __future__ import annotations
 
 import concurrent.futures as cf
+import importlib.util
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 PKG = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(PKG)
@@ -44,8 +48,17 @@ def _run(cmd, what: str) -> None:
         raise RuntimeError(what)
 
 
+def _binding_lacks() -> str | None:
+    """What the binding's build would need and is not here."""
+    if importlib.util.find_spec("torch") is None:
+        return "torch"
+    if shutil.which("g++") is None:
+        return "g++"
+    header = os.path.join(sysconfig.get_paths()["include"], "Python.h")
+    return None if os.path.exists(header) else header
+
+
 def _compile_binding() -> str:
-    import sysconfig
     import torch
     obj = os.path.join(BUILD, "ops_py.o")
     inc = os.path.join(os.path.dirname(torch.__file__), "include")
@@ -69,15 +82,18 @@ def build(jobs: int | None = None) -> str:
     os.makedirs(BUILD, exist_ok=True)
     os.makedirs(LIBDIR, exist_ok=True)
     jobs = jobs or min(8, os.cpu_count() or 1)
+    lacks = _binding_lacks()
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:
-        binding = ex.submit(_compile_binding)
+        binding = None if lacks else ex.submit(_compile_binding)
         objs = list(ex.map(_compile, sources()))
-        binding = binding.result()
     tmp = LIB + ".tmp"
     cmd = [HIPCC, "--offload-arch=gfx950", "-shared", "-fPIC", "-o", tmp, *objs]
     _run(cmd, "link of libqmv.so failed")
     os.replace(tmp, LIB)
-    _link_binding(binding)
+    if lacks:
+        sys.stderr.write(f"{os.path.basename(PY)} is not built (no {lacks}): the calls of ops.py need it\n")
+    else:
+        _link_binding(binding.result())
     return LIB
 
 
