@@ -149,6 +149,10 @@ Tensor output(PyObject* out, PyObject* dtype, at::IntArrayRef shape, c10::Device
     return y;
 }
 
+// Sizes outside the limits are the C ABI's to refuse, by name: what has no memory then, an
+// empty tensor or scratch memory of no size, is not passed as a missing pointer.  It is not read.
+alignas(256) char g_nothing[256];
+
 struct Scratch {
     c10::DataPtr at;
     long long size;
@@ -156,7 +160,11 @@ struct Scratch {
     {
         if (n > 0) at = c10::hip::HIPCachingAllocator::get()->allocate((size_t)n);
     }
+    void* get() const { return at ? at.get() : g_nothing; }
 };
+
+const void* data(const Tensor& t) { return t.numel() > 0 ? t.const_data_ptr() : g_nothing; }
+void* data_out(Tensor& t) { return t.numel() > 0 ? t.mutable_data_ptr() : g_nothing; }
 
 void* stream_of(c10::Device dev) { return c10::hip::getCurrentHIPStream(dev.index()).stream(); }
 
@@ -171,10 +179,10 @@ void check_status(int status, const char* where)
     throw python_error();
 }
 
-const float* floats(const Tensor* t) { return t ? static_cast<const float*>(t->const_data_ptr()) : nullptr; }
+const float* floats(const Tensor* t) { return t ? static_cast<const float*>(data(*t)) : nullptr; }
 const float* floats(const Tensor& t) { return floats(&t); }
-const int32_t* ints(const Tensor& t) { return static_cast<const int32_t*>(t.const_data_ptr()); }
-const uint32_t* words(const Tensor& t) { return static_cast<const uint32_t*>(t.const_data_ptr()); }
+const int32_t* ints(const Tensor& t) { return static_cast<const int32_t*>(data(t)); }
+const uint32_t* words(const Tensor& t) { return static_cast<const uint32_t*>(data(t)); }
 int size32(int64_t v, const char* name)
 {
     TORCH_CHECK_VALUE(v <= INT32_MAX, name, " = ", v, " is too large");
@@ -234,8 +242,8 @@ PyObject* affine_lora(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (M > 0) {
         const int m = size32(M, "M"), k = size32(K, "K"), r = size32(R, "the rank");
         Scratch ws(qmv_affine_lora_workspace(m, k, r));
-        check_status(qmv_affine_lora(words(w), s.const_data_ptr(), b.const_data_ptr(), x.const_data_ptr(), y.mutable_data_ptr(),
-                                     la.const_data_ptr(), lb.const_data_ptr(), ints(ids), floats(scaling), ws.at.get(), ws.size, m,
+        check_status(qmv_affine_lora(words(w), data(s), data(b), data(x), data_out(y),
+                                     data(la), data(lb), ints(ids), floats(scaling), ws.get(), ws.size, m,
                                      size32(N, "N"), k, (int)bits, (int)gs, size32(L, "the adapters"), r, dt_of(x), dt_of(s),
                                      dt_of(y), dt_of(la), stream_of(d.dev)),
                      "qmv_affine_lora");
@@ -303,8 +311,8 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (T > 0) {
         const int t = size32(T, "T"), dd = size32(D, "D"), e = size32(E, "E");
         Scratch ws(qmv_route_workspace(t, dd, e));
-        check_status(qmv_route(x.const_data_ptr(), router.const_data_ptr(), static_cast<float*>(weights.mutable_data_ptr()),
-                               static_cast<int32_t*>(ids.mutable_data_ptr()), ws.at.get(), ws.size, t, dd, e, (int)k,
+        check_status(qmv_route(data(x), data(router), static_cast<float*>(data_out(weights)),
+                               static_cast<int32_t*>(data_out(ids)), ws.get(), ws.size, t, dd, e, (int)k,
                                PyObject_IsTrue(a[3]), dt_of(x), dt_of(router), stream_of(d.dev)),
                      "qmv_route");
     }
@@ -338,9 +346,9 @@ PyObject* experts(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (T > 0) {
         const int t = size32(T, "T"), dd = size32(D, "D"), f = size32(ex.F, "F"), kk = size32(k, "top_k");
         Scratch ws(qmv_experts_workspace(t, dd, f, kk));
-        check_status(qmv_experts(x.const_data_ptr(), floats(weights), ints(ids), words(*ex.w13), ex.s13->const_data_ptr(),
-                                 ex.b13->const_data_ptr(), words(*ex.w2), ex.s2->const_data_ptr(), ex.b2->const_data_ptr(),
-                                 y.mutable_data_ptr(), ws.at.get(), ws.size, t, dd, f, size32(ex.E, "E"), kk, (int)bits, (int)gs,
+        check_status(qmv_experts(data(x), floats(weights), ints(ids), words(*ex.w13), data(*ex.s13),
+                                 data(*ex.b13), words(*ex.w2), data(*ex.s2), data(*ex.b2),
+                                 data_out(y), ws.get(), ws.size, t, dd, f, size32(ex.E, "E"), kk, (int)bits, (int)gs,
                                  dt_of(x), dt_of(*ex.s13), dt_of(y), stream_of(d.dev)),
                      "qmv_experts");
     }
@@ -368,10 +376,10 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n)
     if (T > 0) {
         const int t = size32(T, "T"), dd = size32(D, "D"), f = size32(ex.F, "F"), e = size32(E, "E");
         Scratch ws(qmv_moe_workspace(t, dd, f, e, (int)k));
-        check_status(qmv_moe(x.const_data_ptr(), router.const_data_ptr(), words(*ex.w13), ex.s13->const_data_ptr(),
-                             ex.b13->const_data_ptr(), words(*ex.w2), ex.s2->const_data_ptr(), ex.b2->const_data_ptr(),
-                             y.mutable_data_ptr(), static_cast<float*>(weights.mutable_data_ptr()),
-                             static_cast<int32_t*>(ids.mutable_data_ptr()), ws.at.get(), ws.size, t, dd, f, e, (int)k,
+        check_status(qmv_moe(data(x), data(router), words(*ex.w13), data(*ex.s13),
+                             data(*ex.b13), words(*ex.w2), data(*ex.s2), data(*ex.b2),
+                             data_out(y), static_cast<float*>(data_out(weights)),
+                             static_cast<int32_t*>(data_out(ids)), ws.get(), ws.size, t, dd, f, e, (int)k,
                              PyObject_IsTrue(a[9]), (int)bits, (int)gs, dt_of(x), dt_of(router), dt_of(*ex.s13), dt_of(y),
                              stream_of(d.dev)),
                      "qmv_moe");
@@ -424,9 +432,9 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n)
         if (S == 0) q = nullptr;
         const int b = size32(B, "B"), s = size32(S, "S"), v = size32(V, "V");
         Scratch ws(qmv_verify_workspace(b, s, v));
-        check_status(qmv_verify(logits.const_data_ptr(), ints(draft), floats(u), q ? q->const_data_ptr() : nullptr, floats(temp),
-                                len ? ints(*len) : nullptr, static_cast<int32_t*>(tokens.mutable_data_ptr()),
-                                static_cast<int32_t*>(accepted.mutable_data_ptr()), ws.at.get(), ws.size, b, s, v,
+        check_status(qmv_verify(data(logits), ints(draft), floats(u), q ? data(*q) : nullptr, floats(temp),
+                                len ? ints(*len) : nullptr, static_cast<int32_t*>(data_out(tokens)),
+                                static_cast<int32_t*>(data_out(accepted)), ws.get(), ws.size, b, s, v,
                                 logits.stride(0), logits.stride(1), q ? q->stride(0) : 0, q ? q->stride(1) : 0, dt_of(logits),
                                 q ? dt_of(*q) : QMV_DT_F32, stream_of(d.dev)),
                      "qmv_verify");
