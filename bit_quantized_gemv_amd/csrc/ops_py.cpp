@@ -48,6 +48,13 @@ int64_t integer(PyObject* o, const char* name)
     return v;
 }
 
+bool truth(PyObject* o)
+{
+    const int v = PyObject_IsTrue(o);
+    if (v < 0) throw python_error();        // it raised
+    return v != 0;
+}
+
 // ---- checks ---------------------------------------------------------------
 
 std::string dtype_name(ScalarType t)
@@ -301,6 +308,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
     need_args(n, 4);
     const Tensor &x = tensor(a[0], "x"), &router = tensor(a[1], "router");
     const int64_t k = integer(a[2], "top_k");
+    const bool renorm = truth(a[3]);
     need_tokens(x);
     const int64_t T = x.size(0), D = x.size(1), E = need_router(x, router, k);
     Device d;
@@ -313,7 +321,7 @@ PyObject* route(PyObject*, PyObject* const* a, Py_ssize_t n)
         Scratch ws(qmv_route_workspace(t, dd, e));
         check_status(qmv_route(data(x), data(router), static_cast<float*>(data_out(weights)),
                                static_cast<int32_t*>(data_out(ids)), ws.get(), ws.size, t, dd, e, (int)k,
-                               PyObject_IsTrue(a[3]), dt_of(x), dt_of(router), stream_of(d.dev)),
+                               renorm, dt_of(x), dt_of(router), stream_of(d.dev)),
                      "qmv_route");
     }
     return wrap({weights, ids});
@@ -363,6 +371,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n)
     need_args(n, 14);
     const Tensor &x = tensor(a[0], "x"), &router = tensor(a[1], "router");
     const int64_t k = integer(a[8], "top_k"), bits = integer(a[10], "bits"), gs = integer(a[11], "group_size");
+    const bool renorm = truth(a[9]);
     need_tokens(x);
     const int64_t T = x.size(0), D = x.size(1), E = need_router(x, router, k);
     const Experts ex(a + 2, E, D, bits, gs);
@@ -380,7 +389,7 @@ PyObject* moe(PyObject*, PyObject* const* a, Py_ssize_t n)
                              data(*ex.b13), words(*ex.w2), data(*ex.s2), data(*ex.b2),
                              data_out(y), static_cast<float*>(data_out(weights)),
                              static_cast<int32_t*>(data_out(ids)), ws.get(), ws.size, t, dd, f, e, (int)k,
-                             PyObject_IsTrue(a[9]), (int)bits, (int)gs, dt_of(x), dt_of(router), dt_of(*ex.s13), dt_of(y),
+                             renorm, (int)bits, (int)gs, dt_of(x), dt_of(router), dt_of(*ex.s13), dt_of(y),
                              stream_of(d.dev)),
                      "qmv_moe");
     }
