@@ -281,11 +281,14 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(VerifyParams p)
             if (i + 1 < spans) load_raw<LF32>(next, l, i0 + (long long)(i + 1) * kSpan, 64 * PER, p.V, kNone);
 #pragma unroll
             for (int d = 0; d < NV; ++d) unpack<LF32>(v + d * PER, w[d]);
-            // the median of a value, the largest so far and +inf is the larger of the first two, and passes NaN over
+            // a maximum passes quiet NaNs over, and would take a signalling one for its result
             const float old = mine;
             float t4[4] = {mine, mine, mine, mine};
 #pragma unroll
-            for (int d = 0; d < kSpanPer; ++d) t4[d & 3] = __builtin_amdgcn_fmed3f(v[d], t4[d & 3], __builtin_huge_valf());
+            for (int d = 0; d < kSpanPer; d += 2) {
+                float& t = t4[(d >> 1) & 3];
+                t = __builtin_fmaxf(__builtin_fmaxf(t, __builtin_canonicalizef(v[d])), __builtin_canonicalizef(v[d + 1]));
+            }
             mine = __builtin_fmaxf(__builtin_fmaxf(t4[0], t4[1]), __builtin_fmaxf(t4[2], t4[3]));
             if (i > 0) {
                 const float up = __builtin_fmaxf((old - mine) * hi, kLeast), f = __builtin_amdgcn_exp2f(up);

@@ -150,3 +150,16 @@ def test_numbers_below_zero_take_the_first_value(first):
     l[..., :first] = -torch.inf
     t, _ = q.verify(l.to(DEV), torch.zeros(4, 0, dtype=torch.int32, device=DEV), torch.full((4, 1), -0.5, device=DEV))
     assert t[:, 0].tolist() == [first] * 4
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_signalling_nan(dt):
+    """NaNs of every bit pattern have probability 0 and hide nothing beside them."""
+    l, draft, u, probs = masked(16, 2, 5001, dt, -1e4, False, seed=77)
+    bits = l.view(torch.int16 if dt == "bf16" else torch.int32)
+    patterns = [0x7f81, -127, 0x7fff, 0x7fc0] if dt == "bf16" else [0x7f800001, -(0x7fffff - 1), 0x7fffffff, 0x7fc00000]
+    for k, pattern in enumerate(patterns):
+        bits[k::4, :, k::7] = pattern
+    assert l.isnan().float().mean() > 0.1
+    check(l, draft, u, probs, temp=torch.linspace(0.0, 1.5, 16))
+    check(l, draft, u, None)
