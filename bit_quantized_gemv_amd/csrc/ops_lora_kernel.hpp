@@ -88,8 +88,10 @@ struct LoraSpace {
 // first: the first slabs of codes and activations, and by way of the list of
 // adapters the first of their factors and the hidden values, which go to LDS.  The
 // adapters' terms follow the product, their factors streaming through a ring of
-// registers that the product has left.  15360 x 3840, one token, rank 16: 13.8 us,
-// 34 MB at 2.5 TB/s, most of it the start and end of a wave.  17408 x 5120, 64 tokens
+// registers that the product has left.  15360 x 3840, one token, rank 16: 13.4 us,
+// 34 MB at 2.5 TB/s: 1.6 us before a wave's first load, 3.0 until it is there, 5.0 of
+// products, 2.0 of the adapters, join and store, and 2-3 between the first wave's start and
+// the last one's.  (qmv_affine's kernel, without adapters, takes 8.2 over this matrix.)  17408 x 5120, 64 tokens
 // of 32 adapters, rank 64: 81 us, 140 TFLOP/s, 134 MB, bound by the decoding of codes
 // beside the matrix instructions, the 71 MB of factors, and a second round of 32
 // workgroups behind the 512 that fit.
@@ -377,7 +379,10 @@ int lora_scales(const LoraParams& p, bool sbf, hipStream_t st)
     return sbf ? lora_start<Tile<BITS, GS, RT, CT, NP, true, true>>(p, st) : lora_start<Tile<BITS, GS, RT, CT, NP, false, true>>(p, st);
 }
 
-// Token tiles per wave: as many as asked for and the registers hold.
+// Token tiles per wave: as many as asked for and the registers hold.  Some of the rarer
+// instances spill: 67 registers of two row tiles of 2-bit codes in groups of 64 and fp32
+// activations (64 tokens, 15360 x 3840: 79 us, 58 in groups of 128, which do not), 33 of two
+// token tiles of such codes and bf16, 16 to 24 of two token tiles of 4-bit codes and fp32.
 template <int BITS, int GS>
 int lora_pick(const LoraParams& p, int rt, int ct, bool xf32, bool sbf, hipStream_t st)
 {

@@ -366,8 +366,8 @@ int run_route(const char* x, const void* router, float* weights, int32_t* ids, v
 // Pairs are sorted by expert where an expert meets eight or more on average and the
 // products are not small.  Below that a wave's 16 rows are mostly repeats of a few,
 // which cost it little, and sorting is a launch of about 5 us (128 tokens over 32
-// experts of 3840 x 1920, 16 pairs each: 181 us sorted against 236; 64 tokens over 4 of
-// 512 x 512, 32 pairs each: 27.6 against 22.8; over 4 of 1024 x 512, 30.0, 29.7).
+// experts of 3840 x 1920, 16 pairs each: 157 us sorted against 247; 64 tokens over 4 of
+// 512 x 512, 32 pairs each: 27.7 against 23.6; over 4 of 1024 x 512, 30.2, 31.2).
 bool sorted(int n, int k, int E, int D, int F)
 {
     return (long long)n * k >= 8LL * E && (k > kTokenSlots || (long long)n * k * D * F > 1 << 25);

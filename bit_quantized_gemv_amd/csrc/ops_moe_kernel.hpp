@@ -8,10 +8,10 @@
 // activations lie in the order of the lanes (FRAG): gathered row by row, each of a
 // wave's activation loads would look up a cache line per lane.
 //
-// 13 tokens over 128 experts of 2048 x 1024, 8 each: gate and up 46 us, 168 MB at 3.6
-// TB/s; down 35 us, 84 MB at 2.4, whose rows are eight slabs: a wave is mostly its
+// 13 tokens over 128 experts of 2048 x 1024, 8 each: gate and up 46 us, 159 MB at 3.5
+// TB/s; down 42 us, 84 MB at 2.0, whose rows are eight slabs: a wave is mostly its
 // start and end.  128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit: 69 us, 219
-// TFLOP/s, and 61 us, 124 (two planes of hidden values: twice the matrix
+// TFLOP/s, and 75 us, 101 (three planes of hidden values: three times the matrix
 // instructions), bound by the decoding of codes beside the matrix instructions.
 #pragma once
 #include <algorithm>
@@ -226,8 +226,8 @@ __global__ __launch_bounds__(kMaxWaves* kWave, T::WAVES) void expert_kernel(Expe
 }
 
 // Parts of a row's K: with many experts there are waves enough, and a wave of few slabs
-// is mostly its start and end (13 tokens over 128 experts 108 us with two parts of 8
-// and of 4 slabs, 98 with one).
+// is mostly its start and end (13 tokens over 128 experts 106 us with two parts of 8
+// and of 4 slabs, 104 with one).
 inline int expert_parts(int chunks)
 {
     const int n = slabs_of(chunks);
@@ -252,8 +252,8 @@ int expert_start(const ExpertParams& p, hipStream_t st)
     q.meta = Meta(32 * q.groups, K, T::BITS, T::GS, parts);
     // Where the rows alone are fewer waves than fit at once, workgroups share an expert's
     // pairs (as many as twice the average asks for, since experts differ): 128 tokens
-    // over 4 experts of 512 x 512, 2 each: 53.5 us without, 28.5 with; of 2048 x 1024,
-    // 89.0, 48.4; over 16 of 1024 x 768, 4 each: 54.1, 43.3.
+    // over 4 experts of 512 x 512, 2 each: 58.8 us without, 28.6 with; of 2048 x 1024,
+    // 102.8, 48.9; over 16 of 1024 x 768, 4 each: 58.7, 45.0.
     q.takers = std::max(1, std::min(kFit / expert_waves(p, K / (4 * T::VPW), N / ROWS), (2 * p.P / p.E + 16 * T::CT - 1) / (16 * T::CT)));
     const ExpertSpace sp(q.meta, q.groups * parts, 32 * q.groups, p.P);
     const void* fn = reinterpret_cast<const void*>(&expert_kernel<T, GATE>);
@@ -269,7 +269,7 @@ int expert_start(const ExpertParams& p, hipStream_t st)
 // and 32 rows per workgroup: neither the experts' outputs are written nor another
 // launch adds them up, but an expert that two tokens chose is read for each.  The sums
 // are those of the two launches, bit for bit.  One token, 6 experts of 3840 x 1024:
-// 10.5 us for 13.3 MB, of which 3 are the launch and its arguments.
+// 12.4 us for 13.3 MB, of which 3 are the launch and its arguments.
 constexpr int kTokenSlots = kMaxWaves;
 
 inline int token_bytes(const Meta& meta, int k) { return k * (2048 + 2 * Join<1>::kWords * 4 + meta.bytes(32)); }
@@ -328,10 +328,10 @@ __global__ __launch_bounds__(kTokenSlots* kWave, T::WAVES) void token_kernel(Exp
 
 // Whole tokens where their slots fit the waves, a row of w2 is one wave's, and what is
 // read again for experts that tokens share costs less than a launch.  Whole layers, us,
-// by expert and by token: 1 token over 64 experts of 3840 x 1024, 6 each: 35.2, 32.3;
-// 2 tokens: 43.4, 37.0; 8: 89.6, 92.2.  4 experts of 4096 x 2048, 2 each: 4 tokens
-// 38.9, 37.5; 7: 39.8, 41.5.  16 experts of 512 x 512, 4 each, 16 tokens: 23.8, 19.6.
-// 2-bit, 16 experts of 5120 x 768, 8 each: 2 tokens 55.8, 54.3; 6: 61.6, 73.5.
+// by expert and by token: 1 token over 64 experts of 3840 x 1024, 6 each: 36.1, 34.1;
+// 2 tokens: 43.7, 38.1; 8: 92.5, 96.9.  4 experts of 4096 x 2048, 2 each: 1 token 37.7,
+// 33.5; 4: 41.4, 42.4; 7: 42.5, 44.8.  16 experts of 512 x 512, 4 each, 16 tokens: 26.1,
+// 21.1.  2-bit, 16 experts of 5120 x 768, 8 each: 2 tokens 66.8, 62.5; 6: 74.3, 85.5.
 inline bool by_token(int n, int k, int D, int F, int bits)
 {
     return k <= kTokenSlots && expert_parts(F * bits / 128) == 1 && (n == 1 || (long long)n * k * D * F <= 1 << 26);
@@ -362,7 +362,7 @@ int expert_pick(int which, const ExpertParams& p, bool xf32, hipStream_t st)
                       : expert_start<Tile<BITS, GS, 2, 1, 3, SBF, false>, false>(p, st);
     // Two token tiles per wave for sorted pairs of more than 12 per expert, where waves of
     // one each do not fit at once: 128 tokens over 32 experts of 3840 x 1920, 4 each, 2-bit,
-    // whole layers: 152 us with two in the gate and up products, 177 with one.
+    // whole layers: 156 us with two in the gate and up products, 172 with one; 4-bit 203, 199.
     const int waves = expert_waves(p, p.D * BITS / 128, p.F / 16);
     const int ct = p.P > 12 * p.E && waves * ((p.P / p.E + 15) / 16) > kFit ? 2 : 1;
     if (p.base) {

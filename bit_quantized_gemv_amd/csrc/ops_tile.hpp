@@ -51,7 +51,7 @@
 // the smaller count of the two ways in.
 //
 // What bounds it: with one token, the read of the codes and the start and end of a
-// workgroup (15360 x 3840 in 13.8 us, of which the codes and scales are 6.8 at the
+// workgroup (15360 x 3840 in 13.4 us, of which the codes and scales are 6.8 at the
 // rate of a large copy); from about 32 tokens the vector instructions of decoding and
 // folding beside the matrix instructions.
 #pragma once

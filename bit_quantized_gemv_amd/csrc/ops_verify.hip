@@ -7,9 +7,9 @@
 // accept decisions, and adds up the weights of its chunk of the one row that is
 // sampled; the last to finish turns the chunks' sums into the token.  Bound by
 // the read of the logits where there are many, by the chain of dependent loads
-// of the second launch where there are few.  One request of 5 rows of 131072: 3.4 and
-// 11.3 us.  32 requests of 8 rows of 131072 in bf16: 14.5-15.3 us, 67 MB at 4.5 TB/s, which
-// is a large copy's rate, and 21.6.
+// of the second launch where there are few.  One request of 5 rows of 131072: 3.6 and
+// 11.4 us.  32 requests of 8 rows of 131072 in bf16: 15.2 us, 67 MB at 4.4 TB/s, nearly a
+// large copy's rate, and 21.6.
 //
 // Precision.  An accept decision compares one number with one border.  The first
 // pass takes fp32 exponentials, which is what lets it keep up with the read, and

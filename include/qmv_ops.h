@@ -48,7 +48,7 @@ extern "C" {
 enum {
     QMV_E_RANK = 11,      /* adapter rank not in [1, QMV_MAX_RANK], or no adapters */
     QMV_E_EXPERTS = 12,   /* experts not in [1, QMV_MAX_EXPERTS], or top_k not in
-                             [1, min(experts, QMV_MAX_TOP_K)] */
+                             [1, QMV_MAX_TOP_K], or above a router's experts */
     QMV_E_WORKSPACE = 13, /* the workspace is smaller than the call needs */
     QMV_E_VOCAB = 14,     /* vocabulary, draft length or batch outside the limits */
     QMV_E_STRIDE = 15     /* a stride is negative or above 2^40 */
