@@ -15,10 +15,13 @@
 #include <torch/csrc/Exceptions.h>
 #include <torch/csrc/autograd/python_variable.h>
 
+#include <algorithm>
+#include <cmath>
 #include <optional>
 #include <string>
 #include <vector>
 
+#include "qmv_attn.h"
 #include "qmv_ops.h"
 
 namespace {
@@ -44,6 +47,16 @@ int64_t integer(PyObject* o, const char* name)
     if (v == -1 && PyErr_Occurred()) {
         PyErr_Clear();
         TORCH_CHECK_TYPE(false, name, " must be an integer");
+    }
+    return v;
+}
+
+double number(PyObject* o, const char* name)
+{
+    const double v = PyFloat_AsDouble(o);
+    if (v == -1.0 && PyErr_Occurred()) {
+        PyErr_Clear();
+        TORCH_CHECK_TYPE(false, name, " must be a number");
     }
     return v;
 }
@@ -452,6 +465,251 @@ PyObject* verify(PyObject*, PyObject* const* a, Py_ssize_t n)
     END_HANDLE_TH_ERRORS
 }
 
+// ---- norms, rotation and the cache ----------------------------------------
+
+// [T][heads][D], values of a head contiguous, at any stride otherwise
+void need_heads(const Tensor& t, const char* name, int64_t T, int64_t D)
+{
+    TORCH_CHECK_VALUE(t.dim() == 3 && (T < 0 || t.size(0) == T) && (D < 0 || t.size(2) == D), name, " must be [", T < 0 ? "T" : std::to_string(T),
+                      "][heads][", D < 0 ? "D" : std::to_string(D), "], got ", t.sizes());
+    TORCH_CHECK_VALUE(t.numel() == 0 || t.size(2) == 1 || t.stride(2) == 1, name, ": the values of a head must be contiguous");
+}
+
+ScalarType half_dtype(PyObject* dtype)
+{
+    if (dtype == Py_None) return at::kBFloat16;
+    TORCH_CHECK_TYPE(THPDtype_Check(dtype), "out_dtype must be a torch dtype");
+    const ScalarType t = reinterpret_cast<THPDtype*>(dtype)->scalar_type;
+    TORCH_CHECK_TYPE(t == at::kBFloat16 || t == at::kHalf, "out_dtype must be bfloat16 or float16, got ", dtype_name(t));
+    return t;
+}
+
+// freqs, positions, axes, q_weight, k_weight, eps, interleaved at a
+struct Rotation {
+    const Tensor *freqs, *positions, *axes, *qw, *kw;
+    qmv_rotation r{};
+    Rotation(PyObject* const* a, int64_t T, int64_t D)
+        : freqs(optional_tensor(a[0], "freqs")), positions(optional_tensor(a[1], "positions")), axes(optional_tensor(a[2], "axes")),
+          qw(optional_tensor(a[3], "q_weight")), kw(optional_tensor(a[4], "k_weight"))
+    {
+        const double eps = number(a[5], "eps");
+        TORCH_CHECK_VALUE(eps >= 0.0 && std::isfinite(eps), "eps must be a finite number of 0 or more, got ", eps);
+        r.eps = (float)eps;
+        r.interleaved = truth(a[6]);
+        r.n_axes = 1;
+        int64_t half = 0;
+        if (freqs) {
+            need_dtype(*freqs, "freqs", at::kFloat);
+            TORCH_CHECK_VALUE(freqs->dim() == 1, "freqs must be [rotated / 2]");
+            half = freqs->size(0);
+            TORCH_CHECK_VALUE(2 * half <= D && half % 4 == 0, "freqs: ", half, " pairs; a multiple of 4 and at most ", D / 2, " can be rotated");
+        }
+        r.rot = (int)(2 * half);
+        if (positions) {
+            need_dtype(*positions, "positions", at::kInt);
+            TORCH_CHECK_VALUE((positions->dim() == 1 || positions->dim() == 2) && positions->size(-1) == T, "positions must be [", T, "] or [axes][", T,
+                              "], got ", positions->sizes());
+            if (positions->dim() == 2) {
+                TORCH_CHECK_VALUE(positions->size(0) >= 1 && positions->size(0) <= QMV_MAX_AXES, "positions: from 1 to ", QMV_MAX_AXES, " axes, got ",
+                                  positions->size(0));
+                r.n_axes = (int)positions->size(0);
+                r.positions_row = r.n_axes > 1 ? positions->stride(0) : 0;
+            }
+            TORCH_CHECK_VALUE(T <= 1 || positions->stride(-1) == 1, "positions: those of an axis must be contiguous");
+        }
+        if (axes) {
+            need_dtype(*axes, "axes", at::kInt);
+            need_shape(*axes, "axes", {half});
+        } else {
+            TORCH_CHECK_VALUE(r.n_axes == 1, "positions of ", r.n_axes, " axes need axes, which tells each pair's");
+        }
+        for (const Tensor* w : {qw, kw}) {
+            if (!w) continue;
+            const char* name = w == qw ? "q_weight" : "k_weight";
+            need_dtype(*w, name, at::kBFloat16, at::kFloat);
+            need_shape(*w, name, {D});
+            r.w_dt = dt_of(*w);
+        }
+        TORCH_CHECK_TYPE(!qw || !kw || qw->scalar_type() == kw->scalar_type(), "q_weight and k_weight must share a dtype");
+    }
+    void place(Device& d)
+    {
+        if (freqs) d.whole(*freqs, "freqs");
+        if (positions) d.add(*positions, "positions");
+        if (axes) d.whole(*axes, "axes");
+        if (qw) d.whole(*qw, "q_weight");
+        if (kw) d.whole(*kw, "k_weight");
+        r.freqs = floats(freqs);
+        r.positions = positions ? ints(*positions) : nullptr;
+        r.axes = axes ? ints(*axes) : nullptr;
+        r.q_weight = qw ? data(*qw) : nullptr;
+        r.k_weight = kw ? data(*kw) : nullptr;
+    }
+};
+
+// k_cache, v_cache, pages, starts, lengths at a
+struct Pages {
+    const Tensor *k, *v, *pages, *starts, *lengths;
+    qmv_cache c{};
+    explicit Pages(PyObject* const* a)
+        : k(&tensor(a[0], "k_cache")), v(&tensor(a[1], "v_cache")), pages(&tensor(a[2], "pages")), starts(&tensor(a[3], "starts")),
+          lengths(&tensor(a[4], "lengths"))
+    {
+        need_dtype(*k, "k_cache", at::kBFloat16, at::kHalf);
+        TORCH_CHECK_TYPE(v->scalar_type() == k->scalar_type(), "k_cache and v_cache must share a dtype");
+        TORCH_CHECK_VALUE(k->dim() == 4, "k_cache must be [pages][page_size][heads][D], got ", k->sizes());
+        need_shape(*v, "v_cache", k->sizes());
+        need_dtype(*pages, "pages", at::kInt);
+        need_dtype(*starts, "starts", at::kInt);
+        need_dtype(*lengths, "lengths", at::kInt);
+        TORCH_CHECK_VALUE(pages->dim() == 2, "pages must be [sequences][pages of each], got ", pages->sizes());
+        const int64_t B = pages->size(0);
+        need_shape(*lengths, "lengths", {B});
+        need_shape(*starts, "starts", {B + 1});
+        for (const Tensor* t : {k, v})
+            TORCH_CHECK_VALUE(t->size(3) <= 1 || t->stride(3) == 1, t == k ? "k_cache" : "v_cache", ": the values of a head must be contiguous");
+        TORCH_CHECK_VALUE(pages->size(1) <= 1 || pages->stride(1) == 1, "pages: a sequence's pages must be contiguous");
+        c.n_pages = size32(k->size(0), "the pages");
+        c.page_size = size32(k->size(1), "page_size");
+        c.heads = size32(k->size(2), "the heads");
+        c.head_size = size32(k->size(3), "D");
+        c.n_seqs = size32(B, "the sequences");
+        c.max_pages = size32(pages->size(1), "the pages of a sequence");
+        c.k_page = step(*k, 0);
+        c.k_slot = step(*k, 1);
+        c.k_head = step(*k, 2);
+        c.v_page = step(*v, 0);
+        c.v_slot = step(*v, 1);
+        c.v_head = step(*v, 2);
+        c.pages_row = step(*pages, 0);
+        c.dt = dt_of(*k);
+    }
+    // the stride of an axis; of one place it says nothing
+    static int64_t step(const Tensor& t, int64_t axis) { return t.size(axis) <= 1 ? 0 : t.stride(axis); }
+    void place(Device& d)
+    {
+        d.add(*k, "k_cache");
+        d.add(*v, "v_cache");
+        d.add(*pages, "pages");
+        d.whole(*starts, "starts");
+        d.whole(*lengths, "lengths");
+        c.k = const_cast<void*>(data(*k));
+        c.v = const_cast<void*>(data(*v));
+        c.pages = ints(*pages);
+        c.starts = ints(*starts);
+        c.lengths = ints(*lengths);
+    }
+};
+
+int64_t step3(const Tensor& t, int64_t axis) { return Pages::step(t, axis); }
+
+// q, k, freqs, positions, axes, q_weight, k_weight, eps, interleaved, out_dtype
+PyObject* rotate(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    need_args(n, 10);
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k");
+    need_dtype(q, "q", at::kBFloat16, at::kFloat);
+    TORCH_CHECK_TYPE(k.scalar_type() == q.scalar_type(), "q and k must share a dtype");
+    need_heads(q, "q", -1, -1);
+    const int64_t T = q.size(0), D = q.size(2);
+    need_heads(k, "k", T, D);
+    Rotation rot(a + 2, T, D);
+    TORCH_CHECK_VALUE(rot.r.rot == 0 || rot.positions, "positions are missing");
+    const ScalarType kind = half_dtype(a[9]);
+    Device d;
+    d.add(q, "q");
+    d.add(k, "k");
+    rot.place(d);
+    const c10::DeviceGuard guard(d.dev);
+    Tensor yq = fresh({T, q.size(1), D}, kind, d.dev), yk = fresh({T, k.size(1), D}, kind, d.dev);
+    if (T > 0)
+        check_status(qmv_rotate(&rot.r, data(q), data(k), data_out(yq), data_out(yk), size32(T, "T"), size32(q.size(1), "the heads"),
+                                size32(k.size(1), "the heads"), size32(D, "D"), step3(q, 0), step3(q, 1), step3(k, 0), step3(k, 1), dt_of(q),
+                                dt_of(kind), stream_of(d.dev)),
+                     "qmv_rotate");
+    return wrap({yq, yk});
+    END_HANDLE_TH_ERRORS
+}
+
+// q, k, v, freqs, positions, axes, q_weight, k_weight, eps, interleaved, k_cache, v_cache, pages, starts, lengths, out
+PyObject* append(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    need_args(n, 16);
+    const Tensor &q = tensor(a[0], "q"), &k = tensor(a[1], "k"), &v = tensor(a[2], "v");
+    Pages pages(a + 10);
+    need_dtype(q, "q", at::kBFloat16, at::kFloat);
+    TORCH_CHECK_TYPE(k.scalar_type() == q.scalar_type() && v.scalar_type() == q.scalar_type(), "q, k and v must share a dtype");
+    const int64_t D = pages.k->size(3), H = pages.k->size(2);
+    need_heads(q, "q", -1, D);
+    const int64_t T = q.size(0);
+    need_heads(k, "k", T, D);
+    need_heads(v, "v", T, D);
+    TORCH_CHECK_VALUE(k.size(1) == H && v.size(1) == H, "k and v have ", k.size(1), " and ", v.size(1), " heads, the cache ", H);
+    Rotation rot(a + 3, T, D);
+    Device d;
+    d.add(q, "q");
+    d.add(k, "k");
+    d.add(v, "v");
+    pages.place(d);
+    rot.place(d);
+    const c10::DeviceGuard guard(d.dev);
+    Tensor y;
+    const int64_t shape[] = {T, q.size(1), D};
+    if (a[15] == Py_None) {
+        y = fresh(shape, pages.k->scalar_type(), d.dev);
+    } else {
+        y = tensor(a[15], "out");
+        TORCH_CHECK_VALUE(y.device() == d.dev && y.is_contiguous() && y.sizes() == at::IntArrayRef(shape), "out must be a contiguous ",
+                          at::IntArrayRef(shape), " tensor on the inputs' device");
+        need_dtype(y, "out", pages.k->scalar_type());
+    }
+    if (T > 0 && pages.c.n_seqs > 0)
+        check_status(qmv_append(&rot.r, &pages.c, data(q), data(k), data(v), data_out(y), size32(T, "T"), size32(q.size(1), "the heads"),
+                                step3(q, 0), step3(q, 1), step3(k, 0), step3(k, 1), step3(v, 0), step3(v, 1), dt_of(q), stream_of(d.dev)),
+                     "qmv_append");
+    return wrap(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
+// q, k_cache, v_cache, pages, starts, lengths, window, sinks, scale, max_new, max_length, out, out_dtype
+PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n)
+{
+    HANDLE_TH_ERRORS
+    need_args(n, 13);
+    const Tensor& q = tensor(a[0], "q");
+    Pages pages(a + 1);
+    need_dtype(q, "q", pages.k->scalar_type());
+    const int64_t D = pages.k->size(3);
+    need_heads(q, "q", -1, D);
+    const int64_t T = q.size(0), Hq = q.size(1);
+    const int64_t window = a[6] == Py_None ? 0 : integer(a[6], "window"), sinks = integer(a[7], "sinks");
+    TORCH_CHECK_VALUE(window >= 0 && sinks >= 0, "window and sinks must be 0 or more, got ", window, " and ", sinks);
+    const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)std::max<int64_t>(D, 1)) : number(a[8], "scale");
+    TORCH_CHECK_VALUE(std::isfinite(scale), "scale must be finite, got ", scale);
+    const int64_t max_new = a[9] == Py_None ? T : integer(a[9], "max_new");
+    const int64_t places = (int64_t)pages.c.max_pages * pages.c.page_size;
+    const int64_t max_length = a[10] == Py_None ? places : integer(a[10], "max_length");
+    TORCH_CHECK_VALUE(max_new >= 0 && max_length >= 0, "max_new and max_length must be 0 or more, got ", max_new, " and ", max_length);
+    Device d;
+    d.add(q, "q");
+    pages.place(d);
+    const c10::DeviceGuard guard(d.dev);
+    Tensor y = output(a[11], a[12], {T, Hq, D}, d.dev);
+    if (T > 0 && pages.c.n_seqs > 0 && max_new > 0) {
+        const int t = size32(T, "T"), hq = size32(Hq, "the heads");
+        const int w = (int)std::min<int64_t>(window, INT32_MAX), s = (int)std::min<int64_t>(sinks, INT32_MAX);
+        const int mn = (int)std::min<int64_t>(max_new, T), ml = (int)std::min<int64_t>(max_length, INT32_MAX);
+        Scratch ws(qmv_attend_workspace(&pages.c, t, hq, mn, ml, w, s));
+        check_status(qmv_attend(&pages.c, data(q), data_out(y), ws.get(), ws.size, t, hq, step3(q, 0), step3(q, 1), mn, ml, w, s, (float)scale,
+                                dt_of(y), stream_of(d.dev)),
+                     "qmv_attend");
+    }
+    return wrap(std::move(y));
+    END_HANDLE_TH_ERRORS
+}
+
 // the exception type that a status other than QMV_OK raises
 PyObject* set_error(PyObject*, PyObject* type)
 {
@@ -468,7 +726,8 @@ PyMethodDef method(const char* name)
 }
 
 PyMethodDef g_methods[] = {method<affine_lora>("affine_lora"), method<route>("route"), method<experts>("experts"),
-                           method<moe>("moe"), method<verify>("verify"), {"set_error", set_error, METH_O, nullptr},
+                           method<moe>("moe"), method<verify>("verify"), method<rotate>("rotate"), method<append>("append"),
+                           method<attend>("attend"), {"set_error", set_error, METH_O, nullptr},
                            {nullptr, nullptr, 0, nullptr}};
 
 PyModuleDef g_module = {PyModuleDef_HEAD_INIT, "qmv_ops_py", nullptr, -1, g_methods, nullptr, nullptr, nullptr, nullptr};

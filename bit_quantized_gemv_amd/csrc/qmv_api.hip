@@ -11,6 +11,7 @@
 #include <mutex>
 
 #include "qmv.h"
+#include "qmv_attn.h"
 #include "qmv_ops.h"
 #include "qmv_dispatch.hpp"
 
@@ -674,6 +675,8 @@ const char* qmv_status_string(int status)
     case QMV_E_WORKSPACE: return "QMV_E_WORKSPACE";
     case QMV_E_VOCAB: return "QMV_E_VOCAB";
     case QMV_E_STRIDE: return "QMV_E_STRIDE";
+    case QMV_E_HEADS: return "QMV_E_HEADS";
+    case QMV_E_CACHE: return "QMV_E_CACHE";
     default: return "QMV_E_UNKNOWN";
     }
 }

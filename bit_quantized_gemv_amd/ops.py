@@ -1,5 +1,7 @@
-"""The operators beside the quantized product (include/qmv_ops.h): the adapted
-projection, the mixture-of-experts layer and the verification of drafted tokens.
+"""The operators beside the quantized product: the adapted projection, the
+mixture-of-experts layer and the verification of drafted tokens (include/qmv_ops.h);
+norms and rotation of queries and keys, a cache in pages and attention over it
+(include/qmv_attn.h).
 
 Each is one call of the compiled binding (csrc/ops_py.cpp), which checks the
 arguments, allocates outputs and scratch memory on the stream that the call runs
@@ -19,6 +21,21 @@ _lib = None
 _py = None
 
 
+class Cache(ctypes.Structure):
+    """qmv_cache, for calls with raw pointers."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("k", "v")] + \
+               [(n, ctypes.c_longlong) for n in ("k_page", "k_slot", "k_head", "v_page", "v_slot", "v_head")] + \
+               [(n, ctypes.c_void_p) for n in ("pages", "starts", "lengths")] + [("pages_row", ctypes.c_longlong)] + \
+               [(n, ctypes.c_int) for n in ("n_pages", "page_size", "n_seqs", "max_pages", "heads", "head_size", "dt")]
+
+
+class Rotation(ctypes.Structure):
+    """qmv_rotation, for calls with raw pointers."""
+    _fields_ = [(n, ctypes.c_void_p) for n in ("freqs", "positions", "axes", "q_weight", "k_weight")] + \
+               [("positions_row", ctypes.c_longlong), ("eps", ctypes.c_float)] + \
+               [(n, ctypes.c_int) for n in ("rot", "n_axes", "interleaved", "w_dt")]
+
+
 def _load():
     """The C ABI, for calls with raw pointers."""
     global _lib
@@ -36,6 +53,13 @@ def _load():
                         ("qmv_moe_workspace", 5), ("qmv_verify_workspace", 3)):
             f = getattr(L, name)
             f.argtypes, f.restype = [I] * n, Q
+        R, C = ctypes.POINTER(Rotation), ctypes.POINTER(Cache)
+        for name, args, r in (("qmv_rotate", [R] + [P] * 4 + [I] * 4 + [Q] * 4 + [I] * 2 + [P], I),
+                              ("qmv_append", [R, C] + [P] * 4 + [I] * 2 + [Q] * 6 + [I, P], I),
+                              ("qmv_attend_workspace", [C] + [I] * 6, Q),
+                              ("qmv_attend", [C] + [P] * 3 + [Q] + [I] * 2 + [Q] * 2 + [I] * 4 + [ctypes.c_float, I, P], I)):
+            f = getattr(L, name)
+            f.argtypes, f.restype = args, r
         _lib = L
     return _lib
 
@@ -150,3 +174,58 @@ def verify(logits, draft, uniforms, *, draft_probs=None, temperature=None, lengt
     f = (_py or _binding()).verify
     args = (logits, draft, uniforms, draft_probs, temperature, lengths)
     return f(*args) if stream is None else _on(stream, f, args, *args)
+
+
+def rotate(q, k, freqs, positions, *, axes=None, q_weight=None, k_weight=None, eps: float = 1e-6,
+           interleaved: bool = False, out_dtype=None, stream=None):
+    """(q, k) with each head normed and turned to its token's position.
+
+    q: bf16 or fp32 [T][heads][D], k: the same with its own heads, each head's values
+    contiguous, at any stride (views of one projection's output) that is a multiple of 8;
+    D a multiple of 8 up to 256.  q_weight, k_weight: bf16 or fp32 [D], the weights of
+    x / sqrt(mean(x^2) + eps), None for no norm.  freqs: fp32 [R / 2], R <= D a multiple
+    of 8: pair i is turned by positions * freqs[i], computed in fp64 (None: no rotation).  A
+    pair is the values i and i + R / 2, or 2i and 2i + 1 if `interleaved`; values from R on
+    stay.  positions: int32 [T], or [A][T] for A axes (time, height, width), where axes, int32
+    [R / 2], tells each pair's axis (outside [0, A): not turned).  Outputs: out_dtype,
+    bf16 (default) or fp16, rounded once.
+    """
+    f = (_py or _binding()).rotate
+    args = (q, k, freqs, positions, axes, q_weight, k_weight, eps, interleaved, out_dtype)
+    return f(*args) if stream is None else _on(stream, f, args[:7], *args)
+
+
+def append(q, k, v, freqs, k_cache, v_cache, pages, starts, lengths, *, positions=None, axes=None, q_weight=None,
+           k_weight=None, eps: float = 1e-6, interleaved: bool = False, out=None, stream=None):
+    """`rotate` for the new tokens of a cache's sequences: returns q, and writes keys and
+    values to their places in the cache.
+
+    k_cache, v_cache: bf16 or fp16 [pages][page_size][heads][D] in any order of strides;
+    pages: int32 [B][n], place j of sequence b is slot j % page_size of page
+    pages[b][j // page_size] (a page outside the cache holds nothing); starts: int32 [B + 1],
+    tokens starts[b] .. starts[b + 1] - 1 are sequence b's new ones; lengths: int32 [B], its
+    places with them.  positions: default each token's place; the rest as `rotate`.  The
+    returned q has the cache's dtype.  Rows of tokens that are in no sequence are left as they
+    were; places below 0 or outside the table are not written.
+    """
+    f = (_py or _binding()).append
+    args = (q, k, v, freqs, positions, axes, q_weight, k_weight, eps, interleaved, k_cache, v_cache, pages, starts, lengths, out)
+    return f(*args) if stream is None else _on(stream, f, args[:8] + args[10:], *args)
+
+
+def attend(q, k_cache, v_cache, pages, starts, lengths, *, window: int = 0, sinks: int = 0, scale=None, max_new=None,
+           max_length=None, out=None, out_dtype=None, stream=None):
+    """[T][heads][D]: attention of each sequence's new tokens over its places in the cache.
+
+    q: the cache's dtype, [T][heads][D] at any stride that is a multiple of 8, heads a
+    multiple of the cache's; k_cache .. lengths: as `append`.  New token i of sequence b is
+    its place p = lengths[b] - (new tokens of b) + i, and sees place j if j <= p and, with a
+    window, j > p - window or j < sinks.  A token that sees nothing gets zeros; what a token
+    does not see does not touch its output, NaN included.  scale: default 1 / sqrt(D).
+    max_new, max_length: how many new tokens and places a sequence has at most, where the
+    program knows; defaults T and what the table holds (the bounds set the launch's size, and
+    what is above them is left out).  out, out_dtype: as `affine`, bf16 or fp32.
+    """
+    f = (_py or _binding()).attend
+    args = (q, k_cache, v_cache, pages, starts, lengths, window, sinks, scale, max_new, max_length, out, out_dtype)
+    return f(*args) if stream is None else _on(stream, f, args[:6] + (out,), *args)

@@ -1,0 +1,274 @@
+"""qmv_attend against a plain 64-bit form."""
+import math
+
+import pytest
+import torch
+
+import bit_quantized_gemv_amd as q
+from attn_util import DEV, TORCH, Batch, attend64, check_attend, gen
+
+pytestmark = pytest.mark.gpu
+
+
+def queries(c, Hq, seed=1, more=0, size=2.0):
+    return (size * torch.randn(c.T + more, Hq, c.D, generator=gen(seed))).to(TORCH[c.dt])
+
+
+def run(c, qs, **kw):
+    return q.attend(qs.to(DEV), *c.on(), **kw)
+
+
+def check(c, Hq, out="bf16", seed=1, window=0, sinks=0, scale=None, **kw):
+    qs = queries(c, Hq, seed)
+    got = run(c, qs, window=window, sinks=sinks, scale=scale, out_dtype=TORCH[out], **kw)
+    check_attend(got, *attend64(qs, c, window, sinks, scale), c.dt, out, f"{c.new} {c.lengths}")
+    return qs, got
+
+
+# head sizes, groups of heads, page sizes, orders, types
+SHAPES = [(64, 2, 1, 16, "page", "bf16", "bf16"), (128, 2, 4, 16, "page", "bf16", "f32"), (256, 1, 2, 32, "head", "f16", "f32"),
+          (80, 2, 5, 17, "one", "f16", "bf16"), (8, 1, 1, 1, "page", "bf16", "f32"), (96, 3, 3, 5, "head", "bf16", "bf16"),
+          (200, 1, 16, 64, "page", "bf16", "bf16"), (136, 2, 7, 100, "one", "f16", "f32"), (24, 4, 8, 3, "page", "f16", "bf16")]
+# new tokens and lengths: one token; verify blocks; blocks that begin a sequence; chunks; all of them
+BATCHES = [([1], [1]), ([1], [300]), ([13], [13]), ([5, 1, 16], [700, 2, 40]), ([33], [33]), ([70, 1, 0, 17], [331, 129, 9, 530])]
+
+
+@pytest.mark.parametrize("new,lengths", BATCHES)
+@pytest.mark.parametrize("D,H,G,P,order,dt,out", SHAPES)
+def test_shapes(D, H, G, P, order, dt, out, new, lengths):
+    check(Batch(new, lengths, H, D, P, dt, seed=D + P, order=order), H * G, out)
+
+
+@pytest.mark.parametrize("length", [1, 2, 15, 16, 17, 63, 64, 65, 127, 128, 129, 255, 256, 257, 511, 512, 513, 1025, 2048, 2049, 4100])
+@pytest.mark.parametrize("D", [64, 128, 256])
+def test_lengths(length, D):
+    n = min(length, 3)
+    check(Batch([n], [length], 1, D, 16, seed=length), 2, "f32")
+
+
+@pytest.mark.parametrize("n", [1, 2, 15, 16, 17, 31, 32, 33, 64, 65, 127, 128, 129, 200])
+@pytest.mark.parametrize("G", [1, 3, 8])
+def test_new_tokens(n, G):
+    check(Batch([n, 1], [n + 90, 5], 1, 64, 16, seed=n), G)
+
+
+@pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (64, 4), (100, 70), (300, 300), (5000, 3), (7, 600)])
+@pytest.mark.parametrize("new,lengths", [([1], [900]), ([13, 1], [1300, 20]), ([150, 40], [700, 40])])
+@pytest.mark.parametrize("D", [64, 128])
+def test_windows(window, sinks, new, lengths, D):
+    check(Batch(new, lengths, 2, D, 16, seed=window), 4, "f32", window=window, sinks=sinks)
+
+
+def test_long_window():
+    """Blocks far apart: the first tokens and the last of a long sequence."""
+    check(Batch([4], [9000], 1, 64, 16, seed=1), 2, "f32", window=700, sinks=5)
+    check(Batch([40], [9000], 1, 128, 64, seed=2), 2, "bf16", window=500, sinks=300)
+
+
+@pytest.mark.parametrize("scale", [0.0, 1.0, -0.3])
+def test_scale(scale):
+    check(Batch([3, 20], [100, 60], 2, 64, 16), 4, "f32", scale=scale)
+
+
+def test_large_logits():
+    """Weights that all but one key have lost, in every block of keys."""
+    c = Batch([3, 30], [600, 333], 1, 128, 16, seed=3)
+    qs = queries(c, 2, size=60.0)
+    out, reach = attend64(qs, c)
+    got = run(c, qs, out_dtype=torch.float32).cpu().double()
+    # logits of several hundred: an fp32 sum of 128 products is off by up to 2^-17 of their size
+    assert ((got - out).abs() <= 2.0 ** -17 * 128 * 60 * 3 / 128 ** 0.5 * reach.amax(-1, keepdim=True) + 2.0 ** -15 * reach).all()
+
+
+def test_nothing_to_see():
+    """Tokens at places below 0, sequences of no places, pages that hold nothing: zeros."""
+    c = Batch([5, 2, 20], [3, 0, 11], 2, 64, 4, seed=4)
+    qs, got = check(c, 4)
+    assert not got[:2].any() and not got[5:7].any() and not got[7:16].any()
+    c = Batch([2, 30], [7, 40], 2, 64, 4, seed=5)
+    c.pages[:] = -1
+    assert not run(c, queries(c, 4)).any()
+
+
+@pytest.mark.parametrize("bad", [-1, 10 ** 6, -2 ** 31, 2 ** 31 - 1])
+def test_bad_pages(bad):
+    """A page outside the cache holds nothing."""
+    for new in (2, 50):
+        c = Batch([new, 1], [333, 90], 2, 64, 8, seed=6)
+        for b, i in ((0, 0), (0, 7), (0, 20), (0, 41), (1, 3)):
+            c.pages[b, i] = bad
+        check(c, 4, "f32")
+
+
+def test_lengths_beyond_the_table():
+    c = Batch([2, 40], [64, 64], 2, 64, 16, seed=7)
+    qs = queries(c, 2)
+    k, v, pages, starts, lens = c.on()
+    lens.fill_(2 ** 30)
+    check_attend(q.attend(qs.to(DEV), k, v, pages, starts, lens), *attend64(qs, c), "bf16", "bf16")
+    # max_length below them: the same as sequences of that length
+    c.lengths = [50, 50]
+    check_attend(q.attend(qs.to(DEV), k, v, pages, starts, lens, max_length=50), *attend64(qs, c), "bf16", "bf16")
+
+
+def test_starts_out_of_order():
+    """Starts outside the tokens and going back: what lies in a sequence is computed, nothing else is touched."""
+    c = Batch([4, 3], [30, 30], 1, 64, 16, seed=8)
+    qs = queries(c, 2).to(DEV)
+    k, v, pages, _, lens = c.on()
+    for s in ([0, 7, 3], [-5, 4, 100], [7, 7, 7], [2 ** 31 - 1, -2 ** 31, 5]):
+        out = torch.full((7, 2, 64), 3.0, device=DEV)
+        q.attend(qs, k, v, pages, torch.tensor(s, dtype=torch.int32, device=DEV), lens, out=out)
+        torch.cuda.synchronize()
+        if s == [7, 7, 7]:
+            assert (out == 3).all()
+
+
+def test_rows_behind_and_above():
+    """Tokens behind the last sequence, and above max_new, are left as they were."""
+    c = Batch([3, 9], [50, 70], 2, 64, 16, seed=9)
+    qs = queries(c, 4, more=5)
+    want, reach = attend64(qs, c)
+    out = torch.full((17, 4, 64), 8.0, device=DEV)
+    q.attend(qs.to(DEV), *c.on(), out=out)
+    check_attend(out[:12], want[:12], reach[:12], "bf16", "f32")
+    assert (out[12:] == 8).all()
+    out.fill_(8.0)
+    q.attend(qs.to(DEV), *c.on(), out=out, max_new=4)
+    check_attend(out[:7], want[:7], reach[:7], "bf16", "f32")
+    assert (out[7:] == 8).all()
+
+
+@pytest.mark.parametrize("new", [3, 13, 90])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (64, 5)])
+@pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
+def test_hidden_values(new, window, sinks, junk):
+    """What a token does not see does not touch its output: the same bits with NaN or infinities there."""
+    c = Batch([new], [400], 2, 128, 16, seed=10, fill=0.0)
+    qs = queries(c, 4)
+    clean = run(c, qs, window=window, sinks=sinks, out_dtype=torch.float32)
+    places = [400 - new // 2 - 1]                      # the second half of the new tokens sees it
+    if window:
+        places += [400 - new - 30, 9]                  # the first tokens see it, or none
+    for j in places:
+        c.k[c.row(0, j)] = junk
+        c.v[c.row(0, j)] = junk
+    got = run(c, qs, window=window, sinks=sinks, out_dtype=torch.float32)
+    for i in range(new):
+        p = 400 - new + i
+        sees = any(j <= p and (not window or j > p - window or j < sinks) for j in places)
+        if not sees:
+            assert torch.equal(got[i], clean[i]), i
+        elif junk != -math.inf:
+            assert not torch.isfinite(got[i]).any(), i
+
+
+@pytest.mark.parametrize("D,dt", [(64, "bf16"), (128, "f16"), (256, "bf16"), (80, "f16")])
+@pytest.mark.parametrize("window", [0, 200])
+def test_blocks_as_single_tokens(D, dt, window):
+    """Up to 16 new tokens of a sequence get the bits that calls of one token get, whatever else is in the call."""
+    length, n = 2700, 13
+    c = Batch([n, 16], [length, 300], 2, D, 16, dt, seed=11)
+    qs = queries(c, 6).to(DEV)
+    k, v, pages, starts, lens = c.on()
+    kw = dict(window=window, sinks=3 if window else 0)
+    whole = q.attend(qs, k, v, pages, starts, lens, out_dtype=torch.float32, **kw)
+    one = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    for i in range(n):
+        got = q.attend(qs[i:i + 1], k, v, pages[:1], one, lens[:1] - (n - 1 - i), out_dtype=torch.float32, **kw)
+        assert torch.equal(got[0], whole[i]), i
+    many = 40                                         # many sequences: other launch shapes
+    rep = q.attend(qs[:n].repeat(many, 1, 1), k, v, pages[:1].repeat(many, 1), torch.arange(many + 1, dtype=torch.int32, device=DEV) * n,
+                   lens[:1].repeat(many), max_new=n, out_dtype=torch.float32, **kw)
+    assert torch.equal(rep.reshape(many, n, 6, D), whole[:n].expand(many, n, 6, D))
+    again = q.attend(qs, k, v, pages, starts, lens, out_dtype=torch.float32, max_new=16, max_length=length, **kw)
+    assert torch.equal(again, whole)
+
+
+def test_chunks_repeat():
+    """The same call again gives the same bits."""
+    c = Batch([300, 2, 77], [900, 50, 77], 2, 128, 16, seed=12)
+    qs = queries(c, 8)
+    a, b = run(c, qs), run(c, qs)
+    assert torch.equal(a, b)
+
+
+def test_strided_queries():
+    c = Batch([4, 30], [60, 90], 2, 64, 16, seed=13)
+    qs = queries(c, 4)
+    big = torch.randn(c.T, 10, 64).bfloat16().to(DEV)
+    big[:, 3:7] = qs.to(DEV)
+    assert torch.equal(q.attend(big[:, 3:7], *c.on()), run(c, qs))
+    turned = qs.to(DEV).transpose(0, 1).contiguous().transpose(0, 1)
+    assert torch.equal(q.attend(turned, *c.on()), run(c, qs))
+
+
+def test_shared_pages():
+    """Sequences of a common beginning may hold it once, and a page may be in one's table twice."""
+    c = Batch([2, 2], [64, 64], 2, 64, 16, seed=14)
+    c.pages[1, :2] = c.pages[0, :2]
+    c.pages[0, 3] = c.pages[0, 2]
+    check(c, 4, "f32")
+
+
+def test_wide_table():
+    """A slice of a wider table, with more pages than the sequences have."""
+    c = Batch([3, 1], [70, 500], 2, 64, 16, seed=15, wide=50)
+    qs = queries(c, 4)
+    k, v, pages, starts, lens = c.on()
+    wide = torch.full((2, 200), 10 ** 6, dtype=torch.int32, device=DEV)
+    wide[:, 7:7 + pages.shape[1]] = pages
+    got = q.attend(qs.to(DEV), k, v, wide[:, 7:7 + pages.shape[1]], starts, lens)
+    check_attend(got, *attend64(qs, c), "bf16", "bf16")
+
+
+def test_far_pages():
+    """Pages whose offsets pass 32 bits, in elements and bytes."""
+    D, P, H = 128, 16, 1
+    n_pages = 2 ** 32 // (P * D) + 40                 # 8 GiB of keys, of which a few pages are used
+    k = torch.empty(n_pages, P, H, D, dtype=torch.bfloat16, device=DEV)
+    v = torch.empty(n_pages, P, H, D, dtype=torch.bfloat16, device=DEV)
+    for new, length in ((2, 100), (40, 100)):
+        c = Batch([new], [length], H, D, P, seed=16)
+        qs = queries(c, 2)
+        ids = torch.randperm(40, generator=gen(1))[:7] + n_pages - 40
+        for i in range(7):
+            k[ids[i]], v[ids[i]] = c.k[c.pages[0, i].long()].to(DEV), c.v[c.pages[0, i].long()].to(DEV)
+        got = q.attend(qs.to(DEV), k, v, ids.int().reshape(1, -1).to(DEV), c.starts.to(DEV), c.lens.to(DEV))
+        check_attend(got, *attend64(qs, c), "bf16", "bf16")
+
+
+def test_streams_and_graphs():
+    c = Batch([5, 30, 1], [300, 100, 1000], 2, 64, 16, seed=17)
+    qs = queries(c, 4).to(DEV)
+    args = c.on()
+    want = q.attend(qs, *args)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    got = q.attend(qs, *args, stream=s)
+    s.synchronize()
+    assert torch.equal(got, want)
+    outs, graphs = [torch.empty_like(want) for _ in range(2)], [torch.cuda.CUDAGraph() for _ in range(2)]
+    for o, gr in zip(outs, graphs):
+        with torch.cuda.graph(gr):
+            q.attend(qs, *args, out=o)
+    g = gen(3)
+    for i in range(4):
+        qs.copy_(torch.randn(qs.shape, generator=g).to(qs.dtype))
+        args[4].copy_(c.lens - i)
+        want = q.attend(qs, *args)
+        torch.cuda.synchronize()
+        for o, gr in zip(outs, graphs):
+            o.zero_()
+            gr.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(outs[0], want) and torch.equal(outs[1], want)
+
+
+def test_no_tokens():
+    z = lambda *s, dt=torch.bfloat16: torch.zeros(*s, dtype=dt, device=DEV)
+    i = lambda *s: z(*s, dt=torch.int32)
+    assert q.attend(z(0, 4, 64), z(3, 4, 2, 64), z(3, 4, 2, 64), i(1, 2), i(2), i(1)).shape == (0, 4, 64)
+    out = torch.full((3, 4, 64), 2.0, device=DEV)
+    q.attend(z(3, 4, 64), z(3, 4, 2, 64), z(3, 4, 2, 64), i(0, 2), i(1), i(0), out=out)
+    assert (out == 2).all()
