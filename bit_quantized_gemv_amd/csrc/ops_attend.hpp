@@ -1,0 +1,155 @@
+// ops_attend.hpp -- what the kernels of qmv_attend share.
+//
+// Layouts.  Scores are computed turned over, S^T = K Q^T, so that a lane of the 16 x 16
+// result holds four keys of one query row n = lane % 16 (key 4 (lane / 16) + i of a tile of
+// 16), and the outputs too, O^T = V^T P^T: four values of a head of the same row.  Maxima,
+// sums and factors of a row are then a lane's own numbers.  A step of the second product
+// takes 32 keys, two tiles of scores; in which order is free as long as both operands have the
+// same, and the order "four of the first tile, four of the second" for every group of 16
+// lanes is the one in which a lane holds its weights already.  The values of V^T that belong
+// to it are four neighbouring keys of one column: what the transposing read of LDS gives.
+//
+// V in LDS: blocks of 16 keys and 32 columns, 64 bytes a key, the four 16-byte pieces of key
+// j at piece ^ (j / 4): the transposing read of a 16 x 16 tile then meets every bank twice,
+// which its 512 bytes do at best.
+#pragma once
+#include <hip/hip_runtime.h>
+
+#include <cstdint>
+
+#include "ops_cache.hpp"
+
+namespace ops {
+
+typedef __attribute__((ext_vector_type(4))) uint32_t u32x4;
+typedef __attribute__((ext_vector_type(2))) uint32_t u32x2;
+typedef __attribute__((ext_vector_type(4))) float f32x4;
+typedef __attribute__((ext_vector_type(2))) float f32x2;
+typedef __attribute__((ext_vector_type(4))) short s16x4;
+typedef __attribute__((ext_vector_type(8))) __bf16 bf16x8;
+typedef __attribute__((ext_vector_type(2))) __bf16 bf16x2;
+typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
+typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
+typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
+
+constexpr int kBlockTokens = 16;      // up to so many new tokens a sequence is a block, above a chunk
+constexpr int kSuper = 8;             // leaves of a super (the two steps in which blocks of keys are joined)
+constexpr float kGone = -__builtin_huge_valf();
+
+struct AttendParams {
+    const char* q;
+    char* out;
+    float* part;                    // [token][head][slot][D]: sums of weights * values
+    f32x2* stat;                    // [token][head][slot]: largest score and sum of weights
+    long long q_token, q_head;      // bytes
+    int q_heads, heads, group, D;
+    int window, sinks, max_new, out_f32;
+    int slots, units, row_blocks, per_unit;
+    float scale;                    // times log2(e)
+    Cache cache;
+};
+
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c, __bf16)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a), __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mfma(u32x4 a, u32x4 b, f32x4 c, _Float16)
+{
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a), __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+}
+
+__device__ __forceinline__ uint32_t pack(float a, float b, __bf16) { return __builtin_bit_cast(uint32_t, bf16x2{(__bf16)a, (__bf16)b}); }
+__device__ __forceinline__ uint32_t pack(float a, float b, _Float16) { return __builtin_bit_cast(uint32_t, f16x2{(_Float16)a, (_Float16)b}); }
+__device__ __forceinline__ f32x2 unpack(uint32_t v, __bf16) { return __builtin_convertvector(__builtin_bit_cast(bf16x2, v), f32x2); }
+__device__ __forceinline__ f32x2 unpack(uint32_t v, _Float16) { return __builtin_convertvector(__builtin_bit_cast(f16x2, v), f32x2); }
+
+// the exponents of a value that is no number: infinities and NaN
+constexpr uint32_t no_number(__bf16) { return 0x7f80; }
+constexpr uint32_t no_number(_Float16) { return 0x7c00; }
+
+// the word with those of its two values gone that are no numbers
+template <class X>
+__device__ __forceinline__ uint32_t numbers(uint32_t w)
+{
+    constexpr uint32_t E = no_number(X());
+    const uint32_t lo = (w & E) == E ? 0 : w & 0xffff, hi = (w >> 16 & E) == E ? 0 : w & 0xffff0000;
+    return lo | hi;
+}
+
+// A barrier for LDS alone: loads from memory stay in flight over it.
+__device__ __forceinline__ void lds_only_barrier()
+{
+    __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+__device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+__device__ __forceinline__ u32x2 read_turned(const char* lds)
+{
+    typedef __attribute__((address_space(3))) s16x4* At;
+    return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(uintptr_t)(lds)));
+}
+
+// What the new tokens of a sequence see, between them: the places below `first` and those
+// from low to high, in units of U places, listed one after the other.
+struct Visible {
+    int first, low, high;         // high < 0: nothing
+    int front, start, units;      // units of the first places; the unit of `low` after them; all units
+    __device__ __forceinline__ int unit(int i) const { return i < front ? i : start + i - front; }
+    __device__ __forceinline__ bool meets(int from, int to) const { return from < first || (from <= high && to > low); }
+};
+
+// tokens: how many of the sequence's new tokens are computed
+__device__ __forceinline__ Visible visible(const Seq& s, int tokens, int window, int sinks, int U)
+{
+    Visible v;
+    const int place = s.length - s.count;      // of the first
+    v.high = place + tokens - 1;
+    v.low = window > 0 ? max(0, place - window + 1) : 0;
+    v.first = window > 0 ? min(sinks, v.low) : 0;
+    if (v.high < 0) {
+        v.front = v.start = v.units = 0;
+        return v;
+    }
+    v.front = (v.first + U - 1) / U;
+    v.start = max(v.low / U, v.front);
+    v.units = v.front + max(0, v.high / U - v.start + 1);
+    return v;
+}
+
+// One join of a row: the sums so far (m, l, o) and those of the next keys.  Weights go with
+// 2^(score - m); a side that has seen nothing (m = -inf) adds exact zeros.
+struct Factors {
+    float a, b;
+};
+__device__ __forceinline__ Factors join(float& m, float& l, float m2, float l2)
+{
+    const float top = __builtin_fmaxf(m, m2), at = top == kGone ? 0.0f : top;
+    const Factors f{exp2_of(m - at), exp2_of(m2 - at)};
+    m = top;
+    l = __builtin_fmaf(l2, f.b, l * f.a);
+    return f;
+}
+__device__ __forceinline__ f32x4 joined(f32x4 o, f32x4 o2, Factors f)
+{
+    return f32x4{__builtin_fmaf(o2.x, f.b, o.x * f.a), __builtin_fmaf(o2.y, f.b, o.y * f.a), __builtin_fmaf(o2.z, f.b, o.z * f.a),
+                 __builtin_fmaf(o2.w, f.b, o.w * f.a)};
+}
+
+// four values of a row's result; l = 0: the row has seen nothing
+__device__ __forceinline__ void put_result(const AttendParams& p, long long row, int d, f32x4 o, float l)
+{
+    const f32x4 y = l == 0.0f ? f32x4{0, 0, 0, 0} : o / l;
+    if (p.out_f32) *reinterpret_cast<f32x4*>(p.out + (row * p.D + d) * 4) = y;
+    else *reinterpret_cast<bf16x4*>(p.out + (row * p.D + d) * 2) = __builtin_convertvector(y, bf16x4);
+}
+
+// The kernel of a head size (64, 128, 256), cache type, output type and tiles of query rows,
+// and its LDS.
+const void* block_kernel_64(bool f16, bool f32_out, int row_tiles, int* lds);
+const void* block_kernel_128(bool f16, bool f32_out, int row_tiles, int* lds);
+const void* block_kernel_256(bool f16, bool f32_out, int row_tiles, int* lds);
+
+}  // namespace ops

@@ -1,0 +1,321 @@
+// ops_attend_block.hpp -- attention of up to 16 new tokens a sequence: decode and
+// verify.
+//
+// Bound by the read of keys and values.  A workgroup of four waves takes a unit of a
+// sequence's keys for one head of the cache and the 16 NR query rows (tokens times heads
+// that share it) of a block.  It walks the unit in leaves of 64 KB of keys and values
+// each: every wave asks for its quarter of the keys, which go straight to the registers that
+// the matrix instructions read, and for the values, which go through LDS to be turned over;
+// the next leaf's are asked for as soon as the registers are free.  Each wave scores its
+// quarter of the keys, the waves agree on the rows' largest scores, put their weights into
+// LDS, and each sums its quarter of the columns over all keys of the leaf.
+//
+// Order of sums.  Leaves begin at multiples of their length, a leaf's sums begin at zero, and
+// are joined in order to those of the super that the leaf is in (kSuper leaves), and supers
+// in order to a row's; whether by this kernel or the next one.  Leaves that a row sees nothing
+// of change no bit.  So a row's bits depend on its place, keys and head size alone: a
+// verify block gives each token the bits that a call of that token alone gives it, whatever
+// else is in the call.
+#pragma once
+#include "ops_attend.hpp"
+
+namespace ops {
+
+template <int DP, int NP>
+constexpr int block_lds = 65536 + NP * (32768 / DP) * 32 + 2 * 4 * 16 * 4;
+
+template <int DP, class X, int NP, int NR>
+__global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(AttendParams p)
+{
+    constexpr int KT = 32768 / DP;         // keys of a leaf
+    constexpr int WK = KT / 4;             // of which a wave scores
+    constexpr int TILES = WK / 16;         // in tiles of 16
+    constexpr int DS = DP / 32;            // steps of 32 values of a head
+    constexpr int DT = DP / 64;            // tiles of 16 columns that a wave sums
+    constexpr int US = KT / 32;            // steps of 32 keys
+    extern __shared__ __align__(16) char lds[];
+    char* const values = lds;
+    char* const weights = lds + 65536;
+    float* const tops = reinterpret_cast<float*>(weights + NP * KT * 32);
+    float* const sums = tops + 64;
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int b = blockIdx.y;
+    // row blocks of the same keys next to each other on one compute die
+    const int turn = blockIdx.x >> 3, rb = turn % p.row_blocks, f = turn / p.row_blocks * 8 + (blockIdx.x & 7);
+    const int u = f / p.heads, head = f - u * p.heads;
+    if (u >= p.units) return;
+    const Seq s = sequence(p.cache, b);
+    if (s.count > kBlockTokens) return;
+    const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
+    const int r0 = rb * NR * 16;
+    if (r0 >= tokens * p.group) return;
+    const int U = KT * p.per_unit;
+    const Visible vis = visible(s, tokens, p.window, p.sinks, U);
+    if (u >= vis.units && !(u == 0 && p.slots == 1)) return;      // a lone unit writes zeros where nothing is seen
+
+    // this lane's rows
+    int high[NR], low[NR];
+    bool mine[NR];
+    long long row[NR];
+    u32x4 q[NR][DS];
+#pragma unroll
+    for (int rt = 0; rt < NR; ++rt) {
+        const int r = r0 + rt * 16 + n, i = r / p.group, h = head * p.group + r - i * p.group;
+        mine[rt] = i < tokens;
+        high[rt] = mine[rt] ? place0 + i : -1;
+        low[rt] = p.window > 0 ? place0 + i - p.window : -0x7fffffff - 1;
+        const int t = s.start + i;
+        row[rt] = (long long)t * p.q_heads + h;
+#pragma unroll
+        for (int d = 0; d < DS; ++d) {
+            const int c = 4 * d + g;
+            q[rt][d] = u32x4{0, 0, 0, 0};
+            if (mine[rt] && c * 8 < p.D) q[rt][d] = *reinterpret_cast<const u32x4*>(p.q + t * p.q_token + h * p.q_head + c * 16);
+        }
+    }
+    const int i_first = r0 / p.group, i_last = min(tokens - 1, (r0 + NR * 16 - 1) / p.group);
+    const bool whole = p.D == DP;
+
+    f32x4 o[NR][DT];
+    float m[NR], l[NR];
+#pragma unroll
+    for (int rt = 0; rt < NR; ++rt) {
+        m[rt] = kGone;
+        l[rt] = 0.0f;
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0, 0, 0, 0};
+    }
+
+    const int from = u < vis.units ? vis.unit(u) * U : 0, to = u < vis.units ? min(from + U, vis.high + 1) : 0;
+    auto next_leaf = [&](int at) {
+        while (at < to && !vis.meets(at, at + KT)) at += KT;
+        return at < to ? at : -1;
+    };
+
+    // pages of the lane's keys of a leaf, key n of every tile
+    int entry[TILES];
+    auto ask_pages = [&](int leaf) {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int j = leaf + wave * WK + t * 16 + n;
+            const int at = page_index(p.cache, min(j, s.length - 1));
+            entry[t] = p.cache.pages[b * p.cache.pages_row + at];
+        }
+    };
+    u32x4 kf[TILES][DS], vf[TILES][DS];
+    long long v_at[TILES];
+    uint32_t valid[TILES];
+    long long k_at[TILES];
+    // Addresses: keys that hold nothing get the cache's first slot's, and are hidden later.
+    auto addresses = [&](int leaf, uint32_t (&ok)[TILES]) {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int j = leaf + wave * WK + t * 16 + n;
+            const bool fine = j < s.length && (uint32_t)entry[t] < (uint32_t)p.cache.n_pages;
+            const int slot = fine ? j - page_index(p.cache, j) * p.cache.page_size : 0, page = fine ? entry[t] : 0;
+            ok[t] = (uint32_t)__ballot(fine) & 0xffff;
+            k_at[t] = page * p.cache.k_page + slot * p.cache.k_slot + head * p.cache.k_head;
+            const int vpage = __shfl(page, lane >> 2), vslot = __shfl(slot, lane >> 2);
+            v_at[t] = vpage * p.cache.v_page + vslot * p.cache.v_slot + head * p.cache.v_head;
+        }
+    };
+    auto ask_keys = [&] {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int d = 0; d < DS; ++d) {
+                const int c = whole ? 4 * d + g : min(4 * d + g, (p.D >> 3) - 1);
+                kf[t][d] = *reinterpret_cast<const u32x4*>(p.cache.k + k_at[t] + c * 16);
+            }
+    };
+    auto ask_values = [&] {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t)
+#pragma unroll
+            for (int d = 0; d < DS; ++d) {
+                const int c = whole ? 4 * d + (lane & 3) : min(4 * d + (lane & 3), (p.D >> 3) - 1);
+                vf[t][d] = *reinterpret_cast<const u32x4*>(p.cache.v + v_at[t] + c * 16);
+            }
+    };
+
+    int leaf = next_leaf(from);
+    if (leaf >= 0) {
+        ask_pages(leaf);
+        addresses(leaf, valid);
+        ask_keys();
+        ask_values();
+    }
+    while (leaf >= 0) {
+        const int next = next_leaf(leaf + KT);
+        if (next >= 0) ask_pages(next);
+        uint32_t ok[TILES];
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) ok[t] = valid[t];
+        bool full = leaf + KT - 1 <= place0 + i_first && (p.window == 0 || leaf > place0 + i_last - p.window || leaf + KT <= p.sinks);
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) full = full && ok[t] == 0xffff;
+#pragma unroll
+        for (int rt = 0; rt < NR; ++rt) {
+            // scores of the wave's keys
+            f32x4 x[TILES];
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                f32x4 a = {0, 0, 0, 0};
+#pragma unroll
+                for (int d = 0; d < DS; ++d) {
+                    if (32 * d >= p.D) break;
+                    u32x4 k = kf[t][d];
+                    if (!whole && 8 * (4 * d + g) >= p.D) k = u32x4{0, 0, 0, 0};
+                    a = mfma(k, q[rt][d], a, X());
+                }
+                x[t] = a * p.scale;
+            }
+            if (!full) {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        const int j = leaf + wave * WK + t * 16 + 4 * g + i;
+                        const bool sees = j <= high[rt] && (j > low[rt] || j < p.sinks) && (ok[t] >> (4 * g + i) & 1);
+                        x[t][i] = sees ? x[t][i] : kGone;
+                    }
+            }
+            // the leaf's largest score of the row
+            float top = kGone;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) top = __builtin_fmaxf(__builtin_fmaxf(top, __builtin_fmaxf(x[t].x, x[t].y)), __builtin_fmaxf(x[t].z, x[t].w));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            if (g == 0) tops[wave * 16 + n] = top;
+            if (rt == NR - 1 && NR > 1 && next >= 0) ask_keys();
+            lds_only_barrier();
+            if (rt == 0) {
+#pragma unroll
+                for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                    for (int d = 0; d < DS; ++d) {
+                        u32x4 v = vf[t][d];
+                        if (!full && !(ok[t] >> (lane >> 2) & 1)) v = u32x4{0, 0, 0, 0};
+                        *reinterpret_cast<u32x4*>(values + ((wave * TILES + t) * DS + d) * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) << 4)) = v;
+                    }
+                if (next >= 0) {
+                    addresses(next, valid);
+                    if (NR == 1) ask_keys();
+                    ask_values();
+                }
+            }
+            top = __builtin_fmaxf(__builtin_fmaxf(tops[n], tops[16 + n]), __builtin_fmaxf(tops[32 + n], tops[48 + n]));
+            const float at = top == kGone ? 0.0f : top;
+            float sum = 0.0f;
+#pragma unroll
+            for (int t = 0; t < TILES; ++t) {
+                f32x4 w;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) w[i] = exp2_of(x[t][i] - at);
+                sum += (w.x + w.y) + (w.z + w.w);
+                const int block = wave * TILES + t;
+#pragma unroll
+                for (int c = 0; c < NP; ++c) {
+                    const u32x2 h = {pack(w.x, w.y, X()), pack(w.z, w.w, X())};
+                    *reinterpret_cast<u32x2*>(weights + c * KT * 32 + (block >> 1) * 1024 + lane * 16 + (block & 1) * 8) = h;
+                    if (c + 1 < NP) {
+                        const f32x2 lo = unpack(h.x, X()), hi = unpack(h.y, X());
+                        w -= f32x4{lo.x, lo.y, hi.x, hi.y};
+                    }
+                }
+            }
+            sum += __shfl_xor(sum, 16);
+            sum += __shfl_xor(sum, 32);
+            if (g == 0) sums[wave * 16 + n] = sum;
+            lds_only_barrier();
+            sum = (sums[n] + sums[16 + n]) + (sums[32 + n] + sums[48 + n]);
+            const Factors by = join(m[rt], l[rt], top, sum);
+
+            // the wave's columns over the leaf's keys
+            f32x4 a[DT];
+            bool odd = false;
+#pragma unroll
+            for (int d = 0; d < DT; ++d) a[d] = f32x4{0, 0, 0, 0};
+            const int i16 = lane & 15;
+            auto column = [&](int d) {
+                const int tile = wave * DT + d;
+                return values + (tile >> 1) * 1024 + (4 * g + (i16 >> 2)) * 64 + ((((tile & 1) * 2 + ((i16 & 3) >> 1)) ^ g) << 4) + (i16 & 1) * 8;
+            };
+#pragma unroll
+            for (int k = 0; k < US; ++k) {
+                u32x4 w[NP];
+#pragma unroll
+                for (int c = 0; c < NP; ++c) w[c] = *reinterpret_cast<const u32x4*>(weights + c * KT * 32 + k * 1024 + lane * 16);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    const u32x2 v0 = read_turned(column(d) + 2 * k * DS * 1024), v1 = read_turned(column(d) + (2 * k + 1) * DS * 1024);
+                    u32x4 v = {v0.x, v0.y, v1.x, v1.y};
+                    if (!full) {
+                        const u32x4 kept = {numbers<X>(v.x), numbers<X>(v.y), numbers<X>(v.z), numbers<X>(v.w)};
+                        odd = odd || kept.x != v.x || kept.y != v.y || kept.z != v.z || kept.w != v.w;
+                        v = kept;
+                    }
+#pragma unroll
+                    for (int c = 0; c < NP; ++c) a[d] = mfma(v, w[c], a[d], X());
+                }
+            }
+            // A value that is no number goes to the rows that see its key alone: as a factor of a matrix
+            // product it would reach the others too, by zero times infinity.
+            if (!full && __any(odd)) {
+                for (int key = 0; key < KT; ++key) {
+                    const int k = key & 31, slot = (k & 3) + (k >> 4) * 4, from_lane = n + ((k & 15) >> 2) * 16;
+                    const X w = reinterpret_cast<const X*>(weights + (key >> 5) * 1024 + from_lane * 16)[slot];
+#pragma unroll
+                    for (int d = 0; d < DT; ++d)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int col = (wave * DT + d) * 16 + 4 * g + i;
+                            const char* at = values + ((key >> 4) * DS + (col >> 5)) * 1024 + (key & 15) * 64 + (((col >> 3 & 3) ^ (key >> 2 & 3)) << 4) + (col & 7) * 2;
+                            const float v = (float)*reinterpret_cast<const X*>(at);
+                            const uint32_t bits = *reinterpret_cast<const uint16_t*>(at);
+                            if ((bits & no_number(X())) == no_number(X()) && (float)w != 0.0f) a[d][i] = __builtin_fmaf((float)w, v, a[d][i]);
+                        }
+                }
+            }
+#pragma unroll
+            for (int d = 0; d < DT; ++d) o[rt][d] = joined(o[rt][d], a[d], by);
+        }
+        leaf = next;
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < NR; ++rt) {
+        if (!mine[rt]) continue;
+        const long long at = row[rt] * p.slots + u;
+        if (p.slots > 1 && wave == 0 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            const int c = (wave * DT + d) * 16 + 4 * g;
+            if (c >= p.D) continue;
+            if (p.slots == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
+            else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
+        }
+    }
+}
+
+// the kernels of a head size
+template <int DP, class X, int NP>
+const void* block_kernel_rows(int row_tiles, int* lds)
+{
+    *lds = block_lds<DP, NP>;
+    return row_tiles == 1   ? (const void*)&block_kernel<DP, X, NP, 1>
+           : row_tiles == 2 ? (const void*)&block_kernel<DP, X, NP, 2>
+                            : (const void*)&block_kernel<DP, X, NP, 4>;
+}
+
+// a weight in one piece for bf16 outputs; for fp32 ones in as many as hold 22 bits of it or more
+template <int DP>
+const void* block_kernel_types(bool f16, bool f32_out, int row_tiles, int* lds)
+{
+    if (f16) return f32_out ? block_kernel_rows<DP, _Float16, 2>(row_tiles, lds) : block_kernel_rows<DP, _Float16, 1>(row_tiles, lds);
+    return f32_out ? block_kernel_rows<DP, __bf16, 3>(row_tiles, lds) : block_kernel_rows<DP, __bf16, 1>(row_tiles, lds);
+}
+
+}  // namespace ops
