@@ -12,99 +12,109 @@ namespace ops {
 namespace {
 
 constexpr int kThreads = 256;
-constexpr int kAhead = 8;      // slots of a row asked for at once
 
-// The parts of a block's rows, joined: leaves to supers and supers to rows, in order.  2^lanes_log2
-// lanes a row, four values each.
-__global__ __launch_bounds__(kThreads) void join_blocks_kernel(AttendParams p, int leaf, int lanes_log2)
+constexpr int kLanes = 16;                 // of a row's 64 columns
+constexpr int kChains = kThreads / kLanes;
+
+// The parts of rows, joined: those of blocks, or (splits > 0) of chunks, which are `splits` supers each.  Leaves are joined to supers one after the other, as the
+// block's kernel does it; a row is the sum of its supers, in order, each with its weight against
+// the row's largest score.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows.  Bound by
+// latency: every group of 16 lanes asks for eight parts at once.
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int splits, int chains_log2, int columns)
 {
+    __shared__ __align__(16) f32x4 sums[kThreads * kSuper];
+    __shared__ f32x2 stats[kChains * kSuper];
+    __shared__ float tops[kChains];
     const int b = blockIdx.y;
     const Seq s = sequence(p.cache, b);
-    if (s.count > kBlockTokens) return;
-    const int tokens = min(s.count, p.max_new);
-    const int r = blockIdx.x * (kThreads >> lanes_log2) + (threadIdx.x >> lanes_log2), d = (threadIdx.x & ((1 << lanes_log2) - 1)) * 4;
-    if (r >= tokens * p.q_heads || d >= p.D) return;
-    const Visible vis = visible(s, tokens, p.window, p.sinks, leaf * p.per_unit);
+    if ((s.count > kBlockTokens) != (splits > 0)) return;
+    const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
+    const int tid = threadIdx.x, lane = tid & (kLanes - 1), group = tid / kLanes;
+    const int chains = 1 << chains_log2, chain = group & (chains - 1), team = group >> chains_log2;
+    const int block = blockIdx.x / columns, d = (blockIdx.x - block * columns) * 64 + lane * 4;
+    const int r0 = block * (kChains >> chains_log2), r = r0 + team;
+    if (r0 >= tokens * p.q_heads) return;
+    const bool mine = r < tokens * p.q_heads, mine_d = mine && d < p.D;
+    Visible vis = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit);
+    if (splits > 0) vis.units = splits;
     const long long row = (long long)s.start * p.q_heads + r;
     const f32x2* stat = p.stat + row * p.slots;
     const float* part = p.part + row * p.slots * p.D + d;
-    float m = kGone, l = 0.0f, ms = kGone, ls = 0.0f;
-    f32x4 o = {0, 0, 0, 0}, os = {0, 0, 0, 0};
-    int super = -1;
-    for (int u0 = 0; u0 < vis.units; u0 += kAhead) {
-        f32x2 st[kAhead];
-        f32x4 pa[kAhead];
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            const int u = min(u0 + i, vis.units - 1);
-            st[i] = stat[u];
-            pa[i] = *reinterpret_cast<const f32x4*>(part + (long long)u * p.D);
-        }
-#pragma unroll
-        for (int i = 0; i < kAhead; ++i) {
-            if (u0 + i >= vis.units) break;
-            const int now = vis.unit(u0 + i) * p.per_unit / kSuper;
-            if (now != super) {
-                const Factors f = join(m, l, ms, ls);
-                o = joined(o, os, f);
-                ms = kGone;
-                ls = 0.0f;
-                os = f32x4{0, 0, 0, 0};
-                super = now;
-            }
-            const Factors f = join(ms, ls, st[i].x, st[i].y);
-            os = joined(os, pa[i], f);
-        }
-    }
-    const Factors f = join(m, l, ms, ls);
-    o = joined(o, os, f);
-    put_result(p, row, d, o, l);
-}
+    const bool leaves = splits == 0 && p.per_unit == 1;
+    // supers of the row, where units are leaves
+    const Visible all = leaves ? visible(place0, tokens, p.window, p.sinks, leaf * kSuper) : vis;
 
-template <class X>
-__global__ __launch_bounds__(64) void attend_kernel(AttendParams p)
-{
-    const int lane = threadIdx.x, h = blockIdx.x, t = blockIdx.y + blockIdx.z * 65535;
-    if (t >= p.cache.T) return;
-    const int b = sequence_of(p.cache, t, lane);
-    if (b < 0) return;
-    const Seq s = sequence(p.cache, b);
-    const int at = t - s.start;
-    if (s.count <= kBlockTokens || at < 0 || at >= s.count || at >= p.max_new) return;
-    const int place = s.length - s.count + at, kh = h / (p.q_heads / p.heads);
-    constexpr int R = QMV_MAX_HEAD_SIZE / 64;
-    float q[R], o[R];
-    const X* qr = reinterpret_cast<const X*>(p.q + t * p.q_token + h * p.q_head);
-    for (int i = 0; i < R; ++i) {
-        q[i] = i * 64 + lane < p.D ? (float)qr[i * 64 + lane] * p.scale : 0.0f;
-        o[i] = 0.0f;
+    // the parts of the first round are on their way while the largest score is found
+    f32x2 st[kSuper];
+    f32x4 pa[kSuper];
+    int at[kSuper];
+    auto ask = [&](int s0) {
+        const int sup = leaves ? s0 + chain : 0, first = leaves && sup < all.units ? all.unit(sup) * kSuper : 0;
+#pragma unroll
+        for (int i = 0; i < kSuper; ++i) {
+            const int u = leaves ? first + i : s0 + chain * kSuper + i;
+            if (leaves)
+                at[i] = sup >= all.units ? -1 : u < vis.front ? u : u >= vis.start && u - vis.start < vis.units - vis.front ? u - vis.start + vis.front : -1;
+            else
+                at[i] = u < vis.units ? u : -1;
+            st[i] = f32x2{kGone, 0.0f};
+            pa[i] = f32x4{0, 0, 0, 0};
+            if (mine && at[i] >= 0) {
+                st[i] = stat[at[i]];
+                if (mine_d) pa[i] = *reinterpret_cast<const f32x4*>(part + (long long)at[i] * p.D);
+            }
+        }
+    };
+    const int round = leaves ? chains : chains * kSuper;      // supers of a round
+    ask(0);
+    float top = kGone;
+    if (mine)
+        for (int u = chain * kLanes + lane; u < vis.units; u += chains * kLanes) top = __builtin_fmaxf(top, stat[u].x);
+#pragma unroll
+    for (int i = 1; i < kLanes; i <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, i));
+    if (lane == 0) tops[group] = top;
+    lds_only_barrier();
+    for (int i = 0; i < chains; ++i) top = __builtin_fmaxf(top, tops[(team << chains_log2) + i]);
+    const float base = top == kGone ? 0.0f : top;
+
+    float l = 0.0f;
+    f32x4 o = {0, 0, 0, 0};
+    for (int s0 = 0; s0 < all.units; s0 += round) {
+        if (s0 > 0) {
+            ask(s0);
+            lds_only_barrier();
+        }
+        if (leaves) {
+            float ms = kGone, ls = 0.0f;
+            f32x4 os = {0, 0, 0, 0};
+#pragma unroll
+            for (int i = 0; i < kSuper; ++i) {
+                if (at[i] < 0) continue;
+                const Factors f = join(ms, ls, st[i].x, st[i].y);
+                os = joined(os, pa[i], f);
+            }
+            sums[tid] = os;
+            stats[group] = f32x2{ms, ls};
+        } else {
+#pragma unroll
+            for (int i = 0; i < kSuper; ++i) {
+                sums[(group * kSuper + i) * kLanes + lane] = pa[i];
+                stats[group * kSuper + i] = st[i];
+            }
+        }
+        lds_only_barrier();
+        if (chain == 0) {
+            const int n = min(round, all.units - s0), first = team * round;
+            for (int i = 0; i < n; ++i) {
+                const f32x2 t = stats[first + i];
+                const f32x4 v = sums[(first + i) * kLanes + lane];
+                const float w = exp2_of(t.x - base);
+                l = __builtin_fmaf(t.y, w, l);
+                o = f32x4{__builtin_fmaf(v.x, w, o.x), __builtin_fmaf(v.y, w, o.y), __builtin_fmaf(v.z, w, o.z), __builtin_fmaf(v.w, w, o.w)};
+            }
+        }
     }
-    float m = -__builtin_huge_valf(), l = 0.0f;
-    for (int j = 0; j <= place; ++j) {
-        if (p.window > 0 && j <= place - p.window && j >= p.sinks) j = place - p.window + 1;
-        const int index = page_index(p.cache, j), page = page_of(p.cache, b, index);
-        if (page < 0) continue;
-        const int slot = j - index * p.cache.page_size;
-        const X* k = reinterpret_cast<const X*>(p.cache.k + page * p.cache.k_page + slot * p.cache.k_slot + kh * p.cache.k_head);
-        const X* v = reinterpret_cast<const X*>(p.cache.v + page * p.cache.v_page + slot * p.cache.v_slot + kh * p.cache.v_head);
-        float x = 0.0f;
-        for (int i = 0; i < R; ++i)
-            if (i * 64 + lane < p.D) x = __builtin_fmaf(q[i], (float)k[i * 64 + lane], x);
-        for (int i = 1; i < 64; i <<= 1) x += __shfl_xor(x, i);
-        const float top = __builtin_fmaxf(m, x), a = exp2_of(m - top), e = exp2_of(x - top);
-        m = top;
-        l = l * a + e;
-        for (int i = 0; i < R; ++i)
-            if (i * 64 + lane < p.D) o[i] = o[i] * a + e * (float)v[i * 64 + lane];
-    }
-    const float r = l > 0.0f ? 1.0f / l : l;
-    for (int i = 0; i < R; ++i) {
-        const int d = i * 64 + lane;
-        const long long to = ((long long)t * p.q_heads + h) * p.D + d;
-        if (d >= p.D) continue;
-        if (p.out_f32) reinterpret_cast<float*>(p.out)[to] = o[i] * r;
-        else reinterpret_cast<__bf16*>(p.out)[to] = (__bf16)(o[i] * r);
-    }
+    if (mine_d && chain == 0) put_result(p, row, d, o, l);
 }
 
 int check_sizes(const qmv_cache* c, int T, int q_heads, int max_new, int max_length, int window, int sinks)
@@ -117,14 +127,17 @@ int bound_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
 
 // How a call is cut up: by its sizes alone.
 struct Plan {
-    int max_new, length;                          // as far as they matter
-    int window, sinks;
-    int leaf, row_tiles, row_blocks, per_unit;
+    int max_new, length, window, sinks;           // as far as they matter
+    int bound, leaf;
+    int row_tiles, row_blocks, per_unit;          // blocks: a workgroup's tiles of rows, and a unit's leaves
     long long units;                              // of a sequence, at most
-    long long rows, part_bytes, stat_bytes;
+    int chunk_rows, chunk_blocks, splits;         // chunks: a workgroup's rows, and the shares of their keys
+    const void *block, *chunk;
+    int block_lds, chunk_lds, chunk_threads;
+    long long part_bytes, stat_bytes;
 };
 
-// units of U places that a sequence's block can see
+// units of U places that `tokens` neighbouring ones see at most
 long long units_of(const Plan& p, int tokens, long long U)
 {
     const long long all = std::max<long long>(1, (p.length + U - 1) / U);
@@ -132,32 +145,61 @@ long long units_of(const Plan& p, int tokens, long long U)
     return std::min(all, (std::min(p.sinks, p.length) + U - 1) / U + ((long long)p.window + tokens - 1 + U - 1) / U + 1);
 }
 
-Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length, int window, int sinks)
+Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length, int window, int sinks, bool f32_out)
 {
     Plan p;
     p.max_new = std::min(max_new, T);
     p.length = (int)std::min<long long>(max_length, (long long)c->max_pages * c->page_size);
     p.window = std::min(window, QMV_MAX_LENGTH);
     p.sinks = window > 0 ? std::min(sinks, QMV_MAX_LENGTH) : 0;
+    p.bound = c->head_size <= 64 ? 64 : c->head_size <= 128 ? 128 : 256;
+    const bool f16 = c->dt == QMV_DT_F16;
     const int group = q_heads / c->heads, tokens = std::min(p.max_new, kBlockTokens);
     const int rows = tokens * group;
-    p.leaf = 32768 / bound_of(c->head_size);
+    p.leaf = leaf_keys(p.bound);
     p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
     p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
     // leaf by leaf while that is few workgroups, else a super each
     const long long leaves = units_of(p, tokens, p.leaf);
-    p.per_unit = leaves * c->heads * p.row_blocks * c->n_seqs > 2048 ? kSuper : 1;
+    p.per_unit = leaves * c->heads * p.row_blocks * c->n_seqs > 1024 ? kSuper : 1;
     p.units = units_of(p, tokens, (long long)p.leaf * p.per_unit);
-    p.rows = (long long)T * q_heads;
-    p.part_bytes = p.units > 1 ? piece(p.rows * p.units * c->head_size * 4) : 0;
-    p.stat_bytes = p.units > 1 ? piece(p.rows * p.units * 8) : 0;
+    p.block = p.bound == 64    ? block_kernel_64(f16, f32_out, p.row_tiles, &p.block_lds)
+              : p.bound == 128 ? block_kernel_128(f16, f32_out, p.row_tiles, &p.block_lds)
+                               : block_kernel_256(f16, f32_out, p.row_tiles, &p.block_lds);
+    p.chunk = p.bound == 64    ? chunk_kernel_64(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds)
+              : p.bound == 128 ? chunk_kernel_128(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds)
+                               : chunk_kernel_256(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds);
+    p.chunk_blocks = (int)(((long long)p.max_new * group + p.chunk_rows - 1) / p.chunk_rows);
+    p.splits = 0;
+    long long slots = p.units;
+    if (p.max_new > kBlockTokens) {
+        // as many shares as two workgroups of four waves per compute unit, of 512 keys at least
+        const long long groups = (long long)p.chunk_blocks * c->heads * c->n_seqs, room = 131072 / p.chunk_threads / groups;
+        const long long most = (std::min<long long>(p.length, p.window ? (long long)p.window + p.sinks + p.chunk_rows / group : p.length) + 511) / 512;
+        p.splits = (int)std::max<long long>(1, std::min(room, most));
+        slots = std::max<long long>(slots, p.splits);
+    }
+    const long long parts = slots > 1 ? (long long)T * q_heads * slots : 0;
+    p.part_bytes = piece(parts * c->head_size * 4);
+    p.stat_bytes = piece(parts * 8);
     return p;
 }
 
-const void* block_kernel_of(int bound, bool f16, bool f32_out, int row_tiles, int* lds)
+int launch(const void* f, dim3 grid, int threads, void** args, int lds, void* stream)
 {
-    return bound == 64 ? block_kernel_64(f16, f32_out, row_tiles, lds) : bound == 128 ? block_kernel_128(f16, f32_out, row_tiles, lds)
-                                                                                     : block_kernel_256(f16, f32_out, row_tiles, lds);
+    return hipLaunchKernel(f, grid, dim3(threads), args, (size_t)lds, static_cast<hipStream_t>(stream)) == hipSuccess ? QMV_OK : QMV_E_LAUNCH;
+}
+
+// the parts of the blocks' rows, or (splits > 0) the chunks'
+int launch_join(AttendParams& p, const Plan& plan, int splits, int n_seqs, void* stream)
+{
+    int chains_log2 = 0, leaf = plan.leaf, columns = (p.D + 63) / 64;
+    const int eights = (p.slots + kSuper - 1) / kSuper;
+    while (1 << chains_log2 < std::min(kChains, eights)) ++chains_log2;
+    const long long rows = (long long)(splits > 0 ? plan.max_new : std::min(plan.max_new, kBlockTokens)) * p.q_heads;
+    const int per = kChains >> chains_log2;
+    void* args[] = {&p, &leaf, &splits, &chains_log2, &columns};
+    return launch((const void*)&join_kernel, dim3((unsigned)((rows + per - 1) / per * columns), n_seqs), kThreads, args, 0, stream);
 }
 
 }  // namespace
@@ -170,7 +212,7 @@ long long qmv_attend_workspace(const qmv_cache* c, int T, int q_heads, int max_n
 {
     using namespace ops;
     if (!c || check_sizes(c, T, q_heads, max_new, max_length, window, sinks) != QMV_OK) return -1;
-    const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks);
+    const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks, false);
     return plan.part_bytes + plan.stat_bytes;
 }
 
@@ -189,15 +231,17 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     if (q_token % 8 != 0 || q_head % 8 != 0 || !aligned(q, 16) || !aligned(out, 16) || !aligned(workspace, 16)) return QMV_E_ALIGN;
     const long long size[] = {T, q_heads}, stride[] = {q_token, q_head}, nq = extent(size, stride, c->head_size);
     if (nq < 0) return QMV_E_STRIDE;
-    const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks);
+    const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks, out_dt == QMV_DT_F32);
     const long long need = plan.part_bytes + plan.stat_bytes;
     if (workspace_bytes < need) return QMV_E_WORKSPACE;
     const Span in[] = {{q, (size_t)nq * 2}, {c->k, cs.k}, {c->v, cs.v}, {c->pages, cs.pages}, {c->starts, (size_t)(c->n_seqs + 1) * 4},
                        {c->lengths, (size_t)c->n_seqs * 4}};
     const Span outs[] = {{out, (size_t)T * q_heads * c->head_size * size_of(out_dt)}, {workspace, (size_t)need}};
     if (!disjoint(in, outs)) return QMV_E_ALIAS;
-    const long long groups = (plan.units * c->heads + 7) / 8 * 8 * plan.row_blocks;
-    if (groups > (1 << 24) - 1) return QMV_E_CACHE;      // a launch's size in threads is a 32-bit number
+    const long long groups = (plan.units * c->heads + 7) / 8 * 8 * plan.row_blocks, chunk_groups = (long long)plan.chunk_blocks * c->heads;
+    // a launch's size in threads is a 32-bit number, and so is the join's
+    if (groups > (1 << 24) - 1 || chunk_groups > (1 << 22) || (long long)plan.max_new * q_heads * ((c->head_size + 63) / 64) > (1 << 24) - 1)
+        return QMV_E_CACHE;
     AttendParams p;
     p.q = static_cast<const char*>(q);
     p.out = static_cast<char*>(out);
@@ -219,22 +263,15 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.scale = scale * 1.44269504088896340736f;
     p.cache = device_cache(c, T);
     p.cache.max_places = plan.length;
-    hipStream_t st = static_cast<hipStream_t>(stream);
-    int lds;
-    const void* f = block_kernel_of(bound_of(p.D), c->dt == QMV_DT_F16, p.out_f32, plan.row_tiles, &lds);
     void* args[] = {&p};
-    if (hipLaunchKernel(f, dim3((unsigned)groups, c->n_seqs), dim3(kThreads), args, (size_t)lds, st) != hipSuccess) return QMV_E_LAUNCH;
-    if (plan.units > 1) {
-        int lanes_log2 = 1, leaf = plan.leaf;
-        while (4 << lanes_log2 < p.D) ++lanes_log2;
-        const int rows = std::min(plan.max_new, kBlockTokens) * q_heads, per = kThreads >> lanes_log2;
-        void* more[] = {&p, &leaf, &lanes_log2};
-        if (hipLaunchKernel((const void*)&join_blocks_kernel, dim3((rows + per - 1) / per, c->n_seqs), dim3(kThreads), more, 0, st) != hipSuccess)
-            return QMV_E_LAUNCH;
-    }
+    if (int e = launch(plan.block, dim3((unsigned)groups, c->n_seqs), kThreads, args, plan.block_lds, stream)) return e;
+    if (plan.units > 1)
+        if (int e = launch_join(p, plan, 0, c->n_seqs, stream)) return e;
     if (plan.max_new > kBlockTokens) {
-        const void* f = c->dt == QMV_DT_F16 ? (const void*)&attend_kernel<_Float16> : (const void*)&attend_kernel<__bf16>;
-        if (hipLaunchKernel(f, dim3(q_heads, std::min(T, 65535), (T + 65534) / 65535), dim3(64), args, 0, st) != hipSuccess) return QMV_E_LAUNCH;
+        p.slots = plan.splits;
+        if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.chunk_threads, args, plan.chunk_lds, stream)) return e;
+        if (plan.splits > 1)
+            if (int e = launch_join(p, plan, plan.splits, c->n_seqs, stream)) return e;
     }
     return QMV_OK;
 }

@@ -33,6 +33,8 @@ typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 
 constexpr int kBlockTokens = 16;      // up to so many new tokens a sequence is a block, above a chunk
+constexpr int kLeafBytes = 32768;     // of keys in a leaf, and of values
+constexpr int leaf_keys(int head_size) { return kLeafBytes / 2 / head_size; }
 constexpr int kSuper = 8;             // leaves of a super (the two steps in which blocks of keys are joined)
 constexpr float kGone = -__builtin_huge_valf();
 
@@ -63,17 +65,53 @@ __device__ __forceinline__ uint32_t pack(float a, float b, _Float16) { return __
 __device__ __forceinline__ f32x2 unpack(uint32_t v, __bf16) { return __builtin_convertvector(__builtin_bit_cast(bf16x2, v), f32x2); }
 __device__ __forceinline__ f32x2 unpack(uint32_t v, _Float16) { return __builtin_convertvector(__builtin_bit_cast(f16x2, v), f32x2); }
 
-// the exponents of a value that is no number: infinities and NaN
-constexpr uint32_t no_number(__bf16) { return 0x7f80; }
+// Values that are no numbers.  As a factor of a matrix product, the infinity or NaN of one key
+// would reach the rows that do not see the key too, by zero times infinity.  So where rows of a tile
+// see different keys, such values are taken out of the product; and if there were any, products
+// of marks count for every output the NaN, infinities and negative infinities that it sees.
+constexpr uint32_t no_number(__bf16) { return 0x7f80; }       // the exponent
 constexpr uint32_t no_number(_Float16) { return 0x7c00; }
+constexpr uint32_t one(__bf16) { return 0x3f80; }
+constexpr uint32_t one(_Float16) { return 0x3c00; }
 
-// the word with those of its two values gone that are no numbers
+// the two values of a word, those that are no numbers as zeros
 template <class X>
 __device__ __forceinline__ uint32_t numbers(uint32_t w)
 {
     constexpr uint32_t E = no_number(X());
     const uint32_t lo = (w & E) == E ? 0 : w & 0xffff, hi = (w >> 16 & E) == E ? 0 : w & 0xffff0000;
     return lo | hi;
+}
+template <class X>
+__device__ __forceinline__ u32x4 numbers4(u32x4 w, bool& odd)
+{
+    const u32x4 kept = {numbers<X>(w.x), numbers<X>(w.y), numbers<X>(w.z), numbers<X>(w.w)};
+    odd = odd || kept.x != w.x || kept.y != w.y || kept.z != w.z || kept.w != w.w;
+    return kept;
+}
+
+// ones where a value is a NaN (kind 0), an infinity (1), a negative infinity (2), or not zero (3)
+template <class X>
+__device__ __forceinline__ uint32_t marks(uint32_t w, int kind)
+{
+    constexpr uint32_t E = no_number(X());
+    auto is = [&](uint32_t h) {
+        return kind == 0 ? (h & 0x7fff) > E : kind == 1 ? h == E : kind == 2 ? h == (0x8000 | E) : (h & 0x7fff) != 0;
+    };
+    return (is(w & 0xffff) ? one(X()) : 0) | (is(w >> 16) ? one(X()) << 16 : 0);
+}
+template <class X>
+__device__ __forceinline__ u32x4 marks4(u32x4 w, int kind)
+{
+    return u32x4{marks<X>(w.x, kind), marks<X>(w.y, kind), marks<X>(w.z, kind), marks<X>(w.w, kind)};
+}
+// the output that has met `count` of them
+__device__ __forceinline__ f32x4 met(f32x4 o, f32x4 count, int kind)
+{
+    const float what = kind == 0 ? __builtin_nanf("") : kind == 1 ? -kGone : kGone;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) o[i] = count[i] > 0.0f ? o[i] + what : o[i];
+    return o;
 }
 
 // A barrier for LDS alone: loads from memory stay in flight over it.
@@ -92,7 +130,7 @@ __device__ __forceinline__ u32x2 read_turned(const char* lds)
     return __builtin_bit_cast(u32x2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((At)(uintptr_t)(lds)));
 }
 
-// What the new tokens of a sequence see, between them: the places below `first` and those
+// What some new tokens of a sequence see, between them: the places below `first` and those
 // from low to high, in units of U places, listed one after the other.
 struct Visible {
     int first, low, high;         // high < 0: nothing
@@ -101,11 +139,10 @@ struct Visible {
     __device__ __forceinline__ bool meets(int from, int to) const { return from < first || (from <= high && to > low); }
 };
 
-// tokens: how many of the sequence's new tokens are computed
-__device__ __forceinline__ Visible visible(const Seq& s, int tokens, int window, int sinks, int U)
+// of new tokens at places from `place` on
+__device__ __forceinline__ Visible visible(int place, int tokens, int window, int sinks, int U)
 {
     Visible v;
-    const int place = s.length - s.count;      // of the first
     v.high = place + tokens - 1;
     v.low = window > 0 ? max(0, place - window + 1) : 0;
     v.first = window > 0 ? min(sinks, v.low) : 0;
@@ -151,5 +188,9 @@ __device__ __forceinline__ void put_result(const AttendParams& p, long long row,
 const void* block_kernel_64(bool f16, bool f32_out, int row_tiles, int* lds);
 const void* block_kernel_128(bool f16, bool f32_out, int row_tiles, int* lds);
 const void* block_kernel_256(bool f16, bool f32_out, int row_tiles, int* lds);
+// The same for chunks, with the rows and threads of a workgroup.
+const void* chunk_kernel_64(bool f16, bool f32_out, int* rows, int* threads, int* lds);
+const void* chunk_kernel_128(bool f16, bool f32_out, int* rows, int* threads, int* lds);
+const void* chunk_kernel_256(bool f16, bool f32_out, int* rows, int* threads, int* lds);
 
 }  // namespace ops

@@ -3,8 +3,8 @@
 //
 // Bound by the read of keys and values.  A workgroup of four waves takes a unit of a
 // sequence's keys for one head of the cache and the 16 NR query rows (tokens times heads
-// that share it) of a block.  It walks the unit in leaves of 64 KB of keys and values
-// each: every wave asks for its quarter of the keys, which go straight to the registers that
+// that share it) of a block.  It walks the unit in leaves of 32 KB of keys and as
+// much of values: every wave asks for its quarter of the keys, which go straight to the registers that
 // the matrix instructions read, and for the values, which go through LDS to be turned over;
 // the next leaf's are asked for as soon as the registers are free.  Each wave scores its
 // quarter of the keys, the waves agree on the rows' largest scores, put their weights into
@@ -21,13 +21,14 @@
 
 namespace ops {
 
-template <int DP, int NP>
-constexpr int block_lds = 65536 + NP * (32768 / DP) * 32 + 2 * 4 * 16 * 4;
+// queries of more than one tile of rows lie in LDS
+template <int DP, int NP, int NR>
+constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + (NR > 1 ? NR * DP * 32 : 0);
 
 template <int DP, class X, int NP, int NR>
-__global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(AttendParams p)
+__global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParams p)
 {
-    constexpr int KT = 32768 / DP;         // keys of a leaf
+    constexpr int KT = leaf_keys(DP);      // keys of a leaf
     constexpr int WK = KT / 4;             // of which a wave scores
     constexpr int TILES = WK / 16;         // in tiles of 16
     constexpr int DS = DP / 32;            // steps of 32 values of a head
@@ -35,9 +36,10 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
     constexpr int US = KT / 32;            // steps of 32 keys
     extern __shared__ __align__(16) char lds[];
     char* const values = lds;
-    char* const weights = lds + 65536;
+    char* const weights = lds + kLeafBytes;
     float* const tops = reinterpret_cast<float*>(weights + NP * KT * 32);
     float* const sums = tops + 64;
+    char* const queries = reinterpret_cast<char*>(sums + 64);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -52,14 +54,14 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
     const int r0 = rb * NR * 16;
     if (r0 >= tokens * p.group) return;
     const int U = KT * p.per_unit;
-    const Visible vis = visible(s, tokens, p.window, p.sinks, U);
+    const Visible vis = visible(place0, tokens, p.window, p.sinks, U);
     if (u >= vis.units && !(u == 0 && p.slots == 1)) return;      // a lone unit writes zeros where nothing is seen
 
     // this lane's rows
     int high[NR], low[NR];
     bool mine[NR];
     long long row[NR];
-    u32x4 q[NR][DS];
+    u32x4 q[DS];
 #pragma unroll
     for (int rt = 0; rt < NR; ++rt) {
         const int r = r0 + rt * 16 + n, i = r / p.group, h = head * p.group + r - i * p.group;
@@ -68,11 +70,13 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
         low[rt] = p.window > 0 ? place0 + i - p.window : -0x7fffffff - 1;
         const int t = s.start + i;
         row[rt] = (long long)t * p.q_heads + h;
+        if (NR == 1 || rt == wave) {
 #pragma unroll
-        for (int d = 0; d < DS; ++d) {
-            const int c = 4 * d + g;
-            q[rt][d] = u32x4{0, 0, 0, 0};
-            if (mine[rt] && c * 8 < p.D) q[rt][d] = *reinterpret_cast<const u32x4*>(p.q + t * p.q_token + h * p.q_head + c * 16);
+            for (int d = 0; d < DS; ++d) {
+                const int c = 4 * d + g;
+                q[d] = u32x4{0, 0, 0, 0};
+                if (mine[rt] && c * 8 < p.D) q[d] = *reinterpret_cast<const u32x4*>(p.q + t * p.q_token + h * p.q_head + c * 16);
+            }
         }
     }
     const int i_first = r0 / p.group, i_last = min(tokens - 1, (r0 + NR * 16 - 1) / p.group);
@@ -147,6 +151,13 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
         ask_keys();
         ask_values();
     }
+    if constexpr (NR > 1) {
+        if (wave < NR) {
+#pragma unroll
+            for (int d = 0; d < DS; ++d) *reinterpret_cast<u32x4*>(queries + (wave * DS + d) * 1024 + lane * 16) = q[d];
+        }
+        lds_only_barrier();
+    }
     while (leaf >= 0) {
         const int next = next_leaf(leaf + KT);
         if (next >= 0) ask_pages(next);
@@ -159,16 +170,20 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
 #pragma unroll
         for (int rt = 0; rt < NR; ++rt) {
             // scores of the wave's keys
+            if constexpr (NR > 1) {
+#pragma unroll
+                for (int d = 0; d < DS; ++d) q[d] = *reinterpret_cast<const u32x4*>(queries + (rt * DS + d) * 1024 + lane * 16);
+            }
             f32x4 x[TILES];
 #pragma unroll
             for (int t = 0; t < TILES; ++t) {
                 f32x4 a = {0, 0, 0, 0};
 #pragma unroll
                 for (int d = 0; d < DS; ++d) {
-                    if (32 * d >= p.D) break;
+                    if (32 * d >= p.D) continue;
                     u32x4 k = kf[t][d];
                     if (!whole && 8 * (4 * d + g) >= p.D) k = u32x4{0, 0, 0, 0};
-                    a = mfma(k, q[rt][d], a, X());
+                    a = mfma(k, q[d], a, X());
                 }
                 x[t] = a * p.scale;
             }
@@ -252,31 +267,23 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
                 for (int d = 0; d < DT; ++d) {
                     const u32x2 v0 = read_turned(column(d) + 2 * k * DS * 1024), v1 = read_turned(column(d) + (2 * k + 1) * DS * 1024);
                     u32x4 v = {v0.x, v0.y, v1.x, v1.y};
-                    if (!full) {
-                        const u32x4 kept = {numbers<X>(v.x), numbers<X>(v.y), numbers<X>(v.z), numbers<X>(v.w)};
-                        odd = odd || kept.x != v.x || kept.y != v.y || kept.z != v.z || kept.w != v.w;
-                        v = kept;
-                    }
+                    if (!full) v = numbers4<X>(v, odd);
 #pragma unroll
                     for (int c = 0; c < NP; ++c) a[d] = mfma(v, w[c], a[d], X());
                 }
             }
-            // A value that is no number goes to the rows that see its key alone: as a factor of a matrix
-            // product it would reach the others too, by zero times infinity.
             if (!full && __any(odd)) {
-                for (int key = 0; key < KT; ++key) {
-                    const int k = key & 31, slot = (k & 3) + (k >> 4) * 4, from_lane = n + ((k & 15) >> 2) * 16;
-                    const X w = reinterpret_cast<const X*>(weights + (key >> 5) * 1024 + from_lane * 16)[slot];
+                for (int kind = 0; kind < 3; ++kind) {
 #pragma unroll
-                    for (int d = 0; d < DT; ++d)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int col = (wave * DT + d) * 16 + 4 * g + i;
-                            const char* at = values + ((key >> 4) * DS + (col >> 5)) * 1024 + (key & 15) * 64 + (((col >> 3 & 3) ^ (key >> 2 & 3)) << 4) + (col & 7) * 2;
-                            const float v = (float)*reinterpret_cast<const X*>(at);
-                            const uint32_t bits = *reinterpret_cast<const uint16_t*>(at);
-                            if ((bits & no_number(X())) == no_number(X()) && (float)w != 0.0f) a[d][i] = __builtin_fmaf((float)w, v, a[d][i]);
+                    for (int d = 0; d < DT; ++d) {
+                        f32x4 count = {0, 0, 0, 0};
+                        for (int k = 0; k < US; ++k) {
+                            const u32x2 v0 = read_turned(column(d) + 2 * k * DS * 1024), v1 = read_turned(column(d) + (2 * k + 1) * DS * 1024);
+                            const u32x4 w = *reinterpret_cast<const u32x4*>(weights + k * 1024 + lane * 16);
+                            count = mfma(marks4<X>(u32x4{v0.x, v0.y, v1.x, v1.y}, kind), marks4<X>(w, 3), count, X());
                         }
+                        a[d] = met(a[d], count, kind);
+                    }
                 }
             }
 #pragma unroll
@@ -304,7 +311,7 @@ __global__ __launch_bounds__(256, NR == 1 && NP == 1 ? 2 : 1) void block_kernel(
 template <int DP, class X, int NP>
 const void* block_kernel_rows(int row_tiles, int* lds)
 {
-    *lds = block_lds<DP, NP>;
+    *lds = row_tiles == 1 ? block_lds<DP, NP, 1> : row_tiles == 2 ? block_lds<DP, NP, 2> : block_lds<DP, NP, 4>;
     return row_tiles == 1   ? (const void*)&block_kernel<DP, X, NP, 1>
            : row_tiles == 2 ? (const void*)&block_kernel<DP, X, NP, 2>
                             : (const void*)&block_kernel<DP, X, NP, 4>;

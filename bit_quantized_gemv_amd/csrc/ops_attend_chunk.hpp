@@ -1,0 +1,296 @@
+// ops_attend_chunk.hpp -- attention of more than 16 new tokens a sequence: prompts,
+// whole or in chunks.
+//
+// Bound by the matrix instructions and, beside them, the exponentials.  A workgroup takes
+// 32 query rows a wave (tokens times the heads that share a head of the cache), kept in
+// registers with their outputs, and walks the keys that they see in tiles through LDS, the
+// next tile's on their way in registers meanwhile.  A wave scores 32 rows against the tile,
+// takes the weights with the rows' running maxima, and adds the weighted values up; a maximum
+// is followed only when it has grown by 2^8, which weights and sums have room for, since moving it
+// costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
+// keys of a tile of rows, and a second launch joins them.
+#pragma once
+#include "ops_attend.hpp"
+
+namespace ops {
+
+template <int DP>
+struct Chunk {
+    static constexpr int kWaves = DP == 256 ? 8 : 4;
+    static constexpr int kKeys = DP == 256 ? 32 : 64;              // of a tile
+    static constexpr int kRows = kWaves * 32;
+    static constexpr int kTileBytes = kKeys * DP * 2;
+    static constexpr int kLds = 4 * kTileBytes + 2 * 16;           // keys and values, twice, and which keys there are
+};
+
+constexpr float kRoom = 8.0f;
+
+template <int DP, class X, int NP>
+__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(AttendParams p)
+{
+    typedef Chunk<DP> C;
+    constexpr int NK = C::kKeys, KB = NK / 16, DS = DP / 32, DT = DP / 16, US = NK / 32;
+    constexpr int BW = KB * DS / C::kWaves;       // blocks of 16 keys and 32 columns that a wave loads
+    extern __shared__ __align__(16) char lds[];
+    uint32_t* const masks = reinterpret_cast<uint32_t*>(lds + 4 * C::kTileBytes);
+
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int n = lane & 15, g = lane >> 4;
+    const int b = blockIdx.y;
+    const Seq s = sequence(p.cache, b);
+    if (s.count <= kBlockTokens) return;
+    const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
+    const int rows = tokens * p.group, blocks = (rows + C::kRows - 1) / C::kRows;
+    // the rows that see most first
+    const int rb = blocks - 1 - (int)blockIdx.x / p.heads, head = blockIdx.x % p.heads;
+    if (rb < 0) return;
+    const int r0 = rb * C::kRows, i_first = r0 / p.group, i_last = min(tokens - 1, (r0 + C::kRows - 1) / p.group);
+
+    // the tiles of keys that the workgroup's rows see, and its share of them
+    const Visible vis = visible(place0 + i_first, i_last - i_first + 1, p.window, p.sinks, NK);
+    const int t_from = (int)((long long)vis.units * blockIdx.z / gridDim.z), t_to = (int)((long long)vis.units * (blockIdx.z + 1) / gridDim.z);
+
+    // queries, negative scales turned into them
+    const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0;
+    const float scale = __builtin_fabsf(p.scale);
+    const int w_first = (r0 + wave * 32) / p.group, w_last = min(tokens - 1, (r0 + wave * 32 + 31) / p.group);
+    const bool idle = r0 + wave * 32 >= rows;
+    u32x4 q[2][DS];
+    int high[2], low[2];
+    long long row[2];
+    bool mine[2];
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+        const int r = r0 + wave * 32 + rt * 16 + n, i = r / p.group, h = head * p.group + r - i * p.group, t = s.start + i;
+        mine[rt] = r < rows;
+        high[rt] = mine[rt] ? place0 + i : -1;
+        low[rt] = p.window > 0 ? place0 + i - p.window : -0x7fffffff - 1;
+        row[rt] = (long long)t * p.q_heads + h;
+#pragma unroll
+        for (int d = 0; d < DS; ++d) {
+            const int c = 4 * d + g;
+            q[rt][d] = u32x4{0, 0, 0, 0};
+            if (mine[rt] && c * 8 < p.D) q[rt][d] = *reinterpret_cast<const u32x4*>(p.q + t * p.q_token + h * p.q_head + c * 16) ^ flip;
+        }
+    }
+    f32x4 o[2][DT];
+    float m[2] = {kGone, kGone}, l[2] = {0.0f, 0.0f};
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+        for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0, 0, 0, 0};
+
+    // what this wave loads of a tile: rows lane / 4 of tile kb, columns from 32 d0 on
+    const int kb = wave * BW / DS, d0 = wave * BW % DS;
+    const int key_row = kb * 16 + (lane >> 2), piece = lane & 3;
+    const bool whole = p.D == DP;
+    u32x4 kr[BW], vr[BW];
+    bool held = false;
+    int entry = 0;
+    auto place_of = [&](int t) { return vis.unit(t) * NK + key_row; };
+    auto ask_page = [&](int t) {
+        if (t < t_to) entry = p.cache.pages[b * p.cache.pages_row + page_index(p.cache, min(place_of(t), s.length - 1))];
+    };
+    auto ask_tile = [&](int t) {
+        if (t >= t_to) return;
+        const int j = place_of(t);
+        held = j < s.length && (uint32_t)entry < (uint32_t)p.cache.n_pages;
+        const int slot = held ? j - page_index(p.cache, j) * p.cache.page_size : 0, page = held ? entry : 0;
+        const char* k = p.cache.k + page * p.cache.k_page + slot * p.cache.k_slot + head * p.cache.k_head;
+        const char* v = p.cache.v + page * p.cache.v_page + slot * p.cache.v_slot + head * p.cache.v_head;
+#pragma unroll
+        for (int d = 0; d < BW; ++d) {
+            const int c = whole ? 4 * (d0 + d) + piece : min(4 * (d0 + d) + piece, (p.D >> 3) - 1);
+            kr[d] = *reinterpret_cast<const u32x4*>(k + c * 16);
+            vr[d] = *reinterpret_cast<const u32x4*>(v + c * 16);
+        }
+    };
+    auto put_tile = [&](int buffer) {
+        char* const at = lds + buffer * 2 * C::kTileBytes + (kb * DS + d0) * 1024 + (lane >> 2) * 64 + ((piece ^ (lane >> 4)) << 4);
+        const uint64_t there = __ballot(held);
+#pragma unroll
+        for (int d = 0; d < BW; ++d) {
+            u32x4 k = kr[d], v = vr[d];
+            if (!whole && 8 * (4 * (d0 + d) + piece) >= p.D) k = u32x4{0, 0, 0, 0};
+            if (there != ~0ull && !held) v = u32x4{0, 0, 0, 0};
+            *reinterpret_cast<u32x4*>(at + d * 1024) = k;
+            *reinterpret_cast<u32x4*>(at + C::kTileBytes + d * 1024) = v;
+        }
+        // one bit a key
+        if (d0 == 0) {
+            const uint32_t bits = (uint32_t)__ballot(lane < 16 && (there >> (4 * (lane & 15)) & 1));
+            if (lane == 0) masks[buffer * 4 + kb] = bits;
+        }
+    };
+
+    if (t_from < t_to) {
+        ask_page(t_from);
+        ask_tile(t_from);
+        ask_page(t_from + 1);
+        put_tile(0);
+        ask_tile(t_from + 1);
+        ask_page(t_from + 2);
+    }
+    lds_only_barrier();
+    for (int t = t_from; t < t_to; ++t) {
+        const int buffer = (t - t_from) & 1;
+        const char* const keys = lds + buffer * 2 * C::kTileBytes;
+        const char* const values = keys + C::kTileBytes;
+        const int j0 = vis.unit(t) * NK;
+        const bool sees = !idle && j0 <= place0 + w_last && (p.window == 0 || j0 + NK > place0 + w_first - p.window + 1 || j0 < p.sinks);
+        if (sees) {
+            f32x4 x[2][KB];
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) x[rt][k] = f32x4{0, 0, 0, 0};
+#pragma unroll
+                for (int d = 0; d < DS; ++d) {
+                    if (32 * d >= p.D) continue;
+                    const u32x4 f = *reinterpret_cast<const u32x4*>(keys + (k * DS + d) * 1024 + n * 64 + ((g ^ (n >> 2)) << 4));
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) x[rt][k] = mfma(f, q[rt][d], x[rt][k], X());
+                }
+            }
+            bool full = j0 + NK - 1 <= place0 + w_first && (p.window == 0 || j0 > place0 + w_last - p.window || j0 + NK <= p.sinks);
+            uint32_t ok[KB];
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                ok[k] = __builtin_amdgcn_readfirstlane(masks[buffer * 4 + k]);
+                full = full && ok[k] == 0xffff;
+            }
+            if (!full) {
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int k = 0; k < KB; ++k)
+#pragma unroll
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = j0 + k * 16 + 4 * g + i;
+                            const bool see = j <= high[rt] && (j > low[rt] || j < p.sinks) && (ok[k] >> (4 * g + i) & 1);
+                            x[rt][k][i] = see ? x[rt][k][i] : kGone;
+                        }
+            }
+            u32x4 w[2][NP][US];
+            float by[2];
+            bool moved = false;
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) {
+                float top = kGone;
+#pragma unroll
+                for (int k = 0; k < KB; ++k)
+                    top = __builtin_fmaxf(__builtin_fmaxf(top, __builtin_fmaxf(x[rt][k].x, x[rt][k].y)), __builtin_fmaxf(x[rt][k].z, x[rt][k].w));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
+                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+                top = top == kGone ? kGone : top * scale;
+                const bool move = top > m[rt] + kRoom;
+                const float now = move ? top : m[rt];
+                by[rt] = move ? exp2_of(m[rt] - now) : 1.0f;
+                m[rt] = now;
+                moved = moved || move;
+                const float at = now == kGone ? 0.0f : now;
+                float sum = 0.0f;
+#pragma unroll
+                for (int k = 0; k < KB; ++k) {
+                    f32x4 e;
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) {
+                        e[i] = exp2_of(__builtin_fmaf(x[rt][k][i], scale, -at));
+                        if (!full) e[i] = x[rt][k][i] == kGone ? 0.0f : e[i];
+                    }
+                    sum += (e.x + e.y) + (e.z + e.w);
+#pragma unroll
+                    for (int c = 0; c < NP; ++c) {
+                        const u32x2 h = {pack(e.x, e.y, X()), pack(e.z, e.w, X())};
+                        w[rt][c][k >> 1][(k & 1) * 2] = h.x;
+                        w[rt][c][k >> 1][(k & 1) * 2 + 1] = h.y;
+                        if (c + 1 < NP) {
+                            const f32x2 a = unpack(h.x, X()), z = unpack(h.y, X());
+                            e -= f32x4{a.x, a.y, z.x, z.y};
+                        }
+                    }
+                }
+                l[rt] = __builtin_fmaf(l[rt], by[rt], sum);
+            }
+            if (__any(moved)) {
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) o[rt][d] *= by[rt];
+            }
+            bool odd = false;
+            auto column = [&](int d) {
+                return values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ g) << 4) + (n & 1) * 8;
+            };
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                if (16 * d >= p.D) continue;
+                const char* const at = column(d);
+#pragma unroll
+                for (int u = 0; u < US; ++u) {
+                    const u32x2 v0 = read_turned(at + 2 * u * DS * 1024), v1 = read_turned(at + (2 * u + 1) * DS * 1024);
+                    u32x4 v = {v0.x, v0.y, v1.x, v1.y};
+                    if (!full) v = numbers4<X>(v, odd);
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                        for (int c = 0; c < NP; ++c) o[rt][d] = mfma(v, w[rt][c][u], o[rt][d], X());
+                }
+            }
+            if (!full && __any(odd)) {
+                for (int kind = 0; kind < 3; ++kind) {
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) {
+                        u32x4 v[US];
+#pragma unroll
+                        for (int u = 0; u < US; ++u) {
+                            const u32x2 v0 = read_turned(column(d) + 2 * u * DS * 1024), v1 = read_turned(column(d) + (2 * u + 1) * DS * 1024);
+                            v[u] = marks4<X>(u32x4{v0.x, v0.y, v1.x, v1.y}, kind);
+                        }
+#pragma unroll
+                        for (int rt = 0; rt < 2; ++rt) {
+                            f32x4 count = {0, 0, 0, 0};
+#pragma unroll
+                            for (int u = 0; u < US; ++u) count = mfma(v[u], marks4<X>(w[rt][0][u], 3), count, X());
+                            o[rt][d] = met(o[rt][d], count, kind);
+                        }
+                    }
+                }
+            }
+        }
+        if (t + 1 < t_to) {
+            put_tile(buffer ^ 1);
+            ask_tile(t + 2);
+            ask_page(t + 3);
+        }
+        lds_only_barrier();
+    }
+
+#pragma unroll
+    for (int rt = 0; rt < 2; ++rt) {
+        l[rt] += __shfl_xor(l[rt], 16);
+        l[rt] += __shfl_xor(l[rt], 32);
+        if (!mine[rt]) continue;
+        const long long at = row[rt] * p.slots + blockIdx.z;
+        if (gridDim.z > 1 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
+#pragma unroll
+        for (int d = 0; d < DT; ++d) {
+            const int c = d * 16 + 4 * g;
+            if (c >= p.D) continue;
+            if (gridDim.z == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
+            else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
+        }
+    }
+}
+
+template <int DP>
+const void* chunk_kernel_types(bool f16, bool f32_out, int* rows, int* threads, int* lds)
+{
+    *rows = Chunk<DP>::kRows;
+    *threads = Chunk<DP>::kWaves * 64;
+    *lds = Chunk<DP>::kLds;
+    if (f16) return f32_out ? (const void*)&chunk_kernel<DP, _Float16, 2> : (const void*)&chunk_kernel<DP, _Float16, 1>;
+    return f32_out ? (const void*)&chunk_kernel<DP, __bf16, 3> : (const void*)&chunk_kernel<DP, __bf16, 1>;
+}
+
+}  // namespace ops
