@@ -166,9 +166,13 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     p.block = p.bound == 64    ? block_kernel_64(f16, f32_out, p.row_tiles, &p.block_lds)
               : p.bound == 128 ? block_kernel_128(f16, f32_out, p.row_tiles, &p.block_lds)
                                : block_kernel_256(f16, f32_out, p.row_tiles, &p.block_lds);
-    p.chunk = p.bound == 64    ? chunk_kernel_64(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds)
-              : p.bound == 128 ? chunk_kernel_128(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds)
-                               : chunk_kernel_256(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds);
+    // a chunk's kernel multiplies all the columns that it is made for
+    const auto chunk = c->head_size <= 64    ? chunk_kernel_64
+                       : c->head_size <= 96  ? chunk_kernel_96
+                       : c->head_size <= 128 ? chunk_kernel_128
+                       : c->head_size <= 192 ? chunk_kernel_192
+                                             : chunk_kernel_256;
+    p.chunk = chunk(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds);
     p.chunk_blocks = (int)(((long long)p.max_new * group + p.chunk_rows - 1) / p.chunk_rows);
     p.splits = 0;
     long long slots = p.units;

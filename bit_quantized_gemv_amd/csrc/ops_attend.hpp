@@ -67,8 +67,9 @@ __device__ __forceinline__ f32x2 unpack(uint32_t v, _Float16) { return __builtin
 
 // Values that are no numbers.  As a factor of a matrix product, the infinity or NaN of one key
 // would reach the rows that do not see the key too, by zero times infinity.  So where rows of a tile
-// see different keys, such values are taken out of the product; and if there were any, products
-// of marks count for every output the NaN, infinities and negative infinities that it sees.
+// see different keys, the values are looked at on their way to LDS.  If there are any, they are
+// taken out of the product, and products of marks count for every output the NaN, infinities
+// and negative infinities that it sees.
 constexpr uint32_t no_number(__bf16) { return 0x7f80; }       // the exponent
 constexpr uint32_t no_number(_Float16) { return 0x7c00; }
 constexpr uint32_t one(__bf16) { return 0x3f80; }
@@ -83,34 +84,57 @@ __device__ __forceinline__ uint32_t numbers(uint32_t w)
     return lo | hi;
 }
 template <class X>
-__device__ __forceinline__ u32x4 numbers4(u32x4 w, bool& odd)
+__device__ __forceinline__ u32x4 numbers4(u32x4 w)
 {
-    const u32x4 kept = {numbers<X>(w.x), numbers<X>(w.y), numbers<X>(w.z), numbers<X>(w.w)};
-    odd = odd || kept.x != w.x || kept.y != w.y || kept.z != w.z || kept.w != w.w;
-    return kept;
+    return u32x4{numbers<X>(w.x), numbers<X>(w.y), numbers<X>(w.z), numbers<X>(w.w)};
 }
-
-// ones where a value is a NaN (kind 0), an infinity (1), a negative infinity (2), or not zero (3)
-template <class X>
-__device__ __forceinline__ uint32_t marks(uint32_t w, int kind)
+// whether any value of the words is no number
+template <class X, int N>
+__device__ __forceinline__ bool any_odd(const u32x4 (&v)[N])
 {
     constexpr uint32_t E = no_number(X());
-    auto is = [&](uint32_t h) {
-        return kind == 0 ? (h & 0x7fff) > E : kind == 1 ? h == E : kind == 2 ? h == (0x8000 | E) : (h & 0x7fff) != 0;
-    };
-    return (is(w & 0xffff) ? one(X()) : 0) | (is(w >> 16) ? one(X()) << 16 : 0);
+    bool odd = false;
+#pragma unroll
+    for (int i = 0; i < N; ++i)
+#pragma unroll
+        for (int c = 0; c < 4; ++c) odd |= (v[i][c] & E) == E || (v[i][c] >> 16 & E) == E;
+    return odd;
+}
+
+// Ones where a value is of a kind: the bits of `mask` from `low` on, `more` values.
+struct Kind {
+    uint32_t mask, low, more;
+    float what;
+};
+template <class X>
+__device__ __forceinline__ Kind kind_of(int i)
+{
+    constexpr uint32_t E = no_number(X());
+    return Kind{i == 0 ? 0x7fffu : 0xffffu, i == 0 ? E + 1 : i == 1 ? E : 0x8000u | E, i == 0 ? 0x7ffe - E : 0u,
+                i == 0 ? __builtin_nanf("") : i == 1 ? -kGone : kGone};
 }
 template <class X>
-__device__ __forceinline__ u32x4 marks4(u32x4 w, int kind)
+__device__ __forceinline__ uint32_t marks(uint32_t w, Kind k)
 {
-    return u32x4{marks<X>(w.x, kind), marks<X>(w.y, kind), marks<X>(w.z, kind), marks<X>(w.w, kind)};
+    const uint32_t lo = (w & k.mask) - k.low <= k.more ? one(X()) : 0, hi = ((w >> 16) & k.mask) - k.low <= k.more ? one(X()) : 0;
+    return lo | hi << 16;
+}
+template <class X>
+__device__ __forceinline__ u32x4 marks4(u32x4 w, Kind k)
+{
+    return u32x4{marks<X>(w.x, k), marks<X>(w.y, k), marks<X>(w.z, k), marks<X>(w.w, k)};
+}
+// weights that are not zero
+template <class X>
+__device__ __forceinline__ u32x4 weighed(u32x4 w)
+{
+    return marks4<X>(w, Kind{0x7fff, 1, 0x7ffe, 0.0f});
 }
 // the output that has met `count` of them
-__device__ __forceinline__ f32x4 met(f32x4 o, f32x4 count, int kind)
+__device__ __forceinline__ f32x4 met(f32x4 o, f32x4 count, Kind k)
 {
-    const float what = kind == 0 ? __builtin_nanf("") : kind == 1 ? -kGone : kGone;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) o[i] = count[i] > 0.0f ? o[i] + what : o[i];
+    for (int i = 0; i < 4; ++i) o[i] = count[i] > 0.0f ? o[i] + k.what : o[i];
     return o;
 }
 
@@ -120,6 +144,32 @@ __device__ __forceinline__ void lds_only_barrier()
     __builtin_amdgcn_fence(__ATOMIC_RELEASE, "workgroup", "local");
     __builtin_amdgcn_s_barrier();
     __builtin_amdgcn_fence(__ATOMIC_ACQUIRE, "workgroup", "local");
+}
+
+// The larger of two scores.  fmax would first turn a signalling NaN, which a matrix product might
+// leave, into a quiet one, at an instruction for each; the median of three does not.
+__device__ __forceinline__ float larger(float a, float b) { return __builtin_amdgcn_fmed3f(a, b, -kGone); }
+
+// Over the four lanes that hold a row's numbers: 16 and 32 lanes apart.
+__device__ __forceinline__ float row_max(float x)
+{
+    const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    x = __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)a[0]), __builtin_bit_cast(float, (uint32_t)a[1]));
+    const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    return __builtin_fmaxf(__builtin_bit_cast(float, (uint32_t)b[0]), __builtin_bit_cast(float, (uint32_t)b[1]));
+}
+__device__ __forceinline__ float row_sum(float x)
+{
+    const auto a = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    x = __builtin_bit_cast(float, (uint32_t)a[0]) + __builtin_bit_cast(float, (uint32_t)a[1]);
+    const auto b = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(uint32_t, x), __builtin_bit_cast(uint32_t, x), false, false);
+    return __builtin_bit_cast(float, (uint32_t)b[0]) + __builtin_bit_cast(float, (uint32_t)b[1]);
+}
+
+// Whether a row sees a key: places up to `high`, above `low` or below `sinks`; without branches.
+__device__ __forceinline__ bool sees(int j, int high, int low, int sinks, uint32_t held)
+{
+    return (int)(j <= high) & ((int)(j > low) | (int)(j < sinks)) & (int)held & 1;
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
@@ -190,7 +240,9 @@ const void* block_kernel_128(bool f16, bool f32_out, int row_tiles, int* lds);
 const void* block_kernel_256(bool f16, bool f32_out, int row_tiles, int* lds);
 // The same for chunks, with the rows and threads of a workgroup.
 const void* chunk_kernel_64(bool f16, bool f32_out, int* rows, int* threads, int* lds);
+const void* chunk_kernel_96(bool f16, bool f32_out, int* rows, int* threads, int* lds);
 const void* chunk_kernel_128(bool f16, bool f32_out, int* rows, int* threads, int* lds);
+const void* chunk_kernel_192(bool f16, bool f32_out, int* rows, int* threads, int* lds);
 const void* chunk_kernel_256(bool f16, bool f32_out, int* rows, int* threads, int* lds);
 
 }  // namespace ops

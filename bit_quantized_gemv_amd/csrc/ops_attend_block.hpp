@@ -23,7 +23,7 @@ namespace ops {
 
 // queries of more than one tile of rows lie in LDS
 template <int DP, int NP, int NR>
-constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + (NR > 1 ? NR * DP * 32 : 0);
+constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + 16 + (NR > 1 ? NR * DP * 32 : 0);
 
 template <int DP, class X, int NP, int NR>
 __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParams p)
@@ -39,7 +39,8 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
     char* const weights = lds + kLeafBytes;
     float* const tops = reinterpret_cast<float*>(weights + NP * KT * 32);
     float* const sums = tops + 64;
-    char* const queries = reinterpret_cast<char*>(sums + 64);
+    uint32_t* const odds = reinterpret_cast<uint32_t*>(sums + 64);       // whether a wave has met values that are no numbers
+    char* const queries = reinterpret_cast<char*>(odds + 4);
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -164,7 +165,9 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
         uint32_t ok[TILES];
 #pragma unroll
         for (int t = 0; t < TILES; ++t) ok[t] = valid[t];
-        bool full = leaf + KT - 1 <= place0 + i_first && (p.window == 0 || leaf > place0 + i_last - p.window || leaf + KT <= p.sinks);
+        // whether all rows see the same places of the leaf, and whether those of this wave are all there
+        const bool even = leaf + KT - 1 <= place0 + i_first && (p.window == 0 || leaf > place0 + i_last - p.window || leaf + KT <= p.sinks);
+        bool full = even;
 #pragma unroll
         for (int t = 0; t < TILES; ++t) full = full && ok[t] == 0xffff;
 #pragma unroll
@@ -180,7 +183,6 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
                 f32x4 a = {0, 0, 0, 0};
 #pragma unroll
                 for (int d = 0; d < DS; ++d) {
-                    if (32 * d >= p.D) continue;
                     u32x4 k = kf[t][d];
                     if (!whole && 8 * (4 * d + g) >= p.D) k = u32x4{0, 0, 0, 0};
                     a = mfma(k, q[d], a, X());
@@ -193,20 +195,25 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
 #pragma unroll
                     for (int i = 0; i < 4; ++i) {
                         const int j = leaf + wave * WK + t * 16 + 4 * g + i;
-                        const bool sees = j <= high[rt] && (j > low[rt] || j < p.sinks) && (ok[t] >> (4 * g + i) & 1);
-                        x[t][i] = sees ? x[t][i] : kGone;
+                        x[t][i] = sees(j, high[rt], low[rt], p.sinks, ok[t] >> (4 * g + i)) ? x[t][i] : kGone;
                     }
             }
             // the leaf's largest score of the row
             float top = kGone;
 #pragma unroll
             for (int t = 0; t < TILES; ++t) top = __builtin_fmaxf(__builtin_fmaxf(top, __builtin_fmaxf(x[t].x, x[t].y)), __builtin_fmaxf(x[t].z, x[t].w));
-            top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-            top = __builtin_fmaxf(top, __shfl_xor(top, 32));
+            top = row_max(top);
             if (g == 0) tops[wave * 16 + n] = top;
             if (rt == NR - 1 && NR > 1 && next >= 0) ask_keys();
             lds_only_barrier();
             if (rt == 0) {
+                if (!even) {
+                    bool odd = false;
+#pragma unroll
+                    for (int t = 0; t < TILES; ++t) odd |= (ok[t] >> (lane >> 2) & 1) && any_odd<X, DS>(vf[t]);
+                    odd = __any(odd);
+                    if (lane == 0) odds[wave] = odd;
+                }
 #pragma unroll
                 for (int t = 0; t < TILES; ++t)
 #pragma unroll
@@ -241,8 +248,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
                     }
                 }
             }
-            sum += __shfl_xor(sum, 16);
-            sum += __shfl_xor(sum, 32);
+            sum = row_sum(sum);
             if (g == 0) sums[wave * 16 + n] = sum;
             lds_only_barrier();
             sum = (sums[n] + sums[16 + n]) + (sums[32 + n] + sums[48 + n]);
@@ -250,40 +256,50 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
 
             // the wave's columns over the leaf's keys
             f32x4 a[DT];
-            bool odd = false;
 #pragma unroll
             for (int d = 0; d < DT; ++d) a[d] = f32x4{0, 0, 0, 0};
-            const int i16 = lane & 15;
-            auto column = [&](int d) {
+            auto value = [&](int d, int k) {
                 const int tile = wave * DT + d;
-                return values + (tile >> 1) * 1024 + (4 * g + (i16 >> 2)) * 64 + ((((tile & 1) * 2 + ((i16 & 3) >> 1)) ^ g) << 4) + (i16 & 1) * 8;
+                const char* const at = values + (tile >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((tile & 1) * 2 + ((n & 3) >> 1)) ^ g) << 4) + (n & 1) * 8;
+                const u32x2 v0 = read_turned(at + 2 * k * DS * 1024), v1 = read_turned(at + (2 * k + 1) * DS * 1024);
+                return u32x4{v0.x, v0.y, v1.x, v1.y};
             };
+            if (even || __builtin_amdgcn_readfirstlane(odds[0] | odds[1] | odds[2] | odds[3]) == 0) {
 #pragma unroll
-            for (int k = 0; k < US; ++k) {
-                u32x4 w[NP];
+                for (int k = 0; k < US; ++k) {
+                    u32x4 w[NP];
 #pragma unroll
-                for (int c = 0; c < NP; ++c) w[c] = *reinterpret_cast<const u32x4*>(weights + c * KT * 32 + k * 1024 + lane * 16);
-#pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    const u32x2 v0 = read_turned(column(d) + 2 * k * DS * 1024), v1 = read_turned(column(d) + (2 * k + 1) * DS * 1024);
-                    u32x4 v = {v0.x, v0.y, v1.x, v1.y};
-                    if (!full) v = numbers4<X>(v, odd);
-#pragma unroll
-                    for (int c = 0; c < NP; ++c) a[d] = mfma(v, w[c], a[d], X());
-                }
-            }
-            if (!full && __any(odd)) {
-                for (int kind = 0; kind < 3; ++kind) {
+                    for (int c = 0; c < NP; ++c) w[c] = *reinterpret_cast<const u32x4*>(weights + c * KT * 32 + k * 1024 + lane * 16);
 #pragma unroll
                     for (int d = 0; d < DT; ++d) {
-                        f32x4 count = {0, 0, 0, 0};
-                        for (int k = 0; k < US; ++k) {
-                            const u32x2 v0 = read_turned(column(d) + 2 * k * DS * 1024), v1 = read_turned(column(d) + (2 * k + 1) * DS * 1024);
-                            const u32x4 w = *reinterpret_cast<const u32x4*>(weights + k * 1024 + lane * 16);
-                            count = mfma(marks4<X>(u32x4{v0.x, v0.y, v1.x, v1.y}, kind), marks4<X>(w, 3), count, X());
-                        }
-                        a[d] = met(a[d], count, kind);
+                        const u32x4 v = value(d, k);
+#pragma unroll
+                        for (int c = 0; c < NP; ++c) a[d] = mfma(v, w[c], a[d], X());
                     }
+                }
+            } else {
+#pragma unroll 1
+                for (int k = 0; k < US; ++k)
+#pragma unroll 1
+                    for (int c = 0; c < NP; ++c) {
+                        const u32x4 w = *reinterpret_cast<const u32x4*>(weights + c * KT * 32 + k * 1024 + lane * 16);
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) a[d] = mfma(numbers4<X>(value(d, k)), w, a[d], X());
+                    }
+#pragma unroll 1
+                for (int i = 0; i < 3; ++i) {
+                    const Kind kind = kind_of<X>(i);
+                    f32x4 count[DT];
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) count[d] = f32x4{0, 0, 0, 0};
+#pragma unroll 1
+                    for (int k = 0; k < US; ++k) {
+                        const u32x4 w = weighed<X>(*reinterpret_cast<const u32x4*>(weights + k * 1024 + lane * 16));
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) count[d] = mfma(marks4<X>(value(d, k), kind), w, count[d], X());
+                    }
+#pragma unroll
+                    for (int d = 0; d < DT; ++d) a[d] = met(a[d], count[d], kind);
                 }
             }
 #pragma unroll

@@ -10,17 +10,21 @@
 // costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
 // keys of a tile of rows, and a second launch joins them.
 #pragma once
+#include <type_traits>
+
 #include "ops_attend.hpp"
 
 namespace ops {
 
+// A workgroup of four waves, two of which fit a compute unit; of eight where heads are so
+// large that its registers are one's.
 template <int DP>
 struct Chunk {
-    static constexpr int kWaves = DP == 256 ? 8 : 4;
-    static constexpr int kKeys = DP == 256 ? 32 : 64;              // of a tile
+    static constexpr int kWaves = DP > 128 ? 8 : 4;
+    static constexpr int kKeys = DP > 192 ? 32 : 64;               // of a tile
     static constexpr int kRows = kWaves * 32;
     static constexpr int kTileBytes = kKeys * DP * 2;
-    static constexpr int kLds = 4 * kTileBytes + 2 * 16;           // keys and values, twice, and which keys there are
+    static constexpr int kLds = 4 * kTileBytes + 2 * 48;           // keys and values, twice, and what is known of them
 };
 
 constexpr float kRoom = 8.0f;
@@ -32,7 +36,8 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
     constexpr int NK = C::kKeys, KB = NK / 16, DS = DP / 32, DT = DP / 16, US = NK / 32;
     constexpr int BW = KB * DS / C::kWaves;       // blocks of 16 keys and 32 columns that a wave loads
     extern __shared__ __align__(16) char lds[];
-    uint32_t* const masks = reinterpret_cast<uint32_t*>(lds + 4 * C::kTileBytes);
+    uint32_t* const masks = reinterpret_cast<uint32_t*>(lds + 4 * C::kTileBytes);      // which keys there are
+    uint32_t* const odds = masks + 8;                                                   // whether a wave has met values that are no numbers
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -105,16 +110,30 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
             vr[d] = *reinterpret_cast<const u32x4*>(v + c * 16);
         }
     };
-    auto put_tile = [&](int buffer) {
+    // whether all of the workgroup's rows see the same places of a tile
+    auto even = [&](int j0) {
+        return j0 + NK - 1 <= place0 + i_first && (p.window == 0 || j0 > place0 + i_last - p.window || j0 + NK <= p.sinks);
+    };
+    auto put_tile = [&](int buffer, int t) {
         char* const at = lds + buffer * 2 * C::kTileBytes + (kb * DS + d0) * 1024 + (lane >> 2) * 64 + ((piece ^ (lane >> 4)) << 4);
         const uint64_t there = __ballot(held);
+        if (whole && there == ~0ull) {
 #pragma unroll
-        for (int d = 0; d < BW; ++d) {
-            u32x4 k = kr[d], v = vr[d];
-            if (!whole && 8 * (4 * (d0 + d) + piece) >= p.D) k = u32x4{0, 0, 0, 0};
-            if (there != ~0ull && !held) v = u32x4{0, 0, 0, 0};
-            *reinterpret_cast<u32x4*>(at + d * 1024) = k;
-            *reinterpret_cast<u32x4*>(at + C::kTileBytes + d * 1024) = v;
+            for (int d = 0; d < BW; ++d) {
+                *reinterpret_cast<u32x4*>(at + d * 1024) = kr[d];
+                *reinterpret_cast<u32x4*>(at + C::kTileBytes + d * 1024) = vr[d];
+            }
+        } else {
+            const u32x4 none = {0, 0, 0, 0};
+#pragma unroll
+            for (int d = 0; d < BW; ++d) {
+                *reinterpret_cast<u32x4*>(at + d * 1024) = 8 * (4 * (d0 + d) + piece) < p.D ? kr[d] : none;
+                *reinterpret_cast<u32x4*>(at + C::kTileBytes + d * 1024) = held ? vr[d] : none;
+            }
+        }
+        if (!even(vis.unit(t) * NK)) {
+            const uint32_t odd = __any(held && any_odd<X, BW>(vr)) ? 1 : 0;
+            if (lane == 0) odds[buffer * 8 + wave] = odd;
         }
         // one bit a key
         if (d0 == 0) {
@@ -123,11 +142,122 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
         }
     };
 
+    // one tile; FULL: every row sees all of its keys; ODD: it may hold values that are no numbers,
+    // which matters only where rows see different keys
+    auto tile = [&](auto full_, auto odd_, const char* keys, int j0, const uint32_t (&ok)[KB]) {
+        constexpr bool FULL = decltype(full_)::value, ODD = decltype(odd_)::value;
+        const char* const values = keys + C::kTileBytes;
+        f32x4 x[2][KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) {
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt) x[rt][k] = f32x4{0, 0, 0, 0};
+#pragma unroll
+            for (int d = 0; d < DS; ++d) {
+                const u32x4 f = *reinterpret_cast<const u32x4*>(keys + (k * DS + d) * 1024 + n * 64 + ((g ^ (n >> 2)) << 4));
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) x[rt][k] = mfma(f, q[rt][d], x[rt][k], X());
+            }
+        }
+        if constexpr (!FULL) {
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int j = j0 + k * 16 + 4 * g + i;
+                    const uint32_t held = ok[k] >> (4 * g + i);
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) x[rt][k][i] = sees(j, high[rt], low[rt], p.sinks, held) ? x[rt][k][i] : kGone;
+                }
+        }
+        u32x4 w[2][NP][US];
+        float by[2];
+        bool moved = false;
+#pragma unroll
+        for (int rt = 0; rt < 2; ++rt) {
+            float top = x[rt][0][0];
+#pragma unroll
+            for (int k = 0; k < KB; ++k)
+#pragma unroll
+                for (int i = 0; i < 4; ++i) top = k + i > 0 ? larger(top, x[rt][k][i]) : top;
+            top = row_max(top);
+            top = top == kGone ? kGone : top * scale;
+            const bool move = top > m[rt] + kRoom;
+            const float now = move ? top : m[rt];
+            by[rt] = move ? exp2_of(m[rt] - now) : 1.0f;
+            m[rt] = now;
+            moved = moved || move;
+            const float at = now == kGone ? 0.0f : now;
+            float sum = 0.0f;
+#pragma unroll
+            for (int k = 0; k < KB; ++k) {
+                f32x4 e;
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    e[i] = exp2_of(__builtin_fmaf(x[rt][k][i], scale, -at));
+                    if constexpr (!FULL) e[i] = x[rt][k][i] == kGone ? 0.0f : e[i];       // also where the scale is zero
+                }
+                sum += (e.x + e.y) + (e.z + e.w);
+#pragma unroll
+                for (int c = 0; c < NP; ++c) {
+                    const u32x2 h = {pack(e.x, e.y, X()), pack(e.z, e.w, X())};
+                    w[rt][c][k >> 1][(k & 1) * 2] = h.x;
+                    w[rt][c][k >> 1][(k & 1) * 2 + 1] = h.y;
+                    if (c + 1 < NP) {
+                        const f32x2 a = unpack(h.x, X()), z = unpack(h.y, X());
+                        e -= f32x4{a.x, a.y, z.x, z.y};
+                    }
+                }
+            }
+            l[rt] = __builtin_fmaf(l[rt], by[rt], sum);
+        }
+        if (__any(moved)) {
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                for (int d = 0; d < DT; ++d) o[rt][d] *= by[rt];
+        }
+        auto value = [&](int d, int u) {
+            const char* const at = values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ g) << 4) + (n & 1) * 8;
+            const u32x2 v0 = read_turned(at + 2 * u * DS * 1024), v1 = read_turned(at + (2 * u + 1) * DS * 1024);
+            return u32x4{v0.x, v0.y, v1.x, v1.y};
+        };
+#pragma unroll
+        for (int u = 0; u < US; ++u)
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                u32x4 v = value(d, u);
+                if constexpr (ODD) v = numbers4<X>(v);
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                    for (int c = 0; c < NP; ++c) o[rt][d] = mfma(v, w[rt][c][u], o[rt][d], X());
+            }
+        if constexpr (ODD)
+#pragma unroll 1
+            for (int i = 0; i < 3; ++i) {
+                const Kind kind = kind_of<X>(i);
+#pragma unroll
+                for (int d = 0; d < DT; ++d) {
+                    asm volatile("" ::: "memory");       // read again for every kind: registers are short
+                    f32x4 count[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+                    for (int u = 0; u < US; ++u) {
+                        const u32x4 v = marks4<X>(value(d, u), kind);
+#pragma unroll
+                        for (int rt = 0; rt < 2; ++rt) count[rt] = mfma(v, weighed<X>(w[rt][0][u]), count[rt], X());
+                    }
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) o[rt][d] = met(o[rt][d], count[rt], kind);
+                }
+            }
+    };
+
     if (t_from < t_to) {
         ask_page(t_from);
         ask_tile(t_from);
         ask_page(t_from + 1);
-        put_tile(0);
+        put_tile(0, t_from);
         ask_tile(t_from + 1);
         ask_page(t_from + 2);
     }
@@ -135,23 +265,9 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
     for (int t = t_from; t < t_to; ++t) {
         const int buffer = (t - t_from) & 1;
         const char* const keys = lds + buffer * 2 * C::kTileBytes;
-        const char* const values = keys + C::kTileBytes;
         const int j0 = vis.unit(t) * NK;
-        const bool sees = !idle && j0 <= place0 + w_last && (p.window == 0 || j0 + NK > place0 + w_first - p.window + 1 || j0 < p.sinks);
-        if (sees) {
-            f32x4 x[2][KB];
-#pragma unroll
-            for (int k = 0; k < KB; ++k) {
-#pragma unroll
-                for (int rt = 0; rt < 2; ++rt) x[rt][k] = f32x4{0, 0, 0, 0};
-#pragma unroll
-                for (int d = 0; d < DS; ++d) {
-                    if (32 * d >= p.D) continue;
-                    const u32x4 f = *reinterpret_cast<const u32x4*>(keys + (k * DS + d) * 1024 + n * 64 + ((g ^ (n >> 2)) << 4));
-#pragma unroll
-                    for (int rt = 0; rt < 2; ++rt) x[rt][k] = mfma(f, q[rt][d], x[rt][k], X());
-                }
-            }
+        const bool any = !idle && j0 <= place0 + w_last && (p.window == 0 || j0 + NK > place0 + w_first - p.window + 1 || j0 < p.sinks);
+        if (any) {
             bool full = j0 + NK - 1 <= place0 + w_first && (p.window == 0 || j0 > place0 + w_last - p.window || j0 + NK <= p.sinks);
             uint32_t ok[KB];
 #pragma unroll
@@ -159,107 +275,20 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                 ok[k] = __builtin_amdgcn_readfirstlane(masks[buffer * 4 + k]);
                 full = full && ok[k] == 0xffff;
             }
-            if (!full) {
+            if (__builtin_expect(full, 1)) {
+                tile(std::true_type(), std::false_type(), keys, j0, ok);
+            } else {
+                uint32_t odd = 0;
+                if (!even(j0)) {
 #pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                    for (int k = 0; k < KB; ++k)
-#pragma unroll
-                        for (int i = 0; i < 4; ++i) {
-                            const int j = j0 + k * 16 + 4 * g + i;
-                            const bool see = j <= high[rt] && (j > low[rt] || j < p.sinks) && (ok[k] >> (4 * g + i) & 1);
-                            x[rt][k][i] = see ? x[rt][k][i] : kGone;
-                        }
-            }
-            u32x4 w[2][NP][US];
-            float by[2];
-            bool moved = false;
-#pragma unroll
-            for (int rt = 0; rt < 2; ++rt) {
-                float top = kGone;
-#pragma unroll
-                for (int k = 0; k < KB; ++k)
-                    top = __builtin_fmaxf(__builtin_fmaxf(top, __builtin_fmaxf(x[rt][k].x, x[rt][k].y)), __builtin_fmaxf(x[rt][k].z, x[rt][k].w));
-                top = __builtin_fmaxf(top, __shfl_xor(top, 16));
-                top = __builtin_fmaxf(top, __shfl_xor(top, 32));
-                top = top == kGone ? kGone : top * scale;
-                const bool move = top > m[rt] + kRoom;
-                const float now = move ? top : m[rt];
-                by[rt] = move ? exp2_of(m[rt] - now) : 1.0f;
-                m[rt] = now;
-                moved = moved || move;
-                const float at = now == kGone ? 0.0f : now;
-                float sum = 0.0f;
-#pragma unroll
-                for (int k = 0; k < KB; ++k) {
-                    f32x4 e;
-#pragma unroll
-                    for (int i = 0; i < 4; ++i) {
-                        e[i] = exp2_of(__builtin_fmaf(x[rt][k][i], scale, -at));
-                        if (!full) e[i] = x[rt][k][i] == kGone ? 0.0f : e[i];
-                    }
-                    sum += (e.x + e.y) + (e.z + e.w);
-#pragma unroll
-                    for (int c = 0; c < NP; ++c) {
-                        const u32x2 h = {pack(e.x, e.y, X()), pack(e.z, e.w, X())};
-                        w[rt][c][k >> 1][(k & 1) * 2] = h.x;
-                        w[rt][c][k >> 1][(k & 1) * 2 + 1] = h.y;
-                        if (c + 1 < NP) {
-                            const f32x2 a = unpack(h.x, X()), z = unpack(h.y, X());
-                            e -= f32x4{a.x, a.y, z.x, z.y};
-                        }
-                    }
+                    for (int w = 0; w < C::kWaves; ++w) odd |= odds[buffer * 8 + w];
                 }
-                l[rt] = __builtin_fmaf(l[rt], by[rt], sum);
-            }
-            if (__any(moved)) {
-#pragma unroll
-                for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) o[rt][d] *= by[rt];
-            }
-            bool odd = false;
-            auto column = [&](int d) {
-                return values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ g) << 4) + (n & 1) * 8;
-            };
-#pragma unroll
-            for (int d = 0; d < DT; ++d) {
-                if (16 * d >= p.D) continue;
-                const char* const at = column(d);
-#pragma unroll
-                for (int u = 0; u < US; ++u) {
-                    const u32x2 v0 = read_turned(at + 2 * u * DS * 1024), v1 = read_turned(at + (2 * u + 1) * DS * 1024);
-                    u32x4 v = {v0.x, v0.y, v1.x, v1.y};
-                    if (!full) v = numbers4<X>(v, odd);
-#pragma unroll
-                    for (int rt = 0; rt < 2; ++rt)
-#pragma unroll
-                        for (int c = 0; c < NP; ++c) o[rt][d] = mfma(v, w[rt][c][u], o[rt][d], X());
-                }
-            }
-            if (!full && __any(odd)) {
-                for (int kind = 0; kind < 3; ++kind) {
-#pragma unroll
-                    for (int d = 0; d < DT; ++d) {
-                        u32x4 v[US];
-#pragma unroll
-                        for (int u = 0; u < US; ++u) {
-                            const u32x2 v0 = read_turned(column(d) + 2 * u * DS * 1024), v1 = read_turned(column(d) + (2 * u + 1) * DS * 1024);
-                            v[u] = marks4<X>(u32x4{v0.x, v0.y, v1.x, v1.y}, kind);
-                        }
-#pragma unroll
-                        for (int rt = 0; rt < 2; ++rt) {
-                            f32x4 count = {0, 0, 0, 0};
-#pragma unroll
-                            for (int u = 0; u < US; ++u) count = mfma(v[u], marks4<X>(w[rt][0][u], 3), count, X());
-                            o[rt][d] = met(o[rt][d], count, kind);
-                        }
-                    }
-                }
+                if (__builtin_expect(__builtin_amdgcn_readfirstlane(odd) == 0, 1)) tile(std::false_type(), std::false_type(), keys, j0, ok);
+                else tile(std::false_type(), std::true_type(), keys, j0, ok);
             }
         }
         if (t + 1 < t_to) {
-            put_tile(buffer ^ 1);
+            put_tile(buffer ^ 1, t + 1);
             ask_tile(t + 2);
             ask_page(t + 3);
         }

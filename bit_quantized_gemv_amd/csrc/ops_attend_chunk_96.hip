@@ -1,0 +1,8 @@
+// ops_attend_chunk_96.hip -- chunks of new tokens, heads of up to 96 values.
+#include "ops_attend_chunk.hpp"
+
+namespace ops {
+
+const void* chunk_kernel_96(bool f16, bool f32_out, int* rows, int* threads, int* lds) { return chunk_kernel_types<96>(f16, f32_out, rows, threads, lds); }
+
+}  // namespace ops
