@@ -9,9 +9,9 @@
 // lanes is the one in which a lane holds its weights already.  The values of V^T that belong
 // to it are four neighbouring keys of one column: what the transposing read of LDS gives.
 //
-// V in LDS: blocks of 16 keys and 32 columns, 64 bytes a key, the four 16-byte pieces of key
-// j at piece ^ (j / 4): the transposing read of a 16 x 16 tile then meets every bank twice,
-// which its 512 bytes do at best.
+// Keys and values in LDS: blocks of 16 keys and 32 columns, 64 bytes a key, the four 16-byte
+// pieces of key j at piece ^ swizzle(j / 4).  The reads of 16 keys' pieces and the transposing
+// reads of 16 x 16 values then meet every bank as often as their bytes need.
 #pragma once
 #include <hip/hip_runtime.h>
 
@@ -173,6 +173,9 @@ __device__ __forceinline__ bool sees(int j, int high, int low, int sinks, uint32
 }
 
 __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// 0, 2, 3, 1 for the keys 0-3, 4-7, 8-11, 12-15 of a block
+__device__ __forceinline__ int swizzle(int quarter) { return (quarter & 1) << 1 ^ (quarter >> 1) * 3; }
 
 __device__ __forceinline__ u32x2 read_turned(const char* lds)
 {

@@ -220,7 +220,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
                     for (int d = 0; d < DS; ++d) {
                         u32x4 v = vf[t][d];
                         if (!full && !(ok[t] >> (lane >> 2) & 1)) v = u32x4{0, 0, 0, 0};
-                        *reinterpret_cast<u32x4*>(values + ((wave * TILES + t) * DS + d) * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ (lane >> 4)) << 4)) = v;
+                        *reinterpret_cast<u32x4*>(values + ((wave * TILES + t) * DS + d) * 1024 + (lane >> 2) * 64 + (((lane & 3) ^ swizzle(lane >> 4)) << 4)) = v;
                     }
                 if (next >= 0) {
                     addresses(next, valid);
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
             for (int d = 0; d < DT; ++d) a[d] = f32x4{0, 0, 0, 0};
             auto value = [&](int d, int k) {
                 const int tile = wave * DT + d;
-                const char* const at = values + (tile >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((tile & 1) * 2 + ((n & 3) >> 1)) ^ g) << 4) + (n & 1) * 8;
+                const char* const at = values + (tile >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((tile & 1) * 2 + ((n & 3) >> 1)) ^ swizzle(g)) << 4) + (n & 1) * 8;
                 const u32x2 v0 = read_turned(at + 2 * k * DS * 1024), v1 = read_turned(at + (2 * k + 1) * DS * 1024);
                 return u32x4{v0.x, v0.y, v1.x, v1.y};
             };

@@ -79,7 +79,8 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
         }
     }
     f32x4 o[2][DT];
-    float m[2] = {kGone, kGone}, l[2] = {0.0f, 0.0f};
+    float m[2] = {kGone, kGone};
+    f32x4 l[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};       // a row's sum of weights, four times
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
@@ -115,7 +116,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
         return j0 + NK - 1 <= place0 + i_first && (p.window == 0 || j0 > place0 + i_last - p.window || j0 + NK <= p.sinks);
     };
     auto put_tile = [&](int buffer, int t) {
-        char* const at = lds + buffer * 2 * C::kTileBytes + (kb * DS + d0) * 1024 + (lane >> 2) * 64 + ((piece ^ (lane >> 4)) << 4);
+        char* const at = lds + buffer * 2 * C::kTileBytes + (kb * DS + d0) * 1024 + (lane >> 2) * 64 + ((piece ^ swizzle(lane >> 4)) << 4);
         const uint64_t there = __ballot(held);
         if (whole && there == ~0ull) {
 #pragma unroll
@@ -154,7 +155,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
             for (int rt = 0; rt < 2; ++rt) x[rt][k] = f32x4{0, 0, 0, 0};
 #pragma unroll
             for (int d = 0; d < DS; ++d) {
-                const u32x4 f = *reinterpret_cast<const u32x4*>(keys + (k * DS + d) * 1024 + n * 64 + ((g ^ (n >> 2)) << 4));
+                const u32x4 f = *reinterpret_cast<const u32x4*>(keys + (k * DS + d) * 1024 + n * 64 + ((g ^ swizzle(n >> 2)) << 4));
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt) x[rt][k] = mfma(f, q[rt][d], x[rt][k], X());
             }
@@ -188,7 +189,6 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
             m[rt] = now;
             moved = moved || move;
             const float at = now == kGone ? 0.0f : now;
-            float sum = 0.0f;
 #pragma unroll
             for (int k = 0; k < KB; ++k) {
                 f32x4 e;
@@ -197,7 +197,6 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                     e[i] = exp2_of(__builtin_fmaf(x[rt][k][i], scale, -at));
                     if constexpr (!FULL) e[i] = x[rt][k][i] == kGone ? 0.0f : e[i];       // also where the scale is zero
                 }
-                sum += (e.x + e.y) + (e.z + e.w);
 #pragma unroll
                 for (int c = 0; c < NP; ++c) {
                     const u32x2 h = {pack(e.x, e.y, X()), pack(e.z, e.w, X())};
@@ -209,21 +208,28 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                     }
                 }
             }
-            l[rt] = __builtin_fmaf(l[rt], by[rt], sum);
         }
         if (__any(moved)) {
 #pragma unroll
-            for (int rt = 0; rt < 2; ++rt)
+            for (int rt = 0; rt < 2; ++rt) {
+                l[rt] *= by[rt];
 #pragma unroll
                 for (int d = 0; d < DT; ++d) o[rt][d] *= by[rt];
+            }
         }
         auto value = [&](int d, int u) {
-            const char* const at = values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ g) << 4) + (n & 1) * 8;
+            const char* const at = values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ swizzle(g)) << 4) + (n & 1) * 8;
             const u32x2 v0 = read_turned(at + 2 * u * DS * 1024), v1 = read_turned(at + (2 * u + 1) * DS * 1024);
             return u32x4{v0.x, v0.y, v1.x, v1.y};
         };
+        // sums of the weights as they are multiplied, by the matrix product of ones
+        const u32x4 ones = u32x4{0x10001, 0x10001, 0x10001, 0x10001} * one(X());
 #pragma unroll
-        for (int u = 0; u < US; ++u)
+        for (int u = 0; u < US; ++u) {
+#pragma unroll
+            for (int rt = 0; rt < 2; ++rt)
+#pragma unroll
+                for (int c = 0; c < NP; ++c) l[rt] = mfma(ones, w[rt][c][u], l[rt], X());
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
                 u32x4 v = value(d, u);
@@ -233,6 +239,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
 #pragma unroll
                     for (int c = 0; c < NP; ++c) o[rt][d] = mfma(v, w[rt][c][u], o[rt][d], X());
             }
+        }
         if constexpr (ODD)
 #pragma unroll 1
             for (int i = 0; i < 3; ++i) {
@@ -297,16 +304,14 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
 
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
-        l[rt] += __shfl_xor(l[rt], 16);
-        l[rt] += __shfl_xor(l[rt], 32);
         if (!mine[rt]) continue;
         const long long at = row[rt] * p.slots + blockIdx.z;
-        if (gridDim.z > 1 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
+        if (gridDim.z > 1 && g == 0) p.stat[at] = f32x2{m[rt], l[rt].x};
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             const int c = d * 16 + 4 * g;
             if (c >= p.D) continue;
-            if (gridDim.z == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
+            if (gridDim.z == 1) put_result(p, row[rt], c, o[rt][d], l[rt].x);
             else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
         }
     }
