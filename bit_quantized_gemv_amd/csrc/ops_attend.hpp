@@ -67,7 +67,7 @@ __device__ __forceinline__ f32x2 unpack(uint32_t v, _Float16) { return __builtin
 
 // Values that are no numbers.  As a factor of a matrix product, the infinity or NaN of one key
 // would reach the rows that do not see the key too, by zero times infinity.  So where rows of a tile
-// see different keys, the values are looked at on their way to LDS.  If there are any, they are
+// see different keys, the values are looked at in LDS first.  If there are any, they are
 // taken out of the product, and products of marks count for every output the NaN, infinities
 // and negative infinities that it sees.
 constexpr uint32_t no_number(__bf16) { return 0x7f80; }       // the exponent
@@ -88,17 +88,15 @@ __device__ __forceinline__ u32x4 numbers4(u32x4 w)
 {
     return u32x4{numbers<X>(w.x), numbers<X>(w.y), numbers<X>(w.z), numbers<X>(w.w)};
 }
-// whether any value of the words is no number
-template <class X, int N>
-__device__ __forceinline__ bool any_odd(const u32x4 (&v)[N])
+// whether a value of the words is no number
+template <class X>
+__device__ __forceinline__ bool odd(u32x4 v)
 {
     constexpr uint32_t E = no_number(X());
-    bool odd = false;
+    bool r = false;
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-#pragma unroll
-        for (int c = 0; c < 4; ++c) odd |= (v[i][c] & E) == E || (v[i][c] >> 16 & E) == E;
-    return odd;
+    for (int c = 0; c < 4; ++c) r |= (v[c] & E) == E || (v[c] >> 16 & E) == E;
+    return r;
 }
 
 // Ones where a value is of a kind: the bits of `mask` from `low` on, `more` values.
@@ -176,6 +174,21 @@ __device__ __forceinline__ float exp2_of(float x) { return __builtin_amdgcn_exp2
 
 // 0, 2, 3, 1 for the keys 0-3, 4-7, 8-11, 12-15 of a block
 __device__ __forceinline__ int swizzle(int quarter) { return (quarter & 1) << 1 ^ (quarter >> 1) * 3; }
+
+// 16 bytes a lane from memory to LDS, the wave's 1024 one after the other from `to` on, without
+// registers between.  Written out, since the compiler would wait for it before any read of
+// LDS; whoever reads the bytes waits with landed(), then passes a barrier.
+__device__ __forceinline__ void send_to_lds(const char* from, uint32_t to)
+{
+    asm volatile("s_mov_b32 m0, %1\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, off" ::"v"(from), "s"(to) : "memory", "m0");
+}
+__device__ __forceinline__ void landed() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ uint32_t lds_address(const char* at)
+{
+    typedef __attribute__((address_space(3))) const char* At;
+    return (uint32_t)(uintptr_t)(At)at;
+}
 
 __device__ __forceinline__ u32x2 read_turned(const char* lds)
 {

@@ -208,11 +208,13 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
             lds_only_barrier();
             if (rt == 0) {
                 if (!even) {
-                    bool odd = false;
+                    bool found = false;
 #pragma unroll
-                    for (int t = 0; t < TILES; ++t) odd |= (ok[t] >> (lane >> 2) & 1) && any_odd<X, DS>(vf[t]);
-                    odd = __any(odd);
-                    if (lane == 0) odds[wave] = odd;
+                    for (int t = 0; t < TILES; ++t)
+#pragma unroll
+                        for (int d = 0; d < DS; ++d) found |= (ok[t] >> (lane >> 2) & 1) && odd<X>(vf[t][d]);
+                    found = __any(found);
+                    if (lane == 0) odds[wave] = found;
                 }
 #pragma unroll
                 for (int t = 0; t < TILES; ++t)

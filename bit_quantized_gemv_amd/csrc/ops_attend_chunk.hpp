@@ -4,7 +4,7 @@
 // Bound by the matrix instructions and, beside them, the exponentials.  A workgroup takes
 // 32 query rows a wave (tokens times the heads that share a head of the cache), kept in
 // registers with their outputs, and walks the keys that they see in tiles through LDS, the
-// next tile's on their way in registers meanwhile.  A wave scores 32 rows against the tile,
+// next tile's on their way there meanwhile.  A wave scores 32 rows against the tile,
 // takes the weights with the rows' running maxima, and adds the weighted values up; a maximum
 // is followed only when it has grown by 2^8, which weights and sums have room for, since moving it
 // costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
@@ -88,53 +88,47 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
 
     // what this wave loads of a tile: rows lane / 4 of tile kb, columns from 32 d0 on
     const int kb = wave * BW / DS, d0 = wave * BW % DS;
-    const int key_row = kb * 16 + (lane >> 2), piece = lane & 3;
-    const bool whole = p.D == DP;
-    u32x4 kr[BW], vr[BW];
+    const int key_row = kb * 16 + (lane >> 2), piece = (lane & 3) ^ swizzle(lane >> 4);
+    const uint32_t lds_at = lds_address(lds) + (kb * DS + d0) * 1024;
     bool held = false;
     int entry = 0;
     auto place_of = [&](int t) { return vis.unit(t) * NK + key_row; };
     auto ask_page = [&](int t) {
         if (t < t_to) entry = p.cache.pages[b * p.cache.pages_row + page_index(p.cache, min(place_of(t), s.length - 1))];
     };
-    auto ask_tile = [&](int t) {
+    auto ask_tile = [&](int buffer, int t) {
         if (t >= t_to) return;
         const int j = place_of(t);
         held = j < s.length && (uint32_t)entry < (uint32_t)p.cache.n_pages;
         const int slot = held ? j - page_index(p.cache, j) * p.cache.page_size : 0, page = held ? entry : 0;
-        const char* k = p.cache.k + page * p.cache.k_page + slot * p.cache.k_slot + head * p.cache.k_head;
-        const char* v = p.cache.v + page * p.cache.v_page + slot * p.cache.v_slot + head * p.cache.v_head;
+        const char* k = p.cache.k + page * p.cache.k_page + slot * p.cache.k_slot + head * p.cache.k_head + (4 * d0 + piece) * 16;
+        const char* v = p.cache.v + page * p.cache.v_page + slot * p.cache.v_slot + head * p.cache.v_head + (4 * d0 + piece) * 16;
+        const uint32_t to = lds_at + buffer * 2 * C::kTileBytes;
 #pragma unroll
-        for (int d = 0; d < BW; ++d) {
-            const int c = whole ? 4 * (d0 + d) + piece : min(4 * (d0 + d) + piece, (p.D >> 3) - 1);
-            kr[d] = *reinterpret_cast<const u32x4*>(k + c * 16);
-            vr[d] = *reinterpret_cast<const u32x4*>(v + c * 16);
-        }
+        for (int d = 0; d < BW; ++d)
+            if (8 * (4 * (d0 + d) + piece) < p.D) {       // columns above D stay the zeros that they are
+                send_to_lds(k + d * 64, to + d * 1024);
+                send_to_lds(v + d * 64, to + C::kTileBytes + d * 1024);
+            }
     };
     // whether all of the workgroup's rows see the same places of a tile
     auto even = [&](int j0) {
         return j0 + NK - 1 <= place0 + i_first && (p.window == 0 || j0 > place0 + i_last - p.window || j0 + NK <= p.sinks);
     };
-    auto put_tile = [&](int buffer, int t) {
-        char* const at = lds + buffer * 2 * C::kTileBytes + (kb * DS + d0) * 1024 + (lane >> 2) * 64 + ((piece ^ swizzle(lane >> 4)) << 4);
+    auto land = [&](int buffer, int t) {
+        landed();
+        char* const mine_at = lds + (buffer * 2 + 1) * C::kTileBytes + (kb * DS + d0) * 1024 + lane * 16;
         const uint64_t there = __ballot(held);
-        if (whole && there == ~0ull) {
+        if (there != ~0ull && !held) {
 #pragma unroll
-            for (int d = 0; d < BW; ++d) {
-                *reinterpret_cast<u32x4*>(at + d * 1024) = kr[d];
-                *reinterpret_cast<u32x4*>(at + C::kTileBytes + d * 1024) = vr[d];
-            }
-        } else {
-            const u32x4 none = {0, 0, 0, 0};
-#pragma unroll
-            for (int d = 0; d < BW; ++d) {
-                *reinterpret_cast<u32x4*>(at + d * 1024) = 8 * (4 * (d0 + d) + piece) < p.D ? kr[d] : none;
-                *reinterpret_cast<u32x4*>(at + C::kTileBytes + d * 1024) = held ? vr[d] : none;
-            }
+            for (int d = 0; d < BW; ++d) *reinterpret_cast<u32x4*>(mine_at + d * 1024) = u32x4{0, 0, 0, 0};
         }
         if (!even(vis.unit(t) * NK)) {
-            const uint32_t odd = __any(held && any_odd<X, BW>(vr)) ? 1 : 0;
-            if (lane == 0) odds[buffer * 8 + wave] = odd;
+            bool found = false;
+#pragma unroll
+            for (int d = 0; d < BW; ++d) found |= odd<X>(*reinterpret_cast<const u32x4*>(mine_at + d * 1024));
+            const uint32_t any = __any(found) ? 1 : 0;
+            if (lane == 0) odds[buffer * 8 + wave] = any;
         }
         // one bit a key
         if (d0 == 0) {
@@ -260,15 +254,19 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
             }
     };
 
+    if (p.D < DP) {
+        for (int i = threadIdx.x * 16; i < 4 * C::kTileBytes; i += C::kWaves * 1024) *reinterpret_cast<u32x4*>(lds + i) = u32x4{0, 0, 0, 0};
+        lds_only_barrier();
+    }
     if (t_from < t_to) {
         ask_page(t_from);
-        ask_tile(t_from);
+        ask_tile(0, t_from);
         ask_page(t_from + 1);
-        put_tile(0, t_from);
-        ask_tile(t_from + 1);
-        ask_page(t_from + 2);
+        land(0, t_from);
     }
     lds_only_barrier();
+    ask_tile(1, t_from + 1);
+    ask_page(t_from + 2);
     for (int t = t_from; t < t_to; ++t) {
         const int buffer = (t - t_from) & 1;
         const char* const keys = lds + buffer * 2 * C::kTileBytes;
@@ -294,12 +292,10 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                 else tile(std::false_type(), std::true_type(), keys, j0, ok);
             }
         }
-        if (t + 1 < t_to) {
-            put_tile(buffer ^ 1, t + 1);
-            ask_tile(t + 2);
-            ask_page(t + 3);
-        }
+        if (t + 1 < t_to) land(buffer ^ 1, t + 1);
         lds_only_barrier();
+        ask_tile(buffer, t + 2);
+        ask_page(t + 3);
     }
 
 #pragma unroll
