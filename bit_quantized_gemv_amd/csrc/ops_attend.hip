@@ -12,6 +12,7 @@ namespace ops {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kUnits = 256;                // compute units
 
 constexpr int kLanes = 16;                 // of a row's 64 columns
 constexpr int kChains = kThreads / kLanes;
@@ -131,9 +132,10 @@ struct Plan {
     int bound, leaf;
     int row_tiles, row_blocks, per_unit;          // blocks: a workgroup's tiles of rows, and a unit's leaves
     long long units;                              // of a sequence, at most
-    int chunk_rows, chunk_blocks, splits;         // chunks: a workgroup's rows, and the shares of their keys
+    int chunk_blocks, splits;                     // chunks: tiles of rows, and the shares of their keys
     const void *block, *chunk;
-    int block_lds, chunk_lds, chunk_threads;
+    int block_lds;
+    ChunkShape shape;
     long long part_bytes, stat_bytes;
 };
 
@@ -172,14 +174,14 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
                        : c->head_size <= 128 ? chunk_kernel_128
                        : c->head_size <= 192 ? chunk_kernel_192
                                              : chunk_kernel_256;
-    p.chunk = chunk(f16, f32_out, &p.chunk_rows, &p.chunk_threads, &p.chunk_lds);
-    p.chunk_blocks = (int)(((long long)p.max_new * group + p.chunk_rows - 1) / p.chunk_rows);
+    p.chunk = chunk(f16, f32_out, &p.shape);
+    p.chunk_blocks = (int)(((long long)p.max_new * group + p.shape.rows - 1) / p.shape.rows);
     p.splits = 0;
     long long slots = p.units;
     if (p.max_new > kBlockTokens) {
-        // as many shares as two workgroups of four waves per compute unit, of 512 keys at least
-        const long long groups = (long long)p.chunk_blocks * c->heads * c->n_seqs, room = 131072 / p.chunk_threads / groups;
-        const long long most = (std::min<long long>(p.length, p.window ? (long long)p.window + p.sinks + p.chunk_rows / group : p.length) + 511) / 512;
+        // as many shares as there is room for on the compute units, of 512 keys at least
+        const long long groups = (long long)p.chunk_blocks * c->heads * c->n_seqs, room = kUnits * p.shape.at_once / groups;
+        const long long most = (std::min<long long>(p.length, p.window ? (long long)p.window + p.sinks + p.shape.rows / group : p.length) + 511) / 512;
         p.splits = (int)std::max<long long>(1, std::min(room, most));
         slots = std::max<long long>(slots, p.splits);
     }
@@ -264,7 +266,8 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.slots = p.units = (int)plan.units;
     p.row_blocks = plan.row_blocks;
     p.per_unit = plan.per_unit;
-    p.scale = scale * 1.44269504088896340736f;
+    // a scale of zero weighs all places that are seen alike; the smallest does so too, and hides the others
+    p.scale = scale == 0.0f ? 1e-37f : scale * 1.44269504088896340736f;
     p.cache = device_cache(c, T);
     p.cache.max_places = plan.length;
     void* args[] = {&p};
@@ -273,7 +276,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
         if (int e = launch_join(p, plan, 0, c->n_seqs, stream)) return e;
     if (plan.max_new > kBlockTokens) {
         p.slots = plan.splits;
-        if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.chunk_threads, args, plan.chunk_lds, stream)) return e;
+        if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
         if (plan.splits > 1)
             if (int e = launch_join(p, plan, plan.splits, c->n_seqs, stream)) return e;
     }

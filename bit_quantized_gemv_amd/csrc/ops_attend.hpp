@@ -254,11 +254,14 @@ __device__ __forceinline__ void put_result(const AttendParams& p, long long row,
 const void* block_kernel_64(bool f16, bool f32_out, int row_tiles, int* lds);
 const void* block_kernel_128(bool f16, bool f32_out, int row_tiles, int* lds);
 const void* block_kernel_256(bool f16, bool f32_out, int row_tiles, int* lds);
-// The same for chunks, with the rows and threads of a workgroup.
-const void* chunk_kernel_64(bool f16, bool f32_out, int* rows, int* threads, int* lds);
-const void* chunk_kernel_96(bool f16, bool f32_out, int* rows, int* threads, int* lds);
-const void* chunk_kernel_128(bool f16, bool f32_out, int* rows, int* threads, int* lds);
-const void* chunk_kernel_192(bool f16, bool f32_out, int* rows, int* threads, int* lds);
-const void* chunk_kernel_256(bool f16, bool f32_out, int* rows, int* threads, int* lds);
+struct ChunkShape {
+    int rows, threads;       // of a workgroup
+    int at_once, lds;        // workgroups on a compute unit
+};
+const void* chunk_kernel_64(bool f16, bool f32_out, ChunkShape* shape);
+const void* chunk_kernel_96(bool f16, bool f32_out, ChunkShape* shape);
+const void* chunk_kernel_128(bool f16, bool f32_out, ChunkShape* shape);
+const void* chunk_kernel_192(bool f16, bool f32_out, ChunkShape* shape);
+const void* chunk_kernel_256(bool f16, bool f32_out, ChunkShape* shape);
 
 }  // namespace ops

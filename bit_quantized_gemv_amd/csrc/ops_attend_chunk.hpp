@@ -10,27 +10,26 @@
 // costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
 // keys of a tile of rows, and a second launch joins them.
 #pragma once
-#include <type_traits>
-
 #include "ops_attend.hpp"
 
 namespace ops {
 
-// A workgroup of four waves, two of which fit a compute unit; of eight where heads are so
-// large that its registers are one's.
+// Two workgroups of four waves on a compute unit, or one where heads are so large that a
+// wave's outputs and queries fill half of the registers.
 template <int DP>
 struct Chunk {
-    static constexpr int kWaves = DP > 128 ? 8 : 4;
-    static constexpr int kKeys = DP > 192 ? 32 : 64;               // of a tile
+    static constexpr int kWaves = 4;
+    static constexpr int kAtOnce = DP > 192 ? 1 : 2;
+    static constexpr int kKeys = DP > 128 && DP <= 192 ? 32 : 64;  // of a tile
     static constexpr int kRows = kWaves * 32;
     static constexpr int kTileBytes = kKeys * DP * 2;
-    static constexpr int kLds = 4 * kTileBytes + 2 * 48;           // keys and values, twice, and what is known of them
+    static constexpr int kLds = 4 * kTileBytes + 2 * 32;           // keys and values, twice, and what is known of them
 };
 
 constexpr float kRoom = 8.0f;
 
 template <int DP, class X, int NP>
-__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(AttendParams p)
+__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce) void chunk_kernel(AttendParams p)
 {
     typedef Chunk<DP> C;
     constexpr int NK = C::kKeys, KB = NK / 16, DS = DP / 32, DT = DP / 16, US = NK / 32;
@@ -128,7 +127,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
 #pragma unroll
             for (int d = 0; d < BW; ++d) found |= odd<X>(*reinterpret_cast<const u32x4*>(mine_at + d * 1024));
             const uint32_t any = __any(found) ? 1 : 0;
-            if (lane == 0) odds[buffer * 8 + wave] = any;
+            if (lane == 0) odds[buffer * 4 + wave] = any;
         }
         // one bit a key
         if (d0 == 0) {
@@ -137,10 +136,14 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
         }
     };
 
-    // one tile; FULL: every row sees all of its keys; ODD: it may hold values that are no numbers,
-    // which matters only where rows see different keys
-    auto tile = [&](auto full_, auto odd_, const char* keys, int j0, const uint32_t (&ok)[KB]) {
-        constexpr bool FULL = decltype(full_)::value, ODD = decltype(odd_)::value;
+    // a tile of 16 columns and 32 keys, turned over
+    auto value = [&](const char* values, int d, int u) {
+        const char* const at = values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ swizzle(g)) << 4) + (n & 1) * 8;
+        const u32x2 v0 = read_turned(at + 2 * u * DS * 1024), v1 = read_turned(at + (2 * u + 1) * DS * 1024);
+        return u32x4{v0.x, v0.y, v1.x, v1.y};
+    };
+    // one tile of a wave; full: every row sees all of its keys
+    auto tile = [&](bool full, const char* keys, int j0, const uint32_t (&ok)[KB]) {
         const char* const values = keys + C::kTileBytes;
         f32x4 x[2][KB];
 #pragma unroll
@@ -154,7 +157,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                 for (int rt = 0; rt < 2; ++rt) x[rt][k] = mfma(f, q[rt][d], x[rt][k], X());
             }
         }
-        if constexpr (!FULL) {
+        if (!full) {
 #pragma unroll
             for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -176,7 +179,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
 #pragma unroll
                 for (int i = 0; i < 4; ++i) top = k + i > 0 ? larger(top, x[rt][k][i]) : top;
             top = row_max(top);
-            top = top == kGone ? kGone : top * scale;
+            top *= scale;
             const bool move = top > m[rt] + kRoom;
             const float now = move ? top : m[rt];
             by[rt] = move ? exp2_of(m[rt] - now) : 1.0f;
@@ -187,10 +190,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
             for (int k = 0; k < KB; ++k) {
                 f32x4 e;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    e[i] = exp2_of(__builtin_fmaf(x[rt][k][i], scale, -at));
-                    if constexpr (!FULL) e[i] = x[rt][k][i] == kGone ? 0.0f : e[i];       // also where the scale is zero
-                }
+                for (int i = 0; i < 4; ++i) e[i] = exp2_of(__builtin_fmaf(x[rt][k][i], scale, -at));
 #pragma unroll
                 for (int c = 0; c < NP; ++c) {
                     const u32x2 h = {pack(e.x, e.y, X()), pack(e.z, e.w, X())};
@@ -211,11 +211,6 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                 for (int d = 0; d < DT; ++d) o[rt][d] *= by[rt];
             }
         }
-        auto value = [&](int d, int u) {
-            const char* const at = values + (d >> 1) * 1024 + (4 * g + (n >> 2)) * 64 + ((((d & 1) * 2 + ((n & 3) >> 1)) ^ swizzle(g)) << 4) + (n & 1) * 8;
-            const u32x2 v0 = read_turned(at + 2 * u * DS * 1024), v1 = read_turned(at + (2 * u + 1) * DS * 1024);
-            return u32x4{v0.x, v0.y, v1.x, v1.y};
-        };
         // sums of the weights as they are multiplied, by the matrix product of ones
         const u32x4 ones = u32x4{0x10001, 0x10001, 0x10001, 0x10001} * one(X());
 #pragma unroll
@@ -226,32 +221,52 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
                 for (int c = 0; c < NP; ++c) l[rt] = mfma(ones, w[rt][c][u], l[rt], X());
 #pragma unroll
             for (int d = 0; d < DT; ++d) {
-                u32x4 v = value(d, u);
-                if constexpr (ODD) v = numbers4<X>(v);
+                const u32x4 v = value(values, d, u);
 #pragma unroll
                 for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
                     for (int c = 0; c < NP; ++c) o[rt][d] = mfma(v, w[rt][c][u], o[rt][d], X());
             }
         }
-        if constexpr (ODD)
-#pragma unroll 1
-            for (int i = 0; i < 3; ++i) {
-                const Kind kind = kind_of<X>(i);
+    };
+
+    // A tile of which the workgroup's rows see different places, and which holds values that are no
+    // numbers: they go to the outputs of the rows that see them, and out of the tile.
+    auto clean = [&](char* values, int j0, const uint32_t (&ok)[KB]) {
+        u32x4 seen[2][US];
 #pragma unroll
-                for (int d = 0; d < DT; ++d) {
-                    asm volatile("" ::: "memory");       // read again for every kind: registers are short
-                    f32x4 count[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+        for (int rt = 0; rt < 2; ++rt)
 #pragma unroll
-                    for (int u = 0; u < US; ++u) {
-                        const u32x4 v = marks4<X>(value(d, u), kind);
+            for (int k = 0; k < KB; ++k)
 #pragma unroll
-                        for (int rt = 0; rt < 2; ++rt) count[rt] = mfma(v, weighed<X>(w[rt][0][u]), count[rt], X());
-                    }
-#pragma unroll
-                    for (int rt = 0; rt < 2; ++rt) o[rt][d] = met(o[rt][d], count[rt], kind);
+                for (int i = 0; i < 2; ++i) {
+                    const int j = j0 + k * 16 + 4 * g + 2 * i;
+                    const uint32_t held = ok[k] >> (4 * g + 2 * i);
+                    seen[rt][k >> 1][(k & 1) * 2 + i] = (sees(j, high[rt], low[rt], p.sinks, held) ? one(X()) : 0) |
+                                                        (sees(j + 1, high[rt], low[rt], p.sinks, held >> 1) ? one(X()) << 16 : 0);
                 }
+#pragma unroll 1
+        for (int i = 0; i < 3; ++i) {
+            const Kind kind = kind_of<X>(i);
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                asm volatile("" ::: "memory");       // read again for every kind: registers are short
+                f32x4 count[2] = {{0, 0, 0, 0}, {0, 0, 0, 0}};
+#pragma unroll
+                for (int u = 0; u < US; ++u) {
+                    const u32x4 v = marks4<X>(value(values, d, u), kind);
+#pragma unroll
+                    for (int rt = 0; rt < 2; ++rt) count[rt] = mfma(v, seen[rt][u], count[rt], X());
+                }
+#pragma unroll
+                for (int rt = 0; rt < 2; ++rt) o[rt][d] = met(o[rt][d], count[rt], kind);
             }
+        }
+        lds_only_barrier();
+        char* const at = values + (kb * DS + d0) * 1024 + lane * 16;
+#pragma unroll
+        for (int d = 0; d < BW; ++d) *reinterpret_cast<u32x4*>(at + d * 1024) = numbers4<X>(*reinterpret_cast<const u32x4*>(at + d * 1024));
+        lds_only_barrier();
     };
 
     if (p.D < DP) {
@@ -269,28 +284,23 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
     ask_page(t_from + 2);
     for (int t = t_from; t < t_to; ++t) {
         const int buffer = (t - t_from) & 1;
-        const char* const keys = lds + buffer * 2 * C::kTileBytes;
+        char* const keys = lds + buffer * 2 * C::kTileBytes;
         const int j0 = vis.unit(t) * NK;
+        uint32_t ok[KB];
+#pragma unroll
+        for (int k = 0; k < KB; ++k) ok[k] = __builtin_amdgcn_readfirstlane(masks[buffer * 4 + k]);
+        if (!even(j0)) {
+            uint32_t odd = 0;
+#pragma unroll
+            for (int w = 0; w < C::kWaves; ++w) odd |= odds[buffer * 4 + w];
+            if (__builtin_expect(__builtin_amdgcn_readfirstlane(odd) != 0, 0)) clean(keys + C::kTileBytes, j0, ok);
+        }
         const bool any = !idle && j0 <= place0 + w_last && (p.window == 0 || j0 + NK > place0 + w_first - p.window + 1 || j0 < p.sinks);
         if (any) {
             bool full = j0 + NK - 1 <= place0 + w_first && (p.window == 0 || j0 > place0 + w_last - p.window || j0 + NK <= p.sinks);
-            uint32_t ok[KB];
 #pragma unroll
-            for (int k = 0; k < KB; ++k) {
-                ok[k] = __builtin_amdgcn_readfirstlane(masks[buffer * 4 + k]);
-                full = full && ok[k] == 0xffff;
-            }
-            if (__builtin_expect(full, 1)) {
-                tile(std::true_type(), std::false_type(), keys, j0, ok);
-            } else {
-                uint32_t odd = 0;
-                if (!even(j0)) {
-#pragma unroll
-                    for (int w = 0; w < C::kWaves; ++w) odd |= odds[buffer * 8 + w];
-                }
-                if (__builtin_expect(__builtin_amdgcn_readfirstlane(odd) == 0, 1)) tile(std::false_type(), std::false_type(), keys, j0, ok);
-                else tile(std::false_type(), std::true_type(), keys, j0, ok);
-            }
+            for (int k = 0; k < KB; ++k) full = full && ok[k] == 0xffff;
+            tile(full, keys, j0, ok);
         }
         if (t + 1 < t_to) land(buffer ^ 1, t + 1);
         lds_only_barrier();
@@ -314,11 +324,9 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, 2) void chunk_kernel(Attend
 }
 
 template <int DP>
-const void* chunk_kernel_types(bool f16, bool f32_out, int* rows, int* threads, int* lds)
+const void* chunk_kernel_types(bool f16, bool f32_out, ChunkShape* shape)
 {
-    *rows = Chunk<DP>::kRows;
-    *threads = Chunk<DP>::kWaves * 64;
-    *lds = Chunk<DP>::kLds;
+    *shape = ChunkShape{Chunk<DP>::kRows, Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce, Chunk<DP>::kLds};
     if (f16) return f32_out ? (const void*)&chunk_kernel<DP, _Float16, 2> : (const void*)&chunk_kernel<DP, _Float16, 1>;
     return f32_out ? (const void*)&chunk_kernel<DP, __bf16, 3> : (const void*)&chunk_kernel<DP, __bf16, 1>;
 }

@@ -3,6 +3,6 @@
 
 namespace ops {
 
-const void* chunk_kernel_64(bool f16, bool f32_out, int* rows, int* threads, int* lds) { return chunk_kernel_types<64>(f16, f32_out, rows, threads, lds); }
+const void* chunk_kernel_64(bool f16, bool f32_out, ChunkShape* shape) { return chunk_kernel_types<64>(f16, f32_out, shape); }
 
 }  // namespace ops
