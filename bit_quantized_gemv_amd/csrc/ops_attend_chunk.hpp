@@ -14,22 +14,22 @@
 
 namespace ops {
 
-// Two workgroups of four waves on a compute unit, or one where heads are so large that a
-// wave's outputs and queries fill half of the registers.
+// As many waves as the registers hold, in workgroups of four, or of eight where the outputs and
+// queries of two waves fill a unit's.
 template <int DP>
 struct Chunk {
-    static constexpr int kWaves = 4;
-    static constexpr int kAtOnce = DP > 192 ? 1 : 2;
-    static constexpr int kKeys = DP > 128 && DP <= 192 ? 32 : 64;  // of a tile
+    static constexpr int kWaves = DP > 192 ? 8 : 4;
+    static constexpr int kAtOnce = DP > 192 ? 1 : DP > 64 ? 2 : 3;
+    static constexpr int kKeys = DP > 128 ? 32 : 64;               // of a tile
     static constexpr int kRows = kWaves * 32;
     static constexpr int kTileBytes = kKeys * DP * 2;
-    static constexpr int kLds = 4 * kTileBytes + 2 * 32;           // keys and values, twice, and what is known of them
+    static constexpr int kLds = 4 * kTileBytes + 2 * 48;           // keys and values, twice, and what is known of them
 };
 
 constexpr float kRoom = 8.0f;
 
 template <int DP, class X, int NP>
-__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce) void chunk_kernel(AttendParams p)
+__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<DP>::kWaves / 4) void chunk_kernel(AttendParams p)
 {
     typedef Chunk<DP> C;
     constexpr int NK = C::kKeys, KB = NK / 16, DS = DP / 32, DT = DP / 16, US = NK / 32;
@@ -127,7 +127,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce) void ch
 #pragma unroll
             for (int d = 0; d < BW; ++d) found |= odd<X>(*reinterpret_cast<const u32x4*>(mine_at + d * 1024));
             const uint32_t any = __any(found) ? 1 : 0;
-            if (lane == 0) odds[buffer * 4 + wave] = any;
+            if (lane == 0) odds[buffer * 8 + wave] = any;
         }
         // one bit a key
         if (d0 == 0) {
@@ -146,6 +146,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce) void ch
     auto tile = [&](bool full, const char* keys, int j0, const uint32_t (&ok)[KB]) {
         const char* const values = keys + C::kTileBytes;
         f32x4 x[2][KB];
+        __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int k = 0; k < KB; ++k) {
 #pragma unroll
@@ -157,6 +158,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce) void ch
                 for (int rt = 0; rt < 2; ++rt) x[rt][k] = mfma(f, q[rt][d], x[rt][k], X());
             }
         }
+        __builtin_amdgcn_s_setprio(0);
         if (!full) {
 #pragma unroll
             for (int k = 0; k < KB; ++k)
@@ -292,7 +294,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce) void ch
         if (!even(j0)) {
             uint32_t odd = 0;
 #pragma unroll
-            for (int w = 0; w < C::kWaves; ++w) odd |= odds[buffer * 4 + w];
+            for (int w = 0; w < C::kWaves; ++w) odd |= odds[buffer * 8 + w];
             if (__builtin_expect(__builtin_amdgcn_readfirstlane(odd) != 0, 0)) clean(keys + C::kTileBytes, j0, ok);
         }
         const bool any = !idle && j0 <= place0 + w_last && (p.window == 0 || j0 + NK > place0 + w_first - p.window + 1 || j0 < p.sinks);
