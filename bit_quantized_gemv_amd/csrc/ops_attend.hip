@@ -17,31 +17,33 @@ constexpr int kUnits = 256;                // compute units
 constexpr int kLanes = 16;                 // of a row's 64 columns
 constexpr int kChains = kThreads / kLanes;
 
-// The parts of rows, joined: those of blocks, or (splits > 0) of chunks, which are `splits` supers each.  Leaves are joined to supers one after the other, as the
+// The parts of rows, joined: those of blocks, and those of chunks, which are `splits` supers each.  Leaves are joined to supers one after the other, as the
 // block's kernel does it; a row is the sum of its supers, in order, each with its weight against
 // the row's largest score.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows.  Bound by
 // latency: every group of 16 lanes asks for eight parts at once.
-__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int splits, int chains_log2, int columns)
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int splits, int block_chains, int chunk_chains, int columns)
 {
     __shared__ __align__(16) f32x4 sums[kThreads * kSuper];
     __shared__ f32x2 stats[kChains * kSuper];
     __shared__ float tops[kChains];
     const int b = blockIdx.y;
     const Seq s = sequence(p.cache, b);
-    if ((s.count > kBlockTokens) != (splits > 0)) return;
+    const bool chunk = s.count > kBlockTokens;
+    if ((chunk ? splits : p.units) <= 1) return;      // written already
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
     const int tid = threadIdx.x, lane = tid & (kLanes - 1), group = tid / kLanes;
-    const int chains = 1 << chains_log2, chain = group & (chains - 1), team = group >> chains_log2;
+    const int chains_log2 = chunk ? chunk_chains : block_chains, chains = 1 << chains_log2;
+    const int chain = group & (chains - 1), team = group >> chains_log2;
     const int block = blockIdx.x / columns, d = (blockIdx.x - block * columns) * 64 + lane * 4;
     const int r0 = block * (kChains >> chains_log2), r = r0 + team;
     if (r0 >= tokens * p.q_heads) return;
     const bool mine = r < tokens * p.q_heads, mine_d = mine && d < p.D;
     Visible vis = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit);
-    if (splits > 0) vis.units = splits;
+    if (chunk) vis.units = splits;
     const long long row = (long long)s.start * p.q_heads + r;
     const f32x2* stat = p.stat + row * p.slots;
     const float* part = p.part + row * p.slots * p.D + d;
-    const bool leaves = splits == 0 && p.per_unit == 1;
+    const bool leaves = !chunk && p.per_unit == 1;
     // supers of the row, where units are leaves
     const Visible all = leaves ? visible(place0, tokens, p.window, p.sinks, leaf * kSuper) : vis;
 
@@ -176,12 +178,15 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
                                              : chunk_kernel_256;
     p.chunk = chunk(f16, f32_out, &p.shape);
     p.chunk_blocks = (int)(((long long)p.max_new * group + p.shape.rows - 1) / p.shape.rows);
-    p.splits = 0;
+    p.splits = 1;
     long long slots = p.units;
     if (p.max_new > kBlockTokens) {
-        // as many shares as there is room for on the compute units, of 512 keys at least
-        const long long groups = (long long)p.chunk_blocks * c->heads * c->n_seqs, room = kUnits * p.shape.at_once / groups;
-        const long long most = (std::min<long long>(p.length, p.window ? (long long)p.window + p.sinks + p.shape.rows / group : p.length) + 511) / 512;
+        // as many shares as there is room for on the compute units, of 256 keys at least; a chunk has more
+        // tokens than a block, so T bounds how many there are
+        const long long chunks = std::min<long long>(c->n_seqs, T / (kBlockTokens + 1));
+        const long long tiles = std::min(chunks * p.chunk_blocks, (long long)T * group / p.shape.rows + chunks);
+        const long long room = kUnits * p.shape.at_once / std::max<long long>(1, tiles * c->heads);
+        const long long most = (std::min<long long>(p.length, p.window ? (long long)p.window + p.sinks + p.shape.rows / group : p.length) + 255) / 256;
         p.splits = (int)std::max<long long>(1, std::min(room, most));
         slots = std::max<long long>(slots, p.splits);
     }
@@ -196,16 +201,21 @@ int launch(const void* f, dim3 grid, int threads, void** args, int lds, void* st
     return hipLaunchKernel(f, grid, dim3(threads), args, (size_t)lds, static_cast<hipStream_t>(stream)) == hipSuccess ? QMV_OK : QMV_E_LAUNCH;
 }
 
-// the parts of the blocks' rows, or (splits > 0) the chunks'
-int launch_join(AttendParams& p, const Plan& plan, int splits, int n_seqs, void* stream)
+// groups of lanes that share a row of so many parts
+int chains_of(int parts)
 {
-    int chains_log2 = 0, leaf = plan.leaf, columns = (p.D + 63) / 64;
-    const int eights = (p.slots + kSuper - 1) / kSuper;
-    while (1 << chains_log2 < std::min(kChains, eights)) ++chains_log2;
-    const long long rows = (long long)(splits > 0 ? plan.max_new : std::min(plan.max_new, kBlockTokens)) * p.q_heads;
-    const int per = kChains >> chains_log2;
-    void* args[] = {&p, &leaf, &splits, &chains_log2, &columns};
-    return launch((const void*)&join_kernel, dim3((unsigned)((rows + per - 1) / per * columns), n_seqs), kThreads, args, 0, stream);
+    int log2 = 0;
+    while (1 << log2 < std::min(kChains, (parts + kSuper - 1) / kSuper)) ++log2;
+    return log2;
+}
+
+int launch_join(AttendParams& p, const Plan& plan, int n_seqs, void* stream)
+{
+    int leaf = plan.leaf, splits = plan.splits, columns = (p.D + 63) / 64, block_chains = chains_of((int)plan.units), chunk_chains = chains_of(splits);
+    auto groups = [&](long long tokens, int parts, int chains) { return parts > 1 ? (tokens * p.q_heads + (kChains >> chains) - 1) / (kChains >> chains) : 0; };
+    const long long most = std::max(groups(std::min(plan.max_new, kBlockTokens), (int)plan.units, block_chains), groups(plan.max_new, splits, chunk_chains));
+    void* args[] = {&p, &leaf, &splits, &block_chains, &chunk_chains, &columns};
+    return launch((const void*)&join_kernel, dim3((unsigned)(most * columns), n_seqs), kThreads, args, 0, stream);
 }
 
 }  // namespace
@@ -263,7 +273,8 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.sinks = plan.sinks;
     p.max_new = plan.max_new;
     p.out_f32 = out_dt == QMV_DT_F32;
-    p.slots = p.units = (int)plan.units;
+    p.units = (int)plan.units;
+    p.slots = std::max(p.units, plan.splits);
     p.row_blocks = plan.row_blocks;
     p.per_unit = plan.per_unit;
     // a scale of zero weighs all places that are seen alike; the smallest does so too, and hides the others
@@ -272,15 +283,9 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.cache.max_places = plan.length;
     void* args[] = {&p};
     if (int e = launch(plan.block, dim3((unsigned)groups, c->n_seqs), kThreads, args, plan.block_lds, stream)) return e;
-    if (plan.units > 1)
-        if (int e = launch_join(p, plan, 0, c->n_seqs, stream)) return e;
-    if (plan.max_new > kBlockTokens) {
-        p.slots = plan.splits;
+    if (plan.max_new > kBlockTokens)
         if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
-        if (plan.splits > 1)
-            if (int e = launch_join(p, plan, plan.splits, c->n_seqs, stream)) return e;
-    }
-    return QMV_OK;
+    return p.slots > 1 ? launch_join(p, plan, c->n_seqs, stream) : QMV_OK;
 }
 
 }  // extern "C"

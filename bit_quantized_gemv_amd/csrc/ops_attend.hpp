@@ -17,6 +17,7 @@
 
 #include <cstdint>
 
+#include "ops_args.hpp"
 #include "ops_cache.hpp"
 
 namespace ops {

@@ -42,6 +42,8 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
     uint32_t* const odds = reinterpret_cast<uint32_t*>(sums + 64);       // whether a wave has met values that are no numbers
     char* const queries = reinterpret_cast<char*>(odds + 4);
 
+    const Cache& c = p.cache;
+    together(c.pages, c.pages_row, c.starts, c.lengths, c.magic, c.shift, c.max_pages, c.T, p.per_unit, p.window, p.heads, p.row_blocks, p.units);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
     const int b = blockIdx.y;
@@ -49,14 +51,27 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
     const int turn = blockIdx.x >> 3, rb = turn % p.row_blocks, f = turn / p.row_blocks * 8 + (blockIdx.x & 7);
     const int u = f / p.heads, head = f - u * p.heads;
     if (u >= p.units) return;
+    // pages of the lane's keys of a leaf, key n of every tile
+    const int32_t* const table = p.cache.pages + b * p.cache.pages_row;
+    int entry[TILES];
+    auto ask_pages = [&](int leaf) {
+#pragma unroll
+        for (int t = 0; t < TILES; ++t) {
+            const int j = leaf + wave * WK + t * 16 + n;
+            entry[t] = table[min(page_index(p.cache, j), p.cache.max_pages - 1)];
+        }
+    };
+    // Without a window the first leaf is known before the sequence is: its pages are asked for together
+    // with what is known of the sequence.
+    const int U = KT * p.per_unit, early = p.window == 0 ? u * U : -1;
+    if (early >= 0) ask_pages(early);
     const Seq s = sequence(p.cache, b);
     if (s.count > kBlockTokens) return;
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
     const int r0 = rb * NR * 16;
     if (r0 >= tokens * p.group) return;
-    const int U = KT * p.per_unit;
     const Visible vis = visible(place0, tokens, p.window, p.sinks, U);
-    if (u >= vis.units && !(u == 0 && p.slots == 1)) return;      // a lone unit writes zeros where nothing is seen
+    if (u >= vis.units && !(u == 0 && p.units == 1)) return;      // a lone unit writes zeros where nothing is seen
 
     // this lane's rows
     int high[NR], low[NR];
@@ -99,16 +114,6 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
         return at < to ? at : -1;
     };
 
-    // pages of the lane's keys of a leaf, key n of every tile
-    int entry[TILES];
-    auto ask_pages = [&](int leaf) {
-#pragma unroll
-        for (int t = 0; t < TILES; ++t) {
-            const int j = leaf + wave * WK + t * 16 + n;
-            const int at = page_index(p.cache, min(j, s.length - 1));
-            entry[t] = p.cache.pages[b * p.cache.pages_row + at];
-        }
-    };
     u32x4 kf[TILES][DS], vf[TILES][DS];
     long long v_at[TILES];
     uint32_t valid[TILES];
@@ -147,7 +152,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
 
     int leaf = next_leaf(from);
     if (leaf >= 0) {
-        ask_pages(leaf);
+        if (leaf != early) ask_pages(leaf);
         addresses(leaf, valid);
         ask_keys();
         ask_values();
@@ -314,12 +319,12 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
     for (int rt = 0; rt < NR; ++rt) {
         if (!mine[rt]) continue;
         const long long at = row[rt] * p.slots + u;
-        if (p.slots > 1 && wave == 0 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
+        if (p.units > 1 && wave == 0 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             const int c = (wave * DT + d) * 16 + 4 * g;
             if (c >= p.D) continue;
-            if (p.slots == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
+            if (p.units == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
             else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
         }
     }

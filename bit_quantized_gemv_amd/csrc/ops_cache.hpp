@@ -17,7 +17,7 @@ struct Cache {
     long long pages_row;
     uint32_t magic;             // j / page_size = j * magic >> shift, for j < 2^31
     int shift;
-    int n_pages, page_size, n_seqs, max_places;
+    int n_pages, page_size, n_seqs, max_pages, max_places;
     int T;
 };
 
@@ -157,6 +157,7 @@ inline Cache device_cache(const qmv_cache* c, int T)
     d.n_pages = c->n_pages;
     d.page_size = c->page_size;
     d.n_seqs = c->n_seqs;
+    d.max_pages = c->max_pages;
     d.max_places = c->max_pages * c->page_size;
     d.T = T;
     return d;

@@ -1,13 +1,13 @@
 // ops_rotate.hip -- qmv_rotate and qmv_append: norms of queries and keys for
 // each head, their position rotation, and keys and values to a cache's pages.
 //
-// One launch and one pass.  A head of D values is held by the lanes of a group, eight
-// values each: where it is rotated, lane i < rot / 8 holds the values 4i .. 4i + 3 of the
-// pairs' first places and the same of their second ones, so that a pair is turned within a
-// lane, whichever way pairs lie.  The sum of squares is taken over the group's lanes, in
-// fp32.  A workgroup takes all heads of some tokens (or some heads of one, where there
-// are few tokens), since the angles are those of the token: a thread computes one of them,
-// with its sine and cosine, for all heads.
+// One launch and one pass.  A wave takes some heads of a token: a head of D values is held by a
+// group of lanes, 16 values each (eight where sizes do not go by 16: half the bytes a load and
+// store), and the groups take heads side by side, some in flight.  Where a head is rotated,
+// lane i of a group holds the values 8i .. 8i + 7 of the pairs' first places and the same of their
+// second ones, so that a pair is turned within a lane, whichever way pairs lie, and the lane's
+// sines, cosines and weights are the same for all heads.  A lane computes one angle, for the whole wave.  The sum of squares is taken over the
+// group's lanes, in fp32.  There is no barrier.
 //
 // Angles: positions * freqs in fp64, as turns; the fraction of a turn that is left has lost
 // nothing that fp32 holds, also at positions of 2^31.
@@ -26,8 +26,7 @@ typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 typedef __attribute__((ext_vector_type(4))) _Float16 f16x4;
 
 constexpr int kThreads = 256;
-constexpr int kHold = 4;              // heads in flight per group of lanes
-constexpr int kMostTokens = 8;        // per workgroup
+constexpr int kWaves = kThreads / 64;
 constexpr int kMostHalf = QMV_MAX_HEAD_SIZE / 2;
 
 struct RotateParams {
@@ -41,7 +40,7 @@ struct RotateParams {
     float eps;
     int T, q_heads, k_heads, D, half, n_axes, interleaved, w_f32;
     int lanes_log2;                   // lanes of a group
-    int tokens, heads;                // per workgroup
+    int parts, heads;                 // waves that share a token, and the heads of each
     Cache cache;
 };
 
@@ -88,171 +87,155 @@ __device__ __forceinline__ void sine_cosine(double turns, float& s, float& c)
     c = (n + 1) & 2 ? -ca : ca;
 }
 
-// Whose rows a head of the workgroup's list is, and where they are.
-struct Head {
-    const char* from;
-    char* to;              // nullptr: not written
-    int which;             // 0 queries, 1 keys, 2 values
-};
-
-template <class X, class Y, bool APPEND>
+// Q: values of a lane's run in fours; two runs, of 8 Q values of a head together
+template <class X, class Y, bool APPEND, int Q>
 __global__ __launch_bounds__(kThreads) void rotate_kernel(RotateParams p)
 {
     typedef typename Four<X>::type X4;
     typedef typename Four<Y>::type Y4;
-    __shared__ __align__(16) float cosines[kMostTokens * kMostHalf], sines[kMostTokens * kMostHalf];
-    __shared__ int places[kMostTokens];
-    __shared__ long long key_at[kMostTokens], value_at[kMostTokens];
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int t0 = blockIdx.x * p.tokens, tokens = min(p.tokens, p.T - t0);
-    const int all = p.q_heads + (APPEND ? 2 : 1) * p.k_heads;
-    const int h0 = blockIdx.y * p.heads, heads = min(p.heads, all - h0);
-    const int items = tokens * heads;
-    const int group = tid >> p.lanes_log2, part = tid & ((1 << p.lanes_log2) - 1), groups = kThreads >> p.lanes_log2;
-    const bool live = part < p.D >> 3;
-    // the lane's two runs of four values
-    const bool turned = part < p.half >> 2;
-    const int first = turned && !p.interleaved ? 4 * part : 8 * part, second = turned && !p.interleaved ? p.half + 4 * part : 8 * part + 4;
-
-    auto head_of = [&](int item, int& tok) {
-        tok = item / heads;
-        const int h = h0 + item - tok * heads, t = t0 + tok;
-        Head r;
-        if (h < p.q_heads) {
-            r.from = p.q + t * p.q_token + h * p.q_head;
-            r.to = p.q_out + ((long long)t * p.q_heads + h) * p.D * sizeof(Y);
-            r.which = 0;
-        } else if (h < p.q_heads + p.k_heads) {
-            r.from = p.k + t * p.k_token + (h - p.q_heads) * p.k_head;
-            r.to = APPEND ? nullptr : p.k_out + ((long long)t * p.k_heads + h - p.q_heads) * p.D * sizeof(Y);
-            r.which = 1;
-        } else {
-            r.from = p.v + t * p.v_token + (h - p.q_heads - p.k_heads) * p.v_head;
-            r.to = nullptr;
-            r.which = 2;
-        }
-        return r;
+    struct XRun {
+        X4 v[Q];
     };
+    struct __attribute__((aligned(8 * Q))) YRun {
+        Y4 v[Q];
+    };
+    constexpr int kHold = 4 / Q;          // heads in flight per group of lanes
+    __shared__ __align__(16) float cosines[kWaves][kMostHalf], sines[kWaves][kMostHalf];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int job = blockIdx.x * kWaves + wave, t = job / p.parts;
+    if (t >= p.T) return;
+    const int all = p.q_heads + (APPEND ? 2 : 1) * p.k_heads;
+    const int h0 = (job - t * p.parts) * p.heads, h1 = min(all, h0 + p.heads);
+    const int groups = 64 >> p.lanes_log2, group = lane >> p.lanes_log2, part = lane & ((1 << p.lanes_log2) - 1);
+    const bool live = part < p.D / (8 * Q);
+    // the lane's two runs
+    const bool turned = part < p.half / (4 * Q);
+    const int first = turned && !p.interleaved ? 4 * Q * part : 8 * Q * part;
+    const int second = turned && !p.interleaved ? p.half + 4 * Q * part : 8 * Q * part + 4 * Q;
 
-    X4 a[kHold], b[kHold];
+    const char* const q_at = p.q + t * p.q_token;
+    const char* const k_at = p.k + t * p.k_token;
+    const char* const v_at = p.v + t * p.v_token;
+    const int k_from = p.q_heads, v_from = p.q_heads + p.k_heads;
+    XRun a[kHold], b[kHold];
     auto load = [&](int base) {
 #pragma unroll
         for (int i = 0; i < kHold; ++i) {
-            const int item = base + i * groups + group;
-            if (live && item < items) {
-                int tok;
-                const char* from = head_of(item, tok).from;
-                a[i] = *reinterpret_cast<const X4*>(from + first * sizeof(X));
-                b[i] = *reinterpret_cast<const X4*>(from + second * sizeof(X));
+            const int h = base + i * groups + group;
+            if (live && h < h1) {
+                const char* from = h < k_from ? q_at + h * p.q_head : k_at + (h - k_from) * p.k_head;
+                if (APPEND && h >= v_from) from = v_at + (h - v_from) * p.v_head;
+                a[i] = *reinterpret_cast<const XRun*>(__builtin_assume_aligned(from + first * sizeof(X), Q * 8));
+                b[i] = *reinterpret_cast<const XRun*>(__builtin_assume_aligned(from + second * sizeof(X), Q * 8));
             }
         }
     };
-    load(0);
+    load(h0);
 
+    // weights of queries and keys
+    f32x4 wq[2 * Q], wk[2 * Q];
+#pragma unroll
+    for (int i = 0; i < 2 * Q; ++i) {
+        const int at = (i < Q ? first : second) + 4 * (i % Q);
+        wq[i] = wk[i] = f32x4{1, 1, 1, 1};
+        if (p.q_weight && live)
+            wq[i] = p.w_f32 ? *reinterpret_cast<const f32x4*>(p.q_weight + at * 4) : wide_of(*reinterpret_cast<const bf16x4*>(p.q_weight + at * 2));
+        if (p.k_weight && live)
+            wk[i] = p.w_f32 ? *reinterpret_cast<const f32x4*>(p.k_weight + at * 4) : wide_of(*reinterpret_cast<const bf16x4*>(p.k_weight + at * 2));
+    }
+
+    // the token's place, and where its keys and values go
+    int place = 0;
+    char *key_to = nullptr, *value_to = nullptr;
     if (APPEND) {
-        for (int i = wave; i < tokens; i += kThreads / 64) {
-            const int seq = sequence_of(p.cache, t0 + i, lane);
-            if (lane == 0) {
-                int place = 0;
-                long long ka = -1, va = -1;
-                bool in = false;
-                if (seq >= 0) {
-                    const Seq s = sequence(p.cache, seq);
-                    const int at = t0 + i - s.start;
-                    if (at >= 0 && at < s.count) {
-                        in = true;
-                        place = s.length - s.count + at;
-                        if (place >= 0 && place < p.cache.max_places) {
-                            const int index = page_index(p.cache, place), page = page_of(p.cache, seq, index);
-                            if (page >= 0) {
-                                const int slot = place - index * p.cache.page_size;
-                                ka = page * p.cache.k_page + slot * p.cache.k_slot;
-                                va = page * p.cache.v_page + slot * p.cache.v_slot;
-                            }
-                        }
-                    }
-                }
-                places[i] = place;
-                key_at[i] = in ? ka : -2;         // -2: the token is in no sequence, its queries are not written
-                value_at[i] = va;
+        const int seq = __builtin_amdgcn_readfirstlane(sequence_of(p.cache, t, lane));
+        if (seq < 0) return;
+        const Seq s = sequence(p.cache, seq);
+        const int at = t - s.start;
+        if (at < 0 || at >= s.count) return;
+        place = s.length - s.count + at;
+        if (place >= 0 && place < p.cache.max_places) {
+            const int index = page_index(p.cache, place), page = page_of(p.cache, seq, index);
+            if (page >= 0) {
+                const int slot = place - index * p.cache.page_size;
+                key_to = const_cast<char*>(p.cache.k) + page * p.cache.k_page + slot * p.cache.k_slot;
+                value_to = const_cast<char*>(p.cache.v) + page * p.cache.v_page + slot * p.cache.v_slot;
             }
         }
-        __syncthreads();
     }
-    for (int i = tid; i < tokens * p.half; i += kThreads) {
-        const int tok = i / p.half, j = i - tok * p.half;
+    for (int j = lane; j < p.half; j += 64) {
         const int axis = p.axes ? p.axes[j] : 0;
         float s = 0.0f, c = 1.0f;
         if ((uint32_t)axis < (uint32_t)p.n_axes) {
-            const int pos = p.positions ? p.positions[axis * p.positions_row + t0 + tok] : places[tok];
+            const int pos = p.positions ? p.positions[axis * p.positions_row + t] : place;
             const double turns = (double)pos * ((double)p.freqs[j] * 0.15915494309189533576888);
             sine_cosine(turns - __builtin_floor(turns), s, c);
         }
-        cosines[tok * kMostHalf + j] = c;
-        sines[tok * kMostHalf + j] = s;
+        cosines[wave][j] = c;
+        sines[wave][j] = s;
     }
-    __syncthreads();
+    // what a lane has put there, others of its wave read
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+    f32x4 c[Q], s[Q];
+#pragma unroll
+    for (int i = 0; i < Q; ++i) {
+        c[i] = f32x4{1, 1, 1, 1};
+        s[i] = f32x4{0, 0, 0, 0};
+        if (turned) {
+            c[i] = *reinterpret_cast<const f32x4*>(&cosines[wave][4 * Q * part + 4 * i]);
+            s[i] = *reinterpret_cast<const f32x4*>(&sines[wave][4 * Q * part + 4 * i]);
+        }
+    }
+    const float per = 1.0f / (float)p.D;
 
-    for (int base = 0; base < items; base += kHold * groups) {
-        if (base > 0) load(base);
+    for (int base = h0; base < h1; base += kHold * groups) {
+        if (base > h0) load(base);
 #pragma unroll
         for (int i = 0; i < kHold; ++i) {
-            const int item = base + i * groups + group;
-            if (base + i * groups >= items) break;          // the whole workgroup's
-            int tok = 0;
-            Head h{nullptr, nullptr, 2};
-            const bool mine = item < items;
-            if (mine) h = head_of(item, tok);
-            f32x4 x = {0, 0, 0, 0}, y = {0, 0, 0, 0};
-            if (mine && live) {
-                x = wide_of(a[i]);
-                y = wide_of(b[i]);
-            }
-            const char* w = h.which == 0 ? p.q_weight : p.k_weight;
-            const f32x4 sq = x * x + y * y;
+            if (base + i * groups >= h1) break;          // the whole wave's
+            const int h = base + i * groups + group;
+            const bool mine = live && h < h1, key = h >= k_from, value = APPEND && h >= v_from;
+            f32x4 z[2 * Q];
+#pragma unroll
+            for (int j = 0; j < 2 * Q; ++j) z[j] = mine ? wide_of(j < Q ? a[i].v[j] : b[i].v[j - Q]) : f32x4{0, 0, 0, 0};
+            char* to;
+            if (value) to = value_to ? value_to + (h - v_from) * p.cache.v_head : nullptr;
+            else if (!key) to = p.q_out + ((long long)t * p.q_heads + h) * p.D * sizeof(Y);
+            else if (APPEND) to = key_to ? key_to + (h - k_from) * p.cache.k_head : nullptr;
+            else to = p.k_out + ((long long)t * p.k_heads + h - k_from) * p.D * sizeof(Y);
+            // the norm, of a group that has any; lanes of values take part in the sum alone
+            f32x4 sq = {0, 0, 0, 0};
+#pragma unroll
+            for (int j = 0; j < 2 * Q; ++j) sq += z[j] * z[j];
             float sum = (sq.x + sq.y) + (sq.z + sq.w);
             for (int m = 1; m < 1 << p.lanes_log2; m <<= 1) sum += __shfl_xor(sum, m);
-            if (!mine || !live) continue;
-            if (h.which < 2) {
-                if (w) {
-                    const float r = __builtin_amdgcn_rsqf(sum / (float)p.D + p.eps);
-                    f32x4 wa, wb;
-                    if (p.w_f32) {
-                        wa = *reinterpret_cast<const f32x4*>(w + first * 4);
-                        wb = *reinterpret_cast<const f32x4*>(w + second * 4);
+            if (!value && (key ? p.k_weight : p.q_weight)) {
+                const float r = __builtin_amdgcn_rsqf(sum * per + p.eps);
+#pragma unroll
+                for (int j = 0; j < 2 * Q; ++j) z[j] = z[j] * r * (key ? wk[j] : wq[j]);
+            }
+            if (turned && !value) {
+#pragma unroll
+                for (int j = 0; j < Q; ++j) {
+                    if (p.interleaved) {          // pairs side by side: (x0 x1) (x2 x3) (y0 y1) (y2 y3)
+                        const f32x4 x = z[2 * j], y = z[2 * j + 1], e = {x.x, x.z, y.x, y.z}, o = {x.y, x.w, y.y, y.w};
+                        const f32x4 u = e * c[j] - o * s[j], w = o * c[j] + e * s[j];
+                        z[2 * j] = f32x4{u.x, w.x, u.y, w.y};
+                        z[2 * j + 1] = f32x4{u.z, w.z, u.w, w.w};
                     } else {
-                        wa = wide_of(*reinterpret_cast<const bf16x4*>(w + first * 2));
-                        wb = wide_of(*reinterpret_cast<const bf16x4*>(w + second * 2));
-                    }
-                    x = x * r * wa;
-                    y = y * r * wb;
-                }
-                if (turned) {
-                    const f32x4 c = *reinterpret_cast<const f32x4*>(cosines + tok * kMostHalf + 4 * part);
-                    const f32x4 s = *reinterpret_cast<const f32x4*>(sines + tok * kMostHalf + 4 * part);
-                    if (p.interleaved) {          // the pairs are (x0 x1) (x2 x3) (y0 y1) (y2 y3)
-                        const f32x4 e = {x.x, x.z, y.x, y.z}, o = {x.y, x.w, y.y, y.w};
-                        const f32x4 u = e * c - o * s, v = o * c + e * s;
-                        x = f32x4{u.x, v.x, u.y, v.y};
-                        y = f32x4{u.z, v.z, u.w, v.w};
-                    } else {
-                        const f32x4 u = x * c - y * s;
-                        y = y * c + x * s;
-                        x = u;
+                        const f32x4 x = z[j], y = z[Q + j];
+                        z[j] = x * c[j] - y * s[j];
+                        z[Q + j] = y * c[j] + x * s[j];
                     }
                 }
             }
-            char* to = h.to;
-            if (APPEND) {
-                const long long ka = key_at[tok], va = value_at[tok];
-                const int kh = h0 + item - tok * heads - p.q_heads - (h.which == 2 ? p.k_heads : 0);
-                if (h.which == 0) to = ka == -2 ? nullptr : to;
-                else if (h.which == 1) to = ka < 0 ? nullptr : const_cast<char*>(p.cache.k) + ka + kh * p.cache.k_head;
-                else to = va < 0 ? nullptr : const_cast<char*>(p.cache.v) + va + kh * p.cache.v_head;
-            }
-            if (to) {
-                *reinterpret_cast<Y4*>(to + first * sizeof(Y)) = __builtin_convertvector(x, Y4);
-                *reinterpret_cast<Y4*>(to + second * sizeof(Y)) = __builtin_convertvector(y, Y4);
+            if (mine && to) {
+                YRun r[2];
+#pragma unroll
+                for (int j = 0; j < 2 * Q; ++j) r[j / Q].v[j % Q] = __builtin_convertvector(z[j], Y4);
+                *reinterpret_cast<YRun*>(to + first * sizeof(Y)) = r[0];
+                *reinterpret_cast<YRun*>(to + second * sizeof(Y)) = r[1];
             }
         }
     }
@@ -282,6 +265,18 @@ long long input_span(int T, int heads, int D, long long token, long long head, i
     return n * (long long)size_of(dt);
 }
 
+template <class X, class Y, bool APPEND>
+const void* kernel_of_types(bool sixteen)
+{
+    return sixteen ? (const void*)&rotate_kernel<X, Y, APPEND, 2> : (const void*)&rotate_kernel<X, Y, APPEND, 1>;
+}
+template <bool APPEND>
+const void* kernel_of(bool x_f32, bool y_f16, bool sixteen)
+{
+    if (x_f32) return y_f16 ? kernel_of_types<float, _Float16, APPEND>(sixteen) : kernel_of_types<float, __bf16, APPEND>(sixteen);
+    return y_f16 ? kernel_of_types<__bf16, _Float16, APPEND>(sixteen) : kernel_of_types<__bf16, __bf16, APPEND>(sixteen);
+}
+
 int run(RotateParams& p, const qmv_rotation* r, int T, int x_dt, int y_dt, bool append, void* stream)
 {
     p.q_weight = static_cast<const char*>(r->q_weight);
@@ -296,27 +291,19 @@ int run(RotateParams& p, const qmv_rotation* r, int T, int x_dt, int y_dt, bool 
     p.n_axes = r->n_axes;
     p.interleaved = r->interleaved != 0;
     p.w_f32 = r->w_dt == QMV_DT_F32;
+    const bool sixteen = p.D % 16 == 0 && p.half % 8 == 0;
+    const int lanes = p.D / (sixteen ? 16 : 8);
     p.lanes_log2 = 0;
-    while (1 << p.lanes_log2 < p.D / 8) ++p.lanes_log2;
-    const int all = p.q_heads + (append ? 2 : 1) * p.k_heads, groups = kThreads >> p.lanes_log2;
-    // A head per group where that is few workgroups; else all heads of a token (as many as
-    // are in flight at once), or of several tokens, so that angles are computed once.
-    p.tokens = 1;
-    p.heads = std::min(all, groups);
-    if ((long long)T * ((all + p.heads - 1) / p.heads) > 1024) {
-        p.heads = std::min(all, kHold * groups);
-        p.tokens = std::max(1, std::min(kMostTokens, kHold * groups / p.heads));
-    }
+    while (1 << p.lanes_log2 < lanes) ++p.lanes_log2;
+    // Few tokens: as many waves as there are heads to go round; then some rounds a wave, so that
+    // angles and places serve several heads; then all heads, so that a token's memory is one wave's.
+    const int all = p.q_heads + (append ? 2 : 1) * p.k_heads, groups = 64 >> p.lanes_log2;
+    p.heads = T >= 4096 ? all : std::min(all, T >= 256 ? std::max(groups, 16) : groups);
+    p.parts = (all + p.heads - 1) / p.heads;
     const bool xf = x_dt == QMV_DT_F32, yh = y_dt == QMV_DT_F16;
-    const void* f;
-    if (append)
-        f = xf ? (yh ? (const void*)&rotate_kernel<float, _Float16, true> : (const void*)&rotate_kernel<float, __bf16, true>)
-               : (yh ? (const void*)&rotate_kernel<__bf16, _Float16, true> : (const void*)&rotate_kernel<__bf16, __bf16, true>);
-    else
-        f = xf ? (yh ? (const void*)&rotate_kernel<float, _Float16, false> : (const void*)&rotate_kernel<float, __bf16, false>)
-               : (yh ? (const void*)&rotate_kernel<__bf16, _Float16, false> : (const void*)&rotate_kernel<__bf16, __bf16, false>);
+    const void* f = append ? kernel_of<true>(xf, yh, sixteen) : kernel_of<false>(xf, yh, sixteen);
     void* args[] = {&p};
-    const dim3 grid((T + p.tokens - 1) / p.tokens, (all + p.heads - 1) / p.heads);
+    const dim3 grid((unsigned)(((long long)T * p.parts + kWaves - 1) / kWaves));
     return hipLaunchKernel(f, grid, dim3(kThreads), args, 0, static_cast<hipStream_t>(stream)) == hipSuccess ? QMV_OK : QMV_E_LAUNCH;
 }
 
