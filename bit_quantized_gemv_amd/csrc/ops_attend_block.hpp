@@ -26,7 +26,7 @@ template <int DP, int NP, int NR>
 constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + 16 + (NR > 1 ? NR * DP * 32 : 0);
 
 template <int DP, class X, int NP, int NR>
-__global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParams p)
+__global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 ? 3 : 2) void block_kernel(AttendParams p)
 {
     constexpr int KT = leaf_keys(DP);      // keys of a leaf
     constexpr int WK = KT / 4;             // of which a wave scores
@@ -97,6 +97,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
     }
     const int i_first = r0 / p.group, i_last = min(tokens - 1, (r0 + NR * 16 - 1) / p.group);
     const bool whole = p.D == DP;
+    const int last_tile = min(NR - 1, (tokens * p.group - r0 - 1) / 16);      // of rows that there are
 
     f32x4 o[NR][DT];
     float m[NR], l[NR];
@@ -177,6 +178,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
         for (int t = 0; t < TILES; ++t) full = full && ok[t] == 0xffff;
 #pragma unroll
         for (int rt = 0; rt < NR; ++rt) {
+            if (rt > 0 && r0 + rt * 16 >= tokens * p.group) continue;      // the whole workgroup's
             // scores of the wave's keys
             if constexpr (NR > 1) {
 #pragma unroll
@@ -209,7 +211,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
             for (int t = 0; t < TILES; ++t) top = __builtin_fmaxf(__builtin_fmaxf(top, __builtin_fmaxf(x[t].x, x[t].y)), __builtin_fmaxf(x[t].z, x[t].w));
             top = row_max(top);
             if (g == 0) tops[wave * 16 + n] = top;
-            if (rt == NR - 1 && NR > 1 && next >= 0) ask_keys();
+            if (rt > 0 && rt == last_tile && next >= 0) ask_keys();
             lds_only_barrier();
             if (rt == 0) {
                 if (!even) {
@@ -231,7 +233,7 @@ __global__ __launch_bounds__(256, NR == 1 ? 3 : 2) void block_kernel(AttendParam
                     }
                 if (next >= 0) {
                     addresses(next, valid);
-                    if (NR == 1) ask_keys();
+                    if (last_tile == 0) ask_keys();
                     ask_values();
                 }
             }
