@@ -17,14 +17,15 @@ constexpr int kUnits = 256;                // compute units
 constexpr int kLanes = 16;                 // of a row's 64 columns
 constexpr int kChains = kThreads / kLanes;
 
-// The parts of rows, joined: those of blocks, and those of chunks, which are `splits` supers each.  Leaves are joined to supers one after the other, as the
-// block's kernel does it; a row is the sum of its supers, in order, each with its weight against
-// the row's largest score.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows.  Bound by
-// latency: every group of 16 lanes asks for eight parts at once.
+// The parts of rows, joined: those of blocks, and those of chunks, which are `splits` supers each.  Leaves
+// are joined to supers one after the other, as the block's kernel does it; a row is the sum of its
+// supers, each with its weight against the row's largest score, in order: first eights of them,
+// then those.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows.  Bound by latency: every
+// group of 16 lanes asks for eight parts at once.
 __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int splits, int block_chains, int chunk_chains, int columns)
 {
-    __shared__ __align__(16) f32x4 sums[kThreads * kSuper];
-    __shared__ f32x2 stats[kChains * kSuper];
+    __shared__ __align__(16) f32x4 sums[kThreads];
+    __shared__ f32x2 stats[kChains];
     __shared__ float tops[kChains];
     const int b = blockIdx.y;
     const Seq s = sequence(p.cache, b);
@@ -38,28 +39,27 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf
     const int r0 = block * (kChains >> chains_log2), r = r0 + team;
     if (r0 >= tokens * p.q_heads) return;
     const bool mine = r < tokens * p.q_heads, mine_d = mine && d < p.D;
-    Visible vis = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit);
-    if (chunk) vis.units = splits;
     const long long row = (long long)s.start * p.q_heads + r;
     const f32x2* stat = p.stat + row * p.slots;
     const float* part = p.part + row * p.slots * p.D + d;
     const bool leaves = !chunk && p.per_unit == 1;
-    // supers of the row, where units are leaves
-    const Visible all = leaves ? visible(place0, tokens, p.window, p.sinks, leaf * kSuper) : vis;
+    // the row's parts, and their eights: supers of leaves, or eights of supers
+    Visible vis = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit), eights = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit * kSuper);
+    if (chunk) {
+        vis = Visible{0, 0, 0, 0, 0, splits};
+        eights = Visible{0, 0, 0, 0, 0, (splits + kSuper - 1) / kSuper};
+    }
 
     // the parts of the first round are on their way while the largest score is found
     f32x2 st[kSuper];
     f32x4 pa[kSuper];
     int at[kSuper];
-    auto ask = [&](int s0) {
-        const int sup = leaves ? s0 + chain : 0, first = leaves && sup < all.units ? all.unit(sup) * kSuper : 0;
+    auto ask = [&](int e) {
+        const int first = e < eights.units ? eights.unit(e) * kSuper : 0;
 #pragma unroll
         for (int i = 0; i < kSuper; ++i) {
-            const int u = leaves ? first + i : s0 + chain * kSuper + i;
-            if (leaves)
-                at[i] = sup >= all.units ? -1 : u < vis.front ? u : u >= vis.start && u - vis.start < vis.units - vis.front ? u - vis.start + vis.front : -1;
-            else
-                at[i] = u < vis.units ? u : -1;
+            const int u = first + i, last = vis.units - vis.front;
+            at[i] = e >= eights.units ? -1 : u < vis.front ? u : u >= vis.start && u - vis.start < last ? u - vis.start + vis.front : -1;
             st[i] = f32x2{kGone, 0.0f};
             pa[i] = f32x4{0, 0, 0, 0};
             if (mine && at[i] >= 0) {
@@ -68,8 +68,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf
             }
         }
     };
-    const int round = leaves ? chains : chains * kSuper;      // supers of a round
-    ask(0);
+    ask(chain);
     float top = kGone;
     if (mine)
         for (int u = chain * kLanes + lane; u < vis.units; u += chains * kLanes) top = __builtin_fmaxf(top, stat[u].x);
@@ -80,43 +79,64 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf
     for (int i = 0; i < chains; ++i) top = __builtin_fmaxf(top, tops[(team << chains_log2) + i]);
     const float base = top == kGone ? 0.0f : top;
 
-    float l = 0.0f;
-    f32x4 o = {0, 0, 0, 0};
-    for (int s0 = 0; s0 < all.units; s0 += round) {
-        if (s0 > 0) {
-            ask(s0);
+    // o, l: sums of whole eights; oe, le: of the eight that is being added up
+    float l = 0.0f, le = 0.0f;
+    f32x4 o = {0, 0, 0, 0}, oe = {0, 0, 0, 0};
+    int eight = -1;
+    for (int e0 = 0; e0 < eights.units; e0 += chains) {
+        if (e0 > 0) {
+            ask(e0 + chain);
             lds_only_barrier();
         }
+        float ls = 0.0f;
+        f32x4 os = {0, 0, 0, 0};
         if (leaves) {
-            float ms = kGone, ls = 0.0f;
-            f32x4 os = {0, 0, 0, 0};
+            float ms = kGone;
 #pragma unroll
             for (int i = 0; i < kSuper; ++i) {
                 if (at[i] < 0) continue;
                 const Factors f = join(ms, ls, st[i].x, st[i].y);
                 os = joined(os, pa[i], f);
             }
-            sums[tid] = os;
-            stats[group] = f32x2{ms, ls};
+            stats[group] = f32x2{ls, exp2_of(ms - base)};
         } else {
 #pragma unroll
             for (int i = 0; i < kSuper; ++i) {
-                sums[(group * kSuper + i) * kLanes + lane] = pa[i];
-                stats[group * kSuper + i] = st[i];
+                const float w = exp2_of(st[i].x - base);
+                ls = __builtin_fmaf(st[i].y, w, ls);
+#pragma unroll
+                for (int c = 0; c < 4; ++c) os[c] = __builtin_fmaf(pa[i][c], w, os[c]);
             }
+            stats[group] = f32x2{ls, 0.0f};
         }
+        sums[tid] = os;
         lds_only_barrier();
         if (chain == 0) {
-            const int n = min(round, all.units - s0), first = team * round;
+            const int n = min(chains, eights.units - e0);
             for (int i = 0; i < n; ++i) {
-                const f32x2 t = stats[first + i];
-                const f32x4 v = sums[(first + i) * kLanes + lane];
-                const float w = exp2_of(t.x - base);
-                l = __builtin_fmaf(t.y, w, l);
-                o = f32x4{__builtin_fmaf(v.x, w, o.x), __builtin_fmaf(v.y, w, o.y), __builtin_fmaf(v.z, w, o.z), __builtin_fmaf(v.w, w, o.w)};
+                const f32x2 t = stats[group + i];
+                const f32x4 v = sums[tid + i * kLanes];
+                if (leaves) {
+                    const int now = eights.unit(e0 + i) / kSuper;
+                    if (now != eight) {
+                        l += le;
+                        o += oe;
+                        le = 0.0f;
+                        oe = f32x4{0, 0, 0, 0};
+                        eight = now;
+                    }
+                    le = __builtin_fmaf(t.x, t.y, le);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) oe[c] = __builtin_fmaf(v[c], t.y, oe[c]);
+                } else {
+                    l += t.x;
+                    o += v;
+                }
             }
         }
     }
+    l += le;
+    o += oe;
     if (mine_d && chain == 0) put_result(p, row, d, o, l);
 }
 
