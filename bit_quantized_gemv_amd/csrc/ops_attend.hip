@@ -181,12 +181,22 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     const int group = q_heads / c->heads, tokens = std::min(p.max_new, kBlockTokens);
     const int rows = tokens * group;
     p.leaf = leaf_keys(p.bound);
+    auto blocks = [&](int tiles) { return (rows + 16 * tiles - 1) / (16 * tiles); };
     p.row_tiles = rows <= 16 ? 1 : rows <= 32 ? 2 : 4;
-    p.row_blocks = (rows + 16 * p.row_tiles - 1) / (16 * p.row_tiles);
-    // leaf by leaf while that is few workgroups, else a super each
-    const long long leaves = units_of(p, tokens, p.leaf);
-    p.per_unit = leaves * c->heads * p.row_blocks * c->n_seqs > 1024 ? kSuper : 1;
+    // Leaf by leaf while those are about as many workgroups as run at once, a further tile of rows
+    // counted as a third of one.  One token, 8 heads of 128, us: 16384 places 22.6 by leaves and 29.0 by
+    // supers, 32768 42.9 and 39.0; 26 rows of 8 heads of 256, 8192 places: 34.6 and 28.7.
+    const long long lists = (long long)c->heads * std::min(c->n_seqs, T);
+    p.per_unit = units_of(p, tokens, p.leaf) * lists * blocks(p.row_tiles) * (2 + p.row_tiles) / 3 > 1200 ? kSuper : 1;
     p.units = units_of(p, tokens, (long long)p.leaf * p.per_unit);
+    // Supers are few: four tiles of rows a workgroup only where that leaves two workgroups for every
+    // compute unit, two where it leaves one.  13 tokens, 64 query heads on 8 of 128, 8192 places, us: 47.6
+    // with four, 33.2 with two, 39.8 with one; 32 sequences of half the query heads, 2048: 82, 99, 137;
+    // 16 on 8 of 256, 8192: 33.7 with two, 28.7 with one.
+    if (p.per_unit > 1) {
+        while (p.row_tiles > 1 && p.units * lists * blocks(p.row_tiles) < (p.row_tiles == 4 ? 2 : 1) * kUnits) p.row_tiles /= 2;
+    }
+    p.row_blocks = blocks(p.row_tiles);
     p.block = p.bound == 64    ? block_kernel_64(f16, f32_out, p.row_tiles, &p.block_lds)
               : p.bound == 128 ? block_kernel_128(f16, f32_out, p.row_tiles, &p.block_lds)
                                : block_kernel_256(f16, f32_out, p.row_tiles, &p.block_lds);
