@@ -284,9 +284,10 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
                        {c->lengths, (size_t)c->n_seqs * 4}};
     const Span outs[] = {{out, (size_t)T * q_heads * c->head_size * size_of(out_dt)}, {workspace, (size_t)need}};
     if (!disjoint(in, outs)) return QMV_E_ALIAS;
-    const long long groups = (plan.units * c->heads + 7) / 8 * 8 * plan.row_blocks, chunk_groups = (long long)plan.chunk_blocks * c->heads;
     // a launch's size in threads is a 32-bit number, and so is the join's
-    if (groups > (1 << 24) - 1 || chunk_groups > (1 << 22) || (long long)plan.max_new * q_heads * ((c->head_size + 63) / 64) > (1 << 24) - 1)
+    const long long groups = (plan.units * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks, wide = std::min<long long>(groups, 1 << 19);
+    const long long chunk_groups = (long long)plan.chunk_blocks * c->heads;
+    if (groups > 1LL << 31 || chunk_groups > (1 << 22) || (long long)plan.max_new * q_heads * ((c->head_size + 63) / 64) > (1 << 24) - 1)
         return QMV_E_CACHE;
     AttendParams p;
     p.q = static_cast<const char*>(q);
@@ -312,7 +313,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.cache = device_cache(c, T);
     p.cache.max_places = plan.length;
     void* args[] = {&p};
-    if (int e = launch(plan.block, dim3((unsigned)groups, c->n_seqs), kThreads, args, plan.block_lds, stream)) return e;
+    if (int e = launch(plan.block, dim3((unsigned)wide, (unsigned)((groups + wide - 1) / wide)), kThreads, args, plan.block_lds, stream)) return e;
     if (plan.max_new > kBlockTokens)
         if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
     return p.slots > 1 ? launch_join(p, plan, c->n_seqs, stream) : QMV_OK;
