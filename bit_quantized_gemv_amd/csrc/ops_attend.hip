@@ -158,6 +158,8 @@ struct Plan {
     const void *block, *chunk;
     int block_lds;
     ChunkShape shape;
+    int block_chains, chunk_chains, columns;      // the join: groups of lanes to a row, and blocks of 64 columns
+    long long join_groups;
     long long part_bytes, stat_bytes;
 };
 
@@ -167,6 +169,14 @@ long long units_of(const Plan& p, int tokens, long long U)
     const long long all = std::max<long long>(1, (p.length + U - 1) / U);
     if (p.window == 0) return all;
     return std::min(all, (std::min(p.sinks, p.length) + U - 1) / U + ((long long)p.window + tokens - 1 + U - 1) / U + 1);
+}
+
+// groups of lanes that share a row of so many parts
+int chains_of(long long parts)
+{
+    int log2 = 0;
+    while (1 << log2 < std::min<long long>(kChains, (parts + kSuper - 1) / kSuper)) ++log2;
+    return log2;
 }
 
 Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length, int window, int sinks, bool f32_out)
@@ -220,6 +230,11 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
         p.splits = (int)std::max<long long>(1, std::min(room, most));
         slots = std::max<long long>(slots, p.splits);
     }
+    p.columns = (c->head_size + 63) / 64;
+    p.block_chains = chains_of(p.units);
+    p.chunk_chains = chains_of(p.splits);
+    auto joins = [&](long long rows, long long parts, int chains) { return parts > 1 ? (rows + (kChains >> chains) - 1) / (kChains >> chains) : 0; };
+    p.join_groups = std::max(joins((long long)tokens * q_heads, p.units, p.block_chains), joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains)) * p.columns;
     const long long parts = slots > 1 ? (long long)T * q_heads * slots : 0;
     p.part_bytes = piece(parts * c->head_size * 4);
     p.stat_bytes = piece(parts * 8);
@@ -229,23 +244,6 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
 int launch(const void* f, dim3 grid, int threads, void** args, int lds, void* stream)
 {
     return hipLaunchKernel(f, grid, dim3(threads), args, (size_t)lds, static_cast<hipStream_t>(stream)) == hipSuccess ? QMV_OK : QMV_E_LAUNCH;
-}
-
-// groups of lanes that share a row of so many parts
-int chains_of(int parts)
-{
-    int log2 = 0;
-    while (1 << log2 < std::min(kChains, (parts + kSuper - 1) / kSuper)) ++log2;
-    return log2;
-}
-
-int launch_join(AttendParams& p, const Plan& plan, int n_seqs, void* stream)
-{
-    int leaf = plan.leaf, splits = plan.splits, columns = (p.D + 63) / 64, block_chains = chains_of((int)plan.units), chunk_chains = chains_of(splits);
-    auto groups = [&](long long tokens, int parts, int chains) { return parts > 1 ? (tokens * p.q_heads + (kChains >> chains) - 1) / (kChains >> chains) : 0; };
-    const long long most = std::max(groups(std::min(plan.max_new, kBlockTokens), (int)plan.units, block_chains), groups(plan.max_new, splits, chunk_chains));
-    void* args[] = {&p, &leaf, &splits, &block_chains, &chunk_chains, &columns};
-    return launch((const void*)&join_kernel, dim3((unsigned)(most * columns), n_seqs), kThreads, args, 0, stream);
 }
 
 }  // namespace
@@ -268,7 +266,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
                void* stream)
 {
     using namespace ops;
-    if (!c || !q || !out || !workspace) return QMV_E_NULL;
+    if (!c || !q || !out) return QMV_E_NULL;
     if (int e = check_sizes(c, T, q_heads, max_new, max_length, window, sinks)) return e;
     CacheSpans cs;
     if (int e = check_cache(c, T, q_heads, &cs)) return e;
@@ -279,16 +277,16 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     if (nq < 0) return QMV_E_STRIDE;
     const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks, out_dt == QMV_DT_F32);
     const long long need = plan.part_bytes + plan.stat_bytes;
+    if (need > 0 && !workspace) return QMV_E_NULL;
     if (workspace_bytes < need) return QMV_E_WORKSPACE;
     const Span in[] = {{q, (size_t)nq * 2}, {c->k, cs.k}, {c->v, cs.v}, {c->pages, cs.pages}, {c->starts, (size_t)(c->n_seqs + 1) * 4},
                        {c->lengths, (size_t)c->n_seqs * 4}};
     const Span outs[] = {{out, (size_t)T * q_heads * c->head_size * size_of(out_dt)}, {workspace, (size_t)need}};
     if (!disjoint(in, outs)) return QMV_E_ALIAS;
-    // a launch's size in threads is a 32-bit number, and so is the join's
+    // rows are counted, and a launch's threads, in 32 bits
     const long long groups = (plan.units * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks, wide = std::min<long long>(groups, 1 << 19);
     const long long chunk_groups = (long long)plan.chunk_blocks * c->heads;
-    if (groups > 1LL << 31 || chunk_groups > (1 << 22) || (long long)plan.max_new * q_heads * ((c->head_size + 63) / 64) > (1 << 24) - 1)
-        return QMV_E_CACHE;
+    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 31 || chunk_groups >= 1 << 23 || plan.join_groups >= 1 << 24) return QMV_E_CACHE;
     AttendParams p;
     p.q = static_cast<const char*>(q);
     p.out = static_cast<char*>(out);
@@ -316,7 +314,10 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     if (int e = launch(plan.block, dim3((unsigned)wide, (unsigned)((groups + wide - 1) / wide)), kThreads, args, plan.block_lds, stream)) return e;
     if (plan.max_new > kBlockTokens)
         if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
-    return p.slots > 1 ? launch_join(p, plan, c->n_seqs, stream) : QMV_OK;
+    if (p.slots == 1) return QMV_OK;
+    int leaf = plan.leaf, splits = plan.splits, block_chains = plan.block_chains, chunk_chains = plan.chunk_chains, columns = plan.columns;
+    void* join[] = {&p, &leaf, &splits, &block_chains, &chunk_chains, &columns};
+    return launch((const void*)&join_kernel, dim3((unsigned)plan.join_groups, c->n_seqs), kThreads, join, 0, stream);
 }
 
 }  // extern "C"

@@ -70,7 +70,7 @@ __device__ __forceinline__ f32x2 unpack(uint32_t v, _Float16) { return __builtin
 // would reach the rows that do not see the key too, by zero times infinity.  So where rows of a tile
 // see different keys, the values are looked at in LDS first.  If there are any, they are
 // taken out of the product, and products of marks count for every output the NaN, infinities
-// and negative infinities that it sees.
+// and negative infinities that its row sees.
 constexpr uint32_t no_number(__bf16) { return 0x7f80; }       // the exponent
 constexpr uint32_t no_number(_Float16) { return 0x7c00; }
 constexpr uint32_t one(__bf16) { return 0x3f80; }
@@ -122,12 +122,6 @@ template <class X>
 __device__ __forceinline__ u32x4 marks4(u32x4 w, Kind k)
 {
     return u32x4{marks<X>(w.x, k), marks<X>(w.y, k), marks<X>(w.z, k), marks<X>(w.w, k)};
-}
-// weights that are not zero
-template <class X>
-__device__ __forceinline__ u32x4 weighed(u32x4 w)
-{
-    return marks4<X>(w, Kind{0x7fff, 1, 0x7ffe, 0.0f});
 }
 // the output that has met `count` of them
 __device__ __forceinline__ f32x4 met(f32x4 o, f32x4 count, Kind k)

@@ -305,9 +305,14 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
                     for (int d = 0; d < DT; ++d) count[d] = f32x4{0, 0, 0, 0};
 #pragma unroll 1
                     for (int k = 0; k < US; ++k) {
-                        const u32x4 w = weighed<X>(*reinterpret_cast<const u32x4*>(weights + k * 1024 + lane * 16));
+                        u32x4 seen;
 #pragma unroll
-                        for (int d = 0; d < DT; ++d) count[d] = mfma(marks4<X>(value(d, k), kind), w, count[d], X());
+                        for (int i = 0; i < 4; ++i) {
+                            const int j = leaf + k * 32 + (i >> 1) * 16 + 4 * g + 2 * (i & 1);
+                            seen[i] = (sees(j, high[rt], low[rt], p.sinks, 1) ? one(X()) : 0) | (sees(j + 1, high[rt], low[rt], p.sinks, 1) ? one(X()) << 16 : 0);
+                        }
+#pragma unroll
+                        for (int d = 0; d < DT; ++d) count[d] = mfma(marks4<X>(value(d, k), kind), seen, count[d], X());
                     }
 #pragma unroll
                     for (int d = 0; d < DT; ++d) a[d] = met(a[d], count[d], kind);
