@@ -185,6 +185,56 @@ def test_blocks_as_single_tokens(D, dt, window):
     assert torch.equal(again, whole)
 
 
+@pytest.mark.parametrize("D,Hq,Hkv,n", [(64, 32, 2, 13), (128, 64, 8, 13), (128, 20, 4, 16), (256, 16, 8, 13), (256, 32, 4, 16), (96, 9, 3, 5)])
+@pytest.mark.parametrize("window", [0, 333])
+def test_row_tiles(D, Hq, Hkv, n, window):
+    """Blocks of one to many tiles of rows, in calls that are cut up in different ways: the same bits."""
+    length = 1900
+    c = Batch([n], [length], Hkv, D, 16, seed=D + n)
+    qs = queries(c, Hq).to(DEV)
+    k, v, pages, starts, lens = c.on()
+    kw = dict(window=window, sinks=5 if window else 0)
+    whole = q.attend(qs, k, v, pages, starts, lens, **kw)
+    check_attend(whole, *attend64(qs.cpu(), c, **kw), "bf16", "bf16")
+    many = 70
+    rep = q.attend(qs.repeat(many, 1, 1), k, v, pages.repeat(many, 1), torch.arange(many + 1, dtype=torch.int32, device=DEV) * n, lens.repeat(many),
+                   max_new=n, max_length=length, **kw)
+    assert torch.equal(rep.reshape(many, n, Hq, D), whole.expand(many, n, Hq, D))
+    one = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    for i in (0, n - 1):
+        got = q.attend(qs[i:i + 1], k, v, pages, one, lens - (n - 1 - i), **kw)
+        assert torch.equal(got[0], whole[i]), i
+    # beside a chunk, and with loose bounds
+    c2 = Batch([n, 40], [length, 100], Hkv, D, 16, seed=D + n)
+    k2, v2, pages2, starts2, lens2 = c2.on()
+    q2 = torch.cat([qs, queries(c2, Hq)[n:].to(DEV)])
+    again = q.attend(q2, k2, v2, pages2, starts2, lens2, **kw)
+    alone = q.attend(qs, k2, v2, pages2[:1], starts2[:2], lens2[:1], **kw)
+    assert torch.equal(again[:n], alone)
+
+
+@pytest.mark.parametrize("H", [1, 2])
+def test_very_long(H):
+    """More leaves and supers than a join takes in one round."""
+    c = Batch([2], [70001], H, 256, 64, seed=H)
+    qs = queries(c, H)
+    kw = dict(out_dtype=torch.float32)
+    got = run(c, qs, **kw)
+    check_attend(got, *attend64(qs, c), "bf16", "f32")
+    k, v, pages, starts, lens = c.on()
+    one = torch.tensor([0, 1], dtype=torch.int32, device=DEV)
+    for i in range(2):
+        assert torch.equal(q.attend(qs[i:i + 1].to(DEV), k, v, pages, one, lens - 1 + i, **kw)[0], got[i])
+    three = q.attend(qs.repeat(3, 1, 1).to(DEV), k, v, pages.repeat(3, 1), torch.arange(4, dtype=torch.int32, device=DEV) * 2, lens.repeat(3), **kw)
+    assert torch.equal(three.reshape(3, 2, H, 256), got.expand(3, 2, H, 256))
+
+
+@pytest.mark.parametrize("n,length,D", [(17, 20000, 64), (50, 9000, 256), (130, 5000, 192)])
+def test_shared_keys(n, length, D):
+    """Few rows over many keys: workgroups share the keys, and their parts are joined."""
+    check(Batch([n], [length], 1, D, 32, seed=n), 1, "f32")
+
+
 def test_chunks_repeat():
     """The same call again gives the same bits."""
     c = Batch([300, 2, 77], [900, 50, 77], 2, 128, 16, seed=12)

@@ -47,6 +47,8 @@ SHAPES = [
     (700, 33, 7, 96, 96, "f32", "f32", "f16", 2, False, True),
     (257, 1, 1, 16, 16, "bf16", "bf16", "f16", 1, True, False),
     (50, 128, 16, 128, 64, "bf16", "f32", "bf16", 1, False, True),
+    (4200, 2, 1, 48, 32, "bf16", "bf16", "bf16", 1, False, True),
+    (300, 9, 3, 112, 96, "f32", "f32", "f16", 2, True, False),
 ]
 
 
