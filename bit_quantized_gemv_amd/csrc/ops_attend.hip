@@ -22,122 +22,133 @@ constexpr int kChains = kThreads / kLanes;
 // supers, each with its weight against the row's largest score, in order: first eights of them,
 // then those.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows.  Bound by latency: every
 // group of 16 lanes asks for eight parts at once.
-__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int splits, int block_chains, int chunk_chains, int columns)
+template <bool MORE>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int block_chains, int chunk_chains, int columns, Divisor by_columns, int turns)
 {
     __shared__ __align__(16) f32x4 sums[kThreads];
     __shared__ f32x2 stats[kChains];
     __shared__ float tops[kChains];
-    const int b = blockIdx.y;
+    const Cache& c = p.cache;
+    together(p.part, p.stat, p.chunk_part, p.chunk_stat, p.out, c.starts, c.lengths, c.n_seqs, c.max_places, c.T, p.units, p.per_unit, p.splits, p.apart, p.q_heads, p.D,
+             p.window, p.sinks, p.max_new, p.out_f32, p.by_seqs.magic, p.by_seqs.shift, leaf, block_chains, chunk_chains, columns, by_columns.magic, by_columns.shift, turns);
+    // the sequences side by side, so that those without work do not leave compute units to themselves
+    const int group_of = blockIdx.y * gridDim.x + blockIdx.x, over = divide(group_of, by_columns), column = group_of - over * columns;
+    const int turn = divide(over, p.by_seqs), b = over - turn * p.cache.n_seqs;
+    if (turn >= turns) return;
     const Seq s = sequence(p.cache, b);
-    const bool chunk = s.count > kBlockTokens;
-    if ((chunk ? splits : p.units) <= 1) return;      // written already
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
+    const bool chunk = tokens > kBlockTokens;
+    const int slots = chunk ? p.splits : p.units;
+    if (slots <= 1) return;      // written already
     const int tid = threadIdx.x, lane = tid & (kLanes - 1), group = tid / kLanes;
     const int chains_log2 = chunk ? chunk_chains : block_chains, chains = 1 << chains_log2;
     const int chain = group & (chains - 1), team = group >> chains_log2;
-    const int block = blockIdx.x / columns, d = (blockIdx.x - block * columns) * 64 + lane * 4;
-    const int r0 = block * (kChains >> chains_log2), r = r0 + team;
-    if (r0 >= tokens * p.q_heads) return;
-    const bool mine = r < tokens * p.q_heads, mine_d = mine && d < p.D;
-    const long long row = (long long)s.start * p.q_heads + r;
-    const f32x2* stat = p.stat + row * p.slots;
-    const float* part = p.part + row * p.slots * p.D + d;
+    const int d = column * 64 + lane * 4, rows = kChains >> chains_log2;
     const bool leaves = !chunk && p.per_unit == 1;
     // the row's parts, and their eights: supers of leaves, or eights of supers
     Visible vis = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit), eights = visible(place0, tokens, p.window, p.sinks, leaf * p.per_unit * kSuper);
     if (chunk) {
-        vis = Visible{0, 0, 0, 0, 0, splits};
-        eights = Visible{0, 0, 0, 0, 0, (splits + kSuper - 1) / kSuper};
+        vis = Visible{0, 0, 0, 0, 0, slots};
+        eights = Visible{0, 0, 0, 0, 0, (slots + kSuper - 1) / kSuper};
     }
-
-    // the parts of the first round are on their way while the largest score is found
-    f32x2 st[kSuper];
-    f32x4 pa[kSuper];
-    int at[kSuper];
-    auto ask = [&](int e) {
-        const int first = e < eights.units ? eights.unit(e) * kSuper : 0;
-#pragma unroll
-        for (int i = 0; i < kSuper; ++i) {
-            const int u = first + i, last = vis.units - vis.front;
-            at[i] = e >= eights.units ? -1 : u < vis.front ? u : u >= vis.start && u - vis.start < last ? u - vis.start + vis.front : -1;
-            st[i] = f32x2{kGone, 0.0f};
-            pa[i] = f32x4{0, 0, 0, 0};
-            if (mine && at[i] >= 0) {
-                st[i] = stat[at[i]];
-                if (mine_d) pa[i] = *reinterpret_cast<const f32x4*>(part + (long long)at[i] * p.D);
-            }
-        }
-    };
-    ask(chain);
-    float top = kGone;
-    if (mine)
-        for (int u = chain * kLanes + lane; u < vis.units; u += chains * kLanes) top = __builtin_fmaxf(top, stat[u].x);
-#pragma unroll
-    for (int i = 1; i < kLanes; i <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, i));
-    if (lane == 0) tops[group] = top;
-    lds_only_barrier();
-    for (int i = 0; i < chains; ++i) top = __builtin_fmaxf(top, tops[(team << chains_log2) + i]);
-    const float base = top == kGone ? 0.0f : top;
-
-    // o, l: sums of whole eights; oe, le: of the eight that is being added up
-    float l = 0.0f, le = 0.0f;
-    f32x4 o = {0, 0, 0, 0}, oe = {0, 0, 0, 0};
-    int eight = -1;
-    for (int e0 = 0; e0 < eights.units; e0 += chains) {
-        if (e0 > 0) {
-            ask(e0 + chain);
-            lds_only_barrier();
-        }
-        float ls = 0.0f;
-        f32x4 os = {0, 0, 0, 0};
-        if (leaves) {
-            float ms = kGone;
+    const long long first = chunk ? (long long)s.start * p.q_heads : block_row(p, b, s.start);
+    for (int r0 = turn * rows; r0 < tokens * p.q_heads; r0 += turns * rows) {
+        const int r = r0 + team;
+        const bool mine = r < tokens * p.q_heads, mine_d = mine && d < p.D;
+        const long long row = (long long)s.start * p.q_heads + r;
+        const f32x2* stat = (chunk ? p.chunk_stat : p.stat) + (first + r) * slots;
+        const float* part = (chunk ? p.chunk_part : p.part) + (first + r) * slots * p.D + d;
+        // the parts of the first round are on their way while the largest score is found
+        f32x2 st[kSuper];
+        f32x4 pa[kSuper];
+        int at[kSuper];
+        auto ask = [&](int e) {
+            const int from = e < eights.units ? eights.unit(e) * kSuper : 0;
 #pragma unroll
             for (int i = 0; i < kSuper; ++i) {
-                if (at[i] < 0) continue;
-                const Factors f = join(ms, ls, st[i].x, st[i].y);
-                os = joined(os, pa[i], f);
+                const int u = from + i, last = vis.units - vis.front;
+                at[i] = e >= eights.units ? -1 : u < vis.front ? u : u >= vis.start && u - vis.start < last ? u - vis.start + vis.front : -1;
+                st[i] = f32x2{kGone, 0.0f};
+                pa[i] = f32x4{0, 0, 0, 0};
+                if (mine && at[i] >= 0) {
+                    st[i] = stat[at[i]];
+                    if (mine_d) pa[i] = *reinterpret_cast<const f32x4*>(part + (long long)at[i] * p.D);
+                }
             }
-            stats[group] = f32x2{ls, exp2_of(ms - base)};
-        } else {
+        };
+        ask(chain);
+        float top = kGone;
+        if (mine)
+            for (int u = chain * kLanes + lane; u < vis.units; u += chains * kLanes) top = __builtin_fmaxf(top, stat[u].x);
 #pragma unroll
-            for (int i = 0; i < kSuper; ++i) {
-                const float w = exp2_of(st[i].x - base);
-                ls = __builtin_fmaf(st[i].y, w, ls);
-#pragma unroll
-                for (int c = 0; c < 4; ++c) os[c] = __builtin_fmaf(pa[i][c], w, os[c]);
-            }
-            stats[group] = f32x2{ls, 0.0f};
-        }
-        sums[tid] = os;
+        for (int i = 1; i < kLanes; i <<= 1) top = __builtin_fmaxf(top, __shfl_xor(top, i));
+        if (lane == 0) tops[group] = top;
         lds_only_barrier();
-        if (chain == 0) {
-            const int n = min(chains, eights.units - e0);
-            for (int i = 0; i < n; ++i) {
-                const f32x2 t = stats[group + i];
-                const f32x4 v = sums[tid + i * kLanes];
-                if (leaves) {
-                    const int now = eights.unit(e0 + i) / kSuper;
-                    if (now != eight) {
-                        l += le;
-                        o += oe;
-                        le = 0.0f;
-                        oe = f32x4{0, 0, 0, 0};
-                        eight = now;
-                    }
-                    le = __builtin_fmaf(t.x, t.y, le);
+        for (int i = 0; i < chains; ++i) top = __builtin_fmaxf(top, tops[(team << chains_log2) + i]);
+        const float base = top == kGone ? 0.0f : top;
+
+        // o, l: sums of whole eights; oe, le: of the eight that is being added up
+        float l = 0.0f, le = 0.0f;
+        f32x4 o = {0, 0, 0, 0}, oe = {0, 0, 0, 0};
+        int eight = -1;
+        for (int e0 = 0; e0 < eights.units; e0 += chains) {
+            if (e0 > 0) {
+                ask(e0 + chain);
+                lds_only_barrier();
+            }
+            float ls = 0.0f;
+            f32x4 os = {0, 0, 0, 0};
+            if (leaves) {
+                float ms = kGone;
 #pragma unroll
-                    for (int c = 0; c < 4; ++c) oe[c] = __builtin_fmaf(v[c], t.y, oe[c]);
-                } else {
-                    l += t.x;
-                    o += v;
+                for (int i = 0; i < kSuper; ++i) {
+                    if (at[i] < 0) continue;
+                    const Factors f = join(ms, ls, st[i].x, st[i].y);
+                    os = joined(os, pa[i], f);
+                }
+                stats[group] = f32x2{ls, exp2_of(ms - base)};
+            } else {
+#pragma unroll
+                for (int i = 0; i < kSuper; ++i) {
+                    const float w = exp2_of(st[i].x - base);
+                    ls = __builtin_fmaf(st[i].y, w, ls);
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) os[c] = __builtin_fmaf(pa[i][c], w, os[c]);
+                }
+                stats[group] = f32x2{ls, 0.0f};
+            }
+            sums[tid] = os;
+            lds_only_barrier();
+            if (chain == 0) {
+                const int n = min(chains, eights.units - e0);
+                for (int i = 0; i < n; ++i) {
+                    const f32x2 t = stats[group + i];
+                    const f32x4 v = sums[tid + i * kLanes];
+                    if (leaves) {
+                        const int now = eights.unit(e0 + i) / kSuper;
+                        if (now != eight) {
+                            l += le;
+                            o += oe;
+                            le = 0.0f;
+                            oe = f32x4{0, 0, 0, 0};
+                            eight = now;
+                        }
+                        le = __builtin_fmaf(t.x, t.y, le);
+#pragma unroll
+                        for (int c = 0; c < 4; ++c) oe[c] = __builtin_fmaf(v[c], t.y, oe[c]);
+                    } else {
+                        l += t.x;
+                        o += v;
+                    }
                 }
             }
         }
+        l += le;
+        o += oe;
+        if (mine_d && chain == 0) put_result(p, row, d, o, l);
+        if constexpr (!MORE) return;
+        lds_only_barrier();
     }
-    l += le;
-    o += oe;
-    if (mine_d && chain == 0) put_result(p, row, d, o, l);
 }
 
 int check_sizes(const qmv_cache* c, int T, int q_heads, int max_new, int max_length, int window, int sinks)
@@ -154,13 +165,17 @@ struct Plan {
     int bound, leaf;
     int row_tiles, row_blocks, per_unit;          // blocks: a workgroup's tiles of rows, and a unit's leaves
     long long units;                              // of a sequence, at most
-    int chunk_blocks, splits;                     // chunks: tiles of rows, and the shares of their keys
+    long long chunk_tiles;                        // chunks: tiles of rows of all of them, at most
+    int splits;                                   // and the shares of their keys
     const void *block, *chunk;
     int block_lds;
     ChunkShape shape;
     int block_chains, chunk_chains, columns;      // the join: groups of lanes to a row, and blocks of 64 columns
-    long long join_groups;
-    long long part_bytes, stat_bytes;
+    long long join_turns;                         // workgroups of a sequence's 64 columns
+    bool join_more;                               // which may have more than 16 rows each
+    int apart;                                    // rows of a sequence among the parts of blocks; 0: as in q
+    long long part_bytes, stat_bytes, chunk_part_bytes, chunk_stat_bytes;
+    long long bytes() const { return part_bytes + stat_bytes + chunk_part_bytes + chunk_stat_bytes; }
 };
 
 // units of U places that `tokens` neighbouring ones see at most
@@ -219,28 +234,41 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
                        : c->head_size <= 192 ? chunk_kernel_192
                                              : chunk_kernel_256;
     p.chunk = chunk(f16, f32_out, &p.shape);
-    p.chunk_blocks = (int)(((long long)p.max_new * group + p.shape.rows - 1) / p.shape.rows);
+    p.chunk_tiles = 0;
     p.splits = 1;
-    long long slots = p.units;
     if (p.max_new > kBlockTokens) {
         // as many shares as there is room for on the compute units, of 256 keys at least; a chunk has more
         // tokens than a block, so T bounds how many there are
         const long long chunks = std::min<long long>(c->n_seqs, T / (kBlockTokens + 1));
-        const long long tiles = std::min(chunks * p.chunk_blocks, (long long)T * group / p.shape.rows + chunks);
-        const long long room = kUnits * p.shape.at_once / std::max<long long>(1, tiles * c->heads);
+        p.chunk_tiles = std::min(chunks * (((long long)p.max_new * group + p.shape.rows - 1) / p.shape.rows), (long long)T * group / p.shape.rows + chunks);
+        const long long room = kUnits * p.shape.at_once / std::max<long long>(1, p.chunk_tiles * c->heads);
         const long long most = (std::min<long long>(p.length, p.window ? (long long)p.window + p.sinks + p.shape.rows / group : p.length) + 255) / 256;
         p.splits = (int)std::max<long long>(1, std::min(room, most));
-        slots = std::max<long long>(slots, p.splits);
     }
     p.columns = (c->head_size + 63) / 64;
     p.block_chains = chains_of(p.units);
     p.chunk_chains = chains_of(p.splits);
     auto joins = [&](long long rows, long long parts, int chains) { return parts > 1 ? (rows + (kChains >> chains) - 1) / (kChains >> chains) : 0; };
-    p.join_groups = std::max(joins((long long)tokens * q_heads, p.units, p.block_chains), joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains)) * p.columns;
-    const long long parts = slots > 1 ? (long long)T * q_heads * slots : 0;
+    // a workgroup for every 16 rows, or, beside chunks, as many as there is room for, and one token's at least
+    const long long block_turns = joins((long long)tokens * q_heads, p.units, p.block_chains);
+    p.join_turns = p.max_new <= kBlockTokens ? block_turns : std::min(block_turns, std::max(joins(q_heads, p.units, p.block_chains), 4096LL / (p.columns * c->n_seqs)));
+    p.join_more = p.join_turns < block_turns;
+    p.join_turns = std::max(p.join_turns, joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains));
+    p.apart = (long long)c->n_seqs * tokens < T ? tokens : 0;
+    const long long parts = p.units > 1 ? (long long)(p.apart > 0 ? c->n_seqs * tokens : T) * q_heads * p.units : 0;
+    const long long chunk_parts = p.splits > 1 ? (long long)T * q_heads * p.splits : 0;
     p.part_bytes = piece(parts * c->head_size * 4);
     p.stat_bytes = piece(parts * 8);
+    p.chunk_part_bytes = piece(chunk_parts * c->head_size * 4);
+    p.chunk_stat_bytes = piece(chunk_parts * 8);
     return p;
+}
+
+// so many workgroups, as blockIdx.y * gridDim.x + blockIdx.x counts them (and some more)
+dim3 grid_of(long long groups)
+{
+    const long long wide = std::min<long long>(groups, 1 << 19);
+    return dim3((unsigned)wide, (unsigned)((groups + wide - 1) / wide));
 }
 
 int launch(const void* f, dim3 grid, int threads, void** args, int lds, void* stream)
@@ -259,7 +287,7 @@ long long qmv_attend_workspace(const qmv_cache* c, int T, int q_heads, int max_n
     using namespace ops;
     if (!c || check_sizes(c, T, q_heads, max_new, max_length, window, sinks) != QMV_OK) return -1;
     const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks, false);
-    return plan.part_bytes + plan.stat_bytes;
+    return plan.bytes();
 }
 
 int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
@@ -278,7 +306,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     const long long size[] = {T, q_heads}, stride[] = {q_token, q_head}, nq = extent(size, stride, c->head_size);
     if (nq < 0) return QMV_E_STRIDE;
     const Plan plan = plan_of(c, T, q_heads, max_new, max_length, window, sinks, out_dt == QMV_DT_F32);
-    const long long need = plan.part_bytes + plan.stat_bytes;
+    const long long need = plan.bytes();
     if (need > 0 && !workspace) return QMV_E_NULL;
     if (workspace_bytes < need) return QMV_E_WORKSPACE;
     const Span in[] = {{q, (size_t)nq * 2}, {c->k, cs.k}, {c->v, cs.v}, {c->pages, cs.pages}, {c->starts, (size_t)(c->n_seqs + 1) * 4},
@@ -286,14 +314,18 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     const Span outs[] = {{out, (size_t)T * q_heads * c->head_size * size_of(out_dt)}, {workspace, (size_t)need}};
     if (!disjoint(in, outs)) return QMV_E_ALIAS;
     // rows are counted, and a launch's threads, in 32 bits
-    const long long groups = (plan.units * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks, wide = std::min<long long>(groups, 1 << 19);
-    const long long chunk_groups = (long long)plan.chunk_blocks * c->heads;
-    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 31 || chunk_groups >= 1 << 23 || plan.join_groups >= 1 << 24) return QMV_E_CACHE;
+    const long long groups = (plan.units * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks;
+    const long long chunk_groups = plan.chunk_tiles * c->heads, join_groups = plan.join_turns * plan.columns * c->n_seqs;
+    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 31 || chunk_groups >= 1 << 23 || join_groups >= 1LL << 31) return QMV_E_CACHE;
     AttendParams p;
     p.q = static_cast<const char*>(q);
     p.out = static_cast<char*>(out);
-    p.part = static_cast<float*>(workspace);
-    p.stat = reinterpret_cast<f32x2*>(static_cast<char*>(workspace) + plan.part_bytes);
+    char* const scratch = static_cast<char*>(workspace);
+    p.part = reinterpret_cast<float*>(scratch);
+    p.stat = reinterpret_cast<f32x2*>(scratch + plan.part_bytes);
+    p.chunk_part = reinterpret_cast<float*>(scratch + plan.part_bytes + plan.stat_bytes);
+    p.chunk_stat = reinterpret_cast<f32x2*>(scratch + plan.part_bytes + plan.stat_bytes + plan.chunk_part_bytes);
+    p.apart = plan.apart;
     p.q_token = 2 * q_token;
     p.q_head = 2 * q_head;
     p.q_heads = q_heads;
@@ -305,21 +337,28 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.max_new = plan.max_new;
     p.out_f32 = out_dt == QMV_DT_F32;
     p.units = (int)plan.units;
-    p.slots = std::max(p.units, plan.splits);
+    p.splits = plan.splits;
     p.row_blocks = plan.row_blocks;
+    p.rows_last = plan.max_new > kBlockTokens ? (int)(groups / 8 / plan.row_blocks) : 0;
     p.per_unit = plan.per_unit;
     // a scale of zero weighs all places that are seen alike; the smallest does so too, and hides the others
     p.scale = scale == 0.0f ? 1e-37f : scale * 1.44269504088896340736f;
+    p.by_group = divisor(p.group);
+    p.by_heads = divisor(p.heads);
+    p.by_seqs = divisor(c->n_seqs);
+    p.by_rows = divisor(p.rows_last > 0 ? p.rows_last : p.row_blocks);
     p.cache = device_cache(c, T);
     p.cache.max_places = plan.length;
     void* args[] = {&p};
-    if (int e = launch(plan.block, dim3((unsigned)wide, (unsigned)((groups + wide - 1) / wide)), kThreads, args, plan.block_lds, stream)) return e;
-    if (plan.max_new > kBlockTokens)
-        if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, c->n_seqs, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
-    if (p.slots == 1) return QMV_OK;
-    int leaf = plan.leaf, splits = plan.splits, block_chains = plan.block_chains, chunk_chains = plan.chunk_chains, columns = plan.columns;
-    void* join[] = {&p, &leaf, &splits, &block_chains, &chunk_chains, &columns};
-    return launch((const void*)&join_kernel, dim3((unsigned)plan.join_groups, c->n_seqs), kThreads, join, 0, stream);
+    if (int e = launch(plan.block, grid_of(groups), kThreads, args, plan.block_lds, stream)) return e;
+    if (chunk_groups > 0)
+        if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
+    if (p.units == 1 && p.splits == 1) return QMV_OK;
+    int leaf = plan.leaf, block_chains = plan.block_chains, chunk_chains = plan.chunk_chains, columns = plan.columns;
+    int turns = (int)plan.join_turns;
+    Divisor by_columns = divisor(columns);
+    void* join[] = {&p, &leaf, &block_chains, &chunk_chains, &columns, &by_columns, &turns};
+    return launch(plan.join_more ? (const void*)&join_kernel<true> : (const void*)&join_kernel<false>, grid_of(join_groups), kThreads, join, 0, stream);
 }
 
 }  // extern "C"

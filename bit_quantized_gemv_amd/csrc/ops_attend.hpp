@@ -42,13 +42,18 @@ constexpr float kGone = -__builtin_huge_valf();
 struct AttendParams {
     const char* q;
     char* out;
-    float* part;                    // [token][head][slot][D]: sums of weights * values
-    f32x2* stat;                    // [token][head][slot]: largest score and sum of weights
+    float* part;                    // [token][head][unit][D]: a block's sums of weights * values
+    f32x2* stat;                    // [token][head][unit]: their largest scores and sums of weights
+    float* chunk_part;              // the same of chunks, a share of the keys for every unit
+    f32x2* chunk_stat;
     long long q_token, q_head;      // bytes
     int q_heads, heads, group, D;
     int window, sinks, max_new, out_f32;
-    int slots, units, row_blocks, per_unit;
+    int units, row_blocks, per_unit, splits;
+    int rows_last;                  // blocks: workgroups of the first tiles of rows, on a die, after which those of the next come (0: side by side)
+    int apart;                      // a block's tokens in part and stat: by sequence, so many each (0: as in q)
     float scale;                    // times log2(e)
+    Divisor by_group, by_heads, by_seqs, by_rows;      // the last: rows_last, or row_blocks
     Cache cache;
 };
 
@@ -234,6 +239,12 @@ __device__ __forceinline__ f32x4 joined(f32x4 o, f32x4 o2, Factors f)
 {
     return f32x4{__builtin_fmaf(o2.x, f.b, o.x * f.a), __builtin_fmaf(o2.y, f.b, o.y * f.a), __builtin_fmaf(o2.z, f.b, o.z * f.a),
                  __builtin_fmaf(o2.w, f.b, o.w * f.a)};
+}
+
+// The first row of a block's tokens in part and stat.
+__device__ __forceinline__ long long block_row(const AttendParams& p, int b, int start)
+{
+    return (long long)(p.apart > 0 ? b * p.apart : start) * p.q_heads;
 }
 
 // four values of a row's result; l = 0: the row has seen nothing

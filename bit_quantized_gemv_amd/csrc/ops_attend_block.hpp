@@ -43,16 +43,23 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
     char* const queries = reinterpret_cast<char*>(odds + 4);
 
     const Cache& c = p.cache;
-    together(c.pages, c.pages_row, c.starts, c.lengths, c.magic, c.shift, c.max_pages, c.T, p.per_unit, p.window, p.heads, p.row_blocks, p.units);
+    together(c.pages, c.pages_row, c.starts, c.lengths, c.by_page.magic, c.by_page.shift, c.max_pages, c.T, c.n_seqs, p.per_unit, p.window, p.heads, p.row_blocks, p.units,
+             p.rows_last, p.by_rows.magic, p.by_rows.shift, p.by_heads.magic, p.by_heads.shift, p.by_seqs.magic, p.by_seqs.shift);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    // Eight units side by side on the eight compute dies, shifted by the sequence so that short sequences
-    // leave none without work; on a die, all of a unit's heads and row blocks one after the other, since
-    // heads lie next to each other in memory in most caches.  64 ragged sequences of up to 8192 places, 8
-    // heads of 128: 225 us, by heads over the dies 254.
-    const int block = blockIdx.y * gridDim.x + blockIdx.x, turn = block >> 3, rb = turn % p.row_blocks, over = turn / p.row_blocks;
-    const int head = over % p.heads, unit = over / p.heads * 8 + (block & 7), b = unit / p.units, u = (unit - b * p.units + b) % p.units;
-    if (b >= p.cache.n_seqs) return;
+    // The first unit of all sequences, then the second, eight side by side on the eight compute dies, and
+    // each sequence's over all dies: its n_seqs-th next, or the one beside, is an odd number of dies on.
+    // On a die, all of a unit's heads and row blocks one after the other, since heads lie next to
+    // each other in memory in most caches.  Beside chunks, where most sequences have one tile of rows, the
+    // others come last: workgroups without work between the others would leave compute units to themselves.
+    // 255 single tokens of 1000 places, 8 heads of 128, with as many rows as 16 tokens have, us:
+    // 205, 488 side by side.
+    const int block = blockIdx.y * gridDim.x + blockIdx.x, turn = block >> 3;
+    const int rows_turn = divide(turn, p.by_rows), rows_rest = turn - rows_turn * (p.rows_last > 0 ? p.rows_last : p.row_blocks);
+    const int rb = p.rows_last > 0 ? rows_turn : rows_rest, over = p.rows_last > 0 ? rows_rest : rows_turn;
+    const int eight = divide(over, p.by_heads), head = over - eight * p.heads, unit = eight * 8 + (block & 7), u = divide(unit, p.by_seqs);
+    if (u >= p.units || rb >= p.row_blocks) return;
+    const int shifted = unit - u * c.n_seqs + (c.n_seqs & 1 ? 0 : u - divide(u, p.by_seqs) * c.n_seqs), b = shifted < c.n_seqs ? shifted : shifted - c.n_seqs;
     // pages of the lane's keys of a leaf, key n of every tile
     const int32_t* const table = p.cache.pages + b * p.cache.pages_row;
     int entry[TILES];
@@ -68,8 +75,8 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
     const int U = KT * p.per_unit, early = p.window == 0 ? u * U : -1;
     if (early >= 0) ask_pages(early);
     const Seq s = sequence(p.cache, b);
-    if (s.count > kBlockTokens) return;
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
+    if (tokens > kBlockTokens) return;
     const int r0 = rb * NR * 16;
     if (r0 >= tokens * p.group) return;
     const Visible vis = visible(place0, tokens, p.window, p.sinks, U);
@@ -82,7 +89,7 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
     u32x4 q[DS];
 #pragma unroll
     for (int rt = 0; rt < NR; ++rt) {
-        const int r = r0 + rt * 16 + n, i = r / p.group, h = head * p.group + r - i * p.group;
+        const int r = r0 + rt * 16 + n, i = divide(r, p.by_group), h = head * p.group + r - i * p.group;
         mine[rt] = i < tokens;
         high[rt] = mine[rt] ? place0 + i : -1;
         low[rt] = p.window > 0 ? place0 + i - p.window : -0x7fffffff - 1;
@@ -97,7 +104,7 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
             }
         }
     }
-    const int i_first = r0 / p.group, i_last = min(tokens - 1, (r0 + NR * 16 - 1) / p.group);
+    const int i_first = divide(r0, p.by_group), i_last = min(tokens - 1, divide(r0 + NR * 16 - 1, p.by_group));
     const bool whole = p.D == DP;
     const int last_tile = min(NR - 1, (tokens * p.group - r0 - 1) / 16);      // of rows that there are
 
@@ -324,10 +331,11 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
         leaf = next;
     }
 
+    const long long moved = block_row(p, b, s.start) - (long long)s.start * p.q_heads;
 #pragma unroll
     for (int rt = 0; rt < NR; ++rt) {
         if (!mine[rt]) continue;
-        const long long at = row[rt] * p.slots + u;
+        const long long at = (row[rt] + moved) * p.units + u;
         if (p.units > 1 && wave == 0 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
 #pragma unroll
         for (int d = 0; d < DT; ++d) {

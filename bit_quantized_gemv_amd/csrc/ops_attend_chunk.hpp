@@ -40,24 +40,42 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
 
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    const int b = blockIdx.y;
-    const Seq s = sequence(p.cache, b);
-    if (s.count <= kBlockTokens) return;
+    // The sequence whose rows these are: the launch has about as many workgroups as all chunks have
+    // tiles of rows, one after the other.  255 single tokens beside a chunk of 2048, 1000 places each, us:
+    // 1048 when every sequence had as many workgroups as the longest.
+    int left = divide(blockIdx.x, p.by_heads), b = -1, rb = 0;
+    const int head = blockIdx.x - left * p.heads;
+    Seq s;
+    for (int i = 0; i < p.cache.n_seqs && b < 0; i += 64) {
+        Seq of = {0, 0, 0};
+        if (i + lane < p.cache.n_seqs) of = sequence(p.cache, i + lane);
+        const int count = min(of.count, p.max_new), blocks = count > kBlockTokens ? (count * p.group + C::kRows - 1) / C::kRows : 0;
+        for (uint64_t chunks = __ballot(blocks > 0); chunks; chunks &= chunks - 1) {
+            const int at = __builtin_ctzll(chunks), n = __builtin_amdgcn_readlane(blocks, at);
+            if (left < n) {
+                b = i + at;
+                rb = n - 1 - left;      // those that see most first
+                s.start = __builtin_amdgcn_readlane(of.start, at);
+                s.count = __builtin_amdgcn_readlane(of.count, at);
+                s.length = __builtin_amdgcn_readlane(of.length, at);
+                break;
+            }
+            left -= n;
+        }
+    }
+    if (b < 0) return;
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
-    const int rows = tokens * p.group, blocks = (rows + C::kRows - 1) / C::kRows;
-    // the rows that see most first
-    const int rb = blocks - 1 - (int)blockIdx.x / p.heads, head = blockIdx.x % p.heads;
-    if (rb < 0) return;
-    const int r0 = rb * C::kRows, i_first = r0 / p.group, i_last = min(tokens - 1, (r0 + C::kRows - 1) / p.group);
+    const int rows = tokens * p.group;
+    const int r0 = rb * C::kRows, i_first = divide(r0, p.by_group), i_last = min(tokens - 1, divide(r0 + C::kRows - 1, p.by_group));
 
     // the tiles of keys that the workgroup's rows see, and its share of them
     const Visible vis = visible(place0 + i_first, i_last - i_first + 1, p.window, p.sinks, NK);
-    const int t_from = (int)((long long)vis.units * blockIdx.z / gridDim.z), t_to = (int)((long long)vis.units * (blockIdx.z + 1) / gridDim.z);
+    const int t_from = (int)((long long)vis.units * blockIdx.y / p.splits), t_to = (int)((long long)vis.units * (blockIdx.y + 1) / p.splits);
 
     // queries, negative scales turned into them
     const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0;
     const float scale = __builtin_fabsf(p.scale);
-    const int w_first = (r0 + wave * 32) / p.group, w_last = min(tokens - 1, (r0 + wave * 32 + 31) / p.group);
+    const int w_first = divide(r0 + wave * 32, p.by_group), w_last = min(tokens - 1, divide(r0 + wave * 32 + 31, p.by_group));
     const bool idle = r0 + wave * 32 >= rows;
     u32x4 q[2][DS];
     int high[2], low[2];
@@ -65,7 +83,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
     bool mine[2];
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
-        const int r = r0 + wave * 32 + rt * 16 + n, i = r / p.group, h = head * p.group + r - i * p.group, t = s.start + i;
+        const int r = r0 + wave * 32 + rt * 16 + n, i = divide(r, p.by_group), h = head * p.group + r - i * p.group, t = s.start + i;
         mine[rt] = r < rows;
         high[rt] = mine[rt] ? place0 + i : -1;
         low[rt] = p.window > 0 ? place0 + i - p.window : -0x7fffffff - 1;
@@ -313,14 +331,14 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
         if (!mine[rt]) continue;
-        const long long at = row[rt] * p.slots + blockIdx.z;
-        if (gridDim.z > 1 && g == 0) p.stat[at] = f32x2{m[rt], l[rt].x};
+        const long long at = row[rt] * p.splits + blockIdx.y;
+        if (p.splits > 1 && g == 0) p.chunk_stat[at] = f32x2{m[rt], l[rt].x};
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
             const int c = d * 16 + 4 * g;
             if (c >= p.D) continue;
-            if (gridDim.z == 1) put_result(p, row[rt], c, o[rt][d], l[rt].x);
-            else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
+            if (p.splits == 1) put_result(p, row[rt], c, o[rt][d], l[rt].x);
+            else *reinterpret_cast<f32x4*>(p.chunk_part + at * p.D + c) = o[rt][d];
         }
     }
 }

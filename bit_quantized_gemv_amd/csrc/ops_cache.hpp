@@ -10,13 +10,20 @@
 
 namespace ops {
 
+// x / n for x < 2^31, by one product
+struct Divisor {
+    uint32_t magic;
+    int shift;
+};
+
+__host__ __device__ __forceinline__ int divide(int x, Divisor d) { return (int)(((uint64_t)(uint32_t)x * d.magic) >> d.shift); }
+
 struct Cache {
     const char *k, *v;
     long long k_page, k_slot, k_head, v_page, v_slot, v_head;    // bytes
     const int32_t *pages, *starts, *lengths;
     long long pages_row;
-    uint32_t magic;             // j / page_size = j * magic >> shift, for j < 2^31
-    int shift;
+    Divisor by_page;            // the page size
     int n_pages, page_size, n_seqs, max_pages, max_places;
     int T;
 };
@@ -35,7 +42,7 @@ __device__ __forceinline__ Seq sequence(const Cache& c, int b)
     return s;
 }
 
-__device__ __forceinline__ int page_index(const Cache& c, int j) { return (int)(((uint64_t)(uint32_t)j * c.magic) >> c.shift); }
+__device__ __forceinline__ int page_index(const Cache& c, int j) { return divide(j, c.by_page); }
 
 // the page of place j < max_places of sequence b; -1 if it holds nothing
 __device__ __forceinline__ int page_of(const Cache& c, int b, int index)
@@ -133,6 +140,15 @@ inline int check_cache(const qmv_cache* c, int T, int q_heads, CacheSpans* spans
     return QMV_OK;
 }
 
+// n <= 2^l; m = floor(2^(31+l) / n) + 1 is above 2^(31+l) / n by at most 1, so x m / 2^(31+l) is
+// above x / n by less than 2^31 / 2^(31+l) <= 1 / n, which its floor does not see
+inline Divisor divisor(int n)
+{
+    int l = 0;
+    while ((1LL << l) < n) ++l;
+    return Divisor{(uint32_t)((1ULL << (31 + l)) / (unsigned)n + 1), 31 + l};
+}
+
 inline Cache device_cache(const qmv_cache* c, int T)
 {
     Cache d;
@@ -148,12 +164,7 @@ inline Cache device_cache(const qmv_cache* c, int T)
     d.starts = c->starts;
     d.lengths = c->lengths;
     d.pages_row = c->pages_row;
-    // P <= 2^l; m = floor(2^(31+l) / P) + 1 is above 2^(31+l) / P by at most 1, so j m / 2^(31+l) is
-    // above j / P by less than 2^31 / 2^(31+l) <= 1 / P, which its floor does not see
-    int l = 0;
-    while ((1 << l) < c->page_size) ++l;
-    d.shift = 31 + l;
-    d.magic = (uint32_t)((1ULL << d.shift) / (unsigned)c->page_size + 1);
+    d.by_page = divisor(c->page_size);
     d.n_pages = c->n_pages;
     d.page_size = c->page_size;
     d.n_seqs = c->n_seqs;
