@@ -12,6 +12,7 @@ namespace ops {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kMostGroups = 16384;         // of blocks, before they take several units each
 constexpr int kUnits = 256;                // compute units
 
 constexpr int kLanes = 16;                 // of a row's 64 columns
@@ -165,6 +166,7 @@ struct Plan {
     int bound, leaf;
     int row_tiles, row_blocks, per_unit;          // blocks: a workgroup's tiles of rows, and a unit's leaves
     long long units;                              // of a sequence, at most
+    long long share;                              // and those that a workgroup takes
     long long chunk_tiles;                        // chunks: tiles of rows of all of them, at most
     int splits;                                   // and the shares of their keys
     const void *block, *chunk;
@@ -224,9 +226,13 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
         while (p.row_tiles > 1 && p.units * lists * blocks(p.row_tiles) < (p.row_tiles == 4 ? 2 : 1) * kUnits) p.row_tiles /= 2;
     }
     p.row_blocks = blocks(p.row_tiles);
-    p.block = p.bound == 64    ? block_kernel_64(f16, f32_out, p.row_tiles, &p.block_lds)
-              : p.bound == 128 ? block_kernel_128(f16, f32_out, p.row_tiles, &p.block_lds)
-                               : block_kernel_256(f16, f32_out, p.row_tiles, &p.block_lds);
+    // A workgroup takes several units, one after the other, where there would be more than kMostGroups: most
+    // have nothing to do then, their bounds being wide.  256 single tokens of 1000 places, 8 heads of 128, us, with a
+    // bound of 131072: 292, 699 with a workgroup a unit; 203 with a bound of 1024.
+    p.share = p.window > 0 ? 1 : std::min(p.units, (p.units * lists * p.row_blocks + kMostGroups - 1) / kMostGroups);
+    p.block = p.bound == 64    ? block_kernel_64(f16, f32_out, p.share > 1, p.row_tiles, &p.block_lds)
+              : p.bound == 128 ? block_kernel_128(f16, f32_out, p.share > 1, p.row_tiles, &p.block_lds)
+                               : block_kernel_256(f16, f32_out, p.share > 1, p.row_tiles, &p.block_lds);
     // a chunk's kernel multiplies all the columns that it is made for
     const auto chunk = c->head_size <= 64    ? chunk_kernel_64
                        : c->head_size <= 96  ? chunk_kernel_96
@@ -314,7 +320,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     const Span outs[] = {{out, (size_t)T * q_heads * c->head_size * size_of(out_dt)}, {workspace, (size_t)need}};
     if (!disjoint(in, outs)) return QMV_E_ALIAS;
     // rows are counted, and a launch's threads, in 32 bits
-    const long long groups = (plan.units * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks;
+    const long long shares = (plan.units + plan.share - 1) / plan.share, groups = (shares * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks;
     const long long chunk_groups = plan.chunk_tiles * c->heads, join_groups = plan.join_turns * plan.columns * c->n_seqs;
     if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 31 || chunk_groups >= 1 << 23 || join_groups >= 1LL << 31) return QMV_E_CACHE;
     AttendParams p;
@@ -337,6 +343,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.max_new = plan.max_new;
     p.out_f32 = out_dt == QMV_DT_F32;
     p.units = (int)plan.units;
+    p.shares = (int)shares;
     p.splits = plan.splits;
     p.row_blocks = plan.row_blocks;
     p.rows_last = plan.max_new > kBlockTokens ? (int)(groups / 8 / plan.row_blocks) : 0;

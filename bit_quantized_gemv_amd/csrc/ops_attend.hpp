@@ -50,6 +50,7 @@ struct AttendParams {
     int q_heads, heads, group, D;
     int window, sinks, max_new, out_f32;
     int units, row_blocks, per_unit, splits;
+    int shares;                     // blocks: workgroups of a sequence's units; each takes every so many-th
     int rows_last;                  // blocks: workgroups of the first tiles of rows, on a die, after which those of the next come (0: side by side)
     int apart;                      // a block's tokens in part and stat: by sequence, so many each (0: as in q)
     float scale;                    // times log2(e)
@@ -255,11 +256,11 @@ __device__ __forceinline__ void put_result(const AttendParams& p, long long row,
     else *reinterpret_cast<bf16x4*>(p.out + (row * p.D + d) * 2) = __builtin_convertvector(y, bf16x4);
 }
 
-// The kernel of a head size (64, 128, 256), cache type, output type and tiles of query rows,
-// and its LDS.
-const void* block_kernel_64(bool f16, bool f32_out, int row_tiles, int* lds);
-const void* block_kernel_128(bool f16, bool f32_out, int row_tiles, int* lds);
-const void* block_kernel_256(bool f16, bool f32_out, int row_tiles, int* lds);
+// The kernel of a head size (64, 128, 256), cache type, output type, several units a workgroup and
+// tiles of query rows, and its LDS.
+const void* block_kernel_64(bool f16, bool f32_out, bool share, int row_tiles, int* lds);
+const void* block_kernel_128(bool f16, bool f32_out, bool share, int row_tiles, int* lds);
+const void* block_kernel_256(bool f16, bool f32_out, bool share, int row_tiles, int* lds);
 struct ChunkShape {
     int rows, threads;       // of a workgroup
     int at_once, lds;        // workgroups on a compute unit

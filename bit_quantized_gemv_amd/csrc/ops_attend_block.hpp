@@ -25,8 +25,10 @@ namespace ops {
 template <int DP, int NP, int NR>
 constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + 16 + (NR > 1 ? NR * DP * 32 : 0);
 
-template <int DP, class X, int NP, int NR>
-__global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 ? 3 : 2) void block_kernel(AttendParams p)
+// SHARE: a workgroup may take several units; what that holds in registers leaves room for two workgroups on a
+// compute unit where there are three otherwise (64 ragged sequences of up to 8192 places: 235 us, 228 without).
+template <int DP, class X, int NP, int NR, bool SHARE>
+__global__ __launch_bounds__(256, !SHARE && (NR == 1 && DP < 256 || NR == 2 && DP == 64) ? 3 : 2) void block_kernel(AttendParams p)
 {
     constexpr int KT = leaf_keys(DP);      // keys of a leaf
     constexpr int WK = KT / 4;             // of which a wave scores
@@ -43,7 +45,7 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
     char* const queries = reinterpret_cast<char*>(odds + 4);
 
     const Cache& c = p.cache;
-    together(c.pages, c.pages_row, c.starts, c.lengths, c.by_page.magic, c.by_page.shift, c.max_pages, c.T, c.n_seqs, p.per_unit, p.window, p.heads, p.row_blocks, p.units,
+    together(c.pages, c.pages_row, c.starts, c.lengths, c.by_page.magic, c.by_page.shift, c.max_pages, c.T, c.n_seqs, p.per_unit, p.window, p.heads, p.row_blocks, p.shares,
              p.rows_last, p.by_rows.magic, p.by_rows.shift, p.by_heads.magic, p.by_heads.shift, p.by_seqs.magic, p.by_seqs.shift);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
@@ -58,7 +60,7 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
     const int rows_turn = divide(turn, p.by_rows), rows_rest = turn - rows_turn * (p.rows_last > 0 ? p.rows_last : p.row_blocks);
     const int rb = p.rows_last > 0 ? rows_turn : rows_rest, over = p.rows_last > 0 ? rows_rest : rows_turn;
     const int eight = divide(over, p.by_heads), head = over - eight * p.heads, unit = eight * 8 + (block & 7), u = divide(unit, p.by_seqs);
-    if (u >= p.units || rb >= p.row_blocks) return;
+    if (u >= p.shares || rb >= p.row_blocks) return;
     const int shifted = unit - u * c.n_seqs + (c.n_seqs & 1 ? 0 : u - divide(u, p.by_seqs) * c.n_seqs), b = shifted < c.n_seqs ? shifted : shifted - c.n_seqs;
     // pages of the lane's keys of a leaf, key n of every tile
     const int32_t* const table = p.cache.pages + b * p.cache.pages_row;
@@ -110,15 +112,36 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
 
     f32x4 o[NR][DT];
     float m[NR], l[NR];
+    auto begin = [&] {
 #pragma unroll
-    for (int rt = 0; rt < NR; ++rt) {
-        m[rt] = kGone;
-        l[rt] = 0.0f;
+        for (int rt = 0; rt < NR; ++rt) {
+            m[rt] = kGone;
+            l[rt] = 0.0f;
 #pragma unroll
-        for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0, 0, 0, 0};
-    }
+            for (int d = 0; d < DT; ++d) o[rt][d] = f32x4{0, 0, 0, 0};
+        }
+    };
+    // what the rows have found in a unit
+    auto finish = [&](int unit) {
+        const long long moved = block_row(p, b, s.start) - (long long)s.start * p.q_heads;
+#pragma unroll
+        for (int rt = 0; rt < NR; ++rt) {
+            if (!mine[rt]) continue;
+            const long long at = (row[rt] + moved) * p.units + unit;
+            if (p.units > 1 && wave == 0 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
+#pragma unroll
+            for (int d = 0; d < DT; ++d) {
+                const int c = (wave * DT + d) * 16 + 4 * g;
+                if (c >= p.D) continue;
+                if (p.units == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
+                else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
+            }
+        }
+    };
+    begin();
 
-    const int from = u < vis.units ? vis.unit(u) * U : 0, to = u < vis.units ? min(from + U, vis.high + 1) : 0;
+    // several units only without a window, whose units are one after the other from place 0 on
+    const int from = u < vis.units ? vis.unit(u) * U : 0, to = u < vis.units ? SHARE ? vis.high + 1 : min(from + U, vis.high + 1) : 0;
     auto next_leaf = [&](int at) {
         while (at < to && !vis.meets(at, at + KT)) at += KT;
         return at < to ? at : -1;
@@ -160,7 +183,7 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
             }
     };
 
-    int leaf = next_leaf(from);
+    int leaf = next_leaf(from), now = u;
     if (leaf >= 0) {
         if (leaf != early) ask_pages(leaf);
         addresses(leaf, valid);
@@ -175,7 +198,8 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
         lds_only_barrier();
     }
     while (leaf >= 0) {
-        const int next = next_leaf(leaf + KT);
+        const bool last = SHARE && (leaf + KT) % U == 0;      // of its unit
+        const int next = next_leaf(leaf + KT + (last ? (p.shares - 1) * U : 0));
         if (next >= 0) ask_pages(next);
         uint32_t ok[TILES];
 #pragma unroll
@@ -328,41 +352,39 @@ __global__ __launch_bounds__(256, NR == 1 && DP < 256 ? 3 : NR == 2 && DP == 64 
 #pragma unroll
             for (int d = 0; d < DT; ++d) o[rt][d] = joined(o[rt][d], a[d], by);
         }
+        if (last && next >= 0) {
+            finish(now);
+            begin();
+            now = next / U;
+        }
         leaf = next;
     }
 
-    const long long moved = block_row(p, b, s.start) - (long long)s.start * p.q_heads;
-#pragma unroll
-    for (int rt = 0; rt < NR; ++rt) {
-        if (!mine[rt]) continue;
-        const long long at = (row[rt] + moved) * p.units + u;
-        if (p.units > 1 && wave == 0 && g == 0) p.stat[at] = f32x2{m[rt], l[rt]};
-#pragma unroll
-        for (int d = 0; d < DT; ++d) {
-            const int c = (wave * DT + d) * 16 + 4 * g;
-            if (c >= p.D) continue;
-            if (p.units == 1) put_result(p, row[rt], c, o[rt][d], l[rt]);
-            else *reinterpret_cast<f32x4*>(p.part + at * p.D + c) = o[rt][d];
-        }
-    }
+    finish(now);
 }
 
 // the kernels of a head size
-template <int DP, class X, int NP>
+template <int DP, class X, int NP, bool SHARE>
 const void* block_kernel_rows(int row_tiles, int* lds)
 {
     *lds = row_tiles == 1 ? block_lds<DP, NP, 1> : row_tiles == 2 ? block_lds<DP, NP, 2> : block_lds<DP, NP, 4>;
-    return row_tiles == 1   ? (const void*)&block_kernel<DP, X, NP, 1>
-           : row_tiles == 2 ? (const void*)&block_kernel<DP, X, NP, 2>
-                            : (const void*)&block_kernel<DP, X, NP, 4>;
+    return row_tiles == 1   ? (const void*)&block_kernel<DP, X, NP, 1, SHARE>
+           : row_tiles == 2 ? (const void*)&block_kernel<DP, X, NP, 2, SHARE>
+                            : (const void*)&block_kernel<DP, X, NP, 4, SHARE>;
+}
+
+template <int DP, class X, int NP>
+const void* block_kernel_shares(bool share, int row_tiles, int* lds)
+{
+    return share ? block_kernel_rows<DP, X, NP, true>(row_tiles, lds) : block_kernel_rows<DP, X, NP, false>(row_tiles, lds);
 }
 
 // a weight in one piece for bf16 outputs; for fp32 ones in as many as hold 22 bits of it or more
 template <int DP>
-const void* block_kernel_types(bool f16, bool f32_out, int row_tiles, int* lds)
+const void* block_kernel_types(bool f16, bool f32_out, bool share, int row_tiles, int* lds)
 {
-    if (f16) return f32_out ? block_kernel_rows<DP, _Float16, 2>(row_tiles, lds) : block_kernel_rows<DP, _Float16, 1>(row_tiles, lds);
-    return f32_out ? block_kernel_rows<DP, __bf16, 3>(row_tiles, lds) : block_kernel_rows<DP, __bf16, 1>(row_tiles, lds);
+    if (f16) return f32_out ? block_kernel_shares<DP, _Float16, 2>(share, row_tiles, lds) : block_kernel_shares<DP, _Float16, 1>(share, row_tiles, lds);
+    return f32_out ? block_kernel_shares<DP, __bf16, 3>(share, row_tiles, lds) : block_kernel_shares<DP, __bf16, 1>(share, row_tiles, lds);
 }
 
 }  // namespace ops

@@ -3,6 +3,6 @@
 
 namespace ops {
 
-const void* block_kernel_256(bool f16, bool f32_out, int row_tiles, int* lds) { return block_kernel_types<256>(f16, f32_out, row_tiles, lds); }
+const void* block_kernel_256(bool f16, bool f32_out, bool share, int row_tiles, int* lds) { return block_kernel_types<256>(f16, f32_out, share, row_tiles, lds); }
 
 }  // namespace ops

@@ -213,6 +213,70 @@ def test_row_tiles(D, Hq, Hkv, n, window):
     assert torch.equal(again[:n], alone)
 
 
+def of(c, qs, order, pages=None):
+    """The call of a batch's sequences in another order, some of them more than once: q, then the rest."""
+    k, v, table, _, lens = c.on()
+    starts = c.starts.tolist()
+    at = torch.tensor(order, device=DEV)
+    new = torch.cat([qs[starts[b]:starts[b + 1]] for b in order]).to(DEV)
+    begin = torch.tensor([0] + [c.new[b] for b in order]).cumsum(0).int().to(DEV)
+    return new, k, v, (table if pages is None else pages)[at], begin, lens[at]
+
+
+@pytest.mark.parametrize("D,Hq,Hkv,n,out", [(128, 8, 8, 1, "bf16"), (64, 12, 4, 13, "f32"), (256, 6, 2, 5, "bf16"), (128, 24, 2, 7, "f32"), (64, 8, 4, 3, "bf16")])
+def test_wide_bounds(D, Hq, Hkv, n, out):
+    """Bounds far above the lengths: workgroups that take many units each, most of them without work; the same bits."""
+    P, lengths = 64, [9000, n, 1025, 33000, 1024, 6200, 2 * 8192]
+    c = Batch([n] * 7, lengths, Hkv, D, P, seed=D + n)
+    qs = queries(c, Hq)
+    order = [i % 7 for i in range(70)]
+    new, k, v, pages, begin, lens = of(c, qs, order)
+    kw = dict(max_new=n, out_dtype=TORCH[out])
+    tight = torch.cat([q.attend(qs[n * b:n * b + n].to(DEV), k, v, pages[b:b + 1], begin[:2], lens[b:b + 1], max_length=lengths[b], **kw) for b in range(7)])
+    wide = torch.full((70, (1 << 22) // P), -1, dtype=torch.int32, device=DEV)
+    wide[:, :pages.shape[1]] = pages
+    got = q.attend(new, k, v, wide, begin, lens, **kw)
+    assert torch.equal(got.reshape(10, 7 * n, Hq, D), tight.expand(10, 7 * n, Hq, D))
+    ref = Batch([n], [lengths[5]], Hkv, D, P)
+    ref.k, ref.v, ref.pages = c.k, c.v, c.pages[5:6]
+    check_attend(tight[5 * n:6 * n], *attend64(qs[5 * n:6 * n], ref), "bf16", out)
+
+
+@pytest.mark.parametrize("window", [0, 200])
+def test_chunks_among_many(window):
+    """Chunks here and there among hundreds of sequences, blocks of one and of many tokens beside them."""
+    c = Batch([1, 16, 40, 0, 17, 3], [1300, 2100, 40, 77, 1500, 3], 2, 64, 16, seed=window)
+    qs = queries(c, 8)
+    kw = dict(window=window, sinks=3 if window else 0)
+    want, reach = attend64(qs, c, **kw)
+    order = [0, 3, 0, 5] * 50 + [2, 1, 0, 4] + [0, 5, 3] * 40 + [1, 2, 2, 4, 0]
+    new, k, v, pages, begin, lens = of(c, qs, order)
+    got = q.attend(new, k, v, pages, begin, lens, **kw)
+    alone = {}
+    for i, b in enumerate(order):
+        a, z, s = int(begin[i]), int(begin[i + 1]), c.starts.tolist()
+        if c.new[b] > 16:
+            check_attend(got[a:z], want[s[b]:s[b + 1]], reach[s[b]:s[b + 1]], "bf16", "bf16", (i, b))
+        elif c.new[b]:
+            if b not in alone:
+                alone[b] = q.attend(new[a:z], k, v, pages[i:i + 1], begin[i:i + 2] - a, lens[i:i + 1], **kw)
+                check_attend(alone[b], want[s[b]:s[b + 1]], reach[s[b]:s[b + 1]], "bf16", "bf16", b)
+            assert torch.equal(got[a:z], alone[b]), (i, b)
+
+
+@pytest.mark.parametrize("bound", [1, 5, 16, 17, 30])
+def test_more_new_than_bound(bound):
+    """The first max_new tokens of a sequence, at their places; the rows of the others as they were."""
+    c = Batch([40, 3], [700, 500], 2, 128, 16)
+    qs = queries(c, 4)
+    want, reach = attend64(qs, c)
+    out = torch.full((43, 4, 128), 7.0, dtype=torch.bfloat16, device=DEV)
+    run(c, qs, max_new=bound, out=out)
+    for a, n in ((0, min(bound, 40)), (40, min(bound, 3))):
+        check_attend(out[a:a + n], want[a:a + n], reach[a:a + n], "bf16", "bf16")
+    assert (out[min(bound, 40):40] == 7).all() and (out[40 + min(bound, 3):] == 7).all()
+
+
 @pytest.mark.parametrize("H", [1, 2])
 def test_very_long(H):
     """More leaves and supers than a join takes in one round."""
