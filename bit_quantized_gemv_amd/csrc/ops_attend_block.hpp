@@ -10,6 +10,14 @@
 // quarter of the keys, the waves agree on the rows' largest scores, put their weights into
 // LDS, and each sums its quarter of the columns over all keys of the leaf.
 //
+// Measured: one token of 32 query heads on 8 of 128 over 131072 places (537 MB) 110 us and 6.5 of the
+// join, 4.9 TB/s, which is a copy's rate; 64 sequences of up to 8192 places (1.07 GB) 222 and 6,
+// 4.8 TB/s; 13 tokens of 16 heads on 8 of 256 over 16384 places (134 MB) 35 and 5.  Short calls are a
+// chain of dependent loads: one token over 411 places 6.4 and 4.2.
+//
+// Why leaves of 32 KB: of 64 KB the registers hold no leaf in flight beside the one at work (13 tokens over
+// 16384 places 86 us for 46, 64 sequences 346 for 257, both before later steps).
+//
 // Order of sums.  Leaves begin at multiples of their length, a leaf's sums begin at zero, and
 // are joined in order to those of the super that the leaf is in (kSuper leaves), and supers
 // in order to a row's; whether by this kernel or the next one.  Leaves that a row sees nothing

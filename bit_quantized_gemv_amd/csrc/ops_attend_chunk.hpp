@@ -9,11 +9,18 @@
 // is followed only when it has grown by 2^8, which weights and sums have room for, since moving it
 // costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
 // keys of a tile of rows, and a second launch joins them.
+//
+// Measured, 2048 tokens over 16384 places, 32 heads on 8 of 128: 570 us in turn with others' calls, 903 TFLOP/s
+// (677 us back to back, the clock falling), where a library's product of 8192 x 8192 x 8192 reaches 1239.  The
+// matrix instructions are busy 44% of the time, the vector instructions half of it, reads of LDS (32 KB a
+// wave and tile) 41%; two waves on a SIMD overlap them in part.  Over 8192 places, back to back, heads of 64:
+// 580 TFLOP/s, 96: 751, 192: 731, 256: 687; fp32 outputs (three pieces of each weight) 509 at 128.
 #pragma once
 #include "ops_attend.hpp"
 
 namespace ops {
 
+// Tiles of 64 keys of up to 128 values, of 32 above: scores and the next tile fill registers and LDS.
 // As many waves as the registers hold, in workgroups of four, or of eight where the outputs and
 // queries of two waves fill a unit's.
 template <int DP>
@@ -26,6 +33,8 @@ struct Chunk {
     static constexpr int kLds = 4 * kTileBytes + 2 * 48;           // keys and values, twice, and what is known of them
 };
 
+// 0 would follow every maximum, which makes the largest weights exact ones: bf16 outputs are off by 1.8e-3 of their norm
+// then instead of 2.2e-3 (their own rounding alone: 1.7e-3), and the 2048 tokens above take 602 us for 571.
 constexpr float kRoom = 8.0f;
 
 template <int DP, class X, int NP>

@@ -9,6 +9,9 @@
 // sines, cosines and weights are the same for all heads.  A lane computes one angle, for the whole wave.  The sum of squares is taken over the
 // group's lanes, in fp32.  There is no barrier.
 //
+// Bound by memory where tokens are many: 8192 of 48 heads of 128 (201 MB read and written) 43 us, 4.7 TB/s, where a
+// copy reaches 4.9 (8 values a lane instead of 16: 52 to 57); by latency where they are few: one token 4.8.
+//
 // Angles: positions * freqs in fp64, as turns; the fraction of a turn that is left has lost
 // nothing that fp32 holds, also at positions of 2^31.
 #include <hip/hip_runtime.h>
@@ -295,10 +298,14 @@ int run(RotateParams& p, const qmv_rotation* r, int T, int x_dt, int y_dt, bool 
     const int lanes = p.D / (sixteen ? 16 : 8);
     p.lanes_log2 = 0;
     while (1 << p.lanes_log2 < lanes) ++p.lanes_log2;
-    // Few tokens: as many waves as there are heads to go round; then some rounds a wave, so that
-    // angles and places serve several heads; then all heads, so that a token's memory is one wave's.
+    // A wave takes one round of heads, or as many more as leave 4096 waves (four for every SIMD): angles and
+    // places then serve several heads, and a token's memory is one wave's.  48 heads of 128, us, by rounds of 8:
+    // 256 tokens 5.5 with one, 6.4 with two, 10.1 with all; 1024: 12.5, 10.0, 12.8; 2048: 19.1, 16.4, 14.0 with
+    // three, 15.3; 8192: 71, 57, 50, 43.
     const int all = p.q_heads + (append ? 2 : 1) * p.k_heads, groups = 64 >> p.lanes_log2;
-    p.heads = T >= 4096 ? all : std::min(all, T >= 256 ? std::max(groups, 16) : groups);
+    p.heads = groups;
+    while (p.heads < all && (long long)T * ((all + p.heads - 1) / p.heads) > 4096) p.heads += groups;
+    p.heads = std::min(all, p.heads);
     p.parts = (all + p.heads - 1) / p.heads;
     const bool xf = x_dt == QMV_DT_F32, yh = y_dt == QMV_DT_F16;
     const void* f = append ? kernel_of<true>(xf, yh, sixteen) : kernel_of<false>(xf, yh, sixteen);
