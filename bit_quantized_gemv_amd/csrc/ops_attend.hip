@@ -13,6 +13,7 @@ namespace {
 
 constexpr int kThreads = 256;
 constexpr int kMostGroups = 16384;         // of blocks, before they take several units each
+constexpr long long kManyGroups = 4096;    // beside chunks, of which most have nothing to do
 constexpr int kUnits = 256;                // compute units
 
 constexpr int kLanes = 16;                 // of a row's 64 columns
@@ -34,9 +35,8 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf
     const Cache& c = p.cache;
     together(p.part, p.stat, p.chunk_part, p.chunk_stat, p.out, c.starts, c.lengths, c.n_seqs, c.max_places, c.T, p.units, p.per_unit, p.splits, p.apart, p.q_heads, p.D,
              p.window, p.sinks, p.max_new, p.out_f32, p.by_seqs.magic, p.by_seqs.shift, leaf, block_chains, chunk_chains, columns, by_columns.magic, by_columns.shift, turns);
-    // the sequences side by side, so that those without work do not leave compute units to themselves
-    const int group_of = blockIdx.y * gridDim.x + blockIdx.x, over = divide(group_of, by_columns), column = group_of - over * columns;
-    const int turn = divide(over, p.by_seqs), b = over - turn * p.cache.n_seqs;
+    const Turn at_turn = turn_of(blockIdx.y * gridDim.x + blockIdx.x, p);
+    const int turn = divide(at_turn.turn, by_columns), column = at_turn.turn - turn * columns, b = at_turn.b;
     if (turn >= turns) return;
     const Seq s = sequence(p.cache, b);
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
@@ -227,6 +227,10 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     if (p.per_unit > 1) {
         while (p.row_tiles > 1 && p.units * lists * blocks(p.row_tiles) < (p.row_tiles == 4 ? 2 : 1) * kUnits) p.row_tiles /= 2;
     }
+    // Beside chunks, a workgroup takes further tiles of rows where those would be many workgroups, most without work.
+    // 127 sequences of 5 tokens of 1000 places beside a chunk of 512, us: 203 for 304; 255 single tokens: 303 for 311,
+    // or, with a bound of eight times their places, 324 for 311.
+    while (p.max_new > kBlockTokens && p.row_tiles < 4 && p.units * lists * (blocks(p.row_tiles) - 1) > kManyGroups) p.row_tiles *= 2;
     p.row_blocks = blocks(p.row_tiles);
     // A workgroup takes several units, one after the other, where there would be more than kMostGroups: most
     // have nothing to do then, their bounds being wide.  256 single tokens of 1000 places, 8 heads of 128, us, with a
@@ -259,12 +263,13 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     p.block_chains = chains_of(p.units);
     p.chunk_chains = chains_of(p.splits);
     auto joins = [&](long long rows, long long parts, int chains) { return parts > 1 ? (rows + (kChains >> chains) - 1) / (kChains >> chains) : 0; };
-    // A workgroup for every 16 rows, or, beside chunks, where most sequences have one token's, as many as run at
-    // once, and one token's at least: 255 single tokens beside a chunk of 2048, 32 heads, 11 us for 31.
-    const long long block_turns = joins((long long)tokens * q_heads, p.units, p.block_chains);
-    p.join_turns = p.max_new <= kBlockTokens ? block_turns : std::min(block_turns, std::max(joins(q_heads, p.units, p.block_chains), 4096LL / (p.columns * c->n_seqs)));
-    p.join_more = p.join_turns < block_turns;
-    p.join_turns = std::max(p.join_turns, joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains));
+    // A workgroup for every 16 rows, or, where there are chunks and most sequences may have one token, kManyGroups
+    // where those are fewer than half, and one token's at least: 255 single tokens beside a chunk of 2048, 32 heads, 11 us for 31; 15 beside one of
+    // 512 tokens in two shares, 26 for 110.
+    p.join_turns = std::max(joins((long long)tokens * q_heads, p.units, p.block_chains), joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains));
+    const long long most = std::max(joins(q_heads, p.units, p.block_chains), kManyGroups / (p.columns * c->n_seqs));
+    p.join_more = p.max_new > kBlockTokens && p.join_turns > 2 * most;
+    if (p.join_more) p.join_turns = most;
     p.apart = (long long)c->n_seqs * tokens < T ? tokens : 0;
     const long long parts = p.units > 1 ? (long long)(p.apart > 0 ? c->n_seqs * tokens : T) * q_heads * p.units : 0;
     const long long chunk_parts = p.splits > 1 ? (long long)T * q_heads * p.splits : 0;

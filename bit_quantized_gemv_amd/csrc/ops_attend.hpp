@@ -242,6 +242,18 @@ __device__ __forceinline__ f32x4 joined(f32x4 o, f32x4 o2, Factors f)
                  __builtin_fmaf(o2.w, f.b, o.w * f.a)};
 }
 
+// Work of the sequences over the compute dies, to which workgroups go in turn: the first turn of all sequences,
+// then the second, and each sequence's turns over all eight dies, since its next one is an odd number of workgroups
+// on (n_seqs, or one beside it).
+struct Turn {
+    int turn, b;
+};
+__device__ __forceinline__ Turn turn_of(int i, const AttendParams& p)
+{
+    const int n = p.cache.n_seqs, turn = divide(i, p.by_seqs), b = i - turn * n + (n & 1 ? 0 : turn - divide(turn, p.by_seqs) * n);
+    return Turn{turn, b < n ? b : b - n};
+}
+
 // The first row of a block's tokens in part and stat.
 __device__ __forceinline__ long long block_row(const AttendParams& p, int b, int start)
 {

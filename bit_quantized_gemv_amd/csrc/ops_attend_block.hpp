@@ -57,19 +57,18 @@ __global__ __launch_bounds__(256, !SHARE && (NR == 1 && DP < 256 || NR == 2 && D
              p.rows_last, p.by_rows.magic, p.by_rows.shift, p.by_heads.magic, p.by_heads.shift, p.by_seqs.magic, p.by_seqs.shift);
     const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n = lane & 15, g = lane >> 4;
-    // The first unit of all sequences, then the second, eight side by side on the eight compute dies, and
-    // each sequence's over all dies: its n_seqs-th next, or the one beside, is an odd number of dies on.
-    // On a die, all of a unit's heads and row blocks one after the other, since heads lie next to
-    // each other in memory in most caches.  Beside chunks, where most sequences have one tile of rows, the
-    // others come last: workgroups without work between the others would leave compute units to themselves.
-    // 255 single tokens of 1000 places, 8 heads of 128, with as many rows as 16 tokens have, us:
-    // 205, 488 side by side.
+    // Eight units side by side on the eight compute dies; on a die, all of a unit's heads and row blocks one
+    // after the other, since heads lie next to each other in memory in most caches.  Beside chunks, where most
+    // sequences have one tile of rows, the others come last: workgroups without work between the others
+    // would leave compute units to themselves.  255 single tokens of 1000 places, 8 heads of 128, with as many
+    // rows as 16 tokens have, us: 205, 488 side by side.
     const int block = blockIdx.y * gridDim.x + blockIdx.x, turn = block >> 3;
     const int rows_turn = divide(turn, p.by_rows), rows_rest = turn - rows_turn * (p.rows_last > 0 ? p.rows_last : p.row_blocks);
     const int rb = p.rows_last > 0 ? rows_turn : rows_rest, over = p.rows_last > 0 ? rows_rest : rows_turn;
-    const int eight = divide(over, p.by_heads), head = over - eight * p.heads, unit = eight * 8 + (block & 7), u = divide(unit, p.by_seqs);
+    const int eight = divide(over, p.by_heads), head = over - eight * p.heads;
+    const Turn at_turn = turn_of(eight * 8 + (block & 7), p);
+    const int u = at_turn.turn, b = at_turn.b;
     if (u >= p.shares || rb >= p.row_blocks) return;
-    const int shifted = unit - u * c.n_seqs + (c.n_seqs & 1 ? 0 : u - divide(u, p.by_seqs) * c.n_seqs), b = shifted < c.n_seqs ? shifted : shifted - c.n_seqs;
     // pages of the lane's keys of a leaf, key n of every tile
     const int32_t* const table = p.cache.pages + b * p.cache.pages_row;
     int entry[TILES];

@@ -51,14 +51,14 @@ __device__ __forceinline__ int page_of(const Cache& c, int b, int index)
     return (uint32_t)p < (uint32_t)c.n_pages ? p : -1;
 }
 
-// The sequence of token t, told by a whole wave: how many starts are at or below it.
-// -1 if it is in none.
+// The sequence of token t, told by a whole wave: how many starts are at or below it, by steps of
+// 4096, 64 and 1 of ascending starts.  -1 if it is in none.
 __device__ __forceinline__ int sequence_of(const Cache& c, int t, int lane)
 {
     int b = 0;
-    for (int i = 0; i < c.n_seqs; i += 64) {
-        const bool below = i + lane < c.n_seqs && c.starts[i + lane + 1] <= t;
-        b += __popcll(__ballot(below));
+    for (int step = c.n_seqs > 4096 ? 4096 : c.n_seqs > 64 ? 64 : 1; step > 0; step >>= 6) {
+        const int i = b + (lane + 1) * step;
+        b += step * __popcll(__ballot(i <= c.n_seqs && c.starts[i] <= t));
     }
     return b < c.n_seqs ? b : -1;
 }

@@ -242,11 +242,11 @@ def test_wide_bounds(D, Hq, Hkv, n, out):
     check_attend(tight[5 * n:6 * n], *attend64(qs[5 * n:6 * n], ref), "bf16", out)
 
 
-@pytest.mark.parametrize("window", [0, 200])
-def test_chunks_among_many(window):
+@pytest.mark.parametrize("window,H,G,D", [(0, 2, 4, 64), (200, 2, 4, 64), (0, 4, 6, 64), (300, 1, 16, 128), (0, 4, 5, 40)])
+def test_chunks_among_many(window, H, G, D):
     """Chunks here and there among hundreds of sequences, blocks of one and of many tokens beside them."""
-    c = Batch([1, 16, 40, 0, 17, 3], [1300, 2100, 40, 77, 1500, 3], 2, 64, 16, seed=window)
-    qs = queries(c, 8)
+    c = Batch([1, 16, 40, 0, 17, 3], [1300, 2100, 40, 77, 1500, 3], H, D, 16, seed=window)
+    qs = queries(c, H * G)
     kw = dict(window=window, sinks=3 if window else 0)
     want, reach = attend64(qs, c, **kw)
     order = [0, 3, 0, 5] * 50 + [2, 1, 0, 4] + [0, 5, 3] * 40 + [1, 2, 2, 4, 0]
@@ -262,6 +262,23 @@ def test_chunks_among_many(window):
                 alone[b] = q.attend(new[a:z], k, v, pages[i:i + 1], begin[i:i + 2] - a, lens[i:i + 1], **kw)
                 check_attend(alone[b], want[s[b]:s[b + 1]], reach[s[b]:s[b + 1]], "bf16", "bf16", b)
             assert torch.equal(got[a:z], alone[b]), (i, b)
+
+
+@pytest.mark.parametrize("B", [1, 16, 40, 41])
+@pytest.mark.parametrize("G,D", [(16, 64), (7, 200)])
+def test_shares_among_many(B, G, D):
+    """A chunk whose keys several workgroups share, first and last of sequences of single tokens."""
+    c = Batch([300, 1, 11, 130], [1500, 1100, 700, 2000], 1, D, 32, seed=B)
+    qs = queries(c, G)
+    want, reach = attend64(qs, c)
+    order = [0] + [1, 2, 1] * (B // 3) + [3]
+    new, k, v, pages, begin, lens = of(c, qs, order)
+    got = q.attend(new, k, v, pages, begin, lens, out_dtype=torch.float32)
+    s = c.starts.tolist()
+    for i, b in enumerate(order):
+        a, z = int(begin[i]), int(begin[i + 1])
+        check_attend(got[a:z], want[s[b]:s[b + 1]], reach[s[b]:s[b + 1]], "bf16", "f32", (i, b))
+    assert torch.equal(q.attend(new, k, v, pages, begin, lens, out_dtype=torch.float32), got)
 
 
 @pytest.mark.parametrize("bound", [1, 5, 16, 17, 30])

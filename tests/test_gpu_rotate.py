@@ -204,3 +204,24 @@ def test_no_tokens():
     assert a.shape == (0, 4, 64) and b.shape == (0, 2, 64)
     i = lambda *s: z(*s, dt=torch.int32)
     assert q.append(z(0, 4, 64), z(0, 2, 64), z(0, 2, 64), None, z(3, 4, 2, 64), z(3, 4, 2, 64), i(1, 2), i(2), i(1)).shape == (0, 4, 64)
+
+
+@pytest.mark.parametrize("B", [64, 65, 200, 4096, 4097, 9000])
+def test_many_sequences(B):
+    """Places of tokens among thousands of sequences, some of them empty, some of several tokens."""
+    new = torch.arange(B) % 3
+    new[5], new[-1] = 0, 2
+    starts = torch.cat([torch.zeros(1), new.cumsum(0)]).int()
+    T, H, D, P = int(starts[-1]), 1, 16, 4
+    lengths = (new + torch.arange(B) % 5).int()
+    pages = torch.arange(2 * B).int().reshape(B, 2)
+    g = gen(B)
+    k, v = (torch.randn(T, H, D, generator=g).bfloat16() for _ in range(2))
+    kc, vc = (torch.zeros(2 * B, P, H, D, dtype=torch.bfloat16, device=DEV) for _ in range(2))
+    q.append(k.to(DEV), k.to(DEV), v.to(DEV), None, kc, vc, pages.to(DEV), starts.to(DEV), lengths.to(DEV))
+    seq = torch.repeat_interleave(torch.arange(B), new)
+    place = torch.arange(T) - starts[seq] + (lengths - new)[seq]
+    for cache, x in ((kc, k), (vc, v)):
+        want = torch.zeros(2 * B * P, H, D, dtype=torch.bfloat16)
+        want[seq * 2 * P + place] = x
+        assert torch.equal(cache.cpu().reshape(-1, H, D), want)
