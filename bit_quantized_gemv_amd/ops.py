@@ -223,8 +223,10 @@ def attend(q, k_cache, v_cache, pages, starts, lengths, *, window: int = 0, sink
     window, j > p - window or j < sinks.  A token that sees nothing gets zeros; what a token
     does not see does not touch its output, NaN included.  scale: default 1 / sqrt(D).
     max_new, max_length: how many new tokens and places a sequence has at most, where the
-    program knows; defaults T and what the table holds (the bounds set the launch's size, and
-    what is above them is left out).  out, out_dtype: as `affine`, bf16 or fp32.
+    program knows; defaults T and what the table holds (the bounds set the sizes of launch and
+    scratch memory, and what is above them is left out).  out, out_dtype: as `affine`, bf16 or
+    fp32; rows of tokens that are in no sequence are left as they were.  A sequence's up to 16 new
+    tokens get the bits that a call for each of them gives.
     """
     f = (_py or _binding()).attend
     args = (q, k_cache, v_cache, pages, starts, lengths, window, sinks, scale, max_new, max_length, out, out_dtype)

@@ -125,10 +125,19 @@ int qmv_append(const qmv_rotation* r, const qmv_cache* c, const void* q, const v
  *   q    [T][q_heads][head_size] of the cache's dtype: at t * q_token + h * q_head + d,
  *        strides multiples of 8, 16-byte aligned
  *   out  [T][q_heads][head_size] of out_dt (fp32 or bf16), contiguous, 16-byte aligned
- *   max_new, max_length: bounds on the sequences' new tokens (what is above is left
- *        out) and lengths (longer ones count as that long)
- * Products are exact and sums, maxima and exponentials fp32; the weights are rounded to the
- * cache's dtype for the second product, or split into two such pieces if out is fp32.
+ *   max_new, max_length: bounds on the sequences' new tokens (those above are left out, and
+ *        their rows as they were) and lengths (longer ones count as that long).  Launch and
+ *        workspace go by the bounds: both grow with max_length where sequences are far shorter
+ *   workspace: qmv_attend_workspace bytes, 16-byte aligned; NULL where those are 0.  It holds
+ *        nothing between calls, and serves one call at a time
+ * Products are exact, and sums, maxima and exponentials fp32; the weights are rounded to the
+ * cache's dtype for the second product, or split into pieces that hold 22 bits or more of them if
+ * out is fp32.  A value of the cache that is infinite or NaN makes infinite or NaN (either) what
+ * the rows that see it sum up with it.
+ * Sequences of up to 16 new tokens: a token's bits depend on its place, the keys and values that it
+ * sees and the head size alone, so those of a block are those of a call for each token, whatever
+ * else is in the call.  Of longer ones the order of sums goes with the call's sizes.  A
+ * call repeated gives the same bits.  No atomics.
  */
 long long qmv_attend_workspace(const qmv_cache* c, int T, int q_heads, int max_new,
                                int max_length, int window, int sinks);
