@@ -221,11 +221,12 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     p.per_unit = units_of(p, tokens, p.leaf) * lists * blocks(p.row_tiles) * (2 + p.row_tiles) / 3 > 1200 ? kSuper : 1;
     p.units = units_of(p, tokens, (long long)p.leaf * p.per_unit);
     // Supers are few: four tiles of rows a workgroup only where that leaves two workgroups for every
-    // compute unit, two where it leaves one.  13 tokens, 64 query heads on 8 of 128, 8192 places, us: 47.6
+    // compute unit, two where it leaves three for four.  13 tokens, 64 query heads on 8 of 128, 8192 places, us: 47.6
     // with four, 33.2 with two, 39.8 with one; 32 sequences of half the query heads, 2048: 82, 99, 137;
-    // 16 on 8 of 256, 8192: 33.7 with two, 28.7 with one.
+    // 16 on 8 of 256, 8192: 33.7 with two, 28.7 with one,
+    // 12000: 35.7 and 43.9.
     if (p.per_unit > 1) {
-        while (p.row_tiles > 1 && p.units * lists * blocks(p.row_tiles) < (p.row_tiles == 4 ? 2 : 1) * kUnits) p.row_tiles /= 2;
+        while (p.row_tiles > 1 && p.units * lists * blocks(p.row_tiles) < (p.row_tiles == 4 ? 8 : 3) * kUnits / 4) p.row_tiles /= 2;
     }
     // Beside chunks, a workgroup takes further tiles of rows where those would be many workgroups, most without work.
     // 127 sequences of 5 tokens of 1000 places beside a chunk of 512, us: 203 for 304; 255 single tokens: 303 for 311,

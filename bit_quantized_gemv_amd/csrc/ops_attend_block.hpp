@@ -33,10 +33,12 @@ namespace ops {
 template <int DP, int NP, int NR>
 constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + 16 + (NR > 1 ? NR * DP * 32 : 0);
 
+// Three workgroups on a compute unit where one tile of rows leaves the registers for it; two tiles of heads of up to 64
+// would spill eight (64 sequences of 5 tokens over 1024 places 20.6 us with two workgroups, 23.3 with three).
 // SHARE: a workgroup may take several units; what that holds in registers leaves room for two workgroups on a
 // compute unit where there are three otherwise (64 ragged sequences of up to 8192 places: 235 us, 228 without).
 template <int DP, class X, int NP, int NR, bool SHARE>
-__global__ __launch_bounds__(256, !SHARE && (NR == 1 && DP < 256 || NR == 2 && DP == 64) ? 3 : 2) void block_kernel(AttendParams p)
+__global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void block_kernel(AttendParams p)
 {
     constexpr int KT = leaf_keys(DP);      // keys of a leaf
     constexpr int WK = KT / 4;             // of which a wave scores
