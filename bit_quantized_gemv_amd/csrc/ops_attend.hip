@@ -14,7 +14,6 @@ namespace {
 constexpr int kThreads = 256;
 constexpr int kMostGroups = 16384;         // of blocks, before they take several units each
 constexpr long long kManyGroups = 4096;    // beside chunks, of which most have nothing to do
-constexpr int kUnits = 256;                // compute units
 
 constexpr int kLanes = 16;                 // of a row's 64 columns
 constexpr int kChains = kThreads / kLanes;
@@ -213,7 +212,7 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     const int rows = tokens * group, usual = p.max_new > kBlockTokens ? group : rows;
     p.leaf = leaf_keys(p.bound);
     auto blocks = [&](int tiles) { return (rows + 16 * tiles - 1) / (16 * tiles); };
-    p.row_tiles = usual <= 16 ? 1 : usual <= 32 ? 2 : 4;
+    p.row_tiles = usual <= 16 ? 1 : usual <= 32 || p.max_new > kBlockTokens ? 2 : 4;
     // Leaf by leaf while those are about as many workgroups as run at once, a further tile of rows
     // counted as a third of one.  One token, 8 heads of 128, us: 16384 places 22.6 by leaves and 29.0 by
     // supers, 32768 42.9 and 39.0; 26 rows of 8 heads of 256, 8192 places: 34.6 and 28.7.
@@ -231,7 +230,7 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     // Beside chunks, a workgroup takes further tiles of rows where those would be many workgroups, most without work.
     // 127 sequences of 5 tokens of 1000 places beside a chunk of 512, us: 203 for 304; 255 single tokens: 303 for 311,
     // or, with a bound of eight times their places, 324 for 311.
-    while (p.max_new > kBlockTokens && p.row_tiles < 4 && p.units * lists * (blocks(p.row_tiles) - 1) > kManyGroups) p.row_tiles *= 2;
+    if (p.max_new > kBlockTokens && p.units * lists * (blocks(p.row_tiles) - 1) > kManyGroups) p.row_tiles = 2;
     p.row_blocks = blocks(p.row_tiles);
     // A workgroup takes several units, one after the other, where there would be more than kMostGroups: most
     // have nothing to do then, their bounds being wide.  256 single tokens of 1000 places, 8 heads of 128, us, with a
@@ -246,7 +245,7 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
                        : c->head_size <= 128 ? chunk_kernel_128
                        : c->head_size <= 192 ? chunk_kernel_192
                                              : chunk_kernel_256;
-    p.chunk = chunk(f16, f32_out, &p.shape);
+    p.chunk = chunk(f16, f32_out, std::min(p.row_tiles, 2), &p.shape);
     p.chunk_tiles = 0;
     p.splits = 1;
     if (p.max_new > kBlockTokens) {
@@ -333,7 +332,7 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     // rows are counted, and a launch's threads, in 32 bits
     const long long shares = (plan.units + plan.share - 1) / plan.share, groups = (shares * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks;
     const long long chunk_groups = plan.chunk_tiles * c->heads, join_groups = plan.join_turns * plan.columns * c->n_seqs;
-    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 31 || chunk_groups >= 1 << 23 || join_groups >= 1LL << 31) return QMV_E_CACHE;
+    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 30 || chunk_groups * plan.splits >= 1LL << 30 || join_groups >= 1LL << 31) return QMV_E_CACHE;
     AttendParams p;
     p.q = static_cast<const char*>(q);
     p.out = static_cast<char*>(out);
@@ -368,9 +367,17 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.cache = device_cache(c, T);
     p.cache.max_places = plan.length;
     void* args[] = {&p};
-    if (int e = launch(plan.block, grid_of(groups), kThreads, args, plan.block_lds, stream)) return e;
-    if (chunk_groups > 0)
-        if (int e = launch(plan.chunk, dim3((unsigned)chunk_groups, plan.splits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
+    if (chunk_groups > 0) {
+        p.chunk_groups = (int)chunk_groups;
+        p.by_chunk_groups = divisor(p.chunk_groups);
+        p.block_groups = (int)groups;
+        p.chunk_rounds = (int)((chunk_groups * plan.splits + kUnits - 1) / kUnits);
+        const int block_rounds = (int)((groups + kUnits - 1) / kUnits);
+        p.both_rounds = std::min(p.chunk_rounds, block_rounds);
+        if (int e = launch(plan.chunk, grid_of((p.chunk_rounds + (long long)block_rounds) * kUnits), plan.shape.threads, args, plan.shape.lds, stream)) return e;
+    } else if (int e = launch(plan.block, grid_of(groups), kThreads, args, plan.block_lds, stream)) {
+        return e;
+    }
     if (p.units == 1 && p.splits == 1) return QMV_OK;
     int leaf = plan.leaf, block_chains = plan.block_chains, chunk_chains = plan.chunk_chains, columns = plan.columns;
     int turns = (int)plan.join_turns;

@@ -33,6 +33,7 @@ typedef __attribute__((ext_vector_type(4))) __bf16 bf16x4;
 typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 
+constexpr int kUnits = 256;           // compute units
 constexpr int kBlockTokens = 16;      // up to so many new tokens a sequence is a block, above a chunk
 constexpr int kLeafBytes = 32768;     // of keys in a leaf, and of values
 constexpr int leaf_keys(int head_size) { return kLeafBytes / 2 / head_size; }
@@ -55,6 +56,10 @@ struct AttendParams {
     int apart;                      // a block's tokens in part and stat: by sequence, so many each (0: as in q)
     float scale;                    // times log2(e)
     Divisor by_group, by_heads, by_seqs, by_rows;      // the last: rows_last, or row_blocks
+    // calls with chunks: workgroups of a share of the keys, and of blocks, and the rounds of kUnits workgroups of
+    // chunks, and those in which both take turns
+    int chunk_groups, block_groups, chunk_rounds, both_rounds;
+    Divisor by_chunk_groups;
     Cache cache;
 };
 
@@ -277,10 +282,10 @@ struct ChunkShape {
     int rows, threads;       // of a workgroup
     int at_once, lds;        // workgroups on a compute unit
 };
-const void* chunk_kernel_64(bool f16, bool f32_out, ChunkShape* shape);
-const void* chunk_kernel_96(bool f16, bool f32_out, ChunkShape* shape);
-const void* chunk_kernel_128(bool f16, bool f32_out, ChunkShape* shape);
-const void* chunk_kernel_192(bool f16, bool f32_out, ChunkShape* shape);
-const void* chunk_kernel_256(bool f16, bool f32_out, ChunkShape* shape);
+const void* chunk_kernel_64(bool f16, bool f32_out, int row_tiles, ChunkShape* shape);
+const void* chunk_kernel_96(bool f16, bool f32_out, int row_tiles, ChunkShape* shape);
+const void* chunk_kernel_128(bool f16, bool f32_out, int row_tiles, ChunkShape* shape);
+const void* chunk_kernel_192(bool f16, bool f32_out, int row_tiles, ChunkShape* shape);
+const void* chunk_kernel_256(bool f16, bool f32_out, int row_tiles, ChunkShape* shape);
 
 }  // namespace ops

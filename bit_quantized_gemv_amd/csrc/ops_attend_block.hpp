@@ -33,12 +33,9 @@ namespace ops {
 template <int DP, int NP, int NR>
 constexpr int block_lds = kLeafBytes + NP * leaf_keys(DP) * 32 + 2 * 4 * 16 * 4 + 16 + (NR > 1 ? NR * DP * 32 : 0);
 
-// Three workgroups on a compute unit where one tile of rows leaves the registers for it; two tiles of heads of up to 64
-// would spill eight (64 sequences of 5 tokens over 1024 places 20.6 us with two workgroups, 23.3 with three).
-// SHARE: a workgroup may take several units; what that holds in registers leaves room for two workgroups on a
-// compute unit where there are three otherwise (64 ragged sequences of up to 8192 places: 235 us, 228 without).
+// One of the launch's workgroups; SHARE: which may take several units.
 template <int DP, class X, int NP, int NR, bool SHARE>
-__global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void block_kernel(AttendParams p)
+__device__ __forceinline__ void block_body(const AttendParams& p, int block, char* lds)
 {
     constexpr int KT = leaf_keys(DP);      // keys of a leaf
     constexpr int WK = KT / 4;             // of which a wave scores
@@ -46,7 +43,6 @@ __global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void bl
     constexpr int DS = DP / 32;            // steps of 32 values of a head
     constexpr int DT = DP / 64;            // tiles of 16 columns that a wave sums
     constexpr int US = KT / 32;            // steps of 32 keys
-    extern __shared__ __align__(16) char lds[];
     char* const values = lds;
     char* const weights = lds + kLeafBytes;
     float* const tops = reinterpret_cast<float*>(weights + NP * KT * 32);
@@ -64,7 +60,7 @@ __global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void bl
     // sequences have one tile of rows, the others come last: workgroups without work between the others
     // would leave compute units to themselves.  255 single tokens of 1000 places, 8 heads of 128, with as many
     // rows as 16 tokens have, us: 205, 488 side by side.
-    const int block = blockIdx.y * gridDim.x + blockIdx.x, turn = block >> 3;
+    const int turn = block >> 3;
     const int rows_turn = divide(turn, p.by_rows), rows_rest = turn - rows_turn * (p.rows_last > 0 ? p.rows_last : p.row_blocks);
     const int rb = p.rows_last > 0 ? rows_turn : rows_rest, over = p.rows_last > 0 ? rows_rest : rows_turn;
     const int eight = divide(over, p.by_heads), head = over - eight * p.heads;
@@ -150,7 +146,7 @@ __global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void bl
     begin();
 
     // several units only without a window, whose units are one after the other from place 0 on
-    const int from = u < vis.units ? vis.unit(u) * U : 0, to = u < vis.units ? SHARE ? vis.high + 1 : min(from + U, vis.high + 1) : 0;
+    const int from = u < vis.units ? vis.unit(u) * U : 0, to = u < vis.units ? SHARE && p.window == 0 ? vis.high + 1 : min(from + U, vis.high + 1) : 0;
     auto next_leaf = [&](int at) {
         while (at < to && !vis.meets(at, at + KT)) at += KT;
         return at < to ? at : -1;
@@ -370,6 +366,17 @@ __global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void bl
     }
 
     finish(now);
+}
+
+// Three workgroups on a compute unit where one tile of rows leaves the registers for it; two tiles of heads of up to 64
+// would spill eight (64 sequences of 5 tokens over 1024 places 20.6 us with two workgroups, 23.3 with three).
+// SHARE: a workgroup may take several units; what that holds in registers leaves room for two workgroups on a
+// compute unit where there are three otherwise (64 ragged sequences of up to 8192 places: 235 us, 228 without).
+template <int DP, class X, int NP, int NR, bool SHARE>
+__global__ __launch_bounds__(256, !SHARE && NR == 1 && DP < 256 ? 3 : 2) void block_kernel(AttendParams p)
+{
+    extern __shared__ __align__(16) char lds[];
+    block_body<DP, X, NP, NR, SHARE>(p, blockIdx.y * gridDim.x + blockIdx.x, lds);
 }
 
 // the kernels of a head size

@@ -10,13 +10,13 @@
 // costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
 // keys of a tile of rows, and a second launch joins them.
 //
-// Measured, 2048 tokens over 16384 places, 32 heads on 8 of 128: 570 us in turn with others' calls, 903 TFLOP/s
-// (677 us back to back, the clock falling), where a library's product of 8192 x 8192 x 8192 reaches 1239.  The
+// Measured, 2048 tokens over 16384 places, 32 heads on 8 of 128: 569 us in turn with others' calls, 905 TFLOP/s
+// (659 us back to back, the clock falling), where a library's product of 8192 x 8192 x 8192 reaches 1239.  The
 // matrix instructions are busy 44% of the time, the vector instructions half of it, reads of LDS (32 KB a
 // wave and tile) 41%; two waves on a SIMD overlap them in part.  Over 8192 places, back to back, heads of 64:
-// 580 TFLOP/s, 96: 751, 192: 731, 256: 687; fp32 outputs (three pieces of each weight) 509 at 128.
+// 562 TFLOP/s, 96: 727, 192: 695, 256: 678; fp32 outputs (three pieces of each weight) 517 at 128.
 #pragma once
-#include "ops_attend.hpp"
+#include "ops_attend_block.hpp"
 
 namespace ops {
 
@@ -37,13 +37,13 @@ struct Chunk {
 // then instead of 2.2e-3 (their own rounding alone: 1.7e-3), and the 2048 tokens above take 602 us for 571.
 constexpr float kRoom = 8.0f;
 
+// One of the launch's workgroups: a tile of rows and one of a head's shares of their keys.
 template <int DP, class X, int NP>
-__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<DP>::kWaves / 4) void chunk_kernel(AttendParams p)
+__device__ __forceinline__ void chunk_body(const AttendParams& p, int group, int share, char* lds)
 {
     typedef Chunk<DP> C;
     constexpr int NK = C::kKeys, KB = NK / 16, DS = DP / 32, DT = DP / 16, US = NK / 32;
     constexpr int BW = KB * DS / C::kWaves;       // blocks of 16 keys and 32 columns that a wave loads
-    extern __shared__ __align__(16) char lds[];
     uint32_t* const masks = reinterpret_cast<uint32_t*>(lds + 4 * C::kTileBytes);      // which keys there are
     uint32_t* const odds = masks + 8;                                                   // whether a wave has met values that are no numbers
 
@@ -52,8 +52,8 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
     // The sequence whose rows these are: the launch has about as many workgroups as all chunks have
     // tiles of rows, one after the other.  255 single tokens beside a chunk of 2048, 1000 places each, us:
     // 1048 when every sequence had as many workgroups as the longest.
-    int left = divide(blockIdx.x, p.by_heads), b = -1, rb = 0;
-    const int head = blockIdx.x - left * p.heads;
+    int left = divide(group, p.by_heads), b = -1, rb = 0;
+    const int head = group - left * p.heads;
     Seq s;
     for (int i = 0; i < p.cache.n_seqs && b < 0; i += 64) {
         Seq of = {0, 0, 0};
@@ -79,7 +79,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
 
     // the tiles of keys that the workgroup's rows see, and its share of them
     const Visible vis = visible(place0 + i_first, i_last - i_first + 1, p.window, p.sinks, NK);
-    const int t_from = (int)((long long)vis.units * blockIdx.y / p.splits), t_to = (int)((long long)vis.units * (blockIdx.y + 1) / p.splits);
+    const int t_from = (int)((long long)vis.units * share / p.splits), t_to = (int)((long long)vis.units * (share + 1) / p.splits);
 
     // queries, negative scales turned into them
     const uint32_t flip = p.scale < 0.0f ? 0x80008000u : 0;
@@ -340,7 +340,7 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
 #pragma unroll
     for (int rt = 0; rt < 2; ++rt) {
         if (!mine[rt]) continue;
-        const long long at = row[rt] * p.splits + blockIdx.y;
+        const long long at = row[rt] * p.splits + share;
         if (p.splits > 1 && g == 0) p.chunk_stat[at] = f32x2{m[rt], l[rt].x};
 #pragma unroll
         for (int d = 0; d < DT; ++d) {
@@ -352,12 +352,45 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
     }
 }
 
-template <int DP>
-const void* chunk_kernel_types(bool f16, bool f32_out, ChunkShape* shape)
+// A call's blocks in the same launch: they are bound by memory, chunks by the matrix instructions, and neither waits
+// for the other's end.  63 single tokens of 1000 places beside a chunk of 512, 8 heads of 128, us: 98, in two launches 134;
+// 255 beside one of 2048: 291, 305.  They take turns by rounds of a workgroup for every compute unit: parts of the chip
+// would get all of one kind otherwise (a chunk of 2048 over 16384 places by eights in turn with blocks without work:
+// 986 us, by rounds 659).
+template <int DP, class X, int NP, int NR>
+__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<DP>::kWaves / 4) void chunk_kernel(AttendParams p)
 {
-    *shape = ChunkShape{Chunk<DP>::kRows, Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce, Chunk<DP>::kLds};
-    if (f16) return f32_out ? (const void*)&chunk_kernel<DP, _Float16, 2> : (const void*)&chunk_kernel<DP, _Float16, 1>;
-    return f32_out ? (const void*)&chunk_kernel<DP, __bf16, 3> : (const void*)&chunk_kernel<DP, __bf16, 1>;
+    extern __shared__ __align__(16) char lds[];
+    together(p.both_rounds, p.chunk_rounds, p.block_groups, p.chunk_groups, p.by_chunk_groups.magic, p.by_chunk_groups.shift);
+    const int i = blockIdx.y * gridDim.x + blockIdx.x, round = i / kUnits;
+    const bool rest = round >= 2 * p.both_rounds, chunk = rest ? p.chunk_rounds > p.both_rounds : !(round & 1);
+    const int at = (rest ? round - p.both_rounds : round >> 1) * kUnits + i % kUnits;
+    if (chunk) {
+        const int share = divide(at, p.by_chunk_groups);
+        // the arguments read apart from those of blocks: read for both at the start, they are spilled over the loop (5%)
+        typedef __attribute__((address_space(4))) const AttendParams* Args;
+        Args args = (Args)__builtin_amdgcn_kernarg_segment_ptr();
+        asm volatile("" : "+s"(args));
+        if (share < p.splits) chunk_body<DP, X, NP>(*(const AttendParams*)args, at - share * p.chunk_groups, share, lds);
+    } else {
+        if (threadIdx.x < 256 && at < p.block_groups) block_body<(DP > 128 ? 256 : DP > 64 ? 128 : 64), X, NP, NR, true>(p, at, lds);
+    }
+}
+
+template <int DP, class X, int NP>
+const void* chunk_kernel_rows(int row_tiles, ChunkShape* shape)
+{
+    constexpr int BP = DP > 128 ? 256 : DP > 64 ? 128 : 64;
+    const int block = row_tiles == 1 ? block_lds<BP, NP, 1> : block_lds<BP, NP, 2>;
+    *shape = ChunkShape{Chunk<DP>::kRows, Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce, Chunk<DP>::kLds > block ? Chunk<DP>::kLds : block};
+    return row_tiles == 1 ? (const void*)&chunk_kernel<DP, X, NP, 1> : (const void*)&chunk_kernel<DP, X, NP, 2>;
+}
+
+template <int DP>
+const void* chunk_kernel_types(bool f16, bool f32_out, int row_tiles, ChunkShape* shape)
+{
+    if (f16) return f32_out ? chunk_kernel_rows<DP, _Float16, 2>(row_tiles, shape) : chunk_kernel_rows<DP, _Float16, 1>(row_tiles, shape);
+    return f32_out ? chunk_kernel_rows<DP, __bf16, 3>(row_tiles, shape) : chunk_kernel_rows<DP, __bf16, 1>(row_tiles, shape);
 }
 
 }  // namespace ops

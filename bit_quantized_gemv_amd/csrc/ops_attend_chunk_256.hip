@@ -3,6 +3,6 @@
 
 namespace ops {
 
-const void* chunk_kernel_256(bool f16, bool f32_out, ChunkShape* shape) { return chunk_kernel_types<256>(f16, f32_out, shape); }
+const void* chunk_kernel_256(bool f16, bool f32_out, int row_tiles, ChunkShape* shape) { return chunk_kernel_types<256>(f16, f32_out, row_tiles, shape); }
 
 }  // namespace ops
