@@ -21,23 +21,38 @@ constexpr int kChains = kThreads / kLanes;
 // The parts of rows, joined: those of blocks, and those of chunks, which are `splits` supers each.  Leaves
 // are joined to supers one after the other, as the block's kernel does it; a row is the sum of its
 // supers, each with its weight against the row's largest score, in order: first eights of them,
-// then those.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows, or of some times as many (MORE,
-// which costs 20 registers and 0.7 us).  Bound by latency, of the arguments, the sequence and the parts: 4.2 us
+// then those.  A workgroup takes 64 columns of 2^-chains_log2 of 16 rows of a sequence (kRows), of some times
+// as many (kMoreRows: 20 registers more and 0.7 us), or of a token's rows (kTokens).  Bound by latency, of the arguments, the sequence and the parts: 4.2 us
 // for 32 rows of 4 parts, 6.5 for 32 rows of 128; every group of 16 lanes asks for eight parts at once.
 // 16384 rows of 4 parts of 128 values (33 MB): 11 us.
-template <bool MORE>
-__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int block_chains, int chunk_chains, int columns, Divisor by_columns, int turns)
+enum class Join { kRows, kMoreRows, kTokens };
+
+template <Join HOW>
+__global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf, int block_chains, int chunk_chains, int columns, Divisor by_columns, int turns, Divisor by_turns)
 {
     __shared__ __align__(16) f32x4 sums[kThreads];
     __shared__ f32x2 stats[kChains];
     __shared__ float tops[kChains];
     const Cache& c = p.cache;
     together(p.part, p.stat, p.chunk_part, p.chunk_stat, p.out, c.starts, c.lengths, c.n_seqs, c.max_places, c.T, p.units, p.per_unit, p.splits, p.apart, p.q_heads, p.D,
-             p.window, p.sinks, p.max_new, p.out_f32, p.by_seqs.magic, p.by_seqs.shift, leaf, block_chains, chunk_chains, columns, by_columns.magic, by_columns.shift, turns);
-    const Turn at_turn = turn_of(blockIdx.y * gridDim.x + blockIdx.x, p);
-    const int turn = divide(at_turn.turn, by_columns), column = at_turn.turn - turn * columns, b = at_turn.b;
+             p.window, p.sinks, p.max_new, p.out_f32, p.by_seqs.magic, p.by_seqs.shift, leaf, block_chains, chunk_chains, columns, by_columns.magic, by_columns.shift, turns,
+             by_turns.magic, by_turns.shift);
+    int b, over = blockIdx.y * gridDim.x + blockIdx.x, token = 0;
+    if constexpr (HOW == Join::kTokens) {
+        const int all = divide(over, by_columns);
+        token = divide(all, by_turns);
+        over -= token * turns * columns;
+        if (token >= c.T) return;
+        b = __builtin_amdgcn_readfirstlane(sequence_of(c, token, threadIdx.x & 63));
+        if (b < 0) return;
+    } else {
+        const Turn at_turn = turn_of(over, p);
+        over = at_turn.turn;
+        b = at_turn.b;
+    }
+    const int turn = divide(over, by_columns), column = over - turn * columns;
     if (turn >= turns) return;
-    const Seq s = sequence(p.cache, b);
+    const Seq s = sequence(c, b);
     const int tokens = min(s.count, p.max_new), place0 = s.length - s.count;
     const bool chunk = tokens > kBlockTokens;
     const int slots = chunk ? p.splits : p.units;
@@ -54,9 +69,17 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf
         eights = Visible{0, 0, 0, 0, 0, (slots + kSuper - 1) / kSuper};
     }
     const long long first = chunk ? (long long)s.start * p.q_heads : block_row(p, b, s.start);
-    for (int r0 = turn * rows; r0 < tokens * p.q_heads; r0 += turns * rows) {
+    // the rows of the sequence, or of the token
+    int r_from = 0, r_to = tokens * p.q_heads;
+    if constexpr (HOW == Join::kTokens) {
+        const int i = token - s.start;
+        if (i < 0 || i >= tokens) return;
+        r_from = i * p.q_heads;
+        r_to = r_from + p.q_heads;
+    }
+    for (int r0 = r_from + turn * rows; r0 < r_to; r0 += turns * rows) {
         const int r = r0 + team;
-        const bool mine = r < tokens * p.q_heads, mine_d = mine && d < p.D;
+        const bool mine = r < r_to, mine_d = mine && d < p.D;
         const long long row = (long long)s.start * p.q_heads + r;
         const f32x2* stat = (chunk ? p.chunk_stat : p.stat) + (first + r) * slots;
         const float* part = (chunk ? p.chunk_part : p.part) + (first + r) * slots * p.D + d;
@@ -148,7 +171,7 @@ __global__ __launch_bounds__(kThreads) void join_kernel(AttendParams p, int leaf
         l += le;
         o += oe;
         if (mine_d && chain == 0) put_result(p, row, d, o, l);
-        if constexpr (!MORE) return;
+        if constexpr (HOW == Join::kRows) return;
         lds_only_barrier();
     }
 }
@@ -174,8 +197,8 @@ struct Plan {
     int block_lds;
     ChunkShape shape;
     int block_chains, chunk_chains, columns;      // the join: groups of lanes to a row, and blocks of 64 columns
-    long long join_turns;                         // workgroups of a sequence's 64 columns
-    bool join_more;                               // which may have more than 16 rows each
+    long long join_turns, join_groups;            // workgroups of 64 columns of a sequence or token, and all of them
+    Join join;                                    // of a sequence's, or of a token's
     int apart;                                    // rows of a sequence among the parts of blocks; 0: as in q
     long long part_bytes, stat_bytes, chunk_part_bytes, chunk_stat_bytes;
     long long bytes() const { return part_bytes + stat_bytes + chunk_part_bytes + chunk_stat_bytes; }
@@ -263,13 +286,23 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     p.block_chains = chains_of(p.units);
     p.chunk_chains = chains_of(p.splits);
     auto joins = [&](long long rows, long long parts, int chains) { return parts > 1 ? (rows + (kChains >> chains) - 1) / (kChains >> chains) : 0; };
-    // A workgroup for every 16 rows, or, where there are chunks and most sequences may have one token, kManyGroups
-    // where those are fewer than half, and one token's at least: 255 single tokens beside a chunk of 2048, 32 heads, 11 us for 31; 15 beside one of
-    // 512 tokens in two shares, 26 for 110.
+    // A workgroup for every 16 rows (or fewer of many parts) of a sequence, as many for each as the longest may have.  Where
+    // chunks have parts and that is twice what the tokens have, a token's instead: 15 single tokens of 4000 places beside
+    // a chunk of 512 tokens in two shares, whole calls, us: 85, by sequences 96; the chunk alone 61.8 and 59.5.  Where only
+    // blocks beside chunks have parts, kManyGroups if those are fewer than half, and one token's at least, which then take
+    // more rows: the join of 255 single tokens beside a chunk of 2048 11 for 31.
+    p.join = Join::kRows;
     p.join_turns = std::max(joins((long long)tokens * q_heads, p.units, p.block_chains), joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains));
+    const long long of_token = joins(q_heads, p.splits, p.chunk_chains);
     const long long most = std::max(joins(q_heads, p.units, p.block_chains), kManyGroups / (p.columns * c->n_seqs));
-    p.join_more = p.max_new > kBlockTokens && p.join_turns > 2 * most;
-    if (p.join_more) p.join_turns = most;
+    if (p.splits > 1 && p.join_turns * c->n_seqs > 2 * of_token * T) {
+        p.join = Join::kTokens;
+        p.join_turns = of_token;
+    } else if (p.max_new > kBlockTokens && p.join_turns > 2 * most) {
+        p.join = Join::kMoreRows;
+        p.join_turns = most;
+    }
+    p.join_groups = p.join_turns * p.columns * (p.join == Join::kTokens ? T : c->n_seqs);
     p.apart = (long long)c->n_seqs * tokens < T ? tokens : 0;
     const long long parts = p.units > 1 ? (long long)(p.apart > 0 ? c->n_seqs * tokens : T) * q_heads * p.units : 0;
     const long long chunk_parts = p.splits > 1 ? (long long)T * q_heads * p.splits : 0;
@@ -331,8 +364,8 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     if (!disjoint(in, outs)) return QMV_E_ALIAS;
     // rows are counted, and a launch's threads, in 32 bits
     const long long shares = (plan.units + plan.share - 1) / plan.share, groups = (shares * c->n_seqs + 7) / 8 * 8 * c->heads * plan.row_blocks;
-    const long long chunk_groups = plan.chunk_tiles * c->heads, join_groups = plan.join_turns * plan.columns * c->n_seqs;
-    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 30 || chunk_groups * plan.splits >= 1LL << 30 || join_groups >= 1LL << 31) return QMV_E_CACHE;
+    const long long chunk_groups = plan.chunk_tiles * c->heads;
+    if ((long long)plan.max_new * q_heads > 1 << 30 || groups >= 1LL << 30 || chunk_groups * plan.splits >= 1LL << 30 || plan.join_groups >= 1LL << 31) return QMV_E_CACHE;
     AttendParams p;
     p.q = static_cast<const char*>(q);
     p.out = static_cast<char*>(out);
@@ -381,9 +414,12 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     if (p.units == 1 && p.splits == 1) return QMV_OK;
     int leaf = plan.leaf, block_chains = plan.block_chains, chunk_chains = plan.chunk_chains, columns = plan.columns;
     int turns = (int)plan.join_turns;
-    Divisor by_columns = divisor(columns);
-    void* join[] = {&p, &leaf, &block_chains, &chunk_chains, &columns, &by_columns, &turns};
-    return launch(plan.join_more ? (const void*)&join_kernel<true> : (const void*)&join_kernel<false>, grid_of(join_groups), kThreads, join, 0, stream);
+    Divisor by_columns = divisor(columns), by_turns = divisor(turns);
+    void* join[] = {&p, &leaf, &block_chains, &chunk_chains, &columns, &by_columns, &turns, &by_turns};
+    const void* const f = plan.join == Join::kRows       ? (const void*)&join_kernel<Join::kRows>
+                          : plan.join == Join::kMoreRows ? (const void*)&join_kernel<Join::kMoreRows>
+                                                         : (const void*)&join_kernel<Join::kTokens>;
+    return launch(f, grid_of(plan.join_groups), kThreads, join, 0, stream);
 }
 
 }  // extern "C"
