@@ -182,8 +182,6 @@ int check_sizes(const qmv_cache* c, int T, int q_heads, int max_new, int max_len
     return max_new < 1 || max_length < 0 || window < 0 || sinks < 0 ? QMV_E_CACHE : QMV_OK;
 }
 
-int bound_of(int D) { return D <= 64 ? 64 : D <= 128 ? 128 : 256; }
-
 // How a call is cut up: by its sizes alone.
 struct Plan {
     int max_new, length, window, sinks;           // as far as they matter
@@ -245,8 +243,7 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     // Supers are few: four tiles of rows a workgroup only where that leaves two workgroups for every
     // compute unit, two where it leaves three for four.  13 tokens, 64 query heads on 8 of 128, 8192 places, us: 47.6
     // with four, 33.2 with two, 39.8 with one; 32 sequences of half the query heads, 2048: 82, 99, 137;
-    // 16 on 8 of 256, 8192: 33.7 with two, 28.7 with one,
-    // 12000: 35.7 and 43.9.
+    // 16 on 8 of 256, 8192: 33.7 with two, 28.7 with one, 12000: 35.7 and 43.9.
     if (p.per_unit > 1) {
         while (p.row_tiles > 1 && p.units * lists * blocks(p.row_tiles) < (p.row_tiles == 4 ? 8 : 3) * kUnits / 4) p.row_tiles /= 2;
     }
