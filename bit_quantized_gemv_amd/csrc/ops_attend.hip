@@ -286,12 +286,12 @@ Plan plan_of(const qmv_cache* c, int T, int q_heads, int max_new, int max_length
     // A workgroup for every 16 rows (or fewer of many parts) of a sequence, as many for each as the longest may have.  Where
     // chunks have parts and that is twice what the tokens have, a token's instead: 15 single tokens of 4000 places beside
     // a chunk of 512 tokens in two shares, whole calls, us: 85, by sequences 96; the chunk alone 61.8 and 59.5.  Where only
-    // blocks beside chunks have parts, kManyGroups if those are fewer than half, and one token's at least, which then take
-    // more rows: the join of 255 single tokens beside a chunk of 2048 11 for 31.
+    // blocks beside chunks have parts, kManyGroups if those are fewer than half, and one token's at least, of blocks and of
+    // chunks, whichever have parts; they then take more rows: the join of 255 single tokens beside a chunk of 2048 11 for 31.
     p.join = Join::kRows;
     p.join_turns = std::max(joins((long long)tokens * q_heads, p.units, p.block_chains), joins((long long)p.max_new * q_heads, p.splits, p.chunk_chains));
     const long long of_token = joins(q_heads, p.splits, p.chunk_chains);
-    const long long most = std::max(joins(q_heads, p.units, p.block_chains), kManyGroups / (p.columns * c->n_seqs));
+    const long long most = std::max({joins(q_heads, p.units, p.block_chains), of_token, kManyGroups / (p.columns * c->n_seqs)});
     if (p.splits > 1 && p.join_turns * c->n_seqs > 2 * of_token * T) {
         p.join = Join::kTokens;
         p.join_turns = of_token;

@@ -403,3 +403,21 @@ def test_no_tokens():
     out = torch.full((3, 4, 64), 2.0, device=DEV)
     q.attend(z(3, 4, 64), z(3, 4, 2, 64), z(3, 4, 2, 64), i(0, 2), i(1), i(0), out=out)
     assert (out == 2).all()
+
+
+@pytest.mark.parametrize("D,window,many", [(256, 0, 1025), (256, 200, 1025), (128, 0, 2100)])
+def test_shared_chunks_among_thousands(D, window, many):
+    """Chunks whose keys several workgroups share, beside blocks of one part, among so many sequences that a workgroup of the join
+    takes all rows of its own."""
+    c = Batch([1, 17, 17, 0, 3], [500, 512, 300, 9, 70], 1, D, 16, seed=D)
+    qs = queries(c, 2)
+    kw = dict(window=window, sinks=3 if window else 0)
+    want, reach = attend64(qs, c, **kw)
+    order = ([0, 4, 0, 3, 4] * many)[:many - 6] + [1, 0, 2, 3, 1, 4]
+    new, k, v, pages, begin, lens = of(c, qs, order)
+    out = torch.full((new.shape[0] + 7, 2, D), 9.0, device=DEV)
+    q.attend(torch.cat([new, new[:7]]), k, v, pages, begin, lens, out=out, max_new=17, max_length=512, **kw)
+    s, n = c.starts.tolist(), int(begin[-1])
+    rows = torch.tensor([s[b] + i for b in order for i in range(c.new[b])])
+    check_attend(out[:n], want[rows], reach[rows], "bf16", "f32")
+    assert (out[n:] == 9).all()
