@@ -43,6 +43,7 @@ __device__ __forceinline__ void block_body(const AttendParams& p, int block, cha
     constexpr int DS = DP / 32;            // steps of 32 values of a head
     constexpr int DT = DP / 64;            // tiles of 16 columns that a wave sums
     constexpr int US = KT / 32;            // steps of 32 keys
+    constexpr float kLift = 1 << (int)lift_log2(X());      // of a leaf's weights, whose largest is 1: exact, so what fp16 holds without it has the same bits
     char* const values = lds;
     char* const weights = lds + kLeafBytes;
     float* const tops = reinterpret_cast<float*>(weights + NP * KT * 32);
@@ -284,6 +285,7 @@ __device__ __forceinline__ void block_body(const AttendParams& p, int block, cha
 #pragma unroll
                 for (int i = 0; i < 4; ++i) w[i] = exp2_of(x[t][i] - at);
                 sum += (w.x + w.y) + (w.z + w.w);
+                w *= kLift;
                 const int block = wave * TILES + t;
 #pragma unroll
                 for (int c = 0; c < NP; ++c) {
@@ -355,7 +357,7 @@ __device__ __forceinline__ void block_body(const AttendParams& p, int block, cha
                 }
             }
 #pragma unroll
-            for (int d = 0; d < DT; ++d) o[rt][d] = joined(o[rt][d], a[d], by);
+            for (int d = 0; d < DT; ++d) o[rt][d] = joined(o[rt][d], a[d], Factors{by.a, by.b / kLift});
         }
         if (last && next >= 0) {
             finish(now);
@@ -395,7 +397,8 @@ const void* block_kernel_shares(bool share, int row_tiles, int* lds)
     return share ? block_kernel_rows<DP, X, NP, true>(row_tiles, lds) : block_kernel_rows<DP, X, NP, false>(row_tiles, lds);
 }
 
-// a weight in one piece for bf16 outputs; for fp32 ones in as many as hold 22 bits of it or more
+// A weight in one piece for bf16 outputs; for fp32 ones in as many as hold 22 bits of it or more (fp16: down to 2^-18 of the leaf's
+// largest, and below that to 2^-40 of it).
 template <int DP>
 const void* block_kernel_types(bool f16, bool f32_out, bool share, int row_tiles, int* lds)
 {

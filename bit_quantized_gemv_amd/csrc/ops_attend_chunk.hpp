@@ -6,7 +6,7 @@
 // registers with their outputs, and walks the keys that they see in tiles through LDS, the
 // next tile's on their way there meanwhile.  A wave scores 32 rows against the tile,
 // takes the weights with the rows' running maxima, and adds the weighted values up; a maximum
-// is followed only when it has grown by 2^8, which weights and sums have room for, since moving it
+// is followed only when it has grown by 2^8 (fp16: less), which weights and sums have room for, since moving it
 // costs a pass over the outputs.  Where the rows alone are few workgroups, several share the
 // keys of a tile of rows, and a second launch joins them.
 //
@@ -35,7 +35,11 @@ struct Chunk {
 
 // 0 would follow every maximum, which makes the largest weights exact ones: bf16 outputs are off by 1.8e-3 of their norm
 // then instead of 2.2e-3 (their own rounding alone: 1.7e-3), and the 2048 tokens above take 602 us for 571.
-constexpr float kRoom = 8.0f;
+// fp16 has less room: what a maximum may lag by is lost to the smallest weights, which keep all their bits down to 2^(room - 29) of
+// the largest, and for fp32 outputs, in two pieces, down to 2^(room - 18).  2048 tokens over 16384 places: 657 us with 8 (as bf16), 671
+// with 4, 675 with 2, 694 with 0; fp32 out 903 with 8, 936 with 1, 932 with 2.
+constexpr float room(__bf16, int) { return 8.0f; }
+constexpr float room(_Float16, int pieces) { return pieces == 1 ? 4.0f : 1.0f; }
 
 // One of the launch's workgroups: a tile of rows and one of a head's shares of their keys.
 template <int DP, class X, int NP>
@@ -44,6 +48,7 @@ __device__ __forceinline__ void chunk_body(const AttendParams& p, int group, int
     typedef Chunk<DP> C;
     constexpr int NK = C::kKeys, KB = NK / 16, DS = DP / 32, DT = DP / 16, US = NK / 32;
     constexpr int BW = KB * DS / C::kWaves;       // blocks of 16 keys and 32 columns that a wave loads
+    constexpr float kRoom = room(X(), NP), kUp = lift_log2(X()) > 0.0f ? lift_log2(X()) - kRoom : 0.0f;
     uint32_t* const masks = reinterpret_cast<uint32_t*>(lds + 4 * C::kTileBytes);      // which keys there are
     uint32_t* const odds = masks + 8;                                                   // whether a wave has met values that are no numbers
 
@@ -214,7 +219,7 @@ __device__ __forceinline__ void chunk_body(const AttendParams& p, int group, int
             by[rt] = move ? exp2_of(m[rt] - now) : 1.0f;
             m[rt] = now;
             moved = moved || move;
-            const float at = now == kGone ? 0.0f : now;
+            const float at = now == kGone ? 0.0f : now - kUp;
 #pragma unroll
             for (int k = 0; k < KB; ++k) {
                 f32x4 e;

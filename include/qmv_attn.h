@@ -132,7 +132,8 @@ int qmv_append(const qmv_rotation* r, const qmv_cache* c, const void* q, const v
  *        nothing between calls, and serves one call at a time
  * Products are exact, and sums, maxima and exponentials fp32; the weights are rounded to the
  * cache's dtype for the second product, or split into pieces that hold 22 bits or more of them if
- * out is fp32.  A value of the cache that is infinite or NaN makes infinite or NaN (either) what
+ * out is fp32.  fp16 weights below 2^-25 of the row's largest (fp32 out: 2^-17) are held to 2^-36
+ * (2^-39) of that instead.  A value of the cache that is infinite or NaN makes infinite or NaN (either) what
  * the rows that see it sum up with it.
  * Sequences of up to 16 new tokens: a token's bits depend on its place, the keys and values that it
  * sees and the head size alone, so those of a block are those of a call for each token, whatever

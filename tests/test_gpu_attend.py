@@ -421,3 +421,34 @@ def test_shared_chunks_among_thousands(D, window, many):
     rows = torch.tensor([s[b] + i for b in order for i in range(c.new[b])])
     check_attend(out[:n], want[rows], reach[rows], "bf16", "f32")
     assert (out[n:] == 9).all()
+
+
+def peaked(new, length, D, gap, far, seed):
+    """fp16 keys of which the first outweighs each other one by about 2^gap, and holds the value 0; or, if `far`, the last that all see."""
+    c = Batch([new], [length], 1, D, 16, "f16", seed=seed)
+    qs = queries(c, 2)
+    qs[..., 0] = 8.0
+    top = length - new if far else 0
+    for j in range(length):
+        at = c.row(0, j)
+        c.k[at][..., 1:] *= 0.25
+        c.k[at][..., 0] = gap * math.log(2.0) / 8.0 * D ** 0.5 if j == top else 0.0
+        if j == top:
+            c.v[at] = 0.0
+    return c, qs
+
+
+@pytest.mark.parametrize("gap", [16, 20, 24, 26])
+@pytest.mark.parametrize("new,length", [(1, 4096), (13, 4096), (100, 4096), (20, 700)])
+@pytest.mark.parametrize("D,far", [(64, False), (128, True)])
+def test_peaks(new, length, D, far, gap):
+    """A key that takes nearly all the weight, and adds nothing: what the others add, in one share of the keys and in several."""
+    c, qs = peaked(new, length, D, gap, far, seed=gap)
+    want, reach = attend64(qs, c)
+    for out in ("f32", "bf16"):
+        check_attend(run(c, qs, out_dtype=TORCH[out]), want, reach, "f16", out, "shared")
+        many = 140          # enough rows that a chunk's keys are one workgroup's
+        new_q, *args = of(c, qs, [0] * many)
+        got = q.attend(new_q, *args, out_dtype=TORCH[out], max_new=new, max_length=length)
+        check_attend(got[-new:], want, reach, "f16", out, "one share")
+        assert torch.equal(got, got[:new].repeat(many, 1, 1))
