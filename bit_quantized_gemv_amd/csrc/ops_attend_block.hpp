@@ -370,7 +370,8 @@ __device__ __forceinline__ void block_body(const AttendParams& p, int block, cha
     finish(now);
 }
 
-// Three workgroups on a compute unit where one tile of rows leaves the registers for it; two tiles of heads of up to 64
+// Three workgroups on a compute unit where one tile of rows leaves the registers for it (of heads of 64, three pieces of weights fill the LDS
+// of two; bounds of two there: one token over 16384 places 17.8 us for 17.6); two tiles of heads of up to 64
 // would spill eight (64 sequences of 5 tokens over 1024 places 20.6 us with two workgroups, 23.3 with three).
 // SHARE: a workgroup may take several units; what that holds in registers leaves room for two workgroups on a
 // compute unit where there are three otherwise (64 ragged sequences of up to 8192 places: 235 us, 228 without).

@@ -26,7 +26,7 @@ namespace ops {
 template <int DP>
 struct Chunk {
     static constexpr int kWaves = DP > 192 ? 8 : 4;
-    static constexpr int kAtOnce = DP > 192 ? 1 : DP > 64 ? 2 : 3;
+    static constexpr int kAtOnce = DP > 192 ? 1 : DP > 64 ? 2 : 3;     // workgroups on a unit, as far as registers go
     static constexpr int kKeys = DP > 128 ? 32 : 64;               // of a tile
     static constexpr int kRows = kWaves * 32;
     static constexpr int kTileBytes = kKeys * DP * 2;
@@ -362,8 +362,16 @@ __device__ __forceinline__ void chunk_body(const AttendParams& p, int group, int
 // 255 beside one of 2048: 291, 305.  They take turns by rounds of a workgroup for every compute unit: parts of the chip
 // would get all of one kind otherwise (a chunk of 2048 over 16384 places by eights in turn with blocks without work:
 // 986 us, by rounds 659).
+template <int DP, int NP, int NR>
+struct Both {
+    static constexpr int kBlock = DP > 128 ? 256 : DP > 64 ? 128 : 64;       // the block's head size
+    static constexpr int kLds = Chunk<DP>::kLds > block_lds<kBlock, NP, NR> ? Chunk<DP>::kLds : block_lds<kBlock, NP, NR>;
+    // Of heads of 64 with fp32 outputs, the block's pieces of weights may leave room for two alone.  512 tokens over 4096 places, bf16
+    // cache, us: 74 with two planned, 79 with three.
+    static constexpr int kAtOnce = fit(kLds) < Chunk<DP>::kAtOnce ? fit(kLds) : Chunk<DP>::kAtOnce;
+};
 template <int DP, class X, int NP, int NR>
-__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<DP>::kWaves / 4) void chunk_kernel(AttendParams p)
+__global__ __launch_bounds__(Chunk<DP>::kWaves * 64, (Both<DP, NP, NR>::kAtOnce * Chunk<DP>::kWaves / 4)) void chunk_kernel(AttendParams p)
 {
     extern __shared__ __align__(16) char lds[];
     together(p.both_rounds, p.chunk_rounds, p.block_groups, p.chunk_groups, p.by_chunk_groups.magic, p.by_chunk_groups.shift);
@@ -378,17 +386,21 @@ __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce * Chunk<
         asm volatile("" : "+s"(args));
         if (share < p.splits) chunk_body<DP, X, NP>(*(const AttendParams*)args, at - share * p.chunk_groups, share, lds);
     } else {
-        if (threadIdx.x < 256 && at < p.block_groups) block_body<(DP > 128 ? 256 : DP > 64 ? 128 : 64), X, NP, NR, true>(p, at, lds);
+        if (threadIdx.x < 256 && at < p.block_groups) block_body<Both<DP, NP, NR>::kBlock, X, NP, NR, true>(p, at, lds);
     }
 }
 
+template <int DP, class X, int NP, int NR>
+const void* chunk_kernel_shape(ChunkShape* shape)
+{
+    typedef Both<DP, NP, NR> B;
+    *shape = ChunkShape{Chunk<DP>::kRows, Chunk<DP>::kWaves * 64, B::kAtOnce, B::kLds};
+    return (const void*)&chunk_kernel<DP, X, NP, NR>;
+}
 template <int DP, class X, int NP>
 const void* chunk_kernel_rows(int row_tiles, ChunkShape* shape)
 {
-    constexpr int BP = DP > 128 ? 256 : DP > 64 ? 128 : 64;
-    const int block = row_tiles == 1 ? block_lds<BP, NP, 1> : block_lds<BP, NP, 2>;
-    *shape = ChunkShape{Chunk<DP>::kRows, Chunk<DP>::kWaves * 64, Chunk<DP>::kAtOnce, Chunk<DP>::kLds > block ? Chunk<DP>::kLds : block};
-    return row_tiles == 1 ? (const void*)&chunk_kernel<DP, X, NP, 1> : (const void*)&chunk_kernel<DP, X, NP, 2>;
+    return row_tiles == 1 ? chunk_kernel_shape<DP, X, NP, 1>(shape) : chunk_kernel_shape<DP, X, NP, 2>(shape);
 }
 
 template <int DP>
