@@ -76,7 +76,8 @@ typedef struct {
  *   pair i < rot / 2 of n is turned by the angle positions[axes[i]][t] * freqs[i]:
  *   (a, b) -> (a cos - b sin, b cos + a sin); the pair's places are i and i + rot / 2, or
  *   2i and 2i + 1 if `interleaved`; the values from rot on stay
- * The norm is taken in fp32, the angle in fp64, and the result rounded once.
+ * The norm is taken in fp32, of heads of any size that fp32 holds, the angle in fp64, and the
+ * result rounded once.
  *   freqs     fp32 [rot / 2]
  *   positions int32, row a (at a * positions_row) the T positions of axis a
  *   axes      int32 [rot / 2] (NULL: all 0); outside [0, n_axes): not turned

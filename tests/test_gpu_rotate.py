@@ -225,3 +225,28 @@ def test_many_sequences(B):
         want = torch.zeros(2 * B * P, H, D, dtype=torch.bfloat16)
         want[seq * 2 * P + place] = x
         assert torch.equal(cache.cpu().reshape(-1, H, D), want)
+
+
+@pytest.mark.parametrize("eps", [0.0, 1e-45, 2.0 ** -130, 1e-6])
+@pytest.mark.parametrize("x,out", [("f32", "bf16"), ("bf16", "f16")])
+@pytest.mark.parametrize("D,R", [(64, 32), (24, 24), (256, 0)])
+def test_norms_of_any_size(D, R, x, out, eps):
+    """Heads from the smallest numbers to the largest, whose squares fp32 does not hold, and others beside them."""
+    g = gen(D)
+    sizes = [-148, -140, -126, -110, -75, -70, -64, -60, -50, -40, 0, 40, 60, 63, 64, 70, 100, 125]
+    T, H = len(sizes), 3
+    xs = torch.rand(T, H, D, generator=g).double() * (1 - 2 * torch.randint(0, 2, (T, H, D), generator=g)) * 2.0 ** torch.tensor(sizes).double().reshape(T, 1, 1)
+    xs[:, 1] = torch.randn(T, D, generator=g).double()             # an ordinary head beside each
+    xs[5, 2, 0] = 2.0 ** 90                                        # one value above all others of its head
+    xs = xs.float().to(TORCH[x])
+    w = (1 + 0.3 * torch.randn(D, generator=g)).to(TORCH[x])
+    freqs = (10000.0 ** (-torch.arange(R // 2) / max(R // 2, 1))).float() if R else None
+    pos = torch.randint(0, 500, (T,), generator=g).int()
+    dev = lambda t: None if t is None else t.to(DEV)
+    got, _ = q.rotate(dev(xs), dev(xs), dev(freqs), dev(pos), q_weight=dev(w), k_weight=dev(w), eps=eps, out_dtype=TORCH[out])
+    held = float(torch.tensor(eps, dtype=torch.float32))           # eps as the call holds it
+    want, size = rotate64(xs, w, held, angles_of(pos, None, freqs, T), False)
+    there = xs.double().abs().amax(-1) > 0                         # bf16 holds nothing of the smallest: 0 / 0 without eps
+    there |= torch.tensor(held > 0)
+    assert there.any(-1).all()
+    check_rounded(got.cpu()[there], want[there], size[there], out)
