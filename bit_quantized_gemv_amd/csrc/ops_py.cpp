@@ -493,7 +493,7 @@ struct Rotation {
           qw(optional_tensor(a[3], "q_weight")), kw(optional_tensor(a[4], "k_weight"))
     {
         const double eps = number(a[5], "eps");
-        TORCH_CHECK_VALUE(eps >= 0.0 && std::isfinite(eps), "eps must be a finite number of 0 or more, got ", eps);
+        TORCH_CHECK_VALUE(eps >= 0.0 && std::isfinite((float)eps), "eps must be a number of 0 or more that float32 holds, got ", eps);
         r.eps = (float)eps;
         r.interleaved = truth(a[6]);
         r.n_axes = 1;
@@ -687,7 +687,7 @@ PyObject* attend(PyObject*, PyObject* const* a, Py_ssize_t n)
     const int64_t window = a[6] == Py_None ? 0 : integer(a[6], "window"), sinks = integer(a[7], "sinks");
     TORCH_CHECK_VALUE(window >= 0 && sinks >= 0, "window and sinks must be 0 or more, got ", window, " and ", sinks);
     const double scale = a[8] == Py_None ? 1.0 / std::sqrt((double)std::max<int64_t>(D, 1)) : number(a[8], "scale");
-    TORCH_CHECK_VALUE(std::isfinite(scale), "scale must be finite, got ", scale);
+    TORCH_CHECK_VALUE(std::isfinite((float)scale), "scale must be a finite number that float32 holds, got ", scale);
     const int64_t max_new = a[9] == Py_None ? T : integer(a[9], "max_new");
     const int64_t places = (int64_t)pages.c.max_pages * pages.c.page_size;
     const int64_t max_length = a[10] == Py_None ? places : integer(a[10], "max_length");

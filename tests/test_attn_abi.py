@@ -158,3 +158,11 @@ def test_binding_refuses(L, op, kw, error, text):
     import bit_quantized_gemv_amd as q
     with pytest.raises(error, match=text):
         getattr(q, op)(**{**tensors(op), **kw})
+
+
+@pytest.mark.parametrize("op,kw,text", [("rotate", dict(eps=1e39), "eps"), ("append", dict(eps=4e38), "eps"), ("attend", dict(scale=1e39), "scale"),
+                                        ("attend", dict(scale=-3.5e38), "scale")])
+def test_binding_refuses_what_fp32_does_not_hold(L, op, kw, text):
+    import bit_quantized_gemv_amd as q
+    with pytest.raises(ValueError, match=f"{text} must be"):
+        getattr(q, op)(**{**tensors(op), **kw})
