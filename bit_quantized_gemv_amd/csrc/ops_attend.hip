@@ -388,8 +388,9 @@ int qmv_attend(const qmv_cache* c, const void* q, void* out, void* workspace,
     p.row_blocks = plan.row_blocks;
     p.rows_last = plan.max_new > kBlockTokens ? (int)(groups / 8 / plan.row_blocks) : 0;
     p.per_unit = plan.per_unit;
-    // a scale of zero weighs all places that are seen alike; the smallest does so too, and hides the others
-    p.scale = scale == 0.0f ? 1e-37f : scale * 1.44269504088896340736f;
+    // A scale of zero weighs all places that are seen alike; the smallest number, by which no score is 2^-20, does so too, and
+    // leaves the -inf of the others.
+    p.scale = scale == 0.0f ? 0x1p-149f : scale * 1.44269504088896340736f;
     p.by_group = divisor(p.group);
     p.by_heads = divisor(p.heads);
     p.by_seqs = divisor(c->n_seqs);

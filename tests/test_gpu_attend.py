@@ -452,3 +452,14 @@ def test_peaks(new, length, D, far, gap):
         got = q.attend(new_q, *args, out_dtype=TORCH[out], max_new=new, max_length=length)
         check_attend(got[-new:], want, reach, "f16", out, "one share")
         assert torch.equal(got, got[:new].repeat(many, 1, 1))
+
+
+@pytest.mark.parametrize("new", [1, 5, 60])
+@pytest.mark.parametrize("dt,out", [("bf16", "f32"), ("f16", "bf16")])
+def test_scale_zero_of_large_scores(new, dt, out):
+    """A scale of 0 weighs all places alike, however large q . k is."""
+    c = Batch([new], [100], 2, 64, 16, dt, seed=20)
+    c.k *= 2.0 ** 58 if dt == "bf16" else 2.0 ** 12
+    qs = queries(c, 4) * (2.0 ** 58 if dt == "bf16" else 2.0 ** 12)
+    assert torch.isfinite(qs).all()
+    check_attend(run(c, qs, scale=0.0, out_dtype=TORCH[out]), *attend64(qs, c, scale=0.0), dt, out)
