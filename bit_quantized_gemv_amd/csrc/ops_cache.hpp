@@ -32,12 +32,13 @@ struct Seq {
     int start, count, length;   // its new tokens, and its places with them
 };
 
-__device__ __forceinline__ Seq sequence(const Cache& c, int b)
+// Both starts are taken into 0 .. T before one is taken from the other: the difference of any two would not fit 32 bits.
+__host__ __device__ __forceinline__ Seq sequence(const Cache& c, int b)
 {
     const int s0 = c.starts[b], s1 = c.starts[b + 1], n = c.lengths[b];
     Seq s;
     s.start = max(0, min(s0, c.T));
-    s.count = max(0, min(s1, c.T) - s.start);
+    s.count = max(0, max(0, min(s1, c.T)) - s.start);
     s.length = max(0, min(n, c.max_places));
     return s;
 }

@@ -463,3 +463,30 @@ def test_scale_zero_of_large_scores(new, dt, out):
     qs = queries(c, 4) * (2.0 ** 58 if dt == "bf16" else 2.0 ** 12)
     assert torch.isfinite(qs).all()
     check_attend(run(c, qs, scale=0.0, out_dtype=TORCH[out]), *attend64(qs, c, scale=0.0), dt, out)
+
+
+LOW, HIGH = -2 ** 31, 2 ** 31 - 1
+
+
+@pytest.mark.parametrize("T", [7, 60, 400])
+@pytest.mark.parametrize("starts,ends", [((0, 7, 3), ((0, 7), (7, 7))), ((-5, 4, 100), ((0, 4), (4, 7))), ((7, 7, 7), ((7, 7), (7, 7))),
+                                         ((HIGH, LOW, 5), ((7, 7), (0, 5))), ((3, 5, 6), ((3, 5), (5, 6))), ((6, LOW, LOW), ((6, 6), (0, 0))),
+                                         ((7, -100, HIGH), ((7, 7), (0, 7)))])
+def test_starts_of_any_value(T, starts, ends):
+    """Starts are taken into the tokens: those of a sequence are computed, and no other row is touched. Sevenths of T."""
+    at = lambda i: i if abs(i) > 1000 else i * T // 7
+    c = Batch([1, 1], [T + 23, 500], 2, 64, 16, "bf16", seed=8)
+    starts, ends = [at(i) for i in starts], [(at(a), at(z)) for a, z in ends]
+    qs = torch.randn(T, 4, 64, generator=gen(9)).bfloat16()
+    want, reach, mine = torch.zeros(T, 4, 64, dtype=torch.float64), torch.zeros(T, 4, 64, dtype=torch.float64), torch.zeros(T, dtype=torch.bool)
+    for b, (a, z) in enumerate(ends):
+        c.new, c.starts = [0, 0], torch.tensor([0, 0, 0])
+        c.new[b], c.starts[b] = z - a, a
+        w, r = attend64(qs, c)
+        want[a:z], reach[a:z], mine[a:z] = w[a:z], r[a:z], True
+    k, v, pages, _, lens = c.on()
+    whole = torch.full((3 * T, 4, 64), 3.0, device=DEV)           # the rows before and behind the call's own
+    q.attend(qs.to(DEV), k, v, pages, torch.tensor(starts, dtype=torch.int32, device=DEV), lens, out=whole[T:2 * T])
+    out = whole[T:2 * T].cpu()
+    check_attend(out[mine], want[mine], reach[mine], "bf16", "f32")
+    assert (out[~mine] == 3).all() and (whole[:T] == 3).all() and (whole[2 * T:] == 3).all()
