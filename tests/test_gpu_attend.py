@@ -490,3 +490,23 @@ def test_starts_of_any_value(T, starts, ends):
     out = whole[T:2 * T].cpu()
     check_attend(out[mine], want[mine], reach[mine], "bf16", "f32")
     assert (out[~mine] == 3).all() and (whole[:T] == 3).all() and (whole[2 * T:] == 3).all()
+
+
+@pytest.mark.parametrize("new", [3, 13, 90])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (64, 5)])
+@pytest.mark.parametrize("dt", ["bf16", "f16"])
+@pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
+def test_seen_values(new, window, sinks, dt, junk):
+    """An infinity or NaN among the values alone: no output that has met it is a number, in its column, and all else keeps its bits."""
+    c = Batch([new], [400], 2, 128, 16, dt, seed=21, fill=0.0)
+    qs = queries(c, 4, size=1.0)
+    clean = run(c, qs, window=window, sinks=sinks, out_dtype=torch.float32)
+    place = 400 - new // 2 - 1                         # the second half of the new tokens sees it
+    c.v[c.row(0, place)][:, 5] = junk
+    got = run(c, qs, window=window, sinks=sinks, out_dtype=torch.float32)
+    sees = torch.arange(400 - new, 400) >= place
+    assert sees.any() and not (new > 3 and sees.all())
+    assert torch.equal(got[~sees.to(DEV)], clean[~sees.to(DEV)])
+    other = torch.arange(128) != 5
+    assert not torch.isfinite(got[sees.to(DEV)][..., 5]).any() and torch.isfinite(got[..., other.to(DEV)]).all()
+    assert torch.equal(got[..., other.to(DEV)], clean[..., other.to(DEV)])
