@@ -160,7 +160,7 @@ __global__ __launch_bounds__(kThreads, 4) void rotate_kernel(RotateParams p)
         const int at = t - s.start;
         if (at < 0 || at >= s.count) return;
         place = s.length - s.count + at;
-        if (place >= 0 && place < p.cache.max_places) {
+        if (place >= 0) {          // below max_places, as the sequence's length is
             const int index = page_index(p.cache, place), page = page_of(p.cache, seq, index);
             if (page >= 0) {
                 const int slot = place - index * p.cache.page_size;

@@ -206,7 +206,8 @@ def append(q, k, v, freqs, k_cache, v_cache, pages, starts, lengths, *, position
     tokens starts[b] .. starts[b + 1] - 1 are sequence b's new ones; lengths: int32 [B], its
     places with them.  positions: default each token's place; the rest as `rotate`.  The
     returned q has the cache's dtype.  Rows of tokens that are in no sequence are left as they
-    were; places below 0 or outside the table are not written.
+    were; places below 0 are not written.  A length above the n * page_size places of the
+    table counts as that: the new tokens are then the table's last places, and write over them.
     """
     f = (_py or _binding()).append
     args = (q, k, v, freqs, positions, axes, q_weight, k_weight, eps, interleaved, k_cache, v_cache, pages, starts, lengths, out)

@@ -108,9 +108,10 @@ int qmv_rotate(const qmv_rotation* r, const void* q, const void* k, void* q_out,
 /*
  * The same for the new tokens of a cache's sequences: q_out (of the cache's dtype,
  * contiguous), keys and values (v: rounded only) to their places.  positions NULL: a token's
- * place in its sequence.  Places below 0 (more new tokens than the length says), above the
- * table's end or on a page that holds nothing are not written.  The cache's strides must keep its values apart
- * (QMV_E_STRIDE), k and v must not share values, and no two new tokens a slot.
+ * place in its sequence.  Places below 0 (more new tokens than the length says) or on a page that
+ * holds nothing are not written.  A length above the table's counts as the table's, here too: the new
+ * tokens are its last places then, and write over what is there.  The cache's strides must keep its
+ * values apart (QMV_E_STRIDE), k and v must not share values, and no two new tokens a slot.
  */
 int qmv_append(const qmv_rotation* r, const qmv_cache* c, const void* q, const void* k,
                const void* v, void* q_out, int T, int q_heads, long long q_token,
@@ -134,8 +135,8 @@ int qmv_append(const qmv_rotation* r, const qmv_cache* c, const void* q, const v
  * Products are exact, and sums, maxima and exponentials fp32; the weights are rounded to the
  * cache's dtype for the second product, or split into pieces that hold 22 bits or more of them if
  * out is fp32.  fp16 weights below 2^-25 of the row's largest (fp32 out: 2^-17) are held to 2^-36
- * (2^-39) of that instead.  A value of the cache that is infinite or NaN makes infinite or NaN (either) what
- * the rows that see it sum up with it.
+ * (2^-39) of that instead.  A value of the cache that is infinite or NaN makes infinite or NaN
+ * (either) what the rows that see it sum up with it; but a key whose score is -inf weighs nothing.
  * Sequences of up to 16 new tokens: a token's bits depend on its place, the keys and values that it
  * sees and the head size alone, so those of a block are those of a call for each token, whatever
  * else is in the call.  Of longer ones the order of sums goes with the call's sizes.  A
