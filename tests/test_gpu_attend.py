@@ -510,3 +510,74 @@ def test_seen_values(new, window, sinks, dt, junk):
     other = torch.arange(128) != 5
     assert not torch.isfinite(got[sees.to(DEV)][..., 5]).any() and torch.isfinite(got[..., other.to(DEV)]).all()
     assert torch.equal(got[..., other.to(DEV)], clean[..., other.to(DEV)])
+
+
+@pytest.mark.parametrize("new", [3, 13, 90])
+@pytest.mark.parametrize("window,sinks", [(0, 0), (64, 5)])
+@pytest.mark.parametrize("what", ["k", "kv"])
+@pytest.mark.parametrize("junk", [math.nan, math.inf, -math.inf])
+def test_seen_keys(new, window, sinks, what, junk):
+    """Keys of infinities or NaN, whose scores are NaN where queries have both signs: nothing of the rows that see one is a number, and
+    the others keep their bits."""
+    c = Batch([new], [400], 2, 128, 16, seed=10, fill=0.0)
+    qs = queries(c, 4)
+    clean = run(c, qs, window=window, sinks=sinks, out_dtype=torch.float32)
+    places = [400 - new // 2 - 1] + ([400 - new - 30, 9] if window else [])
+    for j in places:
+        c.k[c.row(0, j)] = junk
+        if what == "kv":
+            c.v[c.row(0, j)] = junk
+    got = run(c, qs, window=window, sinks=sinks, out_dtype=torch.float32)
+    for i in range(new):
+        p = 400 - new + i
+        if any(j <= p and (not window or j > p - window or j < sinks) for j in places):
+            assert not torch.isfinite(got[i]).any(), i
+        else:
+            assert torch.equal(got[i], clean[i]), i
+
+
+@pytest.mark.parametrize("new", [1, 4, 40])
+def test_scores_of_minus_infinity(new):
+    """A key whose score is -inf weighs nothing, and a row that sees no other is zeros."""
+    c = Batch([new], [new + 2], 1, 64, 4, seed=22)
+    qs = queries(c, 2)
+    qs[..., 0] = -1.0
+    ref = Batch([new], [new + 2], 1, 64, 4, seed=22)
+    ref.pages[0, 0] = -1                               # places 0 to 3 hold nothing
+    for j in range(4):
+        if c.row(0, j):
+            c.k[c.row(0, j)][..., 0] = math.inf
+    check_attend(run(c, qs, out_dtype=torch.float32), *attend64(qs, ref), "bf16", "f32")
+
+
+@pytest.mark.parametrize("T", [1, 16, 17, 40])
+@pytest.mark.parametrize("Hq,Hkv,D", [(1024, 1024, 8), (1024, 1, 8), (1000, 8, 16), (1024, 2, 64), (1023, 1, 128)])
+def test_many_heads(T, Hq, Hkv, D):
+    n, G = T + 40, Hq // Hkv
+    c = Batch([T], [n], Hkv, D, 16, seed=T)
+    qs = queries(c, Hq, size=1.0)
+    k, v = (torch.stack([t[c.row(0, j)] for j in range(n)]).double().permute(1, 0, 2) for t in (c.k, c.v))
+    s = torch.matmul(qs.double().reshape(T, Hkv, G, D), k.transpose(1, 2)) / D ** 0.5
+    w = torch.softmax(s.masked_fill((torch.arange(n) > 40 + torch.arange(T).unsqueeze(1)).reshape(T, 1, 1, n), -math.inf), -1)
+    check_attend(run(c, qs, out_dtype=torch.float32), torch.matmul(w, v).reshape(T, Hq, D), torch.matmul(w, v.abs()).reshape(T, Hq, D), "bf16", "f32")
+
+
+def test_as_many_sequences_as_there_may_be():
+    """65535 sequences of one token, as blocks alone and as if there were a chunk among them."""
+    B = 65535
+    g = torch.Generator(device=DEV).manual_seed(1)
+    k, v = (torch.randn(4, 4, 1, 8, generator=g, device=DEV).bfloat16() for _ in range(2))
+    qs = torch.randn(B, 2, 8, generator=g, device=DEV).bfloat16()
+    at = torch.arange(B, device=DEV)
+    pages, lens, starts = (at % 4).int().reshape(B, 1), (at % 4 + 1).int(), torch.arange(B + 1, device=DEV).int()
+    got, again = (q.attend(qs, k, v, pages, starts, lens, max_new=n, out_dtype=torch.float32) for n in (1, 17))
+    kk, vv = (t[at % 4, :, 0].double() for t in (k, v))
+    s = torch.matmul(qs.double(), kk.transpose(1, 2).contiguous()) / 8 ** 0.5
+    w = torch.softmax(s.masked_fill((torch.arange(4, device=DEV) >= lens.unsqueeze(1)).unsqueeze(1), -math.inf), -1)
+    check_attend(got, torch.matmul(w, vv).cpu(), torch.matmul(w, vv.abs()).cpu(), "bf16", "f32")
+    assert torch.equal(got, again)
+
+
+@pytest.mark.parametrize("P,lengths", [(65536, [700, 900]), (40000, [3, 41000]), (4096, [4095, 4126])])
+def test_large_pages(P, lengths):
+    check(Batch([3, 20], lengths, 1, 16, P, seed=1), 2, "f32")

@@ -250,3 +250,18 @@ def test_norms_of_any_size(D, R, x, out, eps):
     there |= torch.tensor(held > 0)
     assert there.any(-1).all()
     check_rounded(got.cpu()[there], want[there], size[there], out)
+
+
+@pytest.mark.parametrize("T,Hq,Hk,D", [(2 ** 22, 1, 1, 8), (70001, 16, 2, 16), (3, 1024, 1024, 256)])
+def test_as_many_tokens_and_heads_as_there_may_be(T, Hq, Hk, D):
+    g = torch.Generator(device=DEV).manual_seed(T)
+    x, y = (torch.randn(T, h, D, generator=g, device=DEV).bfloat16() for h in (Hq, Hk))
+    w = torch.rand(D, generator=g, device=DEV) + 0.5
+    freqs = torch.rand(D // 2, generator=g, device=DEV)
+    pos = torch.randint(0, 1000, (T,), generator=g, device=DEV).int()
+    got = q.rotate(x, y, freqs, pos, q_weight=w, k_weight=w)
+    some = torch.cat([torch.arange(min(T, 5)), torch.arange(max(0, T - 5), T), torch.randint(0, T, (200,), generator=gen(1))])
+    on = some.to(DEV)
+    for out, x in zip(got, (x, y)):
+        want, size = rotate64(x[on].cpu(), w.cpu(), 1e-6, angles_of(pos[on], None, freqs, len(some)), False)
+        check_rounded(out[on], want, size, "bf16")
