@@ -34,11 +34,11 @@ typedef __attribute__((ext_vector_type(8))) _Float16 f16x8;
 typedef __attribute__((ext_vector_type(2))) _Float16 f16x2;
 
 constexpr int kUnits = 256;           // compute units
-constexpr int kBlockTokens = 16;      // up to so many new tokens a sequence is a block, above a chunk
-constexpr int kLeafBytes = 32768;     // of keys in a leaf, and of values
 // workgroups of so much LDS on a compute unit, which hands out its 160 KB in pieces of 1280 bytes (768 workgroups of one
 // length: 307 us with 53760 bytes each, 604 with 53776)
 constexpr int fit(int lds) { return 128 / ((lds + 1279) / 1280); }
+constexpr int kBlockTokens = 16;      // up to so many new tokens a sequence is a block, above a chunk
+constexpr int kLeafBytes = 32768;     // of keys in a leaf, and of values
 constexpr int leaf_keys(int head_size) { return kLeafBytes / 2 / head_size; }
 constexpr int kSuper = 8;             // leaves of a super (the two steps in which blocks of keys are joined)
 constexpr float kGone = -__builtin_huge_valf();

@@ -357,11 +357,7 @@ __device__ __forceinline__ void chunk_body(const AttendParams& p, int group, int
     }
 }
 
-// A call's blocks in the same launch: they are bound by memory, chunks by the matrix instructions, and neither waits
-// for the other's end.  63 single tokens of 1000 places beside a chunk of 512, 8 heads of 128, us: 98, in two launches 134;
-// 255 beside one of 2048: 291, 305.  They take turns by rounds of a workgroup for every compute unit: parts of the chip
-// would get all of one kind otherwise (a chunk of 2048 over 16384 places by eights in turn with blocks without work:
-// 986 us, by rounds 659).
+// What a launch of chunks and blocks asks for.
 template <int DP, int NP, int NR>
 struct Both {
     static constexpr int kBlock = DP > 128 ? 256 : DP > 64 ? 128 : 64;       // the block's head size
@@ -370,6 +366,12 @@ struct Both {
     // cache, us: 74 with two planned, 79 with three.
     static constexpr int kAtOnce = fit(kLds) < Chunk<DP>::kAtOnce ? fit(kLds) : Chunk<DP>::kAtOnce;
 };
+
+// A call's blocks in the same launch: they are bound by memory, chunks by the matrix instructions, and neither waits
+// for the other's end.  63 single tokens of 1000 places beside a chunk of 512, 8 heads of 128, us: 98, in two launches 134;
+// 255 beside one of 2048: 291, 305.  They take turns by rounds of a workgroup for every compute unit: parts of the chip
+// would get all of one kind otherwise (a chunk of 2048 over 16384 places by eights in turn with blocks without work:
+// 986 us, by rounds 659).
 template <int DP, class X, int NP, int NR>
 __global__ __launch_bounds__(Chunk<DP>::kWaves * 64, (Both<DP, NP, NR>::kAtOnce * Chunk<DP>::kWaves / 4)) void chunk_kernel(AttendParams p)
 {
